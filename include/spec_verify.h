@@ -304,6 +304,22 @@ SPEC_API int spec_verify_linear_rope(const spec_bf16* X, int M, int K, int ldx, 
 SPEC_API int spec_rope_table(const int32_t* cu_rows, const int32_t* ctx_len, int B, int M, int D, float theta,
                              float* cs, spec_stream stream);
 
+/* The same table for positions with several axes (time, height and width of the patches of an image
+ * or a video; text advances all axes together): cs[r][i] = (cos, sin) of
+ * pos[a(i)][r] * theta^(-2i/D), i < D/2, where frequency i belongs to axis a(i):
+ *   interleaved = 0: the first sections[0] frequencies to axis 0, the next sections[1] to axis 1, ...
+ *   interleaved = 1: i to axis i mod axes while i < axes * sections[i mod axes], else to axis 0
+ *   pos       [axes] rows of M int32 (device), row a at pos + a * ldpos; negative positions are
+ *             allowed.  The angle is reduced in integers (turns of 2^-64), so it is as good at
+ *             position 2^31 - 1 as the fp64 frequency is
+ *   sections  [axes] host integers >= 0 with sum D/2
+ *   cs        [M x D/2] pairs of fp32 out, as spec_rope_table's (spec_verify_linear_rope and
+ *             spec_kv_append_paged read it)
+ * Requires 1 <= axes <= 8, ldpos >= M, D even, D <= 256, theta finite and > 0; interleaved sections
+ * must fit (a + axes * (sections[a] - 1) < D/2 for a >= 1).  One kernel, no workspace. */
+SPEC_API int spec_rope_table_axes(const int32_t* pos, int ldpos, int axes, int M, int D, float theta,
+                                  const int32_t* sections, int interleaved, float* cs, spec_stream stream);
+
 /* Fused gate|up projection and SwiGLU activation of the MLP:
  *   A[r, i] = silu(gate[r, i]) * up[r, i],  gate = X Wg^T, up = X Wu^T,
  * silu(g) = g / (1 + e^-g), fp32 from the fp32 accumulators, one bf16 rounding.
@@ -394,6 +410,62 @@ SPEC_API int spec_verify_attention_paged(const spec_bf16* Q, int ldq, const spec
                                          int Hq, int Hkv, int D, float scale,
                                          spec_bf16* O, int ldo, void* workspace, size_t workspace_bytes,
                                          spec_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Prompt side of the paged cache: append a chunk's keys, attend with its rows */
+/* ------------------------------------------------------------------------ */
+/* Before a sequence can be verified its prompt has to be in the cache ([P3] "Prefill and Decode": the
+ * prompt's tokens are processed together, bound by arithmetic).  A prompt is run in chunks of any
+ * length (1 row and more) of several sequences at once: per layer, QKV projection,
+ * spec_kv_append_paged, spec_chunk_attention_paged; the caller then advances ctx_len by the rows.
+ *
+ * Append: row r of sequence b (cu_rows[b] <= r < cu_rows[b + 1]) sits at position
+ * p = ctx_len[b] + r - cu_rows[b]; its keys and values go to row p % 128 of page
+ * block_table[b * max_pages + p / 128] of each kv head's pool, the keys rotated on the way
+ * (rotate-half pairs (i, i + D/2) with cs[r], fp32, one rounding to bf16), and its queries, rotated
+ * the same way, to Qrot.
+ *   Knew, Vnew  row r, kv head g at + r*ldkv + g*D (bf16, not rotated)
+ *   cs          [M x D/2] pairs (cos, sin) (spec_rope_table / _axes), 16-byte aligned, or NULL: the
+ *               keys are copied as they are (a projection that rotates them already; Q must be NULL)
+ *   Q, Qrot     row r, query head h at + r*ldq + h*D, Qrot likewise with ldqr; Qrot may be Q itself
+ *               (same pointer and leading dimension).  Q NULL: only keys and values (Hq is ignored)
+ *   cu_rows [B+1], ctx_len [B], block_table [B x max_pages] int32 device arrays
+ *   Kpool, Vpool [Hkv][num_pages][128][D] bf16 (in/out), as spec_verify_attention_paged's; no input may
+ *               overlap them
+ * M is the rows of the buffers; rows outside cu_rows[0] .. cu_rows[B] - 1 are padding: not read, and
+ * Qrot's left as they were.  Sequences without rows are allowed.  A page that receives rows must belong to one
+ * sequence.  Checked on the device, with the status word set: a sequence outside the M rows or
+ * past 128 * max_pages keys is skipped; a row whose page id is outside [0, num_pages) is not written to
+ * the pools.  Requires D == 128, leading dimensions multiples of 8, 16-byte aligned pointers.  One
+ * kernel, no workspace. */
+SPEC_API int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr, const spec_bf16* Knew,
+                                  const spec_bf16* Vnew, int ldkv, const float* cs, const int32_t* cu_rows,
+                                  const int32_t* ctx_len, int B, int M, spec_bf16* Kpool, spec_bf16* Vpool,
+                                  int num_pages, const int32_t* block_table, int max_pages, int Hq, int Hkv, int D,
+                                  spec_stream stream);
+
+/* Attention of a chunk of new tokens: row j of sequence b attends keys 0 .. ctx_len[b] + j of its
+ * pages (its own and the chunk's earlier keys already appended), softmax(scale q.k) v with fp32 sums
+ * and statistics; the softmax weights enter the product with V as bf16 and the output is rounded once.
+ * Any number of rows per sequence, from one to the whole prompt, mixed in one call; only reads the
+ * cache.
+ *   Q [M x Hq*D] bf16 with leading dimension ldq (rotation applied), O likewise with ldo (out; must
+ *   not overlap Q or the pools); the rest as spec_kv_append_paged.  Query head h reads kv head
+ *   h / (Hq / Hkv).
+ * Pages are read to the last key of the sequence only: what lies behind it (in its last page or in
+ * table entries past it) may hold anything, NaN included.  Rows outside cu_rows[0] .. cu_rows[B] - 1
+ * are padding: their O is left as it was.  A non-finite value in V of a new key also reaches the rows of its
+ * own chunk before it that share its 128-key tile (0 * inf).  Checked on the device, with the status
+ * word set: a sequence outside the M rows or past 128 * max_pages keys is skipped; a page id outside
+ * [0, num_pages) reads page 0 instead.
+ * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, scale finite and >= 0.
+ * Workspace: spec_chunk_attention_workspace_bytes. */
+SPEC_API size_t spec_chunk_attention_workspace_bytes(int B, int M, int Hq, int Hkv, int D, int max_pages);
+SPEC_API int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len,
+                                        int B, int M, const spec_bf16* Kpool, const spec_bf16* Vpool, int num_pages,
+                                        const int32_t* block_table, int max_pages, int Hq, int Hkv, int D,
+                                        float scale, spec_bf16* O, int ldo, void* workspace,
+                                        size_t workspace_bytes, spec_stream stream);
 
 /* ------------------------------------------------------------------------ */
 /* LM head + softmax: P = softmax((H W_lm^T) / T); T == 0 -> one-hot argmax  */

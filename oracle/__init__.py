@@ -21,6 +21,8 @@ What it computes, and where the pages define it:
 * ``ops.rmsnorm`` / ``ops.rope`` / ``ops.silu_mul`` and ``stack`` — the
   layer glue of a Qwen3-8B-shaped stack.  The pages only give the layer and
   head counts; the layer internals are the builder's reading.
+* ``prompt`` — the prompt side of the paged cache (rotation table of several
+  position axes, append, attention of a chunk of new tokens).
 * ``formulas`` — the closed forms the pages print (expected tokens per
   round, Theorem 3.11's arithmetic increase, the speedup / break-even model,
   the verify-cost division, vLLM's acceptance metrics).
@@ -28,4 +30,4 @@ What it computes, and where the pages define it:
 Parity pins (tests marked ``not gpu``) tie every function here to values the
 pages print, closed forms, invariants or brute force; see ``tests/``.
 """
-from . import bf16, formulas, ops, sampler, stack  # noqa: F401
+from . import bf16, formulas, ops, prompt, sampler, stack  # noqa: F401

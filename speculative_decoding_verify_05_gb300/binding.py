@@ -42,6 +42,12 @@ _SIGS = {
     "spec_linear_chain_workspace_bytes": (_sz, [_vp, _i, _i]),
     "spec_verify_linear_chain": (_i, [_vp, _i, _i, _vp, _sz, _vp]),
     "spec_rope_table": (_i, [_vp, _vp, _i, _i, _i, _f, _vp, _vp]),
+    "spec_rope_table_axes": (_i, [_vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _vp]),
+    "spec_kv_append_paged": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _vp, _i,
+                                  _i, _i, _i, _vp]),
+    "spec_chunk_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "spec_chunk_attention_paged": (_i, [_vp, _i, _vp, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _vp, _i,
+                                        _vp, _sz, _vp]),
     "spec_swiglu_linear_workspace_bytes": (_sz, [_i, _i, _i]),
     "spec_verify_linear_swiglu": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _i, _vp, _sz, _vp]),
     "spec_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
@@ -340,6 +346,25 @@ def spec_rope_table(cu_rows, ctx_len, M: int, D: int, theta: float = 1e6, cs=Non
     return cs
 
 
+def spec_rope_table_axes(pos, sections, D: int, theta: float = 1e6, interleaved: bool = False, cs=None, stream=None):
+    """(cos, sin) per row and frequency for positions with several axes: pos [axes, M] int32, sections
+    the frequencies of each axis (sum D/2; consecutive, or interleaved); returns cs [M, D/2, 2] fp32."""
+    _need(pos, torch.int32, "pos")
+    ld = _rowmajor(pos, "pos")
+    axes, M = pos.shape
+    if len(sections) != axes:
+        raise ValueError("sections must have an entry per axis of pos")
+    if cs is None:
+        cs = torch.empty((M, D // 2, 2), dtype=torch.float32, device=pos.device)
+    _need(cs, torch.float32, "cs")
+    if not cs.is_contiguous() or cs.shape != (M, D // 2, 2):
+        raise ValueError("cs must be a contiguous [M, D/2, 2] tensor")
+    sec = (ctypes.c_int32 * axes)(*[int(v) for v in sections])
+    _check(_lib.spec_rope_table_axes(_p(pos), ld, axes, M, int(D), float(theta), sec, 1 if interleaved else 0, _p(cs),
+                                     _stream(stream)), True)
+    return cs
+
+
 def spec_verify_linear_rope(X, W, cs, rope_heads: int, Y=None, ws: Workspace | None = None, stream=None,
                             norm=None):
     """Y = X W^T with the first rope_heads 128-column heads rotated by the table cs [M, 64, 2]."""
@@ -476,6 +501,86 @@ def spec_verify_attention_paged(Q, Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, b
         _p(Q), _rowmajor(Q, "Q"), _p(Knew), _p(Vnew), ldkv, _p(cu_rows), _p(ctx_len), B, int(max_rows),
         _p(Kpool), _p(Vpool), num_pages, _p(block_table), max_pages, Hq, Hkv, D, float(scale), _p(O),
         _rowmajor(O, "O"), wp, wn, _stream(stream)), True)
+    return O
+
+
+# --------------------------------------------------------------------------- prompt side of the paged cache
+def _paged(cu_rows, ctx_len, Kpool, Vpool, block_table):
+    """Checks the batch and cache arguments of a chunk call; returns (B, Hkv, num_pages, D, max_pages)."""
+    for t, n in ((Kpool, "Kpool"), (Vpool, "Vpool")):
+        _need(t, torch.bfloat16, n)
+    for t, n in ((cu_rows, "cu_rows"), (ctx_len, "ctx_len"), (block_table, "block_table")):
+        _need(t, torch.int32, n)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    if Kpool.dim() != 4 or Kpool.shape[2] != 128 or not (Kpool.is_contiguous() and Vpool.is_contiguous()
+                                                         and Vpool.shape == Kpool.shape):
+        raise ValueError("Kpool/Vpool must be contiguous [Hkv, num_pages, 128, D]")
+    B = cu_rows.numel() - 1
+    if block_table.dim() != 2 or block_table.shape[0] != B or ctx_len.numel() != B:
+        raise ValueError("cu_rows, ctx_len and block_table must be [B + 1], [B] and [B, max_pages]")
+    Hkv, num_pages, _, D = Kpool.shape
+    return B, Hkv, num_pages, D, block_table.shape[1]
+
+
+def spec_kv_append_paged(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table, cs=None, Q=None, Qrot=None,
+                         stream=None):
+    """Appends a chunk's keys and values (Knew/Vnew [M, Hkv*D]) to the pages of Kpool/Vpool [Hkv, num_pages,
+    128, D] at positions ctx_len.., the keys rotated with the table cs [M, D/2, 2] (cs None: copied as
+    they are); Q [M, Hq*D], if given, is rotated into Qrot (default: in place).  Returns Qrot."""
+    B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table)
+    M = Knew.shape[0]
+    for t, n in ((Knew, "Knew"), (Vnew, "Vnew")):
+        _need(t, torch.bfloat16, n)
+        if t.shape != (M, Hkv * D):
+            raise ValueError(f"{n} must be [M, Hkv*D]")
+    ldkv = _rowmajor(Knew, "Knew")
+    if _rowmajor(Vnew, "Vnew") != ldkv:
+        raise ValueError("Knew and Vnew must share a leading dimension")
+    if cs is not None:
+        _need(cs, torch.float32, "cs")
+        if not cs.is_contiguous() or cs.dim() != 3 or cs.shape[0] < M or cs.shape[1:] != (D // 2, 2):
+            raise ValueError("cs must be a contiguous [M, D/2, 2] table with an entry per row")
+    Hq = 0
+    if Q is not None:
+        _need(Q, torch.bfloat16, "Q")
+        Qrot = Q if Qrot is None else Qrot
+        _need(Qrot, torch.bfloat16, "Qrot")
+        if Q.shape[0] != M or Q.shape[1] % D or Qrot.shape != Q.shape:
+            raise ValueError("Q and Qrot must be [M, Hq*D]")
+        Hq = Q.shape[1] // D
+    _check(_lib.spec_kv_append_paged(
+        _p(Q), _rowmajor(Q, "Q") if Q is not None else 0, _p(Qrot), _rowmajor(Qrot, "Qrot") if Qrot is not None else 0,
+        _p(Knew), _p(Vnew), ldkv, _p(cs), _p(cu_rows), _p(ctx_len), B, M, _p(Kpool), _p(Vpool), num_pages,
+        _p(block_table), max_pages, Hq, Hkv, D, _stream(stream)), True)
+    return Qrot
+
+
+def spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages) -> int:
+    return _lib.spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages)
+
+
+def spec_chunk_attention_paged(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, scale: float | None = None, O=None,
+                               ws: Workspace | None = None, stream=None):
+    """Attention of a chunk of new tokens over the paged cache that already holds their keys: row j of
+    sequence b (Q [M, Hq*D]) attends keys 0 .. ctx_len[b] + j; returns O [M, Hq*D]."""
+    B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table)
+    _need(Q, torch.bfloat16, "Q")
+    M = Q.shape[0]
+    if Q.shape[1] % D:
+        raise ValueError("Q must be [M, Hq*D]")
+    Hq = Q.shape[1] // D
+    if O is None:
+        O = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=Q.device)
+    _need(O, torch.bfloat16, "O")
+    if O.shape != Q.shape:
+        raise ValueError("O must be [M, Hq*D]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    wp, wn = _ws_args(ws, spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages), Q.device)
+    _check(_lib.spec_chunk_attention_paged(
+        _p(Q), _rowmajor(Q, "Q"), _p(cu_rows), _p(ctx_len), B, M, _p(Kpool), _p(Vpool), num_pages, _p(block_table),
+        max_pages, Hq, Hkv, D, float(scale), _p(O), _rowmajor(O, "O"), wp, wn, _stream(stream)), True)
     return O
 
 

@@ -1151,6 +1151,47 @@ int spec_rope_table(const int32_t* cu_rows, const int32_t* ctx_len, int B, int M
   return ok(1);
 }
 
+int spec_rope_table_axes(const int32_t* pos, int ldpos, int axes, int M, int D, float theta, const int32_t* sections,
+                         int interleaved, float* cs, spec_stream stream) {
+  if (M < 0) return fail(SPEC_EINVAL, "M=%d < 0", M);
+  if (axes < 1 || axes > 8) return fail(SPEC_EUNSUPPORTED, "axes=%d must be in [1, 8]", axes);
+  if (D <= 0 || D % 2 || D > 256) return fail(SPEC_EUNSUPPORTED, "D=%d must be even and <= 256", D);
+  if (!(theta > 0.f) || std::isinf(theta)) return fail(SPEC_EINVAL, "theta must be finite and > 0");
+  if (interleaved != 0 && interleaved != 1) return fail(SPEC_EINVAL, "interleaved must be 0 or 1");
+  if (!sections) return fail(SPEC_EINVAL, "sections must be non-NULL");
+  const int half = D / 2;
+  long long sum = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (sections[a] < 0) return fail(SPEC_EINVAL, "sections[%d]=%d < 0", a, sections[a]);
+    sum += sections[a];
+    if (interleaved && a > 0 && sections[a] > 0 && a + (long long)axes * (sections[a] - 1) >= half)
+      return fail(SPEC_EINVAL, "sections[%d]=%d: frequency %lld is past D/2=%d", a, sections[a],
+                  a + (long long)axes * (sections[a] - 1), half);
+  }
+  if (sum != half) return fail(SPEC_EINVAL, "the sections sum to %lld, not D/2=%d", sum, half);
+  if (M == 0) return ok();
+  if (!pos || !cs) return fail(SPEC_EINVAL, "NULL argument");
+  if (ldpos < M && axes > 1) return fail(SPEC_EINVAL, "ldpos=%d < M=%d", ldpos, M);
+  RopeAxes f{};
+  for (int i = 0, a = 0, end = sections[0]; i < half; ++i) {
+    if (interleaved) {
+      a = i % axes;
+      if (i >= axes * sections[a]) a = 0;
+    } else {
+      while (i >= end) end += sections[++a];
+    }
+    f.axis[i] = (unsigned char)a;
+    // the frequency in turns, its whole turns dropped (positions are whole numbers)
+    double t = std::pow((double)theta, -2.0 * (double)i / (double)D) / 6.283185307179586476925286766559;
+    t -= std::floor(t);
+    f.turn[i] = (unsigned long long)std::ldexp(t, 64);
+  }
+  cudaError_t e = launch_rope_table_axes(pos, ldpos, M, half, f, reinterpret_cast<float2*>(cs),
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_table_axes launch");
+  return ok(1);
+}
+
 }  // extern "C"
 
 static int verify_linear_rope_impl(const spec_bf16* X, int M, int K, int ldx, const spec_bf16* W, int N, int ldw,
@@ -1637,6 +1678,98 @@ int spec_verify_attention_paged(const spec_bf16* Q, int ldq, const spec_bf16* Kn
   return verify_attention_impl(Q, ldq, Knew, Vnew, ldkv, cu_rows, ctx_len, B, max_rows, Kpool, Vpool,
                                max_pages * attention_tc_key_tile(), block_table, max_pages, num_pages, Hq, Hkv, D,
                                scale, O, ldo, workspace, workspace_bytes, stream);
+}
+
+// --------------------------------------------------------------------------- prompt side of the paged cache
+// Checks shared by the append and the attention of a chunk.
+static int check_paged_chunk(const int32_t* cu_rows, const int32_t* ctx_len, int B, const spec_bf16* Kpool,
+                             const spec_bf16* Vpool, int num_pages, const int32_t* block_table, int max_pages,
+                             int Hkv, int D) {
+  if (!cu_rows || !ctx_len || !block_table || !Kpool || !Vpool) return fail(SPEC_EINVAL, "NULL tensor argument");
+  if (D != 128) return fail(SPEC_EUNSUPPORTED, "head_dim %d: only 128 is implemented", D);
+  if (Hkv <= 0) return fail(SPEC_EINVAL, "Hkv=%d must be >= 1", Hkv);
+  if (num_pages <= 0 || max_pages <= 0)
+    return fail(SPEC_EINVAL, "num_pages=%d and max_pages=%d must be >= 1", num_pages, max_pages);
+  if ((long long)max_pages * attention_tc_key_tile() > INT32_MAX / 2)
+    return fail(SPEC_EINVAL, "max_pages=%d too large", max_pages);
+  if ((long long)num_pages * Hkv > INT32_MAX) return fail(SPEC_EINVAL, "num_pages=%d too large", num_pages);
+  if (!aligned16(Kpool) || !aligned16(Vpool)) return fail(SPEC_EINVAL, "the pools must be 16-byte aligned");
+  return SPEC_OK;
+}
+
+int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr, const spec_bf16* Knew,
+                         const spec_bf16* Vnew, int ldkv, const float* cs, const int32_t* cu_rows,
+                         const int32_t* ctx_len, int B, int M, spec_bf16* Kpool, spec_bf16* Vpool, int num_pages,
+                         const int32_t* block_table, int max_pages, int Hq, int Hkv, int D, spec_stream stream) {
+  if (B < 0 || M < 0) return fail(SPEC_EINVAL, "bad sizes B=%d M=%d", B, M);
+  if (B == 0 || M == 0) return ok();
+  if (int rc = check_paged_chunk(cu_rows, ctx_len, B, Kpool, Vpool, num_pages, block_table, max_pages, Hkv, D))
+    return rc;
+  if (!Knew || !Vnew) return fail(SPEC_EINVAL, "Knew and Vnew must be non-NULL");
+  if (ldkv < (long long)Hkv * D || ldkv % 8) return fail(SPEC_EINVAL, "bad leading dimension ldkv=%d", ldkv);
+  if (!aligned16(Knew) || !aligned16(Vnew) || !aligned16(cs) || !aligned16(Q) || !aligned16(Qrot))
+    return fail(SPEC_EINVAL, "tensors must be 16-byte aligned");
+  if (Q) {
+    if (!cs) return fail(SPEC_EINVAL, "queries without a rotation table");
+    if (!Qrot) return fail(SPEC_EINVAL, "Qrot must be non-NULL with Q");
+    if (Hq <= 0) return fail(SPEC_EINVAL, "Hq=%d must be >= 1", Hq);
+    if (ldq < (long long)Hq * D || ldqr < (long long)Hq * D || ldq % 8 || ldqr % 8)
+      return fail(SPEC_EINVAL, "bad leading dimensions ldq=%d ldqr=%d", ldq, ldqr);
+    if (Q == Qrot && ldq != ldqr) return fail(SPEC_EINVAL, "Qrot may be Q only with the same leading dimension");
+  } else if (Qrot) {
+    return fail(SPEC_EINVAL, "Qrot without Q");
+  }
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
+  KvAppendArgs a{};
+  a.Q = Q; a.ldq = ldq; a.Qrot = Qrot; a.ldqr = ldqr;
+  a.Knew = Knew; a.Vnew = Vnew; a.ldkv = ldkv;
+  a.cs = reinterpret_cast<const float2*>(cs);
+  a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M;
+  a.Kpool = Kpool; a.Vpool = Vpool;
+  a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages;
+  a.Hq = Q ? Hq : 0; a.Hkv = Hkv;
+  a.status = d->status;
+  cudaError_t e = launch_kv_append(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return ok(1);
+}
+
+size_t spec_chunk_attention_workspace_bytes(int B, int M, int Hq, int Hkv, int D, int max_pages) {
+  if (B <= 0 || M <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_pages <= 0) return 0;
+  return 0;
+}
+
+int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len, int B,
+                               int M, const spec_bf16* Kpool, const spec_bf16* Vpool, int num_pages,
+                               const int32_t* block_table, int max_pages, int Hq, int Hkv, int D, float scale,
+                               spec_bf16* O, int ldo, void* workspace, size_t workspace_bytes, spec_stream stream) {
+  if (B < 0 || M < 0) return fail(SPEC_EINVAL, "bad sizes B=%d M=%d", B, M);
+  if (B == 0 || M == 0) return ok();
+  if (int rc = check_paged_chunk(cu_rows, ctx_len, B, Kpool, Vpool, num_pages, block_table, max_pages, Hkv, D))
+    return rc;
+  if (!Q || !O) return fail(SPEC_EINVAL, "NULL tensor argument");
+  if (Hq <= 0 || Hq % Hkv) return fail(SPEC_EINVAL, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
+  if (Hq / Hkv > 128) return fail(SPEC_EUNSUPPORTED, "Hq/Hkv = %d > 128", Hq / Hkv);
+  if (ldq < (long long)Hq * D || ldo < (long long)Hq * D || ldq % 8 || ldo % 8)
+    return fail(SPEC_EINVAL, "bad leading dimensions ldq=%d ldo=%d", ldq, ldo);
+  if (!aligned16(Q) || !aligned16(O)) return fail(SPEC_EINVAL, "bf16 tensors must be 16-byte aligned");
+  if (!std::isfinite(scale) || scale < 0.f) return fail(SPEC_EINVAL, "scale must be finite and >= 0");
+  const size_t need = spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(SPEC_EINVAL, "workspace too small: need %zu bytes", need);
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
+  ChunkAttnArgs a{};
+  a.Q = Q; a.ldq = ldq; a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M;
+  a.Kpool = Kpool; a.Vpool = Vpool; a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages;
+  a.Hkv = Hkv; a.G = Hq / Hkv;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.O = O; a.ldo = ldo;
+  a.status = d->status;
+  cudaError_t e = launch_chunk_attention(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  return ok(1);
 }
 
 // --------------------------------------------------------------------------- sampler

@@ -187,6 +187,39 @@ int attention_tc_rows(int G, int max_rows);   // padded query rows per kv head, 
 cudaError_t launch_attention_tc(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, int grid,
                                 cudaStream_t s);
 
+// ---- prompt side of the paged cache: rotation table of several position axes, append, chunk attention
+struct RopeAxes {
+  unsigned long long turn[128];   // frequency i in turns per position, modulo one turn, in units of 2^-64
+  unsigned char axis[128];        // its position axis
+};
+cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int half, const RopeAxes& f, float2* cs,
+                                   cudaStream_t s);
+struct KvAppendArgs {
+  const uint16_t* Q; int ldq;           // nullptr: no queries
+  uint16_t* Qrot; int ldqr;
+  const uint16_t* Knew; const uint16_t* Vnew; int ldkv;
+  const float2* cs;                     // [M][64], nullptr: no rotation
+  const int32_t* cu_rows; const int32_t* ctx_len;
+  int B, M;
+  uint16_t* Kpool; uint16_t* Vpool;     // [Hkv][num_pages][128][128]
+  const int32_t* block_table;
+  int num_pages, max_pages, Hq, Hkv;    // Hq = 0 without queries
+  unsigned* status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
+struct ChunkAttnArgs {
+  const uint16_t* Q; int ldq;
+  const int32_t* cu_rows; const int32_t* ctx_len;
+  int B, M;
+  const uint16_t* Kpool; const uint16_t* Vpool;
+  const int32_t* block_table;
+  int num_pages, max_pages, Hkv, G;
+  float scale_log2;                     // softmax scale * log2(e)
+  uint16_t* O; int ldo;
+  unsigned* status;
+};
+cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t s);
+
 // ---- rejection sampler
 cudaError_t launch_reject_sample(const float* P, const float* Q, const int32_t* draft,
                                  const float* U, const int32_t* cu_rows, int B, int V,
