@@ -1735,9 +1735,24 @@ int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr,
   return ok(1);
 }
 
+struct ChunkPlan {
+  int grid;
+  size_t o_off, ml_off, item_off, bytes;
+};
+static ChunkPlan plan_chunk() {
+  ChunkPlan p;
+  p.grid = g_force_grid > 0 ? g_force_grid : plan_sms();
+  const size_t rows = size_t(p.grid) * 2 * 256;
+  p.o_off = kCounterBytes;
+  p.ml_off = p.o_off + rows * 128 * 4;
+  p.item_off = p.ml_off + rows * 8;
+  p.bytes = p.item_off + round_up(size_t(p.grid) * 16, 256);
+  return p;
+}
+
 size_t spec_chunk_attention_workspace_bytes(int B, int M, int Hq, int Hkv, int D, int max_pages) {
   if (B <= 0 || M <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_pages <= 0) return 0;
-  return 0;
+  return plan_chunk().bytes;
 }
 
 int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len, int B,
@@ -1755,21 +1770,43 @@ int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_ro
     return fail(SPEC_EINVAL, "bad leading dimensions ldq=%d ldo=%d", ldq, ldo);
   if (!aligned16(Q) || !aligned16(O)) return fail(SPEC_EINVAL, "bf16 tensors must be 16-byte aligned");
   if (!std::isfinite(scale) || scale < 0.f) return fail(SPEC_EINVAL, "scale must be finite and >= 0");
-  const size_t need = spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages);
-  if (need && (!workspace || workspace_bytes < need))
-    return fail(SPEC_EINVAL, "workspace too small: need %zu bytes", need);
+  const ChunkPlan p = plan_chunk();
+  if (!workspace || workspace_bytes < p.bytes)
+    return fail(SPEC_EINVAL, "workspace too small: need %zu bytes", p.bytes);
+  if (!aligned16(workspace)) return fail(SPEC_EINVAL, "the workspace must be 16-byte aligned");
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
+  const int G = Hq / Hkv, tpt = 128 / G;
+  CUtensorMap tq, tk, tv;
+  {
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)M};
+    cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)ldq * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tpt};
+    if (int rc = encode_bf16(&tq, Q, 3, dims, str, box, "Q")) return rc;
+  }
+  {
+    const cuuint64_t kt = attention_tc_key_tile();
+    cuuint64_t dims[3] = {(cuuint64_t)D, kt, (cuuint64_t)num_pages * Hkv};
+    cuuint64_t str[2] = {(cuuint64_t)D * 2, kt * D * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)kt, 1};
+    if (int rc = encode_bf16(&tk, Kpool, 3, dims, str, box, "Kpool", g_kv_promotion)) return rc;
+    if (int rc = encode_bf16(&tv, Vpool, 3, dims, str, box, "Vpool", g_kv_promotion)) return rc;
+  }
+  char* ws = static_cast<char*>(workspace);
   ChunkAttnArgs a{};
   a.Q = Q; a.ldq = ldq; a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M;
   a.Kpool = Kpool; a.Vpool = Vpool; a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages;
-  a.Hkv = Hkv; a.G = Hq / Hkv;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.Hkv = Hkv; a.G = G; a.tpt = tpt;
+  // (a scale of 0 weighs every visible key alike; masked scores have to stay -inf under it)
+  a.scale_log2 = std::max(scale * 1.4426950408889634f, 1e-30f);
   a.O = O; a.ldo = ldo;
+  a.part_o = reinterpret_cast<float*>(ws + p.o_off);
+  a.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
+  a.part_item = reinterpret_cast<int4*>(ws + p.item_off);
   a.status = d->status;
-  cudaError_t e = launch_chunk_attention(a, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_chunk_attention(tq, tk, tv, a, p.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
-  return ok(1);
+  return ok(2);
 }
 
 // --------------------------------------------------------------------------- sampler

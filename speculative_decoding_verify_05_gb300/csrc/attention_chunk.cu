@@ -1,8 +1,28 @@
-// Attention of a chunk of new tokens over the paged cache: row j of sequence b attends keys
-// 0 .. ctx_b + j of its pages.
+// Attention of a chunk of new tokens over the paged cache on tcgen05 tensor cores: row j of sequence b
+// attends keys 0 .. ctx_b + j of its pages (the chunk's own keys are already in them).
 //
-// One warp per (row, query head), four dims per lane, one pass over the keys with the running
-// maximum and sum.
+// Rows.  The G query heads of a kv head share its keys, so a row tile packs TPT = 128 / G tokens x G
+// heads (row m = token m / G, head m % G) into the MMA's 128 rows; an item is two row tiles (2 TPT
+// tokens of one sequence and kv head) over all key tiles (one page, 128 keys) that its last token sees.
+//   S[row, key] = Q . K_tile^T    tcgen05.mma M = 128, N = 128 keys, K = 128 dims (smem x smem)
+//   softmax                       one thread per row: running maximum and sum in registers, fp32
+//   O[row, d]  += P . V_tile      tcgen05.mma M = 128, N = 128 dims, K = 128 keys, P (bf16) read
+//                                 from TMEM, where it replaces the scores it came from
+// TMEM holds S and O of two slots (4 x 128 columns, all of it).  The steps of a CTA alternate between the
+// slots, so that one slot's softmax runs beside the other slot's products.  An item of two row tiles
+// gives each slot one of them and both use every key tile (one load, two products); an item with a single
+// row tile (few rows: decode steps, ends of prompts) gives the slots its key tiles in turn, each
+// with its own running maximum, sum and O, joined at the end.
+//
+// Work.  The key tiles of all items in a row (sequence, kv head, item) are cut into equal shares by cost, one
+// per CTA; every CTA works out the same cuts from the lengths on the device (closed form per
+// sequence, so one graph serves any lengths).  Where a cut falls into an item its pieces go to the
+// workspace as unnormalised O, maximum and sum, and a second small kernel joins them in CTA order.
+//
+// Roles (11 warps): 0-3 and 4-7 softmax and epilogue of slot 0 and 1 (thread = TMEM lane = row); 8 loads K
+// and V tiles by TMA into one ring of 5; 9 issues the MMAs; 10 loads the Q tiles and zeroes the rows of
+// a sequence's last V tile behind its last key (up to the next multiple of 16, where the product
+// stops), which may hold anything (0 * NaN would reach the sums).
 #include "common.cuh"
 #include "internal.h"
 
@@ -10,60 +30,754 @@ namespace spec {
 namespace {
 
 constexpr int D = 128;
-constexpr int PAGE = 128;
+constexpr int KT = 128;                   // keys per tile (one page)
+constexpr int TM = 128;                   // rows per row tile
+constexpr int ST = 5;                     // ring stages of one K or V tile
+constexpr int HALF = 128 * 128;           // 128 rows x 64 bf16 (128-byte swizzled rows), 16 KB
+constexpr int TILE = 2 * HALF;
+constexpr int THREADS = 352;
+constexpr int OFF_Q = 0;                  // two row tiles
+constexpr int OFF_RING = 2 * TILE;
+constexpr int OFF_BAR = OFF_RING + ST * TILE;
+constexpr int N_BARS = 3 * ST + 10;
+constexpr int OFF_SCHED = OFF_BAR + (N_BARS + 1) * 8;
+constexpr int OFF_ML = OFF_BAR + 512;     // (max, sum) of 128 rows for each slot
+constexpr int SMEM = OFF_ML + 2 * TM * 8;
+static_assert(SMEM <= 227 * 1024, "shared memory budget");
+constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 
-__global__ void __launch_bounds__(128) chunk_attention_kernel(const ChunkAttnArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int r = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {                     // the last sequence with cu_rows[b] <= r
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cu_rows[mid] <= r) lo = mid; else hi = mid - 1;
+// Cost of a key tile for an item of two row tiles and of one, and of an item's start and end.
+constexpr long long W_DUAL = 4, W_ONE = 3, W_ITEM = 4;
+
+// 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one asm
+__device__ __forceinline__ void tmem_ld_cols128(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128+0];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%128+32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%128+64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128+96];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 32 consecutive TMEM columns of this thread's lane stored (complete after tmem_st_wait)
+__device__ __forceinline__ void tmem_st_cols32(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D += A B with A (bf16, two consecutive k per 32-bit column) in TMEM.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Shared-memory descriptor of an MN-major operand stored as 128-byte swizzled rows (8-row atoms 1024 B
+// apart along K; 64-element columns `lbo` apart along N).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= uint64_t((smem_addr & 0x3FFFFu) >> 4);
+  d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+// 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// ----------------------------------------------------------------- the batch
+struct Seq {
+  int r0, rows, ctx;
+};
+// Sequence b; one that breaks its bounds counts as having no rows (*bad set).
+__device__ __forceinline__ Seq seq_of(const ChunkAttnArgs& a, int b, bool* bad = nullptr) {
+  const int c0 = a.cu_rows[b], c1 = a.cu_rows[b + 1], ctx = a.ctx_len[b];
+  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.M && ctx >= 0 &&
+                  (long long)ctx + (c1 - c0) <= (long long)a.max_pages * KT;
+  if (bad) *bad = !ok;
+  return Seq{c0, ok ? c1 - c0 : 0, ctx};
+}
+// sum of floor((s i + o) / m) over i < n, in the steps of the Euclidean algorithm
+__device__ long long floor_sum(long long n, long long m, long long s, long long o) {
+  long long sum = 0;
+  while (n > 0) {
+    if (s >= m) {
+      sum += n * (n - 1) / 2 * (s / m);
+      s %= m;
+    }
+    if (o >= m) {
+      sum += n * (o / m);
+      o %= m;
+    }
+    const long long y = s * n + o;
+    if (y < m) break;
+    n = y / m;
+    o = y % m;
+    const long long t = m;
+    m = s;
+    s = t;
   }
-  const int c0 = a.cu_rows[lo], c1 = a.cu_rows[lo + 1], ctx = a.ctx_len[lo];
-  if (r < c0 || r >= c1 || h >= a.Hkv * a.G) return;
-  if (c0 < 0 || c1 > a.M || ctx < 0 || (long long)ctx + (c1 - c0) > (long long)a.max_pages * PAGE) {
-    if (threadIdx.x == 0) set_status(a.status, 0x7F1u);
+  return sum;
+}
+// Cost of the first q items (all of two row tiles) of one kv head of a sequence: item i sees
+// ctx + (i + 1) T keys.
+__device__ __forceinline__ long long items_cost(int q, int T, int ctx) {
+  return W_DUAL * floor_sum(q, KT, T, (long long)ctx + T + KT - 1) + W_ITEM * q;
+}
+// ... and of all its items.
+__device__ __forceinline__ long long head_cost(const Seq& s, int T) {
+  if (s.rows == 0) return 0;
+  const int last = (s.rows - 1) / T;
+  const bool dual = s.rows - last * T > T / 2;
+  return items_cost(last, T, s.ctx) + (dual ? W_DUAL : W_ONE) * ((s.ctx + s.rows + KT - 1) / KT) + W_ITEM;
+}
+
+// Where a cut falls: before tile t of item q of kv head h of sequence b.
+struct Cut {
+  int b, h, q, t;
+};
+// The cut at cost x of sequence b (0 <= x < cost of all its heads), on a whole tile.
+__device__ Cut cut_in(const Seq& s, int b, int T, long long x) {
+  const long long head = head_cost(s, T);
+  Cut c;
+  c.b = b;
+  c.h = (int)(x / head);
+  x -= c.h * head;
+  int lo = 0, hi = (s.rows - 1) / T;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (items_cost(mid, T, s.ctx) <= x) lo = mid; else hi = mid - 1;
+  }
+  c.q = lo;
+  x -= items_cost(lo, T, s.ctx) + W_ITEM;
+  const int tok = min(T, s.rows - lo * T);
+  const int nt = (s.ctx + lo * T + tok + KT - 1) / KT;
+  const long long w = tok > T / 2 ? W_DUAL : W_ONE;
+  const long long t = x <= 0 ? 0 : (x + w / 2) / w;
+  c.t = t < nt ? (int)t : nt;
+  return c;
+}
+
+// A CTA's consecutive key tiles of one item.
+struct Piece {
+  int b, h, q;
+  int t0, t1, nt;      // tiles t0 .. t1 - 1 of the item's nt
+  int r0, rows, ctx;   // its sequence
+  int tok, pos;        // tokens of the item, position of the first
+  bool dual;           // two row tiles
+
+  __device__ __forceinline__ int ops() const { return dual ? 2 * (t1 - t0) : t1 - t0; }
+  __device__ __forceinline__ int keys() const { return pos + tok; }
+  __device__ __forceinline__ void item(int T) {
+    tok = min(T, rows - q * T);
+    pos = ctx + q * T;
+    nt = (pos + tok + KT - 1) / KT;
+    dual = tok > T / 2;
+  }
+  __device__ __forceinline__ void sequence(const ChunkAttnArgs& a) {
+    const Seq s = seq_of(a, b);
+    r0 = s.r0;
+    rows = s.rows;
+    ctx = s.ctx;
+  }
+  // the piece ends at the item's end or at the CTA's
+  __device__ __forceinline__ bool clip(const Cut& e) {
+    t1 = nt;
+    if (b == e.b && h == e.h && q == e.q) t1 = e.t;
+    else if (b > e.b || (b == e.b && (h > e.h || (h == e.h && q > e.q)))) t1 = 0;
+    return t1 > t0;
+  }
+  // first piece of [s, e); false: none
+  __device__ __forceinline__ bool first(const ChunkAttnArgs& a, const Cut& s, const Cut& e) {
+    if (s.b >= a.B) return false;
+    b = s.b; h = s.h; q = s.q; t0 = s.t;
+    sequence(a);
+    item(2 * a.tpt);
+    if (t0 >= nt) return next(a, e);
+    return clip(e);
+  }
+  __device__ __forceinline__ bool next(const ChunkAttnArgs& a, const Cut& e) {
+    t0 = 0;
+    if (++q * 2 * a.tpt >= rows) {
+      q = 0;
+      if (++h == a.Hkv) {
+        h = 0;
+        do {
+          if (++b >= a.B || b > e.b) return false;
+          sequence(a);
+        } while (rows == 0);
+      }
+    }
+    item(2 * a.tpt);
+    return clip(e);
+  }
+};
+
+// Steps of a CTA in order, one row tile against one key tile each; step n belongs to slot n % 2.
+struct Steps {
+  Piece p;
+  int i, n;            // step within the piece, steps of the piece
+  bool more;
+  __device__ __forceinline__ void start(const ChunkAttnArgs& a, const Cut& s, const Cut& e) {
+    more = p.first(a, s, e);
+    i = 0;
+    n = more ? p.ops() : 0;
+  }
+  __device__ __forceinline__ void step(const ChunkAttnArgs& a, const Cut& e) {
+    if (++i == n) {
+      more = p.next(a, e);
+      i = 0;
+      n = more ? p.ops() : 0;
+    }
+  }
+  __device__ __forceinline__ int tile() const { return p.t0 + (p.dual ? i >> 1 : i); }
+  __device__ __forceinline__ bool opens() const { return !p.dual || !(i & 1); }    // first use of its tile
+  __device__ __forceinline__ bool closes() const { return !p.dual || (i & 1); }    // last use
+};
+
+// Flags of a CTA for the joining kernel.
+constexpr int F_OPENS = 1;      // its last piece starts an item and does not end it (partial slot 1)
+constexpr int F_JOINS = 2;      // its first piece continues an item (partial slot 0) ...
+constexpr int F_ENDS = 4;       // ... to its end
+
+__global__ void __launch_bounds__(THREADS, 1)
+chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const ChunkAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* full = bars;                   // [ST] tile ready
+  uint64_t* empty = full + ST;             // [ST] its products done
+  uint64_t* land = empty + ST;             // [ST] load landed of a V tile whose end is to be zeroed
+  uint64_t* q_full = land + ST;            // [2]  row tile of a slot ready
+  uint64_t* q_empty = q_full + 2;          // [2]  its last Q K^T of a piece done
+  uint64_t* s_full = q_empty + 2;          // [2]  scores in TMEM (and the slot's P V before them done)
+  uint64_t* p_full = s_full + 2;           // [2]  P in TMEM, O rescaled
+  uint64_t* o_full = p_full + 2;           // [2]  last P V of a piece done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
+  Cut* s_cut = reinterpret_cast<Cut*>(smem + OFF_SCHED);                          // [2] start, end
+  long long* s_sum = reinterpret_cast<long long*>(smem + OFF_SCHED + 32);         // [12] warp sums
+  float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = 2 * a.tpt;
+  if ((smem_u32(smem) & 1023u) != 0) {     // (the swizzled tiles need it; the same for every thread)
+    if (tid == 0) set_status(a.status, 0x7F3u);
     return;
   }
-  const int keys = ctx + (r - c0) + 1, g = h / a.G;
-  const uint2 qv = *reinterpret_cast<const uint2*>(a.Q + (size_t)r * a.ldq + (size_t)h * D + lane * 4);
-  const float q0 = bf16lo(qv.x), q1 = bf16hi(qv.x), q2 = bf16lo(qv.y), q3 = bf16hi(qv.y);
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-  for (int t = 0; t * PAGE < keys; ++t) {
-    int page = a.block_table[(size_t)lo * a.max_pages + t];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) set_status(a.status, 0x7F2u);
-      page = 0;
+  if (tid == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    for (int i = 0; i < 3 * ST; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
     }
-    const size_t base = ((size_t)g * a.num_pages + page) * PAGE * D + lane * 4;
-    const int n = min(PAGE, keys - t * PAGE);
-    for (int k = 0; k < n; ++k) {
-      const uint2 kv = *reinterpret_cast<const uint2*>(a.Kpool + base + (size_t)k * D);
-      const uint2 vv = *reinterpret_cast<const uint2*>(a.Vpool + base + (size_t)k * D);
-      float x = q0 * bf16lo(kv.x) + q1 * bf16hi(kv.x) + q2 * bf16lo(kv.y) + q3 * bf16hi(kv.y);
+    fence_barrier_init();
+    s_cut[0] = s_cut[1] = Cut{a.B, 0, 0, 0};
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, TMEM_COLS);
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- cuts: total cost, then this CTA's two cuts from the running sum
+  {
+    long long total = 0, own = 0;
+    bool any_bad = false;
+    for (int b = tid; b < a.B; b += THREADS) {
+      bool bad;
+      const Seq s = seq_of(a, b, &bad);
+      any_bad |= bad;
+      own = head_cost(s, T) * a.Hkv;
+      total += own;
+    }
+    if (any_bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      x *= a.scale_log2;
-      const float mn = fmaxf(m, x), f = exp2f(m - mn), e = exp2f(x - mn);
-      m = mn;
-      l = l * f + e;
-      o0 = o0 * f + e * bf16lo(vv.x);
-      o1 = o1 * f + e * bf16hi(vv.x);
-      o2 = o2 * f + e * bf16lo(vv.y);
-      o3 = o3 * f + e * bf16hi(vv.y);
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_sum[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w];
+    const long long x[2] = {total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x};
+    long long before = 0;
+    for (int base = 0; base < a.B; base += THREADS) {
+      const int b = base + tid;
+      if (a.B > THREADS) own = b < a.B ? head_cost(seq_of(a, b), T) * a.Hkv : 0;
+      else if (b >= a.B) own = 0;
+      long long incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      long long off = before;
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) off += s_sum[w];
+        before += s_sum[w];
+      }
+      const long long lo = off + incl - own;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (x[k] >= lo && x[k] < lo + own) s_cut[k] = cut_in(seq_of(a, b), b, T, x[k] - lo);
     }
   }
-  const float inv = 1.f / l;
-  *reinterpret_cast<uint2*>(a.O + (size_t)r * a.ldo + (size_t)h * D + lane * 4) =
-      make_uint2(pack_bf16x2(o0 * inv, o1 * inv), pack_bf16x2(o2 * inv, o3 * inv));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Cut cut0 = s_cut[0], cut1 = s_cut[1];
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ K and V tiles
+    // in the order of their first products: V of step n, then K of step n + 2
+    Steps k, v;
+    k.start(a, cut0, cut1);
+    v = k;
+    int idx = 0, pages_k = 0, pages_v = 0;
+    bool ok = true;
+    uint32_t landed = 0;                   // stages whose last load signals `land`
+    uint32_t n_land = 0;                   // its phase, one bit per stage
+    const uint64_t pol = l2_policy_evict_first();
+    auto load = [&](Steps& c, int& pages, bool is_v) {
+      const int t = c.tile();
+      // 32 page ids at a time, one per lane
+      if (c.i == 0 || ((t - c.p.t0) & 31) == 0) {
+        const int tl = t + lane;
+        pages = tl < c.p.t1 ? a.block_table[(size_t)c.p.b * a.max_pages + tl] : 0;
+        if (pages < 0 || pages >= a.num_pages) {
+          set_status(a.status, 0x7F2u);
+          pages = 0;
+        }
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, (t - c.p.t0) & 31);
+      const int st = idx % ST;
+      if (idx >= ST) ok = ok && mbar_wait(&empty[st], (uint32_t)((idx / ST - 1) & 1), a.status, 0x711u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const bool tail = is_v && t == c.p.nt - 1 && (c.p.keys() & 15);
+      uint64_t* bar = tail ? &land[st] : &full[st];
+      if (lane == 0) {
+        const CUtensorMap* tm = is_v ? &tmV : &tmK;
+        uint8_t* dst = smem + OFF_RING + st * TILE;
+        const int z = c.p.h * a.num_pages + page;
+        mbar_arrive_expect_tx(bar, TILE);
+        if (c.p.rows <= T) {               // read once
+          tma_load_3d_hint(dst, tm, bar, 0, 0, z, pol);
+          tma_load_3d_hint(dst + HALF, tm, bar, 64, 0, z, pol);
+        } else {
+          tma_load_3d(dst, tm, bar, 0, 0, z);
+          tma_load_3d(dst + HALF, tm, bar, 64, 0, z);
+        }
+      }
+      if (tail) {
+        landed |= 1u << st;
+        n_land ^= 1u << st;
+      } else {
+        landed &= ~(1u << st);
+      }
+      ++idx;
+    };
+    for (int lead = 0; lead < 2 && k.more && ok; ++lead) {
+      if (k.opens()) load(k, pages_k, false);
+      k.step(a, cut1);
+    }
+    while (v.more && ok) {
+      if (v.opens()) load(v, pages_v, true);
+      v.step(a, cut1);
+      if (k.more && ok) {
+        if (k.opens()) load(k, pages_k, false);
+        k.step(a, cut1);
+      }
+    }
+    if (!ok) {                             // gave up: see the copies in flight land before leaving
+      for (int j = idx > ST ? idx - ST : 0; j < idx; ++j) {
+        const int st = j % ST;
+        if ((landed >> st) & 1u) mbar_wait(&land[st], ((n_land >> st) & 1u) ^ 1u, a.status, 0x712u);
+        else mbar_wait(&full[st], (uint32_t)((j / ST) & 1), a.status, 0x712u);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
+      Steps s, v;
+      s.start(a, cut0, cut1);
+      v = s;
+      int idx = 0, st_k = 0, st_v = 0;
+      uint32_t ns = 0, nv = 0;             // steps done
+      uint32_t n_q[2] = {0, 0};
+      bool ok = true;
+      auto take = [&]() {
+        const int st = idx % ST;
+        ok = ok && mbar_wait(&full[st], (uint32_t)((idx / ST) & 1), a.status, 0x721u);
+        ++idx;
+        return st;
+      };
+      auto scores = [&]() {
+        const int sl = ns & 1;
+        if (s.i < 2) {
+          ok = ok && mbar_wait(&q_full[sl], (uint32_t)(n_q[sl] & 1), a.status, 0x722u);
+          ++n_q[sl];
+        }
+        if (s.opens()) st_k = take();
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t k_addr = smem_u32(smem + OFF_RING + st_k * TILE);
+        const uint32_t q_addr = smem_u32(smem + OFF_Q + sl * TILE);
+        const uint32_t d = tmem + (uint32_t)sl * KT;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
+          umma_bf16(d, umma_desc_sw128(q_addr + off), umma_desc_sw128(k_addr + off), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        if (s.closes()) umma_commit(&empty[st_k]);
+        umma_commit(&s_full[sl]);
+        if (s.i >= s.n - 2) umma_commit(&q_empty[sl]);
+        ++ns;
+        s.step(a, cut1);
+      };
+      for (int lead = 0; lead < 2 && s.more && ok; ++lead) scores();
+      while (v.more && ok) {
+        const int sl = nv & 1;
+        if (v.opens()) st_v = take();
+        ok = ok && mbar_wait(&p_full[sl], (uint32_t)((nv >> 1) & 1), a.status, 0x723u);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t v_addr = smem_u32(smem + OFF_RING + st_v * TILE);
+        const uint32_t p = tmem + (uint32_t)sl * KT, o = tmem + 2 * KT + (uint32_t)sl * D;
+        const int left = v.p.keys() - v.tile() * KT;
+        const int steps = left >= KT ? 8 : (left + 15) >> 4;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (kk < steps)
+            umma_bf16_ts(o, p + kk * 8, desc_mn(v_addr + kk * 16 * 128, HALF), idesc_pv,
+                         (v.i >= 2 || kk > 0) ? 1u : 0u);
+        if (v.closes()) umma_commit(&empty[st_v]);
+        if (v.i >= v.n - 2) umma_commit(&o_full[sl]);
+        ++nv;
+        v.step(a, cut1);
+        if (s.more && ok) scores();
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ Q tiles, ends of the last V tiles
+    Piece p, before;
+    bool more = p.first(a, cut0, cut1), had = false, ok = true;
+    uint32_t n_q[2] = {0, 0}, n_land = 0;
+    int n0 = 0, tiles = 0;                 // steps and key tiles of the pieces so far
+    const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * D * 2);
+    while ((more || had) && ok) {
+      if (more) {
+        const int n = min(2, p.ops());
+        for (int i = 0; i < n; ++i) {
+          const int sl = (n0 + i) & 1;
+          if (n_q[sl] > 0) ok = ok && mbar_wait(&q_empty[sl], (n_q[sl] - 1) & 1, a.status, 0x731u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++n_q[sl];
+          if (lane == 0) {
+            uint8_t* dst = smem + OFF_Q + sl * TILE;
+            const int row = p.r0 + p.q * T + (p.dual ? i * a.tpt : 0);
+            mbar_arrive_expect_tx(&q_full[sl], q_bytes);
+            tma_load_3d(dst, &tmQ, &q_full[sl], 0, p.h * a.G, row);
+            tma_load_3d(dst + HALF, &tmQ, &q_full[sl], 64, p.h * a.G, row);
+          }
+        }
+        if (!ok) break;
+      }
+      // the piece before: rows of its last V tile from the sequence's last key to the next multiple of 16
+      if (had && before.t1 == before.nt && (before.keys() & 15)) {
+        // loads before that tile: every K and V before it, its own K, and with one row tile the K of
+        // the step after it
+        const int st = (2 * (tiles - 1) + 1 + (!before.dual && more ? 1 : 0)) % ST;
+        ok = mbar_wait(&land[st], (n_land >> st) & 1u, a.status, 0x732u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        n_land ^= 1u << st;
+        uint8_t* vt = smem + OFF_RING + st * TILE;
+        const int r0 = before.keys() - (before.nt - 1) * KT, r1 = (r0 + 15) & ~15;
+        for (int r = r0 + (lane >> 4); r < r1; r += 2) {
+          const int ch = lane & 15;
+          *reinterpret_cast<uint4*>(vt + (ch >> 3) * HALF + sw128_off(r, (ch & 7) * 8)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+      had = more;
+      if (more) {
+        before = p;
+        n0 += p.ops();
+        tiles += p.t1 - p.t0;
+        more = p.next(a, cut1);
+      }
+    }
+    if (!ok && lane == 0)                  // gave up: see the Q copies land before leaving
+      for (int sl = 0; sl < 2; ++sl)
+        if (n_q[sl] > 0) mbar_wait(&q_full[sl], (n_q[sl] - 1) & 1, a.status, 0x733u);
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue of slot sl
+    const int sl = warp >> 2, row = tid & 127;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + (uint32_t)sl * KT + lanes, t_o = tmem + 2 * KT + (uint32_t)sl * D + lanes;
+    const int row_tok = row / a.G, row_head = row - row_tok * a.G;
+    const bool row_used = row_tok < a.tpt;
+    const float scale = a.scale_log2;
+    uint32_t n_s = 0, n_o[2] = {0, 0};
+    int n0 = 0, flags = 0;
+    bool ok = true;
+    Piece p;
+    bool more = p.first(a, cut0, cut1);
+    Cut opened{0, 0, 0, 0};
+    while (more) {
+      const int n = p.ops();
+      const int i0 = sl ^ (n0 & 1);        // this slot's first step of the piece
+      const int x = p.dual ? i0 : 0;       // its row tile
+      const int tok = x * a.tpt + row_tok;
+      const bool used = row_used && tok < p.tok;
+      const int pos = p.pos + min(tok, p.tok - 1);        // the row sees keys 0 .. pos
+      const int first_pos = p.pos + min(x * a.tpt, p.tok - 1);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int i = i0; i < n; i += 2) {
+        const int key0 = (p.t0 + (p.dual ? i >> 1 : i)) * KT;
+        ok = ok && mbar_wait(&s_full[sl], n_s & 1, a.status, 0x741u);
+        ++n_s;
+        tc_fence_after();
+        uint32_t r[128];
+        tmem_ld_cols128(t_s, r);
+        if (key0 + KT - 1 > first_pos) {
+          const int lim = pos - key0;
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k > lim) r[k] = 0xff800000u;              // -inf
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 128; k += 2)
+          mx4[(k >> 1) & 3] = fmaxf(fmaxf(mx4[(k >> 1) & 3], __uint_as_float(r[k])), __uint_as_float(r[k + 1]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale;
+        // the running maximum follows only when a tile exceeds it by more than 8 (2^8 in the weights): O and
+        // the sum keep one common reference, so the result is the same and O is rarely rescaled
+        const float m_new = mx > m_run + 8.f ? mx : m_run;
+        const bool grew = m_new != m_run;
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = ex2(m_run - base);
+        m_run = m_new;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(-base, -base);
+        uint32_t pk[64];
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          float2 e = fma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nb2);
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          sum[k & 1] = add2(sum[k & 1], e);
+          pk[k] = cvt_bf16x2(e.x, e.y);
+        }
+        tmem_st_cols32(t_s, pk);
+        tmem_st_cols32(t_s + 32, pk + 32);
+        const float2 s2 = add2(sum[0], sum[1]);
+        l_run = l_run * alpha + (s2.x + s2.y);
+        // O is whole here: the scores' barrier came after the slot's P V before them
+        if (i >= 2 && __any_sync(0xffffffffu, grew)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld_cols32(t_o + c, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st_cols32(t_o + c, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sl]);
+      }
+      // ---- the piece's end
+      const bool whole = p.t0 == 0 && p.t1 == p.nt;
+      const int part = p.t0 > 0 ? 0 : 1;                  // workspace slot of a piece
+      if (!whole) {
+        if (p.t0 > 0) flags |= F_JOINS | (p.t1 == p.nt ? F_ENDS : 0);
+        else {
+          flags |= F_OPENS;
+          opened = Cut{p.b, p.h, p.q, 0};
+        }
+      }
+      uint16_t* orow = a.O + (size_t)(p.r0 + p.q * T + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D;
+      const size_t prow = ((size_t)blockIdx.x * 2 + part) * (2 * TM) + x * TM + row;
+      auto out = [&](int c, const float* v, float f) {    // 32 dims from c
+        if (!used) return;
+        if (whole) {
+#pragma unroll
+          for (int d = 0; d < 32; d += 8)
+            *reinterpret_cast<uint4*>(orow + c + d) =
+                make_uint4(cvt_bf16x2(v[d] * f, v[d + 1] * f), cvt_bf16x2(v[d + 2] * f, v[d + 3] * f),
+                           cvt_bf16x2(v[d + 4] * f, v[d + 5] * f), cvt_bf16x2(v[d + 6] * f, v[d + 7] * f));
+        } else {
+#pragma unroll
+          for (int d = 0; d < 32; d += 4)
+            __stcg(reinterpret_cast<float4*>(a.part_o + prow * D + c + d), make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
+        }
+      };
+      if (p.dual) {
+        ok = ok && mbar_wait(&o_full[sl], n_o[sl] & 1, a.status, 0x742u);
+        ++n_o[0];
+        ++n_o[1];
+        tc_fence_after();
+        const float inv = 1.f / l_run;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld_cols<32>(t_o + c, v);
+          out(c, v, inv);
+        }
+        if (!whole && used) a.part_ml[prow] = make_float2(m_run, l_run);
+        tc_fence_before();
+      } else {
+        // the slots' sums joined; each slot's warps write half of the dims
+        const int f_slot = n0 & 1;                        // slot of the piece's first step
+        for (int j = 0; j < 2; ++j)
+          if (j == f_slot || n > 1) {
+            ok = ok && mbar_wait(&o_full[j], n_o[j] & 1, a.status, 0x743u);
+            ++n_o[j];
+          }
+        tc_fence_after();
+        s_ml[sl * TM + row] = make_float2(m_run, l_run);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float2 other = s_ml[(sl ^ 1) * TM + row];
+        const float m = fmaxf(m_run, other.x), base = m == -INFINITY ? 0.f : m;
+        const float fa = ex2(m_run - base), fb = ex2(other.x - base);
+        const float l = l_run * fa + other.y * fb, inv = 1.f / l;
+        const bool has_a = n > 1 || sl == f_slot, has_b = n > 1 || sl != f_slot;
+        const uint32_t t_a = t_o, t_b = tmem + 2 * KT + (uint32_t)(sl ^ 1) * D + lanes;
+#pragma unroll 1
+        for (int c = sl * 64; c < sl * 64 + 64; c += 32) {
+          float va[32], vb[32];
+          tmem_ld_cols<32>(t_a + c, va);
+          tmem_ld_cols<32>(t_b + c, vb);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) va[k] = (has_a ? va[k] * fa : 0.f) + (has_b ? vb[k] * fb : 0.f);
+          out(c, va, inv);
+        }
+        if (!whole && used && sl == 0) a.part_ml[prow] = make_float2(m, l);
+        tc_fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");    // O and s_ml free again
+      }
+      n0 += n;
+      more = p.next(a, cut1);
+    }
+    if (tid == 0) a.part_item[blockIdx.x] = make_int4(flags, opened.b, opened.h, opened.q);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the pieces of every item that a cut fell into: block (c, y) takes rows y * 16 .. of the item that CTA c
+// opened and did not end, one warp per row, four dims per lane; pieces in CTA order.
+constexpr int JOIN_ROWS = 16;
+__global__ void __launch_bounds__(128) chunk_join_kernel(const ChunkAttnArgs a, int grid) {
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 it = a.part_item[c0];
+  if (!(it.x & F_OPENS)) return;
+  Piece p;
+  p.b = it.y; p.h = it.z; p.q = it.w;
+  p.sequence(a);
+  p.item(2 * a.tpt);
+  int c1 = c0;                             // the CTA that ends the item
+  do {
+    ++c1;
+  } while (c1 < grid - 1 && (a.part_item[c1].x & (F_JOINS | F_ENDS)) != (F_JOINS | F_ENDS));
+  for (int rr = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5); rr < (int)(blockIdx.y + 1) * JOIN_ROWS; rr += 4) {
+    const int m = rr & 127, t = m / a.G, tok = (rr >> 7) * a.tpt + t;
+    if (t >= a.tpt || tok >= p.tok) continue;
+    auto at = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * (2 * TM) + rr; };
+    auto has = [&](int c) { return c == c0 || (a.part_item[c].x & F_JOINS); };
+    float mx = -INFINITY;
+    for (int c = c0; c <= c1; ++c)
+      if (has(c)) mx = fmaxf(mx, __ldcg(&a.part_ml[at(c)]).x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      if (!has(c)) continue;
+      const float2 ml = __ldcg(&a.part_ml[at(c)]);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(c) * D) + lane);
+      const float f = ex2(ml.x - mx);
+      l += ml.y * f;
+      o.x += v.x * f;
+      o.y += v.y * f;
+      o.z += v.z * f;
+      o.w += v.w * f;
+    }
+    const float inv = 1.f / l;
+    *reinterpret_cast<uint2*>(a.O + (size_t)(p.r0 + p.q * 2 * a.tpt + tok) * a.ldo +
+                              (size_t)(p.h * a.G + m - t * a.G) * D + lane * 4) =
+        make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_k(chunk_attention_kernel, dim3(a.M, (a.Hkv * a.G + 3) / 4), dim3(128), 0, s, a);
+cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const ChunkAttnArgs& a, int grid, cudaStream_t s) {
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  cudaError_t e = launch_k(chunk_attention_kernel, dim3(grid), dim3(THREADS), SMEM, s, tq, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  e = launch_k(chunk_join_kernel, dim3(grid, 2 * TM / JOIN_ROWS), dim3(128), 0, s, a, grid);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -214,11 +214,18 @@ struct ChunkAttnArgs {
   const uint16_t* Kpool; const uint16_t* Vpool;
   const int32_t* block_table;
   int num_pages, max_pages, Hkv, G;
-  float scale_log2;                     // softmax scale * log2(e)
+  int tpt;                              // tokens per row tile: 128 / G
+  float scale_log2;                     // softmax scale * log2(e), > 0
   uint16_t* O; int ldo;
+  // pieces of items that two CTAs or more share: rows of slot s of CTA c at ((2 c + s) 256 + row)
+  float* part_o;                        // [grid][2][256][128] unnormalised outputs
+  float2* part_ml;                      // [grid][2][256] running maximum (times scale_log2) and sum
+  int4* part_item;                      // [grid] flags; sequence, kv head and index of the item it opened
   unsigned* status;
 };
-cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t s);
+// Q map: boxes of 64 dims x G heads x tpt rows; K / V maps: boxes of 64 dims x one page.  `grid` CTAs.
+cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const ChunkAttnArgs& a, int grid, cudaStream_t s);
 
 // ---- rejection sampler
 cudaError_t launch_reject_sample(const float* P, const float* Q, const int32_t* draft,

@@ -83,8 +83,18 @@ def attn_args(S, **kw):
     (dict(num_pages=0), "SPEC_EINVAL"), (dict(max_pages=0), "SPEC_EINVAL"), (dict(Hq=7), "SPEC_EINVAL"),
     (dict(Hq=0), "SPEC_EINVAL"), (dict(Hq=258), "SPEC_EUNSUPPORTED"), (dict(ldq=1016), "SPEC_EINVAL"),
     (dict(ldo=1028), "SPEC_EINVAL"), (dict(scale=float("nan")), "SPEC_EINVAL"), (dict(scale=float("inf")), "SPEC_EINVAL"),
-    (dict(scale=-0.1), "SPEC_EINVAL"),
+    (dict(scale=-0.1), "SPEC_EINVAL"), (dict(ws_bytes=16), "SPEC_EINVAL"), (dict(ws=None, ws_bytes=0), "SPEC_EINVAL"),
+    (dict(ws=ODD), "SPEC_EINVAL"),
 ])
 def test_attention_refusals(S, kw, code):
     assert attn_args(S, **kw) == getattr(S, code)
     assert S._lib.spec_last_error() and S._lib.spec_launches() == 0
+
+
+def test_workspace_query_is_host_only(S):
+    n = S.spec_chunk_attention_workspace_bytes(8, 1000, 32, 8, 128, 64)
+    assert n > 64 * 1024
+    # a batch with more rows or sequences never needs less
+    assert S.spec_chunk_attention_workspace_bytes(9, 1000, 32, 8, 128, 64) >= n
+    assert S.spec_chunk_attention_workspace_bytes(8, 2000, 32, 8, 128, 64) >= n
+    assert S.spec_chunk_attention_workspace_bytes(0, 1000, 32, 8, 128, 64) == 0
