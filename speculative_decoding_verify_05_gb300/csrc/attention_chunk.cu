@@ -19,10 +19,12 @@
 // sequence, so one graph serves any lengths).  Where a cut falls into an item its pieces go to the
 // workspace as unnormalised O, maximum and sum, and a second small kernel joins them in CTA order.
 //
-// Roles (11 warps): 0-3 and 4-7 softmax and epilogue of slot 0 and 1 (thread = TMEM lane = row); 8 loads K
+// Roles (12 warps): 0-3 and 4-7 softmax and epilogue of slot 0 and 1 (thread = TMEM lane = row); 8 loads K
 // and V tiles by TMA into one ring of 5; 9 issues the MMAs; 10 loads the Q tiles and zeroes the rows of
 // a sequence's last V tile behind its last key (up to the next multiple of 16, where the product
-// stops), which may hold anything (0 * NaN would reach the sums).
+// stops), which may hold anything (0 * NaN would reach the sums); 11 walks the batch and posts each of
+// the CTA's pieces (consecutive key tiles of one item) to a small ring that the others read, so that
+// none of them waits for the lengths or keeps a walk in registers.
 #include "common.cuh"
 #include "internal.h"
 
@@ -35,12 +37,15 @@ constexpr int TM = 128;                   // rows per row tile
 constexpr int ST = 5;                     // ring stages of one K or V tile
 constexpr int HALF = 128 * 128;           // 128 rows x 64 bf16 (128-byte swizzled rows), 16 KB
 constexpr int TILE = 2 * HALF;
-constexpr int THREADS = 352;
+constexpr int THREADS = 384;
+constexpr int REGS_ALL = 168, REGS_SOFTMAX = 208, REGS_OTHER = 80;
+static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * REGS_ALL, "register split");
 constexpr int OFF_Q = 0;                  // two row tiles
 constexpr int OFF_RING = 2 * TILE;
 constexpr int OFF_BAR = OFF_RING + ST * TILE;
-constexpr int N_BARS = 3 * ST + 10;
-constexpr int OFF_SCHED = OFF_BAR + (N_BARS + 1) * 8;
+constexpr int PR = 4;                     // posted pieces
+constexpr int N_BARS = 3 * ST + 14 + 2 * PR;
+constexpr int OFF_SCHED = OFF_BAR + (N_BARS + 1) * 8;   // cuts and warp sums of the setup, then the posted pieces
 constexpr int OFF_ML = OFF_BAR + 512;     // (max, sum) of 128 rows for each slot
 constexpr int SMEM = OFF_ML + 2 * TM * 8;
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
@@ -191,81 +196,101 @@ __device__ Cut cut_in(const Seq& s, int b, int T, long long x) {
   return c;
 }
 
-// A CTA's consecutive key tiles of one item.
+// A CTA's consecutive key tiles of one item, as posted.
 struct Piece {
   int b, h, q;
   int t0, t1, nt;      // tiles t0 .. t1 - 1 of the item's nt
-  int r0, rows, ctx;   // its sequence
+  int row0;            // first packed row
   int tok, pos;        // tokens of the item, position of the first
-  bool dual;           // two row tiles
+  int dual;            // two row tiles
+  int once;            // the sequence's only item of this head: its keys are read once
+  int more;            // 0: no piece, the CTA is done
 
   __device__ __forceinline__ int ops() const { return dual ? 2 * (t1 - t0) : t1 - t0; }
   __device__ __forceinline__ int keys() const { return pos + tok; }
+  __device__ __forceinline__ bool tail() const { return t1 == nt && (keys() & 15) != 0; }
+};
+static_assert(sizeof(Piece) == 48 && OFF_SCHED + PR * 48 <= OFF_ML && OFF_SCHED % 16 == 0, "posted pieces");
+
+// The walk over a CTA's pieces.
+struct Walk {
+  Piece p;
+  Seq s;
   __device__ __forceinline__ void item(int T) {
-    tok = min(T, rows - q * T);
-    pos = ctx + q * T;
-    nt = (pos + tok + KT - 1) / KT;
-    dual = tok > T / 2;
-  }
-  __device__ __forceinline__ void sequence(const ChunkAttnArgs& a) {
-    const Seq s = seq_of(a, b);
-    r0 = s.r0;
-    rows = s.rows;
-    ctx = s.ctx;
+    p.tok = min(T, s.rows - p.q * T);
+    p.row0 = s.r0 + p.q * T;
+    p.pos = s.ctx + p.q * T;
+    p.nt = (p.pos + p.tok + KT - 1) / KT;
+    p.dual = p.tok > T / 2;
+    p.once = s.rows <= T;
   }
   // the piece ends at the item's end or at the CTA's
-  __device__ __forceinline__ bool clip(const Cut& e) {
-    t1 = nt;
-    if (b == e.b && h == e.h && q == e.q) t1 = e.t;
-    else if (b > e.b || (b == e.b && (h > e.h || (h == e.h && q > e.q)))) t1 = 0;
-    return t1 > t0;
+  __device__ __forceinline__ void clip(const Cut& e) {
+    p.t1 = p.nt;
+    if (p.b == e.b && p.h == e.h && p.q == e.q) p.t1 = e.t;
+    else if (p.b > e.b || (p.b == e.b && (p.h > e.h || (p.h == e.h && p.q > e.q)))) p.t1 = 0;
+    p.more = p.t1 > p.t0;
   }
-  // first piece of [s, e); false: none
-  __device__ __forceinline__ bool first(const ChunkAttnArgs& a, const Cut& s, const Cut& e) {
-    if (s.b >= a.B) return false;
-    b = s.b; h = s.h; q = s.q; t0 = s.t;
-    sequence(a);
+  // first piece of [c, e)
+  __device__ __forceinline__ void first(const ChunkAttnArgs& a, const Cut& c, const Cut& e) {
+    p.more = 0;
+    if (c.b >= a.B) return;
+    p.b = c.b; p.h = c.h; p.q = c.q; p.t0 = c.t;
+    s = seq_of(a, p.b);
     item(2 * a.tpt);
-    if (t0 >= nt) return next(a, e);
-    return clip(e);
+    if (p.t0 >= p.nt) next(a, e);
+    else clip(e);
   }
-  __device__ __forceinline__ bool next(const ChunkAttnArgs& a, const Cut& e) {
-    t0 = 0;
-    if (++q * 2 * a.tpt >= rows) {
-      q = 0;
-      if (++h == a.Hkv) {
-        h = 0;
+  __device__ __forceinline__ void next(const ChunkAttnArgs& a, const Cut& e) {
+    p.t0 = 0;
+    p.more = 0;
+    if (++p.q * 2 * a.tpt >= s.rows) {
+      p.q = 0;
+      if (++p.h == a.Hkv) {
+        p.h = 0;
         do {
-          if (++b >= a.B || b > e.b) return false;
-          sequence(a);
-        } while (rows == 0);
+          if (++p.b >= a.B || p.b > e.b) return;
+          s = seq_of(a, p.b);
+        } while (s.rows == 0);
       }
     }
     item(2 * a.tpt);
-    return clip(e);
+    clip(e);
   }
 };
 
-// Steps of a CTA in order, one row tile against one key tile each; step n belongs to slot n % 2.
+// Steps of a CTA in order, one row tile against one key tile each; step n belongs to slot n % 2.  A cursor over
+// them that reads the posted pieces.
 struct Steps {
-  Piece p;
-  int i, n;            // step within the piece, steps of the piece
-  bool more;
-  __device__ __forceinline__ void start(const ChunkAttnArgs& a, const Cut& s, const Cut& e) {
-    more = p.first(a, s, e);
+  const Piece* ring;
+  uint64_t* posted;
+  unsigned* status;
+  unsigned site;
+  const Piece* p;
+  int k;               // pieces so far
+  int i, n;            // step within the piece, steps of the piece (0: done)
+  bool ok, dual;
+  __device__ __forceinline__ void start(const Piece* r, uint64_t* post, unsigned* st, unsigned where) {
+    ring = r; posted = post; status = st; site = where;
+    k = 0;
+    ok = true;
+    open();
+  }
+  __device__ __forceinline__ void open() {
+    ok = ok && mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), status, site);
+    p = ring + k % PR;
+    ++k;
     i = 0;
-    n = more ? p.ops() : 0;
+    dual = ok && p->dual;
+    n = ok && p->more ? p->ops() : 0;
   }
-  __device__ __forceinline__ void step(const ChunkAttnArgs& a, const Cut& e) {
-    if (++i == n) {
-      more = p.next(a, e);
-      i = 0;
-      n = more ? p.ops() : 0;
-    }
+  __device__ __forceinline__ void step() {
+    if (++i == n) open();
   }
-  __device__ __forceinline__ int tile() const { return p.t0 + (p.dual ? i >> 1 : i); }
-  __device__ __forceinline__ bool opens() const { return !p.dual || !(i & 1); }    // first use of its tile
-  __device__ __forceinline__ bool closes() const { return !p.dual || (i & 1); }    // last use
+  __device__ __forceinline__ bool more() const { return n > 0; }
+  __device__ __forceinline__ int tile() const { return p->t0 + (dual ? i >> 1 : i); }
+  __device__ __forceinline__ bool opens() const { return !dual || !(i & 1); }    // first use of its tile
+  __device__ __forceinline__ bool closes() const { return !dual || (i & 1); }    // last use
 };
 
 // Flags of a CTA for the joining kernel.
@@ -284,8 +309,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint64_t* q_full = land + ST;            // [2]  row tile of a slot ready
   uint64_t* q_empty = q_full + 2;          // [2]  its last Q K^T of a piece done
   uint64_t* s_full = q_empty + 2;          // [2]  scores in TMEM (and the slot's P V before them done)
-  uint64_t* p_full = s_full + 2;           // [2]  P in TMEM, O rescaled
+  uint64_t* p_half = s_full + 2;           // [2]  P of keys 0-63 in TMEM, O rescaled
+  uint64_t* p_full = p_half + 2;           // [2]  all of P
   uint64_t* o_full = p_full + 2;           // [2]  last P V of a piece done
+  uint64_t* pair = o_full + 2;             // [2]  both slots' softmax warps: sums exchanged, O read
+  uint64_t* posted = pair + 2;             // [PR] piece posted
+  uint64_t* taken = posted + PR;           // [PR] everyone is done with its entry
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
   Cut* s_cut = reinterpret_cast<Cut*>(smem + OFF_SCHED);                          // [2] start, end
   long long* s_sum = reinterpret_cast<long long*>(smem + OFF_SCHED + 32);         // [12] warp sums
@@ -306,8 +335,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
+      mbar_init(&pair[i], 8);
+    }
+    for (int i = 0; i < PR; ++i) {
+      mbar_init(&posted[i], 1);
+      mbar_init(&taken[i], 11);              // loads, MMA, Q tiles, 8 softmax warps
     }
     fence_barrier_init();
     s_cut[0] = s_cut[1] = Cut{a.B, 0, 0, 0};
@@ -365,42 +400,62 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Cut cut0 = s_cut[0], cut1 = s_cut[1];
+  Piece* ring = reinterpret_cast<Piece*>(smem + OFF_SCHED);
+  __syncthreads();                           // (the cuts lie where the pieces are posted)
 
-  if (warp == 8) {
+  // the softmax warps hold a row of scores each: the other warpgroup leaves them its registers
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+  if (warp == 11) {
+    // ------------------------------------------------------------ pieces
+    if (lane == 0) {
+      Walk w;
+      w.first(a, cut0, cut1);
+      for (int k = 0;; ++k) {
+        if (k >= PR && !mbar_wait(&taken[k % PR], (uint32_t)((k / PR - 1) & 1), a.status, 0x701u)) break;
+        ring[k % PR] = w.p;
+        mbar_arrive(&posted[k % PR]);
+        if (!w.p.more) break;
+        w.next(a, cut1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
     // ------------------------------------------------------------ K and V tiles
     // in the order of their first products: V of step n, then K of step n + 2
     Steps k, v;
-    k.start(a, cut0, cut1);
+    k.start(ring, posted, a.status, 0x713u);
     v = k;
     int idx = 0, pages_k = 0, pages_v = 0;
-    bool ok = true;
+    bool ok = k.ok;
     uint32_t landed = 0;                   // stages whose last load signals `land`
     uint32_t n_land = 0;                   // its phase, one bit per stage
     const uint64_t pol = l2_policy_evict_first();
-    auto load = [&](Steps& c, int& pages, bool is_v) {
-      const int t = c.tile();
+    auto load = [&](const Steps& c, int& pages, bool is_v) {
+      const Piece* p = c.p;
+      const int t = c.tile(), dt = t - p->t0;
       // 32 page ids at a time, one per lane
-      if (c.i == 0 || ((t - c.p.t0) & 31) == 0) {
+      if ((dt & 31) == 0) {
         const int tl = t + lane;
-        pages = tl < c.p.t1 ? a.block_table[(size_t)c.p.b * a.max_pages + tl] : 0;
+        pages = tl < p->t1 ? a.block_table[(size_t)p->b * a.max_pages + tl] : 0;
         if (pages < 0 || pages >= a.num_pages) {
           set_status(a.status, 0x7F2u);
           pages = 0;
         }
       }
-      const int page = __shfl_sync(0xffffffffu, pages, (t - c.p.t0) & 31);
+      const int page = __shfl_sync(0xffffffffu, pages, dt & 31);
       const int st = idx % ST;
       if (idx >= ST) ok = ok && mbar_wait(&empty[st], (uint32_t)((idx / ST - 1) & 1), a.status, 0x711u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      const bool tail = is_v && t == c.p.nt - 1 && (c.p.keys() & 15);
+      const bool tail = is_v && t == p->nt - 1 && (p->keys() & 15);
       uint64_t* bar = tail ? &land[st] : &full[st];
       if (lane == 0) {
         const CUtensorMap* tm = is_v ? &tmV : &tmK;
         uint8_t* dst = smem + OFF_RING + st * TILE;
-        const int z = c.p.h * a.num_pages + page;
+        const int z = p->h * a.num_pages + page;
         mbar_arrive_expect_tx(bar, TILE);
-        if (c.p.rows <= T) {               // read once
+        if (p->once) {
           tma_load_3d_hint(dst, tm, bar, 0, 0, z, pol);
           tma_load_3d_hint(dst + HALF, tm, bar, 64, 0, z, pol);
         } else {
@@ -416,17 +471,22 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
       ++idx;
     };
-    for (int lead = 0; lead < 2 && k.more && ok; ++lead) {
+    for (int lead = 0; lead < 2 && k.more() && ok; ++lead) {
       if (k.opens()) load(k, pages_k, false);
-      k.step(a, cut1);
+      k.step();
     }
-    while (v.more && ok) {
+    while (v.more() && ok) {
       if (v.opens()) load(v, pages_v, true);
-      v.step(a, cut1);
-      if (k.more && ok) {
+      if (!ok) break;
+      const int done = v.k;
+      v.step();
+      __syncwarp();
+      if (v.k != done && lane == 0) mbar_arrive(&taken[(done - 1) % PR]);
+      if (k.more()) {
         if (k.opens()) load(k, pages_k, false);
-        k.step(a, cut1);
+        k.step();
       }
+      ok = __all_sync(0xffffffffu, ok && k.ok && v.ok);
     }
     if (!ok) {                             // gave up: see the copies in flight land before leaving
       for (int j = idx > ST ? idx - ST : 0; j < idx; ++j) {
@@ -441,12 +501,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
       constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
       Steps s, v;
-      s.start(a, cut0, cut1);
+      s.start(ring, posted, a.status, 0x724u);
       v = s;
       int idx = 0, st_k = 0, st_v = 0;
       uint32_t ns = 0, nv = 0;             // steps done
-      uint32_t n_q[2] = {0, 0};
-      bool ok = true;
+      uint32_t n_q = 0;                    // phase of each slot's Q tile
+      bool ok = s.ok;
       auto take = [&]() {
         const int st = idx % ST;
         ok = ok && mbar_wait(&full[st], (uint32_t)((idx / ST) & 1), a.status, 0x721u);
@@ -456,8 +516,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       auto scores = [&]() {
         const int sl = ns & 1;
         if (s.i < 2) {
-          ok = ok && mbar_wait(&q_full[sl], (uint32_t)(n_q[sl] & 1), a.status, 0x722u);
-          ++n_q[sl];
+          ok = ok && mbar_wait(&q_full[sl], (n_q >> sl) & 1u, a.status, 0x722u);
+          n_q ^= 1u << sl;
         }
         if (s.opens()) st_k = take();
         if (!ok) return;
@@ -465,51 +525,66 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const uint32_t k_addr = smem_u32(smem + OFF_RING + st_k * TILE);
         const uint32_t q_addr = smem_u32(smem + OFF_Q + sl * TILE);
         const uint32_t d = tmem + (uint32_t)sl * KT;
+        const uint64_t qd = umma_desc_sw128(q_addr), kd = umma_desc_sw128(k_addr);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
-          umma_bf16(d, umma_desc_sw128(q_addr + off), umma_desc_sw128(k_addr + off), idesc_s, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;    // (descriptor addresses count 16 bytes)
+          umma_bf16(d, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
         }
         if (s.closes()) umma_commit(&empty[st_k]);
         umma_commit(&s_full[sl]);
         if (s.i >= s.n - 2) umma_commit(&q_empty[sl]);
         ++ns;
-        s.step(a, cut1);
+        s.step();
+        ok = ok && s.ok;
       };
-      for (int lead = 0; lead < 2 && s.more && ok; ++lead) scores();
-      while (v.more && ok) {
+      for (int lead = 0; lead < 2 && s.more() && ok; ++lead) scores();
+      while (v.more() && ok) {
         const int sl = nv & 1;
         if (v.opens()) st_v = take();
-        ok = ok && mbar_wait(&p_full[sl], (uint32_t)((nv >> 1) & 1), a.status, 0x723u);
+        ok = ok && mbar_wait(&p_half[sl], (uint32_t)((nv >> 1) & 1), a.status, 0x723u);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t v_addr = smem_u32(smem + OFF_RING + st_v * TILE);
+        const uint64_t vd = desc_mn(smem_u32(smem + OFF_RING + st_v * TILE), HALF);
         const uint32_t p = tmem + (uint32_t)sl * KT, o = tmem + 2 * KT + (uint32_t)sl * D;
-        const int left = v.p.keys() - v.tile() * KT;
+        const int left = v.p->keys() - v.tile() * KT;
         const int steps = left >= KT ? 8 : (left + 15) >> 4;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          if (kk < steps)
-            umma_bf16_ts(o, p + kk * 8, desc_mn(v_addr + kk * 16 * 128, HALF), idesc_pv,
-                         (v.i >= 2 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < steps) umma_bf16_ts(o, p + kk * 8, vd + kk * 128, idesc_pv, (v.i >= 2 || kk > 0) ? 1u : 0u);
+        ok = mbar_wait(&p_full[sl], (uint32_t)((nv >> 1) & 1), a.status, 0x725u);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk)
+          if (kk < steps) umma_bf16_ts(o, p + kk * 8, vd + kk * 128, idesc_pv, 1u);
         if (v.closes()) umma_commit(&empty[st_v]);
         if (v.i >= v.n - 2) umma_commit(&o_full[sl]);
         ++nv;
-        v.step(a, cut1);
-        if (s.more && ok) scores();
+        const int done = v.k;
+        v.step();
+        ok = ok && v.ok;
+        if (v.k != done) mbar_arrive(&taken[(done - 1) % PR]);
+        if (s.more() && ok) scores();
       }
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else {
     // ------------------------------------------------------------ Q tiles, ends of the last V tiles
-    Piece p, before;
-    bool more = p.first(a, cut0, cut1), had = false, ok = true;
     uint32_t n_q[2] = {0, 0}, n_land = 0;
     int n0 = 0, tiles = 0;                 // steps and key tiles of the pieces so far
     const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * D * 2);
-    while ((more || had) && ok) {
+    bool ok = true, had = false, more = true;
+    for (int k = 0; (more || had) && ok; ++k) {
+      const Piece* p = ring + k % PR;
+      const Piece* before = ring + (k + PR - 1) % PR;
       if (more) {
-        const int n = min(2, p.ops());
+        ok = __all_sync(0xffffffffu, mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x734u));
+        if (!ok) break;
+        more = p->more != 0;
+      }
+      if (more) {
+        const int n = min(2, p->ops());
         for (int i = 0; i < n; ++i) {
           const int sl = (n0 + i) & 1;
           if (n_q[sl] > 0) ok = ok && mbar_wait(&q_empty[sl], (n_q[sl] - 1) & 1, a.status, 0x731u);
@@ -518,45 +593,49 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           ++n_q[sl];
           if (lane == 0) {
             uint8_t* dst = smem + OFF_Q + sl * TILE;
-            const int row = p.r0 + p.q * T + (p.dual ? i * a.tpt : 0);
+            const int row = p->row0 + (p->dual ? i * a.tpt : 0);
             mbar_arrive_expect_tx(&q_full[sl], q_bytes);
-            tma_load_3d(dst, &tmQ, &q_full[sl], 0, p.h * a.G, row);
-            tma_load_3d(dst + HALF, &tmQ, &q_full[sl], 64, p.h * a.G, row);
+            tma_load_3d(dst, &tmQ, &q_full[sl], 0, p->h * a.G, row);
+            tma_load_3d(dst + HALF, &tmQ, &q_full[sl], 64, p->h * a.G, row);
           }
         }
         if (!ok) break;
       }
       // the piece before: rows of its last V tile from the sequence's last key to the next multiple of 16
-      if (had && before.t1 == before.nt && (before.keys() & 15)) {
-        // loads before that tile: every K and V before it, its own K, and with one row tile the K of
-        // the step after it
-        const int st = (2 * (tiles - 1) + 1 + (!before.dual && more ? 1 : 0)) % ST;
-        ok = mbar_wait(&land[st], (n_land >> st) & 1u, a.status, 0x732u);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        n_land ^= 1u << st;
-        uint8_t* vt = smem + OFF_RING + st * TILE;
-        const int r0 = before.keys() - (before.nt - 1) * KT, r1 = (r0 + 15) & ~15;
-        for (int r = r0 + (lane >> 4); r < r1; r += 2) {
-          const int ch = lane & 15;
-          *reinterpret_cast<uint4*>(vt + (ch >> 3) * HALF + sw128_off(r, (ch & 7) * 8)) = make_uint4(0, 0, 0, 0);
+      if (had) {
+        if (before->tail()) {
+          // loads before that tile: every K and V before it, its own K, and with one row tile the K of
+          // the step after it
+          const int st = (2 * (tiles - 1) + 1 + (!before->dual && more ? 1 : 0)) % ST;
+          ok = mbar_wait(&land[st], (n_land >> st) & 1u, a.status, 0x732u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          n_land ^= 1u << st;
+          uint8_t* vt = smem + OFF_RING + st * TILE;
+          const int r0 = before->keys() - (before->nt - 1) * KT, r1 = (r0 + 15) & ~15;
+          for (int r = r0 + (lane >> 4); r < r1; r += 2) {
+            const int ch = lane & 15;
+            *reinterpret_cast<uint4*>(vt + (ch >> 3) * HALF + sw128_off(r, (ch & 7) * 8)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[st]);
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
+        if (lane == 0) mbar_arrive(&taken[(k + PR - 1) % PR]);
       }
       had = more;
       if (more) {
-        before = p;
-        n0 += p.ops();
-        tiles += p.t1 - p.t0;
-        more = p.next(a, cut1);
+        n0 += p->ops();
+        tiles += p->t1 - p->t0;
       }
     }
     if (!ok && lane == 0)                  // gave up: see the Q copies land before leaving
       for (int sl = 0; sl < 2; ++sl)
         if (n_q[sl] > 0) mbar_wait(&q_full[sl], (n_q[sl] - 1) & 1, a.status, 0x733u);
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     // ------------------------------------------------------------ softmax and epilogue of slot sl
     const int sl = warp >> 2, row = tid & 127;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -564,13 +643,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     const bool row_used = row_tok < a.tpt;
     const float scale = a.scale_log2;
-    uint32_t n_s = 0, n_o[2] = {0, 0};
+    uint32_t n_s = 0, n_pair = 0, n_o[2] = {0, 0};
     int n0 = 0, flags = 0;
     bool ok = true;
-    Piece p;
-    bool more = p.first(a, cut0, cut1);
-    Cut opened{0, 0, 0, 0};
-    while (more) {
+    int4 item = make_int4(0, 0, 0, 0);
+    // (after a wait that ran out a warp stops waiting and leaves at its next piece)
+    for (int k = 0; ok; ++k) {
+      ok = mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x744u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const Piece p = ring[k % PR];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&taken[k % PR]);
+      if (!p.more) break;
       const int n = p.ops();
       const int i0 = sl ^ (n0 & 1);        // this slot's first step of the piece
       const int x = p.dual ? i0 : 0;       // its row tile
@@ -604,21 +689,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const float base = m_new == -INFINITY ? 0.f : m_new;
         const float alpha = ex2(m_run - base);
         m_run = m_new;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(-base, -base);
-        uint32_t pk[64];
-#pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          float2 e = fma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nb2);
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-          sum[k & 1] = add2(sum[k & 1], e);
-          pk[k] = cvt_bf16x2(e.x, e.y);
-        }
-        tmem_st_cols32(t_s, pk);
-        tmem_st_cols32(t_s + 32, pk + 32);
-        const float2 s2 = add2(sum[0], sum[1]);
-        l_run = l_run * alpha + (s2.x + s2.y);
         // O is whole here: the scores' barrier came after the slot's P V before them
         if (i >= 2 && __any_sync(0xffffffffu, grew)) {
 #pragma unroll 1
@@ -630,10 +700,28 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             tmem_st_cols32(t_o + c, o);
           }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[sl]);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(-base, -base);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float2 e = fma2(make_float2(__uint_as_float(r[64 * half + 2 * k]), __uint_as_float(r[64 * half + 2 * k + 1])),
+                            sc2, nb2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[k & 1] = add2(sum[k & 1], e);
+            pk[k] = cvt_bf16x2(e.x, e.y);
+          }
+          tmem_st_cols32(t_s + 32 * half, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(half ? &p_full[sl] : &p_half[sl]);
+        }
+        const float2 s2 = add2(sum[0], sum[1]);
+        l_run = l_run * alpha + (s2.x + s2.y);
       }
       // ---- the piece's end
       const bool whole = p.t0 == 0 && p.t1 == p.nt;
@@ -642,10 +730,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         if (p.t0 > 0) flags |= F_JOINS | (p.t1 == p.nt ? F_ENDS : 0);
         else {
           flags |= F_OPENS;
-          opened = Cut{p.b, p.h, p.q, 0};
+          item = make_int4(0, p.b, p.h, p.q);
         }
       }
-      uint16_t* orow = a.O + (size_t)(p.r0 + p.q * T + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D;
+      uint16_t* orow = a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D;
       const size_t prow = ((size_t)blockIdx.x * 2 + part) * (2 * TM) + x * TM + row;
       auto out = [&](int c, const float* v, float f) {    // 32 dims from c
         if (!used) return;
@@ -685,7 +773,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           }
         tc_fence_after();
         s_ml[sl * TM + row] = make_float2(m_run, l_run);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair[0]);
+        ok = ok && mbar_wait(&pair[0], n_pair & 1, a.status, 0x745u);
         const float2 other = s_ml[(sl ^ 1) * TM + row];
         const float m = fmaxf(m_run, other.x), base = m == -INFINITY ? 0.f : m;
         const float fa = ex2(m_run - base), fb = ex2(other.x - base);
@@ -703,12 +793,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
         if (!whole && used && sl == 0) a.part_ml[prow] = make_float2(m, l);
         tc_fence_before();
-        asm volatile("bar.sync 1, 256;" ::: "memory");    // O and s_ml free again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair[1]);               // O and s_ml free again
+        ok = ok && mbar_wait(&pair[1], n_pair & 1, a.status, 0x746u);
+        ++n_pair;
       }
       n0 += n;
-      more = p.next(a, cut1);
     }
-    if (tid == 0) a.part_item[blockIdx.x] = make_int4(flags, opened.b, opened.h, opened.q);
+    if (tid == 0) a.part_item[blockIdx.x] = make_int4(flags, item.y, item.z, item.w);
   }
   tc_fence_before();
   __syncthreads();
@@ -727,10 +819,11 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const ChunkAttnArgs a, 
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int4 it = a.part_item[c0];
   if (!(it.x & F_OPENS)) return;
-  Piece p;
-  p.b = it.y; p.h = it.z; p.q = it.w;
-  p.sequence(a);
-  p.item(2 * a.tpt);
+  Walk w;
+  w.p.b = it.y; w.p.h = it.z; w.p.q = it.w;
+  w.s = seq_of(a, it.y);
+  w.item(2 * a.tpt);
+  const Piece& p = w.p;
   int c1 = c0;                             // the CTA that ends the item
   do {
     ++c1;
@@ -757,7 +850,7 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const ChunkAttnArgs a, 
       o.w += v.w * f;
     }
     const float inv = 1.f / l;
-    *reinterpret_cast<uint2*>(a.O + (size_t)(p.r0 + p.q * 2 * a.tpt + tok) * a.ldo +
+    *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + tok) * a.ldo +
                               (size_t)(p.h * a.G + m - t * a.G) * D + lane * 4) =
         make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
   }
@@ -773,6 +866,11 @@ cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk,
   if (dev < 0 || dev >= 64 || !configured[dev]) {
     cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
+    // the split of registers between the warpgroups draws on what the launch has
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, chunk_attention_kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < REGS_ALL) return cudaErrorLaunchOutOfResources;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   cudaError_t e = launch_k(chunk_attention_kernel, dim3(grid), dim3(THREADS), SMEM, s, tq, tk, tv, a);
