@@ -105,6 +105,11 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -269,6 +274,7 @@ struct Steps {
   const Piece* p;
   int k;               // pieces so far
   int i, n;            // step within the piece, steps of the piece (0: done)
+  int tail;            // 16-key steps of the piece's last tile up to the last key
   bool ok, dual;
   __device__ __forceinline__ void start(const Piece* r, uint64_t* post, unsigned* st, unsigned where) {
     ring = r; posted = post; status = st; site = where;
@@ -283,6 +289,7 @@ struct Steps {
     i = 0;
     dual = ok && p->dual;
     n = ok && p->more ? p->ops() : 0;
+    tail = ok ? min(8, (p->keys() - (p->t1 - 1) * KT + 15) >> 4) : 0;
   }
   __device__ __forceinline__ void step() {
     if (++i == n) open();
@@ -398,7 +405,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;             // (all 512 columns are this CTA's)
+  if (*tmem_slot != tmem && tid == 0) set_status(a.status, 0x7F4u);
   const Cut cut0 = s_cut[0], cut1 = s_cut[1];
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_SCHED);
   __syncthreads();                           // (the cuts lie where the pieces are posted)
@@ -497,78 +505,105 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
-      Steps s, v;
-      s.start(ring, posted, a.status, 0x724u);
-      v = s;
-      int idx = 0, st_k = 0, st_v = 0;
-      uint32_t ns = 0, nv = 0;             // steps done
-      uint32_t n_q = 0;                    // phase of each slot's Q tile
-      bool ok = s.ok;
-      auto take = [&]() {
-        const int st = idx % ST;
-        ok = ok && mbar_wait(&full[st], (uint32_t)((idx / ST) & 1), a.status, 0x721u);
-        ++idx;
-        return st;
-      };
-      auto scores = [&]() {
-        const int sl = ns & 1;
-        if (s.i < 2) {
-          ok = ok && mbar_wait(&q_full[sl], (n_q >> sl) & 1u, a.status, 0x722u);
-          n_q ^= 1u << sl;
-        }
-        if (s.opens()) st_k = take();
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t k_addr = smem_u32(smem + OFF_RING + st_k * TILE);
-        const uint32_t q_addr = smem_u32(smem + OFF_Q + sl * TILE);
-        const uint32_t d = tmem + (uint32_t)sl * KT;
-        const uint64_t qd = umma_desc_sw128(q_addr), kd = umma_desc_sw128(k_addr);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;    // (descriptor addresses count 16 bytes)
-          umma_bf16(d, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        if (s.closes()) umma_commit(&empty[st_k]);
-        umma_commit(&s_full[sl]);
-        if (s.i >= s.n - 2) umma_commit(&q_empty[sl]);
-        ++ns;
-        s.step();
-        ok = ok && s.ok;
-      };
-      for (int lead = 0; lead < 2 && s.more() && ok; ++lead) scores();
-      while (v.more() && ok) {
-        const int sl = nv & 1;
-        if (v.opens()) st_v = take();
-        ok = ok && mbar_wait(&p_half[sl], (uint32_t)((nv >> 1) & 1), a.status, 0x723u);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t vd = desc_mn(smem_u32(smem + OFF_RING + st_v * TILE), HALF);
-        const uint32_t p = tmem + (uint32_t)sl * KT, o = tmem + 2 * KT + (uint32_t)sl * D;
-        const int left = v.p->keys() - v.tile() * KT;
-        const int steps = left >= KT ? 8 : (left + 15) >> 4;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (kk < steps) umma_bf16_ts(o, p + kk * 8, vd + kk * 128, idesc_pv, (v.i >= 2 || kk > 0) ? 1u : 0u);
-        ok = mbar_wait(&p_full[sl], (uint32_t)((nv >> 1) & 1), a.status, 0x725u);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 4; kk < 8; ++kk)
-          if (kk < steps) umma_bf16_ts(o, p + kk * 8, vd + kk * 128, idesc_pv, 1u);
-        if (v.closes()) umma_commit(&empty[st_v]);
-        if (v.i >= v.n - 2) umma_commit(&o_full[sl]);
-        ++nv;
-        const int done = v.k;
-        v.step();
-        ok = ok && v.ok;
-        if (v.k != done) mbar_arrive(&taken[(done - 1) % PR]);
-        if (s.more() && ok) scores();
+    // The whole warp walks the steps and one elected lane issues: addresses are then the same in every lane
+    // (TMEM and Q addresses constants of the slot, the ring stage broadcast), which the MMAs take
+    // from uniform registers.  Issued from a divergent branch each MMA cost 60 to 100 cycles of operand moves,
+    // its 64 cycles on the tensor core twice over.
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
+    constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
+    const uint64_t q0 = umma_desc_sw128(smem_u32(smem + OFF_Q)), k0 = umma_desc_sw128(smem_u32(smem + OFF_RING));
+    const uint64_t v0 = desc_mn(smem_u32(smem + OFF_RING), HALF);
+    Steps s, v;
+    s.start(ring, posted, a.status, 0x724u);
+    v = s;
+    int st = 0, st_k = 0, st_v = 0;        // next ring stage; those of the steps' K and V tiles
+    uint32_t ph = 0, ph_p = 0, ph_q = 0;   // phases: the ring's, the weights' (of both slots), each slot's Q tile
+    bool ok = s.ok;
+    auto take = [&]() {
+      const int mine = st;
+      ok = ok && mbar_wait(&full[mine], ph, a.status, 0x721u);
+      if (++st == ST) {
+        st = 0;
+        ph ^= 1u;
       }
+      return __shfl_sync(0xffffffffu, mine, 0);
+    };
+    auto scores = [&](const int sl) {
+      if (s.i < 2) {
+        ok = ok && mbar_wait(&q_full[sl], (ph_q >> sl) & 1u, a.status, 0x722u);
+        ph_q ^= 1u << sl;
+      }
+      if (s.opens()) st_k = take();
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc_fence_after();
+      const bool closes = s.closes(), last = s.i >= s.n - 2;
+      if (leader) {
+        const uint64_t qd = q0 + sl * (TILE >> 4), kd = k0 + (uint32_t)(st_k * (TILE >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {   // (descriptor addresses count 16 bytes)
+          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+          umma_bf16(sl * KT, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[sl]);
+        if (closes) umma_commit(&empty[st_k]);
+        if (last) umma_commit(&q_empty[sl]);
+      }
+      __syncwarp();
+      s.step();
+      ok = ok && s.ok;
+    };
+    auto weigh = [&](const int sl) {
+      if (v.opens()) st_v = take();
+      ok = ok && mbar_wait(&p_half[sl], ph_p, a.status, 0x723u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc_fence_after();
+      const bool closes = v.closes(), last = v.i >= v.n - 2, more = v.i >= 2;
+      // 16-key steps up to the last key
+      const int steps = (v.dual ? last : v.i == v.n - 1) ? v.tail : 8;
+      const uint64_t vd = v0 + (uint32_t)(st_v * (TILE >> 4));
+      constexpr uint32_t t_o = 2 * KT;
+      if (leader) {
+        umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, more ? 1u : 0u);
+#pragma unroll
+        for (int kk = 1; kk < 4; ++kk)
+          if (kk < steps) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
+      }
+      ok = mbar_wait(&p_full[sl], ph_p, a.status, 0x725u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc_fence_after();
+      if (leader) {
+        if (steps == 8) {
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
+        } else {
+#pragma unroll
+          for (int kk = 4; kk < 7; ++kk)
+            if (kk < steps) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
+        }
+        if (closes) umma_commit(&empty[st_v]);
+        if (last) umma_commit(&o_full[sl]);
+      }
+      __syncwarp();
+      const int done = v.k;
+      v.step();
+      ok = ok && v.ok;
+      if (v.k != done && leader) mbar_arrive(&taken[(done - 1) % PR]);
+    };
+    // step n belongs to slot n % 2: scores two steps ahead of the products with V
+    if (ok && s.more()) scores(0);
+    if (ok && s.more()) scores(1);
+    while (ok && v.more()) {
+      weigh(0);
+      if (ok && s.more()) scores(0);
+      if (!ok || !v.more()) break;
+      weigh(1);
+      ph_p ^= 1u;
+      if (ok && s.more()) scores(1);
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ Q tiles, ends of the last V tiles
     uint32_t n_q[2] = {0, 0}, n_land = 0;
