@@ -211,7 +211,12 @@ struct Piece {
   int once;            // the sequence's only item of this head: its keys are read once
   int more;            // 0: no piece, the CTA is done
 
-  __device__ __forceinline__ int ops() const { return dual ? 2 * (t1 - t0) : t1 - t0; }
+  __device__ __forceinline__ int tiles() const { return t1 - t0; }
+  // the piece in pairs of steps (slot 0, slot 1); the second of the last pair may be void
+  __device__ __forceinline__ int pairs() const { return dual ? tiles() : (tiles() + 1) >> 1; }
+  // steps of a slot, and the key tile of its j-th
+  __device__ __forceinline__ int steps(int sl) const { return dual ? tiles() : (tiles() + 1 - sl) >> 1; }
+  __device__ __forceinline__ int tile(int sl, int j) const { return t0 + (dual ? j : 2 * j + sl); }
   __device__ __forceinline__ int keys() const { return pos + tok; }
   __device__ __forceinline__ bool tail() const { return t1 == nt && (keys() & 15) != 0; }
 };
@@ -262,42 +267,6 @@ struct Walk {
     item(2 * a.tpt);
     clip(e);
   }
-};
-
-// Steps of a CTA in order, one row tile against one key tile each; step n belongs to slot n % 2.  A cursor over
-// them that reads the posted pieces.
-struct Steps {
-  const Piece* ring;
-  uint64_t* posted;
-  unsigned* status;
-  unsigned site;
-  const Piece* p;
-  int k;               // pieces so far
-  int i, n;            // step within the piece, steps of the piece (0: done)
-  int tail;            // 16-key steps of the piece's last tile up to the last key
-  bool ok, dual;
-  __device__ __forceinline__ void start(const Piece* r, uint64_t* post, unsigned* st, unsigned where) {
-    ring = r; posted = post; status = st; site = where;
-    k = 0;
-    ok = true;
-    open();
-  }
-  __device__ __forceinline__ void open() {
-    ok = ok && mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), status, site);
-    p = ring + k % PR;
-    ++k;
-    i = 0;
-    dual = ok && p->dual;
-    n = ok && p->more ? p->ops() : 0;
-    tail = ok ? min(8, (p->keys() - (p->t1 - 1) * KT + 15) >> 4) : 0;
-  }
-  __device__ __forceinline__ void step() {
-    if (++i == n) open();
-  }
-  __device__ __forceinline__ bool more() const { return n > 0; }
-  __device__ __forceinline__ int tile() const { return p->t0 + (dual ? i >> 1 : i); }
-  __device__ __forceinline__ bool opens() const { return !dual || !(i & 1); }    // first use of its tile
-  __device__ __forceinline__ bool closes() const { return !dual || (i & 1); }    // last use
 };
 
 // Flags of a CTA for the joining kernel.
@@ -430,40 +399,38 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     __syncwarp();
   } else if (warp == 8) {
     // ------------------------------------------------------------ K and V tiles
-    // in the order of their first products: V of step n, then K of step n + 2
-    Steps k, v;
-    k.start(ring, posted, a.status, 0x713u);
-    v = k;
-    int idx = 0, pages_k = 0, pages_v = 0;
-    bool ok = k.ok;
+    // in the order of their first products: a step's V tile, then the K tile of its slot's next step
+    int idx = 0;
+    bool ok = true;
     uint32_t landed = 0;                   // stages whose last load signals `land`
     uint32_t n_land = 0;                   // its phase, one bit per stage
     const uint64_t pol = l2_policy_evict_first();
-    auto load = [&](const Steps& c, int& pages, bool is_v) {
-      const Piece* p = c.p;
-      const int t = c.tile(), dt = t - p->t0;
-      // 32 page ids at a time, one per lane
-      if ((dt & 31) == 0) {
-        const int tl = t + lane;
-        pages = tl < p->t1 ? a.block_table[(size_t)p->b * a.max_pages + tl] : 0;
-        if (pages < 0 || pages >= a.num_pages) {
+    // page ids of 32 tiles at a time, one per lane
+    struct Pages {
+      int id, base;
+    };
+    auto load = [&](const Piece& p, Pages& pg, int t, bool is_v) {
+      if (pg.base < 0 || t >= pg.base + 32) {
+        pg.base = t;
+        pg.id = t + lane < p.t1 ? a.block_table[(size_t)p.b * a.max_pages + t + lane] : 0;
+        if (pg.id < 0 || pg.id >= a.num_pages) {
           set_status(a.status, 0x7F2u);
-          pages = 0;
+          pg.id = 0;
         }
       }
-      const int page = __shfl_sync(0xffffffffu, pages, dt & 31);
+      const int page = __shfl_sync(0xffffffffu, pg.id, t - pg.base);
       const int st = idx % ST;
       if (idx >= ST) ok = ok && mbar_wait(&empty[st], (uint32_t)((idx / ST - 1) & 1), a.status, 0x711u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      const bool tail = is_v && t == p->nt - 1 && (p->keys() & 15);
+      const bool tail = is_v && t == p.nt - 1 && p.tail();
       uint64_t* bar = tail ? &land[st] : &full[st];
       if (lane == 0) {
         const CUtensorMap* tm = is_v ? &tmV : &tmK;
         uint8_t* dst = smem + OFF_RING + st * TILE;
-        const int z = p->h * a.num_pages + page;
+        const int z = p.h * a.num_pages + page;
         mbar_arrive_expect_tx(bar, TILE);
-        if (p->once) {
+        if (p.once) {
           tma_load_3d_hint(dst, tm, bar, 0, 0, z, pol);
           tma_load_3d_hint(dst + HALF, tm, bar, 64, 0, z, pol);
         } else {
@@ -479,22 +446,39 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
       ++idx;
     };
-    for (int lead = 0; lead < 2 && k.more() && ok; ++lead) {
-      if (k.opens()) load(k, pages_k, false);
-      k.step();
+    auto open = [&](int k) {
+      ok = ok && mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x713u);
+      ok = __all_sync(0xffffffffu, ok);
+      Piece p = ring[k % PR];
+      if (!ok) p.more = 0;
+      return p;
+    };
+    Piece p = open(0), nx = p;
+    Pages pv{0, -1}, pk{0, -1};
+    if (p.more) {
+      load(p, pk, p.tile(0, 0), false);
+      if (ok && !p.dual && p.steps(1) > 0) load(p, pk, p.tile(1, 0), false);
     }
-    while (v.more() && ok) {
-      if (v.opens()) load(v, pages_v, true);
-      if (!ok) break;
-      const int done = v.k;
-      v.step();
-      __syncwarp();
-      if (v.k != done && lane == 0) mbar_arrive(&taken[(done - 1) % PR]);
-      if (k.more()) {
-        if (k.opens()) load(k, pages_k, false);
-        k.step();
+    for (int k = 0, j = 0; ok && p.more;) {
+      const bool ends = j + 1 == p.pairs();
+      if (ends) {
+        nx = open(k + 1);
+        pk.base = -1;
       }
-      ok = __all_sync(0xffffffffu, ok && k.ok && v.ok);
+      const int nj = ends ? 0 : j + 1;
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl) {
+        if (ok && (sl == 0 || !p.dual) && j < p.steps(sl)) load(p, pv, p.tile(sl, j), true);
+        if (ok && nx.more && (sl == 0 || !nx.dual) && nj < nx.steps(sl)) load(nx, pk, nx.tile(sl, nj), false);
+      }
+      j = nj;
+      if (ends) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[k % PR]);
+        ++k;
+        p = nx;
+        pv.base = -1;
+      }
     }
     if (!ok) {                             // gave up: see the copies in flight land before leaving
       for (int j = idx > ST ? idx - ST : 0; j < idx; ++j) {
@@ -508,106 +492,122 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     // The whole warp walks the steps and one elected lane issues: addresses are then the same in every lane
     // (TMEM and Q addresses constants of the slot, the ring stage broadcast), which the MMAs take
     // from uniform registers.  Issued from a divergent branch each MMA cost 60 to 100 cycles of operand moves,
-    // its 64 cycles on the tensor core twice over.
+    // its 64 cycles on the tensor core twice over.  Few MMAs queue, so what the warp does between them
+    // leaves the tensor core idle: the tiles of a pair are waited for before its weights, and after a wait that
+    // ran out the warp goes on without waiting (to garbage that nobody reads) instead of voting each time.
     const bool leader = elect_one();
     constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
     constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
     const uint64_t q0 = umma_desc_sw128(smem_u32(smem + OFF_Q)), k0 = umma_desc_sw128(smem_u32(smem + OFF_RING));
     const uint64_t v0 = desc_mn(smem_u32(smem + OFF_RING), HALF);
-    Steps s, v;
-    s.start(ring, posted, a.status, 0x724u);
-    v = s;
-    int st = 0, st_k = 0, st_v = 0;        // next ring stage; those of the steps' K and V tiles
-    uint32_t ph = 0, ph_p = 0, ph_q = 0;   // phases: the ring's, the weights' (of both slots), each slot's Q tile
-    bool ok = s.ok;
+    int st = 0;                            // next ring stage
+    uint32_t ph = 0, ph_p = 0, ph_q = 0;   // phases: the ring's; each slot's weights and Q tile, one bit per slot
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+      if (ok) ok = mbar_wait(bar, parity, a.status, site);
+    };
     auto take = [&]() {
-      const int mine = st;
-      ok = ok && mbar_wait(&full[mine], ph, a.status, 0x721u);
+      const int mine = __shfl_sync(0xffffffffu, st, 0);
+      wait(&full[mine], ph, 0x721u);
       if (++st == ST) {
         st = 0;
         ph ^= 1u;
       }
-      return __shfl_sync(0xffffffffu, mine, 0);
+      return mine;
     };
-    auto scores = [&](const int sl) {
-      if (s.i < 2) {
-        ok = ok && mbar_wait(&q_full[sl], (ph_q >> sl) & 1u, a.status, 0x722u);
+    // scores of a slot from the K tile of stage kst; first / last: of the slot's steps of the piece
+    auto scores = [&](const int sl, int kst, bool first, bool last, bool release) {
+      if (first) {
+        wait(&q_full[sl], (ph_q >> sl) & 1u, 0x722u);
         ph_q ^= 1u << sl;
       }
-      if (s.opens()) st_k = take();
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
       tc_fence_after();
-      const bool closes = s.closes(), last = s.i >= s.n - 2;
       if (leader) {
-        const uint64_t qd = q0 + sl * (TILE >> 4), kd = k0 + (uint32_t)(st_k * (TILE >> 4));
+        const uint64_t qd = q0 + sl * (TILE >> 4), kd = k0 + (uint32_t)(kst * (TILE >> 4));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {   // (descriptor addresses count 16 bytes)
           const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
           umma_bf16(sl * KT, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[sl]);
-        if (closes) umma_commit(&empty[st_k]);
+        if (release) umma_commit(&empty[kst]);
         if (last) umma_commit(&q_empty[sl]);
       }
-      __syncwarp();
-      s.step();
-      ok = ok && s.ok;
     };
-    auto weigh = [&](const int sl) {
-      if (v.opens()) st_v = take();
-      ok = ok && mbar_wait(&p_half[sl], ph_p, a.status, 0x723u);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      tc_fence_after();
-      const bool closes = v.closes(), last = v.i >= v.n - 2, more = v.i >= 2;
-      // 16-key steps up to the last key
-      const int steps = (v.dual ? last : v.i == v.n - 1) ? v.tail : 8;
-      const uint64_t vd = v0 + (uint32_t)(st_v * (TILE >> 4));
+    // O += P V of a slot from the V tile of stage vst, over `steps` times 16 keys
+    auto weigh = [&](const int sl, int vst, int steps, bool first, bool last, bool release) {
+      const uint64_t vd = v0 + (uint32_t)(vst * (TILE >> 4));
       constexpr uint32_t t_o = 2 * KT;
+      const uint32_t parity = (ph_p >> sl) & 1u;
+      ph_p ^= 1u << sl;
+      wait(&p_half[sl], parity, 0x723u);
+      tc_fence_after();
       if (leader) {
-        umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, more ? 1u : 0u);
+        umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, first ? 0u : 1u);
 #pragma unroll
         for (int kk = 1; kk < 4; ++kk)
           if (kk < steps) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
       }
-      ok = mbar_wait(&p_full[sl], ph_p, a.status, 0x725u);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
+      wait(&p_full[sl], parity, 0x725u);
       tc_fence_after();
       if (leader) {
-        if (steps == 8) {
 #pragma unroll
-          for (int kk = 4; kk < 8; ++kk) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
-        } else {
-#pragma unroll
-          for (int kk = 4; kk < 7; ++kk)
-            if (kk < steps) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
-        }
-        if (closes) umma_commit(&empty[st_v]);
+        for (int kk = 4; kk < 8; ++kk)
+          if (kk < steps) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
+        if (release) umma_commit(&empty[vst]);
         if (last) umma_commit(&o_full[sl]);
       }
-      __syncwarp();
-      const int done = v.k;
-      v.step();
-      ok = ok && v.ok;
-      if (v.k != done && leader) mbar_arrive(&taken[(done - 1) % PR]);
     };
-    // step n belongs to slot n % 2: scores two steps ahead of the products with V
-    if (ok && s.more()) scores(0);
-    if (ok && s.more()) scores(1);
-    while (ok && v.more()) {
-      weigh(0);
-      if (ok && s.more()) scores(0);
-      if (!ok || !v.more()) break;
-      weigh(1);
-      ph_p ^= 1u;
-      if (ok && s.more()) scores(1);
+    struct Run {                           // what a piece's steps need
+      bool more, dual;
+      int n0, n1;                          // steps of the slots
+      int tail;                            // 16-key steps of its last tile up to the last key
+    };
+    auto open = [&](int k) {
+      wait(&posted[k % PR], (uint32_t)((k / PR) & 1), 0x724u);
+      ok = __all_sync(0xffffffffu, ok);
+      const Piece& p = ring[k % PR];
+      Run r{ok && p.more, p.dual != 0, p.steps(0), p.steps(1), min(8, (p.keys() - (p.t1 - 1) * KT + 15) >> 4)};
+      return r;
+    };
+    Run r = open(0), nx = r;
+    int k_a = 0, k_b = 0;                  // stages of the K tiles of the next scores
+    if (r.more) {
+      k_a = take();
+      scores(0, k_a, true, r.n0 == 1, !r.dual);
+      if (r.n1 > 0) {
+        k_b = r.dual ? k_a : take();
+        scores(1, k_b, true, r.n1 == 1, true);
+      }
     }
+    for (int k = 0, j = 0; r.more;) {
+      const bool ends = j + 1 == r.n0;     // (slot 0 has a step in every pair)
+      if (ends) nx = open(k + 1);
+      const int nj = ends ? 0 : j + 1;
+      const bool next_a = nx.more, next_b = nx.more && nj < nx.n1, now_b = j < r.n1;
+      const bool last_tile_b = !r.dual && now_b && ends;      // slot 1 holds the piece's last tile
+      int v_a, v_b = 0;
+      v_a = take();
+      if (next_a) k_a = take();
+      weigh(0, v_a, ends && !last_tile_b ? r.tail : 8, j == 0, ends, !r.dual);
+      if (next_a) scores(0, k_a, nj == 0, nj + 1 == nx.n0, !nx.dual);
+      if (now_b) v_b = r.dual ? v_a : take();
+      if (next_b) k_b = nx.dual ? k_a : take();
+      if (now_b) weigh(1, v_b, ends ? r.tail : 8, j == 0, j + 1 == r.n1, true);
+      if (next_b) scores(1, k_b, nj == 0, nj + 1 == nx.n1, true);
+      j = nj;
+      if (ends) {
+        __syncwarp();
+        if (leader) mbar_arrive(&taken[k % PR]);
+        ++k;
+        r = nx;
+      }
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ Q tiles, ends of the last V tiles
     uint32_t n_q[2] = {0, 0}, n_land = 0;
-    int n0 = 0, tiles = 0;                 // steps and key tiles of the pieces so far
+    int tiles = 0;                         // key tiles of the pieces so far
     const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * D * 2);
     bool ok = true, had = false, more = true;
     for (int k = 0; (more || had) && ok; ++k) {
@@ -619,16 +619,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         more = p->more != 0;
       }
       if (more) {
-        const int n = min(2, p->ops());
-        for (int i = 0; i < n; ++i) {
-          const int sl = (n0 + i) & 1;
+        for (int sl = 0; sl < 2 && p->steps(sl) > 0; ++sl) {
           if (n_q[sl] > 0) ok = ok && mbar_wait(&q_empty[sl], (n_q[sl] - 1) & 1, a.status, 0x731u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++n_q[sl];
           if (lane == 0) {
             uint8_t* dst = smem + OFF_Q + sl * TILE;
-            const int row = p->row0 + (p->dual ? i * a.tpt : 0);
+            const int row = p->row0 + (p->dual ? sl * a.tpt : 0);
             mbar_arrive_expect_tx(&q_full[sl], q_bytes);
             tma_load_3d(dst, &tmQ, &q_full[sl], 0, p->h * a.G, row);
             tma_load_3d(dst + HALF, &tmQ, &q_full[sl], 64, p->h * a.G, row);
@@ -639,9 +637,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       // the piece before: rows of its last V tile from the sequence's last key to the next multiple of 16
       if (had) {
         if (before->tail()) {
-          // loads before that tile: every K and V before it, its own K, and with one row tile the K of
-          // the step after it
-          const int st = (2 * (tiles - 1) + 1 + (!before->dual && more ? 1 : 0)) % ST;
+          // loads before that tile: every K and V before it, its own K, and the first K of the next piece
+          // if it came before slot 1's V
+          const int st = (2 * (tiles - 1) + 1 + (!before->dual && !(before->tiles() & 1) && more ? 1 : 0)) % ST;
           ok = mbar_wait(&land[st], (n_land >> st) & 1u, a.status, 0x732u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -660,10 +658,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         if (lane == 0) mbar_arrive(&taken[(k + PR - 1) % PR]);
       }
       had = more;
-      if (more) {
-        n0 += p->ops();
-        tiles += p->t1 - p->t0;
-      }
+      if (more) tiles += p->tiles();
     }
     if (!ok && lane == 0)                  // gave up: see the Q copies land before leaving
       for (int sl = 0; sl < 2; ++sl)
@@ -679,7 +674,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const bool row_used = row_tok < a.tpt;
     const float scale = a.scale_log2;
     uint32_t n_s = 0, n_pair = 0, n_o[2] = {0, 0};
-    int n0 = 0, flags = 0;
+    int flags = 0;
     bool ok = true;
     int4 item = make_int4(0, 0, 0, 0);
     // (after a wait that ran out a warp stops waiting and leaves at its next piece)
@@ -691,16 +686,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(&taken[k % PR]);
       if (!p.more) break;
-      const int n = p.ops();
-      const int i0 = sl ^ (n0 & 1);        // this slot's first step of the piece
-      const int x = p.dual ? i0 : 0;       // its row tile
+      const int n = p.steps(sl);
+      const int x = p.dual ? sl : 0;       // the slot's row tile
       const int tok = x * a.tpt + row_tok;
       const bool used = row_used && tok < p.tok;
       const int pos = p.pos + min(tok, p.tok - 1);        // the row sees keys 0 .. pos
       const int first_pos = p.pos + min(x * a.tpt, p.tok - 1);
       float m_run = -INFINITY, l_run = 0.f;
-      for (int i = i0; i < n; i += 2) {
-        const int key0 = (p.t0 + (p.dual ? i >> 1 : i)) * KT;
+      for (int j = 0; j < n; ++j) {
+        const int key0 = p.tile(sl, j) * KT;
         ok = ok && mbar_wait(&s_full[sl], n_s & 1, a.status, 0x741u);
         ++n_s;
         tc_fence_after();
@@ -725,7 +719,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const float alpha = ex2(m_run - base);
         m_run = m_new;
         // O is whole here: the scores' barrier came after the slot's P V before them
-        if (i >= 2 && __any_sync(0xffffffffu, grew)) {
+        if (j > 0 && __any_sync(0xffffffffu, grew)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -800,12 +794,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         tc_fence_before();
       } else {
         // the slots' sums joined; each slot's warps write half of the dims
-        const int f_slot = n0 & 1;                        // slot of the piece's first step
-        for (int j = 0; j < 2; ++j)
-          if (j == f_slot || n > 1) {
-            ok = ok && mbar_wait(&o_full[j], n_o[j] & 1, a.status, 0x743u);
-            ++n_o[j];
-          }
+        const bool both = p.tiles() > 1;                  // (a piece of one tile leaves slot 1 out)
+        for (int j = 0; j < (both ? 2 : 1); ++j) {
+          ok = ok && mbar_wait(&o_full[j], n_o[j] & 1, a.status, 0x743u);
+          ++n_o[j];
+        }
         tc_fence_after();
         s_ml[sl * TM + row] = make_float2(m_run, l_run);
         __syncwarp();
@@ -815,7 +808,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const float m = fmaxf(m_run, other.x), base = m == -INFINITY ? 0.f : m;
         const float fa = ex2(m_run - base), fb = ex2(other.x - base);
         const float l = l_run * fa + other.y * fb, inv = 1.f / l;
-        const bool has_a = n > 1 || sl == f_slot, has_b = n > 1 || sl != f_slot;
+        const bool has_a = both || sl == 0, has_b = both || sl == 1;
         const uint32_t t_a = t_o, t_b = tmem + 2 * KT + (uint32_t)(sl ^ 1) * D + lanes;
 #pragma unroll 1
         for (int c = sl * 64; c < sl * 64 + 64; c += 32) {
@@ -833,7 +826,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         ok = ok && mbar_wait(&pair[1], n_pair & 1, a.status, 0x746u);
         ++n_pair;
       }
-      n0 += n;
     }
     if (tid == 0) a.part_item[blockIdx.x] = make_int4(flags, item.y, item.z, item.w);
   }
