@@ -458,7 +458,7 @@ SPEC_API int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, 
  * own chunk before it that share its 128-key tile (0 * inf).  Checked on the device, with the status
  * word set: a sequence outside the M rows or past 128 * max_pages keys is skipped; a page id outside
  * [0, num_pages) reads page 0 instead.
- * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, scale finite and >= 0.
+ * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, scale finite and >= 0.
  * Workspace: spec_chunk_attention_workspace_bytes. */
 SPEC_API size_t spec_chunk_attention_workspace_bytes(int B, int M, int Hq, int Hkv, int D, int max_pages);
 SPEC_API int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len,

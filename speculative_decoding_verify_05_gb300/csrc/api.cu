@@ -1766,6 +1766,7 @@ int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_ro
   if (!Q || !O) return fail(SPEC_EINVAL, "NULL tensor argument");
   if (Hq <= 0 || Hq % Hkv) return fail(SPEC_EINVAL, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
   if (Hq / Hkv > 128) return fail(SPEC_EUNSUPPORTED, "Hq/Hkv = %d > 128", Hq / Hkv);
+  if (M > 1 << 22) return fail(SPEC_EUNSUPPORTED, "M=%d > %d rows", M, 1 << 22);
   if (ldq < (long long)Hq * D || ldo < (long long)Hq * D || ldq % 8 || ldo % 8)
     return fail(SPEC_EINVAL, "bad leading dimensions ldq=%d ldo=%d", ldq, ldo);
   if (!aligned16(Q) || !aligned16(O)) return fail(SPEC_EINVAL, "bf16 tensors must be 16-byte aligned");

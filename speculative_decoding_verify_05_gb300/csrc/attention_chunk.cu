@@ -128,6 +128,24 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+// Lanes 4 k .. 4 k + 3 transpose their 4 x 4 pieces of 16 bytes: w[j] of lane i becomes w[i] of lane j.
+__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
+  auto swap = [&](uint4& a, uint4& b, int bit) {          // a of the upper lanes against b of the lower
+    const bool up = lane & bit;
+    const uint4 send = up ? a : b;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
+    got.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
+    got.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
+    got.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
+    if (up) a = got; else b = got;
+  };
+  swap(w[0], w[1], 1);
+  swap(w[2], w[3], 1);
+  swap(w[0], w[2], 2);
+  swap(w[1], w[3], 2);
+}
+
 // ----------------------------------------------------------------- the batch
 struct Seq {
   int r0, rows, ctx;
@@ -140,23 +158,24 @@ __device__ __forceinline__ Seq seq_of(const ChunkAttnArgs& a, int b, bool* bad =
   if (bad) *bad = !ok;
   return Seq{c0, ok ? c1 - c0 : 0, ctx};
 }
-// sum of floor((s i + o) / m) over i < n, in the steps of the Euclidean algorithm
-__device__ long long floor_sum(long long n, long long m, long long s, long long o) {
+// sum of floor((s i + o) / m) over i < n, in the steps of the Euclidean algorithm (n < 2^22, s, m <= 256,
+// o < 2^31: the products fit 32 bits, the sums do not)
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned s, unsigned o) {
   long long sum = 0;
   while (n > 0) {
     if (s >= m) {
-      sum += n * (n - 1) / 2 * (s / m);
+      sum += (long long)(n * (unsigned long long)(n - 1) / 2) * (s / m);
       s %= m;
     }
     if (o >= m) {
-      sum += n * (o / m);
+      sum += (unsigned long long)n * (o / m);
       o %= m;
     }
-    const long long y = s * n + o;
+    const unsigned y = s * n + o;
     if (y < m) break;
     n = y / m;
     o = y % m;
-    const long long t = m;
+    const unsigned t = m;
     m = s;
     s = t;
   }
@@ -165,7 +184,7 @@ __device__ long long floor_sum(long long n, long long m, long long s, long long 
 // Cost of the first q items (all of two row tiles) of one kv head of a sequence: item i sees
 // ctx + (i + 1) T keys.
 __device__ __forceinline__ long long items_cost(int q, int T, int ctx) {
-  return W_DUAL * floor_sum(q, KT, T, (long long)ctx + T + KT - 1) + W_ITEM * q;
+  return W_DUAL * floor_sum(q, KT, T, ctx + T + KT - 1) + W_ITEM * q;
 }
 // ... and of all its items.
 __device__ __forceinline__ long long head_cost(const Seq& s, int T) {
@@ -178,26 +197,34 @@ __device__ __forceinline__ long long head_cost(const Seq& s, int T) {
 // Where a cut falls: before tile t of item q of kv head h of sequence b.
 struct Cut {
   int b, h, q, t;
+  Seq s;
 };
-// The cut at cost x of sequence b (0 <= x < cost of all its heads), on a whole tile.
-__device__ Cut cut_in(const Seq& s, int b, int T, long long x) {
+static_assert(sizeof(Cut) == 28, "cuts");
+// The cut at cost x of sequence b (0 <= x < cost of all its heads), on a whole tile; by a whole warp.
+__device__ __forceinline__ Cut cut_in(const Seq& s, int b, int T, long long x, int lane) {
   const long long head = head_cost(s, T);
   Cut c;
   c.b = b;
-  c.h = (int)(x / head);
+  c.s = s;
+  c.h = (int)((unsigned long long)x / (unsigned long long)head);
   x -= c.h * head;
-  int lo = 0, hi = (s.rows - 1) / T;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (items_cost(mid, T, s.ctx) <= x) lo = mid; else hi = mid - 1;
+  // the last item that starts at or before x: 32 candidates at a time
+  int lo = 0, n = (s.rows - 1) / T + 1;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, q = lo + lane * step;
+    const unsigned before = __ballot_sync(0xffffffffu, q < lo + n && items_cost(min(q, lo + n - 1), T, s.ctx) <= x);
+    const int k = 31 - __clz(before);      // (the first always is)
+    n = min(step, n - k * step);
+    lo += k * step;
   }
   c.q = lo;
   x -= items_cost(lo, T, s.ctx) + W_ITEM;
   const int tok = min(T, s.rows - lo * T);
   const int nt = (s.ctx + lo * T + tok + KT - 1) / KT;
-  const long long w = tok > T / 2 ? W_DUAL : W_ONE;
-  const long long t = x <= 0 ? 0 : (x + w / 2) / w;
-  c.t = t < nt ? (int)t : nt;
+  const int w = (int)(tok > T / 2 ? W_DUAL : W_ONE);
+  // (x is below the item's cost: nt times w at most, w * 2^23 < 2^31)
+  const int t = x <= 0 ? 0 : ((int)x + w / 2) / w;
+  c.t = t < nt ? t : nt;
   return c;
 }
 
@@ -220,7 +247,7 @@ struct Piece {
   __device__ __forceinline__ int keys() const { return pos + tok; }
   __device__ __forceinline__ bool tail() const { return t1 == nt && (keys() & 15) != 0; }
 };
-static_assert(sizeof(Piece) == 48 && OFF_SCHED + PR * 48 <= OFF_ML && OFF_SCHED % 16 == 0, "posted pieces");
+static_assert(sizeof(Piece) == 48 && OFF_SCHED + PR * 48 <= OFF_ML && PR * 48 >= 96 + 12 * 8 && OFF_SCHED % 16 == 0, "posted pieces");
 
 // The walk over a CTA's pieces.
 struct Walk {
@@ -246,7 +273,7 @@ struct Walk {
     p.more = 0;
     if (c.b >= a.B) return;
     p.b = c.b; p.h = c.h; p.q = c.q; p.t0 = c.t;
-    s = seq_of(a, p.b);
+    s = c.s;
     item(2 * a.tpt);
     if (p.t0 >= p.nt) next(a, e);
     else clip(e);
@@ -292,8 +319,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint64_t* posted = pair + 2;             // [PR] piece posted
   uint64_t* taken = posted + PR;           // [PR] everyone is done with its entry
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
+  struct Own {
+    long long x;
+    int b;
+  };
   Cut* s_cut = reinterpret_cast<Cut*>(smem + OFF_SCHED);                          // [2] start, end
-  long long* s_sum = reinterpret_cast<long long*>(smem + OFF_SCHED + 32);         // [12] warp sums
+  Own* s_own = reinterpret_cast<Own*>(smem + OFF_SCHED + 64);                     // [2] their sequences
+  long long* s_sum = reinterpret_cast<long long*>(smem + OFF_SCHED + 96);         // [12] warp sums
   float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -321,7 +353,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       mbar_init(&taken[i], 11);              // loads, MMA, Q tiles, 8 softmax warps
     }
     fence_barrier_init();
-    s_cut[0] = s_cut[1] = Cut{a.B, 0, 0, 0};
+    s_own[0].b = s_own[1].b = a.B;
   }
   if (warp == 9) tmem_alloc(tmem_slot, TMEM_COLS);
   pdl_wait();
@@ -368,7 +400,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const long long lo = off + incl - own;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (x[k] >= lo && x[k] < lo + own) s_cut[k] = cut_in(seq_of(a, b), b, T, x[k] - lo);
+        if (x[k] >= lo && x[k] < lo + own) {
+          s_own[k].b = b;
+          s_own[k].x = x[k] - lo;
+        }
+    }
+    __syncthreads();
+    if (warp < 2) {                        // one warp for each cut
+      const Own o = s_own[warp];
+      Cut c;
+      if (o.b < a.B) c = cut_in(seq_of(a, o.b), o.b, T, o.x, lane);
+      else c = Cut{a.B, 0, 0, 0, Seq{0, 0, 0}};
+      __syncwarp();
+      if (lane == 0) s_cut[warp] = c;
     }
   }
   tc_fence_before();
@@ -762,20 +806,37 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           item = make_int4(0, p.b, p.h, p.q);
         }
       }
-      uint16_t* orow = a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D;
-      const size_t prow = ((size_t)blockIdx.x * 2 + part) * (2 * TM) + x * TM + row;
-      auto out = [&](int c, const float* v, float f) {    // 32 dims from c
-        if (!used) return;
-        if (whole) {
+      // Four lanes (rows of a quad) exchange 16-byte pieces, so that each writes a quarter of 64 consecutive
+      // bytes of one row after the other: a row per lane would put every store of a warp on 32 lines.
+      uint16_t* orow[4];
+      {
+        const unsigned long long mine = used ? reinterpret_cast<unsigned long long>(
+            a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D) : 0ull;
 #pragma unroll
-          for (int d = 0; d < 32; d += 8)
-            *reinterpret_cast<uint4*>(orow + c + d) =
-                make_uint4(cvt_bf16x2(v[d] * f, v[d + 1] * f), cvt_bf16x2(v[d + 2] * f, v[d + 3] * f),
-                           cvt_bf16x2(v[d + 4] * f, v[d + 5] * f), cvt_bf16x2(v[d + 6] * f, v[d + 7] * f));
-        } else {
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const unsigned long long o = __shfl_sync(0xffffffffu, mine, (lane & ~3) + r4);
+          orow[r4] = o ? reinterpret_cast<uint16_t*>(o) + (lane & 3) * 8 : nullptr;
+        }
+      }
+      // pieces go to the workspace as [dim / 4][row][4]: consecutive rows in consecutive 16 bytes
+      const size_t pbase = (size_t)blockIdx.x * 2 + part;
+      float* pout = a.part_o + pbase * (2 * TM * D) + (x * TM + row) * 4;
+      auto out = [&](int c, const float* v, float f) {    // 32 dims from c
+        if (whole) {
+          uint4 w[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            w[d] = make_uint4(cvt_bf16x2(v[8 * d] * f, v[8 * d + 1] * f), cvt_bf16x2(v[8 * d + 2] * f, v[8 * d + 3] * f),
+                              cvt_bf16x2(v[8 * d + 4] * f, v[8 * d + 5] * f), cvt_bf16x2(v[8 * d + 6] * f, v[8 * d + 7] * f));
+          transpose4(w, lane);
+#pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4)
+            if (orow[r4]) *reinterpret_cast<uint4*>(orow[r4] + c) = w[r4];
+        } else if (used) {
 #pragma unroll
           for (int d = 0; d < 32; d += 4)
-            __stcg(reinterpret_cast<float4*>(a.part_o + prow * D + c + d), make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
+            __stcg(reinterpret_cast<float4*>(pout + (size_t)((c + d) >> 2) * (2 * TM * 4)),
+                   make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
         }
       };
       if (p.dual) {
@@ -790,7 +851,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           tmem_ld_cols<32>(t_o + c, v);
           out(c, v, inv);
         }
-        if (!whole && used) a.part_ml[prow] = make_float2(m_run, l_run);
+        if (!whole && used) a.part_ml[pbase * (2 * TM) + x * TM + row] = make_float2(m_run, l_run);
         tc_fence_before();
       } else {
         // the slots' sums joined; each slot's warps write half of the dims
@@ -819,7 +880,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           for (int k = 0; k < 32; ++k) va[k] = (has_a ? va[k] * fa : 0.f) + (has_b ? vb[k] * fb : 0.f);
           out(c, va, inv);
         }
-        if (!whole && used && sl == 0) a.part_ml[prow] = make_float2(m, l);
+        if (!whole && used && sl == 0) a.part_ml[pbase * (2 * TM) + row] = make_float2(m, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pair[1]);               // O and s_ml free again
@@ -838,12 +899,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 }
 
 // Joins the pieces of every item that a cut fell into: block (c, y) takes rows y * 16 .. of the item that CTA c
-// opened and did not end, one warp per row, four dims per lane; pieces in CTA order.
+// opened and did not end; pieces in CTA order.  A thread sums 4 dims x 4 of one row, and the rows go out through
+// shared memory in whole lines.
 constexpr int JOIN_ROWS = 16;
 __global__ void __launch_bounds__(128) chunk_join_kernel(const ChunkAttnArgs a, int grid) {
+  __shared__ uint2 s_out[JOIN_ROWS][33];
   pdl_wait();
   pdl_trigger();
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x, tid = threadIdx.x;
   const int4 it = a.part_item[c0];
   if (!(it.x & F_OPENS)) return;
   Walk w;
@@ -851,35 +914,73 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const ChunkAttnArgs a, 
   w.s = seq_of(a, it.y);
   w.item(2 * a.tpt);
   const Piece& p = w.p;
-  int c1 = c0;                             // the CTA that ends the item
-  do {
-    ++c1;
-  } while (c1 < grid - 1 && (a.part_item[c1].x & (F_JOINS | F_ENDS)) != (F_JOINS | F_ENDS));
-  for (int rr = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5); rr < (int)(blockIdx.y + 1) * JOIN_ROWS; rr += 4) {
-    const int m = rr & 127, t = m / a.G, tok = (rr >> 7) * a.tpt + t;
-    if (t >= a.tpt || tok >= p.tok) continue;
-    auto at = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * (2 * TM) + rr; };
-    auto has = [&](int c) { return c == c0 || (a.part_item[c].x & F_JOINS); };
-    float mx = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-      if (has(c)) mx = fmaxf(mx, __ldcg(&a.part_ml[at(c)]).x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      if (!has(c)) continue;
-      const float2 ml = __ldcg(&a.part_ml[at(c)]);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(c) * D) + lane);
-      const float f = ex2(ml.x - mx);
-      l += ml.y * f;
-      o.x += v.x * f;
-      o.y += v.y * f;
-      o.z += v.z * f;
-      o.w += v.w * f;
+  auto token = [&](int rr) { return (rr >> 7) * a.tpt + (rr & 127) / a.G; };
+  auto used = [&](int rr) { return (rr & 127) / a.G < a.tpt && token(rr) < p.tok; };
+  const int rr = blockIdx.y * JOIN_ROWS + (tid & 15), d4 = tid >> 4;
+  // (rows of a block that is wholly behind the item's tokens)
+  if (token(blockIdx.y * JOIN_ROWS) >= p.tok) return;
+  const bool mine = used(rr);
+  float mx = -INFINITY, l = 0.f;
+  float4 o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // flags of 32 CTAs at a time, so that the loads of their pieces do not wait for one another; the opening CTA's
+  // piece lies in slot 1, the others' in slot 0, and CTAs without work have none
+  bool ended = false;
+  for (int base = c0; !ended && base < grid; base += 32) {
+    const int c = base + (tid & 31);
+    const int f = c < grid && c > c0 ? a.part_item[c].x : 0;
+    unsigned has = __ballot_sync(0xffffffffu, c == c0 || (f & F_JOINS));
+    const unsigned ends = __ballot_sync(0xffffffffu, (f & F_ENDS) != 0);
+    if (ends) has &= 2u * (ends & -ends) - 1u;
+    ended = ends != 0;
+    if (!mine) continue;
+    auto slot = [&](int k) { return (size_t)(base + k) * 2 + (base + k == c0 ? 1 : 0); };
+    float top = mx;
+    for (unsigned m = has; m; m &= m - 1)
+      top = fmaxf(top, __ldcg(&a.part_ml[slot(__ffs(m) - 1) * (2 * TM) + rr]).x);
+    const float keep = mx == top ? 1.f : ex2(mx - top);
+    mx = top;
+    l *= keep;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      o[k].x *= keep;
+      o[k].y *= keep;
+      o[k].z *= keep;
+      o[k].w *= keep;
     }
+#pragma unroll 4
+    for (unsigned m = has; m; m &= m - 1) {
+      const size_t at = slot(__ffs(m) - 1);
+      const float2 ml = __ldcg(&a.part_ml[at * (2 * TM) + rr]);
+      const float4* src = reinterpret_cast<const float4*>(a.part_o + at * (2 * TM * D)) + rr;
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = __ldcg(src + (size_t)(d4 + 8 * k) * (2 * TM));
+      const float fc = ex2(ml.x - mx);
+      l += ml.y * fc;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[k].x += v[k].x * fc;
+        o[k].y += v[k].y * fc;
+        o[k].z += v[k].z * fc;
+        o[k].w += v[k].w * fc;
+      }
+    }
+  }
+  if (mine) {
     const float inv = 1.f / l;
-    *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + tok) * a.ldo +
-                              (size_t)(p.h * a.G + m - t * a.G) * D + lane * 4) =
-        make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      s_out[tid & 15][d4 + 8 * k] =
+          make_uint2(cvt_bf16x2(o[k].x * inv, o[k].y * inv), cvt_bf16x2(o[k].z * inv, o[k].w * inv));
+  }
+  __syncthreads();
+  for (int i = tid >> 5; i < JOIN_ROWS; i += 4) {
+    const int r = blockIdx.y * JOIN_ROWS + i;
+    if (!used(r)) continue;
+    *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + token(r)) * a.ldo + (size_t)(p.h * a.G + (r & 127) % a.G) * D +
+                              (tid & 31) * 4) = s_out[i][tid & 31];
   }
 }
 

@@ -217,8 +217,8 @@ struct ChunkAttnArgs {
   int tpt;                              // tokens per row tile: 128 / G
   float scale_log2;                     // softmax scale * log2(e), > 0
   uint16_t* O; int ldo;
-  // pieces of items that two CTAs or more share: rows of slot s of CTA c at ((2 c + s) 256 + row)
-  float* part_o;                        // [grid][2][256][128] unnormalised outputs
+  // pieces of items that two CTAs or more share, two slots per CTA
+  float* part_o;                        // [grid][2][32][256][4] unnormalised outputs, [dim / 4][row][dim % 4]
   float2* part_ml;                      // [grid][2][256] running maximum (times scale_log2) and sum
   int4* part_item;                      // [grid] flags; sequence, kv head and index of the item it opened
   unsigned* status;

@@ -84,7 +84,7 @@ def attn_args(S, **kw):
     (dict(Hq=0), "SPEC_EINVAL"), (dict(Hq=258), "SPEC_EUNSUPPORTED"), (dict(ldq=1016), "SPEC_EINVAL"),
     (dict(ldo=1028), "SPEC_EINVAL"), (dict(scale=float("nan")), "SPEC_EINVAL"), (dict(scale=float("inf")), "SPEC_EINVAL"),
     (dict(scale=-0.1), "SPEC_EINVAL"), (dict(ws_bytes=16), "SPEC_EINVAL"), (dict(ws=None, ws_bytes=0), "SPEC_EINVAL"),
-    (dict(ws=ODD), "SPEC_EINVAL"),
+    (dict(ws=ODD), "SPEC_EINVAL"), (dict(M=(1 << 22) + 1), "SPEC_EUNSUPPORTED"),
 ])
 def test_attention_refusals(S, kw, code):
     assert attn_args(S, **kw) == getattr(S, code)
