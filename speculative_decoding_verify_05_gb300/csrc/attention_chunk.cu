@@ -44,9 +44,10 @@ constexpr int OFF_Q = 0;                  // two row tiles
 constexpr int OFF_RING = 2 * TILE;
 constexpr int OFF_BAR = OFF_RING + ST * TILE;
 constexpr int PR = 4;                     // posted pieces
-constexpr int N_BARS = 3 * ST + 14 + 2 * PR;
-constexpr int OFF_SCHED = OFF_BAR + (N_BARS + 1) * 8;   // cuts and warp sums of the setup, then the posted pieces
+constexpr int N_BARS = 3 * ST + 12 + 2 * PR;
+constexpr int OFF_RINGP = OFF_BAR + (N_BARS + 1) * 8;   // posted pieces
 constexpr int OFF_ML = OFF_BAR + 512;     // (max, sum) of 128 rows for each slot
+constexpr int OFF_SCHED = OFF_ML;         // (the setup's cuts and sums, before the first of them)
 constexpr int SMEM = OFF_ML + 2 * TM * 8;
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
@@ -81,6 +82,15 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// ... only if `go` (a predicated instruction, not a branch).
+__device__ __forceinline__ void umma_bf16_ts_if(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                bool go) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %4, 0;\n setp.eq.u32 p, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)go)
       : "memory");
 }
 // Shared-memory descriptor of an MN-major operand stored as 128-byte swizzled rows (8-row atoms 1024 B
@@ -194,37 +204,56 @@ __device__ __forceinline__ long long head_cost(const Seq& s, int T) {
   return items_cost(last, T, s.ctx) + (dual ? W_DUAL : W_ONE) * ((s.ctx + s.rows + KT - 1) / KT) + W_ITEM;
 }
 
-// Where a cut falls: before tile t of item q of kv head h of sequence b.
+__device__ __forceinline__ unsigned long long div_u64(unsigned long long x, unsigned long long y) {
+  return ((x | y) >> 32) == 0 ? (unsigned)x / (unsigned)y : x / y;
+}
+
+// Where a cut falls: before tile t of item q of kv head h of sequence b (which is s).
 struct Cut {
   int b, h, q, t;
   Seq s;
 };
-static_assert(sizeof(Cut) == 28, "cuts");
-// The cut at cost x of sequence b (0 <= x < cost of all its heads), on a whole tile; by a whole warp.
-__device__ __forceinline__ Cut cut_in(const Seq& s, int b, int T, long long x, int lane) {
-  const long long head = head_cost(s, T);
+// A cut at cost x of sequence b (0 <= x < cost of all its heads), as the thread that found it leaves it.
+struct Found {
+  long long x;
+  int b;
+  Seq s;
+};
+// The cut on a whole tile, by 16 lanes.
+__device__ __forceinline__ Cut cut_of(const Found& f, int T, int lane) {
   Cut c;
-  c.b = b;
-  c.s = s;
-  c.h = (int)((unsigned long long)x / (unsigned long long)head);
-  x -= c.h * head;
-  // the last item that starts at or before x: 32 candidates at a time
-  int lo = 0, n = (s.rows - 1) / T + 1;
-  while (n > 1) {
-    const int step = (n + 31) >> 5, q = lo + lane * step;
-    const unsigned before = __ballot_sync(0xffffffffu, q < lo + n && items_cost(min(q, lo + n - 1), T, s.ctx) <= x);
-    const int k = 31 - __clz(before);      // (the first always is)
-    n = min(step, n - k * step);
-    lo += k * step;
+  c.b = f.b;
+  c.s = f.s;
+  c.h = c.q = c.t = 0;
+  long long x = f.x;
+  int lo = 0, n = 0;
+  if (f.s.rows > 0) {
+    const long long head = head_cost(f.s, T);
+    c.h = (int)div_u64(x, head);
+    x -= c.h * head;
+    n = (f.s.rows - 1) / T + 1;
   }
-  c.q = lo;
-  x -= items_cost(lo, T, s.ctx) + W_ITEM;
-  const int tok = min(T, s.rows - lo * T);
-  const int nt = (s.ctx + lo * T + tok + KT - 1) / KT;
-  const int w = (int)(tok > T / 2 ? W_DUAL : W_ONE);
-  // (x is below the item's cost: nt times w at most, w * 2^23 < 2^31)
-  const int t = x <= 0 ? 0 : ((int)x + w / 2) / w;
-  c.t = t < nt ? t : nt;
+  // the last item that starts at or before x: 16 candidates at a time
+  while (__any_sync(0xffffffffu, n > 1)) {
+    const int step = (n + 15) >> 4, q = lo + (lane & 15) * step;
+    const bool in = n > 1 && q < lo + n;
+    const unsigned votes = __ballot_sync(0xffffffffu, in && items_cost(q, T, f.s.ctx) <= x);
+    if (n > 1) {
+      const int k = 31 - __clz((votes >> (lane & 16)) & 0xffffu);      // (the first always is)
+      n = min(step, n - k * step);
+      lo += k * step;
+    }
+  }
+  if (f.s.rows > 0) {
+    c.q = lo;
+    x -= items_cost(lo, T, f.s.ctx) + W_ITEM;
+    const int tok = min(T, f.s.rows - lo * T);
+    const int nt = (f.s.ctx + lo * T + tok + KT - 1) / KT;
+    const int w = (int)(tok > T / 2 ? W_DUAL : W_ONE);
+    // (x is below the item's cost: nt times w at most, w * 2^23 < 2^31)
+    const int t = x <= 0 ? 0 : ((int)x + w / 2) / w;
+    c.t = t < nt ? t : nt;
+  }
   return c;
 }
 
@@ -247,7 +276,7 @@ struct Piece {
   __device__ __forceinline__ int keys() const { return pos + tok; }
   __device__ __forceinline__ bool tail() const { return t1 == nt && (keys() & 15) != 0; }
 };
-static_assert(sizeof(Piece) == 48 && OFF_SCHED + PR * 48 <= OFF_ML && PR * 48 >= 96 + 12 * 8 && OFF_SCHED % 16 == 0, "posted pieces");
+static_assert(sizeof(Piece) == 48 && OFF_RINGP + PR * 48 <= OFF_ML && OFF_RINGP % 8 == 0, "posted pieces");
 
 // The walk over a CTA's pieces.
 struct Walk {
@@ -312,20 +341,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint64_t* q_full = land + ST;            // [2]  row tile of a slot ready
   uint64_t* q_empty = q_full + 2;          // [2]  its last Q K^T of a piece done
   uint64_t* s_full = q_empty + 2;          // [2]  scores in TMEM (and the slot's P V before them done)
-  uint64_t* p_half = s_full + 2;           // [2]  P of keys 0-63 in TMEM, O rescaled
-  uint64_t* p_full = p_half + 2;           // [2]  all of P
+  uint64_t* p_full = s_full + 2;           // [2]  P in TMEM, O rescaled
   uint64_t* o_full = p_full + 2;           // [2]  last P V of a piece done
   uint64_t* pair = o_full + 2;             // [2]  both slots' softmax warps: sums exchanged, O read
   uint64_t* posted = pair + 2;             // [PR] piece posted
   uint64_t* taken = posted + PR;           // [PR] everyone is done with its entry
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
-  struct Own {
-    long long x;
-    int b;
-  };
-  Cut* s_cut = reinterpret_cast<Cut*>(smem + OFF_SCHED);                          // [2] start, end
-  Own* s_own = reinterpret_cast<Own*>(smem + OFF_SCHED + 64);                     // [2] their sequences
-  long long* s_sum = reinterpret_cast<long long*>(smem + OFF_SCHED + 96);         // [12] warp sums
+  Found* s_found = reinterpret_cast<Found*>(smem + OFF_SCHED);                    // [2] start, end
+  long long* s_sum = reinterpret_cast<long long*>(smem + OFF_SCHED + 64);         // [12] warp sums
+  Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RINGP);
   float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -343,7 +367,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_half[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&pair[i], 8);
@@ -353,37 +376,24 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       mbar_init(&taken[i], 11);              // loads, MMA, Q tiles, 8 softmax warps
     }
     fence_barrier_init();
-    s_own[0].b = s_own[1].b = a.B;
+    s_found[0] = s_found[1] = Found{0, a.B, Seq{0, 0, 0}};
   }
   if (warp == 9) tmem_alloc(tmem_slot, TMEM_COLS);
   pdl_wait();
   pdl_trigger();
 
-  // ---- cuts: total cost, then this CTA's two cuts from the running sum
+  // ---- cuts: the costs of the sequences before each, their total, and the two sequences that this CTA's share
+  // starts and ends in
   {
-    long long total = 0, own = 0;
-    bool any_bad = false;
-    for (int b = tid; b < a.B; b += THREADS) {
-      bool bad;
-      const Seq s = seq_of(a, b, &bad);
-      any_bad |= bad;
-      own = head_cost(s, T) * a.Hkv;
-      total += own;
-    }
-    if (any_bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) s_sum[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w];
-    const long long x[2] = {total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x};
-    long long before = 0;
-    for (int base = 0; base < a.B; base += THREADS) {
+    Seq sq{0, 0, 0};
+    long long own = 0, incl = 0, before = 0, total = 0;
+    bool bad = false;
+    auto scan = [&](int base) {            // a sequence per thread; its cost, and the running sum
       const int b = base + tid;
-      if (a.B > THREADS) own = b < a.B ? head_cost(seq_of(a, b), T) * a.Hkv : 0;
-      else if (b >= a.B) own = 0;
-      long long incl = own;
+      bool wrong = false;
+      sq = b < a.B ? seq_of(a, b, &wrong) : Seq{0, 0, 0};
+      bad |= wrong;
+      own = incl = head_cost(sq, T) * a.Hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -392,52 +402,59 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       __syncthreads();
       if (lane == 31) s_sum[warp] = incl;
       __syncthreads();
-      long long off = before;
+      incl += before;
+#pragma unroll
       for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) off += s_sum[w];
-        before += s_sum[w];
+        const long long v = s_sum[w];
+        if (w < warp) incl += v;
+        before += v;
       }
-      const long long lo = off + incl - own;
+    };
+    scan(0);
+    const bool one = a.B <= THREADS;       // (larger batches are walked twice)
+    for (int base = THREADS; base < a.B; base += THREADS) scan(base);
+    total = before;
+    before = 0;
+    const unsigned grid = gridDim.x;
+    const long long per = div_u64(total, grid);
+    const unsigned rest = (unsigned)(total - per * grid);
+    long long x[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) x[k] = per * (blockIdx.x + k) + rest * (blockIdx.x + k) / grid;
+    for (int base = 0; base < a.B; base += THREADS) {
+      if (!one) scan(base);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (x[k] >= lo && x[k] < lo + own) {
-          s_own[k].b = b;
-          s_own[k].x = x[k] - lo;
-        }
+        if (x[k] >= incl - own && x[k] < incl) s_found[k] = Found{x[k] - (incl - own), base + tid, sq};
     }
-    __syncthreads();
-    if (warp < 2) {                        // one warp for each cut
-      const Own o = s_own[warp];
-      Cut c;
-      if (o.b < a.B) c = cut_in(seq_of(a, o.b), o.b, T, o.x, lane);
-      else c = Cut{a.B, 0, 0, 0, Seq{0, 0, 0}};
-      __syncwarp();
-      if (lane == 0) s_cut[warp] = c;
-    }
+    if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0;             // (all 512 columns are this CTA's)
   if (*tmem_slot != tmem && tid == 0) set_status(a.status, 0x7F4u);
-  const Cut cut0 = s_cut[0], cut1 = s_cut[1];
-  Piece* ring = reinterpret_cast<Piece*>(smem + OFF_SCHED);
-  __syncthreads();                           // (the cuts lie where the pieces are posted)
 
   // the softmax warps hold a row of scores each: the other warpgroup leaves them its registers
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
   if (warp == 11) {
     // ------------------------------------------------------------ pieces
+    const Cut mine = cut_of(s_found[lane >> 4], T, lane);       // lanes 0-15 the start, 16-31 the end
+    Cut end;
+    end.b = __shfl_sync(0xffffffffu, mine.b, 16);
+    end.h = __shfl_sync(0xffffffffu, mine.h, 16);
+    end.q = __shfl_sync(0xffffffffu, mine.q, 16);
+    end.t = __shfl_sync(0xffffffffu, mine.t, 16);
     if (lane == 0) {
       Walk w;
-      w.first(a, cut0, cut1);
+      w.first(a, mine, end);
       for (int k = 0;; ++k) {
         if (k >= PR && !mbar_wait(&taken[k % PR], (uint32_t)((k / PR - 1) & 1), a.status, 0x701u)) break;
         ring[k % PR] = w.p;
         mbar_arrive(&posted[k % PR]);
         if (!w.p.more) break;
-        w.next(a, cut1);
+        w.next(a, end);
       }
     }
     __syncwarp();
@@ -534,7 +551,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issue
     // The whole warp walks the steps and one elected lane issues: addresses are then the same in every lane
-    // (TMEM and Q addresses constants of the slot, the ring stage broadcast), which the MMAs take
+    // (TMEM and Q addresses constants of the slot, the ring stage a uniform count), which the MMAs take
     // from uniform registers.  Issued from a divergent branch each MMA cost 60 to 100 cycles of operand moves,
     // its 64 cycles on the tensor core twice over.  Few MMAs queue, so what the warp does between them
     // leaves the tensor core idle: the tiles of a pair are waited for before its weights, and after a wait that
@@ -550,22 +567,28 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
       if (ok) ok = mbar_wait(bar, parity, a.status, site);
     };
+    // the next ring stage and its phase
+    struct Stage {
+      int st;
+      uint32_t ph;
+    };
     auto take = [&]() {
-      const int mine = __shfl_sync(0xffffffffu, st, 0);
-      wait(&full[mine], ph, 0x721u);
+      const Stage mine{st, ph};
       if (++st == ST) {
         st = 0;
         ph ^= 1u;
       }
       return mine;
     };
+    auto ready = [&](const Stage& t) { return mbar_try_wait(&full[t.st], t.ph); };
+    auto wait_tile = [&](const Stage& t) { wait(&full[t.st], t.ph, 0x721u); };
     // scores of a slot from the K tile of stage kst; first / last: of the slot's steps of the piece
     auto scores = [&](const int sl, int kst, bool first, bool last, bool release) {
       if (first) {
         wait(&q_full[sl], (ph_q >> sl) & 1u, 0x722u);
         ph_q ^= 1u << sl;
+        tc_fence_after();
       }
-      tc_fence_after();
       if (leader) {
         const uint64_t qd = q0 + sl * (TILE >> 4), kd = k0 + (uint32_t)(kst * (TILE >> 4));
 #pragma unroll
@@ -580,24 +603,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     };
     // O += P V of a slot from the V tile of stage vst, over `steps` times 16 keys
     auto weigh = [&](const int sl, int vst, int steps, bool first, bool last, bool release) {
-      const uint64_t vd = v0 + (uint32_t)(vst * (TILE >> 4));
-      constexpr uint32_t t_o = 2 * KT;
-      const uint32_t parity = (ph_p >> sl) & 1u;
-      ph_p ^= 1u << sl;
-      wait(&p_half[sl], parity, 0x723u);
-      tc_fence_after();
       if (leader) {
+        const uint64_t vd = v0 + (uint32_t)(vst * (TILE >> 4));
+        constexpr uint32_t t_o = 2 * KT;
         umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 1; kk < 4; ++kk)
-          if (kk < steps) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
-      }
-      wait(&p_full[sl], parity, 0x725u);
-      tc_fence_after();
-      if (leader) {
-#pragma unroll
-        for (int kk = 4; kk < 8; ++kk)
-          if (kk < steps) umma_bf16_ts(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, 1u);
+        for (int kk = 1; kk < 8; ++kk)
+          umma_bf16_ts_if(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, kk < steps);
         if (release) umma_commit(&empty[vst]);
         if (last) umma_commit(&o_full[sl]);
       }
@@ -615,13 +627,17 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       return r;
     };
     Run r = open(0), nx = r;
-    int k_a = 0, k_b = 0;                  // stages of the K tiles of the next scores
+    Stage k_a{0, 0}, k_b{0, 0}, v_a{0, 0}, v_b{0, 0};
     if (r.more) {
       k_a = take();
-      scores(0, k_a, true, r.n0 == 1, !r.dual);
+      wait_tile(k_a);
+      tc_fence_after();
+      scores(0, k_a.st, true, r.n0 == 1, !r.dual);
       if (r.n1 > 0) {
         k_b = r.dual ? k_a : take();
-        scores(1, k_b, true, r.n1 == 1, true);
+        wait_tile(k_b);
+        tc_fence_after();
+        scores(1, k_b.st, true, r.n1 == 1, true);
       }
     }
     for (int k = 0, j = 0; r.more;) {
@@ -630,15 +646,37 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const int nj = ends ? 0 : j + 1;
       const bool next_a = nx.more, next_b = nx.more && nj < nx.n1, now_b = j < r.n1;
       const bool last_tile_b = !r.dual && now_b && ends;      // slot 1 holds the piece's last tile
-      int v_a, v_b = 0;
+      // one look at all that slot 0 needs; what is not there is waited for in turn
       v_a = take();
       if (next_a) k_a = take();
-      weigh(0, v_a, ends && !last_tile_b ? r.tail : 8, j == 0, ends, !r.dual);
-      if (next_a) scores(0, k_a, nj == 0, nj + 1 == nx.n0, !nx.dual);
+      const uint32_t pa = ph_p & 1u, pb = (ph_p >> 1) & 1u;
+      const bool r0 = ready(v_a), r1 = ready(k_a), r2 = mbar_try_wait(&p_full[0], pa);
+      if (!(r0 && (r1 || !next_a) && r2)) {
+        wait_tile(v_a);
+        if (next_a) wait_tile(k_a);
+        wait(&p_full[0], pa, 0x723u);
+      }
+      tc_fence_after();
+      weigh(0, v_a.st, ends && !last_tile_b ? r.tail : 8, j == 0, ends, !r.dual);
+      if (next_a) scores(0, k_a.st, nj == 0, nj + 1 == nx.n0, !nx.dual);
+      ph_p ^= 1u;
       if (now_b) v_b = r.dual ? v_a : take();
       if (next_b) k_b = nx.dual ? k_a : take();
-      if (now_b) weigh(1, v_b, ends ? r.tail : 8, j == 0, j + 1 == r.n1, true);
-      if (next_b) scores(1, k_b, nj == 0, nj + 1 == nx.n1, true);
+      if (now_b) {
+        const bool s0 = ready(v_b), s1 = ready(k_b), s2 = mbar_try_wait(&p_full[1], pb);
+        if (!(s0 && (s1 || !next_b) && s2)) {
+          wait_tile(v_b);
+          if (next_b) wait_tile(k_b);
+          wait(&p_full[1], pb, 0x725u);
+        }
+        tc_fence_after();
+        weigh(1, v_b.st, ends ? r.tail : 8, j == 0, j + 1 == r.n1, true);
+        ph_p ^= 2u;
+      } else if (next_b) {
+        wait_tile(k_b);
+        tc_fence_after();
+      }
+      if (next_b) scores(1, k_b.st, nj == 0, nj + 1 == nx.n1, true);
       j = nj;
       if (ends) {
         __syncwarp();
@@ -721,6 +759,95 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     int flags = 0;
     bool ok = true;
     int4 item = make_int4(0, 0, 0, 0);
+    // The end of a piece: O scaled and written, as rows or as a piece for the joining kernel.  (Loops that run once
+    // in a while are kept short: unrolled, their instructions came from L2 each time, 65 -> 73 us for eight
+    // prompts of 100 to 1900 rows.)
+    auto finish = [&](const Piece& p, float f_m, float f_l) {
+      const int x = p.dual ? sl : 0, tok = x * a.tpt + row_tok;
+      const bool used = row_used && tok < p.tok;
+      const bool whole = p.t0 == 0 && p.t1 == p.nt;
+      // Four lanes (rows of a quad) exchange 16-byte pieces, so that each writes a quarter of 64 consecutive
+      // bytes of one row after the other: a row per lane would put every store of a warp on 32 lines.
+      uint16_t* orow[4];
+      {
+        const unsigned long long mine = used ? reinterpret_cast<unsigned long long>(
+            a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D) : 0ull;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const unsigned long long o = __shfl_sync(0xffffffffu, mine, (lane & ~3) + r4);
+          orow[r4] = o ? reinterpret_cast<uint16_t*>(o) + (lane & 3) * 8 : nullptr;
+        }
+      }
+      // pieces go to the workspace as [dim / 4][row][4]: consecutive rows in consecutive 16 bytes
+      const size_t pbase = (size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1);
+      float* pout = a.part_o + pbase * (2 * TM * D) + (x * TM + row) * 4;
+      auto out = [&](int c, const float* v, float f) {    // 32 dims from c
+        if (whole) {
+          uint4 w[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            w[d] = make_uint4(cvt_bf16x2(v[8 * d] * f, v[8 * d + 1] * f), cvt_bf16x2(v[8 * d + 2] * f, v[8 * d + 3] * f),
+                              cvt_bf16x2(v[8 * d + 4] * f, v[8 * d + 5] * f), cvt_bf16x2(v[8 * d + 6] * f, v[8 * d + 7] * f));
+          transpose4(w, lane);
+#pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4)
+            if (orow[r4]) *reinterpret_cast<uint4*>(orow[r4] + c) = w[r4];
+        } else if (used) {
+#pragma unroll
+          for (int d = 0; d < 32; d += 4)
+            __stcg(reinterpret_cast<float4*>(pout + (size_t)((c + d) >> 2) * (2 * TM * 4)),
+                   make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
+        }
+      };
+      if (p.dual) {
+        ok = ok && mbar_wait(&o_full[sl], n_o[sl] & 1, a.status, 0x742u);
+        ++n_o[0];
+        ++n_o[1];
+        tc_fence_after();
+        const float inv = 1.f / f_l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld_cols<32>(t_o + c, v);
+          out(c, v, inv);
+        }
+        if (!whole && used) a.part_ml[pbase * (2 * TM) + x * TM + row] = make_float2(f_m, f_l);
+      } else {
+        // the slots' sums joined; each slot's warps write half of the dims
+        const bool both = p.tiles() > 1;                  // (a piece of one tile leaves slot 1 out)
+        for (int j = 0; j < (both ? 2 : 1); ++j) {
+          ok = ok && mbar_wait(&o_full[j], n_o[j] & 1, a.status, 0x743u);
+          ++n_o[j];
+        }
+        tc_fence_after();
+        s_ml[sl * TM + row] = make_float2(f_m, f_l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair[0]);
+        ok = ok && mbar_wait(&pair[0], n_pair & 1, a.status, 0x745u);
+        const float2 other = s_ml[(sl ^ 1) * TM + row];
+        const float m = fmaxf(f_m, other.x), base = m == -INFINITY ? 0.f : m;
+        const float fa = ex2(f_m - base), fb = ex2(other.x - base);
+        const float l = f_l * fa + other.y * fb, inv = 1.f / l;
+        const bool has_a = both || sl == 0, has_b = both || sl == 1;
+        const uint32_t t_a = t_o, t_b = tmem + 2 * KT + (uint32_t)(sl ^ 1) * D + lanes;
+#pragma unroll 1
+        for (int c = sl * 64; c < sl * 64 + 64; c += 32) {
+          float va[32], vb[32];
+          tmem_ld_cols<32>(t_a + c, va);
+          tmem_ld_cols<32>(t_b + c, vb);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) va[k] = (has_a ? va[k] * fa : 0.f) + (has_b ? vb[k] * fb : 0.f);
+          out(c, va, inv);
+        }
+        if (!whole && used && sl == 0) a.part_ml[pbase * (2 * TM) + row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair[1]);               // O and s_ml free again
+        ok = ok && mbar_wait(&pair[1], n_pair & 1, a.status, 0x746u);
+        ++n_pair;
+      }
+      tc_fence_before();
+    };
     // (after a wait that ran out a warp stops waiting and leaves at its next piece)
     for (int k = 0; ok; ++k) {
       ok = mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x744u);
@@ -729,12 +856,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const Piece p = ring[k % PR];
       __syncwarp();
       if (lane == 0) mbar_arrive(&taken[k % PR]);
+      const int n = p.more ? p.steps(sl) : 0;
       if (!p.more) break;
-      const int n = p.steps(sl);
       const int x = p.dual ? sl : 0;       // the slot's row tile
-      const int tok = x * a.tpt + row_tok;
-      const bool used = row_used && tok < p.tok;
-      const int pos = p.pos + min(tok, p.tok - 1);        // the row sees keys 0 .. pos
+      const int pos = p.pos + min(x * a.tpt + row_tok, p.tok - 1);      // the row sees keys 0 .. pos
       const int first_pos = p.pos + min(x * a.tpt, p.tok - 1);
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
@@ -788,105 +913,22 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             pk[k] = cvt_bf16x2(e.x, e.y);
           }
           tmem_st_cols32(t_s + 32 * half, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(half ? &p_full[sl] : &p_half[sl]);
         }
+        tmem_st_wait();
         const float2 s2 = add2(sum[0], sum[1]);
         l_run = l_run * alpha + (s2.x + s2.y);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sl]);
       }
-      // ---- the piece's end
-      const bool whole = p.t0 == 0 && p.t1 == p.nt;
-      const int part = p.t0 > 0 ? 0 : 1;                  // workspace slot of a piece
-      if (!whole) {
+      if (!(p.t0 == 0 && p.t1 == p.nt)) {
         if (p.t0 > 0) flags |= F_JOINS | (p.t1 == p.nt ? F_ENDS : 0);
         else {
           flags |= F_OPENS;
           item = make_int4(0, p.b, p.h, p.q);
         }
       }
-      // Four lanes (rows of a quad) exchange 16-byte pieces, so that each writes a quarter of 64 consecutive
-      // bytes of one row after the other: a row per lane would put every store of a warp on 32 lines.
-      uint16_t* orow[4];
-      {
-        const unsigned long long mine = used ? reinterpret_cast<unsigned long long>(
-            a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D) : 0ull;
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const unsigned long long o = __shfl_sync(0xffffffffu, mine, (lane & ~3) + r4);
-          orow[r4] = o ? reinterpret_cast<uint16_t*>(o) + (lane & 3) * 8 : nullptr;
-        }
-      }
-      // pieces go to the workspace as [dim / 4][row][4]: consecutive rows in consecutive 16 bytes
-      const size_t pbase = (size_t)blockIdx.x * 2 + part;
-      float* pout = a.part_o + pbase * (2 * TM * D) + (x * TM + row) * 4;
-      auto out = [&](int c, const float* v, float f) {    // 32 dims from c
-        if (whole) {
-          uint4 w[4];
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            w[d] = make_uint4(cvt_bf16x2(v[8 * d] * f, v[8 * d + 1] * f), cvt_bf16x2(v[8 * d + 2] * f, v[8 * d + 3] * f),
-                              cvt_bf16x2(v[8 * d + 4] * f, v[8 * d + 5] * f), cvt_bf16x2(v[8 * d + 6] * f, v[8 * d + 7] * f));
-          transpose4(w, lane);
-#pragma unroll
-          for (int r4 = 0; r4 < 4; ++r4)
-            if (orow[r4]) *reinterpret_cast<uint4*>(orow[r4] + c) = w[r4];
-        } else if (used) {
-#pragma unroll
-          for (int d = 0; d < 32; d += 4)
-            __stcg(reinterpret_cast<float4*>(pout + (size_t)((c + d) >> 2) * (2 * TM * 4)),
-                   make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
-        }
-      };
-      if (p.dual) {
-        ok = ok && mbar_wait(&o_full[sl], n_o[sl] & 1, a.status, 0x742u);
-        ++n_o[0];
-        ++n_o[1];
-        tc_fence_after();
-        const float inv = 1.f / l_run;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float v[32];
-          tmem_ld_cols<32>(t_o + c, v);
-          out(c, v, inv);
-        }
-        if (!whole && used) a.part_ml[pbase * (2 * TM) + x * TM + row] = make_float2(m_run, l_run);
-        tc_fence_before();
-      } else {
-        // the slots' sums joined; each slot's warps write half of the dims
-        const bool both = p.tiles() > 1;                  // (a piece of one tile leaves slot 1 out)
-        for (int j = 0; j < (both ? 2 : 1); ++j) {
-          ok = ok && mbar_wait(&o_full[j], n_o[j] & 1, a.status, 0x743u);
-          ++n_o[j];
-        }
-        tc_fence_after();
-        s_ml[sl * TM + row] = make_float2(m_run, l_run);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pair[0]);
-        ok = ok && mbar_wait(&pair[0], n_pair & 1, a.status, 0x745u);
-        const float2 other = s_ml[(sl ^ 1) * TM + row];
-        const float m = fmaxf(m_run, other.x), base = m == -INFINITY ? 0.f : m;
-        const float fa = ex2(m_run - base), fb = ex2(other.x - base);
-        const float l = l_run * fa + other.y * fb, inv = 1.f / l;
-        const bool has_a = both || sl == 0, has_b = both || sl == 1;
-        const uint32_t t_a = t_o, t_b = tmem + 2 * KT + (uint32_t)(sl ^ 1) * D + lanes;
-#pragma unroll 1
-        for (int c = sl * 64; c < sl * 64 + 64; c += 32) {
-          float va[32], vb[32];
-          tmem_ld_cols<32>(t_a + c, va);
-          tmem_ld_cols<32>(t_b + c, vb);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) va[k] = (has_a ? va[k] * fa : 0.f) + (has_b ? vb[k] * fb : 0.f);
-          out(c, va, inv);
-        }
-        if (!whole && used && sl == 0) a.part_ml[pbase * (2 * TM) + row] = make_float2(m, l);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pair[1]);               // O and s_ml free again
-        ok = ok && mbar_wait(&pair[1], n_pair & 1, a.status, 0x746u);
-        ++n_pair;
-      }
+      finish(p, m_run, l_run);
     }
     if (tid == 0) a.part_item[blockIdx.x] = make_int4(flags, item.y, item.z, item.w);
   }
