@@ -44,16 +44,15 @@ constexpr int OFF_Q = 0;                  // two row tiles
 constexpr int OFF_RING = 2 * TILE;
 constexpr int OFF_BAR = OFF_RING + ST * TILE;
 constexpr int PR = 4;                     // posted pieces
-constexpr int N_BARS = 3 * ST + 12 + 2 * PR;
+constexpr int N_BARS = 3 * ST + 18 + 2 * PR;
 constexpr int OFF_RINGP = OFF_BAR + (N_BARS + 1) * 8;   // posted pieces
-constexpr int OFF_ML = OFF_BAR + 512;     // (max, sum) of 128 rows for each slot
-constexpr int OFF_SCHED = OFF_ML;         // (the setup's cuts and sums, before the first of them)
+constexpr int OFF_ML = OFF_BAR + 1024;    // (max, sum) of 128 rows for each slot
 constexpr int SMEM = OFF_ML + 2 * TM * 8;
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 
-// Cost of a key tile for an item of two row tiles and of one, and of an item's start and end.
-constexpr long long W_DUAL = 4, W_ONE = 3, W_ITEM = 4;
+// Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys.
+constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 192;
 
 // 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one asm
 __device__ __forceinline__ void tmem_ld_cols128(uint32_t taddr, uint32_t* r) {
@@ -71,6 +70,13 @@ __device__ __forceinline__ void tmem_ld_cols128(uint32_t taddr, uint32_t* r) {
 // 32 consecutive TMEM columns of this thread's lane stored (complete after tmem_st_wait)
 __device__ __forceinline__ void tmem_st_cols32(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_cols16(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                   taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+               "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -103,6 +109,16 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t smem_addr, uint32_t lbo) {
   d |= uint64_t(1) << 46;
   d |= uint64_t(2) << 61;
   return d;
+}
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned add_acq_rel(unsigned* p, unsigned v) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 // 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0)
 __device__ __forceinline__ float ex2(float x) {
@@ -138,22 +154,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// Lanes 4 k .. 4 k + 3 transpose their 4 x 4 pieces of 16 bytes: w[j] of lane i becomes w[i] of lane j.
-__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
-  auto swap = [&](uint4& a, uint4& b, int bit) {          // a of the upper lanes against b of the lower
-    const bool up = lane & bit;
-    const uint4 send = up ? a : b;
-    uint4 got;
-    got.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
-    got.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
-    got.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
-    got.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
-    if (up) a = got; else b = got;
-  };
-  swap(w[0], w[1], 1);
-  swap(w[2], w[3], 1);
-  swap(w[0], w[2], 2);
-  swap(w[1], w[3], 2);
+// 32 bytes to a 32-byte boundary: a row per lane then fills whole sectors (as 16-byte stores the outputs of a prompt of
+// 8192 rows took 24 us more; exchanged between lanes first to fill lines, 8 us more).
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // ----------------------------------------------------------------- the batch
@@ -168,59 +174,51 @@ __device__ __forceinline__ Seq seq_of(const ChunkAttnArgs& a, int b, bool* bad =
   if (bad) *bad = !ok;
   return Seq{c0, ok ? c1 - c0 : 0, ctx};
 }
-// sum of floor((s i + o) / m) over i < n, in the steps of the Euclidean algorithm (n < 2^22, s, m <= 256,
-// o < 2^31: the products fit 32 bits, the sums do not)
-__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned s, unsigned o) {
-  long long sum = 0;
-  while (n > 0) {
-    if (s >= m) {
-      sum += (long long)(n * (unsigned long long)(n - 1) / 2) * (s / m);
-      s %= m;
-    }
-    if (o >= m) {
-      sum += (unsigned long long)n * (o / m);
-      o %= m;
-    }
-    const unsigned y = s * n + o;
-    if (y < m) break;
-    n = y / m;
-    o = y % m;
-    const unsigned t = m;
-    m = s;
-    s = t;
-  }
-  return sum;
-}
+// n / T for n <= 2^22 (T = 2 tpt <= 256; t_magic = floor(2^32 / T) + 1)
+__device__ __forceinline__ int div_t(const ChunkAttnArgs& a, int n) { return (int)__umulhi((unsigned)n, a.t_magic); }
 // Cost of the first q items (all of two row tiles) of one kv head of a sequence: item i sees
 // ctx + (i + 1) T keys.
 __device__ __forceinline__ long long items_cost(int q, int T, int ctx) {
-  return W_DUAL * floor_sum(q, KT, T, ctx + T + KT - 1) + W_ITEM * q;
+  return W_DUAL * ((long long)q * (ctx + ITEM_KEYS) + (long long)q * (q + 1) / 2 * T);
 }
 // ... and of all its items.
-__device__ __forceinline__ long long head_cost(const Seq& s, int T) {
+__device__ __forceinline__ long long head_cost(const ChunkAttnArgs& a, const Seq& s) {
   if (s.rows == 0) return 0;
-  const int last = (s.rows - 1) / T;
-  const bool dual = s.rows - last * T > T / 2;
-  return items_cost(last, T, s.ctx) + (dual ? W_DUAL : W_ONE) * ((s.ctx + s.rows + KT - 1) / KT) + W_ITEM;
+  const int T = 2 * a.tpt, last = div_t(a, s.rows - 1);
+  const int w = s.rows - last * T > a.tpt ? W_DUAL : W_ONE;
+  return items_cost(last, T, s.ctx) + (long long)w * (s.ctx + s.rows + ITEM_KEYS);
+}
+// The tile that a cut at cost y of an item (its start 0) falls before: 0 .. nt.
+__device__ __forceinline__ int cut_tile(long long y, bool dual, int keys, int nt) {
+  const int w = dual ? W_DUAL : W_ONE;
+  y -= w * ITEM_KEYS;
+  if (y <= 0) return 0;
+  if (y >= (long long)w * keys) return nt;
+  const unsigned z = (unsigned)y + w * KT / 2;
+  const int t = (int)(dual ? z / (W_DUAL * KT) : z / (W_ONE * KT));
+  return t * KT + KT / 2 >= keys ? nt : t;              // (no piece of a few keys)
+}
+// Where CTA c's share starts (c = grid: where the last one ends); inv_grid = floor((2^64 - 1) / grid).
+__device__ __forceinline__ long long share_start(const ChunkAttnArgs& a, long long total, int c) {
+  return c >= (int)gridDim.x ? total : (long long)__umul64hi((unsigned long long)total, (unsigned)c * a.inv_grid);
 }
 
-__device__ __forceinline__ unsigned long long div_u64(unsigned long long x, unsigned long long y) {
-  return ((x | y) >> 32) == 0 ? (unsigned)x / (unsigned)y : x / y;
-}
-
-// Where a cut falls: before tile t of item q of kv head h of sequence b (which is s).
+// Where a cut falls: before tile t of item q of kv head h of sequence b (which is s); `start`: the cost of
+// everything before the item.
 struct Cut {
+  long long start;
   int b, h, q, t;
   Seq s;
 };
-// A cut at cost x of sequence b (0 <= x < cost of all its heads), as the thread that found it leaves it.
+// A cut at cost x of sequence b (0 <= x < cost of all its heads; `before`: of everything before it).
 struct Found {
-  long long x;
+  long long x, before;
   int b;
   Seq s;
 };
 // The cut on a whole tile, by 16 lanes.
-__device__ __forceinline__ Cut cut_of(const Found& f, int T, int lane) {
+__device__ __forceinline__ Cut cut_of(const ChunkAttnArgs& a, const Found& f, int lane) {
+  const int T = 2 * a.tpt;
   Cut c;
   c.b = f.b;
   c.s = f.s;
@@ -228,16 +226,19 @@ __device__ __forceinline__ Cut cut_of(const Found& f, int T, int lane) {
   long long x = f.x;
   int lo = 0, n = 0;
   if (f.s.rows > 0) {
-    const long long head = head_cost(f.s, T);
-    c.h = (int)div_u64(x, head);
-    x -= c.h * head;
-    n = (f.s.rows - 1) / T + 1;
+    const long long head = head_cost(a, f.s);
+    int h = (int)__fdividef(__ll2float_rz(x), __ll2float_ru(head));      // (off by one at most, then put right)
+    h = h < a.Hkv ? h : a.Hkv - 1;
+    while (h > 0 && h * head > x) --h;
+    while ((h + 1) * head <= x) ++h;
+    c.h = h;
+    x -= h * head;
+    n = div_t(a, f.s.rows - 1) + 1;
   }
   // the last item that starts at or before x: 16 candidates at a time
   while (__any_sync(0xffffffffu, n > 1)) {
     const int step = (n + 15) >> 4, q = lo + (lane & 15) * step;
-    const bool in = n > 1 && q < lo + n;
-    const unsigned votes = __ballot_sync(0xffffffffu, in && items_cost(q, T, f.s.ctx) <= x);
+    const unsigned votes = __ballot_sync(0xffffffffu, n > 1 && q < lo + n && items_cost(q, T, f.s.ctx) <= x);
     if (n > 1) {
       const int k = 31 - __clz((votes >> (lane & 16)) & 0xffffu);      // (the first always is)
       n = min(step, n - k * step);
@@ -246,14 +247,11 @@ __device__ __forceinline__ Cut cut_of(const Found& f, int T, int lane) {
   }
   if (f.s.rows > 0) {
     c.q = lo;
-    x -= items_cost(lo, T, f.s.ctx) + W_ITEM;
-    const int tok = min(T, f.s.rows - lo * T);
-    const int nt = (f.s.ctx + lo * T + tok + KT - 1) / KT;
-    const int w = (int)(tok > T / 2 ? W_DUAL : W_ONE);
-    // (x is below the item's cost: nt times w at most, w * 2^23 < 2^31)
-    const int t = x <= 0 ? 0 : ((int)x + w / 2) / w;
-    c.t = t < nt ? t : nt;
+    x -= items_cost(lo, T, f.s.ctx);
+    const int tok = min(T, f.s.rows - lo * T), keys = f.s.ctx + lo * T + tok;
+    c.t = cut_tile(x, tok > a.tpt, keys, (keys + KT - 1) / KT);
   }
+  c.start = f.before + f.x - x;
   return c;
 }
 
@@ -266,6 +264,7 @@ struct Piece {
   int dual;            // two row tiles
   int once;            // the sequence's only item of this head: its keys are read once
   int more;            // 0: no piece, the CTA is done
+  long long start;     // cost of everything before the item (where a cut falls into it)
 
   __device__ __forceinline__ int tiles() const { return t1 - t0; }
   // the piece in pairs of steps (slot 0, slot 1); the second of the last pair may be void
@@ -276,13 +275,14 @@ struct Piece {
   __device__ __forceinline__ int keys() const { return pos + tok; }
   __device__ __forceinline__ bool tail() const { return t1 == nt && (keys() & 15) != 0; }
 };
-static_assert(sizeof(Piece) == 48 && OFF_RINGP + PR * 48 <= OFF_ML && OFF_RINGP % 8 == 0, "posted pieces");
+static_assert(OFF_RINGP + (PR + 1) * sizeof(Piece) + 8 <= OFF_ML && OFF_RINGP % 8 == 0, "posted pieces");
 
 // The walk over a CTA's pieces.
 struct Walk {
   Piece p;
   Seq s;
   __device__ __forceinline__ void item(int T) {
+    p.start = 0;
     p.tok = min(T, s.rows - p.q * T);
     p.row0 = s.r0 + p.q * T;
     p.pos = s.ctx + p.q * T;
@@ -293,8 +293,10 @@ struct Walk {
   // the piece ends at the item's end or at the CTA's
   __device__ __forceinline__ void clip(const Cut& e) {
     p.t1 = p.nt;
-    if (p.b == e.b && p.h == e.h && p.q == e.q) p.t1 = e.t;
-    else if (p.b > e.b || (p.b == e.b && (p.h > e.h || (p.h == e.h && p.q > e.q)))) p.t1 = 0;
+    if (p.b == e.b && p.h == e.h && p.q == e.q) {
+      p.t1 = e.t;
+      p.start = e.start;
+    } else if (p.b > e.b || (p.b == e.b && (p.h > e.h || (p.h == e.h && p.q > e.q)))) p.t1 = 0;
     p.more = p.t1 > p.t0;
   }
   // first piece of [c, e)
@@ -304,6 +306,7 @@ struct Walk {
     p.b = c.b; p.h = c.h; p.q = c.q; p.t0 = c.t;
     s = c.s;
     item(2 * a.tpt);
+    p.start = c.start;
     if (p.t0 >= p.nt) next(a, e);
     else clip(e);
   }
@@ -343,17 +346,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint64_t* s_full = q_empty + 2;          // [2]  scores in TMEM (and the slot's P V before them done)
   uint64_t* p_full = s_full + 2;           // [2]  P in TMEM, O rescaled
   uint64_t* o_full = p_full + 2;           // [2]  last P V of a piece done
-  uint64_t* pair = o_full + 2;             // [2]  both slots' softmax warps: sums exchanged, O read
-  uint64_t* posted = pair + 2;             // [PR] piece posted
+  uint64_t* pair = o_full + 2;             // [4][2] the warps of both slots with the same rows: sums exchanged, O read
+  uint64_t* posted = pair + 8;             // [PR] piece posted
   uint64_t* taken = posted + PR;           // [PR] everyone is done with its entry
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
-  Found* s_found = reinterpret_cast<Found*>(smem + OFF_SCHED);                    // [2] start, end
-  long long* s_sum = reinterpret_cast<long long*>(smem + OFF_SCHED + 64);         // [12] warp sums
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RINGP);
+  Piece* s_first = ring + PR;              // the CTA's first piece, for the end
+  long long* s_total = reinterpret_cast<long long*>(ring + PR + 1);               // cost of the batch
   float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = 2 * a.tpt;
   if ((smem_u32(smem) & 1023u) != 0) {     // (the swizzled tiles need it; the same for every thread)
     if (tid == 0) set_status(a.status, 0x7F3u);
     return;
@@ -369,79 +371,77 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
-      mbar_init(&pair[i], 8);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&pair[i], 2);
     for (int i = 0; i < PR; ++i) {
       mbar_init(&posted[i], 1);
       mbar_init(&taken[i], 11);              // loads, MMA, Q tiles, 8 softmax warps
     }
     fence_barrier_init();
-    s_found[0] = s_found[1] = Found{0, a.B, Seq{0, 0, 0}};
   }
   if (warp == 9) tmem_alloc(tmem_slot, TMEM_COLS);
-  pdl_wait();
-  pdl_trigger();
 
-  // ---- cuts: the costs of the sequences before each, their total, and the two sequences that this CTA's share
-  // starts and ends in
-  {
-    Seq sq{0, 0, 0};
-    long long own = 0, incl = 0, before = 0, total = 0;
-    bool bad = false;
-    auto scan = [&](int base) {            // a sequence per thread; its cost, and the running sum
-      const int b = base + tid;
-      bool wrong = false;
-      sq = b < a.B ? seq_of(a, b, &wrong) : Seq{0, 0, 0};
-      bad |= wrong;
-      own = incl = head_cost(sq, T) * a.Hkv;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      __syncthreads();
-      if (lane == 31) s_sum[warp] = incl;
-      __syncthreads();
-      incl += before;
-#pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
-        const long long v = s_sum[w];
-        if (w < warp) incl += v;
-        before += v;
-      }
-    };
-    scan(0);
-    const bool one = a.B <= THREADS;       // (larger batches are walked twice)
-    for (int base = THREADS; base < a.B; base += THREADS) scan(base);
-    total = before;
-    before = 0;
-    const unsigned grid = gridDim.x;
-    const long long per = div_u64(total, grid);
-    const unsigned rest = (unsigned)(total - per * grid);
-    long long x[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) x[k] = per * (blockIdx.x + k) + rest * (blockIdx.x + k) / grid;
-    for (int base = 0; base < a.B; base += THREADS) {
-      if (!one) scan(base);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (x[k] >= incl - own && x[k] < incl) s_found[k] = Found{x[k] - (incl - own), base + tid, sq};
-    }
-    if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0;             // (all 512 columns are this CTA's)
   if (*tmem_slot != tmem && tid == 0) set_status(a.status, 0x7F4u);
+  // everything above overlaps the kernel before; global memory only below
+  pdl_wait();
+  pdl_trigger();
 
   // the softmax warps hold a row of scores each: the other warpgroup leaves them its registers
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
   if (warp == 11) {
     // ------------------------------------------------------------ pieces
-    const Cut mine = cut_of(s_found[lane >> 4], T, lane);       // lanes 0-15 the start, 16-31 the end
+    // The sequences' costs, a run of them per lane; then the two sequences that this CTA's share starts and ends
+    // in, found by the lanes that have them.
+    const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
+    long long own = 0;
+    bool bad = false;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) {
+      bool wrong;
+      const Seq s = seq_of(a, b, &wrong);
+      bad |= wrong;
+      own += head_cost(a, s) * a.Hkv;
+    }
+    if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
+    long long before = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    const long long total = __shfl_sync(0xffffffffu, before, 31);
+    before -= own;
+    Found f{0, 0, a.B, Seq{0, 0, 0}};      // lanes 0-15: of the start, 16-31: of the end
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long x = share_start(a, total, blockIdx.x + k);
+      const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + own);
+      if (owner == 0) continue;            // (the end of everything, or nothing at all)
+      Found g{0, before, b0, Seq{0, 0, 0}};
+      if (x >= before && x < before + own)
+        for (;; ++g.b) {
+          g.s = seq_of(a, g.b);
+          const long long c = head_cost(a, g.s) * a.Hkv;
+          if (x < g.before + c) break;
+          g.before += c;
+        }
+      const int from = __ffs(owner) - 1;
+      g.before = __shfl_sync(0xffffffffu, g.before, from);
+      g.b = __shfl_sync(0xffffffffu, g.b, from);
+      g.s.r0 = __shfl_sync(0xffffffffu, g.s.r0, from);
+      g.s.rows = __shfl_sync(0xffffffffu, g.s.rows, from);
+      g.s.ctx = __shfl_sync(0xffffffffu, g.s.ctx, from);
+      g.x = x - g.before;
+      if ((lane >> 4) == k) f = g;
+    }
+    const Cut mine = cut_of(a, f, lane);
     Cut end;
+    end.start = __shfl_sync(0xffffffffu, mine.start, 16);
     end.b = __shfl_sync(0xffffffffu, mine.b, 16);
     end.h = __shfl_sync(0xffffffffu, mine.h, 16);
     end.q = __shfl_sync(0xffffffffu, mine.q, 16);
@@ -449,6 +449,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     if (lane == 0) {
       Walk w;
       w.first(a, mine, end);
+      *s_first = w.p;
+      *s_total = total;
       for (int k = 0;; ++k) {
         if (k >= PR && !mbar_wait(&taken[k % PR], (uint32_t)((k / PR - 1) & 1), a.status, 0x701u)) break;
         ring[k % PR] = w.p;
@@ -755,126 +757,250 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     const bool row_used = row_tok < a.tpt;
     const float scale = a.scale_log2;
-    uint32_t n_s = 0, n_pair = 0, n_o[2] = {0, 0};
+    uint32_t n_s = 0, n_pair = 0, ph_o = 0;     // (ph_o: a phase bit per slot)
     int flags = 0;
     bool ok = true;
     int4 item = make_int4(0, 0, 0, 0);
-    // The end of a piece: O scaled and written, as rows or as a piece for the joining kernel.  (Loops that run once
-    // in a while are kept short: unrolled, their instructions came from L2 each time, 65 -> 73 us for eight
-    // prompts of 100 to 1900 rows.)
-    auto finish = [&](const Piece& p, float f_m, float f_l) {
-      const int x = p.dual ? sl : 0, tok = x * a.tpt + row_tok;
-      const bool used = row_used && tok < p.tok;
-      const bool whole = p.t0 == 0 && p.t1 == p.nt;
-      // Four lanes (rows of a quad) exchange 16-byte pieces, so that each writes a quarter of 64 consecutive
-      // bytes of one row after the other: a row per lane would put every store of a warp on 32 lines.
-      uint16_t* orow[4];
-      {
-        const unsigned long long mine = used ? reinterpret_cast<unsigned long long>(
-            a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D) : 0ull;
+    // A warp's rows of a piece, at its end: all dims of its slot's row tile (dual), or its slot's half of the dims
+    // of the one row tile.  (Loops that run once in a while are kept short: unrolled, their instructions
+    // came from L2 each time.)
+    struct Rows {
+      bool used;
+      int c_lo, c_hi, c_first;             // dims; the CTA that opened the item
+      uint16_t* out;
+      float *part_o;                       // of CTA 0, slot 0
+      float2* part_ml;
+      unsigned* arrived;
+    };
+    const int me = blockIdx.x;
+    long long total = 0;
+    auto rows_of = [&](const Piece& p) {
+      Rows r;
+      const int x = p.dual ? sl : 0, tok = x * a.tpt + row_tok, prow = x * TM + row;
+      r.used = row_used && tok < p.tok;
+      r.c_lo = p.dual ? 0 : sl * 64;
+      r.c_hi = p.dual ? D : sl * 64 + 64;
+      r.out = a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + row_head) * D;
+      // pieces in the workspace are [dim / 4][row][4]: consecutive rows in consecutive 16 bytes
+      r.part_o = a.part_o + prow * 4;
+      r.part_ml = a.part_ml + sl * (2 * TM) + prow;
+      r.c_first = me;
+      r.arrived = nullptr;
+      if (!a.join && (p.t0 > 0 || p.t1 < p.nt)) {
+        while (cut_tile(share_start(a, total, r.c_first) - p.start, p.dual, p.keys(), p.nt) > 0) --r.c_first;
+        r.arrived = a.counters + 8 * r.c_first + warp;
+      }
+      return r;
+    };
+    auto part_at = [&](const Rows& r, int c) { return (size_t)c * 2 + (c == r.c_first ? 1 : 0); };
+    auto store = [&](const Rows& r, int c, const float* v, float f) {      // 64 dims from c
+      uint32_t w[32];
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const unsigned long long o = __shfl_sync(0xffffffffu, mine, (lane & ~3) + r4);
-          orow[r4] = o ? reinterpret_cast<uint16_t*>(o) + (lane & 3) * 8 : nullptr;
+      for (int d = 0; d < 32; ++d) w[d] = cvt_bf16x2(v[2 * d] * f, v[2 * d + 1] * f);
+      if (!r.used) return;
+      if (a.wide) {
+#pragma unroll
+        for (int d = 0; d < 32; d += 8) st_global_32(r.out + c + 2 * d, w + d);
+      } else {
+#pragma unroll
+        for (int d = 0; d < 32; d += 4)
+          *reinterpret_cast<uint4*>(r.out + c + 2 * d) = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
+      }
+    };
+    // 64 unnormalised dims from c of this CTA's piece, from TMEM: O of the slot, or both slots' joined
+    float fa = 1.f, fb = 0.f;
+    bool have_b = false;
+    auto own64 = [&](const Piece& p, int c, float* v) {
+      tmem_ld_cols<64>(2 * KT + (p.dual ? (uint32_t)sl * D : 0u) + lanes + c, v);
+      if (!p.dual) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) v[k] *= fa;
+        if (have_b) {
+          float w[64];
+          tmem_ld_cols<64>(3 * KT + lanes + c, w);
+#pragma unroll
+          for (int k = 0; k < 64; ++k) v[k] += w[k] * fb;
         }
       }
-      // pieces go to the workspace as [dim / 4][row][4]: consecutive rows in consecutive 16 bytes
-      const size_t pbase = (size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1);
-      float* pout = a.part_o + pbase * (2 * TM * D) + (x * TM + row) * 4;
-      auto out = [&](int c, const float* v, float f) {    // 32 dims from c
-        if (whole) {
-          uint4 w[4];
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            w[d] = make_uint4(cvt_bf16x2(v[8 * d] * f, v[8 * d + 1] * f), cvt_bf16x2(v[8 * d + 2] * f, v[8 * d + 3] * f),
-                              cvt_bf16x2(v[8 * d + 4] * f, v[8 * d + 5] * f), cvt_bf16x2(v[8 * d + 6] * f, v[8 * d + 7] * f));
-          transpose4(w, lane);
-#pragma unroll
-          for (int r4 = 0; r4 < 4; ++r4)
-            if (orow[r4]) *reinterpret_cast<uint4*>(orow[r4] + c) = w[r4];
-        } else if (used) {
-#pragma unroll
-          for (int d = 0; d < 32; d += 4)
-            __stcg(reinterpret_cast<float4*>(pout + (size_t)((c + d) >> 2) * (2 * TM * 4)),
-                   make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
+    };
+    // Joins the rows of all pieces of an item, in CTA order whoever does it; `here`: this CTA's own is not in the
+    // workspace but in TMEM, with maximum m and sum l.
+    auto join = [&](const Piece& p, const Rows& r, bool here, float m, float l) {
+      auto each = [&](auto&& f) {
+        for (int base = r.c_first, t = 0; t < p.nt; base += 32) {           // 32 CTAs' cuts at a time
+          const int to = cut_tile(share_start(a, total, base + lane + 1) - p.start, p.dual, p.keys(), p.nt);
+          const int before = __shfl_up_sync(0xffffffffu, to, 1);
+          unsigned has = __ballot_sync(0xffffffffu, to > (lane == 0 ? t : before));        // (without work: no piece)
+          t = __shfl_sync(0xffffffffu, to, 31);
+          for (; has; has &= has - 1) f(base + __ffs(has) - 1);
         }
       };
-      if (p.dual) {
-        ok = ok && mbar_wait(&o_full[sl], n_o[sl] & 1, a.status, 0x742u);
-        ++n_o[0];
-        ++n_o[1];
-        tc_fence_after();
-        const float inv = 1.f / f_l;
+      float top = -INFINITY, sum = 0.f;
+      each([&](int c) {
+        float2 ml = make_float2(m, l);
+        if (!(here && c == me)) ml = r.used ? __ldcg(r.part_ml + part_at(r, c) * (4 * TM)) : make_float2(0.f, 1.f);
+        const float t = fmaxf(top, ml.x), base = t == -INFINITY ? 0.f : t;
+        sum = sum * ex2(top - base) + ml.y * ex2(ml.x - base);
+        top = t;
+      });
+      const float inv = 1.f / sum;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float v[32];
-          tmem_ld_cols<32>(t_o + c, v);
-          out(c, v, inv);
-        }
-        if (!whole && used) a.part_ml[pbase * (2 * TM) + x * TM + row] = make_float2(f_m, f_l);
-      } else {
-        // the slots' sums joined; each slot's warps write half of the dims
-        const bool both = p.tiles() > 1;                  // (a piece of one tile leaves slot 1 out)
-        for (int j = 0; j < (both ? 2 : 1); ++j) {
-          ok = ok && mbar_wait(&o_full[j], n_o[j] & 1, a.status, 0x743u);
-          ++n_o[j];
-        }
-        tc_fence_after();
-        s_ml[sl * TM + row] = make_float2(f_m, f_l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pair[0]);
-        ok = ok && mbar_wait(&pair[0], n_pair & 1, a.status, 0x745u);
-        const float2 other = s_ml[(sl ^ 1) * TM + row];
-        const float m = fmaxf(f_m, other.x), base = m == -INFINITY ? 0.f : m;
-        const float fa = ex2(f_m - base), fb = ex2(other.x - base);
-        const float l = f_l * fa + other.y * fb, inv = 1.f / l;
-        const bool has_a = both || sl == 0, has_b = both || sl == 1;
-        const uint32_t t_a = t_o, t_b = tmem + 2 * KT + (uint32_t)(sl ^ 1) * D + lanes;
-#pragma unroll 1
-        for (int c = sl * 64; c < sl * 64 + 64; c += 32) {
-          float va[32], vb[32];
-          tmem_ld_cols<32>(t_a + c, va);
-          tmem_ld_cols<32>(t_b + c, vb);
+      for (int c64 = r.c_lo; c64 < r.c_hi; c64 += 64) {
+        float acc[64];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) va[k] = (has_a ? va[k] * fa : 0.f) + (has_b ? vb[k] * fb : 0.f);
-          out(c, va, inv);
-        }
-        if (!whole && used && sl == 0) a.part_ml[pbase * (2 * TM) + row] = make_float2(m, l);
-        tc_fence_before();
+        for (int k = 0; k < 64; ++k) acc[k] = 0.f;
+        each([&](int c) {
+          if (here && c == me) {
+            float v[64];
+            own64(p, c64, v);
+            const float f = ex2(m - top);
+#pragma unroll
+            for (int k = 0; k < 64; ++k) acc[k] += v[k] * f;
+          } else if (r.used) {
+            const float* src = r.part_o + part_at(r, c) * (2 * TM * D) + (size_t)(c64 >> 2) * (2 * TM * 4);
+            const float m_c = __ldcg(r.part_ml + part_at(r, c) * (4 * TM)).x;
+            float4 u[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) u[k] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)k * (2 * TM * 4)));
+            const float f = ex2(m_c - top);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              acc[4 * k] += u[k].x * f;
+              acc[4 * k + 1] += u[k].y * f;
+              acc[4 * k + 2] += u[k].z * f;
+              acc[4 * k + 3] += u[k].w * f;
+            }
+          }
+          __syncwarp();
+        });
+        store(r, c64, acc, inv);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pair[1]);               // O and s_ml free again
-        ok = ok && mbar_wait(&pair[1], n_pair & 1, a.status, 0x746u);
-        ++n_pair;
+      }
+      if (lane == 0) *r.arrived = 0u;      // (nobody else comes here in this launch)
+    };
+    unsigned later = 0;                    // lane 0: what had arrived with the first piece
+    bool deferred = false;
+    auto finish = [&](const Piece& p, float m, float l) {
+      const bool whole = p.t0 == 0 && p.t1 == p.nt;
+      const Rows r = rows_of(p);
+      // a piece of a shared item: how much of it has arrived by now (looked at while O is waited for)
+      unsigned seen = 0;
+      if (r.arrived && lane == 0) seen = ld_acquire(r.arrived);
+      fa = 1.f;
+      if (p.dual) {
+        ok = ok && mbar_wait(&o_full[sl], (ph_o >> sl) & 1u, a.status, 0x742u);
+        ph_o ^= 3u;
+      } else {
+        // the slots' sums joined
+        have_b = p.tiles() > 1;            // (a piece of one tile leaves slot 1 out)
+        ok = ok && mbar_wait(&o_full[0], ph_o & 1u, a.status, 0x743u);
+        if (have_b) ok = ok && mbar_wait(&o_full[1], (ph_o >> 1) & 1u, a.status, 0x748u);
+        ph_o ^= have_b ? 3u : 1u;
+        s_ml[sl * TM + row] = make_float2(m, l);
+        __syncwarp();
+        uint64_t* both = pair + 2 * (warp & 3);
+        if (lane == 0) mbar_arrive(both);
+        ok = ok && mbar_wait(both, n_pair & 1, a.status, 0x745u);
+        const float2 first = s_ml[row], second = s_ml[TM + row];
+        m = fmaxf(first.x, second.x);
+        const float base = m == -INFINITY ? 0.f : m;
+        fa = ex2(first.x - base);
+        fb = ex2(second.x - base);
+        l = first.y * fa + second.y * fb;
+      }
+      __syncwarp();
+      tc_fence_after();
+      if (whole) {
+        const float inv = 1.f / l;
+#pragma unroll 1
+        for (int c = r.c_lo; c < r.c_hi; c += 64) {
+          float v[64];
+          own64(p, c, v);
+          store(r, c, v, inv);
+          __syncwarp();
+        }
+      } else {
+        // The warp whose rows arrive last joins the item's pieces.  If the others are all there, this one need not
+        // go through memory.  The CTA that opened an item comes to its end last as a rule, so the others
+        // (their first piece) look at the answer only when they are done with everything.
+        if (p.t0 > 0) flags |= F_JOINS | (p.t1 == p.nt ? F_ENDS : 0);
+        else {
+          flags |= F_OPENS;
+          item = make_int4(0, p.b, p.h, p.q);
+        }
+        const unsigned tiles = p.tiles(), nt = p.nt;
+        if (!a.join && __shfl_sync(0xffffffffu, seen, 0) + tiles == nt) {
+          join(p, r, true, m, l);
+        } else {
+          const size_t at = (size_t)me * 2 + (p.t0 > 0 ? 0 : 1);
+#pragma unroll 1
+          for (int c = r.c_lo; c < r.c_hi; c += 64) {
+            float v[64];
+            own64(p, c, v);
+            float* dst = r.part_o + at * (2 * TM * D) + (size_t)(c >> 2) * (2 * TM * 4);
+            if (r.used) {
+#pragma unroll
+              for (int d = 0; d < 64; d += 4)
+                __stcg(reinterpret_cast<float4*>(dst + (size_t)(d >> 2) * (2 * TM * 4)),
+                       make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
+            }
+            __syncwarp();
+          }
+          if (r.used) __stcg(r.part_ml + at * (4 * TM), make_float2(m, l));
+          if (!a.join) {
+            __syncwarp();
+            if (lane == 0) later = add_acq_rel(r.arrived, tiles) + tiles;
+            __syncwarp();
+            if (p.t0 > 0) deferred = true;
+            else if (__shfl_sync(0xffffffffu, later, 0) == nt) join(p, r, false, 0.f, 0.f);
+          }
+        }
       }
       tc_fence_before();
+      if (!p.dual) {
+        __syncwarp();
+        uint64_t* both = pair + 2 * (warp & 3) + 1;
+        if (lane == 0) mbar_arrive(both);  // O and s_ml free again
+        ok = ok && mbar_wait(both, n_pair & 1, a.status, 0x746u);
+        ++n_pair;
+      }
     };
     // (after a wait that ran out a warp stops waiting and leaves at its next piece)
     for (int k = 0; ok; ++k) {
       ok = mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x744u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const Piece p = ring[k % PR];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&taken[k % PR]);
-      const int n = p.more ? p.steps(sl) : 0;
+      const Piece& p = ring[k % PR];
+      if (k == 0) total = *s_total;
       if (!p.more) break;
-      const int x = p.dual ? sl : 0;       // the slot's row tile
+      const bool dual = p.dual != 0;
+      const int n = p.steps(sl), t0 = p.t0;
+      const int x = dual ? sl : 0;         // the slot's row tile
       const int pos = p.pos + min(x * a.tpt + row_tok, p.tok - 1);      // the row sees keys 0 .. pos
-      const int first_pos = p.pos + min(x * a.tpt, p.tok - 1);
+      const int pos_lo = __shfl_sync(0xffffffffu, pos, 0), pos_hi = __shfl_sync(0xffffffffu, pos, 31);
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int key0 = p.tile(sl, j) * KT;
+        const int key0 = (t0 + (dual ? j : 2 * j + sl)) * KT;
         ok = ok && mbar_wait(&s_full[sl], n_s & 1, a.status, 0x741u);
         ++n_s;
         tc_fence_after();
+        // hidden scores become -inf in place: the columns that some row of the warp does not see, 16 at a time
+        // (a few of them only, and few instructions for what happens once per item)
+        if (key0 + KT - 1 > pos_lo) {
+          const int lim = pos - key0, hi = pos_hi - key0;
+#pragma unroll 1
+          for (int c = max(0, pos_lo + 1 - key0) & ~15; c < KT; c += 16) {
+            uint32_t h[16];
+            if (c <= hi) tmem_ld_cols16(t_s + c, h);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (c + k > lim) h[k] = 0xff800000u;        // -inf
+            tmem_st_cols16(t_s + c, h);
+          }
+          tmem_st_wait();
+        }
         uint32_t r[128];
         tmem_ld_cols128(t_s, r);
-        if (key0 + KT - 1 > first_pos) {
-          const int lim = pos - key0;
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k > lim) r[k] = 0xff800000u;              // -inf
-        }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int k = 0; k < 128; k += 2)
@@ -921,16 +1047,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sl]);
       }
-      if (!(p.t0 == 0 && p.t1 == p.nt)) {
-        if (p.t0 > 0) flags |= F_JOINS | (p.t1 == p.nt ? F_ENDS : 0);
-        else {
-          flags |= F_OPENS;
-          item = make_int4(0, p.b, p.h, p.q);
-        }
-      }
       finish(p, m_run, l_run);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&taken[k % PR]);
     }
-    if (tid == 0) a.part_item[blockIdx.x] = make_int4(flags, item.y, item.z, item.w);
+    if (deferred && __all_sync(0xffffffffu, ok)) {
+      const Piece& p = *s_first;
+      if (__shfl_sync(0xffffffffu, later, 0) == (unsigned)p.nt) join(p, rows_of(p), false, 0.f, 0.f);
+    }
+    if (tid == 0 && a.join) a.part_item[blockIdx.x] = make_int4(flags, item.y, item.z, item.w);
   }
   tc_fence_before();
   __syncthreads();
@@ -940,17 +1065,36 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   }
 }
 
-// Joins the pieces of every item that a cut fell into: block (c, y) takes rows y * 16 .. of the item that CTA c
-// opened and did not end; pieces in CTA order.  A thread sums 4 dims x 4 of one row, and the rows go out through
-// shared memory in whole lines.
-constexpr int JOIN_ROWS = 16;
-__global__ void __launch_bounds__(128) chunk_join_kernel(const ChunkAttnArgs a, int grid) {
-  __shared__ uint2 s_out[JOIN_ROWS][33];
+// Joins the pieces of every item that a cut fell into, for calls whose items have many pieces of many rows (one CTA
+// joining them all would take longer than this launch): block (c, y) takes 8 rows at a time of the item that CTA
+// c opened and did not end.  Each of 8 warps sums every 8th piece, all its loads in flight together; the warps'
+// sums are added in warp order.
+constexpr int JOIN_ROWS = 8, JOIN_BLOCKS = 8;
+__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkAttnArgs a, int grid) {
+  __shared__ float4 s_o[8][32][JOIN_ROWS + 1];
+  __shared__ float2 s_ml[8][JOIN_ROWS];
+  __shared__ int s_list[1024];            // contributing CTAs
+  __shared__ int s_n;
   pdl_wait();
   pdl_trigger();
-  const int c0 = blockIdx.x, tid = threadIdx.x;
+  const int c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int4 it = a.part_item[c0];
   if (!(it.x & F_OPENS)) return;
+  if (warp == 0) {
+    int n = 0;
+    for (int base = c0; base < grid; base += 32) {
+      const int c = base + lane;
+      const int f = c < grid && c > c0 ? a.part_item[c].x : 0;
+      unsigned has = __ballot_sync(0xffffffffu, c == c0 || (f & F_JOINS));
+      const unsigned ends = __ballot_sync(0xffffffffu, (f & F_ENDS) != 0);
+      if (ends) has &= 2u * (ends & -ends) - 1u;
+      const int at = n + __popc(has & ((1u << lane) - 1u));
+      if (((has >> lane) & 1u) && at < 1024) s_list[at] = c;
+      n += __popc(has);
+      if (ends) break;
+    }
+    if (lane == 0) s_n = min(n, 1024);
+  }
   Walk w;
   w.p.b = it.y; w.p.h = it.z; w.p.q = it.w;
   w.s = seq_of(a, it.y);
@@ -958,71 +1102,70 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const ChunkAttnArgs a, 
   const Piece& p = w.p;
   auto token = [&](int rr) { return (rr >> 7) * a.tpt + (rr & 127) / a.G; };
   auto used = [&](int rr) { return (rr & 127) / a.G < a.tpt && token(rr) < p.tok; };
-  const int rr = blockIdx.y * JOIN_ROWS + (tid & 15), d4 = tid >> 4;
-  // (rows of a block that is wholly behind the item's tokens)
-  if (token(blockIdx.y * JOIN_ROWS) >= p.tok) return;
-  const bool mine = used(rr);
-  float mx = -INFINITY, l = 0.f;
-  float4 o[4];
+  __syncthreads();
+  const int n = s_n;
+  for (int y = blockIdx.y; y < 2 * TM / JOIN_ROWS; y += gridDim.y) {
+    // (rows wholly behind the item's tokens)
+    if (token(y * JOIN_ROWS) >= p.tok) continue;
+    {
+      const int rr = y * JOIN_ROWS + (lane & 7), d4 = lane >> 3;
+      const bool mine = used(rr);
+      float m = -INFINITY, l = 0.f;
+      float4 o[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // flags of 32 CTAs at a time, so that the loads of their pieces do not wait for one another; the opening CTA's
-  // piece lies in slot 1, the others' in slot 0, and CTAs without work have none
-  bool ended = false;
-  for (int base = c0; !ended && base < grid; base += 32) {
-    const int c = base + (tid & 31);
-    const int f = c < grid && c > c0 ? a.part_item[c].x : 0;
-    unsigned has = __ballot_sync(0xffffffffu, c == c0 || (f & F_JOINS));
-    const unsigned ends = __ballot_sync(0xffffffffu, (f & F_ENDS) != 0);
-    if (ends) has &= 2u * (ends & -ends) - 1u;
-    ended = ends != 0;
-    if (!mine) continue;
-    auto slot = [&](int k) { return (size_t)(base + k) * 2 + (base + k == c0 ? 1 : 0); };
-    float top = mx;
-    for (unsigned m = has; m; m &= m - 1)
-      top = fmaxf(top, __ldcg(&a.part_ml[slot(__ffs(m) - 1) * (2 * TM) + rr]).x);
-    const float keep = mx == top ? 1.f : ex2(mx - top);
-    mx = top;
-    l *= keep;
+      for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine)
+        for (int i = warp; i < n; i += 8) {
+          const int c = s_list[i];
+          const size_t at = (size_t)c * 2 + (c == c0 ? 1 : 0);
+          // (with one row tile each half of the dims has its own copy of the maximum and sum: the same)
+          const float2 ml = __ldcg(&a.part_ml[(at * 2 + (p.dual ? rr >> 7 : 0)) * (2 * TM) + rr]);
+          const float4* src = reinterpret_cast<const float4*>(a.part_o + at * (2 * TM * D)) + rr;
+          float4 v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[k].x *= keep;
-      o[k].y *= keep;
-      o[k].z *= keep;
-      o[k].w *= keep;
+          for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (size_t)(d4 + 4 * k) * (2 * TM));
+          const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+          const float fo = ex2(m - base), fc = ex2(ml.x - base);
+          m = top;
+          l = l * fo + ml.y * fc;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            o[k].x = o[k].x * fo + v[k].x * fc;
+            o[k].y = o[k].y * fo + v[k].y * fc;
+            o[k].z = o[k].z * fo + v[k].z * fc;
+            o[k].w = o[k].w * fo + v[k].w * fc;
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s_o[warp][d4 + 4 * k][lane & 7] = o[k];
+      if (lane < JOIN_ROWS) s_ml[warp][lane] = make_float2(m, l);
     }
-#pragma unroll 4
-    for (unsigned m = has; m; m &= m - 1) {
-      const size_t at = slot(__ffs(m) - 1);
-      const float2 ml = __ldcg(&a.part_ml[at * (2 * TM) + rr]);
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + at * (2 * TM * D)) + rr;
-      float4 v[4];
+    __syncthreads();
+    {
+      const int r = y * JOIN_ROWS + warp;  // a row per warp, four dims per lane
+      if (used(r)) {
+        float m = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __ldcg(src + (size_t)(d4 + 8 * k) * (2 * TM));
-      const float fc = ex2(ml.x - mx);
-      l += ml.y * fc;
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, s_ml[k][warp].x);
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o[k].x += v[k].x * fc;
-        o[k].y += v[k].y * fc;
-        o[k].z += v[k].z * fc;
-        o[k].w += v[k].w * fc;
+        for (int k = 0; k < 8; ++k) {
+          const float f = ex2(s_ml[k][warp].x - m);
+          const float4 v = s_o[k][lane][warp];
+          l += s_ml[k][warp].y * f;
+          o.x += v.x * f;
+          o.y += v.y * f;
+          o.z += v.z * f;
+          o.w += v.w * f;
+        }
+        const float inv = 1.f / l;
+        *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + token(r)) * a.ldo +
+                                  (size_t)(p.h * a.G + (r & 127) % a.G) * D + lane * 4) =
+            make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
       }
     }
-  }
-  if (mine) {
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      s_out[tid & 15][d4 + 8 * k] =
-          make_uint2(cvt_bf16x2(o[k].x * inv, o[k].y * inv), cvt_bf16x2(o[k].z * inv, o[k].w * inv));
-  }
-  __syncthreads();
-  for (int i = tid >> 5; i < JOIN_ROWS; i += 4) {
-    const int r = blockIdx.y * JOIN_ROWS + i;
-    if (!used(r)) continue;
-    *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + token(r)) * a.ldo + (size_t)(p.h * a.G + (r & 127) % a.G) * D +
-                              (tid & 31) * 4) = s_out[i][tid & 31];
+    __syncthreads();
   }
 }
 
@@ -1045,7 +1188,7 @@ cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk,
   }
   cudaError_t e = launch_k(chunk_attention_kernel, dim3(grid), dim3(THREADS), SMEM, s, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
-  e = launch_k(chunk_join_kernel, dim3(grid, 2 * TM / JOIN_ROWS), dim3(128), 0, s, a, grid);
+  if (a.join) e = launch_k(chunk_join_kernel, dim3(grid, JOIN_BLOCKS), dim3(256), 0, s, a, grid);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

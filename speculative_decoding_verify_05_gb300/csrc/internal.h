@@ -215,12 +215,19 @@ struct ChunkAttnArgs {
   const int32_t* block_table;
   int num_pages, max_pages, Hkv, G;
   int tpt;                              // tokens per row tile: 128 / G
+  unsigned t_magic;                     // floor(2^32 / (2 tpt)) + 1
+  unsigned long long inv_grid;          // floor((2^64 - 1) / grid)
   float scale_log2;                     // softmax scale * log2(e), > 0
   uint16_t* O; int ldo;
+  int wide;                             // O's rows start on 32-byte boundaries
   // pieces of items that two CTAs or more share, two slots per CTA
   float* part_o;                        // [grid][2][32][256][4] unnormalised outputs, [dim / 4][row][dim % 4]
-  float2* part_ml;                      // [grid][2][256] running maximum (times scale_log2) and sum
+  float2* part_ml;                      // [grid][2][2][256] running maximum (times scale_log2) and sum, as left by
+                                        // the warps of slot 0 and of slot 1
+  int join;                             // 1: a second kernel joins the pieces, 0: the last CTA of each item does
   int4* part_item;                      // [grid] flags; sequence, kv head and index of the item it opened
+  unsigned* counters;                   // [grid][8] key tiles of an item's pieces that have arrived, at the CTA that
+                                        // opened it, per warp (its rows, or its rows and half of the dims)
   unsigned* status;
 };
 // Q map: boxes of 64 dims x G heads x tpt rows; K / V maps: boxes of 64 dims x one page.  `grid` CTAs.
