@@ -119,12 +119,19 @@ def launch_count() -> int:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# (a stream object per call costs several microseconds of host time: more than a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _rowmajor(t: torch.Tensor, name: str) -> int:
@@ -346,20 +353,24 @@ def spec_rope_table(cu_rows, ctx_len, M: int, D: int, theta: float = 1e6, cs=Non
     return cs
 
 
+_SECTIONS = [ctypes.c_int32 * n for n in range(9)]
+
+
 def spec_rope_table_axes(pos, sections, D: int, theta: float = 1e6, interleaved: bool = False, cs=None, stream=None):
     """(cos, sin) per row and frequency for positions with several axes: pos [axes, M] int32, sections
     the frequencies of each axis (sum D/2; consecutive, or interleaved); returns cs [M, D/2, 2] fp32."""
     _need(pos, torch.int32, "pos")
     ld = _rowmajor(pos, "pos")
     axes, M = pos.shape
-    if len(sections) != axes:
-        raise ValueError("sections must have an entry per axis of pos")
+    if len(sections) != axes or axes > 8:
+        raise ValueError("sections must have an entry per axis of pos (8 at most)")
     if cs is None:
         cs = torch.empty((M, D // 2, 2), dtype=torch.float32, device=pos.device)
-    _need(cs, torch.float32, "cs")
-    if not cs.is_contiguous() or cs.shape != (M, D // 2, 2):
-        raise ValueError("cs must be a contiguous [M, D/2, 2] tensor")
-    sec = (ctypes.c_int32 * axes)(*[int(v) for v in sections])
+    else:
+        _need(cs, torch.float32, "cs")
+        if not cs.is_contiguous() or cs.shape != (M, D // 2, 2):
+            raise ValueError("cs must be a contiguous [M, D/2, 2] tensor")
+    sec = _SECTIONS[axes](*sections)
     _check(_lib.spec_rope_table_axes(_p(pos), ld, axes, M, int(D), float(theta), sec, 1 if interleaved else 0, _p(cs),
                                      _stream(stream)), True)
     return cs
@@ -505,22 +516,31 @@ def spec_verify_attention_paged(Q, Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, b
 
 
 # --------------------------------------------------------------------------- prompt side of the paged cache
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
 def _paged(cu_rows, ctx_len, Kpool, Vpool, block_table):
-    """Checks the batch and cache arguments of a chunk call; returns (B, Hkv, num_pages, D, max_pages)."""
-    for t, n in ((Kpool, "Kpool"), (Vpool, "Vpool")):
-        _need(t, torch.bfloat16, n)
-    for t, n in ((cu_rows, "cu_rows"), (ctx_len, "ctx_len"), (block_table, "block_table")):
-        _need(t, torch.int32, n)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    if Kpool.dim() != 4 or Kpool.shape[2] != 128 or not (Kpool.is_contiguous() and Vpool.is_contiguous()
-                                                         and Vpool.shape == Kpool.shape):
+    """Checks the batch and cache arguments of a chunk call; returns (B, Hkv, num_pages, D, max_pages).
+
+    (A decode step's call costs as much host time as its kernel takes: one expression for what is right as
+    a rule, and the checks one by one only to name what is not.)"""
+    if not (Kpool.dtype is _BF16 and Vpool.dtype is _BF16 and cu_rows.dtype is _I32 and ctx_len.dtype is _I32
+            and block_table.dtype is _I32 and Kpool.is_cuda and Vpool.is_cuda and cu_rows.is_cuda and ctx_len.is_cuda
+            and block_table.is_cuda):
+        for t, n in ((Kpool, "Kpool"), (Vpool, "Vpool")):
+            _need(t, _BF16, n)
+        for t, n in ((cu_rows, "cu_rows"), (ctx_len, "ctx_len"), (block_table, "block_table")):
+            _need(t, _I32, n)
+    if not (cu_rows.is_contiguous() and ctx_len.is_contiguous() and block_table.is_contiguous()):
+        raise ValueError("cu_rows, ctx_len and block_table must be contiguous")
+    pool = Kpool.shape
+    if len(pool) != 4 or pool[2] != 128 or Vpool.shape != pool or not (Kpool.is_contiguous() and Vpool.is_contiguous()):
         raise ValueError("Kpool/Vpool must be contiguous [Hkv, num_pages, 128, D]")
+    table = block_table.shape
     B = cu_rows.numel() - 1
-    if block_table.dim() != 2 or block_table.shape[0] != B or ctx_len.numel() != B:
+    if len(table) != 2 or table[0] != B or ctx_len.numel() != B:
         raise ValueError("cu_rows, ctx_len and block_table must be [B + 1], [B] and [B, max_pages]")
-    Hkv, num_pages, _, D = Kpool.shape
-    return B, Hkv, num_pages, D, block_table.shape[1]
+    return B, pool[0], pool[1], pool[3], table[1]
 
 
 def spec_kv_append_paged(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table, cs=None, Q=None, Qrot=None,
@@ -529,30 +549,39 @@ def spec_kv_append_paged(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table
     128, D] at positions ctx_len.., the keys rotated with the table cs [M, D/2, 2] (cs None: copied as
     they are); Q [M, Hq*D], if given, is rotated into Qrot (default: in place).  Returns Qrot."""
     B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table)
-    M = Knew.shape[0]
-    for t, n in ((Knew, "Knew"), (Vnew, "Vnew")):
-        _need(t, torch.bfloat16, n)
-        if t.shape != (M, Hkv * D):
-            raise ValueError(f"{n} must be [M, Hkv*D]")
+    if not (Knew.dtype is _BF16 and Vnew.dtype is _BF16 and Knew.is_cuda and Vnew.is_cuda):
+        _need(Knew, _BF16, "Knew"); _need(Vnew, _BF16, "Vnew")
     ldkv = _rowmajor(Knew, "Knew")
-    if _rowmajor(Vnew, "Vnew") != ldkv:
+    if Vnew.stride() != (ldkv, 1):
         raise ValueError("Knew and Vnew must share a leading dimension")
+    M, width = shape = Knew.shape
+    if width != Hkv * D or Vnew.shape != shape:
+        raise ValueError("Knew and Vnew must be [M, Hkv*D]")
     if cs is not None:
         _need(cs, torch.float32, "cs")
-        if not cs.is_contiguous() or cs.dim() != 3 or cs.shape[0] < M or cs.shape[1:] != (D // 2, 2):
+        table = cs.shape
+        if len(table) != 3 or table[0] < M or table[1] != D // 2 or table[2] != 2 or not cs.is_contiguous():
             raise ValueError("cs must be a contiguous [M, D/2, 2] table with an entry per row")
-    Hq = 0
+    Hq = ldq = ldqr = 0
     if Q is not None:
         _need(Q, torch.bfloat16, "Q")
-        Qrot = Q if Qrot is None else Qrot
-        _need(Qrot, torch.bfloat16, "Qrot")
-        if Q.shape[0] != M or Q.shape[1] % D or Qrot.shape != Q.shape:
+        ldq = ldqr = _rowmajor(Q, "Q")
+        shape = Q.shape
+        if Qrot is None:
+            Qrot = Q
+        else:
+            _need(Qrot, torch.bfloat16, "Qrot")
+            ldqr = _rowmajor(Qrot, "Qrot")
+            if Qrot.shape != shape:
+                raise ValueError("Q and Qrot must be [M, Hq*D]")
+        if shape[0] != M or shape[1] % D:
             raise ValueError("Q and Qrot must be [M, Hq*D]")
-        Hq = Q.shape[1] // D
+        Hq = shape[1] // D
+    elif Qrot is not None:
+        raise ValueError("Qrot without Q")
     _check(_lib.spec_kv_append_paged(
-        _p(Q), _rowmajor(Q, "Q") if Q is not None else 0, _p(Qrot), _rowmajor(Qrot, "Qrot") if Qrot is not None else 0,
-        _p(Knew), _p(Vnew), ldkv, _p(cs), _p(cu_rows), _p(ctx_len), B, M, _p(Kpool), _p(Vpool), num_pages,
-        _p(block_table), max_pages, Hq, Hkv, D, _stream(stream)), True)
+        _p(Q), ldq, _p(Qrot), ldqr, _p(Knew), _p(Vnew), ldkv, _p(cs), _p(cu_rows), _p(ctx_len), B, M, _p(Kpool),
+        _p(Vpool), num_pages, _p(block_table), max_pages, Hq, Hkv, D, _stream(stream)), True)
     return Qrot
 
 
@@ -566,21 +595,22 @@ def spec_chunk_attention_paged(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, s
     sequence b (Q [M, Hq*D]) attends keys 0 .. ctx_len[b] + j; returns O [M, Hq*D]."""
     B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table)
     _need(Q, torch.bfloat16, "Q")
-    M = Q.shape[0]
-    if Q.shape[1] % D:
+    ldq = _rowmajor(Q, "Q")
+    M, width = shape = Q.shape
+    if width % D:
         raise ValueError("Q must be [M, Hq*D]")
-    Hq = Q.shape[1] // D
     if O is None:
-        O = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=Q.device)
+        O = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
     _need(O, torch.bfloat16, "O")
-    if O.shape != Q.shape:
+    if O.shape != shape:
         raise ValueError("O must be [M, Hq*D]")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    Hq = width // D
     wp, wn = _ws_args(ws, spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages), Q.device)
     _check(_lib.spec_chunk_attention_paged(
-        _p(Q), _rowmajor(Q, "Q"), _p(cu_rows), _p(ctx_len), B, M, _p(Kpool), _p(Vpool), num_pages, _p(block_table),
-        max_pages, Hq, Hkv, D, float(scale), _p(O), _rowmajor(O, "O"), wp, wn, _stream(stream)), True)
+        _p(Q), ldq, _p(cu_rows), _p(ctx_len), B, M, _p(Kpool), _p(Vpool), num_pages, _p(block_table), max_pages, Hq,
+        Hkv, D, float(scale), _p(O), _rowmajor(O, "O"), wp, wn, _stream(stream)), True)
     return O
 
 

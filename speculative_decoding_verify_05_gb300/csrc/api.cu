@@ -1173,7 +1173,11 @@ int spec_rope_table_axes(const int32_t* pos, int ldpos, int axes, int M, int D, 
   if (!pos || !cs) return fail(SPEC_EINVAL, "NULL argument");
   if (ldpos < M && axes > 1) return fail(SPEC_EINVAL, "ldpos=%d < M=%d", ldpos, M);
   RopeAxes f{};
+  // theta^(-2 i / D) = theta^(-2 (i - i % 8) / D) theta^(-2 (i % 8) / D): a quarter of the powers, 1.5 roundings
+  double coarse = 1.0, fine[8];
+  for (int j = 0; j < 8; ++j) fine[j] = std::pow((double)theta, -2.0 * (double)j / (double)D);
   for (int i = 0, a = 0, end = sections[0]; i < half; ++i) {
+    if (i % 8 == 0) coarse = std::pow((double)theta, -2.0 * (double)i / (double)D);
     if (interleaved) {
       a = i % axes;
       if (i >= axes * sections[a]) a = 0;
@@ -1182,7 +1186,7 @@ int spec_rope_table_axes(const int32_t* pos, int ldpos, int axes, int M, int D, 
     }
     f.axis[i] = (unsigned char)a;
     // the frequency in turns, its whole turns dropped (positions are whole numbers)
-    double t = std::pow((double)theta, -2.0 * (double)i / (double)D) / 6.283185307179586476925286766559;
+    double t = coarse * fine[i % 8] / 6.283185307179586476925286766559;
     t -= std::floor(t);
     f.turn[i] = (unsigned long long)std::ldexp(t, 64);
   }
@@ -1742,7 +1746,7 @@ struct ChunkPlan {
 };
 static ChunkPlan plan_chunk() {
   ChunkPlan p;
-  p.grid = std::min(g_force_grid > 0 ? g_force_grid : plan_sms(), 1024);   // (one resident CTA per SM)
+  p.grid = std::min(g_force_grid > 0 ? g_force_grid : plan_sms(), CHUNK_MAX_GRID);   // (one resident CTA per SM)
   const size_t rows = size_t(p.grid) * 2 * 256;
   p.o_off = kCounterBytes;
   p.ml_off = p.o_off + rows * 128 * 4;

@@ -51,6 +51,7 @@ constexpr int SMEM = OFF_ML + 2 * TM * 8;
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 
+constexpr int MAX_GRID = CHUNK_MAX_GRID;
 // Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys.
 constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 192;
 
@@ -926,7 +927,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         if (p.t0 > 0) flags |= F_JOINS | (p.t1 == p.nt ? F_ENDS : 0);
         else {
           flags |= F_OPENS;
-          item = make_int4(0, p.b, p.h, p.q);
+          item = make_int4(0, p.row0, p.tok, p.h);
         }
         const unsigned tiles = p.tiles(), nt = p.nt;
         if (!a.join && __shfl_sync(0xffffffffu, seen, 0) + tiles == nt) {
@@ -1065,48 +1066,39 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   }
 }
 
-// Joins the pieces of every item that a cut fell into, for calls whose items have many pieces of many rows (one CTA
-// joining them all would take longer than this launch): block (c, y) takes 8 rows at a time of the item that CTA
-// c opened and did not end.  Each of 8 warps sums every 8th piece, all its loads in flight together; the warps'
-// sums are added in warp order.
-constexpr int JOIN_ROWS = 8, JOIN_BLOCKS = 8;
+// Joins the pieces of every item that a cut fell into, 8 rows of an item at a time.  Every block reads all CTAs' flags
+// (one round trip) and takes its share of the (rows, item) tasks; of a task's pieces each of 8 warps sums every 8th,
+// all its loads in flight together, and the warps' sums are added in warp order.
+constexpr int JOIN_ROWS = 8;
 __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkAttnArgs a, int grid) {
   __shared__ float4 s_o[8][32][JOIN_ROWS + 1];
   __shared__ float2 s_ml[8][JOIN_ROWS];
-  __shared__ int s_list[1024];            // contributing CTAs
+  __shared__ uint8_t s_flag[MAX_GRID];
+  __shared__ uint16_t s_open[MAX_GRID];   // the CTAs that opened an item, in order (every block's list is the same)
   __shared__ int s_n;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
-  const int c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int4 it = a.part_item[c0];
-  if (!(it.x & F_OPENS)) return;
+  for (int c = tid; c < grid; c += 256) s_flag[c] = (uint8_t)a.part_item[c].x;
+  __syncthreads();
   if (warp == 0) {
-    int n = 0;
-    for (int base = c0; base < grid; base += 32) {
-      const int c = base + lane;
-      const int f = c < grid && c > c0 ? a.part_item[c].x : 0;
-      unsigned has = __ballot_sync(0xffffffffu, c == c0 || (f & F_JOINS));
-      const unsigned ends = __ballot_sync(0xffffffffu, (f & F_ENDS) != 0);
-      if (ends) has &= 2u * (ends & -ends) - 1u;
-      const int at = n + __popc(has & ((1u << lane) - 1u));
-      if (((has >> lane) & 1u) && at < 1024) s_list[at] = c;
-      n += __popc(has);
-      if (ends) break;
+    int at = 0;
+    for (int base = 0; base < grid; base += 32) {
+      const bool opens = base + lane < grid && (s_flag[base + lane] & F_OPENS);
+      const unsigned m = __ballot_sync(0xffffffffu, opens);
+      if (opens) s_open[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(base + lane);
+      at += __popc(m);
     }
-    if (lane == 0) s_n = min(n, 1024);
+    if (lane == 0) s_n = at;
   }
-  Walk w;
-  w.p.b = it.y; w.p.h = it.z; w.p.q = it.w;
-  w.s = seq_of(a, it.y);
-  w.item(2 * a.tpt);
-  const Piece& p = w.p;
-  auto token = [&](int rr) { return (rr >> 7) * a.tpt + (rr & 127) / a.G; };
-  auto used = [&](int rr) { return (rr & 127) / a.G < a.tpt && token(rr) < p.tok; };
   __syncthreads();
   const int n = s_n;
-  for (int y = blockIdx.y; y < 2 * TM / JOIN_ROWS; y += gridDim.y) {
-    // (rows wholly behind the item's tokens)
-    if (token(y * JOIN_ROWS) >= p.tok) continue;
+  for (int task = blockIdx.x; task < n * (2 * TM / JOIN_ROWS); task += gridDim.x) {
+    const int y = task / n, c0 = s_open[task - y * n];
+    const int4 it = a.part_item[c0];       // flags, first row, tokens, kv head
+    auto token = [&](int rr) { return (rr >> 7) * a.tpt + (rr & 127) / a.G; };
+    auto used = [&](int rr) { return (rr & 127) / a.G < a.tpt && token(rr) < it.z; };
+    if (token(y * JOIN_ROWS) >= it.z) continue;                    // (rows behind the item's tokens)
     {
       const int rr = y * JOIN_ROWS + (lane & 7), d4 = lane >> 3;
       const bool mine = used(rr);
@@ -1114,28 +1106,36 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkAttnArgs a, 
       float4 o[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (mine)
-        for (int i = warp; i < n; i += 8) {
-          const int c = s_list[i];
-          const size_t at = (size_t)c * 2 + (c == c0 ? 1 : 0);
-          // (with one row tile each half of the dims has its own copy of the maximum and sum: the same)
-          const float2 ml = __ldcg(&a.part_ml[(at * 2 + (p.dual ? rr >> 7 : 0)) * (2 * TM) + rr]);
-          const float4* src = reinterpret_cast<const float4*>(a.part_o + at * (2 * TM * D)) + rr;
-          float4 v[8];
+      int count = 0;
+      for (int base = c0, ends = 0; !ends && base < grid; base += 32) {
+        const int c = base + lane, f = c < grid && c > c0 ? s_flag[c] : 0;
+        unsigned has = __ballot_sync(0xffffffffu, c == c0 || (f & F_JOINS));
+        ends = (int)__ballot_sync(0xffffffffu, (f & F_ENDS) != 0);
+        if (ends) has &= 2u * (unsigned)(ends & -ends) - 1u;
+        for (; has; has &= has - 1)
+          if ((count++ & 7) == warp && mine) {
+            const int from = base + __ffs(has) - 1;
+            const size_t at = (size_t)from * 2 + (from == c0 ? 1 : 0);
+            // (with one row tile each half of the dims has its own copy of the maximum and sum: the same)
+            const float2 ml = __ldcg(&a.part_ml[(at * 2 + (it.z > a.tpt ? rr >> 7 : 0)) * (2 * TM) + rr]);
+            const float4* src = reinterpret_cast<const float4*>(a.part_o + at * (2 * TM * D)) + rr;
+            float4 v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (size_t)(d4 + 4 * k) * (2 * TM));
-          const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
-          const float fo = ex2(m - base), fc = ex2(ml.x - base);
-          m = top;
-          l = l * fo + ml.y * fc;
+            for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (size_t)(d4 + 4 * k) * (2 * TM));
+            const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+            const float fo = ex2(m - ref), fc = ex2(ml.x - ref);
+            m = top;
+            l = l * fo + ml.y * fc;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            o[k].x = o[k].x * fo + v[k].x * fc;
-            o[k].y = o[k].y * fo + v[k].y * fc;
-            o[k].z = o[k].z * fo + v[k].z * fc;
-            o[k].w = o[k].w * fo + v[k].w * fc;
+            for (int k = 0; k < 8; ++k) {
+              o[k].x = o[k].x * fo + v[k].x * fc;
+              o[k].y = o[k].y * fo + v[k].y * fc;
+              o[k].z = o[k].z * fo + v[k].z * fc;
+              o[k].w = o[k].w * fo + v[k].w * fc;
+            }
           }
-        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) s_o[warp][d4 + 4 * k][lane & 7] = o[k];
       if (lane < JOIN_ROWS) s_ml[warp][lane] = make_float2(m, l);
@@ -1160,9 +1160,8 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkAttnArgs a, 
           o.w += v.w * f;
         }
         const float inv = 1.f / l;
-        *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + token(r)) * a.ldo +
-                                  (size_t)(p.h * a.G + (r & 127) % a.G) * D + lane * 4) =
-            make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2*>(a.O + (size_t)(it.y + token(r)) * a.ldo + (size_t)(it.w * a.G + (r & 127) % a.G) * D +
+                                  lane * 4) = make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
       }
     }
     __syncthreads();
@@ -1188,7 +1187,7 @@ cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk,
   }
   cudaError_t e = launch_k(chunk_attention_kernel, dim3(grid), dim3(THREADS), SMEM, s, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
-  if (a.join) e = launch_k(chunk_join_kernel, dim3(grid, JOIN_BLOCKS), dim3(256), 0, s, a, grid);
+  if (a.join) e = launch_k(chunk_join_kernel, dim3(2 * grid), dim3(256), 0, s, a, grid);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -225,11 +225,12 @@ struct ChunkAttnArgs {
   float2* part_ml;                      // [grid][2][2][256] running maximum (times scale_log2) and sum, as left by
                                         // the warps of slot 0 and of slot 1
   int join;                             // 1: a second kernel joins the pieces, 0: the last CTA of each item does
-  int4* part_item;                      // [grid] flags; sequence, kv head and index of the item it opened
+  int4* part_item;                      // [grid] flags; first row, tokens and kv head of the item it opened
   unsigned* counters;                   // [grid][8] key tiles of an item's pieces that have arrived, at the CTA that
                                         // opened it, per warp (its rows, or its rows and half of the dims)
   unsigned* status;
 };
+constexpr int CHUNK_MAX_GRID = 1024;
 // Q map: boxes of 64 dims x G heads x tpt rows; K / V maps: boxes of 64 dims x one page.  `grid` CTAs.
 cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                    const ChunkAttnArgs& a, int grid, cudaStream_t s);

@@ -10,88 +10,136 @@ namespace {
 constexpr int D = 128;
 constexpr int PAGE = 128;
 
-// (cos, sin) of x turns, x = u / 2^64.  The position times the frequency is formed modulo one turn in 64-bit
-// integers (wrap-around is the reduction, exact for any 32-bit position), the nearest quarter turn
-// is split off, and what is left, at most an eighth of a turn, is exact to 2^-33 turns before its one
-// rounding to fp32.  No fp64 instruction: the chip has few of them.
+// (cos, sin) of u / 2^64 turns.  The position times the frequency is formed modulo one turn in 64-bit integers
+// (wrap-around is the reduction, exact for any 32-bit position), the nearest quarter turn is split off,
+// and what is left, at most an eighth of a turn, is exact to 2^-33 turns before its one rounding to fp32.  There
+// the Taylor series of sin(pi x) and cos(pi x) on |x| <= 1/4 (terms to (pi x)^9 and (pi x)^10: the next are below
+// 2e-9) take 11 multiply-adds; sincospif, which has the whole line to care for, made the 16000-row table
+// 7.6 us instead of 4.5.  No fp64 instruction: the chip has few of them.
 __device__ __forceinline__ float2 cos_sin_turns(unsigned long long u) {
   const unsigned hi = (unsigned)(u >> 32);
   const unsigned quarter = (hi + (1u << 29)) >> 30;                 // 0..4, 4 = 0
-  const int rem = (int)(hi - (quarter << 30));                      // [-2^29, 2^29)
-  float s, c;
-  sincospif((float)rem * 0x1p-31f, &s, &c);                         // 2 pi rem / 2^32 = pi (rem / 2^31)
-  switch (quarter & 3u) {
-    case 0: return make_float2(c, s);
-    case 1: return make_float2(-s, c);
-    case 2: return make_float2(-c, -s);
-    default: return make_float2(s, -c);
-  }
+  const float x = (float)(int)(hi - (quarter << 30)) * 0x1p-31f;    // 2 pi rem / 2^32 = pi (rem / 2^31)
+  const float z = x * x;
+  // pi^k / k!; pi in two parts
+  float s = 0.08214588661112822879880237f;
+  s = fmaf(s, z, -0.5992645293207919f);
+  s = fmaf(s, z, 2.550164039877345f);
+  s = fmaf(s, z, -5.167712780049969f);
+  s = fmaf(s, z, -8.742278012618954e-8f);
+  s = fmaf(x, 3.1415927410125732421875f, x * s);
+  float c = -0.02580689139001405f;
+  c = fmaf(c, z, 0.23533063035889312f);
+  c = fmaf(c, z, -1.3352627688545893f);
+  c = fmaf(c, z, 4.058712126416768f);
+  c = fmaf(c, z, -4.934802200544679f);
+  c = fmaf(c, z, 1.f);
+  // a quarter turn maps (c, s) to (-s, c)
+  const float a = (quarter & 1u) ? s : c, b = (quarter & 1u) ? c : s;
+  return make_float2(((quarter + 1u) & 2u) ? -a : a, (quarter & 2u) ? -b : b);
 }
 
-// One thread per table entry.
+// A thread keeps one frequency and walks `rows` rows with it (its turn and axis come from the parameter bank, where
+// 32 lanes with 32 addresses are served one after the other: per entry that, and integer divisions, took
+// 16.4 us for 16000 rows of 64).
 __global__ void __launch_bounds__(256)
-rope_table_axes_kernel(const int32_t* __restrict__ pos, int ldpos, int M, int half, const __grid_constant__ RopeAxes f,
-                       float2* __restrict__ cs) {
+rope_table_axes_kernel(const int32_t* __restrict__ pos, int ldpos, int M, int half, int rows,
+                       const __grid_constant__ RopeAxes f, float2* __restrict__ cs) {
   pdl_wait();
   pdl_trigger();
-  const long long total = (long long)M * half;
-  for (long long idx = blockIdx.x * 256ll + threadIdx.x; idx < total; idx += gridDim.x * 256ll) {
-    const int r = (int)(idx / half), i = (int)(idx - (long long)r * half);
-    const int p = pos[(size_t)f.axis[i] * ldpos + r];
-    cs[idx] = cos_sin_turns((unsigned long long)(long long)p * f.turn[i]);
+  const int i = threadIdx.x;
+  if (i >= half) return;
+  const unsigned long long turn = f.turn[i];
+  const int32_t* p = pos + (size_t)f.axis[i] * ldpos;
+  const int r0 = (blockIdx.x * blockDim.y + threadIdx.y) * rows, r1 = min(r0 + rows, M);
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) cs[(size_t)r * half + i] = cos_sin_turns((unsigned long long)(long long)p[r] * turn);
+}
+
+// The last sequence with cu_rows[b] <= r, -1 if none: 32 candidates at a time, by a whole warp.
+__device__ __forceinline__ int sequence_of(int r, const int32_t* __restrict__ cu_rows, int B, int lane) {
+  int lo = 0, n = B;
+  while (true) {
+    const int step = (n + 31) >> 5, b = lo + lane * step;
+    const unsigned votes = __ballot_sync(0xffffffffu, b < lo + n && cu_rows[b] <= r);
+    if (votes == 0) return -1;                          // (only before the first)
+    const int k = 31 - __clz(votes);
+    if (step == 1) return lo + k;
+    n = min(step, n - k * step);
+    lo += k * step;
   }
 }
 
-// One CTA per row; a thread moves one 8-element pair of chunks (i, i + 64) of a head at a time.
+// One CTA per row.  A thread moves pairs of 16-byte chunks (dims i0 .. and 64 + i0 ..) of heads 16 apart, so its
+// eight angles stay in registers; up to UNITS pairs are loaded before the row's place in the cache is known,
+// which takes three dependent loads.  Bound by HBM: 8192 rows of 32 + 2 x 8 heads, 206 MB, in 33.4 us (6.2 TB/s);
+// 24 sequences of 1 to 999 rows, 81 MB, in 15.9 us with a binary search and a unit at a time.
+constexpr int UNITS = 4;
 __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.x;
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {                     // the last sequence with cu_rows[b] <= r
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cu_rows[mid] <= r) lo = mid; else hi = mid - 1;
-  }
-  const int c0 = a.cu_rows[lo], c1 = a.cu_rows[lo + 1], ctx = a.ctx_len[lo];
-  if (r < c0 || r >= c1) return;        // padding
-  if (c0 < 0 || c1 > a.M || ctx < 0 || (long long)ctx + (c1 - c0) > (long long)a.max_pages * PAGE) {
-    if (threadIdx.x == 0) set_status(a.status, 0x6F1u);
-    return;
-  }
-  const int p = ctx + (r - c0);
-  const int page = a.block_table[(size_t)lo * a.max_pages + p / PAGE];
-  const bool bad = page < 0 || page >= a.num_pages;
-  if (bad && threadIdx.x == 0) set_status(a.status, 0x6F2u);
-  for (int u = threadIdx.x; u < (a.Hq + 2 * a.Hkv) * 8; u += 128) {
-    const int hd = u >> 3, i0 = (u & 7) * 8;
-    const uint16_t* src;
-    uint16_t* dst;
-    bool turn = a.cs != nullptr;
-    if (hd < a.Hq) {
-      src = a.Q + (size_t)r * a.ldq + (size_t)hd * D;
-      dst = a.Qrot + (size_t)r * a.ldqr + (size_t)hd * D;
-    } else {
-      if (bad) continue;
-      const bool is_v = hd >= a.Hq + a.Hkv;
-      const int g = hd - a.Hq - (is_v ? a.Hkv : 0);
-      turn = turn && !is_v;
-      src = (is_v ? a.Vnew : a.Knew) + (size_t)r * a.ldkv + (size_t)g * D;
-      dst = (is_v ? a.Vpool : a.Kpool) + (((size_t)g * a.num_pages + page) * PAGE + p % PAGE) * D;
-    }
-    uint4 x = *reinterpret_cast<const uint4*>(src + i0), y = *reinterpret_cast<const uint4*>(src + 64 + i0);
-    if (turn) {
-      uint32_t* xa = reinterpret_cast<uint32_t*>(&x);
-      uint32_t* ya = reinterpret_cast<uint32_t*>(&y);
+  const int r = blockIdx.x, tid = threadIdx.x, i0 = (tid & 7) * 8;
+  const int heads = a.Hq + 2 * a.Hkv;
+  float4 t[4];                                          // (cos, sin) of dims i0 ..
+  if (a.cs)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 t0 = a.cs[(size_t)r * 64 + i0 + 2 * e], t1 = a.cs[(size_t)r * 64 + i0 + 2 * e + 1];
-        const float a0 = bf16lo(xa[e]), a1 = bf16hi(xa[e]), b0 = bf16lo(ya[e]), b1 = bf16hi(ya[e]);
-        xa[e] = pack_bf16x2(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
-        ya[e] = pack_bf16x2(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
+    for (int k = 0; k < 4; ++k) t[k] = *(reinterpret_cast<const float4*>(a.cs + (size_t)r * 64 + i0) + k);
+  int b = -2, page = 0, p = 0;
+  for (int h0 = tid >> 3; h0 < heads || b == -2; h0 += 16 * UNITS) {
+    uint4 x[UNITS], y[UNITS];
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+      const int hd = h0 + 16 * k;
+      if (hd >= heads) continue;
+      const uint16_t* src;
+      if (hd < a.Hq) src = a.Q + (size_t)r * a.ldq + (size_t)hd * D;
+      else if (hd < a.Hq + a.Hkv) src = a.Knew + (size_t)r * a.ldkv + (size_t)(hd - a.Hq) * D;
+      else src = a.Vnew + (size_t)r * a.ldkv + (size_t)(hd - a.Hq - a.Hkv) * D;
+      x[k] = *reinterpret_cast<const uint4*>(src + i0);
+      y[k] = *reinterpret_cast<const uint4*>(src + 64 + i0);
+    }
+    if (b == -2) {                                      // the row's sequence, position and page
+      b = sequence_of(r, a.cu_rows, a.B, tid & 31);
+      if (b < 0) return;                                // padding
+      const int c0 = a.cu_rows[b], c1 = a.cu_rows[b + 1], ctx = a.ctx_len[b];
+      if (r >= c1) return;                              // padding
+      if (c0 < 0 || c1 > a.M || ctx < 0 || (long long)ctx + (c1 - c0) > (long long)a.max_pages * PAGE) {
+        if (tid == 0) set_status(a.status, 0x6F1u);
+        return;
+      }
+      p = ctx + (r - c0);
+      page = a.block_table[(size_t)b * a.max_pages + p / PAGE];
+      if (page < 0 || page >= a.num_pages) {
+        if (tid == 0) set_status(a.status, 0x6F2u);
+        page = -1;
       }
     }
-    *reinterpret_cast<uint4*>(dst + i0) = x;
-    *reinterpret_cast<uint4*>(dst + 64 + i0) = y;
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+      const int hd = h0 + 16 * k;
+      if (hd >= heads) continue;
+      const bool is_v = hd >= a.Hq + a.Hkv;
+      uint16_t* dst;
+      if (hd < a.Hq) {
+        dst = a.Qrot + (size_t)r * a.ldqr + (size_t)hd * D;
+      } else {
+        if (page < 0) continue;
+        const int g = hd - a.Hq - (is_v ? a.Hkv : 0);
+        dst = (is_v ? a.Vpool : a.Kpool) + (((size_t)g * a.num_pages + page) * PAGE + p % PAGE) * D;
+      }
+      if (a.cs && !is_v) {
+        uint32_t* xa = reinterpret_cast<uint32_t*>(&x[k]);
+        uint32_t* ya = reinterpret_cast<uint32_t*>(&y[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a0 = bf16lo(xa[e]), a1 = bf16hi(xa[e]), b0 = bf16lo(ya[e]), b1 = bf16hi(ya[e]);
+          xa[e] = pack_bf16x2(a0 * t[e].x - b0 * t[e].y, a1 * t[e].z - b1 * t[e].w);
+          ya[e] = pack_bf16x2(b0 * t[e].x + a0 * t[e].y, b1 * t[e].z + a1 * t[e].w);
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + i0) = x[k];
+      *reinterpret_cast<uint4*>(dst + 64 + i0) = y[k];
+    }
   }
 }
 
@@ -99,9 +147,11 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
 
 cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int half, const RopeAxes& f, float2* cs,
                                    cudaStream_t s) {
-  long long grid = ((long long)M * half + 255) / 256;
-  if (grid > 152 * 8) grid = 152 * 8;
-  cudaError_t e = launch_k(rope_table_axes_kernel, dim3((unsigned)grid), dim3(256), 0, s, pos, ldpos, M, half, f, cs);
+  // rows per thread: one while that fills the chip, more (up to 8) when there are many
+  const int bx = (half + 31) / 32 * 32, by = bx < 256 ? 256 / bx : 1;
+  const int rows = M / (by * 152 * 4) < 1 ? 1 : (M / (by * 152 * 4) > 8 ? 8 : M / (by * 152 * 4));
+  cudaError_t e = launch_k(rope_table_axes_kernel, dim3((unsigned)((M + by * rows - 1) / (by * rows))), dim3(bx, by), 0, s,
+                           pos, ldpos, M, half, rows, f, cs);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
