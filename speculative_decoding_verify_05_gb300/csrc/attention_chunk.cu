@@ -978,8 +978,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const int n = p.steps(sl), t0 = p.t0;
       const int x = dual ? sl : 0;         // the slot's row tile
       const int pos = p.pos + min(x * a.tpt + row_tok, p.tok - 1);      // the row sees keys 0 .. pos
+      const bool live = row_used && x * a.tpt + row_tok < p.tok;        // (the other rows hold anything)
       const int pos_lo = __shfl_sync(0xffffffffu, pos, 0), pos_hi = __shfl_sync(0xffffffffu, pos, 31);
-      float m_run = -INFINITY, l_run = 0.f;
+      float ref = 0.f, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
         const int key0 = (t0 + (dual ? j : 2 * j + sl)) * KT;
         ok = ok && mbar_wait(&s_full[sl], n_s & 1, a.status, 0x741u);
@@ -1000,55 +1001,64 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           }
           tmem_st_wait();
         }
-        uint32_t r[128];
-        tmem_ld_cols128(t_s, r);
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // Weights relative to the row's reference, not to its maximum: any reference within 2^20 above and 2^60
+        // below the maximum gives the same quotients (bf16 and fp32 have exponents to spare), so nothing
+        // waits for a maximum.  The tile's sum tells when the reference is out of that range (or the first keys
+        // in sight are); then the maximum is found and taken, O rescaled, and the weights formed again.
+        uint32_t pk[64];
+        float tile_sum;
+        for (bool again = false;; again = true) {
+          uint32_t r[128];
+          tmem_ld_cols128(t_s, r);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(-ref, -ref);
 #pragma unroll
-        for (int k = 0; k < 128; k += 2)
-          mx4[(k >> 1) & 3] = fmaxf(fmaxf(mx4[(k >> 1) & 3], __uint_as_float(r[k])), __uint_as_float(r[k + 1]));
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale;
-        // the running maximum follows only when a tile exceeds it by more than 8 (2^8 in the weights): O and
-        // the sum keep one common reference, so the result is the same and O is rarely rescaled
-        const float m_new = mx > m_run + 8.f ? mx : m_run;
-        const bool grew = m_new != m_run;
-        const float base = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = ex2(m_run - base);
-        m_run = m_new;
-        // O is whole here: the scores' barrier came after the slot's P V before them
-        if (j > 0 && __any_sync(0xffffffffu, grew)) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld_cols32(t_o + c, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st_cols32(t_o + c, o);
-          }
-        }
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(-base, -base);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float2 e = fma2(make_float2(__uint_as_float(r[64 * half + 2 * k]), __uint_as_float(r[64 * half + 2 * k + 1])),
-                            sc2, nb2);
+          for (int k = 0; k < 64; ++k) {
+            float2 e = fma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nb2);
             e.x = ex2(e.x);
             e.y = ex2(e.y);
             sum[k & 1] = add2(sum[k & 1], e);
             pk[k] = cvt_bf16x2(e.x, e.y);
           }
-          tmem_st_cols32(t_s + 32 * half, pk);
+          const float2 s2 = add2(sum[0], sum[1]);
+          tile_sum = s2.x + s2.y;
+          const bool out = live && (!(tile_sum <= 0x1p27f) || (l_run == 0.f && !(tile_sum >= 0x1p-60f)));
+          if (again || !__any_sync(0xffffffffu, out)) break;
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < KT; c += 32) {
+            float v[32];
+            tmem_ld_cols<32>(t_s + c, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
+          }
+          mx *= scale;
+          // (a sum above 2^27 has a weight above 2^20; nothing in sight: the reference stays)
+          const bool move = mx > ref + 19.f || (l_run == 0.f && mx < ref - 40.f && mx > -INFINITY);
+          const float alpha = !move ? 1.f : (l_run == 0.f ? 0.f : ex2(ref - mx));
+          if (move) ref = mx;
+          l_run *= alpha;
+          // O is whole here: the scores' barrier came after the slot's P V before them
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld_cols32(t_o + c, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st_cols32(t_o + c, o);
+            }
+          }
         }
+        l_run += tile_sum;
+        tmem_st_cols32(t_s, pk);
+        tmem_st_cols32(t_s + 32, pk + 32);
         tmem_st_wait();
-        const float2 s2 = add2(sum[0], sum[1]);
-        l_run = l_run * alpha + (s2.x + s2.y);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sl]);
       }
-      finish(p, m_run, l_run);
+      finish(p, l_run == 0.f ? -INFINITY : ref, l_run);          // (no key in sight: no say in the reference)
       __syncwarp();
       if (lane == 0) mbar_arrive(&taken[k % PR]);
     }
