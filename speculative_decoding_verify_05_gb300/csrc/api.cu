@@ -1739,10 +1739,9 @@ int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr,
   return ok(1);
 }
 
-constexpr long long kChunkJoinRows = 1024;   // rows of all pieces of an item from which a second launch joins them
 struct ChunkPlan {
   int grid;
-  size_t o_off, ml_off, item_off, bytes;
+  size_t o_off, ml_off, bytes;
 };
 static ChunkPlan plan_chunk() {
   ChunkPlan p;
@@ -1750,8 +1749,7 @@ static ChunkPlan plan_chunk() {
   const size_t rows = size_t(p.grid) * 2 * 256;
   p.o_off = kCounterBytes;
   p.ml_off = p.o_off + rows * 128 * 4;
-  p.item_off = p.ml_off + rows * 16;
-  p.bytes = p.item_off + round_up(size_t(p.grid) * 16, 256);
+  p.bytes = p.ml_off + rows * 16;
   return p;
 }
 
@@ -1809,20 +1807,13 @@ int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_ro
   a.wide = (reinterpret_cast<uintptr_t>(O) & 31u) == 0 && ldo % 16 == 0 ? 1 : 0;
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
   a.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
-  a.part_item = reinterpret_cast<int4*>(ws + p.item_off);
   a.counters = reinterpret_cast<unsigned*>(ws);
   a.t_magic = (unsigned)((1ull << 32) / (2 * tpt)) + 1;
   a.inv_grid = ~0ull / p.grid;
-  // Pieces of an item: the CTAs per item, and the rows of each, by what the host knows of the batch (the lengths
-  // are on the device).  Few: the last CTA joins them; many: a second launch does (one CTA would read them at
-  // 100 GB/s or so).
-  const long long items = std::max(1LL, (long long)Hkv * std::max((M + 2 * tpt - 1) / (2 * tpt), std::min(B, M)));
-  const long long rows_per_item = std::min(256LL, (long long)M * G);
-  a.join = p.grid * rows_per_item > items * kChunkJoinRows ? 1 : 0;
   a.status = d->status;
   cudaError_t e = launch_chunk_attention(tq, tk, tv, a, p.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
-  return ok(a.join ? 2 : 1);
+  return ok(1);
 }
 
 // --------------------------------------------------------------------------- sampler

@@ -51,7 +51,7 @@ constexpr int SMEM = OFF_ML + 2 * TM * 8;
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 
-constexpr int MAX_GRID = CHUNK_MAX_GRID;
+constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys.
 constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 192;
 
@@ -116,10 +116,8 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ unsigned add_acq_rel(unsigned* p, unsigned v) {
-  unsigned old;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
+__device__ __forceinline__ void red_release(unsigned* p, unsigned v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 // 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0)
 __device__ __forceinline__ float ex2(float x) {
@@ -131,6 +129,23 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// The library's bounded wait, short: thirty of them are in this kernel, and what runs once per piece runs from a
+// cold instruction cache.  Each role tells the status word itself when one ran out.
+// (The limit is in cycles, a second or more: the wall clock takes long to read.)
+constexpr uint32_t WAIT_CYCLES = 1u << 31;
+__device__ __forceinline__ uint32_t cycles() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %clock;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = cycles();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (cycles() - t0 < WAIT_CYCLES);
+  return false;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -329,11 +344,6 @@ struct Walk {
   }
 };
 
-// Flags of a CTA for the joining kernel.
-constexpr int F_OPENS = 1;      // its last piece starts an item and does not end it (partial slot 1)
-constexpr int F_JOINS = 2;      // its first piece continues an item (partial slot 0) ...
-constexpr int F_ENDS = 4;       // ... to its end
-
 __global__ void __launch_bounds__(THREADS, 1)
 chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const ChunkAttnArgs a) {
@@ -401,7 +411,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
     long long own = 0;
     bool bad = false;
-#pragma unroll 4
+#pragma unroll 2
     for (int b = b0; b < b1; ++b) {
       bool wrong;
       const Seq s = seq_of(a, b, &wrong);
@@ -453,7 +463,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       *s_first = w.p;
       *s_total = total;
       for (int k = 0;; ++k) {
-        if (k >= PR && !mbar_wait(&taken[k % PR], (uint32_t)((k / PR - 1) & 1), a.status, 0x701u)) break;
+        if (k >= PR && !wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1))) {
+          set_status(a.status, 0x701u);
+          break;
+        }
         ring[k % PR] = w.p;
         mbar_arrive(&posted[k % PR]);
         if (!w.p.more) break;
@@ -484,7 +497,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
       const int page = __shfl_sync(0xffffffffu, pg.id, t - pg.base);
       const int st = idx % ST;
-      if (idx >= ST) ok = ok && mbar_wait(&empty[st], (uint32_t)((idx / ST - 1) & 1), a.status, 0x711u);
+      if (idx >= ST) ok = ok && wait_for(&empty[st], (uint32_t)((idx / ST - 1) & 1));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       const bool tail = is_v && t == p.nt - 1 && p.tail();
@@ -511,29 +524,30 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       ++idx;
     };
     auto open = [&](int k) {
-      ok = ok && mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x713u);
+      ok = ok && wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1));
       ok = __all_sync(0xffffffffu, ok);
       Piece p = ring[k % PR];
       if (!ok) p.more = 0;
       return p;
     };
+    // pair by pair (before the first: K only): V and the next K of slot 0, then of slot 1
     Piece p = open(0), nx = p;
     Pages pv{0, -1}, pk{0, -1};
-    if (p.more) {
-      load(p, pk, p.tile(0, 0), false);
-      if (ok && !p.dual && p.steps(1) > 0) load(p, pk, p.tile(1, 0), false);
-    }
-    for (int k = 0, j = 0; ok && p.more;) {
+    for (int k = 0, j = -1; ok && nx.more;) {
       const bool ends = j + 1 == p.pairs();
       if (ends) {
         nx = open(k + 1);
         pk.base = -1;
       }
       const int nj = ends ? 0 : j + 1;
-#pragma unroll
-      for (int sl = 0; sl < 2; ++sl) {
-        if (ok && (sl == 0 || !p.dual) && j < p.steps(sl)) load(p, pv, p.tile(sl, j), true);
-        if (ok && nx.more && (sl == 0 || !nx.dual) && nj < nx.steps(sl)) load(nx, pk, nx.tile(sl, nj), false);
+#pragma unroll 1
+      for (int q = 0; q < 4 && ok; ++q) {
+        const int sl = q >> 1;
+        const bool is_v = !(q & 1);
+        const Piece& from = is_v ? p : nx;
+        const int at = is_v ? j : nj;
+        if (at >= 0 && from.more && (sl == 0 || !from.dual) && at < from.steps(sl))
+          load(from, is_v ? pv : pk, from.tile(sl, at), is_v);
       }
       j = nj;
       if (ends) {
@@ -545,10 +559,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
     }
     if (!ok) {                             // gave up: see the copies in flight land before leaving
+      set_status(a.status, 0x711u);
       for (int j = idx > ST ? idx - ST : 0; j < idx; ++j) {
         const int st = j % ST;
-        if ((landed >> st) & 1u) mbar_wait(&land[st], ((n_land >> st) & 1u) ^ 1u, a.status, 0x712u);
-        else mbar_wait(&full[st], (uint32_t)((j / ST) & 1), a.status, 0x712u);
+        if ((landed >> st) & 1u) wait_for(&land[st], ((n_land >> st) & 1u) ^ 1u);
+        else wait_for(&full[st], (uint32_t)((j / ST) & 1));
       }
     }
   } else if (warp == 9) {
@@ -567,8 +582,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     int st = 0;                            // next ring stage
     uint32_t ph = 0, ph_p = 0, ph_q = 0;   // phases: the ring's; each slot's weights and Q tile, one bit per slot
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
-      if (ok) ok = mbar_wait(bar, parity, a.status, site);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = wait_for(bar, parity);
     };
     // the next ring stage and its phase
     struct Stage {
@@ -584,11 +599,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       return mine;
     };
     auto ready = [&](const Stage& t) { return mbar_try_wait(&full[t.st], t.ph); };
-    auto wait_tile = [&](const Stage& t) { wait(&full[t.st], t.ph, 0x721u); };
+    auto wait_tile = [&](const Stage& t) { wait(&full[t.st], t.ph); };
     // scores of a slot from the K tile of stage kst; first / last: of the slot's steps of the piece
     auto scores = [&](const int sl, int kst, bool first, bool last, bool release) {
       if (first) {
-        wait(&q_full[sl], (ph_q >> sl) & 1u, 0x722u);
+        wait(&q_full[sl], (ph_q >> sl) & 1u);
         ph_q ^= 1u << sl;
         tc_fence_after();
       }
@@ -623,61 +638,79 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       int tail;                            // 16-key steps of its last tile up to the last key
     };
     auto open = [&](int k) {
-      wait(&posted[k % PR], (uint32_t)((k / PR) & 1), 0x724u);
+      wait(&posted[k % PR], (uint32_t)((k / PR) & 1));
       ok = __all_sync(0xffffffffu, ok);
       const Piece& p = ring[k % PR];
       Run r{ok && p.more, p.dual != 0, p.steps(0), p.steps(1), min(8, (p.keys() - (p.t1 - 1) * KT + 15) >> 4)};
       return r;
     };
+    // pair by pair (before the first: scores only)
     Run r = open(0), nx = r;
     Stage k_a{0, 0}, k_b{0, 0}, v_a{0, 0}, v_b{0, 0};
-    if (r.more) {
-      k_a = take();
-      wait_tile(k_a);
-      tc_fence_after();
-      scores(0, k_a.st, true, r.n0 == 1, !r.dual);
-      if (r.n1 > 0) {
-        k_b = r.dual ? k_a : take();
-        wait_tile(k_b);
+    for (int k = 0, j = -1; nx.more;) {
+      // two row tiles, and the next pair of the same piece: nothing to decide (with the general case's
+      // decisions in the way 2048 rows at 30000 keys took 700 us instead of 650)
+      while (r.dual && j >= 0 && j + 1 < r.n0) {
+        const Stage v = take(), t = take();
+        const uint32_t pa = ph_p & 1u, pb = (ph_p >> 1) & 1u;
+        const bool r0 = ready(v), r1 = ready(t), r2 = mbar_try_wait(&p_full[0], pa);
+        if (!(r0 && r1 && r2)) {
+          wait_tile(v);
+          wait_tile(t);
+          wait(&p_full[0], pa);
+        }
         tc_fence_after();
-        scores(1, k_b.st, true, r.n1 == 1, true);
+        weigh(0, v.st, 8, j == 0, false, false);
+        scores(0, t.st, false, j + 2 == r.n0, false);
+        wait(&p_full[1], pb);
+        tc_fence_after();
+        weigh(1, v.st, 8, j == 0, false, true);
+        scores(1, t.st, false, j + 2 == r.n0, true);
+        ph_p ^= 3u;
+        ++j;
       }
-    }
-    for (int k = 0, j = 0; r.more;) {
       const bool ends = j + 1 == r.n0;     // (slot 0 has a step in every pair)
       if (ends) nx = open(k + 1);
       const int nj = ends ? 0 : j + 1;
-      const bool next_a = nx.more, next_b = nx.more && nj < nx.n1, now_b = j < r.n1;
+      const bool now_a = j >= 0, now_b = now_a && j < r.n1, next_a = nx.more, next_b = nx.more && nj < nx.n1;
       const bool last_tile_b = !r.dual && now_b && ends;      // slot 1 holds the piece's last tile
       // one look at all that slot 0 needs; what is not there is waited for in turn
-      v_a = take();
+      if (now_a) v_a = take();
       if (next_a) k_a = take();
       const uint32_t pa = ph_p & 1u, pb = (ph_p >> 1) & 1u;
-      const bool r0 = ready(v_a), r1 = ready(k_a), r2 = mbar_try_wait(&p_full[0], pa);
-      if (!(r0 && (r1 || !next_a) && r2)) {
-        wait_tile(v_a);
+      // (a try that cannot succeed is not made: it holds the warp for microseconds)
+      bool all = false;
+      if (now_a && next_a) {
+        const bool r0 = ready(v_a), r1 = ready(k_a), r2 = mbar_try_wait(&p_full[0], pa);
+        all = r0 && r1 && r2;
+      }
+      if (!all) {
+        if (now_a) wait_tile(v_a);
         if (next_a) wait_tile(k_a);
-        wait(&p_full[0], pa, 0x723u);
+        if (now_a) wait(&p_full[0], pa);
       }
       tc_fence_after();
-      weigh(0, v_a.st, ends && !last_tile_b ? r.tail : 8, j == 0, ends, !r.dual);
+      if (now_a) {
+        weigh(0, v_a.st, ends && !last_tile_b ? r.tail : 8, j == 0, ends, !r.dual);
+        ph_p ^= 1u;
+      }
       if (next_a) scores(0, k_a.st, nj == 0, nj + 1 == nx.n0, !nx.dual);
-      ph_p ^= 1u;
       if (now_b) v_b = r.dual ? v_a : take();
       if (next_b) k_b = nx.dual ? k_a : take();
-      if (now_b) {
+      all = false;
+      if (now_b && next_b) {
         const bool s0 = ready(v_b), s1 = ready(k_b), s2 = mbar_try_wait(&p_full[1], pb);
-        if (!(s0 && (s1 || !next_b) && s2)) {
-          wait_tile(v_b);
-          if (next_b) wait_tile(k_b);
-          wait(&p_full[1], pb, 0x725u);
-        }
-        tc_fence_after();
+        all = s0 && s1 && s2;
+      }
+      if (!all) {
+        if (now_b) wait_tile(v_b);
+        if (next_b) wait_tile(k_b);
+        if (now_b) wait(&p_full[1], pb);
+      }
+      tc_fence_after();
+      if (now_b) {
         weigh(1, v_b.st, ends ? r.tail : 8, j == 0, j + 1 == r.n1, true);
         ph_p ^= 2u;
-      } else if (next_b) {
-        wait_tile(k_b);
-        tc_fence_after();
       }
       if (next_b) scores(1, k_b.st, nj == 0, nj + 1 == nx.n1, true);
       j = nj;
@@ -688,6 +721,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         r = nx;
       }
     }
+    if (!ok) set_status(a.status, 0x721u);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ Q tiles, ends of the last V tiles
@@ -699,13 +733,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const Piece* p = ring + k % PR;
       const Piece* before = ring + (k + PR - 1) % PR;
       if (more) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x734u));
+        ok = __all_sync(0xffffffffu, wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1)));
         if (!ok) break;
         more = p->more != 0;
       }
       if (more) {
         for (int sl = 0; sl < 2 && p->steps(sl) > 0; ++sl) {
-          if (n_q[sl] > 0) ok = ok && mbar_wait(&q_empty[sl], (n_q[sl] - 1) & 1, a.status, 0x731u);
+          if (n_q[sl] > 0) ok = ok && wait_for(&q_empty[sl], (n_q[sl] - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++n_q[sl];
@@ -725,7 +759,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           // loads before that tile: every K and V before it, its own K, and the first K of the next piece
           // if it came before slot 1's V
           const int st = (2 * (tiles - 1) + 1 + (!before->dual && !(before->tiles() & 1) && more ? 1 : 0)) % ST;
-          ok = mbar_wait(&land[st], (n_land >> st) & 1u, a.status, 0x732u);
+          ok = wait_for(&land[st], (n_land >> st) & 1u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           n_land ^= 1u << st;
@@ -745,9 +779,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       had = more;
       if (more) tiles += p->tiles();
     }
+    if (!ok) set_status(a.status, 0x731u);
     if (!ok && lane == 0)                  // gave up: see the Q copies land before leaving
       for (int sl = 0; sl < 2; ++sl)
-        if (n_q[sl] > 0) mbar_wait(&q_full[sl], (n_q[sl] - 1) & 1, a.status, 0x733u);
+        if (n_q[sl] > 0) wait_for(&q_full[sl], (n_q[sl] - 1) & 1);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
@@ -759,9 +794,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const bool row_used = row_tok < a.tpt;
     const float scale = a.scale_log2;
     uint32_t n_s = 0, n_pair = 0, ph_o = 0;     // (ph_o: a phase bit per slot)
-    int flags = 0;
     bool ok = true;
-    int4 item = make_int4(0, 0, 0, 0);
     // A warp's rows of a piece, at its end: all dims of its slot's row tile (dual), or its slot's half of the dims
     // of the one row tile.  (Loops that run once in a while are kept short: unrolled, their instructions
     // came from L2 each time.)
@@ -771,7 +804,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       uint16_t* out;
       float *part_o;                       // of CTA 0, slot 0
       float2* part_ml;
-      unsigned* arrived;
+      unsigned *arrived, *taken;           // of a shared item (nullptr otherwise)
     };
     const int me = blockIdx.x;
     long long total = 0;
@@ -786,122 +819,168 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       r.part_o = a.part_o + prow * 4;
       r.part_ml = a.part_ml + sl * (2 * TM) + prow;
       r.c_first = me;
-      r.arrived = nullptr;
-      if (!a.join && (p.t0 > 0 || p.t1 < p.nt)) {
+      r.arrived = r.taken = nullptr;
+      if (p.t0 > 0 || p.t1 < p.nt) {
         while (cut_tile(share_start(a, total, r.c_first) - p.start, p.dual, p.keys(), p.nt) > 0) --r.c_first;
-        r.arrived = a.counters + 8 * r.c_first + warp;
+        r.arrived = a.counters + 16 * r.c_first + warp;
+        r.taken = r.arrived + 8;
       }
       return r;
     };
     auto part_at = [&](const Rows& r, int c) { return (size_t)c * 2 + (c == r.c_first ? 1 : 0); };
-    auto store = [&](const Rows& r, int c, const float* v, float f) {      // 64 dims from c
-      uint32_t w[32];
+    auto store = [&](const Rows& r, int c, const float* v, float f) {      // 32 dims from c
+      uint32_t w[16];
 #pragma unroll
-      for (int d = 0; d < 32; ++d) w[d] = cvt_bf16x2(v[2 * d] * f, v[2 * d + 1] * f);
+      for (int d = 0; d < 16; ++d) w[d] = cvt_bf16x2(v[2 * d] * f, v[2 * d + 1] * f);
       if (!r.used) return;
       if (a.wide) {
-#pragma unroll
-        for (int d = 0; d < 32; d += 8) st_global_32(r.out + c + 2 * d, w + d);
+        st_global_32(r.out + c, w);
+        st_global_32(r.out + c + 16, w + 8);
       } else {
 #pragma unroll
-        for (int d = 0; d < 32; d += 4)
+        for (int d = 0; d < 16; d += 4)
           *reinterpret_cast<uint4*>(r.out + c + 2 * d) = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
       }
     };
-    // 64 unnormalised dims from c of this CTA's piece, from TMEM: O of the slot, or both slots' joined
+    // 32 unnormalised dims from c of this CTA's piece, from TMEM: O of the slot, or both slots' joined
     float fa = 1.f, fb = 0.f;
     bool have_b = false;
-    auto own64 = [&](const Piece& p, int c, float* v) {
-      tmem_ld_cols<64>(2 * KT + (p.dual ? (uint32_t)sl * D : 0u) + lanes + c, v);
+    auto own32 = [&](const Piece& p, int c, float* v) {
+      tmem_ld_cols<32>(2 * KT + (p.dual ? (uint32_t)sl * D : 0u) + lanes + c, v);
       if (!p.dual) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) v[k] *= fa;
+        for (int k = 0; k < 32; ++k) v[k] *= fa;
         if (have_b) {
-          float w[64];
-          tmem_ld_cols<64>(3 * KT + lanes + c, w);
+          float w[32];
+          tmem_ld_cols<32>(3 * KT + lanes + c, w);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) v[k] += w[k] * fb;
+          for (int k = 0; k < 32; ++k) v[k] += w[k] * fb;
         }
       }
     };
-    // Joins the rows of all pieces of an item, in CTA order whoever does it; `here`: this CTA's own is not in the
-    // workspace but in TMEM, with maximum m and sum l.
-    auto join = [&](const Piece& p, const Rows& r, bool here, float m, float l) {
-      auto each = [&](auto&& f) {
-        for (int base = r.c_first, t = 0; t < p.nt; base += 32) {           // 32 CTAs' cuts at a time
-          const int to = cut_tile(share_start(a, total, base + lane + 1) - p.start, p.dual, p.keys(), p.nt);
-          const int before = __shfl_up_sync(0xffffffffu, to, 1);
-          unsigned has = __ballot_sync(0xffffffffu, to > (lane == 0 ? t : before));        // (without work: no piece)
-          t = __shfl_sync(0xffffffffu, to, 31);
-          for (; has; has &= has - 1) f(base + __ffs(has) - 1);
+    // The CTAs that have a piece of an item: those of the first 32 from c_first on, and whether there are more.
+    struct Sharers {
+      unsigned has;
+      int t;                               // tiles up to the last of the 32
+    };
+    auto sharers = [&](const Piece& p, int base, int t) {
+      const int to = cut_tile(share_start(a, total, base + lane + 1) - p.start, p.dual, p.keys(), p.nt);
+      const int before = __shfl_up_sync(0xffffffffu, to, 1);
+      Sharers s;
+      s.has = __ballot_sync(0xffffffffu, to > (lane == 0 ? t : before));   // (a CTA without work has no piece)
+      s.t = __shfl_sync(0xffffffffu, to, 31);
+      return s;
+    };
+    constexpr int BATCH = 2;
+    // f(c) for batches of BATCH sharers in CTA order (-1: none)
+    auto batches = [&](const Piece& p, const Rows& r, const Sharers& first, auto&& f) {
+      Sharers s = first;
+      for (int base = r.c_first;; base += 32) {
+        while (s.has) {
+          int c[BATCH];
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            c[k] = s.has ? base + __ffs(s.has) - 1 : -1;
+            s.has &= s.has - 1;
+          }
+          f(c);
         }
-      };
+        if (s.t >= p.nt) break;
+        s = sharers(p, base + 32, s.t);
+      }
+    };
+    const Piece* shared_last = nullptr;    // the CTA's last piece, where its item goes on in the next CTA
+    bool shared_first = false;             // the first piece's item came from the CTA before
+    bool direct = false;                   // the last piece is joined from TMEM, with this maximum and sum
+    float m_last = 0.f, l_last = 0.f;
+    // Joins groups of 32 dims of the pieces' rows, in CTA order whoever does it, as long as some are left to take (`here`:
+    // all, with this CTA's piece from TMEM).  Returns the number of sharers.
+    auto join = [&](const Piece& p, const Rows& r, const Sharers& first, bool here) {
+      const int groups = (r.c_hi - r.c_lo) >> 5;
       float top = -INFINITY, sum = 0.f;
-      each([&](int c) {
-        float2 ml = make_float2(m, l);
-        if (!(here && c == me)) ml = r.used ? __ldcg(r.part_ml + part_at(r, c) * (4 * TM)) : make_float2(0.f, 1.f);
-        const float t = fmaxf(top, ml.x), base = t == -INFINITY ? 0.f : t;
-        sum = sum * ex2(top - base) + ml.y * ex2(ml.x - base);
-        top = t;
-      });
-      const float inv = 1.f / sum;
+      int n = 0;
 #pragma unroll 1
-      for (int c64 = r.c_lo; c64 < r.c_hi; c64 += 64) {
-        float acc[64];
+      for (int g = -1; g < groups;) {      // (-1: the maximum and the sum)
+        const int c32 = r.c_lo + 32 * max(g, 0);
+        float acc[32];
 #pragma unroll
-        for (int k = 0; k < 64; ++k) acc[k] = 0.f;
-        each([&](int c) {
-          if (here && c == me) {
-            float v[64];
-            own64(p, c64, v);
-            const float f = ex2(m - top);
+        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+        batches(p, r, first, [&](const int (&c)[BATCH]) {
+          float4 u[BATCH][8];
+          float2 ml[BATCH];
 #pragma unroll
-            for (int k = 0; k < 64; ++k) acc[k] += v[k] * f;
-          } else if (r.used) {
-            const float* src = r.part_o + part_at(r, c) * (2 * TM * D) + (size_t)(c64 >> 2) * (2 * TM * 4);
-            const float m_c = __ldcg(r.part_ml + part_at(r, c) * (4 * TM)).x;
-            float4 u[16];
+          for (int k = 0; k < BATCH; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)k * (2 * TM * 4)));
-            const float f = ex2(m_c - top);
+            for (int d = 0; d < 8; ++d) u[k][d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (here && c[k] == me) {
+              ml[k] = make_float2(m_last, l_last);
+            } else if (c[k] >= 0 && r.used) {
+              ml[k] = __ldcg(r.part_ml + part_at(r, c[k]) * (4 * TM));
+              const float* src = r.part_o + part_at(r, c[k]) * (2 * TM * D) + (size_t)(c32 >> 2) * (2 * TM * 4);
+              if (g >= 0)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              acc[4 * k] += u[k].x * f;
-              acc[4 * k + 1] += u[k].y * f;
-              acc[4 * k + 2] += u[k].z * f;
-              acc[4 * k + 3] += u[k].w * f;
+                for (int d = 0; d < 8; ++d) u[k][d] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)d * (2 * TM * 4)));
             }
           }
           __syncwarp();
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            if (g < 0) {
+              const float t = fmaxf(top, ml[k].x), base = t == -INFINITY ? 0.f : t;
+              sum = sum * ex2(top - base) + ml[k].y * ex2(ml[k].x - base);
+              top = t;
+              n += c[k] >= 0;
+            } else {
+              if (here && c[k] == me) {
+                float v[32];
+                own32(p, c32, v);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) u[k][d] = make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+              }
+              const float w = ex2(ml[k].x - top);
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                acc[4 * d] += u[k][d].x * w;
+                acc[4 * d + 1] += u[k][d].y * w;
+                acc[4 * d + 2] += u[k][d].z * w;
+                acc[4 * d + 3] += u[k][d].w * w;
+              }
+            }
+          }
         });
-        store(r, c64, acc, inv);
+        if (g >= 0) store(r, c32, acc, 1.f / sum);
         __syncwarp();
+        if (here) {
+          ++g;
+        } else {
+          unsigned t = 0;
+          if (lane == 0) t = atomicAdd(r.taken, 1u) & 0xffffu;
+          g = (int)__shfl_sync(0xffffffffu, t, 0);
+        }
       }
-      if (lane == 0) *r.arrived = 0u;      // (nobody else comes here in this launch)
+      return n;
     };
-    unsigned later = 0;                    // lane 0: what had arrived with the first piece
-    bool deferred = false;
     auto finish = [&](const Piece& p, float m, float l) {
-      const bool whole = p.t0 == 0 && p.t1 == p.nt;
       const Rows r = rows_of(p);
       // a piece of a shared item: how much of it has arrived by now (looked at while O is waited for)
       unsigned seen = 0;
       if (r.arrived && lane == 0) seen = ld_acquire(r.arrived);
       fa = 1.f;
       if (p.dual) {
-        ok = ok && mbar_wait(&o_full[sl], (ph_o >> sl) & 1u, a.status, 0x742u);
+        ok = ok && wait_for(&o_full[sl], (ph_o >> sl) & 1u);
         ph_o ^= 3u;
       } else {
         // the slots' sums joined
         have_b = p.tiles() > 1;            // (a piece of one tile leaves slot 1 out)
-        ok = ok && mbar_wait(&o_full[0], ph_o & 1u, a.status, 0x743u);
-        if (have_b) ok = ok && mbar_wait(&o_full[1], (ph_o >> 1) & 1u, a.status, 0x748u);
+        ok = ok && wait_for(&o_full[0], ph_o & 1u);
+        if (have_b) ok = ok && wait_for(&o_full[1], (ph_o >> 1) & 1u);
         ph_o ^= have_b ? 3u : 1u;
         s_ml[sl * TM + row] = make_float2(m, l);
         __syncwarp();
         uint64_t* both = pair + 2 * (warp & 3);
         if (lane == 0) mbar_arrive(both);
-        ok = ok && mbar_wait(both, n_pair & 1, a.status, 0x745u);
+        ok = ok && wait_for(both, n_pair & 1);
         const float2 first = s_ml[row], second = s_ml[TM + row];
         m = fmaxf(first.x, second.x);
         const float base = m == -INFINITY ? 0.f : m;
@@ -911,50 +990,47 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
       __syncwarp();
       tc_fence_after();
-      if (whole) {
+      if (!r.arrived) {
         const float inv = 1.f / l;
 #pragma unroll 1
-        for (int c = r.c_lo; c < r.c_hi; c += 64) {
-          float v[64];
-          own64(p, c, v);
+        for (int c = r.c_lo; c < r.c_hi; c += 32) {
+          float v[32];
+          own32(p, c, v);
           store(r, c, v, inv);
           __syncwarp();
         }
       } else {
-        // The warp whose rows arrive last joins the item's pieces.  If the others are all there, this one need not
-        // go through memory.  The CTA that opened an item comes to its end last as a rule, so the others
-        // (their first piece) look at the answer only when they are done with everything.
-        if (p.t0 > 0) flags |= F_JOINS | (p.t1 == p.nt ? F_ENDS : 0);
-        else {
-          flags |= F_OPENS;
-          item = make_int4(0, p.row0, p.tok, p.h);
-        }
-        const unsigned tiles = p.tiles(), nt = p.nt;
-        if (!a.join && __shfl_sync(0xffffffffu, seen, 0) + tiles == nt) {
-          join(p, r, true, m, l);
-        } else {
-          const size_t at = (size_t)me * 2 + (p.t0 > 0 ? 0 : 1);
+        if (p.t0 > 0) shared_first = true;
+        else shared_last = &p;             // (its entry of the ring is not posted again)
+        // If all other pieces are there when the CTA that opened the item comes to its end, as a rule where two share
+        // it, its piece need not go through memory.
+        const Sharers all = sharers(p, r.c_first, 0);
+        direct = p.t0 == 0 && all.t >= p.nt && __popc(all.has) == 2 &&
+                 __shfl_sync(0xffffffffu, seen, 0) + (unsigned)p.tiles() == (unsigned)p.nt;
+        m_last = m;
+        l_last = l;
+        if (!direct) {
+          const size_t at = part_at(r, me);
 #pragma unroll 1
-          for (int c = r.c_lo; c < r.c_hi; c += 64) {
-            float v[64];
-            own64(p, c, v);
+          for (int c = r.c_lo; c < r.c_hi; c += 32) {
+            float v[32];
+            own32(p, c, v);
             float* dst = r.part_o + at * (2 * TM * D) + (size_t)(c >> 2) * (2 * TM * 4);
             if (r.used) {
 #pragma unroll
-              for (int d = 0; d < 64; d += 4)
+              for (int d = 0; d < 32; d += 4)
                 __stcg(reinterpret_cast<float4*>(dst + (size_t)(d >> 2) * (2 * TM * 4)),
                        make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]));
             }
             __syncwarp();
           }
           if (r.used) __stcg(r.part_ml + at * (4 * TM), make_float2(m, l));
-          if (!a.join) {
-            __syncwarp();
-            if (lane == 0) later = add_acq_rel(r.arrived, tiles) + tiles;
-            __syncwarp();
-            if (p.t0 > 0) deferred = true;
-            else if (__shfl_sync(0xffffffffu, later, 0) == nt) join(p, r, false, 0.f, 0.f);
-          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          // (direct: nothing is left for the other sharer)
+          if (direct) atomicAdd(r.taken, (unsigned)(r.c_hi - r.c_lo) >> 5);
+          red_release(r.arrived, (unsigned)p.tiles());
         }
       }
       tc_fence_before();
@@ -962,13 +1038,41 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         __syncwarp();
         uint64_t* both = pair + 2 * (warp & 3) + 1;
         if (lane == 0) mbar_arrive(both);  // O and s_ml free again
-        ok = ok && mbar_wait(both, n_pair & 1, a.status, 0x746u);
+        ok = ok && wait_for(both, n_pair & 1);
         ++n_pair;
       }
     };
+    // At the CTA's end: the rows of a shared item are joined by the warps of all its CTAs that are still here when
+    // the last piece arrives, a group of dims at a time.  A warp waits for that a while only: the warp that
+    // brings the last piece joins whatever is left, so no CTA needs another one to run beside it.
+    auto share = [&](const Piece& p, bool here) {
+      const Rows r = rows_of(p);
+      const Sharers all = sharers(p, r.c_first, 0);
+      unsigned there = 0;
+      if (lane == 0 && !here) {
+        const uint64_t t0 = globaltimer();
+        do {
+          there = ld_acquire(r.arrived) == (unsigned)p.nt;
+        } while (!there && globaltimer() - t0 < JOIN_WAIT_NS);
+      }
+      int n = __popc(all.has);
+      if (here || __shfl_sync(0xffffffffu, there, 0)) {
+        __syncwarp();
+        n = join(p, r, all, here);
+      } else {
+        Sharers s = all;
+        for (int base = r.c_first; s.t < p.nt; n += __popc(s.has)) s = sharers(p, base += 32, s.t);
+      }
+      // done with it; the last of the sharers clears their two words for the next launch
+      if (lane == 0 && (int)(atomicAdd(r.taken, 0x10000u) >> 16) + 1 == n) {
+        *r.taken = 0u;
+        *r.arrived = 0u;
+      }
+      __syncwarp();
+    };
     // (after a wait that ran out a warp stops waiting and leaves at its next piece)
     for (int k = 0; ok; ++k) {
-      ok = mbar_wait(&posted[k % PR], (uint32_t)((k / PR) & 1), a.status, 0x744u);
+      ok = wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const Piece& p = ring[k % PR];
@@ -983,7 +1087,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       float ref = 0.f, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
         const int key0 = (t0 + (dual ? j : 2 * j + sl)) * KT;
-        ok = ok && mbar_wait(&s_full[sl], n_s & 1, a.status, 0x741u);
+        ok = ok && wait_for(&s_full[sl], n_s & 1);
         ++n_s;
         tc_fence_after();
         // hidden scores become -inf in place: the columns that some row of the warp does not see, 16 at a time
@@ -1062,119 +1166,17 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(&taken[k % PR]);
     }
-    if (deferred && __all_sync(0xffffffffu, ok)) {
-      const Piece& p = *s_first;
-      if (__shfl_sync(0xffffffffu, later, 0) == (unsigned)p.nt) join(p, rows_of(p), false, 0.f, 0.f);
-    }
-    if (tid == 0 && a.join) a.part_item[blockIdx.x] = make_int4(flags, item.y, item.z, item.w);
+    if (!ok) set_status(a.status, 0x741u);
+    ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k)
+      if (ok && (k ? shared_first : shared_last != nullptr)) share(k ? *s_first : *shared_last, !k && direct);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
-  }
-}
-
-// Joins the pieces of every item that a cut fell into, 8 rows of an item at a time.  Every block reads all CTAs' flags
-// (one round trip) and takes its share of the (rows, item) tasks; of a task's pieces each of 8 warps sums every 8th,
-// all its loads in flight together, and the warps' sums are added in warp order.
-constexpr int JOIN_ROWS = 8;
-__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkAttnArgs a, int grid) {
-  __shared__ float4 s_o[8][32][JOIN_ROWS + 1];
-  __shared__ float2 s_ml[8][JOIN_ROWS];
-  __shared__ uint8_t s_flag[MAX_GRID];
-  __shared__ uint16_t s_open[MAX_GRID];   // the CTAs that opened an item, in order (every block's list is the same)
-  __shared__ int s_n;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
-  for (int c = tid; c < grid; c += 256) s_flag[c] = (uint8_t)a.part_item[c].x;
-  __syncthreads();
-  if (warp == 0) {
-    int at = 0;
-    for (int base = 0; base < grid; base += 32) {
-      const bool opens = base + lane < grid && (s_flag[base + lane] & F_OPENS);
-      const unsigned m = __ballot_sync(0xffffffffu, opens);
-      if (opens) s_open[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(base + lane);
-      at += __popc(m);
-    }
-    if (lane == 0) s_n = at;
-  }
-  __syncthreads();
-  const int n = s_n;
-  for (int task = blockIdx.x; task < n * (2 * TM / JOIN_ROWS); task += gridDim.x) {
-    const int y = task / n, c0 = s_open[task - y * n];
-    const int4 it = a.part_item[c0];       // flags, first row, tokens, kv head
-    auto token = [&](int rr) { return (rr >> 7) * a.tpt + (rr & 127) / a.G; };
-    auto used = [&](int rr) { return (rr & 127) / a.G < a.tpt && token(rr) < it.z; };
-    if (token(y * JOIN_ROWS) >= it.z) continue;                    // (rows behind the item's tokens)
-    {
-      const int rr = y * JOIN_ROWS + (lane & 7), d4 = lane >> 3;
-      const bool mine = used(rr);
-      float m = -INFINITY, l = 0.f;
-      float4 o[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      int count = 0;
-      for (int base = c0, ends = 0; !ends && base < grid; base += 32) {
-        const int c = base + lane, f = c < grid && c > c0 ? s_flag[c] : 0;
-        unsigned has = __ballot_sync(0xffffffffu, c == c0 || (f & F_JOINS));
-        ends = (int)__ballot_sync(0xffffffffu, (f & F_ENDS) != 0);
-        if (ends) has &= 2u * (unsigned)(ends & -ends) - 1u;
-        for (; has; has &= has - 1)
-          if ((count++ & 7) == warp && mine) {
-            const int from = base + __ffs(has) - 1;
-            const size_t at = (size_t)from * 2 + (from == c0 ? 1 : 0);
-            // (with one row tile each half of the dims has its own copy of the maximum and sum: the same)
-            const float2 ml = __ldcg(&a.part_ml[(at * 2 + (it.z > a.tpt ? rr >> 7 : 0)) * (2 * TM) + rr]);
-            const float4* src = reinterpret_cast<const float4*>(a.part_o + at * (2 * TM * D)) + rr;
-            float4 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (size_t)(d4 + 4 * k) * (2 * TM));
-            const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
-            const float fo = ex2(m - ref), fc = ex2(ml.x - ref);
-            m = top;
-            l = l * fo + ml.y * fc;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              o[k].x = o[k].x * fo + v[k].x * fc;
-              o[k].y = o[k].y * fo + v[k].y * fc;
-              o[k].z = o[k].z * fo + v[k].z * fc;
-              o[k].w = o[k].w * fo + v[k].w * fc;
-            }
-          }
-        __syncwarp();
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s_o[warp][d4 + 4 * k][lane & 7] = o[k];
-      if (lane < JOIN_ROWS) s_ml[warp][lane] = make_float2(m, l);
-    }
-    __syncthreads();
-    {
-      const int r = y * JOIN_ROWS + warp;  // a row per warp, four dims per lane
-      if (used(r)) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, s_ml[k][warp].x);
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float f = ex2(s_ml[k][warp].x - m);
-          const float4 v = s_o[k][lane][warp];
-          l += s_ml[k][warp].y * f;
-          o.x += v.x * f;
-          o.y += v.y * f;
-          o.z += v.z * f;
-          o.w += v.w * f;
-        }
-        const float inv = 1.f / l;
-        *reinterpret_cast<uint2*>(a.O + (size_t)(it.y + token(r)) * a.ldo + (size_t)(it.w * a.G + (r & 127) % a.G) * D +
-                                  lane * 4) = make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
-      }
-    }
-    __syncthreads();
   }
 }
 
@@ -1196,8 +1198,6 @@ cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk,
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   cudaError_t e = launch_k(chunk_attention_kernel, dim3(grid), dim3(THREADS), SMEM, s, tq, tk, tv, a);
-  if (e != cudaSuccess) return e;
-  if (a.join) e = launch_k(chunk_join_kernel, dim3(2 * grid), dim3(256), 0, s, a, grid);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

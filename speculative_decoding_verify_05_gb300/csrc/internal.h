@@ -224,10 +224,9 @@ struct ChunkAttnArgs {
   float* part_o;                        // [grid][2][32][256][4] unnormalised outputs, [dim / 4][row][dim % 4]
   float2* part_ml;                      // [grid][2][2][256] running maximum (times scale_log2) and sum, as left by
                                         // the warps of slot 0 and of slot 1
-  int join;                             // 1: a second kernel joins the pieces, 0: the last CTA of each item does
-  int4* part_item;                      // [grid] flags; first row, tokens and kv head of the item it opened
-  unsigned* counters;                   // [grid][8] key tiles of an item's pieces that have arrived, at the CTA that
-                                        // opened it, per warp (its rows, or its rows and half of the dims)
+  unsigned* counters;                   // [grid][2][8] per CTA that opened a shared item and warp (its rows, or its rows
+                                        // and half of the dims): key tiles arrived; dim groups taken to be joined, and
+                                        // in the upper half sharers that are done
   unsigned* status;
 };
 constexpr int CHUNK_MAX_GRID = 1024;
