@@ -821,7 +821,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       r.c_first = me;
       r.arrived = r.taken = nullptr;
       if (p.t0 > 0 || p.t1 < p.nt) {
-        while (cut_tile(share_start(a, total, r.c_first) - p.start, p.dual, p.keys(), p.nt) > 0) --r.c_first;
+        // the last CTA up to this one whose share does not start inside the item, 32 at a time
+        for (unsigned out = 0; out == 0; r.c_first -= out ? __ffs(out) - 1 : 32)
+          out = __ballot_sync(0xffffffffu, cut_tile(share_start(a, total, max(r.c_first - lane, 0)) - p.start, p.dual,
+                                                    p.keys(), p.nt) == 0);
         r.arrived = a.counters + 16 * r.c_first + warp;
         r.taken = r.arrived + 8;
       }
@@ -894,72 +897,74 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     bool direct = false;                   // the last piece is joined from TMEM, with this maximum and sum
     float m_last = 0.f, l_last = 0.f;
     // Joins groups of 32 dims of the pieces' rows, in CTA order whoever does it, as long as some are left to take (`here`:
-    // all, with this CTA's piece from TMEM).  Returns the number of sharers.
+    // all, with this CTA's piece from TMEM).  One pass over the pieces per group, their maxima and sums with
+    // it (they mostly agree in the reference, so nothing is rescaled as a rule).
     auto join = [&](const Piece& p, const Rows& r, const Sharers& first, bool here) {
       const int groups = (r.c_hi - r.c_lo) >> 5;
-      float top = -INFINITY, sum = 0.f;
-      int n = 0;
-#pragma unroll 1
-      for (int g = -1; g < groups;) {      // (-1: the maximum and the sum)
-        const int c32 = r.c_lo + 32 * max(g, 0);
+      for (int g = 0;; ++g) {
+        if (!here) {
+          unsigned t = 0;
+          if (lane == 0) t = atomicAdd(r.taken, 1u) & 0xffffu;
+          g = (int)__shfl_sync(0xffffffffu, t, 0);
+        }
+        if (g >= groups) break;
+        const int c32 = r.c_lo + 32 * g;
+        float top = -INFINITY, sum = 0.f;
         float acc[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) acc[k] = 0.f;
         batches(p, r, first, [&](const int (&c)[BATCH]) {
           float4 u[BATCH][8];
           float2 ml[BATCH];
+          float high = top;
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
             ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int d = 0; d < 8; ++d) u[k][d] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (here && c[k] == me) {
-              ml[k] = make_float2(m_last, l_last);
-            } else if (c[k] >= 0 && r.used) {
+            if (c[k] >= 0 && r.used && !(here && c[k] == me)) {
               ml[k] = __ldcg(r.part_ml + part_at(r, c[k]) * (4 * TM));
               const float* src = r.part_o + part_at(r, c[k]) * (2 * TM * D) + (size_t)(c32 >> 2) * (2 * TM * 4);
-              if (g >= 0)
 #pragma unroll
-                for (int d = 0; d < 8; ++d) u[k][d] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)d * (2 * TM * 4)));
+              for (int d = 0; d < 8; ++d) u[k][d] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)d * (2 * TM * 4)));
             }
           }
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
-            if (g < 0) {
-              const float t = fmaxf(top, ml[k].x), base = t == -INFINITY ? 0.f : t;
-              sum = sum * ex2(top - base) + ml[k].y * ex2(ml[k].x - base);
-              top = t;
-              n += c[k] >= 0;
-            } else {
-              if (here && c[k] == me) {
-                float v[32];
-                own32(p, c32, v);
+            if (here && c[k] == me) {
+              float v[32];
+              own32(p, c32, v);
+              ml[k] = make_float2(m_last, l_last);
 #pragma unroll
-                for (int d = 0; d < 8; ++d) u[k][d] = make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
-              }
-              const float w = ex2(ml[k].x - top);
+              for (int d = 0; d < 8; ++d) u[k][d] = make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+            }
+            high = fmaxf(high, ml[k].x);
+          }
+          const float ref = high == -INFINITY ? 0.f : high;
+          if (__any_sync(0xffffffffu, top != high)) {
+            const float keep = ex2(top - ref);
+            sum *= keep;
 #pragma unroll
-              for (int d = 0; d < 8; ++d) {
-                acc[4 * d] += u[k][d].x * w;
-                acc[4 * d + 1] += u[k][d].y * w;
-                acc[4 * d + 2] += u[k][d].z * w;
-                acc[4 * d + 3] += u[k][d].w * w;
-              }
+            for (int d = 0; d < 32; ++d) acc[d] *= keep;
+            top = high;
+          }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const float w = ex2(ml[k].x - ref);
+            sum += ml[k].y * w;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              acc[4 * d] += u[k][d].x * w;
+              acc[4 * d + 1] += u[k][d].y * w;
+              acc[4 * d + 2] += u[k][d].z * w;
+              acc[4 * d + 3] += u[k][d].w * w;
             }
           }
         });
-        if (g >= 0) store(r, c32, acc, 1.f / sum);
+        store(r, c32, acc, 1.f / sum);
         __syncwarp();
-        if (here) {
-          ++g;
-        } else {
-          unsigned t = 0;
-          if (lane == 0) t = atomicAdd(r.taken, 1u) & 0xffffu;
-          g = (int)__shfl_sync(0xffffffffu, t, 0);
-        }
       }
-      return n;
     };
     auto finish = [&](const Piece& p, float m, float l) {
       const Rows r = rows_of(p);
@@ -1056,12 +1061,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         } while (!there && globaltimer() - t0 < JOIN_WAIT_NS);
       }
       int n = __popc(all.has);
+      Sharers s = all;
+      for (int base = r.c_first; s.t < p.nt; n += __popc(s.has)) s = sharers(p, base += 32, s.t);
       if (here || __shfl_sync(0xffffffffu, there, 0)) {
         __syncwarp();
-        n = join(p, r, all, here);
-      } else {
-        Sharers s = all;
-        for (int base = r.c_first; s.t < p.nt; n += __popc(s.has)) s = sharers(p, base += 32, s.t);
+        join(p, r, all, here);
       }
       // done with it; the last of the sharers clears their two words for the next launch
       if (lane == 0 && (int)(atomicAdd(r.taken, 0x10000u) >> 16) + 1 == n) {
