@@ -14,6 +14,10 @@ and LM head.  By default the SwiGLU activation runs in the gate/up GEMM's
 epilogue (spec_verify_linear_swiglu), which wants the gate and up weight rows
 interleaved in blocks of 16: the engine relays each layer's ``w_gu`` out once,
 in place, when it is built.
+
+Over a paged cache the engine also runs the prompts that a verify pass starts from, in chunks of any
+length (``prefill``): per layer the QKV projection, spec_kv_append_paged (which rotates q and k on
+the way to the pages), spec_chunk_attention_paged, and the rest as above.
 """
 from __future__ import annotations
 
@@ -35,6 +39,8 @@ class Dims:
     layers: int = 36
     eps: float = 1e-6
     theta: float = 1e6
+    rope_sections: tuple = ()         # frequencies of each position axis (sum D/2); (): one axis
+    rope_interleaved: bool = False    # the axes take the frequencies in turn instead of one after the other
 
     @property
     def qkv(self) -> int:
@@ -130,9 +136,12 @@ class VerifyEngine:
 
     def __init__(self, dims: Dims, weights: StackW, kcaches, vcaches, max_M: int, max_rows: int,
                  device=None, fused_swiglu: bool = True, fused_sampler: bool = True, fused_rope: bool = True,
-                 fold_norms: bool = True):
+                 fold_norms: bool = True, block_table=None):
+        """kcaches, vcaches: per layer [B, Hkv, cap, D], or with block_table [B, max_pages] int32 the pools
+        [Hkv, num_pages, 128, D] of a paged cache (every layer's pages under the same ids)."""
         self.dims = dims
         self.w = weights
+        self.block_table = block_table
         # verify_round: LM head and sampler in one call that never materialises p
         self.fused_sampler = fused_sampler
         # RoPE applied by the QKV projection from a per-pass (cos, sin) table (head size 128 only)
@@ -163,7 +172,9 @@ class VerifyEngine:
         self.ssq = torch.empty((max_M, (dims.d + 127) // 128), dtype=torch.float32, device=dev)
         self.norm_in = S.row_norm(in_ssq=self.ssq, eps=dims.eps) if fold_norms else None
         self.norm_out = S.row_norm(out_ssq=self.ssq) if fold_norms else None
-        self.P = torch.empty((max_M, dims.V), dtype=torch.float32, device=dev) if weights.w_lm is not None else None
+        # rows that reach the LM head: of a verify pass (a prompt's chunk is longer)
+        head_M = max_M if block_table is None else min(max_M, block_table.shape[0] * max_rows)
+        self.P = torch.empty((head_M, dims.V), dtype=torch.float32, device=dev) if weights.w_lm is not None else None
         B, cap = (kcaches[0].shape[0], kcaches[0].shape[2]) if kcaches else (1, 1)
         need = 0
         for M in range(1, max_M + 1):
@@ -176,17 +187,21 @@ class VerifyEngine:
                 need = max(need, S.spec_linear_norm_workspace_bytes(M, dims.qkv, dims.d),
                            S.spec_linear_norm_workspace_bytes(M, 2 * dims.I, dims.d),
                            S.spec_linear_norm_workspace_bytes(M, dims.I, dims.d, swiglu=True))
-        if kcaches:
+        if kcaches and block_table is not None:
+            B, mp = block_table.shape
+            need = max(need, S.spec_attention_paged_workspace_bytes(B, max_rows, dims.Hq, dims.Hkv, dims.D, mp),
+                       S.spec_chunk_attention_workspace_bytes(B, max_M, dims.Hq, dims.Hkv, dims.D, mp))
+        elif kcaches:
             need = max(need, S.spec_attention_workspace_bytes(B, max_rows, dims.Hq, dims.Hkv, dims.D, cap))
         if weights.w_lm is not None:
-            need = max(need, S.spec_lmhead_workspace_bytes(max_M, dims.d, dims.V))
+            need = max(need, S.spec_lmhead_workspace_bytes(head_M, dims.d, dims.V))
             if fused_sampler:
-                need = max(need, S.spec_lmhead_sample_workspace_bytes(max_M, dims.d, dims.V, 1.0))
+                need = max(need, S.spec_lmhead_sample_workspace_bytes(head_M, dims.d, dims.V, 1.0))
         self.ws = S.Workspace(dev, need)
         self._graphs = []          # captured rounds (kept alive with the engine)
 
     # ------------------------------------------------------------------ one layer
-    def layer(self, li: int, M: int, cu_rows, ctx_len, B: int, max_rows: int):
+    def layer(self, li: int, M: int, cu_rows, ctx_len, B: int, max_rows: int, prompt: bool = False):
         dm, lw = self.dims, self.w.layers[li]
         x, h, qkv, o, a = (self.x[:M], self.h[:M], self.qkv[:M], self.o[:M], self.a[:M])
         hq = dm.Hq * dm.D
@@ -197,15 +212,25 @@ class VerifyEngine:
         if not self.fold_norms:
             S.spec_rmsnorm(x, lw.attn_norm, dm.eps, Y=h)
         hin = x if self.fold_norms else h
-        if self.fused_rope:
+        if self.fused_rope and not prompt:
             S.spec_verify_linear_rope(hin, lw.w_qkv, self.cs[:M], dm.Hq + dm.Hkv, Y=qkv, ws=self.ws, norm=nin)
         else:
             S.spec_verify_linear(hin, lw.w_qkv, Y=qkv, ws=self.ws, norm=nin)
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
-        if not self.fused_rope:
-            S.spec_rope(q, k, cu_rows, ctx_len, dm.D, dm.theta)
-        S.spec_verify_attention(q, k, v, cu_rows, ctx_len, self.kc[li], self.vc[li], max_rows, O=o,
-                                ws=self.ws)
+        if prompt:
+            S.spec_kv_append_paged(k, v, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table,
+                                   cs=self.cs[:M], Q=q)
+            S.spec_chunk_attention_paged(q, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table, O=o,
+                                         ws=self.ws)
+        else:
+            if not self.fused_rope:
+                S.spec_rope(q, k, cu_rows, ctx_len, dm.D, dm.theta)
+            if self.block_table is not None:
+                S.spec_verify_attention_paged(q, k, v, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table,
+                                              max_rows, O=o, ws=self.ws)
+            else:
+                S.spec_verify_attention(q, k, v, cu_rows, ctx_len, self.kc[li], self.vc[li], max_rows, O=o,
+                                        ws=self.ws)
         S.spec_verify_linear(o, lw.w_o, Y=x, residual=x, ws=self.ws, norm=nout)
         if not self.fold_norms:
             S.spec_rmsnorm(x, lw.mlp_norm, dm.eps, Y=h)
@@ -216,9 +241,11 @@ class VerifyEngine:
             S.spec_silu_mul(self.gu[:M], A=a)
         S.spec_verify_linear(a, lw.w_down, Y=x, residual=x, ws=self.ws, norm=nout)
 
-    def _stack(self, x0, cu_rows, ctx_len, max_rows, n_layers, final_norm: bool = True):
+    def _stack(self, x0, cu_rows, ctx_len, max_rows, n_layers, final_norm: bool = True, prompt: bool = False,
+               positions=None):
         """All layers and (with final_norm) the final RMSNorm over the packed rows into self.h.  With
-        folded norms and final_norm False, the LM head reads self.x with the sums of squares."""
+        folded norms and final_norm False, the LM head reads self.x with the sums of squares.  positions
+        [axes, M] int32: the rows' positions on dims.rope_sections' axes (default: the tokens' own)."""
         M = x0.shape[0]
         B = cu_rows.numel() - 1
         max_rows = self.max_rows if max_rows is None else max_rows
@@ -227,31 +254,55 @@ class VerifyEngine:
         if x0.data_ptr() != self.x.data_ptr():
             self.x[:M].copy_(x0)
         L = len(self.w.layers) if n_layers is None else n_layers
-        if self.fused_rope and L > 0:
+        if positions is not None:
+            if not (self.fused_rope or prompt):
+                raise ValueError("positions need the rotation table (fused_rope)")
+            sections = self.dims.rope_sections or (self.dims.D // 2,)
+            S.spec_rope_table_axes(positions, sections, self.dims.D, self.dims.theta, self.dims.rope_interleaved,
+                                   cs=self.cs[:M])
+        elif (self.fused_rope or prompt) and L > 0:
             S.spec_rope_table(cu_rows, ctx_len, M, self.dims.D, self.dims.theta, cs=self.cs[:M])
         if self.fold_norms and L > 0:
             S.spec_row_ssq(self.x[:M], out=self.ssq[:M])     # the first layer's input has no producer
         for li in range(L):
-            self.layer(li, M, cu_rows, ctx_len, B, max_rows)
+            self.layer(li, M, cu_rows, ctx_len, B, max_rows, prompt)
         if self.w.w_lm is not None and (final_norm or not self.fold_norms):
             S.spec_rmsnorm(self.x[:M], self.w.final_norm, self.dims.eps, Y=self.h[:M])
         return M
 
+    def prefill(self, x0, cu_rows, ctx_len, temperature: float | None = None, positions=None):
+        """One chunk of the prompts through the stack: x0 [M, d] are the packed embedding rows of
+        sequences that have ctx_len tokens in the paged cache already (any number of rows each, none
+        included).  Leaves the rows' keys and values in their pages (the caller then advances ctx_len by
+        the rows) and returns the hidden rows x [M, d] after the last layer, or with a temperature
+        (x, P): P [B, V] the next token's probabilities after each sequence's last row of the chunk
+        (those of a sequence without rows mean nothing).  At most max_M rows."""
+        if self.block_table is None:
+            raise ValueError("prefill needs a paged cache (block_table)")
+        M = self._stack(x0, cu_rows, ctx_len, 1, None, final_norm=False, prompt=True, positions=positions)
+        if temperature is None:
+            return self.x[:M]
+        last = (cu_rows[1:] - 1).clamp_(min=0)
+        B = last.numel()
+        h = S.spec_rmsnorm(self.x[:M].index_select(0, last), self.w.final_norm, self.dims.eps)
+        P = self.P[:B] if B <= self.P.shape[0] else None
+        return self.x[:M], S.spec_lmhead_softmax(h, self.w.w_lm, temperature, P=P, ws=self.ws)
+
     def verify_pass(self, x0, cu_rows, ctx_len, temperature: float, max_rows: int | None = None,
-                    n_layers: int | None = None):
+                    n_layers: int | None = None, positions=None):
         """All layers + LM head over the packed rows; returns P [M, V] (fp32 view)."""
-        M = self._stack(x0, cu_rows, ctx_len, max_rows, n_layers)
+        M = self._stack(x0, cu_rows, ctx_len, max_rows, n_layers, positions=positions)
         if self.w.w_lm is None:
             return None
         return S.spec_lmhead_softmax(self.h[:M], self.w.w_lm, temperature, P=self.P[:M], ws=self.ws)
 
     def verify_round(self, x0, cu_rows, ctx_len, q, drafts, U, temperature: float,
-                     tie_eps: float = 1e-5, max_rows: int | None = None, out=None):
+                     tie_eps: float = 1e-5, max_rows: int | None = None, out=None, positions=None):
         """Verify pass + rejection sampler; returns (n_acc, out_tok, near_tie)."""
         if not self.fused_sampler:
-            P = self.verify_pass(x0, cu_rows, ctx_len, temperature, max_rows)
+            P = self.verify_pass(x0, cu_rows, ctx_len, temperature, max_rows, positions=positions)
             return S.spec_reject_sample(P, q, drafts, U, cu_rows, tie_eps, out=out)
-        M = self._stack(x0, cu_rows, ctx_len, max_rows, None, final_norm=False)
+        M = self._stack(x0, cu_rows, ctx_len, max_rows, None, final_norm=False, positions=positions)
         if self.fold_norms:
             if self.dims.layers == 0:
                 S.spec_row_ssq(self.x[:M], out=self.ssq[:M])
@@ -297,13 +348,16 @@ class DraftEngine:
     the library's kernels; the engine only sequences the calls and advances positions.
     """
 
-    def __init__(self, dims: Dims, weights: StackW, kcaches, vcaches, B: int, gamma: int, device=None):
+    def __init__(self, dims: Dims, weights: StackW, kcaches, vcaches, B: int, gamma: int, device=None, block_table=None,
+                 max_M: int | None = None):
+        """block_table: a paged cache, as VerifyEngine's; max_M: rows of the largest prompt chunk that
+        ``eng.prefill`` takes (default: B)."""
         self.dims = dims
         self.B = B
         self.gamma = gamma
         # (the LM head is the embedding table here: its rows must stay unscaled, so no folded norms)
-        self.eng = VerifyEngine(dims, weights, kcaches, vcaches, max_M=B, max_rows=1, device=device,
-                                fused_sampler=False, fold_norms=False)
+        self.eng = VerifyEngine(dims, weights, kcaches, vcaches, max_M=max(B, max_M or B), max_rows=1, device=device,
+                                fused_sampler=False, fold_norms=False, block_table=block_table)
         dev = self.eng.device
         self.table = weights.w_lm
         self.cu = torch.arange(B + 1, dtype=torch.int32, device=dev)

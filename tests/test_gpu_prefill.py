@@ -1,0 +1,150 @@
+"""The engine's prompts over a paged cache: chunks of uneven length, then verify passes on the same pages,
+against the oracle's single pass over the whole sequences."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import bf16 as obf, ops as oops, stack as ostack
+
+from gpu_util import STACK_PROB_BOUND, assert_close_chain, bf16_dev, dev, f64_of_bf16
+from test_gpu_glue_stack import _tiny_stack
+
+pytestmark = pytest.mark.gpu
+PAGE = 128
+
+
+class Paged:
+    """Per-layer pools full of NaN and a block table in a random order."""
+
+    def __init__(self, dims, lengths, seed=3):
+        need = [(n + PAGE - 1) // PAGE for n in lengths]
+        perm = np.random.default_rng(seed).permutation(sum(need) + 2)
+        self.table_h = np.full((len(lengths), max(need)), -1, np.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table_h[b, :n] = perm[at:at + n]
+            at += n
+        pool = lambda: torch.full((dims.Hkv, sum(need) + 2, PAGE, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        self.k, self.v = [pool() for _ in range(dims.layers)], [pool() for _ in range(dims.layers)]
+        self.table = dev(self.table_h)
+
+
+def whole(osw, od, x_bits, lengths):
+    """The oracle's one pass over the sequences from position 0: hidden rows, logits per sequence."""
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    zeros = [np.zeros((len(lengths), od.Hkv, max(lengths), 128)) for _ in range(od.layers)]
+    x, lg, _, _ = ostack.verify_pass(obf.decode(np.concatenate(x_bits)), osw, od, cu, [0] * len(lengths), zeros, zeros)
+    return [x[cu[b]:cu[b + 1]] for b in range(len(lengths))], [lg[cu[b]:cu[b + 1]] for b in range(len(lengths))]
+
+
+def run_chunks(eng, x_bits, cuts, lib, temperature=None, positions=None):
+    """Runs the cuts' chunks through eng.prefill; the hidden rows per sequence (and the last P)."""
+    out, P = [[] for _ in x_bits], None
+    for at, to in zip(cuts[:-1], cuts[1:]):
+        rows = [t - a for a, t in zip(at, to)]
+        cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        x0 = bf16_dev(np.concatenate([x[a:t] for x, a, t in zip(x_bits, at, to)]))
+        pos = None if positions is None else positions(at, to)
+        r = eng.prefill(x0, dev(cu), dev(np.array(at, np.int32)), temperature=temperature, positions=pos)
+        x, P = r if temperature is not None else (r, None)
+        x = f64_of_bf16(x)
+        for b in range(len(x_bits)):
+            out[b].append(x[cu[b]:cu[b + 1]])
+    lib.spec_device_status()
+    return [np.concatenate(o) for o in out], P
+
+
+@pytest.mark.parametrize("L,fold,fused", [(1, True, True), (2, True, True), (2, False, False)])
+def test_prompt_then_verify(lib, L, fold, fused):
+    """Three sequences' prompts in uneven chunks (one of them brings nothing at times), then a verify pass."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(L, 70 + L)
+    lengths, gammas = [200, 131, 7], [3, 0, 4]
+    total = [n + g + 1 for n, g in zip(lengths, gammas)]
+    x_bits = [synth.normal_bf16_bits(90 + b, (total[b], dims.d), 1.0) for b in range(3)]
+    cache = Paged(dims, total)
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=400, max_rows=5, fold_norms=fold, fused_rope=fused,
+                         block_table=cache.table)
+    cuts = [(0, 0, 0), (129, 1, 0), (129, 130, 6), (200, 131, 7)]
+    hidden, P = run_chunks(eng, x_bits, cuts, lib, temperature=1.0)
+    ref_x, ref_lg = whole(osw, od, x_bits, total)
+    for b in range(3):
+        assert_close_chain(hidden[b], ref_x[b][:lengths[b]], L, f"prompt rows of sequence {b}")
+        # the next token's probabilities behind the prompt
+        p = P[b].cpu().numpy().astype(np.float64)
+        assert abs(p - oops.target_probs(ref_lg[b][lengths[b] - 1:lengths[b]], 1.0)[0]).max() < STACK_PROB_BOUND
+    cu = np.concatenate([[0], np.cumsum([g + 1 for g in gammas])]).astype(np.int32)
+    x0 = bf16_dev(np.concatenate([x[n:] for x, n in zip(x_bits, lengths)]))
+    P = eng.verify_pass(x0, dev(cu), dev(np.array(lengths, np.int32)), 1.0)
+    lib.spec_device_status()
+    ref = np.concatenate([x[n:] for x, n in zip(ref_x, lengths)])
+    assert_close_chain(f64_of_bf16(eng.x[:cu[-1]]), ref, L, "verify rows behind the prompts")
+    lg = np.concatenate([x[n:] for x, n in zip(ref_lg, lengths)])
+    assert abs(P.cpu().numpy().astype(np.float64) - oops.target_probs(lg, 1.0)).max() < STACK_PROB_BOUND
+
+
+def test_positions_of_several_axes(lib):
+    """Text's positions on three axes are its one position; attention only sees differences, so positions that are
+    all 5000 further on give the same rows."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(1, 81)
+    dims.rope_sections, dims.rope_interleaved = (24, 20, 20), True
+    lengths = [150, 40]
+    x_bits = [synth.normal_bf16_bits(95 + b, (lengths[b], dims.d), 1.0) for b in range(2)]
+    ref_x, _ = whole(osw, od, x_bits, lengths)
+    for shift in (0, 5000):
+        cache = Paged(dims, lengths)
+        eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=200, max_rows=1, block_table=cache.table)
+
+        def positions(at, to):
+            pos = np.concatenate([np.arange(a, t) for a, t in zip(at, to)]) + shift
+            return dev(np.stack([pos] * 3).astype(np.int32))
+        hidden, _ = run_chunks(eng, x_bits, [(0, 0), (100, 1), (150, 40)], lib, positions=positions)
+        for b in range(2):
+            assert_close_chain(hidden[b], ref_x[b], 1, f"shift {shift}, sequence {b}")
+
+
+def test_draft_engine_over_pages(lib):
+    """The draft phase on a paged cache that a prompt filled: the same drafts and q as on a contiguous cache with the
+    same keys (one row per sequence takes the same key tiles in the same order)."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(1, 83)
+    B, gamma, lengths = 2, 3, [140, 20]
+    cache = Paged(dims, [n + gamma for n in lengths])
+    g = E.DraftEngine(dims, gsw, cache.k, cache.v, B, gamma, block_table=cache.table, max_M=160)
+    x_bits = [synth.normal_bf16_bits(97 + b, (lengths[b], dims.d), 1.0) for b in range(B)]
+    run_chunks(g.eng, x_bits, [(0, 0), (140, 20)], lib)
+    kc = torch.zeros((B, dims.Hkv, 2 * PAGE, 128), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    for b in range(B):
+        for t in range((lengths[b] + gamma + PAGE - 1) // PAGE):
+            n = min(PAGE, lengths[b] - t * PAGE)
+            kc[b, :, t * PAGE:t * PAGE + n] = cache.k[0][:, cache.table_h[b, t], :n]
+            vc[b, :, t * PAGE:t * PAGE + n] = cache.v[0][:, cache.table_h[b, t], :n]
+    c = E.DraftEngine(dims, gsw, [kc], [vc], B, gamma)
+    tok, ctx = dev(np.array([5, 9], np.int32)), dev(np.array(lengths, np.int32))
+    U = dev(synth.uniforms_f32(4, gamma * B).reshape(gamma, B))
+    res = []
+    for e in (g, c):
+        Q = torch.zeros((B * gamma, dims.V), device="cuda")
+        drafts = torch.zeros(B * gamma, dtype=torch.int32, device="cuda")
+        e.draft(tok, ctx, U, 1.0, Q, drafts)
+        lib.spec_device_status()
+        res.append((Q, drafts))
+    assert torch.equal(res[0][1], res[1][1]) and torch.equal(res[0][0], res[1][0])
+
+
+def test_prefill_refusals(lib):
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, _, _, gsw = _tiny_stack(1, 85)
+    x = torch.zeros((2, dims.d), dtype=torch.bfloat16, device="cuda")
+    cu, ctx = dev(np.array([0, 2], np.int32)), dev(np.zeros(1, np.int32))
+    kc = [torch.zeros((1, dims.Hkv, 8, 128), dtype=torch.bfloat16, device="cuda")]
+    eng = E.VerifyEngine(dims, gsw, kc, [kc[0].clone()], max_M=4, max_rows=2)
+    with pytest.raises(ValueError):
+        eng.prefill(x, cu, ctx)                                  # contiguous cache
+    cache = Paged(dims, [8])
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=1, max_rows=1, block_table=cache.table)
+    with pytest.raises(ValueError):
+        eng.prefill(x, cu, ctx)                                  # more rows than the engine was sized for
