@@ -432,8 +432,8 @@ SPEC_API int spec_verify_attention_paged(const spec_bf16* Q, int ldq, const spec
  *   cu_rows [B+1], ctx_len [B], block_table [B x max_pages] int32 device arrays
  *   Kpool, Vpool [Hkv][num_pages][128][D] bf16 (in/out), as spec_verify_attention_paged's; no input may
  *               overlap them
- * M is the rows of the buffers; rows outside cu_rows[0] .. cu_rows[B] - 1 are padding: not read, and
- * Qrot's left as they were.  Sequences without rows are allowed.  A page that receives rows must belong to one
+ * M is the rows of the buffers; rows outside cu_rows[0] .. cu_rows[B] - 1 are padding: they may hold
+ * anything, and Qrot's are left as they were.  Sequences without rows are allowed.  A page that receives rows must belong to one
  * sequence.  Checked on the device, with the status word set: a sequence outside the M rows or
  * past 128 * max_pages keys is skipped; a row whose page id is outside [0, num_pages) is not written to
  * the pools.  Requires D == 128, leading dimensions multiples of 8, 16-byte aligned pointers.  One
@@ -455,7 +455,8 @@ SPEC_API int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, 
  * Pages are read to the last key of the sequence only: what lies behind it (in its last page or in
  * table entries past it) may hold anything, NaN included.  Rows outside cu_rows[0] .. cu_rows[B] - 1
  * are padding: their O is left as it was.  A non-finite value in V of a new key also reaches the rows of its
- * own chunk before it that share its 128-key tile (0 * inf).  Checked on the device, with the status
+ * own chunk before it that share its 128-key tile (0 * inf).  Values up to 1e25 keep the unnormalised
+ * sums in range.  Checked on the device, with the status
  * word set: a sequence outside the M rows or past 128 * max_pages keys is skipped; a page id outside
  * [0, num_pages) reads page 0 instead.
  * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, scale finite and >= 0.

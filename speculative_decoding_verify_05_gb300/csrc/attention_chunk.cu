@@ -5,19 +5,30 @@
 // heads (row m = token m / G, head m % G) into the MMA's 128 rows; an item is two row tiles (2 TPT
 // tokens of one sequence and kv head) over all key tiles (one page, 128 keys) that its last token sees.
 //   S[row, key] = Q . K_tile^T    tcgen05.mma M = 128, N = 128 keys, K = 128 dims (smem x smem)
-//   softmax                       one thread per row: running maximum and sum in registers, fp32
+//   softmax                       one thread per row: running reference and sum in registers, fp32
 //   O[row, d]  += P . V_tile      tcgen05.mma M = 128, N = 128 dims, K = 128 keys, P (bf16) read
 //                                 from TMEM, where it replaces the scores it came from
 // TMEM holds S and O of two slots (4 x 128 columns, all of it).  The steps of a CTA alternate between the
 // slots, so that one slot's softmax runs beside the other slot's products.  An item of two row tiles
 // gives each slot one of them and both use every key tile (one load, two products); an item with a single
 // row tile (few rows: decode steps, ends of prompts) gives the slots its key tiles in turn, each
-// with its own running maximum, sum and O, joined at the end.
+// with its own reference, sum and O, joined at the end.
 //
 // Work.  The key tiles of all items in a row (sequence, kv head, item) are cut into equal shares by cost, one
 // per CTA; every CTA works out the same cuts from the lengths on the device (closed form per
 // sequence, so one graph serves any lengths).  Where a cut falls into an item its pieces go to the
-// workspace as unnormalised O, maximum and sum, and a second small kernel joins them in CTA order.
+// workspace as unnormalised O, reference and sum; the warps of the item's CTAs that are done when the last
+// piece arrives join it together, in CTA order whoever does it (a second kernel for this took 5 to 8 us
+// longer).  Without these shares a prompt's last items would leave most of the chip idle, and a few rows over
+// a long cache all but a few CTAs.
+//
+// Bound.  With many rows, the tensor cores: a key tile's four products of 128^3 take 2048 of their cycles, in which
+// the softmax warps have to form 256 x 128 weights, which is why nothing else is in their way: no
+// maximum per tile (the reference below), two fp32 operations per instruction, a row per thread.  A prompt of 8192 rows
+// (32 + 2 x 8 heads) takes 333 us = 1650 TFLOP/s, 2048 rows at 30000 keys 640 us.  With few rows, HBM: 61 rows at
+// 131000 keys 98 us = 5.5 TB/s.  In between and below, what a call costs whatever its size: 4 to 5 us
+// to the first product (lengths, cuts, page table, first tiles), 5 to 7 us to join shared items, which one token
+// of 4 sequences (15 us) and a chunk of 512 at 7680 keys (56 us) pay.
 //
 // Roles (12 warps): 0-3 and 4-7 softmax and epilogue of slot 0 and 1 (thread = TMEM lane = row); 8 loads K
 // and V tiles by TMA into one ring of 5; 9 issues the MMAs; 10 loads the Q tiles and zeroes the rows of
@@ -210,8 +221,8 @@ __device__ __forceinline__ int cut_tile(long long y, bool dual, int keys, int nt
   y -= w * ITEM_KEYS;
   if (y <= 0) return 0;
   if (y >= (long long)w * keys) return nt;
-  const unsigned z = (unsigned)y + w * KT / 2;
-  const int t = (int)(dual ? z / (W_DUAL * KT) : z / (W_ONE * KT));
+  const unsigned z = dual ? (unsigned)y / W_DUAL : (unsigned)y / W_ONE;      // (keys <= 2^30)
+  const int t = (int)((z + KT / 2) / KT);
   return t * KT + KT / 2 >= keys ? nt : t;              // (no piece of a few keys)
 }
 // Where CTA c's share starts (c = grid: where the last one ends); inv_grid = floor((2^64 - 1) / grid).
@@ -403,387 +414,387 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 
   // the softmax warps hold a row of scores each: the other warpgroup leaves them its registers
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-  if (warp == 11) {
-    // ------------------------------------------------------------ pieces
-    // The sequences' costs, a run of them per lane; then the two sequences that this CTA's share starts and ends
-    // in, found by the lanes that have them.
-    const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
-    long long own = 0;
-    bool bad = false;
-#pragma unroll 2
-    for (int b = b0; b < b1; ++b) {
-      bool wrong;
-      const Seq s = seq_of(a, b, &wrong);
-      bad |= wrong;
-      own += head_cost(a, s) * a.Hkv;
-    }
-    if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
-    long long before = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += v;
-    }
-    const long long total = __shfl_sync(0xffffffffu, before, 31);
-    before -= own;
-    Found f{0, 0, a.B, Seq{0, 0, 0}};      // lanes 0-15: of the start, 16-31: of the end
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const long long x = share_start(a, total, blockIdx.x + k);
-      const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + own);
-      if (owner == 0) continue;            // (the end of everything, or nothing at all)
-      Found g{0, before, b0, Seq{0, 0, 0}};
-      if (x >= before && x < before + own)
-        for (;; ++g.b) {
-          g.s = seq_of(a, g.b);
-          const long long c = head_cost(a, g.s) * a.Hkv;
-          if (x < g.before + c) break;
-          g.before += c;
-        }
-      const int from = __ffs(owner) - 1;
-      g.before = __shfl_sync(0xffffffffu, g.before, from);
-      g.b = __shfl_sync(0xffffffffu, g.b, from);
-      g.s.r0 = __shfl_sync(0xffffffffu, g.s.r0, from);
-      g.s.rows = __shfl_sync(0xffffffffu, g.s.rows, from);
-      g.s.ctx = __shfl_sync(0xffffffffu, g.s.ctx, from);
-      g.x = x - g.before;
-      if ((lane >> 4) == k) f = g;
-    }
-    const Cut mine = cut_of(a, f, lane);
-    Cut end;
-    end.start = __shfl_sync(0xffffffffu, mine.start, 16);
-    end.b = __shfl_sync(0xffffffffu, mine.b, 16);
-    end.h = __shfl_sync(0xffffffffu, mine.h, 16);
-    end.q = __shfl_sync(0xffffffffu, mine.q, 16);
-    end.t = __shfl_sync(0xffffffffu, mine.t, 16);
-    if (lane == 0) {
-      Walk w;
-      w.first(a, mine, end);
-      *s_first = w.p;
-      *s_total = total;
-      for (int k = 0;; ++k) {
-        if (k >= PR && !wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1))) {
-          set_status(a.status, 0x701u);
-          break;
-        }
-        ring[k % PR] = w.p;
-        mbar_arrive(&posted[k % PR]);
-        if (!w.p.more) break;
-        w.next(a, end);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    if (warp == 11) {
+      // ------------------------------------------------------------ pieces
+      // The sequences' costs, a run of them per lane; then the two sequences that this CTA's share starts and ends
+      // in, found by the lanes that have them.
+      const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
+      long long own = 0;
+      bool bad = false;
+  #pragma unroll 2
+      for (int b = b0; b < b1; ++b) {
+        bool wrong;
+        const Seq s = seq_of(a, b, &wrong);
+        bad |= wrong;
+        own += head_cost(a, s) * a.Hkv;
       }
-    }
-    __syncwarp();
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ K and V tiles
-    // in the order of their first products: a step's V tile, then the K tile of its slot's next step
-    int idx = 0;
-    bool ok = true;
-    uint32_t landed = 0;                   // stages whose last load signals `land`
-    uint32_t n_land = 0;                   // its phase, one bit per stage
-    const uint64_t pol = l2_policy_evict_first();
-    // page ids of 32 tiles at a time, one per lane
-    struct Pages {
-      int id, base;
-    };
-    auto load = [&](const Piece& p, Pages& pg, int t, bool is_v) {
-      if (pg.base < 0 || t >= pg.base + 32) {
-        pg.base = t;
-        pg.id = t + lane < p.t1 ? a.block_table[(size_t)p.b * a.max_pages + t + lane] : 0;
-        if (pg.id < 0 || pg.id >= a.num_pages) {
-          set_status(a.status, 0x7F2u);
-          pg.id = 0;
-        }
+      if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
+      long long before = own;
+  #pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
       }
-      const int page = __shfl_sync(0xffffffffu, pg.id, t - pg.base);
-      const int st = idx % ST;
-      if (idx >= ST) ok = ok && wait_for(&empty[st], (uint32_t)((idx / ST - 1) & 1));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const bool tail = is_v && t == p.nt - 1 && p.tail();
-      uint64_t* bar = tail ? &land[st] : &full[st];
+      const long long total = __shfl_sync(0xffffffffu, before, 31);
+      before -= own;
+      Found f{0, 0, a.B, Seq{0, 0, 0}};      // lanes 0-15: of the start, 16-31: of the end
+  #pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const long long x = share_start(a, total, blockIdx.x + k);
+        const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + own);
+        if (owner == 0) continue;            // (the end of everything, or nothing at all)
+        Found g{0, before, b0, Seq{0, 0, 0}};
+        if (x >= before && x < before + own)
+          for (;; ++g.b) {
+            g.s = seq_of(a, g.b);
+            const long long c = head_cost(a, g.s) * a.Hkv;
+            if (x < g.before + c) break;
+            g.before += c;
+          }
+        const int from = __ffs(owner) - 1;
+        g.before = __shfl_sync(0xffffffffu, g.before, from);
+        g.b = __shfl_sync(0xffffffffu, g.b, from);
+        g.s.r0 = __shfl_sync(0xffffffffu, g.s.r0, from);
+        g.s.rows = __shfl_sync(0xffffffffu, g.s.rows, from);
+        g.s.ctx = __shfl_sync(0xffffffffu, g.s.ctx, from);
+        g.x = x - g.before;
+        if ((lane >> 4) == k) f = g;
+      }
+      const Cut mine = cut_of(a, f, lane);
+      Cut end;
+      end.start = __shfl_sync(0xffffffffu, mine.start, 16);
+      end.b = __shfl_sync(0xffffffffu, mine.b, 16);
+      end.h = __shfl_sync(0xffffffffu, mine.h, 16);
+      end.q = __shfl_sync(0xffffffffu, mine.q, 16);
+      end.t = __shfl_sync(0xffffffffu, mine.t, 16);
       if (lane == 0) {
-        const CUtensorMap* tm = is_v ? &tmV : &tmK;
-        uint8_t* dst = smem + OFF_RING + st * TILE;
-        const int z = p.h * a.num_pages + page;
-        mbar_arrive_expect_tx(bar, TILE);
-        if (p.once) {
-          tma_load_3d_hint(dst, tm, bar, 0, 0, z, pol);
-          tma_load_3d_hint(dst + HALF, tm, bar, 64, 0, z, pol);
-        } else {
-          tma_load_3d(dst, tm, bar, 0, 0, z);
-          tma_load_3d(dst + HALF, tm, bar, 64, 0, z);
+        Walk w;
+        w.first(a, mine, end);
+        *s_first = w.p;
+        *s_total = total;
+        for (int k = 0;; ++k) {
+          if (k >= PR && !wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1))) {
+            set_status(a.status, 0x701u);
+            break;
+          }
+          ring[k % PR] = w.p;
+          mbar_arrive(&posted[k % PR]);
+          if (!w.p.more) break;
+          w.next(a, end);
         }
       }
-      if (tail) {
-        landed |= 1u << st;
-        n_land ^= 1u << st;
-      } else {
-        landed &= ~(1u << st);
-      }
-      ++idx;
-    };
-    auto open = [&](int k) {
-      ok = ok && wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1));
-      ok = __all_sync(0xffffffffu, ok);
-      Piece p = ring[k % PR];
-      if (!ok) p.more = 0;
-      return p;
-    };
-    // pair by pair (before the first: K only): V and the next K of slot 0, then of slot 1
-    Piece p = open(0), nx = p;
-    Pages pv{0, -1}, pk{0, -1};
-    for (int k = 0, j = -1; ok && nx.more;) {
-      const bool ends = j + 1 == p.pairs();
-      if (ends) {
-        nx = open(k + 1);
-        pk.base = -1;
-      }
-      const int nj = ends ? 0 : j + 1;
-#pragma unroll 1
-      for (int q = 0; q < 4 && ok; ++q) {
-        const int sl = q >> 1;
-        const bool is_v = !(q & 1);
-        const Piece& from = is_v ? p : nx;
-        const int at = is_v ? j : nj;
-        if (at >= 0 && from.more && (sl == 0 || !from.dual) && at < from.steps(sl))
-          load(from, is_v ? pv : pk, from.tile(sl, at), is_v);
-      }
-      j = nj;
-      if (ends) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&taken[k % PR]);
-        ++k;
-        p = nx;
-        pv.base = -1;
-      }
-    }
-    if (!ok) {                             // gave up: see the copies in flight land before leaving
-      set_status(a.status, 0x711u);
-      for (int j = idx > ST ? idx - ST : 0; j < idx; ++j) {
-        const int st = j % ST;
-        if ((landed >> st) & 1u) wait_for(&land[st], ((n_land >> st) & 1u) ^ 1u);
-        else wait_for(&full[st], (uint32_t)((j / ST) & 1));
-      }
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issue
-    // The whole warp walks the steps and one elected lane issues: addresses are then the same in every lane
-    // (TMEM and Q addresses constants of the slot, the ring stage a uniform count), which the MMAs take
-    // from uniform registers.  Issued from a divergent branch each MMA cost 60 to 100 cycles of operand moves,
-    // its 64 cycles on the tensor core twice over.  Few MMAs queue, so what the warp does between them
-    // leaves the tensor core idle: the tiles of a pair are waited for before its weights, and after a wait that
-    // ran out the warp goes on without waiting (to garbage that nobody reads) instead of voting each time.
-    const bool leader = elect_one();
-    constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
-    constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
-    const uint64_t q0 = umma_desc_sw128(smem_u32(smem + OFF_Q)), k0 = umma_desc_sw128(smem_u32(smem + OFF_RING));
-    const uint64_t v0 = desc_mn(smem_u32(smem + OFF_RING), HALF);
-    int st = 0;                            // next ring stage
-    uint32_t ph = 0, ph_p = 0, ph_q = 0;   // phases: the ring's; each slot's weights and Q tile, one bit per slot
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = wait_for(bar, parity);
-    };
-    // the next ring stage and its phase
-    struct Stage {
-      int st;
-      uint32_t ph;
-    };
-    auto take = [&]() {
-      const Stage mine{st, ph};
-      if (++st == ST) {
-        st = 0;
-        ph ^= 1u;
-      }
-      return mine;
-    };
-    auto ready = [&](const Stage& t) { return mbar_try_wait(&full[t.st], t.ph); };
-    auto wait_tile = [&](const Stage& t) { wait(&full[t.st], t.ph); };
-    // scores of a slot from the K tile of stage kst; first / last: of the slot's steps of the piece
-    auto scores = [&](const int sl, int kst, bool first, bool last, bool release) {
-      if (first) {
-        wait(&q_full[sl], (ph_q >> sl) & 1u);
-        ph_q ^= 1u << sl;
-        tc_fence_after();
-      }
-      if (leader) {
-        const uint64_t qd = q0 + sl * (TILE >> 4), kd = k0 + (uint32_t)(kst * (TILE >> 4));
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {   // (descriptor addresses count 16 bytes)
-          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-          umma_bf16(sl * KT, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[sl]);
-        if (release) umma_commit(&empty[kst]);
-        if (last) umma_commit(&q_empty[sl]);
-      }
-    };
-    // O += P V of a slot from the V tile of stage vst, over `steps` times 16 keys
-    auto weigh = [&](const int sl, int vst, int steps, bool first, bool last, bool release) {
-      if (leader) {
-        const uint64_t vd = v0 + (uint32_t)(vst * (TILE >> 4));
-        constexpr uint32_t t_o = 2 * KT;
-        umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, first ? 0u : 1u);
-#pragma unroll
-        for (int kk = 1; kk < 8; ++kk)
-          umma_bf16_ts_if(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, kk < steps);
-        if (release) umma_commit(&empty[vst]);
-        if (last) umma_commit(&o_full[sl]);
-      }
-    };
-    struct Run {                           // what a piece's steps need
-      bool more, dual;
-      int n0, n1;                          // steps of the slots
-      int tail;                            // 16-key steps of its last tile up to the last key
-    };
-    auto open = [&](int k) {
-      wait(&posted[k % PR], (uint32_t)((k / PR) & 1));
-      ok = __all_sync(0xffffffffu, ok);
-      const Piece& p = ring[k % PR];
-      Run r{ok && p.more, p.dual != 0, p.steps(0), p.steps(1), min(8, (p.keys() - (p.t1 - 1) * KT + 15) >> 4)};
-      return r;
-    };
-    // pair by pair (before the first: scores only)
-    Run r = open(0), nx = r;
-    Stage k_a{0, 0}, k_b{0, 0}, v_a{0, 0}, v_b{0, 0};
-    for (int k = 0, j = -1; nx.more;) {
-      // two row tiles, and the next pair of the same piece: nothing to decide (with the general case's
-      // decisions in the way 2048 rows at 30000 keys took 700 us instead of 650)
-      while (r.dual && j >= 0 && j + 1 < r.n0) {
-        const Stage v = take(), t = take();
-        const uint32_t pa = ph_p & 1u, pb = (ph_p >> 1) & 1u;
-        const bool r0 = ready(v), r1 = ready(t), r2 = mbar_try_wait(&p_full[0], pa);
-        if (!(r0 && r1 && r2)) {
-          wait_tile(v);
-          wait_tile(t);
-          wait(&p_full[0], pa);
-        }
-        tc_fence_after();
-        weigh(0, v.st, 8, j == 0, false, false);
-        scores(0, t.st, false, j + 2 == r.n0, false);
-        wait(&p_full[1], pb);
-        tc_fence_after();
-        weigh(1, v.st, 8, j == 0, false, true);
-        scores(1, t.st, false, j + 2 == r.n0, true);
-        ph_p ^= 3u;
-        ++j;
-      }
-      const bool ends = j + 1 == r.n0;     // (slot 0 has a step in every pair)
-      if (ends) nx = open(k + 1);
-      const int nj = ends ? 0 : j + 1;
-      const bool now_a = j >= 0, now_b = now_a && j < r.n1, next_a = nx.more, next_b = nx.more && nj < nx.n1;
-      const bool last_tile_b = !r.dual && now_b && ends;      // slot 1 holds the piece's last tile
-      // one look at all that slot 0 needs; what is not there is waited for in turn
-      if (now_a) v_a = take();
-      if (next_a) k_a = take();
-      const uint32_t pa = ph_p & 1u, pb = (ph_p >> 1) & 1u;
-      // (a try that cannot succeed is not made: it holds the warp for microseconds)
-      bool all = false;
-      if (now_a && next_a) {
-        const bool r0 = ready(v_a), r1 = ready(k_a), r2 = mbar_try_wait(&p_full[0], pa);
-        all = r0 && r1 && r2;
-      }
-      if (!all) {
-        if (now_a) wait_tile(v_a);
-        if (next_a) wait_tile(k_a);
-        if (now_a) wait(&p_full[0], pa);
-      }
-      tc_fence_after();
-      if (now_a) {
-        weigh(0, v_a.st, ends && !last_tile_b ? r.tail : 8, j == 0, ends, !r.dual);
-        ph_p ^= 1u;
-      }
-      if (next_a) scores(0, k_a.st, nj == 0, nj + 1 == nx.n0, !nx.dual);
-      if (now_b) v_b = r.dual ? v_a : take();
-      if (next_b) k_b = nx.dual ? k_a : take();
-      all = false;
-      if (now_b && next_b) {
-        const bool s0 = ready(v_b), s1 = ready(k_b), s2 = mbar_try_wait(&p_full[1], pb);
-        all = s0 && s1 && s2;
-      }
-      if (!all) {
-        if (now_b) wait_tile(v_b);
-        if (next_b) wait_tile(k_b);
-        if (now_b) wait(&p_full[1], pb);
-      }
-      tc_fence_after();
-      if (now_b) {
-        weigh(1, v_b.st, ends ? r.tail : 8, j == 0, j + 1 == r.n1, true);
-        ph_p ^= 2u;
-      }
-      if (next_b) scores(1, k_b.st, nj == 0, nj + 1 == nx.n1, true);
-      j = nj;
-      if (ends) {
-        __syncwarp();
-        if (leader) mbar_arrive(&taken[k % PR]);
-        ++k;
-        r = nx;
-      }
-    }
-    if (!ok) set_status(a.status, 0x721u);
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ Q tiles, ends of the last V tiles
-    uint32_t n_q[2] = {0, 0}, n_land = 0;
-    int tiles = 0;                         // key tiles of the pieces so far
-    const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * D * 2);
-    bool ok = true, had = false, more = true;
-    for (int k = 0; (more || had) && ok; ++k) {
-      const Piece* p = ring + k % PR;
-      const Piece* before = ring + (k + PR - 1) % PR;
-      if (more) {
-        ok = __all_sync(0xffffffffu, wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1)));
-        if (!ok) break;
-        more = p->more != 0;
-      }
-      if (more) {
-        for (int sl = 0; sl < 2 && p->steps(sl) > 0; ++sl) {
-          if (n_q[sl] > 0) ok = ok && wait_for(&q_empty[sl], (n_q[sl] - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ++n_q[sl];
-          if (lane == 0) {
-            uint8_t* dst = smem + OFF_Q + sl * TILE;
-            const int row = p->row0 + (p->dual ? sl * a.tpt : 0);
-            mbar_arrive_expect_tx(&q_full[sl], q_bytes);
-            tma_load_3d(dst, &tmQ, &q_full[sl], 0, p->h * a.G, row);
-            tma_load_3d(dst + HALF, &tmQ, &q_full[sl], 64, p->h * a.G, row);
+      __syncwarp();
+    } else if (warp == 8) {
+      // ------------------------------------------------------------ K and V tiles
+      // in the order of their first products: a step's V tile, then the K tile of its slot's next step
+      int idx = 0;
+      bool ok = true;
+      uint32_t landed = 0;                   // stages whose last load signals `land`
+      uint32_t n_land = 0;                   // its phase, one bit per stage
+      const uint64_t pol = l2_policy_evict_first();
+      // page ids of 32 tiles at a time, one per lane
+      struct Pages {
+        int id, base;
+      };
+      auto load = [&](const Piece& p, Pages& pg, int t, bool is_v) {
+        if (pg.base < 0 || t >= pg.base + 32) {
+          pg.base = t;
+          pg.id = t + lane < p.t1 ? a.block_table[(size_t)p.b * a.max_pages + t + lane] : 0;
+          if (pg.id < 0 || pg.id >= a.num_pages) {
+            set_status(a.status, 0x7F2u);
+            pg.id = 0;
           }
         }
-        if (!ok) break;
-      }
-      // the piece before: rows of its last V tile from the sequence's last key to the next multiple of 16
-      if (had) {
-        if (before->tail()) {
-          // loads before that tile: every K and V before it, its own K, and the first K of the next piece
-          // if it came before slot 1's V
-          const int st = (2 * (tiles - 1) + 1 + (!before->dual && !(before->tiles() & 1) && more ? 1 : 0)) % ST;
-          ok = wait_for(&land[st], (n_land >> st) & 1u);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+        const int page = __shfl_sync(0xffffffffu, pg.id, t - pg.base);
+        const int st = idx % ST;
+        if (idx >= ST) ok = ok && wait_for(&empty[st], (uint32_t)((idx / ST - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        const bool tail = is_v && t == p.nt - 1 && p.tail();
+        uint64_t* bar = tail ? &land[st] : &full[st];
+        if (lane == 0) {
+          const CUtensorMap* tm = is_v ? &tmV : &tmK;
+          uint8_t* dst = smem + OFF_RING + st * TILE;
+          const int z = p.h * a.num_pages + page;
+          mbar_arrive_expect_tx(bar, TILE);
+          if (p.once) {
+            tma_load_3d_hint(dst, tm, bar, 0, 0, z, pol);
+            tma_load_3d_hint(dst + HALF, tm, bar, 64, 0, z, pol);
+          } else {
+            tma_load_3d(dst, tm, bar, 0, 0, z);
+            tma_load_3d(dst + HALF, tm, bar, 64, 0, z);
+          }
+        }
+        if (tail) {
+          landed |= 1u << st;
           n_land ^= 1u << st;
-          uint8_t* vt = smem + OFF_RING + st * TILE;
-          const int r0 = before->keys() - (before->nt - 1) * KT, r1 = (r0 + 15) & ~15;
-          for (int r = r0 + (lane >> 4); r < r1; r += 2) {
-            const int ch = lane & 15;
-            *reinterpret_cast<uint4*>(vt + (ch >> 3) * HALF + sw128_off(r, (ch & 7) * 8)) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[st]);
+        } else {
+          landed &= ~(1u << st);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&taken[(k + PR - 1) % PR]);
+        ++idx;
+      };
+      auto open = [&](int k) {
+        ok = ok && wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        Piece p = ring[k % PR];
+        if (!ok) p.more = 0;
+        return p;
+      };
+      // pair by pair (before the first: K only): V and the next K of slot 0, then of slot 1
+      Piece p = open(0), nx = p;
+      Pages pv{0, -1}, pk{0, -1};
+      for (int k = 0, j = -1; ok && nx.more;) {
+        const bool ends = j + 1 == p.pairs();
+        if (ends) {
+          nx = open(k + 1);
+          pk.base = -1;
+        }
+        const int nj = ends ? 0 : j + 1;
+  #pragma unroll 1
+        for (int q = 0; q < 4 && ok; ++q) {
+          const int sl = q >> 1;
+          const bool is_v = !(q & 1);
+          const Piece& from = is_v ? p : nx;
+          const int at = is_v ? j : nj;
+          if (at >= 0 && from.more && (sl == 0 || !from.dual) && at < from.steps(sl))
+            load(from, is_v ? pv : pk, from.tile(sl, at), is_v);
+        }
+        j = nj;
+        if (ends) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&taken[k % PR]);
+          ++k;
+          p = nx;
+          pv.base = -1;
+        }
       }
-      had = more;
-      if (more) tiles += p->tiles();
+      if (!ok) {                             // gave up: see the copies in flight land before leaving
+        set_status(a.status, 0x711u);
+        for (int j = idx > ST ? idx - ST : 0; j < idx; ++j) {
+          const int st = j % ST;
+          if ((landed >> st) & 1u) wait_for(&land[st], ((n_land >> st) & 1u) ^ 1u);
+          else wait_for(&full[st], (uint32_t)((j / ST) & 1));
+        }
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMA issue
+      // The whole warp walks the steps and one elected lane issues: addresses are then the same in every lane
+      // (TMEM and Q addresses constants of the slot, the ring stage a uniform count), which the MMAs take
+      // from uniform registers.  Issued from a divergent branch each MMA cost 60 to 100 cycles of operand moves,
+      // its 64 cycles on the tensor core twice over.  Few MMAs queue, so what the warp does between them
+      // leaves the tensor core idle: the tiles of a pair are waited for before its weights, and after a wait that
+      // ran out the warp goes on without waiting (to garbage that nobody reads) instead of voting each time.
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
+      const uint64_t q0 = umma_desc_sw128(smem_u32(smem + OFF_Q)), k0 = umma_desc_sw128(smem_u32(smem + OFF_RING));
+      const uint64_t v0 = desc_mn(smem_u32(smem + OFF_RING), HALF);
+      int st = 0;                            // next ring stage
+      uint32_t ph = 0, ph_p = 0, ph_q = 0;   // phases: the ring's; each slot's weights and Q tile, one bit per slot
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = wait_for(bar, parity);
+      };
+      // the next ring stage and its phase
+      struct Stage {
+        int st;
+        uint32_t ph;
+      };
+      auto take = [&]() {
+        const Stage mine{st, ph};
+        if (++st == ST) {
+          st = 0;
+          ph ^= 1u;
+        }
+        return mine;
+      };
+      auto ready = [&](const Stage& t) { return mbar_try_wait(&full[t.st], t.ph); };
+      auto wait_tile = [&](const Stage& t) { wait(&full[t.st], t.ph); };
+      // scores of a slot from the K tile of stage kst; first / last: of the slot's steps of the piece
+      auto scores = [&](const int sl, int kst, bool first, bool last, bool release) {
+        if (first) {
+          wait(&q_full[sl], (ph_q >> sl) & 1u);
+          ph_q ^= 1u << sl;
+          tc_fence_after();
+        }
+        if (leader) {
+          const uint64_t qd = q0 + sl * (TILE >> 4), kd = k0 + (uint32_t)(kst * (TILE >> 4));
+  #pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {   // (descriptor addresses count 16 bytes)
+            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+            umma_bf16(sl * KT, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[sl]);
+          if (release) umma_commit(&empty[kst]);
+          if (last) umma_commit(&q_empty[sl]);
+        }
+      };
+      // O += P V of a slot from the V tile of stage vst, over `steps` times 16 keys
+      auto weigh = [&](const int sl, int vst, int steps, bool first, bool last, bool release) {
+        if (leader) {
+          const uint64_t vd = v0 + (uint32_t)(vst * (TILE >> 4));
+          constexpr uint32_t t_o = 2 * KT;
+          umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, first ? 0u : 1u);
+  #pragma unroll
+          for (int kk = 1; kk < 8; ++kk)
+            umma_bf16_ts_if(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, kk < steps);
+          if (release) umma_commit(&empty[vst]);
+          if (last) umma_commit(&o_full[sl]);
+        }
+      };
+      struct Run {                           // what a piece's steps need
+        bool more, dual;
+        int n0, n1;                          // steps of the slots
+        int tail;                            // 16-key steps of its last tile up to the last key
+      };
+      auto open = [&](int k) {
+        wait(&posted[k % PR], (uint32_t)((k / PR) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        const Piece& p = ring[k % PR];
+        Run r{ok && p.more, p.dual != 0, p.steps(0), p.steps(1), min(8, (p.keys() - (p.t1 - 1) * KT + 15) >> 4)};
+        return r;
+      };
+      // pair by pair (before the first: scores only)
+      Run r = open(0), nx = r;
+      Stage k_a{0, 0}, k_b{0, 0}, v_a{0, 0}, v_b{0, 0};
+      for (int k = 0, j = -1; nx.more;) {
+        // two row tiles, and the next pair of the same piece: nothing to decide (with the general case's
+        // decisions in the way 2048 rows at 30000 keys took 700 us instead of 650)
+        while (r.dual && j >= 0 && j + 1 < r.n0) {
+          const Stage v = take(), t = take();
+          const uint32_t pa = ph_p & 1u, pb = (ph_p >> 1) & 1u;
+          const bool r0 = ready(v), r1 = ready(t), r2 = mbar_try_wait(&p_full[0], pa);
+          if (!(r0 && r1 && r2)) {
+            wait_tile(v);
+            wait_tile(t);
+            wait(&p_full[0], pa);
+          }
+          tc_fence_after();
+          weigh(0, v.st, 8, j == 0, false, false);
+          scores(0, t.st, false, j + 2 == r.n0, false);
+          wait(&p_full[1], pb);
+          tc_fence_after();
+          weigh(1, v.st, 8, j == 0, false, true);
+          scores(1, t.st, false, j + 2 == r.n0, true);
+          ph_p ^= 3u;
+          ++j;
+        }
+        const bool ends = j + 1 == r.n0;     // (slot 0 has a step in every pair)
+        if (ends) nx = open(k + 1);
+        const int nj = ends ? 0 : j + 1;
+        const bool now_a = j >= 0, now_b = now_a && j < r.n1, next_a = nx.more, next_b = nx.more && nj < nx.n1;
+        const bool last_tile_b = !r.dual && now_b && ends;      // slot 1 holds the piece's last tile
+        // one look at all that slot 0 needs; what is not there is waited for in turn
+        if (now_a) v_a = take();
+        if (next_a) k_a = take();
+        const uint32_t pa = ph_p & 1u, pb = (ph_p >> 1) & 1u;
+        // (a try that cannot succeed is not made: it holds the warp for microseconds)
+        bool all = false;
+        if (now_a && next_a) {
+          const bool r0 = ready(v_a), r1 = ready(k_a), r2 = mbar_try_wait(&p_full[0], pa);
+          all = r0 && r1 && r2;
+        }
+        if (!all) {
+          if (now_a) wait_tile(v_a);
+          if (next_a) wait_tile(k_a);
+          if (now_a) wait(&p_full[0], pa);
+        }
+        tc_fence_after();
+        if (now_a) {
+          weigh(0, v_a.st, ends && !last_tile_b ? r.tail : 8, j == 0, ends, !r.dual);
+          ph_p ^= 1u;
+        }
+        if (next_a) scores(0, k_a.st, nj == 0, nj + 1 == nx.n0, !nx.dual);
+        if (now_b) v_b = r.dual ? v_a : take();
+        if (next_b) k_b = nx.dual ? k_a : take();
+        all = false;
+        if (now_b && next_b) {
+          const bool s0 = ready(v_b), s1 = ready(k_b), s2 = mbar_try_wait(&p_full[1], pb);
+          all = s0 && s1 && s2;
+        }
+        if (!all) {
+          if (now_b) wait_tile(v_b);
+          if (next_b) wait_tile(k_b);
+          if (now_b) wait(&p_full[1], pb);
+        }
+        tc_fence_after();
+        if (now_b) {
+          weigh(1, v_b.st, ends ? r.tail : 8, j == 0, j + 1 == r.n1, true);
+          ph_p ^= 2u;
+        }
+        if (next_b) scores(1, k_b.st, nj == 0, nj + 1 == nx.n1, true);
+        j = nj;
+        if (ends) {
+          __syncwarp();
+          if (leader) mbar_arrive(&taken[k % PR]);
+          ++k;
+          r = nx;
+        }
+      }
+      if (!ok) set_status(a.status, 0x721u);
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ Q tiles, ends of the last V tiles
+      uint32_t n_q[2] = {0, 0}, n_land = 0;
+      int tiles = 0;                         // key tiles of the pieces so far
+      const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * D * 2);
+      bool ok = true, had = false, more = true;
+      for (int k = 0; (more || had) && ok; ++k) {
+        const Piece* p = ring + k % PR;
+        const Piece* before = ring + (k + PR - 1) % PR;
+        if (more) {
+          ok = __all_sync(0xffffffffu, wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1)));
+          if (!ok) break;
+          more = p->more != 0;
+        }
+        if (more) {
+          for (int sl = 0; sl < 2 && p->steps(sl) > 0; ++sl) {
+            if (n_q[sl] > 0) ok = ok && wait_for(&q_empty[sl], (n_q[sl] - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ++n_q[sl];
+            if (lane == 0) {
+              uint8_t* dst = smem + OFF_Q + sl * TILE;
+              const int row = p->row0 + (p->dual ? sl * a.tpt : 0);
+              mbar_arrive_expect_tx(&q_full[sl], q_bytes);
+              tma_load_3d(dst, &tmQ, &q_full[sl], 0, p->h * a.G, row);
+              tma_load_3d(dst + HALF, &tmQ, &q_full[sl], 64, p->h * a.G, row);
+            }
+          }
+          if (!ok) break;
+        }
+        // the piece before: rows of its last V tile from the sequence's last key to the next multiple of 16
+        if (had) {
+          if (before->tail()) {
+            // loads before that tile: every K and V before it, its own K, and the first K of the next piece
+            // if it came before slot 1's V
+            const int st = (2 * (tiles - 1) + 1 + (!before->dual && !(before->tiles() & 1) && more ? 1 : 0)) % ST;
+            ok = wait_for(&land[st], (n_land >> st) & 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            n_land ^= 1u << st;
+            uint8_t* vt = smem + OFF_RING + st * TILE;
+            const int r0 = before->keys() - (before->nt - 1) * KT, r1 = (r0 + 15) & ~15;
+            for (int r = r0 + (lane >> 4); r < r1; r += 2) {
+              const int ch = lane & 15;
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * HALF + sw128_off(r, (ch & 7) * 8)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&taken[(k + PR - 1) % PR]);
+        }
+        had = more;
+        if (more) tiles += p->tiles();
+      }
+      if (!ok) set_status(a.status, 0x731u);
+      if (!ok && lane == 0)                  // gave up: see the Q copies land before leaving
+        for (int sl = 0; sl < 2; ++sl)
+          if (n_q[sl] > 0) wait_for(&q_full[sl], (n_q[sl] - 1) & 1);
     }
-    if (!ok) set_status(a.status, 0x731u);
-    if (!ok && lane == 0)                  // gave up: see the Q copies land before leaving
-      for (int sl = 0; sl < 2; ++sl)
-        if (n_q[sl] > 0) wait_for(&q_full[sl], (n_q[sl] - 1) & 1);
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     // ------------------------------------------------------------ softmax and epilogue of slot sl
@@ -1110,9 +1121,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           tmem_st_wait();
         }
         // Weights relative to the row's reference, not to its maximum: any reference within 2^20 above and 2^60
-        // below the maximum gives the same quotients (bf16 and fp32 have exponents to spare), so nothing
-        // waits for a maximum.  The tile's sum tells when the reference is out of that range (or the first keys
-        // in sight are); then the maximum is found and taken, O rescaled, and the weights formed again.
+        // below the maximum gives the same quotients (bf16 and fp32 have exponents to spare, with values up to
+        // 1e25), so nothing waits for a maximum.  The tile's sum tells when the reference is out of that range
+        // (or the first keys in sight are); then the maximum is found and taken, O rescaled, and the weights
+        // formed again.
         uint32_t pk[64];
         float tile_sum;
         for (bool again = false;; again = true) {

@@ -4,6 +4,8 @@
 #include "common.cuh"
 #include "internal.h"
 
+#include <climits>
+
 namespace spec {
 namespace {
 
@@ -15,7 +17,7 @@ constexpr int PAGE = 128;
 // and what is left, at most an eighth of a turn, is exact to 2^-33 turns before its one rounding to fp32.  There
 // the Taylor series of sin(pi x) and cos(pi x) on |x| <= 1/4 (terms to (pi x)^9 and (pi x)^10: the next are below
 // 2e-9) take 11 multiply-adds; sincospif, which has the whole line to care for, made the 16000-row table
-// 7.6 us instead of 4.5.  No fp64 instruction: the chip has few of them.
+// 7.6 us instead of 5.9.  No fp64 instruction: the chip has few of them.
 __device__ __forceinline__ float2 cos_sin_turns(unsigned long long u) {
   const unsigned hi = (unsigned)(u >> 32);
   const unsigned quarter = (hi + (1u << 29)) >> 30;                 // 0..4, 4 = 0
@@ -56,26 +58,46 @@ rope_table_axes_kernel(const int32_t* __restrict__ pos, int ldpos, int M, int ha
   for (int r = r0; r < r1; ++r) cs[(size_t)r * half + i] = cos_sin_turns((unsigned long long)(long long)p[r] * turn);
 }
 
-// The last sequence with cu_rows[b] <= r, -1 if none: 32 candidates at a time, by a whole warp.
-__device__ __forceinline__ int sequence_of(int r, const int32_t* __restrict__ cu_rows, int B, int lane) {
-  int lo = 0, n = B;
+// The last sequence with cu_rows[b] <= r, 32 candidates at a time by a whole warp; its lengths come with the last
+// 32, so that they cost no load of their own after it.
+struct Place {
+  int b, c0, c1, ctx;                                   // b -1: r is before the first
+};
+__device__ __forceinline__ Place place_of(int r, const KvAppendArgs& a, int lane) {
+  int lo = 0, n = a.B;
   while (true) {
     const int step = (n + 31) >> 5, b = lo + lane * step;
-    const unsigned votes = __ballot_sync(0xffffffffu, b < lo + n && cu_rows[b] <= r);
-    if (votes == 0) return -1;                          // (only before the first)
+    const bool in = b < lo + n, last = step == 1;
+    int c0 = INT_MAX, c1 = 0, ctx = 0;
+    if (in) {
+      c0 = a.cu_rows[b];
+      if (last) {
+        c1 = a.cu_rows[b + 1];
+        ctx = a.ctx_len[b];
+      }
+    }
+    const unsigned votes = __ballot_sync(0xffffffffu, in && c0 <= r);
+    if (votes == 0) return Place{-1, 0, 0, 0};          // (only before the first)
     const int k = 31 - __clz(votes);
-    if (step == 1) return lo + k;
+    if (last)
+      return Place{lo + k, __shfl_sync(0xffffffffu, c0, k), __shfl_sync(0xffffffffu, c1, k),
+                   __shfl_sync(0xffffffffu, ctx, k)};
     n = min(step, n - k * step);
     lo += k * step;
   }
 }
 
-// One CTA per row.  A thread moves pairs of 16-byte chunks (dims i0 .. and 64 + i0 ..) of heads 16 apart, so its
-// eight angles stay in registers; up to UNITS pairs are loaded before the row's place in the cache is known,
-// which takes three dependent loads.  Bound by HBM: 8192 rows of 32 + 2 x 8 heads, 206 MB, in 33.4 us (6.2 TB/s);
-// 24 sequences of 1 to 999 rows, 81 MB, in 15.9 us with a binary search and a unit at a time.
-constexpr int UNITS = 4;
-__global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
+// One CTA per row.  A thread moves pairs of 16-byte chunks (dims i0 .. and 64 + i0 ..) of heads 4 WARPS apart, so
+// its eight angles stay in registers; up to UNITS pairs are loaded before the row's place in the cache is known,
+// which takes two dependent loads.  Bound by HBM: 8192 rows of 32 + 2 x 8 heads, 206 MB, take 32.9 us (6.3 TB/s),
+// 24 sequences of 1 to 999 rows, 81 MB, 14.3 us.
+// Two shapes.  Few rows: a row's whole traffic in flight at once, 4 warps and up to 4 pairs (8 rows 2.5 us, 1000 rows
+// 4.6; the other shape 3.3 and 5.3).  Many rows: CTAs that are small enough for 16 and more to share an SM, so that
+// some move data while others look their place up (8192 rows 32.9 us, the 24 sequences 14.3; the other shape
+// 33.8 and 17.3).  The two meet at 10 rows per SM (1500 rows: 8.4 us both).
+template <int WARPS, int UNITS>
+__global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArgs a) {
+  constexpr int STEP = 4 * WARPS;                       // heads between a thread's pairs
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, tid = threadIdx.x, i0 = (tid & 7) * 8;
@@ -85,11 +107,11 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) t[k] = *(reinterpret_cast<const float4*>(a.cs + (size_t)r * 64 + i0) + k);
   int b = -2, page = 0, p = 0;
-  for (int h0 = tid >> 3; h0 < heads || b == -2; h0 += 16 * UNITS) {
+  for (int h0 = tid >> 3; h0 < heads || b == -2; h0 += STEP * UNITS) {
     uint4 x[UNITS], y[UNITS];
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
-      const int hd = h0 + 16 * k;
+      const int hd = h0 + STEP * k;
       if (hd >= heads) continue;
       const uint16_t* src;
       if (hd < a.Hq) src = a.Q + (size_t)r * a.ldq + (size_t)hd * D;
@@ -99,15 +121,14 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
       y[k] = *reinterpret_cast<const uint4*>(src + 64 + i0);
     }
     if (b == -2) {                                      // the row's sequence, position and page
-      b = sequence_of(r, a.cu_rows, a.B, tid & 31);
-      if (b < 0) return;                                // padding
-      const int c0 = a.cu_rows[b], c1 = a.cu_rows[b + 1], ctx = a.ctx_len[b];
-      if (r >= c1) return;                              // padding
-      if (c0 < 0 || c1 > a.M || ctx < 0 || (long long)ctx + (c1 - c0) > (long long)a.max_pages * PAGE) {
+      const Place at = place_of(r, a, tid & 31);
+      b = at.b;
+      if (b < 0 || r >= at.c1) return;                  // padding
+      if (at.c0 < 0 || at.c1 > a.M || at.ctx < 0 || (long long)at.ctx + (at.c1 - at.c0) > (long long)a.max_pages * PAGE) {
         if (tid == 0) set_status(a.status, 0x6F1u);
         return;
       }
-      p = ctx + (r - c0);
+      p = at.ctx + (r - at.c0);
       page = a.block_table[(size_t)b * a.max_pages + p / PAGE];
       if (page < 0 || page >= a.num_pages) {
         if (tid == 0) set_status(a.status, 0x6F2u);
@@ -116,7 +137,7 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
-      const int hd = h0 + 16 * k;
+      const int hd = h0 + STEP * k;
       if (hd >= heads) continue;
       const bool is_v = hd >= a.Hq + a.Hkv;
       uint16_t* dst;
@@ -156,7 +177,9 @@ cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int hal
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_k(kv_append_kernel, dim3(a.M), dim3(128), 0, s, a);
+  const bool many = a.M > 10 * 152;
+  cudaError_t e = many ? launch_k(kv_append_kernel<2, 2>, dim3(a.M), dim3(64), 0, s, a)
+                       : launch_k(kv_append_kernel<4, 4>, dim3(a.M), dim3(128), 0, s, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

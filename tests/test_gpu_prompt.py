@@ -143,6 +143,7 @@ def test_table_axes_equals_plain_table_on_text(lib):
 APPEND = [
     ([1], [0], 32, 8), ([1, 1, 1], [127, 128, 300], 32, 8), ([300, 0, 1, 129], [100, 50, 255, 0], 16, 8),
     ([40], [88], 5, 1), ([2, 3], [0, 126], 28, 4), ([0, 0, 7], [0, 0, 121], 3, 3), ([5] * 40, list(range(100, 140)), 8, 2),
+    ([900, 0, 1, 640], [100, 5, 300, 0], 28, 4), ([1, 1600], [7, 50], 5, 1),
 ]
 
 
@@ -413,6 +414,37 @@ def test_binding_refuses_wrong_tensors(lib):
         lib.spec_kv_append_paged(q[:, :2 * D], q[:, :2 * D], cu, ctx, kp, vp, table, Q=q)     # no table
     with pytest.raises(ValueError):
         lib.spec_rope_table_axes(torch.zeros((2, 3), dtype=torch.int32, device="cuda"), [64], 128)
+
+
+@pytest.mark.parametrize("falling", [True, False])
+def test_attention_scores_far_below_zero(lib, falling):
+    """Every score far below 0 (no weight near 1 until the row's reference is taken), falling or rising from tile to
+    tile; rows of one item that see a tile that others do not."""
+    c = Case(60, [90, 4, 1], [400, 126, 3000], 8, 2)
+    for b in range(3):
+        for t in range(c.need[b]):
+            k = -4.0 * (t + 1 if falling else c.need[b] - t)
+            c.kp[:, c.table[b, t]] = synth.f32_to_bf16_bits(np.full(1, k, np.float32))[0]
+    c.q[:] = synth.f32_to_bf16_bits(np.full(1, 1.0, np.float32))[0]
+    check_attention(lib, c, f"falling {falling}")
+
+
+@pytest.mark.parametrize("size", [1e25, 1e-15])
+def test_attention_values_far_from_one(lib, size):
+    c = Case(61, [130, 2], [300, 2000], 8, 2, q_std=6.0)
+    c.vp = synth.f32_to_bf16_bits((obf.decode(c.vp) * size).astype(np.float32))
+    check_attention(lib, c, f"values of {size}")
+
+
+@pytest.mark.parametrize("grid", [1, 3, 37, 600])
+def test_attention_grids(lib, grid):
+    """Fewer and more CTAs than the chip holds: whole items, items in hundreds of pieces, sharers that run after
+    one another."""
+    lib.spec_set_option("persistent_grid", grid)
+    try:
+        check_attention(lib, Case(62, [300, 1, 0, 7, 61], [0, 4000, 9, 130, 9000], 8, 2, poison=True), f"grid {grid}")
+    finally:
+        lib.spec_set_option("persistent_grid", 0)
 
 
 # --------------------------------------------------------------------------- together
