@@ -14,21 +14,23 @@
 // row tile (few rows: decode steps, ends of prompts) gives the slots its key tiles in turn, each
 // with its own reference, sum and O, joined at the end.
 //
-// Work.  The key tiles of all items in a row (sequence, kv head, item) are cut into equal shares by cost, one
-// per CTA; every CTA works out the same cuts from the lengths on the device (closed form per
-// sequence, so one graph serves any lengths).  Where a cut falls into an item its pieces go to the
+// Work.  Where the items come out about even (prompts), whole items, the longest first, are dealt to the CTAs in rows
+// that run forth and back.  Otherwise the key tiles of all items in a row (sequence, kv head, item) are cut into
+// equal shares by cost, one per CTA; without that a prompt's chunk over a long cache would leave a
+// wave half empty, and a few rows all but a few CTAs idle.  Where a cut falls into an item its pieces go to the
 // workspace as unnormalised O, reference and sum; the warps of the item's CTAs that are done when the last
 // piece arrives join it together, in CTA order whoever does it (a second kernel for this took 5 to 8 us
-// longer).  Without these shares a prompt's last items would leave most of the chip idle, and a few rows over
-// a long cache all but a few CTAs.
+// longer).  Every CTA works all of this out from the lengths on the device (closed form per
+// sequence), so one graph serves any lengths.
 //
 // Bound.  With many rows, the tensor cores: a key tile's four products of 128^3 take 2048 of their cycles, in which
 // the softmax warps have to form 256 x 128 weights, which is why nothing else is in their way: no
 // maximum per tile (the reference below), two fp32 operations per instruction, a row per thread.  A prompt of 8192 rows
-// (32 + 2 x 8 heads) takes 333 us = 1650 TFLOP/s, 2048 rows at 30000 keys 640 us.  With few rows, HBM: 61 rows at
-// 131000 keys 98 us = 5.5 TB/s.  In between and below, what a call costs whatever its size: 4 to 5 us
-// to the first product (lengths, cuts, page table, first tiles), 5 to 7 us to join shared items, which one token
-// of 4 sequences (15 us) and a chunk of 512 at 7680 keys (56 us) pay.
+// (32 + 2 x 8 heads) takes 320 us = 1715 TFLOP/s, 2048 rows at 30000 keys 640 us = 1630.  With few rows, HBM: 61 rows
+// at 131000 keys 99 us = 5.4 TB/s, 16 x 32 rows at 4000 keys 47 us = 5.8 TB/s.  In between and below, what a
+// call costs whatever its size: 4 to 5 us to the first product (lengths, the CTA's pieces, page table, first
+// tiles) and, where items are shared, about 8 us to join them; one token of 4 sequences (12.9 us) pays the first,
+// a chunk of 512 at 7680 keys (55 us) both.
 //
 // Roles (12 warps): 0-3 and 4-7 softmax and epilogue of slot 0 and 1 (thread = TMEM lane = row); 8 loads K
 // and V tiles by TMA into one ring of 5; 9 issues the MMAs; 10 loads the Q tiles and zeroes the rows of
@@ -38,6 +40,8 @@
 // none of them waits for the lengths or keeps a walk in registers.
 #include "common.cuh"
 #include "internal.h"
+
+#include <climits>
 
 namespace spec {
 namespace {
@@ -63,8 +67,9 @@ static_assert(SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
-// Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys.
-constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 320;
+// Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys; the time that
+// joining shared items takes at the end, in keys of two row tiles.
+constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 320, JOIN_KEYS = 1280;
 
 // 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one asm
 __device__ __forceinline__ void tmem_ld_cols128(uint32_t taddr, uint32_t* r) {
@@ -282,6 +287,13 @@ __device__ __forceinline__ Cut cut_of(const ChunkAttnArgs& a, const Found& f, in
   return c;
 }
 
+// Items of one kv head of a sequence that see x keys or more (x >= 1; keys = ctx + rows, 0 without rows).
+__device__ __forceinline__ int items_from(const ChunkAttnArgs& a, int rows, int keys, int x) {
+  if (x > keys) return 0;
+  const int last = div_t(a, rows - 1);
+  return last + 1 - min(div_t(a, max(x - 1 - (keys - rows), 0)), last);
+}
+
 // A CTA's consecutive key tiles of one item, as posted.
 struct Piece {
   int b, h, q;
@@ -417,71 +429,137 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     if (warp == 11) {
       // ------------------------------------------------------------ pieces
-      // The sequences' costs, a run of them per lane; then the two sequences that this CTA's share starts and ends
-      // in, found by the lanes that have them.
+      // The sequences, a run of them per lane.
       const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
       long long own = 0;
       bool bad = false;
-  #pragma unroll 2
+      Seq mine{0, 0, 0};
+#pragma unroll 2
       for (int b = b0; b < b1; ++b) {
         bool wrong;
-        const Seq s = seq_of(a, b, &wrong);
+        mine = seq_of(a, b, &wrong);
         bad |= wrong;
-        own += head_cost(a, s) * a.Hkv;
+        own += head_cost(a, mine) * a.Hkv;
       }
       if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
-      long long before = own;
-  #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
+      // Where they come out about even, whole items, the longest first, dealt to the CTAs in rows that run forth and
+      // back: nothing is left to join.  (8 prompts of 100 to 1900 rows 42.0 us, cut 52.5; one of 2048 rows 30.4,
+      // cut 42.6; of 8192 rows 320, cut 335; 16 x 32 rows at 4000 keys 47.2, cut 53.4.)  What the deal leaves uneven
+      // is about the longest item of the last row times the share of the CTAs that the row leaves out: the rule is
+      // that this costs less than joining.  It decided for the faster side at each of 20 batches but within 1 us.
+      const int T = 2 * a.tpt, grid = (int)gridDim.x;
+      const int keys = mine.rows > 0 ? mine.ctx + mine.rows : 0;
+      const int items = run > 1 ? 0 : __reduce_add_sync(0xffffffffu, items_from(a, mine.rows, keys, 1)) * a.Hkv;
+      bool whole = false;
+      if (items > 0) {
+        const int before = (items - 1) / grid * grid, out = grid - (items - before);
+        const int x = out == 0 ? INT_MAX : JOIN_KEYS * grid / out - ITEM_KEYS + 1;
+        whole = __reduce_add_sync(0xffffffffu, items_from(a, mine.rows, keys, x)) * a.Hkv <= before;
       }
-      const long long total = __shfl_sync(0xffffffffu, before, 31);
-      before -= own;
-      Found f{0, 0, a.B, Seq{0, 0, 0}};      // lanes 0-15: of the start, 16-31: of the end
-  #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const long long x = share_start(a, total, blockIdx.x + k);
-        const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + own);
-        if (owner == 0) continue;            // (the end of everything, or nothing at all)
-        Found g{0, before, b0, Seq{0, 0, 0}};
-        if (x >= before && x < before + own)
-          for (;; ++g.b) {
-            g.s = seq_of(a, g.b);
-            const long long c = head_cost(a, g.s) * a.Hkv;
-            if (x < g.before + c) break;
-            g.before += c;
-          }
-        const int from = __ffs(owner) - 1;
-        g.before = __shfl_sync(0xffffffffu, g.before, from);
-        g.b = __shfl_sync(0xffffffffu, g.b, from);
-        g.s.r0 = __shfl_sync(0xffffffffu, g.s.r0, from);
-        g.s.rows = __shfl_sync(0xffffffffu, g.s.rows, from);
-        g.s.ctx = __shfl_sync(0xffffffffu, g.s.ctx, from);
-        g.x = x - g.before;
-        if ((lane >> 4) == k) f = g;
-      }
-      const Cut mine = cut_of(a, f, lane);
-      Cut end;
-      end.start = __shfl_sync(0xffffffffu, mine.start, 16);
-      end.b = __shfl_sync(0xffffffffu, mine.b, 16);
-      end.h = __shfl_sync(0xffffffffu, mine.h, 16);
-      end.q = __shfl_sync(0xffffffffu, mine.q, 16);
-      end.t = __shfl_sync(0xffffffffu, mine.t, 16);
-      if (lane == 0) {
+      if (whole) {
         Walk w;
-        w.first(a, mine, end);
-        *s_first = w.p;
-        *s_total = total;
+        int x = 1, n = (int)__reduce_max_sync(0xffffffffu, (unsigned)keys);
         for (int k = 0;; ++k) {
-          if (k >= PR && !wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1))) {
-            set_status(a.status, 0x701u);
+          const int at = k * grid + ((k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+          const bool more = at < items;
+          if (more) {
+            // the most keys that more than `rank` items see, 32 candidates at a time
+            const int rank = at / a.Hkv;
+            while (n > 1) {
+              const int step = (n + 31) >> 5, c = x + lane * step;
+              int count = 0;
+              for (int b = 0; b < a.B; ++b)
+                count += items_from(a, __shfl_sync(0xffffffffu, mine.rows, b), __shfl_sync(0xffffffffu, keys, b), c);
+              const int i = 31 - __clz(__ballot_sync(0xffffffffu, c < x + n && count > rank));   // (the first always)
+              n = min(step, n - i * step);
+              x += i * step;
+            }
+            // of the items that see just as many, one per sequence, the one whose turn it is
+            const int from = items_from(a, mine.rows, keys, x), above = items_from(a, mine.rows, keys, x + 1);
+            const unsigned same = __ballot_sync(0xffffffffu, from > above);
+            const int turn = rank - __reduce_add_sync(0xffffffffu, above);
+            const bool me = from > above && __popc(same & ((1u << lane) - 1u)) == turn;
+            const int b = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+            w.p.b = b;
+            w.p.h = at - rank * a.Hkv;
+            w.p.q = __shfl_sync(0xffffffffu, items_from(a, mine.rows, keys, 1) - from, b);
+            w.s.r0 = __shfl_sync(0xffffffffu, mine.r0, b);
+            w.s.rows = __shfl_sync(0xffffffffu, mine.rows, b);
+            w.s.ctx = __shfl_sync(0xffffffffu, mine.ctx, b);
+            w.item(T);
+            n = x;                         // (the next item sees as many at most)
+            x = 1;
+          }
+          w.p.t0 = 0;
+          w.p.t1 = w.p.nt;
+          w.p.more = more;
+          const bool ok = k < PR || wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1));
+          if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) set_status(a.status, 0x701u);
             break;
           }
-          ring[k % PR] = w.p;
-          mbar_arrive(&posted[k % PR]);
-          if (!w.p.more) break;
-          w.next(a, end);
+          if (lane == 0) {
+            ring[k % PR] = w.p;
+            mbar_arrive(&posted[k % PR]);
+          }
+          __syncwarp();
+          if (!more) break;
+        }
+      } else {
+        // Equal shares by cost: the two sequences that this CTA's starts and ends in, found by the lanes that have them.
+        long long before = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += v;
+        }
+        const long long total = __shfl_sync(0xffffffffu, before, 31);
+        before -= own;
+        Found f{0, 0, a.B, Seq{0, 0, 0}};      // lanes 0-15: of the start, 16-31: of the end
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const long long x = share_start(a, total, blockIdx.x + k);
+          const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + own);
+          if (owner == 0) continue;            // (the end of everything, or nothing at all)
+          Found g{0, before, b0, Seq{0, 0, 0}};
+          if (x >= before && x < before + own)
+            for (;; ++g.b) {
+              g.s = seq_of(a, g.b);
+              const long long c = head_cost(a, g.s) * a.Hkv;
+              if (x < g.before + c) break;
+              g.before += c;
+            }
+          const int from = __ffs(owner) - 1;
+          g.before = __shfl_sync(0xffffffffu, g.before, from);
+          g.b = __shfl_sync(0xffffffffu, g.b, from);
+          g.s.r0 = __shfl_sync(0xffffffffu, g.s.r0, from);
+          g.s.rows = __shfl_sync(0xffffffffu, g.s.rows, from);
+          g.s.ctx = __shfl_sync(0xffffffffu, g.s.ctx, from);
+          g.x = x - g.before;
+          if ((lane >> 4) == k) f = g;
+        }
+        const Cut start = cut_of(a, f, lane);
+        Cut end;
+        end.start = __shfl_sync(0xffffffffu, start.start, 16);
+        end.b = __shfl_sync(0xffffffffu, start.b, 16);
+        end.h = __shfl_sync(0xffffffffu, start.h, 16);
+        end.q = __shfl_sync(0xffffffffu, start.q, 16);
+        end.t = __shfl_sync(0xffffffffu, start.t, 16);
+        if (lane == 0) {
+          Walk w;
+          w.first(a, start, end);
+          *s_first = w.p;
+          *s_total = total;
+          for (int k = 0;; ++k) {
+            if (k >= PR && !wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1))) {
+              set_status(a.status, 0x701u);
+              break;
+            }
+            ring[k % PR] = w.p;
+            mbar_arrive(&posted[k % PR]);
+            if (!w.p.more) break;
+            w.next(a, end);
+          }
         }
       }
       __syncwarp();
@@ -551,7 +629,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           pk.base = -1;
         }
         const int nj = ends ? 0 : j + 1;
-  #pragma unroll 1
+#pragma unroll 1
         for (int q = 0; q < 4 && ok; ++q) {
           const int sl = q >> 1;
           const bool is_v = !(q & 1);
@@ -620,7 +698,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
         if (leader) {
           const uint64_t qd = q0 + sl * (TILE >> 4), kd = k0 + (uint32_t)(kst * (TILE >> 4));
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < 8; ++kk) {   // (descriptor addresses count 16 bytes)
             const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
             umma_bf16(sl * KT, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
@@ -636,7 +714,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           const uint64_t vd = v0 + (uint32_t)(vst * (TILE >> 4));
           constexpr uint32_t t_o = 2 * KT;
           umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, first ? 0u : 1u);
-  #pragma unroll
+#pragma unroll
           for (int kk = 1; kk < 8; ++kk)
             umma_bf16_ts_if(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, kk < steps);
           if (release) umma_commit(&empty[vst]);

@@ -436,6 +436,20 @@ def test_attention_values_far_from_one(lib, size):
     check_attention(lib, c, f"values of {size}")
 
 
+@pytest.mark.parametrize("rows,ctx,Hq,Hkv", [
+    ([500] * 8, [0] * 8, 8, 2), ([130, 0] * 16, [(37 * b) % 500 for b in range(32)], 4, 4), ([2048], [0], 16, 8),
+    ([1, 600, 257, 256, 255], [255, 0, 128, 127, 130], 28, 4), ([700], [1], 16, 1)])
+def test_attention_many_items(lib, rows, ctx, Hq, Hkv):
+    """Prompts whose items outnumber the CTAs, with equal and unequal lengths; and on a few CTAs."""
+    c = Case(63, rows, ctx, Hq, Hkv, poison=True, pad=2)
+    check_attention(lib, c, "many items")
+    lib.spec_set_option("persistent_grid", 5)
+    try:
+        check_attention(lib, c, "many items on 5 CTAs")
+    finally:
+        lib.spec_set_option("persistent_grid", 0)
+
+
 @pytest.mark.parametrize("grid", [1, 3, 37, 600])
 def test_attention_grids(lib, grid):
     """Fewer and more CTAs than the chip holds: whole items, items in hundreds of pieces, sharers that run after
