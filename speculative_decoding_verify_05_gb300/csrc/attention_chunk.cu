@@ -69,7 +69,7 @@ constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys; the time that
 // joining shared items takes at the end, in keys of two row tiles.
-constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 320, JOIN_KEYS = 1280;
+constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 384, JOIN_KEYS = 1280;
 
 // 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one asm
 __device__ __forceinline__ void tmem_ld_cols128(uint32_t taddr, uint32_t* r) {
