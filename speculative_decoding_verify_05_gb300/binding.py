@@ -136,9 +136,10 @@ def _stream(stream):
 
 def _rowmajor(t: torch.Tensor, name: str) -> int:
     """Leading dimension of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.stride(1) != 1:
+    strides = t.stride()
+    if len(strides) != 2 or strides[1] != 1:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    return t.stride(0)
+    return strides[0]
 
 
 def _need(t, dtype, name):

@@ -881,7 +881,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const uint32_t t_s = tmem + (uint32_t)sl * KT + lanes, t_o = tmem + 2 * KT + (uint32_t)sl * D + lanes;
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     const bool row_used = row_tok < a.tpt;
-    const float scale = a.scale_log2;
     uint32_t n_s = 0, n_pair = 0, ph_o = 0;     // (ph_o: a phase bit per slot)
     bool ok = true;
     // A warp's rows of a piece, at its end: all dims of its slot's row tile (dual), or its slot's half of the dims
@@ -1177,6 +1176,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const int pos = p.pos + min(x * a.tpt + row_tok, p.tok - 1);      // the row sees keys 0 .. pos
       const bool live = row_used && x * a.tpt + row_tok < p.tok;        // (the other rows hold anything)
       const int pos_lo = __shfl_sync(0xffffffffu, pos, 0), pos_hi = __shfl_sync(0xffffffffu, pos, 31);
+      // (a sequence's first row: one key, whose weight is then 1, which bf16 has exactly, whatever the score)
+      const float scale = pos == 0 ? 1e-30f : a.scale_log2;
       float ref = 0.f, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
         const int key0 = (t0 + (dual ? j : 2 * j + sl)) * KT;

@@ -429,6 +429,14 @@ def test_attention_scores_far_below_zero(lib, falling):
     check_attention(lib, c, f"falling {falling}")
 
 
+def test_attention_of_a_single_key_is_its_value(lib):
+    """First tokens: one weight, whatever the score (the weight enters the product as bf16, so it has to be 1)."""
+    c = Case(64, [1] * 9, [0] * 9, 8, 2, q_std=3.0)
+    got = bits_of(run_attention(lib, c)).reshape(9, 2, 4, D)
+    want = np.stack([c.vp[:, c.table[b, 0], 0] for b in range(9)])
+    assert np.array_equal(got, np.broadcast_to(want[:, :, None], got.shape))
+
+
 @pytest.mark.parametrize("size", [1e25, 1e-15])
 def test_attention_values_far_from_one(lib, size):
     c = Case(61, [130, 2], [300, 2000], 8, 2, q_std=6.0)
