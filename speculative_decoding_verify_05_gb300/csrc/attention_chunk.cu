@@ -316,7 +316,7 @@ struct Piece {
 };
 static_assert(OFF_RINGP + (PR + 1) * sizeof(Piece) + 8 <= OFF_ML && OFF_RINGP % 8 == 0, "posted pieces");
 
-// The walk over a CTA's pieces.
+// The walk over a CTA's pieces, by a whole warp.
 struct Walk {
   Piece p;
   Seq s;
@@ -339,27 +339,36 @@ struct Walk {
     p.more = p.t1 > p.t0;
   }
   // first piece of [c, e)
-  __device__ __forceinline__ void first(const ChunkAttnArgs& a, const Cut& c, const Cut& e) {
+  __device__ __forceinline__ void first(const ChunkAttnArgs& a, const Cut& c, const Cut& e, int lane) {
     p.more = 0;
     if (c.b >= a.B) return;
     p.b = c.b; p.h = c.h; p.q = c.q; p.t0 = c.t;
     s = c.s;
     item(2 * a.tpt);
     p.start = c.start;
-    if (p.t0 >= p.nt) next(a, e);
+    if (p.t0 >= p.nt) next(a, e, lane);
     else clip(e);
   }
-  __device__ __forceinline__ void next(const ChunkAttnArgs& a, const Cut& e) {
+  __device__ __forceinline__ void next(const ChunkAttnArgs& a, const Cut& e, int lane) {
     p.t0 = 0;
     p.more = 0;
     if (++p.q * 2 * a.tpt >= s.rows) {
       p.q = 0;
       if (++p.h == a.Hkv) {
         p.h = 0;
-        do {
-          if (++p.b >= a.B || p.b > e.b) return;
-          s = seq_of(a, p.b);
-        } while (s.rows == 0);
+        // the next sequence with rows, 32 candidates at a time (a padded batch may have hundreds without)
+        for (int from = p.b + 1;; from += 32) {
+          if (from >= a.B || from > e.b) return;
+          const Seq c = from + lane < a.B ? seq_of(a, from + lane) : Seq{0, 0, 0};
+          const unsigned has = __ballot_sync(0xffffffffu, c.rows > 0);
+          if (has == 0) continue;
+          const int k = __ffs(has) - 1;
+          p.b = from + k;
+          s.r0 = __shfl_sync(0xffffffffu, c.r0, k);
+          s.rows = __shfl_sync(0xffffffffu, c.rows, k);
+          s.ctx = __shfl_sync(0xffffffffu, c.ctx, k);
+          break;
+        }
       }
     }
     item(2 * a.tpt);
@@ -434,7 +443,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       long long own = 0;
       bool bad = false;
       Seq mine{0, 0, 0};
-#pragma unroll 2
+#pragma unroll 4
       for (int b = b0; b < b1; ++b) {
         bool wrong;
         mine = seq_of(a, b, &wrong);
@@ -456,6 +465,20 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const int x = out == 0 ? INT_MAX : JOIN_KEYS * grid / out - ITEM_KEYS + 1;
         whole = __reduce_add_sync(0xffffffffu, items_from(a, mine.rows, keys, x)) * a.Hkv <= before;
       }
+      // the k-th piece to the others; false after a wait that ran out
+      auto post = [&](int k, const Piece& p) {
+        const bool ok = k < PR || wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1));
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) set_status(a.status, 0x701u);
+          return false;
+        }
+        if (lane == 0) {
+          ring[k % PR] = p;
+          mbar_arrive(&posted[k % PR]);
+        }
+        __syncwarp();
+        return true;
+      };
       if (whole) {
         Walk w;
         int x = 1, n = (int)__reduce_max_sync(0xffffffffu, (unsigned)keys);
@@ -493,17 +516,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           w.p.t0 = 0;
           w.p.t1 = w.p.nt;
           w.p.more = more;
-          const bool ok = k < PR || wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1));
-          if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) set_status(a.status, 0x701u);
-            break;
-          }
-          if (lane == 0) {
-            ring[k % PR] = w.p;
-            mbar_arrive(&posted[k % PR]);
-          }
-          __syncwarp();
-          if (!more) break;
+          if (!post(k, w.p) || !more) break;
         }
       } else {
         // Equal shares by cost: the two sequences that this CTA's starts and ends in, found by the lanes that have them.
@@ -538,29 +551,27 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           g.x = x - g.before;
           if ((lane >> 4) == k) f = g;
         }
-        const Cut start = cut_of(a, f, lane);
-        Cut end;
-        end.start = __shfl_sync(0xffffffffu, start.start, 16);
-        end.b = __shfl_sync(0xffffffffu, start.b, 16);
-        end.h = __shfl_sync(0xffffffffu, start.h, 16);
-        end.q = __shfl_sync(0xffffffffu, start.q, 16);
-        end.t = __shfl_sync(0xffffffffu, start.t, 16);
+        const Cut cut = cut_of(a, f, lane);
+        auto lane_of = [&](int from) {
+          Cut c;
+          c.start = __shfl_sync(0xffffffffu, cut.start, from);
+          c.b = __shfl_sync(0xffffffffu, cut.b, from);
+          c.h = __shfl_sync(0xffffffffu, cut.h, from);
+          c.q = __shfl_sync(0xffffffffu, cut.q, from);
+          c.t = __shfl_sync(0xffffffffu, cut.t, from);
+          c.s.r0 = __shfl_sync(0xffffffffu, cut.s.r0, from);
+          c.s.rows = __shfl_sync(0xffffffffu, cut.s.rows, from);
+          c.s.ctx = __shfl_sync(0xffffffffu, cut.s.ctx, from);
+          return c;
+        };
+        const Cut start = lane_of(0), end = lane_of(16);
+        Walk w;
+        w.first(a, start, end, lane);
         if (lane == 0) {
-          Walk w;
-          w.first(a, start, end);
           *s_first = w.p;
           *s_total = total;
-          for (int k = 0;; ++k) {
-            if (k >= PR && !wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1))) {
-              set_status(a.status, 0x701u);
-              break;
-            }
-            ring[k % PR] = w.p;
-            mbar_arrive(&posted[k % PR]);
-            if (!w.p.more) break;
-            w.next(a, end);
-          }
         }
+        for (int k = 0; post(k, w.p) && w.p.more; ++k) w.next(a, end, lane);
       }
       __syncwarp();
     } else if (warp == 8) {

@@ -84,6 +84,41 @@ def test_prompt_then_verify(lib, L, fold, fused):
     assert abs(P.cpu().numpy().astype(np.float64) - oops.target_probs(lg, 1.0)).max() < STACK_PROB_BOUND
 
 
+def test_prefill_captured(lib):
+    """One graph of a chunk of up to 64 rows, replayed for the chunks of the prompts."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(1, 87)
+    lengths = [150, 41]
+    x_bits = [synth.normal_bf16_bits(89 + b, (lengths[b], dims.d), 1.0) for b in range(2)]
+    cache = Paged(dims, lengths)
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=64, max_rows=1, block_table=cache.table)
+    x0 = torch.zeros((64, dims.d), dtype=torch.bfloat16, device="cuda")
+    cu, ctx = dev(np.array([0, 0, 0], np.int32)), dev(np.zeros(2, np.int32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eng.prefill(x0, cu, ctx, temperature=1.0)            # (all rows padding)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        x, P = eng.prefill(x0, cu, ctx, temperature=1.0)
+    ref_x, ref_lg = whole(osw, od, x_bits, lengths)
+    for at, to in zip([(0, 0), (40, 20), (100, 20)], [(40, 20), (100, 20), (150, 34)]):
+        rows = [t - a for a, t in zip(at, to)]
+        cu.copy_(dev(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)))
+        ctx.copy_(dev(np.array(at, np.int32)))
+        x0[:sum(rows)] = bf16_dev(np.concatenate([xb[a:t] for xb, a, t in zip(x_bits, at, to)]))
+        graph.replay()
+        lib.spec_device_status()
+        got, probs = f64_of_bf16(x), P.cpu().numpy().astype(np.float64)
+        r0 = 0
+        for b in range(2):
+            assert_close_chain(got[r0:r0 + rows[b]], ref_x[b][at[b]:to[b]], 1, f"replayed chunk at {at}, sequence {b}")
+            r0 += rows[b]
+            if rows[b]:
+                assert abs(probs[b] - oops.target_probs(ref_lg[b][to[b] - 1:to[b]], 1.0)[0]).max() < STACK_PROB_BOUND
+
+
 def test_positions_of_several_axes(lib):
     """Text's positions on three axes are its one position; attention only sees differences, so positions that are
     all 5000 further on give the same rows."""

@@ -263,6 +263,15 @@ def test_attention_many_sequences(lib):
     check_attention(lib, Case(34, rows, ctx, 4, 1, poison=True), "700 sequences")
 
 
+def test_attention_padded_batch(lib):
+    """Hundreds of slots without rows between the sequences that have some."""
+    rows = [0] * 900
+    rows[3], rows[4], rows[500], rows[897] = 1, 70, 2, 1
+    ctx = [(11 * b) % 300 for b in range(900)]
+    ctx[3], ctx[897] = 2000, 1000
+    check_attention(lib, Case(65, rows, ctx, 8, 2, poison=True), "padded batch")
+
+
 def test_attention_all_sequences_empty(lib):
     check_attention(lib, Case(35, [0, 0], [5, 0], 4, 1, pad=4), "no rows")
 
