@@ -202,7 +202,7 @@ class Workspace:
     def args(self):
         if self.buf is None:
             return None, 0
-        return ctypes.c_void_p(self.buf.data_ptr()), self.buf.numel()
+        return self.buf.data_ptr(), self.buf.numel()
 
 
 def _ws_args(ws: Workspace | None, need: int, device):
@@ -523,7 +523,7 @@ _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 def _paged(cu_rows, ctx_len, Kpool, Vpool, block_table):
     """Checks the batch and cache arguments of a chunk call; returns (B, Hkv, num_pages, D, max_pages).
 
-    (A decode step's call costs as much host time as its kernel takes: one expression for what is right as
+    (A decode step's call costs more host time than its kernel takes: one expression for what is right as
     a rule, and the checks one by one only to name what is not.)"""
     if not (Kpool.dtype is _BF16 and Vpool.dtype is _BF16 and cu_rows.dtype is _I32 and ctx_len.dtype is _I32
             and block_table.dtype is _I32 and Kpool.is_cuda and Vpool.is_cuda and cu_rows.is_cuda and ctx_len.is_cuda
@@ -537,11 +537,22 @@ def _paged(cu_rows, ctx_len, Kpool, Vpool, block_table):
     pool = Kpool.shape
     if len(pool) != 4 or pool[2] != 128 or Vpool.shape != pool or not (Kpool.is_contiguous() and Vpool.is_contiguous()):
         raise ValueError("Kpool/Vpool must be contiguous [Hkv, num_pages, 128, D]")
+    Hkv, num_pages, _, D = pool
     table = block_table.shape
     B = cu_rows.numel() - 1
     if len(table) != 2 or table[0] != B or ctx_len.numel() != B:
         raise ValueError("cu_rows, ctx_len and block_table must be [B + 1], [B] and [B, max_pages]")
-    return B, pool[0], pool[1], pool[3], table[1]
+    return B, Hkv, num_pages, D, table[1]
+
+
+def _rows_bf16(t, name):
+    """Shape and leading dimension of a 2-D bf16 tensor whose rows are contiguous."""
+    if t.dtype is not _BF16 or not t.is_cuda:
+        _need(t, _BF16, name)
+    strides = t.stride()
+    if len(strides) != 2 or strides[1] != 1:
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    return t.shape, strides[0]
 
 
 def spec_kv_append_paged(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table, cs=None, Q=None, Qrot=None,
@@ -550,30 +561,27 @@ def spec_kv_append_paged(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table
     128, D] at positions ctx_len.., the keys rotated with the table cs [M, D/2, 2] (cs None: copied as
     they are); Q [M, Hq*D], if given, is rotated into Qrot (default: in place).  Returns Qrot."""
     B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table)
-    if not (Knew.dtype is _BF16 and Vnew.dtype is _BF16 and Knew.is_cuda and Vnew.is_cuda):
-        _need(Knew, _BF16, "Knew"); _need(Vnew, _BF16, "Vnew")
-    ldkv = _rowmajor(Knew, "Knew")
-    if Vnew.stride() != (ldkv, 1):
+    shape, ldkv = _rows_bf16(Knew, "Knew")
+    vshape, ldv = _rows_bf16(Vnew, "Vnew")
+    if ldv != ldkv:
         raise ValueError("Knew and Vnew must share a leading dimension")
-    M, width = shape = Knew.shape
-    if width != Hkv * D or Vnew.shape != shape:
+    M, width = shape
+    if width != Hkv * D or vshape != shape:
         raise ValueError("Knew and Vnew must be [M, Hkv*D]")
     if cs is not None:
-        _need(cs, torch.float32, "cs")
+        if cs.dtype is not _F32 or not cs.is_cuda:
+            _need(cs, _F32, "cs")
         table = cs.shape
         if len(table) != 3 or table[0] < M or table[1] != D // 2 or table[2] != 2 or not cs.is_contiguous():
             raise ValueError("cs must be a contiguous [M, D/2, 2] table with an entry per row")
     Hq = ldq = ldqr = 0
     if Q is not None:
-        _need(Q, torch.bfloat16, "Q")
-        ldq = ldqr = _rowmajor(Q, "Q")
-        shape = Q.shape
+        shape, ldq = _rows_bf16(Q, "Q")
         if Qrot is None:
-            Qrot = Q
+            Qrot, ldqr = Q, ldq
         else:
-            _need(Qrot, torch.bfloat16, "Qrot")
-            ldqr = _rowmajor(Qrot, "Qrot")
-            if Qrot.shape != shape:
+            rshape, ldqr = _rows_bf16(Qrot, "Qrot")
+            if rshape != shape:
                 raise ValueError("Q and Qrot must be [M, Hq*D]")
         if shape[0] != M or shape[1] % D:
             raise ValueError("Q and Qrot must be [M, Hq*D]")
@@ -581,8 +589,9 @@ def spec_kv_append_paged(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table
     elif Qrot is not None:
         raise ValueError("Qrot without Q")
     _check(_lib.spec_kv_append_paged(
-        _p(Q), ldq, _p(Qrot), ldqr, _p(Knew), _p(Vnew), ldkv, _p(cs), _p(cu_rows), _p(ctx_len), B, M, _p(Kpool),
-        _p(Vpool), num_pages, _p(block_table), max_pages, Hq, Hkv, D, _stream(stream)), True)
+        _p(Q), ldq, _p(Qrot), ldqr, Knew.data_ptr(), Vnew.data_ptr(), ldkv, _p(cs), cu_rows.data_ptr(),
+        ctx_len.data_ptr(), B, M, Kpool.data_ptr(), Vpool.data_ptr(), num_pages, block_table.data_ptr(), max_pages, Hq,
+        Hkv, D, _stream(stream)), True)
     return Qrot
 
 
@@ -595,23 +604,23 @@ def spec_chunk_attention_paged(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, s
     """Attention of a chunk of new tokens over the paged cache that already holds their keys: row j of
     sequence b (Q [M, Hq*D]) attends keys 0 .. ctx_len[b] + j; returns O [M, Hq*D]."""
     B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table)
-    _need(Q, torch.bfloat16, "Q")
-    ldq = _rowmajor(Q, "Q")
-    M, width = shape = Q.shape
+    shape, ldq = _rows_bf16(Q, "Q")
+    M, width = shape
     if width % D:
         raise ValueError("Q must be [M, Hq*D]")
     if O is None:
-        O = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
-    _need(O, torch.bfloat16, "O")
-    if O.shape != shape:
-        raise ValueError("O must be [M, Hq*D]")
+        O, ldo = torch.empty(shape, dtype=_BF16, device=Q.device), width
+    else:
+        oshape, ldo = _rows_bf16(O, "O")
+        if oshape != shape:
+            raise ValueError("O must be [M, Hq*D]")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     Hq = width // D
     wp, wn = _ws_args(ws, spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages), Q.device)
     _check(_lib.spec_chunk_attention_paged(
-        _p(Q), ldq, _p(cu_rows), _p(ctx_len), B, M, _p(Kpool), _p(Vpool), num_pages, _p(block_table), max_pages, Hq,
-        Hkv, D, float(scale), _p(O), _rowmajor(O, "O"), wp, wn, _stream(stream)), True)
+        Q.data_ptr(), ldq, cu_rows.data_ptr(), ctx_len.data_ptr(), B, M, Kpool.data_ptr(), Vpool.data_ptr(), num_pages,
+        block_table.data_ptr(), max_pages, Hq, Hkv, D, scale, O.data_ptr(), ldo, wp, wn, _stream(stream)), True)
     return O
 
 
