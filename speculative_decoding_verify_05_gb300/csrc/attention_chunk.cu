@@ -455,7 +455,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       // back: nothing is left to join.  (8 prompts of 100 to 1900 rows 42.0 us, cut 52.5; one of 2048 rows 30.4,
       // cut 42.6; of 8192 rows 320, cut 335; 16 x 32 rows at 4000 keys 47.2, cut 53.4.)  What the deal leaves uneven
       // is about the longest item of the last row times the share of the CTAs that the row leaves out: the rule is
-      // that this costs less than joining.  It decided for the faster side at each of 20 batches but within 1 us.
+      // that this costs less than joining.  Over 20 batches it took the faster side, or one within 1 us of it.
       const int T = 2 * a.tpt, grid = (int)gridDim.x;
       const int keys = mine.rows > 0 ? mine.ctx + mine.rows : 0;
       const int items = run > 1 ? 0 : __reduce_add_sync(0xffffffffu, items_from(a, mine.rows, keys, 1)) * a.Hkv;
