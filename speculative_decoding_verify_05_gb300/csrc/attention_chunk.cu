@@ -68,8 +68,8 @@ constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys; the time that
-// joining shared items takes at the end, in keys of two row tiles.
-constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 384, JOIN_KEYS = 1280;
+// joining shared items takes at the end, in keys of two row tiles; what reading a piece back takes, in keys of one.
+constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 384, JOIN_KEYS = 1280, PIECE_KEYS = 51;
 
 // 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one asm
 __device__ __forceinline__ void tmem_ld_cols128(uint32_t taddr, uint32_t* r) {
@@ -230,9 +230,17 @@ __device__ __forceinline__ int cut_tile(long long y, bool dual, int keys, int nt
   const int t = (int)((z + KT / 2) / KT);
   return t * KT + KT / 2 >= keys ? nt : t;              // (no piece of a few keys)
 }
-// Where CTA c's share starts (c = grid: where the last one ends); inv_grid = floor((2^64 - 1) / grid).
-__device__ __forceinline__ long long share_start(const ChunkAttnArgs& a, long long total, int c) {
-  return c >= (int)gridDim.x ? total : (long long)__umul64hi((unsigned long long)total, (unsigned)c * a.inv_grid);
+// The cost of the batch and of a CTA's share of it (the last ones' may be smaller or nothing).
+struct Shares {
+  long long total, each;
+  __device__ __forceinline__ long long start(int c) const { return min(total, c * each); }
+};
+// Equal shares, but of so many keys that an item's pieces are not joined for longer than they take: with `keys` of the
+// longest item and a piece's reading back as long as PIECE_KEYS, n sharers take keys / n and n PIECE_KEYS (9 rows of 5
+// heads at 63118 keys: 63 us with 152 sharers, 33 with 35).  inv_grid = floor((2^64 - 1) / grid).
+__device__ __forceinline__ Shares shares_of(const ChunkAttnArgs& a, long long total, int keys) {
+  const long long even = (long long)__umul64hi((unsigned long long)total, a.inv_grid) + 1;
+  return Shares{total, max(even, (long long)(W_ONE * sqrtf((float)PIECE_KEYS * keys)))};
 }
 
 // Where a cut falls: before tile t of item q of kv head h of sequence b (which is s); `start`: the cost of
@@ -314,7 +322,7 @@ struct Piece {
   __device__ __forceinline__ int keys() const { return pos + tok; }
   __device__ __forceinline__ bool tail() const { return t1 == nt && (keys() & 15) != 0; }
 };
-static_assert(OFF_RINGP + (PR + 1) * sizeof(Piece) + 8 <= OFF_ML && OFF_RINGP % 8 == 0, "posted pieces");
+static_assert(OFF_RINGP + (PR + 1) * sizeof(Piece) + sizeof(Shares) <= OFF_ML && OFF_RINGP % 8 == 0, "posted pieces");
 
 // The walk over a CTA's pieces, by a whole warp.
 struct Walk {
@@ -395,7 +403,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RINGP);
   Piece* s_first = ring + PR;              // the CTA's first piece, for the end
-  long long* s_total = reinterpret_cast<long long*>(ring + PR + 1);               // cost of the batch
+  Shares* s_shares = reinterpret_cast<Shares*>(ring + PR + 1);
   float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -443,12 +451,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       long long own = 0;
       bool bad = false;
       Seq mine{0, 0, 0};
+      int longest = 0;
 #pragma unroll 4
       for (int b = b0; b < b1; ++b) {
         bool wrong;
         mine = seq_of(a, b, &wrong);
         bad |= wrong;
         own += head_cost(a, mine) * a.Hkv;
+        if (mine.rows > 0) longest = max(longest, mine.ctx + mine.rows);
       }
       if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
       // Where they come out about even, whole items, the longest first, dealt to the CTAs in rows that run forth and
@@ -457,7 +467,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       // is about the longest item of the last row times the share of the CTAs that the row leaves out: the rule is
       // that this costs less than joining.  Over 20 batches it took the faster side, or one within 1 us of it.
       const int T = 2 * a.tpt, grid = (int)gridDim.x;
-      const int keys = mine.rows > 0 ? mine.ctx + mine.rows : 0;
+      const int keys = longest;              // (of the lane's one sequence, below)
       const int items = run > 1 ? 0 : __reduce_add_sync(0xffffffffu, items_from(a, mine.rows, keys, 1)) * a.Hkv;
       bool whole = false;
       if (items > 0) {
@@ -526,12 +536,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           const long long v = __shfl_up_sync(0xffffffffu, before, o);
           if (lane >= o) before += v;
         }
-        const long long total = __shfl_sync(0xffffffffu, before, 31);
+        const Shares shares = shares_of(a, __shfl_sync(0xffffffffu, before, 31),
+                                        (int)__reduce_max_sync(0xffffffffu, (unsigned)longest));
         before -= own;
         Found f{0, 0, a.B, Seq{0, 0, 0}};      // lanes 0-15: of the start, 16-31: of the end
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const long long x = share_start(a, total, blockIdx.x + k);
+          const long long x = shares.start(blockIdx.x + k);
           const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + own);
           if (owner == 0) continue;            // (the end of everything, or nothing at all)
           Found g{0, before, b0, Seq{0, 0, 0}};
@@ -569,7 +580,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         w.first(a, start, end, lane);
         if (lane == 0) {
           *s_first = w.p;
-          *s_total = total;
+          *s_shares = shares;
         }
         for (int k = 0; post(k, w.p) && w.p.more; ++k) w.next(a, end, lane);
       }
@@ -906,7 +917,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       unsigned *arrived, *taken;           // of a shared item (nullptr otherwise)
     };
     const int me = blockIdx.x;
-    long long total = 0;
+    Shares shares{0, 0};
     auto rows_of = [&](const Piece& p) {
       Rows r;
       const int x = p.dual ? sl : 0, tok = x * a.tpt + row_tok, prow = x * TM + row;
@@ -922,7 +933,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       if (p.t0 > 0 || p.t1 < p.nt) {
         // the last CTA up to this one whose share does not start inside the item, 32 at a time
         for (unsigned out = 0; out == 0; r.c_first -= out ? __ffs(out) - 1 : 32)
-          out = __ballot_sync(0xffffffffu, cut_tile(share_start(a, total, max(r.c_first - lane, 0)) - p.start, p.dual,
+          out = __ballot_sync(0xffffffffu, cut_tile(shares.start(max(r.c_first - lane, 0)) - p.start, p.dual,
                                                     p.keys(), p.nt) == 0);
         r.arrived = a.counters + 16 * r.c_first + warp;
         r.taken = r.arrived + 8;
@@ -966,7 +977,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       int t;                               // tiles up to the last of the 32
     };
     auto sharers = [&](const Piece& p, int base, int t) {
-      const int to = cut_tile(share_start(a, total, base + lane + 1) - p.start, p.dual, p.keys(), p.nt);
+      const int to = cut_tile(shares.start(base + lane + 1) - p.start, p.dual, p.keys(), p.nt);
       const int before = __shfl_up_sync(0xffffffffu, to, 1);
       Sharers s;
       s.has = __ballot_sync(0xffffffffu, to > (lane == 0 ? t : before));   // (a CTA without work has no piece)
@@ -1179,7 +1190,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const Piece& p = ring[k % PR];
-      if (k == 0) total = *s_total;
+      if (k == 0) shares = *s_shares;
       if (!p.more) break;
       const bool dual = p.dual != 0;
       const int n = p.steps(sl), t0 = p.t0;

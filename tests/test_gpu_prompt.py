@@ -256,6 +256,11 @@ def test_attention_long_contexts(lib, rows, ctx):
     check_attention(lib, Case(33, rows, ctx, 8, 2, poison=True), f"{rows} at {ctx}")
 
 
+def test_attention_one_item_for_all(lib):
+    """One row tile over a long cache: shares longer than an even cut's, most CTAs without any."""
+    check_attention(lib, Case(66, [9], [40100], 5, 1, poison=True), "one item")
+
+
 def test_attention_many_sequences(lib):
     rng = np.random.default_rng(4)
     rows = [int(x) for x in rng.integers(0, 4, 700)]
