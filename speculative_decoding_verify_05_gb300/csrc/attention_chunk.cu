@@ -465,12 +465,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       // back: nothing is left to join.  (8 prompts of 100 to 1900 rows 42.0 us, cut 52.5; one of 2048 rows 30.4,
       // cut 42.6; of 8192 rows 320, cut 335; 16 x 32 rows at 4000 keys 47.2, cut 53.4.)  What the deal leaves uneven
       // is about the longest item of the last row times the share of the CTAs that the row leaves out: the rule is
-      // that this costs less than joining.  Over 20 batches it took the faster side, or one within 1 us of it.
+      // that this costs less than joining.  Over 20 batches it took the faster side, or one within 1 us of it.  Items of
+      // one tile are never cut.
       const int T = 2 * a.tpt, grid = (int)gridDim.x;
       const int keys = longest;              // (of the lane's one sequence, below)
       const int items = run > 1 ? 0 : __reduce_add_sync(0xffffffffu, items_from(a, mine.rows, keys, 1)) * a.Hkv;
       bool whole = false;
-      if (items > 0) {
+      if (__any_sync(0xffffffffu, longest > KT) && items > 0) {
         const int before = (items - 1) / grid * grid, out = grid - (items - before);
         const int x = out == 0 ? INT_MAX : JOIN_KEYS * grid / out - ITEM_KEYS + 1;
         whole = __reduce_add_sync(0xffffffffu, items_from(a, mine.rows, keys, x)) * a.Hkv <= before;
@@ -501,6 +502,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             while (n > 1) {
               const int step = (n + 31) >> 5, c = x + lane * step;
               int count = 0;
+#pragma unroll 4
               for (int b = 0; b < a.B; ++b)
                 count += items_from(a, __shfl_sync(0xffffffffu, mine.rows, b), __shfl_sync(0xffffffffu, keys, b), c);
               const int i = 31 - __clz(__ballot_sync(0xffffffffu, c < x + n && count > rank));   // (the first always)

@@ -460,7 +460,9 @@ def test_attention_values_far_from_one(lib, size):
 
 @pytest.mark.parametrize("rows,ctx,Hq,Hkv", [
     ([500] * 8, [0] * 8, 8, 2), ([130, 0] * 16, [(37 * b) % 500 for b in range(32)], 4, 4), ([2048], [0], 16, 8),
-    ([1, 600, 257, 256, 255], [255, 0, 128, 127, 130], 28, 4), ([700], [1], 16, 1)])
+    ([1, 600, 257, 256, 255], [255, 0, 128, 127, 130], 28, 4), ([700], [1], 16, 1),
+    ([130, 1, 0, 77] * 12, [(53 * b) % 300 for b in range(48)], 8, 2), ([90] * 33, [0] * 33, 8, 2),
+    (list(range(10, 202, 3)), [200 - 3 * b for b in range(64)], 5, 1)])
 def test_attention_many_items(lib, rows, ctx, Hq, Hkv):
     """Prompts whose items outnumber the CTAs, with equal and unequal lengths; and on a few CTAs."""
     c = Case(63, rows, ctx, Hq, Hkv, poison=True, pad=2)
