@@ -40,7 +40,8 @@
  *     call, can serve any sequence of calls on one stream without clearing.
  *     Calls that may run concurrently must not share a workspace.
  *   - Device-side waits (TMA/MMA pipelines) are bounded; a wait that runs out
- *     sets a status word read by spec_device_status().
+ *     sets a status word read by spec_device_status().  Zero-fill the
+ *     workspace again after that: its counters may have been left half-way.
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H
@@ -433,7 +434,8 @@ SPEC_API int spec_verify_attention_paged(const spec_bf16* Q, int ldq, const spec
  *   Kpool, Vpool [Hkv][num_pages][128][D] bf16 (in/out), as spec_verify_attention_paged's; no input may
  *               overlap them
  * M is the rows of the buffers; rows outside cu_rows[0] .. cu_rows[B] - 1 are padding: they may hold
- * anything, and Qrot's are left as they were.  Sequences without rows are allowed.  A page that receives rows must belong to one
+ * anything, and Qrot's are left as they were.  Sequences without rows are allowed (their ctx_len
+ * and pages are not looked at).  A page that receives rows must belong to one
  * sequence.  Checked on the device, with the status word set: a sequence outside the M rows or
  * past 128 * max_pages keys is skipped; a row whose page id is outside [0, num_pages) is not written to
  * the pools.  Requires D == 128, leading dimensions multiples of 8, 16-byte aligned pointers.  One

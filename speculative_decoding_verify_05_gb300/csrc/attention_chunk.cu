@@ -201,8 +201,8 @@ struct Seq {
 // Sequence b; one that breaks its bounds counts as having no rows (*bad set).
 __device__ __forceinline__ Seq seq_of(const ChunkAttnArgs& a, int b, bool* bad = nullptr) {
   const int c0 = a.cu_rows[b], c1 = a.cu_rows[b + 1], ctx = a.ctx_len[b];
-  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.M && ctx >= 0 &&
-                  (long long)ctx + (c1 - c0) <= (long long)a.max_pages * KT;
+  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.M &&
+                  (c0 == c1 || (ctx >= 0 && (long long)ctx + (c1 - c0) <= (long long)a.max_pages * KT));
   if (bad) *bad = !ok;
   return Seq{c0, ok ? c1 - c0 : 0, ctx};
 }

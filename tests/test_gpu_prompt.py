@@ -268,6 +268,17 @@ def test_attention_many_sequences(lib):
     check_attention(lib, Case(34, rows, ctx, 4, 1, poison=True), "700 sequences")
 
 
+def test_empty_sequences_are_not_looked_at(lib):
+    """Slots without rows whose lengths (and pages) mean nothing."""
+    c = Case(67, [0, 3, 0, 40, 0], [0, 130, 0, 7, 0], 8, 2)
+    c.ctx[[0, 2, 4]] = [-5, 1 << 30, 128 * c.max_pages + 1]
+    check_attention(lib, c, "empty sequences")
+    cu, ctx, kp, vp, table = c.dev()
+    kv = bf16_dev(synth.normal_bf16_bits(68, (c.M, 4 * D), 1.0))
+    lib.spec_kv_append_paged(kv[:, :2 * D], kv[:, 2 * D:], cu, ctx, kp, vp, table)
+    lib.spec_device_status()
+
+
 def test_attention_padded_batch(lib):
     """Hundreds of slots without rows between the sequences that have some."""
     rows = [0] * 900
