@@ -312,11 +312,11 @@ class VerifyEngine:
                                            out=out, ws=self.ws)
 
     def capture_round(self, x0, cu_rows, ctx_len, q, drafts, U, temperature: float, out,
-                      tie_eps: float = 1e-5, max_rows: int | None = None):
+                      tie_eps: float = 1e-5, max_rows: int | None = None, positions=None):
         """verify_round on these device buffers, captured once in a CUDA graph; returns the replay
         function.  A serving loop writes each round's inputs into the same buffers and replays:
         every launch of the round is re-issued with no per-launch host work.  M and B stay those
-        of the capture; cu_rows, ctx_len, the tokens, q and U may change between rounds (the
+        of the capture; cu_rows, ctx_len, the tokens, q, U and positions may change between rounds (the
         kernels read them from device memory).  The buffers must hold a valid round when this is
         called: the capture runs it twice.  The graph keeps the engine's workspace pointer, so that
         workspace must not be regrown afterwards (it is sized for every call the engine makes; give
@@ -325,11 +325,11 @@ class VerifyEngine:
         side = torch.cuda.Stream(device=dev)
         side.wait_stream(torch.cuda.current_stream(dev))
         with torch.cuda.stream(side):
-            self.verify_round(x0, cu_rows, ctx_len, q, drafts, U, temperature, tie_eps, max_rows, out)
+            self.verify_round(x0, cu_rows, ctx_len, q, drafts, U, temperature, tie_eps, max_rows, out, positions)
         side.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            self.verify_round(x0, cu_rows, ctx_len, q, drafts, U, temperature, tie_eps, max_rows, out)
+            self.verify_round(x0, cu_rows, ctx_len, q, drafts, U, temperature, tie_eps, max_rows, out, positions)
         torch.cuda.current_stream(dev).wait_stream(side)
         self._graphs.append(graph)
         return graph.replay

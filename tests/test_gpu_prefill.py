@@ -7,7 +7,7 @@ import torch
 import synth
 from oracle import bf16 as obf, ops as oops, stack as ostack
 
-from gpu_util import STACK_PROB_BOUND, assert_close_chain, bf16_dev, dev, f64_of_bf16
+from gpu_util import STACK_PROB_BOUND, assert_close_chain, bf16_dev, bits_of, dev, f64_of_bf16
 from test_gpu_glue_stack import _tiny_stack
 
 pytestmark = pytest.mark.gpu
@@ -138,6 +138,44 @@ def test_positions_of_several_axes(lib):
         hidden, _ = run_chunks(eng, x_bits, [(0, 0), (100, 1), (150, 40)], lib, positions=positions)
         for b in range(2):
             assert_close_chain(hidden[b], ref_x[b], 1, f"shift {shift}, sequence {b}")
+
+
+def test_captured_round_with_positions(lib):
+    """A round captured over pages and positions on three axes: after other tokens, lengths and positions are written
+    into its buffers a replay gives what the eager round gives on them."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(2, 89)
+    dims.rope_sections = (24, 20, 20)
+    lengths = [140, 20]
+    cache = Paged(dims, [n + 8 for n in lengths])
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=160, max_rows=6, block_table=cache.table)
+    run_chunks(eng, [synth.normal_bf16_bits(99 + b, (lengths[b], dims.d), 1.0) for b in range(2)], [(0, 0), (140, 20)], lib)
+
+    def inputs(seed, rows, ctx, shift):
+        rng = np.random.default_rng(seed)
+        q = rng.dirichlet(np.full(dims.V, 0.5), size=sum(rows) - 2).astype(np.float32)
+        drafts = np.array([int(rng.integers(dims.V)) for _ in q], np.int32)
+        pos = np.concatenate([np.arange(c, c + n) for c, n in zip(ctx, rows)])
+        return (bf16_dev(synth.normal_bf16_bits(seed, (sum(rows), dims.d), 1.0)),
+                dev(np.array([0, rows[0], sum(rows)], np.int32)), dev(np.array(ctx, np.int32)), dev(q), dev(drafts),
+                dev(synth.uniforms_f32(seed + 1, sum(rows)))), dev(np.stack([pos + shift, pos, pos + 2 * shift]).astype(np.int32))
+
+    bufs, pos = inputs(5, [3, 5], lengths, 0)
+    out = tuple(torch.empty(n, dtype=torch.int32, device="cuda") for n in (2, 8, 2))
+    replay = eng.capture_round(*bufs, 0.8, out, positions=pos)
+    other, other_pos = inputs(6, [6, 2], [137, 19], 11)
+    want = [t.cpu() for t in eng.verify_round(*other, 0.8, positions=other_pos)]
+    written = [bits_of(k) for k in eng.kc]
+    for buf, new in zip((*bufs, pos), (*other, other_pos)):
+        buf.copy_(new)
+    replay()
+    lib.spec_device_status()
+    assert all(torch.equal(o.cpu(), w) for o, w in zip(out, want))
+    assert all(np.array_equal(bits_of(k), w) for k, w in zip(eng.kc, written))
+    # the positions count: the same round at the plain ones writes other keys
+    eng.verify_round(*other, 0.8)
+    lib.spec_device_status()
+    assert any(not np.array_equal(bits_of(k), w) for k, w in zip(eng.kc, written))
 
 
 def test_draft_engine_over_pages(lib):
