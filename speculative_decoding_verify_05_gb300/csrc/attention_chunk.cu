@@ -187,10 +187,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // 32 bytes to a 32-byte boundary: a row per lane then fills whole sectors (as 16-byte stores the outputs of a prompt of
-// 8192 rows took 24 us more; exchanged between lanes first to fill lines, 8 us more).
+// 8192 rows took 24 us more; exchanged between lanes first to fill lines, 8 us more).  Past L1, whose lines the 32 rows
+// of a warp would take one each (8 prompts of 500 rows 30.2 us without the hint, 27.5 with it).
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void st_global_16(void* p, const uint32_t* w) {      // (outputs at odd 16 bytes)
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3])
                : "memory");
 }
 
@@ -953,8 +959,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         st_global_32(r.out + c + 16, w + 8);
       } else {
 #pragma unroll
-        for (int d = 0; d < 16; d += 4)
-          *reinterpret_cast<uint4*>(r.out + c + 2 * d) = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
+        for (int d = 0; d < 16; d += 4) st_global_16(r.out + c + 2 * d, w + d);
       }
     };
     // 32 unnormalised dims from c of this CTA's piece, from TMEM: O of the slot, or both slots' joined
