@@ -468,8 +468,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
       if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
       // Where they come out about even, whole items, the longest first, dealt to the CTAs in rows that run forth and
-      // back: nothing is left to join.  (8 prompts of 100 to 1900 rows 42.0 us, cut 52.5; one of 2048 rows 30.4,
-      // cut 42.6; of 8192 rows 320, cut 335; 16 x 32 rows at 4000 keys 47.2, cut 53.4.)  What the deal leaves uneven
+      // back: nothing is left to join.  (8 prompts of 100 to 1900 rows 39.7 us, cut 52.2; one of 2048 rows 29.2,
+      // cut 41.2; of 8192 rows 318, cut 335; 16 x 32 rows at 4000 keys 47.0, cut 53.1.)  What the deal leaves uneven
       // is about the longest item of the last row times the share of the CTAs that the row leaves out: the rule is
       // that this costs less than joining.  Over 20 batches it took the faster side, or one within 1 us of it.  Items of
       // one tile are never cut.

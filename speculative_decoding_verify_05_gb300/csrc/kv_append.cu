@@ -87,23 +87,39 @@ __device__ __forceinline__ Place place_of(int r, const KvAppendArgs& a, int lane
   }
 }
 
+// 16 bytes past L1, which has no use for them.
+__device__ __forceinline__ uint4 ld_past_l1(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void st_past_l1(uint16_t* p, const uint4& v) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // One CTA per row.  A thread moves pairs of 16-byte chunks (dims i0 .. and 64 + i0 ..) of heads 4 WARPS apart, so
 // its eight angles stay in registers; up to UNITS pairs are loaded before the row's place in the cache is known,
 // which takes two dependent loads.  Bound by HBM: 8192 rows of 32 + 2 x 8 heads, 206 MB, take 32.9 us (6.3 TB/s),
-// 24 sequences of 1 to 999 rows, 81 MB, 14.3 us.
+// 24 sequences of 1 to 999 rows, 81 MB, 13.9 us (5.8).
 // Two shapes.  Few rows: a row's whole traffic in flight at once, 4 warps and up to 4 pairs (8 rows 2.5 us, 1000 rows
-// 4.6; the other shape 3.3 and 5.3).  Many rows: CTAs that are small enough for 16 and more to share an SM, so that
-// some move data while others look their place up (8192 rows 32.9 us, the 24 sequences 14.3; the other shape
+// 4.4; the other shape 3.3 and 5.3).  Many rows: CTAs that are small enough for 16 and more to share an SM, so that
+// some move data while others look their place up (8192 rows 32.9 us, the 24 sequences 14.2; the other shape
 // 33.8 and 17.3).  The two meet at 10 rows per SM (1500 rows: 8.4 us both).
-template <int WARPS, int UNITS>
+// Stores go past L1 (3600 rows of keys and values 5.4 -> 4.7 us, none slower); loads only where many rows are turned
+// (the 24 sequences 14.2 -> 13.9 us; the copy of 3600 rows would take 5.3).
+template <int WARPS, int UNITS, bool TURN>
 __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArgs a) {
   constexpr int STEP = 4 * WARPS;                       // heads between a thread's pairs
+  constexpr bool LOAD_PAST_L1 = WARPS == 2 && TURN;
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, tid = threadIdx.x, i0 = (tid & 7) * 8;
   const int heads = a.Hq + 2 * a.Hkv;
   float4 t[4];                                          // (cos, sin) of dims i0 ..
-  if (a.cs)
+  if constexpr (TURN)
 #pragma unroll
     for (int k = 0; k < 4; ++k) t[k] = *(reinterpret_cast<const float4*>(a.cs + (size_t)r * 64 + i0) + k);
   int b = -2, page = 0, p = 0;
@@ -117,8 +133,8 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArg
       if (hd < a.Hq) src = a.Q + (size_t)r * a.ldq + (size_t)hd * D;
       else if (hd < a.Hq + a.Hkv) src = a.Knew + (size_t)r * a.ldkv + (size_t)(hd - a.Hq) * D;
       else src = a.Vnew + (size_t)r * a.ldkv + (size_t)(hd - a.Hq - a.Hkv) * D;
-      x[k] = *reinterpret_cast<const uint4*>(src + i0);
-      y[k] = *reinterpret_cast<const uint4*>(src + 64 + i0);
+      x[k] = LOAD_PAST_L1 ? ld_past_l1(src + i0) : *reinterpret_cast<const uint4*>(src + i0);
+      y[k] = LOAD_PAST_L1 ? ld_past_l1(src + 64 + i0) : *reinterpret_cast<const uint4*>(src + 64 + i0);
     }
     if (b == -2) {                                      // the row's sequence, position and page
       const Place at = place_of(r, a, tid & 31);
@@ -148,7 +164,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArg
         const int g = hd - a.Hq - (is_v ? a.Hkv : 0);
         dst = (is_v ? a.Vpool : a.Kpool) + (((size_t)g * a.num_pages + page) * PAGE + p % PAGE) * D;
       }
-      if (a.cs && !is_v) {
+      if (TURN && !is_v) {
         uint32_t* xa = reinterpret_cast<uint32_t*>(&x[k]);
         uint32_t* ya = reinterpret_cast<uint32_t*>(&y[k]);
 #pragma unroll
@@ -158,8 +174,8 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArg
           ya[e] = pack_bf16x2(b0 * t[e].x + a0 * t[e].y, b1 * t[e].z + a1 * t[e].w);
         }
       }
-      *reinterpret_cast<uint4*>(dst + i0) = x[k];
-      *reinterpret_cast<uint4*>(dst + 64 + i0) = y[k];
+      st_past_l1(dst + i0, x[k]);
+      st_past_l1(dst + 64 + i0, y[k]);
     }
   }
 }
@@ -178,8 +194,10 @@ cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int hal
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s) {
   const bool many = a.M > 10 * 152;
-  cudaError_t e = many ? launch_k(kv_append_kernel<2, 2>, dim3(a.M), dim3(64), 0, s, a)
-                       : launch_k(kv_append_kernel<4, 4>, dim3(a.M), dim3(128), 0, s, a);
+  const dim3 block(many ? 64 : 128);
+  auto* turn = many ? kv_append_kernel<2, 2, true> : kv_append_kernel<4, 4, true>;
+  auto* copy = many ? kv_append_kernel<2, 2, false> : kv_append_kernel<4, 4, false>;
+  cudaError_t e = launch_k(a.cs ? turn : copy, dim3(a.M), block, 0, s, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
