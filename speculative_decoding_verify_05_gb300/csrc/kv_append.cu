@@ -17,7 +17,7 @@ constexpr int PAGE = 128;
 // and what is left, at most an eighth of a turn, is exact to 2^-33 turns before its one rounding to fp32.  There
 // the Taylor series of sin(pi x) and cos(pi x) on |x| <= 1/4 (terms to (pi x)^9 and (pi x)^10: the next are below
 // 2e-9) take 11 multiply-adds; sincospif, which has the whole line to care for, made the 16000-row table
-// 7.6 us instead of 5.9.  No fp64 instruction: the chip has few of them.
+// 1.7 us more.  No fp64 instruction: the chip has few of them.
 __device__ __forceinline__ float2 cos_sin_turns(unsigned long long u) {
   const unsigned hi = (unsigned)(u >> 32);
   const unsigned quarter = (hi + (1u << 29)) >> 30;                 // 0..4, 4 = 0
@@ -41,9 +41,15 @@ __device__ __forceinline__ float2 cos_sin_turns(unsigned long long u) {
   return make_float2(((quarter + 1u) & 2u) ? -a : a, (quarter & 2u) ? -b : b);
 }
 
-// A thread keeps one frequency and walks `rows` rows with it (its turn and axis come from the parameter bank, where
-// 32 lanes with 32 addresses are served one after the other: per entry that, and integer divisions, took
-// 16.4 us for 16000 rows of 64).
+// A thread keeps one frequency and walks `rows` rows with it.  Its turn and axis are parameters, read by ordinary
+// loads (the pointers' origin hidden from the compiler): from the parameter bank 32 lanes with 32 addresses are served
+// one after the other, for every CTA anew (16000 rows of 64 frequencies 4.2 us instead of 3.3; per entry, with
+// integer divisions, 16.4).
+template <typename T>
+__device__ __forceinline__ const T* as_memory(const T* p) {
+  asm volatile("" : "+l"(p));
+  return p;
+}
 __global__ void __launch_bounds__(256)
 rope_table_axes_kernel(const int32_t* __restrict__ pos, int ldpos, int M, int half, int rows,
                        const __grid_constant__ RopeAxes f, float2* __restrict__ cs) {
@@ -51,8 +57,8 @@ rope_table_axes_kernel(const int32_t* __restrict__ pos, int ldpos, int M, int ha
   pdl_trigger();
   const int i = threadIdx.x;
   if (i >= half) return;
-  const unsigned long long turn = f.turn[i];
-  const int32_t* p = pos + (size_t)f.axis[i] * ldpos;
+  const unsigned long long turn = as_memory(f.turn)[i];
+  const int32_t* p = pos + (size_t)as_memory(f.axis)[i] * ldpos;
   const int r0 = (blockIdx.x * blockDim.y + threadIdx.y) * rows, r1 = min(r0 + rows, M);
 #pragma unroll 4
   for (int r = r0; r < r1; ++r) cs[(size_t)r * half + i] = cos_sin_turns((unsigned long long)(long long)p[r] * turn);
@@ -186,7 +192,7 @@ cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int hal
                                    cudaStream_t s) {
   // rows per thread: one while that fills the chip, more (up to 8) when there are many
   const int bx = (half + 31) / 32 * 32, by = bx < 256 ? 256 / bx : 1;
-  const int rows = M / (by * 152 * 4) < 1 ? 1 : (M / (by * 152 * 4) > 8 ? 8 : M / (by * 152 * 4));
+  const int fill = M / (by * 152 * 2), rows = fill < 1 ? 1 : (fill > 8 ? 8 : fill);
   cudaError_t e = launch_k(rope_table_axes_kernel, dim3((unsigned)((M + by * rows - 1) / (by * rows))), dim3(bx, by), 0, s,
                            pos, ldpos, M, half, rows, f, cs);
   return e != cudaSuccess ? e : cudaGetLastError();
