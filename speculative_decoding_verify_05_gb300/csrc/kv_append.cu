@@ -16,8 +16,8 @@ constexpr int PAGE = 128;
 // (wrap-around is the reduction, exact for any 32-bit position), the nearest quarter turn is split off,
 // and what is left, at most an eighth of a turn, is exact to 2^-33 turns before its one rounding to fp32.  There
 // the Taylor series of sin(pi x) and cos(pi x) on |x| <= 1/4 (terms to (pi x)^9 and (pi x)^10: the next are below
-// 2e-9) take 11 multiply-adds; sincospif, which has the whole line to care for, made the 16000-row table
-// 1.7 us more.  No fp64 instruction: the chip has few of them.
+// 2e-9) take 11 multiply-adds; sincospif, which has the whole line to care for, took 1.7 us
+// more for the 16000-row table.  No fp64 instruction: the chip has few of them.
 __device__ __forceinline__ float2 cos_sin_turns(unsigned long long u) {
   const unsigned hi = (unsigned)(u >> 32);
   const unsigned quarter = (hi + (1u << 29)) >> 30;                 // 0..4, 4 = 0
