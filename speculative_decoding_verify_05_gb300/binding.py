@@ -617,10 +617,15 @@ def spec_chunk_attention_paged(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, s
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     Hq = width // D
-    wp, wn = _ws_args(ws, spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages), Q.device)
-    _check(_lib.spec_chunk_attention_paged(
-        Q.data_ptr(), ldq, cu_rows.data_ptr(), ctx_len.data_ptr(), B, M, Kpool.data_ptr(), Vpool.data_ptr(), num_pages,
-        block_table.data_ptr(), max_pages, Hq, Hkv, D, scale, O.data_ptr(), ldo, wp, wn, _stream(stream)), True)
+    args = (Q.data_ptr(), ldq, cu_rows.data_ptr(), ctx_len.data_ptr(), B, M, Kpool.data_ptr(), Vpool.data_ptr(),
+            num_pages, block_table.data_ptr(), max_pages, Hq, Hkv, D, scale, O.data_ptr(), ldo)
+    wp, wn = (None, 0) if ws is None else ws.args()
+    rc = _lib.spec_chunk_attention_paged(*args, wp, wn, _stream(stream))
+    # (asking for the size first would cost a decode step's call another microsecond)
+    if rc != SPEC_OK and wn < (need := spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages)):
+        wp, wn = _ws_args(ws, need, Q.device)
+        rc = _lib.spec_chunk_attention_paged(*args, wp, wn, _stream(stream))
+    _check(rc, True)
     return O
 
 
