@@ -69,7 +69,7 @@ constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys; the time that
 // joining shared items takes at the end, in keys of two row tiles; what reading a piece back takes, in keys of one.
-constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 384, JOIN_KEYS = 1280, PIECE_KEYS = 51;
+constexpr int W_DUAL = 4, W_ONE = 3, ITEM_KEYS = 384, JOIN_KEYS = 1280, PIECE_KEYS = 36;
 
 // 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one asm
 __device__ __forceinline__ void tmem_ld_cols128(uint32_t taddr, uint32_t* r) {
@@ -200,6 +200,11 @@ __device__ __forceinline__ void st_global_16(void* p, const uint32_t* w) {      
                : "memory");
 }
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 // ----------------------------------------------------------------- the batch
 struct Seq {
   int r0, rows, ctx;
@@ -243,7 +248,7 @@ struct Shares {
 };
 // Equal shares, but of so many keys that an item's pieces are not joined for longer than they take: with `keys` of the
 // longest item and a piece's reading back as long as PIECE_KEYS, n sharers take keys / n and n PIECE_KEYS (9 rows of 5
-// heads at 63118 keys: 63 us with 152 sharers, 33 with 35).  inv_grid = floor((2^64 - 1) / grid).
+// heads at 63118 keys: 63 us with 152 sharers, 28 with 42).  inv_grid = floor((2^64 - 1) / grid).
 __device__ __forceinline__ Shares shares_of(const ChunkAttnArgs& a, long long total, int keys) {
   const long long even = (long long)__umul64hi((unsigned long long)total, a.inv_grid) + 1;
   return Shares{total, max(even, (long long)(W_ONE * sqrtf((float)PIECE_KEYS * keys)))};
@@ -949,17 +954,18 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       return r;
     };
     auto part_at = [&](const Rows& r, int c) { return (size_t)c * 2 + (c == r.c_first ? 1 : 0); };
-    auto store = [&](const Rows& r, int c, const float* v, float f) {      // 32 dims from c
-      uint32_t w[16];
+    auto store = [&](const Rows& r, int c, const float* v, float f, auto dims) {      // `dims` of them from c
+      constexpr int N = decltype(dims)::value / 2;
+      uint32_t w[N];
 #pragma unroll
-      for (int d = 0; d < 16; ++d) w[d] = cvt_bf16x2(v[2 * d] * f, v[2 * d + 1] * f);
+      for (int d = 0; d < N; ++d) w[d] = cvt_bf16x2(v[2 * d] * f, v[2 * d + 1] * f);
       if (!r.used) return;
       if (a.wide) {
-        st_global_32(r.out + c, w);
-        st_global_32(r.out + c + 16, w + 8);
+#pragma unroll
+        for (int d = 0; d < N; d += 8) st_global_32(r.out + c + 2 * d, w + d);
       } else {
 #pragma unroll
-        for (int d = 0; d < 16; d += 4) st_global_16(r.out + c + 2 * d, w + d);
+        for (int d = 0; d < N; d += 4) st_global_16(r.out + c + 2 * d, w + d);
       }
     };
     // 32 unnormalised dims from c of this CTA's piece, from TMEM: O of the slot, or both slots' joined
@@ -991,9 +997,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       s.t = __shfl_sync(0xffffffffu, to, 31);
       return s;
     };
-    constexpr int BATCH = 2;
-    // f(c) for batches of BATCH sharers in CTA order (-1: none)
-    auto batches = [&](const Piece& p, const Rows& r, const Sharers& first, auto&& f) {
+    // f(c) for batches of N sharers in CTA order (-1: none)
+    auto batches = [&](const Piece& p, const Rows& r, const Sharers& first, auto n, auto&& f) {
+      constexpr int BATCH = decltype(n)::value;
       Sharers s = first;
       for (int base = r.c_first;; base += 32) {
         while (s.has) {
@@ -1013,11 +1019,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     bool shared_first = false;             // the first piece's item came from the CTA before
     bool direct = false;                   // the last piece is joined from TMEM, with this maximum and sum
     float m_last = 0.f, l_last = 0.f;
-    // Joins groups of 32 dims of the pieces' rows, in CTA order whoever does it, as long as some are left to take (`here`:
-    // all, with this CTA's piece from TMEM).  One pass over the pieces per group, their maxima and sums with
-    // it (they mostly agree in the reference, so nothing is rescaled as a rule).
-    auto join = [&](const Piece& p, const Rows& r, const Sharers& first, bool here) {
-      const int groups = (r.c_hi - r.c_lo) >> 5;
+    // Joins groups of dims of the pieces' rows, in CTA order whoever does it, as long as some are left to take (`here`:
+    // all, with this CTA's piece from TMEM).  One pass over the pieces per group, their references and sums with
+    // it (they mostly agree in the reference, so nothing is rescaled as a rule).  A few sharers take 32 dims at a
+    // time and two pieces at once; many 16 and four, so that twice as many of them have a part and take fewer
+    // rounds of loads (one token at 100000 keys of 8 heads on one kv head 37.4 -> 31.3 us, 64 rows of 16 heads at 60000
+    // keys 42.2 -> 37.0; two sharers would lose 1 to 2 us to the smaller groups).
+    auto join = [&](const Piece& p, const Rows& r, const Sharers& first, auto dims, auto batch, bool here) {
+      constexpr int N = decltype(dims)::value, BATCH = decltype(batch)::value;
+      const int groups = (r.c_hi - r.c_lo) / N;
       for (int g = 0;; ++g) {
         if (!here) {
           unsigned t = 0;
@@ -1025,37 +1035,39 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           g = (int)__shfl_sync(0xffffffffu, t, 0);
         }
         if (g >= groups) break;
-        const int c32 = r.c_lo + 32 * g;
+        const int c0 = r.c_lo + N * g;
         float top = -INFINITY, sum = 0.f;
-        float acc[32];
+        float acc[N];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-        batches(p, r, first, [&](const int (&c)[BATCH]) {
-          float4 u[BATCH][8];
+        for (int k = 0; k < N; ++k) acc[k] = 0.f;
+        batches(p, r, first, batch, [&](const int (&c)[BATCH]) {
+          float4 u[BATCH][N / 4];
           float2 ml[BATCH];
           float high = top;
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
             ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int d = 0; d < 8; ++d) u[k][d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int d = 0; d < N / 4; ++d) u[k][d] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (c[k] >= 0 && r.used && !(here && c[k] == me)) {
               ml[k] = __ldcg(r.part_ml + part_at(r, c[k]) * (4 * TM));
-              const float* src = r.part_o + part_at(r, c[k]) * (2 * TM * D) + (size_t)(c32 >> 2) * (2 * TM * 4);
+              const float* src = r.part_o + part_at(r, c[k]) * (2 * TM * D) + (size_t)(c0 >> 2) * (2 * TM * 4);
 #pragma unroll
-              for (int d = 0; d < 8; ++d) u[k][d] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)d * (2 * TM * 4)));
+              for (int d = 0; d < N / 4; ++d)
+                u[k][d] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)d * (2 * TM * 4)));
             }
           }
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
-            if (here && c[k] == me) {
-              float v[32];
-              own32(p, c32, v);
-              ml[k] = make_float2(m_last, l_last);
+            if constexpr (N == 32)
+              if (here && c[k] == me) {
+                float v[32];
+                own32(p, c0, v);
+                ml[k] = make_float2(m_last, l_last);
 #pragma unroll
-              for (int d = 0; d < 8; ++d) u[k][d] = make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
-            }
+                for (int d = 0; d < 8; ++d) u[k][d] = make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+              }
             high = fmaxf(high, ml[k].x);
           }
           const float ref = high == -INFINITY ? 0.f : high;
@@ -1063,7 +1075,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             const float keep = ex2(top - ref);
             sum *= keep;
 #pragma unroll
-            for (int d = 0; d < 32; ++d) acc[d] *= keep;
+            for (int d = 0; d < N; ++d) acc[d] *= keep;
             top = high;
           }
 #pragma unroll
@@ -1071,7 +1083,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             const float w = ex2(ml[k].x - ref);
             sum += ml[k].y * w;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
+            for (int d = 0; d < N / 4; ++d) {
               acc[4 * d] += u[k][d].x * w;
               acc[4 * d + 1] += u[k][d].y * w;
               acc[4 * d + 2] += u[k][d].z * w;
@@ -1079,7 +1091,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             }
           }
         });
-        store(r, c32, acc, 1.f / sum);
+        store(r, c0, acc, 1.f / sum, dims);
         __syncwarp();
       }
     };
@@ -1118,7 +1130,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         for (int c = r.c_lo; c < r.c_hi; c += 32) {
           float v[32];
           own32(p, c, v);
-          store(r, c, v, inv);
+          store(r, c, v, inv, Int<32>{});
           __syncwarp();
         }
       } else {
@@ -1182,7 +1194,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       for (int base = r.c_first; s.t < p.nt; n += __popc(s.has)) s = sharers(p, base += 32, s.t);
       if (here || __shfl_sync(0xffffffffu, there, 0)) {
         __syncwarp();
-        join(p, r, all, here);
+        if (__popc(all.has) > 4 || all.t < p.nt) join(p, r, all, Int<16>{}, Int<4>{}, false);
+        else join(p, r, all, Int<32>{}, Int<2>{}, here);
       }
       // done with it; the last of the sharers clears their two words for the next launch
       if (lane == 0 && (int)(atomicAdd(r.taken, 0x10000u) >> 16) + 1 == n) {
