@@ -276,14 +276,20 @@ class VerifyEngine:
         included).  Leaves the rows' keys and values in their pages (the caller then advances ctx_len by
         the rows) and returns the hidden rows x [M, d] after the last layer, or with a temperature
         (x, P): P [B, V] the next token's probabilities after each sequence's last row of the chunk
-        (those of a sequence without rows mean nothing).  At most max_M rows."""
+        (those of a sequence without rows, or outside the M rows, mean nothing).  At most max_M rows."""
         if self.block_table is None:
             raise ValueError("prefill needs a paged cache (block_table)")
+        if temperature is not None and self.w.w_lm is None:
+            raise ValueError("next-token probabilities need an LM head (w_lm)")
         M = self._stack(x0, cu_rows, ctx_len, 1, None, final_norm=False, prompt=True, positions=positions)
         if temperature is None:
             return self.x[:M]
-        last = (cu_rows[1:] - 1).clamp_(min=0)
-        B = last.numel()
+        B = cu_rows.numel() - 1
+        if M == 0:
+            return self.x[:0], torch.zeros((B, self.dims.V), dtype=torch.float32, device=self.device)
+        # (cu_rows may hold anything: the kernels refuse what is outside the M rows with the status word set, and
+        # so must no index here leave them)
+        last = (cu_rows[1:] - 1).clamp_(0, M - 1)
         h = S.spec_rmsnorm(self.x[:M].index_select(0, last), self.w.final_norm, self.dims.eps)
         P = self.P[:B] if B <= self.P.shape[0] else None
         return self.x[:M], S.spec_lmhead_softmax(h, self.w.w_lm, temperature, P=P, ws=self.ws)

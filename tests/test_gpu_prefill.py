@@ -221,3 +221,47 @@ def test_prefill_refusals(lib):
     eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=1, max_rows=1, block_table=cache.table)
     with pytest.raises(ValueError):
         eng.prefill(x, cu, ctx)                                  # more rows than the engine was sized for
+
+
+def test_prefill_with_a_sequence_outside_the_rows(lib):
+    """cu_rows past the chunk's rows: the status word says so, no index leaves the buffers, and the sequence that
+    is in them gets its rows and its probabilities."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(1, 91)
+    lengths = [5, 4, 3]
+    x_bits = [synth.normal_bf16_bits(101 + b, (lengths[b], dims.d), 1.0) for b in range(3)]
+    cache = Paged(dims, lengths)
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=16, max_rows=1, block_table=cache.table)
+    x0 = bf16_dev(np.concatenate(x_bits)[:7])
+    ref_x, ref_lg = whole(osw, od, x_bits, lengths)
+    for ends in ([5, 9, 12], [5, 1 << 30, 1 << 30], [5, 9, 1 << 30]):
+        x, P = eng.prefill(x0, dev(np.array([0] + ends, np.int32)), dev(np.zeros(3, np.int32)), temperature=1.0)
+        rc, _ = lib.spec_device_status_code()
+        assert rc == lib.SPEC_EINVAL, ends
+        assert_close_chain(f64_of_bf16(x)[:5], ref_x[0], 1, f"rows of the sequence in bounds, {ends}")
+        p = P[0].cpu().numpy().astype(np.float64)
+        assert abs(p - oops.target_probs(ref_lg[0][-1:], 1.0)[0]).max() < STACK_PROB_BOUND
+        lib.spec_device_status()
+
+
+def test_prefill_of_no_rows(lib):
+    """A chunk to which no sequence brings a row, with and without the probabilities; and probabilities without an LM
+    head are refused before anything runs."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, _, _, gsw = _tiny_stack(1, 93)
+    cache = Paged(dims, [8, 8])
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=4, max_rows=1, block_table=cache.table)
+    x0 = torch.empty((0, dims.d), dtype=torch.bfloat16, device="cuda")
+    none, ctx = dev(np.zeros(3, np.int32)), dev(np.array([3, 0], np.int32))
+    before = [bits_of(k) for k in cache.k]
+    assert eng.prefill(x0, none, ctx).shape == (0, dims.d)
+    x, P = eng.prefill(x0, none, ctx, temperature=1.0)
+    lib.spec_device_status()
+    assert x.shape == (0, dims.d) and P.shape == (2, dims.V)
+    assert all(np.array_equal(bits_of(k), b) for k, b in zip(cache.k, before))
+    gsw.w_lm = None
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=4, max_rows=1, block_table=cache.table)
+    launched = lib.launch_count()
+    with pytest.raises(ValueError):
+        eng.prefill(x0.new_zeros((2, dims.d)), dev(np.array([0, 2, 2], np.int32)), ctx, temperature=1.0)
+    assert lib.launch_count() == launched
