@@ -448,7 +448,8 @@ SPEC_API int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, 
 
 /* Attention of a chunk of new tokens: row j of sequence b attends keys 0 .. ctx_len[b] + j of its
  * pages (its own and the chunk's earlier keys already appended), softmax(scale q.k) v with fp32 sums
- * and statistics; the softmax weights enter the product with V as bf16 and the output is rounded once.
+ * and statistics; the softmax weights enter the product with V as bf16 (each rounded by half a step at most;
+ * not the largest of a row of up to 128 keys), and the output is rounded once.
  * Any number of rows per sequence, from one to the whole prompt, mixed in one call; only reads the
  * cache.
  *   Q [M x Hq*D] bf16 with leading dimension ldq (rotation applied), O likewise with ldo (out; must
@@ -457,8 +458,8 @@ SPEC_API int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, 
  * Pages are read to the last key of the sequence only: what lies behind it (in its last page or in
  * table entries past it) may hold anything, NaN included.  Rows outside cu_rows[0] .. cu_rows[B] - 1
  * are padding: their O is left as it was.  A non-finite value in V of a new key also reaches the rows of its
- * own chunk before it that share its 128-key tile (0 * inf).  Values up to 1e25 keep the unnormalised
- * sums in range.  Checked on the device, with the status
+ * own chunk before it that share its 128-key tile (0 * inf).  Values of 1e-30 to 1e25 (and 0) keep the
+ * unnormalised sums in range.  Checked on the device, with the status
  * word set: a sequence outside the M rows or past 128 * max_pages keys is skipped; a page id outside
  * [0, num_pages) reads page 0 instead.
  * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, scale finite and >= 0.

@@ -24,8 +24,8 @@
 // sequence), so one graph serves any lengths.
 //
 // Bound.  With many rows, the tensor cores: a key tile's four products of 128^3 take 2048 of their cycles, in which
-// the softmax warps have to form 256 x 128 weights, which is why nothing else is in their way: no
-// maximum per tile (the reference below), two fp32 operations per instruction, a row per thread.  A prompt of 8192 rows
+// the softmax warps have to form 256 x 128 weights, which is why nothing else is in their way: a
+// maximum once per row (the reference below), two fp32 operations per instruction, a row per thread.  A prompt of 8192 rows
 // (32 + 2 x 8 heads) takes 320 us = 1715 TFLOP/s, 2048 rows at 30000 keys 640 us = 1630.  With few rows, HBM: 61 rows
 // at 131000 keys 99 us = 5.4 TB/s, 16 x 32 rows at 4000 keys 47 us = 5.8 TB/s.  In between and below, what a
 // call costs whatever its size: 4 to 5 us to the first product (lengths, the CTA's pieces, page table, first
@@ -1241,14 +1241,45 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           }
           tmem_st_wait();
         }
-        // Weights relative to the row's reference, not to its maximum: any reference within 2^20 above and 2^60
-        // below the maximum gives the same quotients (bf16 and fp32 have exponents to spare, with values up to
-        // 1e25), so nothing waits for a maximum.  The tile's sum tells when the reference is out of that range
-        // (or the first keys in sight are); then the maximum is found and taken, O rescaled, and the weights
+        // Weights relative to the row's reference: the maximum of the first tile in which it sees a key, whose own weight
+        // is then 1, exactly.  (bf16 weights are off by 1.7e-3 each in rms; a reference that is no maximum leaves that
+        // to the largest weight too: rows of 16 keys 2.3e-3 off instead of 1.85e-3, of 128 keys 2.35e-3 instead of
+        // 1.9e-3, logits of a few units; and scores far below a reference of 0 take small values out of fp32's range.
+        // Looking costs 1 to 3 % on short prompts: 8 of 500 rows 27.5 -> 28.3 us, of 100 to 1900 rows 40.0 -> 40.9.)
+        // Later tiles keep it, so that they need not wait for a maximum: any reference down to 2^20 below
+        // the maximum gives the same quotients (bf16 and fp32 have exponents to spare, with values up to 1e25).
+        // The tile's sum tells when it is out of that range; then the maximum is taken, O rescaled, and the weights
         // formed again.
         uint32_t pk[64];
         float tile_sum;
-        for (bool again = false;; again = true) {
+        for (bool look = __any_sync(0xffffffffu, live && l_run == 0.f);; look = true) {
+          if (look) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c = 0; c < KT; c += 64) {
+              float v[64];
+              tmem_ld_cols<64>(t_s + c, v);
+#pragma unroll
+              for (int k = 0; k < 64; ++k) top[k & 3] = fmaxf(top[k & 3], v[k]);
+            }
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            // (a sum above 2^27 has a weight above 2^20; nothing in sight: the reference stays)
+            const bool move = l_run == 0.f ? mx > -INFINITY : mx > ref + 19.f;
+            const float alpha = move && l_run != 0.f ? ex2(ref - mx) : 1.f;
+            if (move) ref = mx;
+            l_run *= alpha;
+            // O is whole here: the scores' barrier came after the slot's P V before them
+            if (__any_sync(0xffffffffu, live && alpha != 1.f)) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld_cols32(t_o + c, o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st_cols32(t_o + c, o);
+              }
+            }
+          }
           uint32_t r[128];
           tmem_ld_cols128(t_s, r);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -1263,33 +1294,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           }
           const float2 s2 = add2(sum[0], sum[1]);
           tile_sum = s2.x + s2.y;
-          const bool out = live && (!(tile_sum <= 0x1p27f) || (l_run == 0.f && !(tile_sum >= 0x1p-60f)));
-          if (again || !__any_sync(0xffffffffu, out)) break;
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < KT; c += 32) {
-            float v[32];
-            tmem_ld_cols<32>(t_s + c, v);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
-          }
-          mx *= scale;
-          // (a sum above 2^27 has a weight above 2^20; nothing in sight: the reference stays)
-          const bool move = mx > ref + 19.f || (l_run == 0.f && mx < ref - 40.f && mx > -INFINITY);
-          const float alpha = !move ? 1.f : (l_run == 0.f ? 0.f : ex2(ref - mx));
-          if (move) ref = mx;
-          l_run *= alpha;
-          // O is whole here: the scores' barrier came after the slot's P V before them
-          if (j > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld_cols32(t_o + c, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st_cols32(t_o + c, o);
-            }
-          }
+          if (look || !__any_sync(0xffffffffu, live && !(tile_sum <= 0x1p27f))) break;
         }
         l_run += tile_sum;
         tmem_st_cols32(t_s, pk);

@@ -546,3 +546,37 @@ def test_prompt_in_chunks_then_verify(lib):
         # 2^-4 here and the attention's own tests hold them to theirs
         g = np.concatenate(got[b]).reshape(ref.shape)
         assert np.all(abs(g - ref) <= HALF_BF16 * abs(ref) + 2.0 ** -4 * mag)
+
+
+# --------------------------------------------------------------------------- the weights' reference
+def test_attention_largest_weight_is_not_rounded(lib):
+    """Rows of 8 to 128 keys: the largest weight enters the product exactly, so what is left are the output's rounding
+    and the other weights'.  A rounding to bf16 of values spread over the octaves errs by a uniform
+    +-2^-8 / m for a mantissa m, 1 <= m < 2, of density 1 / (m ln 2): its mean square is (2^-7)^2 / 12 * (3/8) / ln 2.
+    The errors are independent and their squares add up; a tenth above the sum is far outside what 150000
+    outputs can deviate by (the largest weight's rounding would add half of it)."""
+    c = Case(70, [1] * 150, [7 + (37 * b) % 121 for b in range(150)], 8, 2, q_std=2.0)
+    got = f64_of_bf16(run_attention(lib, c)).reshape(c.M, 8, D)
+    ref, _ = c.oracle(1.0 / np.sqrt(D))
+    step2 = 2.0 ** -14 / 12 * 0.375 / np.log(2)
+    q = obf.decode(c.q).reshape(c.M, 2, 4, D)
+    others = 0.0
+    for b in range(c.B):
+        page, n = c.table[b, 0], c.ctx[b] + 1
+        k, v = (obf.decode(x[:, page, :n]) for x in (c.kp, c.vp))
+        s = np.einsum("ghd,gkd->ghk", q[b], k) / np.sqrt(D)
+        w = np.exp(s - s.max(-1, keepdims=True))
+        w /= w.sum(-1, keepdims=True)
+        np.put_along_axis(w, w.argmax(-1)[..., None], 0.0, -1)
+        others += np.einsum("ghk,gkd->", w ** 2, v ** 2)
+    assert ((got - ref) ** 2).sum() <= 1.1 * step2 * ((ref ** 2).sum() + others)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-25, 1.0])
+def test_attention_scores_below_zero_with_small_values(lib, size):
+    """Scores about -28 (2^-41 as a weight relative to 0) and values down to 1e-30: their products must not leave fp32."""
+    c = Case(71, [130, 2, 1, 40], [0, 500, 2000, 90], 8, 2)
+    c.kp[:] = synth.f32_to_bf16_bits((obf.decode(c.kp) * 0.1 - 2.5).astype(np.float32))
+    c.q[:] = synth.f32_to_bf16_bits(np.full(1, 1.0, np.float32))[0]
+    c.vp = synth.f32_to_bf16_bits((obf.decode(c.vp) * size).astype(np.float32))
+    check_attention(lib, c, f"values of {size}")
