@@ -457,8 +457,10 @@ SPEC_API int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, 
  *   h / (Hq / Hkv).
  * Pages are read to the last key of the sequence only: what lies behind it (in its last page or in
  * table entries past it) may hold anything, NaN included.  Rows outside cu_rows[0] .. cu_rows[B] - 1
- * are padding: their O is left as it was.  A non-finite value in V of a new key also reaches the rows of its
- * own chunk before it that share its 128-key tile (0 * inf).  Values of 1e-30 to 1e25 (and 0) keep the
+ * are padding: their O is left as it was.  A non-finite value in V of a new key (not in K) also reaches, in its
+ * dim of its kv head, the rows before it of its block: the rows of a sequence's chunk count in blocks of
+ * 2 * floor(128 / (Hq / Hkv)) that multiply their key tiles together (0 * inf).  So rows without a
+ * meaning belong outside cu_rows, not behind the others of their sequence.  Values of 1e-30 to 1e25 (and 0) keep the
  * unnormalised sums in range.  Checked on the device, with the status
  * word set: a sequence outside the M rows or past 128 * max_pages keys is skipped; a page id outside
  * [0, num_pages) reads page 0 instead.

@@ -580,3 +580,26 @@ def test_attention_scores_below_zero_with_small_values(lib, size):
     c.q[:] = synth.f32_to_bf16_bits(np.full(1, 1.0, np.float32))[0]
     c.vp = synth.f32_to_bf16_bits((obf.decode(c.vp) * size).astype(np.float32))
     check_attention(lib, c, f"values of {size}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,block", [(8, 2, 64), (4, 4, 256), (12, 4, 84)])
+@pytest.mark.parametrize("what", ["K nan", "K inf", "V nan", "V inf"])
+def test_attention_reach_of_a_non_finite_new_key(lib, Hq, Hkv, block, what):
+    """A NaN or infinity in one dim of a new key: in K it is seen by the rows that see the key, in V by them and the
+    earlier rows of the block of rows, in this dim of this kv head only.  Everything else is as without it."""
+    rows, ctx, at, dim = 3 * block + 5, 100, 2 * block - 3, 21
+    c = Case(72, [rows, 9], [ctx, 40], Hq, Hkv)
+    ref, mag = c.oracle(1.0 / np.sqrt(D))
+    pool = c.kp if what[0] == "K" else c.vp
+    pool[0, c.table[0, (ctx + at) // PAGE], (ctx + at) % PAGE, dim] = 0x7FC0 if what.endswith("nan") else 0x7F80
+    got = f64_of_bf16(run_attention(lib, c)).reshape(ref.shape)
+    clean = np.ones(ref.shape, bool)
+    heads = slice(0, Hq // Hkv)
+    if what[0] == "K":          # (an infinite score may be -inf: no weight, and nothing to see)
+        clean[at:rows, heads] = False
+        if what == "K nan":
+            assert np.all(np.isnan(got[at:rows, heads]))
+    else:
+        clean[block:rows, heads, dim] = False
+        assert not np.any(np.isfinite(got[at:rows, heads, dim]))
+    assert_attended(got[clean], ref[clean], mag[clean], what)
