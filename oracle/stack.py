@@ -25,7 +25,7 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from . import ops
+from . import ops, prompt
 from .bf16 import decode, round_to_bf16 as r16
 
 
@@ -40,6 +40,8 @@ class Dims:
     layers: int = 36
     eps: float = 1e-6
     theta: float = 1e6
+    rope_sections: tuple = ()         # frequencies of each position axis (sum D/2); (): one axis
+    rope_interleaved: bool = False
 
 
 @dataclass
@@ -60,10 +62,11 @@ class StackWeights:
     w_lm: np.ndarray | None = None   # [V, d]
 
 
-def layer_forward(x, lw: LayerWeights, dims: Dims, cu_rows, ctx_len, Kc, Vc):
+def layer_forward(x, lw: LayerWeights, dims: Dims, cu_rows, ctx_len, Kc, Vc, positions=None):
     """One decoder layer over the packed verify rows.
 
-    x [M, d] (bf16 values, fp64); Kc/Vc [B, Hkv, cap, D] this layer's cache.
+    x [M, d] (bf16 values, fp64); Kc/Vc [B, Hkv, cap, D] this layer's cache; positions [axes, M]
+    the rows' positions on dims.rope_sections' axes (default: ctx_b + j, one axis).
     Returns (x', Kc', Vc').
     """
     M = x.shape[0]
@@ -75,8 +78,11 @@ def layer_forward(x, lw: LayerWeights, dims: Dims, cu_rows, ctx_len, Kc, Vc):
     q = qkv[:, :Hq * D].reshape(M, Hq, D)
     k = qkv[:, Hq * D:(Hq + Hkv) * D].reshape(M, Hkv, D)
     v = r16(qkv[:, (Hq + Hkv) * D:]).reshape(M, Hkv, D)
-    q = r16(ops.rope(q, pos, dims.theta))
-    k = r16(ops.rope(k, pos, dims.theta))
+    if positions is None:
+        q, k = r16(ops.rope(q, pos, dims.theta)), r16(ops.rope(k, pos, dims.theta))
+    else:
+        cs = prompt.rope_table_axes(positions, dims.rope_sections or (D // 2,), D, dims.theta, dims.rope_interleaved)
+        q, k = r16(prompt.rotate(q, cs)[0]), r16(prompt.rotate(k, cs)[0])
     o, Kc, Vc = ops.verify_attention(q, k, v, cu_rows, Kc, Vc, ctx_len, 1.0 / np.sqrt(D))
     o = r16(o)
     x = r16(ops.linear(o.reshape(M, Hq * D), decode(lw.w_o), residual=x))
@@ -94,8 +100,8 @@ def head_logits(x, sw: StackWeights, dims: Dims):
 
 
 def verify_pass(x0, sw: StackWeights, dims: Dims, cu_rows, ctx_len, Kcaches, Vcaches,
-                n_layers: int | None = None):
-    """Run the stack once over all packed verify rows.
+                n_layers: int | None = None, positions=None):
+    """Run the stack once over all packed verify rows (positions: see layer_forward).
 
     Returns (final hidden x [M, d], logits [M, V] or None if there is no LM
     head, updated caches).
@@ -105,7 +111,7 @@ def verify_pass(x0, sw: StackWeights, dims: Dims, cu_rows, ctx_len, Kcaches, Vca
     Vc = list(Vcaches)
     L = len(sw.layers) if n_layers is None else n_layers
     for li in range(L):
-        x, Kc[li], Vc[li] = layer_forward(x, sw.layers[li], dims, cu_rows, ctx_len, Kc[li], Vc[li])
+        x, Kc[li], Vc[li] = layer_forward(x, sw.layers[li], dims, cu_rows, ctx_len, Kc[li], Vc[li], positions)
     logits = head_logits(x, sw, dims) if sw.w_lm is not None else None
     return x, logits, Kc, Vc
 

@@ -370,19 +370,26 @@ class DraftEngine:
         self.ctx = torch.empty((gamma, B), dtype=torch.int32, device=dev)
         self.step_tok = torch.empty((gamma + 1, B), dtype=torch.int32, device=dev)
         self.steps = torch.arange(gamma, dtype=torch.int32, device=dev)[:, None]
+        self.pos = torch.empty((gamma, len(dims.rope_sections) or 1, B), dtype=torch.int32, device=dev)
 
-    def draft(self, tok0, ctx_len, U, temperature: float, Q, drafts):
+    def draft(self, tok0, ctx_len, U, temperature: float, Q, drafts, positions=None):
         """tok0 [B] int32 (each sequence's last committed token), ctx_len [B] int32 (tokens in the
         draft cache), U [gamma, B] fp32; writes Q [B * gamma, V] fp32 (q rows, sequence-major) and
-        drafts [B * gamma] int32 (sequence b's drafts at b * gamma ..)."""
+        drafts [B * gamma] int32 (sequence b's drafts at b * gamma ..).  positions [axes, B] int32: tok0's
+        positions on dims.rope_sections' axes, where the cached prompt had positions of its own; the drafts
+        follow one further on every axis per step (default: ctx_b + i)."""
         B, g, V = self.B, self.gamma, self.dims.V
         e = self.eng
+        if positions is not None and positions.shape != self.pos.shape[1:]:
+            raise ValueError("positions must be [axes, B]")
         self.step_tok[0].copy_(tok0)
         torch.add(ctx_len[None, :], self.steps, out=self.ctx)     # positions ctx_b + i
+        if positions is not None:
+            torch.add(positions[None], self.steps[:, None], out=self.pos)
         Qv = Q.view(B, g, V)
         for i in range(g):
             S.spec_embed(self.step_tok[i], self.table, X=e.x[:B])
-            e._stack(e.x[:B], self.cu, self.ctx[i], 1, None)
+            e._stack(e.x[:B], self.cu, self.ctx[i], 1, None, positions=None if positions is None else self.pos[i])
             S.spec_lmhead_softmax(e.h[:B], self.table, temperature, P=Qv[:, i, :], ws=e.ws)
             S.spec_sample_rows(Qv[:, i, :], U[i], out=self.step_tok[i + 1])
         drafts.view(B, g).copy_(self.step_tok[1:].t())

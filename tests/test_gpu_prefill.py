@@ -265,3 +265,49 @@ def test_prefill_of_no_rows(lib):
     with pytest.raises(ValueError):
         eng.prefill(x0.new_zeros((2, dims.d)), dev(np.array([0, 2, 2], np.int32)), ctx, temperature=1.0)
     assert lib.launch_count() == launched
+
+
+def grid_positions(n, lead):
+    """[3, n]: text, then a grid of patches 7 wide (one time, rows and columns apart), behind `lead` tokens."""
+    i = np.arange(n)
+    j = np.clip(i - lead, 0, None)
+    grid = np.stack([0 * j, j // 7, j % 7]) + lead
+    return np.where(i < lead, i, grid)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_draft_behind_a_prompt_with_positions(lib, interleaved):
+    """Drafts behind prompts whose positions differ between the axes and from the token's index: hidden rows and q are
+    those of one pass over the whole sequences at the given positions (the token's index would be off by 30 and
+    10 times the bounds)."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(1, 97)
+    for d in (dims, od):
+        d.rope_sections, d.rope_interleaved = (24, 20, 20), interleaved
+    B, gamma, lengths = 2, 3, [140, 20]
+    cache = Paged(dims, [n + gamma for n in lengths])
+    g = E.DraftEngine(dims, gsw, cache.k, cache.v, B, gamma, block_table=cache.table, max_M=160)
+    pos = [grid_positions(n, 5 + b) for b, n in enumerate(lengths)]
+    x_bits = [synth.normal_bf16_bits(300 + b, (lengths[b], dims.d), 1.0) for b in range(B)]
+    run_chunks(g.eng, x_bits, [(0, 0), (90, 1), (140, 20)], lib, positions=lambda at, to: dev(
+        np.concatenate([p[:, a:t] for p, a, t in zip(pos, at, to)], axis=1).astype(np.int32)))
+    tok, ctx = np.array([5, 9], np.int32), dev(np.array(lengths, np.int32))
+    first = np.stack([np.full(3, p.max() + 1) for p in pos], axis=1).astype(np.int32)       # [3, B]
+    Q = torch.zeros((B * gamma, dims.V), device="cuda")
+    drafts = torch.zeros(B * gamma, dtype=torch.int32, device="cuda")
+    U = dev(synth.uniforms_f32(4, gamma * B).reshape(gamma, B))
+    g.draft(dev(tok), ctx, U, 1.0, Q, drafts, positions=dev(first))
+    lib.spec_device_status()
+    hidden, q, d = f64_of_bf16(g.eng.x[:B]), Q.cpu().numpy().astype(np.float64), drafts.cpu().numpy().reshape(B, gamma)
+    table = obf.decode(osw.w_lm)
+    for b in range(B):
+        n = lengths[b] + gamma
+        fed = table[[tok[b], *d[b, :-1]]]
+        at = np.concatenate([pos[b], first[:, b:b + 1] + np.arange(gamma)], axis=1)
+        zeros = [np.zeros((1, dims.Hkv, n, 128))]
+        x, lg, _, _ = ostack.verify_pass(np.concatenate([obf.decode(x_bits[b]), fed]), osw, od, [0, n], [0], zeros, zeros,
+                                         positions=at)
+        assert_close_chain(hidden[b:b + 1], x[-1:], 1, f"last drafted row of sequence {b}")
+        assert abs(q[b * gamma:(b + 1) * gamma] - oops.target_probs(lg[-gamma:], 1.0)).max() < STACK_PROB_BOUND
+    with pytest.raises(ValueError):
+        g.draft(dev(tok), ctx, U, 1.0, Q, drafts, positions=dev(first[:1]))
