@@ -311,3 +311,35 @@ def test_draft_behind_a_prompt_with_positions(lib, interleaved):
         assert abs(q[b * gamma:(b + 1) * gamma] - oops.target_probs(lg[-gamma:], 1.0)).max() < STACK_PROB_BOUND
     with pytest.raises(ValueError):
         g.draft(dev(tok), ctx, U, 1.0, Q, drafts, positions=dev(first[:1]))
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_unequal_axes_against_the_oracle(lib, interleaved):
+    """Prompt and verify rows at positions that differ between the axes: the oracle's pass at the same positions (with two
+    axes exchanged rows are off by 29 times the bound and more)."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(2, 103)
+    for d in (dims, od):
+        d.rope_sections, d.rope_interleaved = (24, 20, 20), interleaved
+    lengths, new = [140, 20], [3, 5]
+    pos = [grid_positions(n + m, 5 + b) for b, (n, m) in enumerate(zip(lengths, new))]
+    x_bits = [synth.normal_bf16_bits(310 + b, (p.shape[1], dims.d), 1.0) for b, p in enumerate(pos)]
+    cache = Paged(dims, [p.shape[1] for p in pos])
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=160, max_rows=5, block_table=cache.table)
+
+    def packed(at, to):
+        return dev(np.concatenate([p[:, a:t] for p, a, t in zip(pos, at, to)], axis=1).astype(np.int32))
+    got, _ = run_chunks(eng, x_bits, [(0, 0), (77, 3), (140, 20)], lib, positions=packed)
+    total = [n + m for n, m in zip(lengths, new)]
+    x0 = bf16_dev(np.concatenate([x[n:] for x, n in zip(x_bits, lengths)]))
+    P = eng.verify_pass(x0, dev(np.array([0, 3, 8], np.int32)), dev(np.array(lengths, np.int32)), 1.0,
+                        positions=packed(lengths, total))
+    lib.spec_device_status()
+    probs, verified = P.cpu().numpy().astype(np.float64), np.split(f64_of_bf16(eng.x[:8]), [3])
+    for b in range(2):
+        zeros = [np.zeros((1, dims.Hkv, total[b], 128))] * 2
+        x, lg, _, _ = ostack.verify_pass(obf.decode(x_bits[b]), osw, od, [0, total[b]], [0], zeros, zeros, positions=pos[b])
+        assert_close_chain(got[b], x[:lengths[b]], 2, f"prompt rows of sequence {b}")
+        assert_close_chain(verified[b], x[lengths[b]:], 2, f"verify rows of sequence {b}")
+        rows = slice(0, 3) if b == 0 else slice(3, 8)
+        assert abs(probs[rows] - oops.target_probs(lg[lengths[b]:], 1.0)).max() < STACK_PROB_BOUND
