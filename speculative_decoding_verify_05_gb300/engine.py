@@ -172,8 +172,10 @@ class VerifyEngine:
         self.ssq = torch.empty((max_M, (dims.d + 127) // 128), dtype=torch.float32, device=dev)
         self.norm_in = S.row_norm(in_ssq=self.ssq, eps=dims.eps) if fold_norms else None
         self.norm_out = S.row_norm(out_ssq=self.ssq) if fold_norms else None
-        # rows that reach the LM head: of a verify pass (a prompt's chunk is longer)
-        head_M = max_M if block_table is None else min(max_M, block_table.shape[0] * max_rows)
+        # rows that reach the LM head: of a verify pass (a prompt's chunk is longer), or a row of every slot
+        # (prefill, with or without rows of the slot in the chunk)
+        slots = 0 if block_table is None else block_table.shape[0]
+        head_M = max_M if block_table is None else max(slots, min(max_M, slots * max_rows))
         self.P = torch.empty((head_M, dims.V), dtype=torch.float32, device=dev) if weights.w_lm is not None else None
         B, cap = (kcaches[0].shape[0], kcaches[0].shape[2]) if kcaches else (1, 1)
         need = 0
@@ -286,13 +288,12 @@ class VerifyEngine:
             return self.x[:M]
         B = cu_rows.numel() - 1
         if M == 0:
-            return self.x[:0], torch.zeros((B, self.dims.V), dtype=torch.float32, device=self.device)
+            return self.x[:0], self.P[:B].zero_()
         # (cu_rows may hold anything: the kernels refuse what is outside the M rows with the status word set, and
         # so must no index here leave them)
         last = (cu_rows[1:] - 1).clamp_(0, M - 1)
         h = S.spec_rmsnorm(self.x[:M].index_select(0, last), self.w.final_norm, self.dims.eps)
-        P = self.P[:B] if B <= self.P.shape[0] else None
-        return self.x[:M], S.spec_lmhead_softmax(h, self.w.w_lm, temperature, P=P, ws=self.ws)
+        return self.x[:M], S.spec_lmhead_softmax(h, self.w.w_lm, temperature, P=self.P[:B], ws=self.ws)
 
     def verify_pass(self, x0, cu_rows, ctx_len, temperature: float, max_rows: int | None = None,
                     n_layers: int | None = None, positions=None):

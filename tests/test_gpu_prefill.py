@@ -343,3 +343,23 @@ def test_unequal_axes_against_the_oracle(lib, interleaved):
         assert_close_chain(verified[b], x[lengths[b]:], 2, f"verify rows of sequence {b}")
         rows = slice(0, 3) if b == 0 else slice(3, 8)
         assert abs(probs[rows] - oops.target_probs(lg[lengths[b]:], 1.0)).max() < STACK_PROB_BOUND
+
+
+def test_more_slots_than_chunk_rows(lib):
+    """40 slots and chunks of 8 rows at most: the LM head runs on a row per slot in the engine's own buffers (captured
+    rounds keep their pointers), and the probabilities of the slots with rows are the oracle's."""
+    from speculative_decoding_verify_05_gb300 import engine as E
+    dims, od, osw, gsw = _tiny_stack(1, 107)
+    lengths = [0] * 40
+    lengths[0], lengths[17], lengths[39] = 3, 4, 1
+    x_bits = [synth.normal_bf16_bits(320 + b, (n, dims.d), 1.0) for b, n in enumerate(lengths)]
+    cache = Paged(dims, [max(n, 1) for n in lengths])
+    eng = E.VerifyEngine(dims, gsw, cache.k, cache.v, max_M=8, max_rows=1, block_table=cache.table)
+    buf, size = eng.ws.buf.data_ptr(), eng.ws.buf.numel()
+    _, P = run_chunks(eng, x_bits, [[0] * 40, lengths], lib, temperature=1.0)
+    assert P.data_ptr() == eng.P.data_ptr() and P.shape == (40, dims.V)
+    assert (eng.ws.buf.data_ptr(), eng.ws.buf.numel()) == (buf, size)
+    assert size >= lib.spec_lmhead_workspace_bytes(40, dims.d, dims.V)
+    for b in (0, 17, 39):
+        _, lg = whole(osw, od, [x_bits[b]], [lengths[b]])
+        assert abs(P[b].cpu().numpy().astype(np.float64) - oops.target_probs(lg[0][-1:], 1.0)[0]).max() < STACK_PROB_BOUND
