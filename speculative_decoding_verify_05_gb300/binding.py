@@ -191,27 +191,46 @@ class Workspace:
     def __init__(self, device=None, nbytes: int = 0):
         self.device = torch.device("cuda") if device is None else torch.device(device)
         self.buf = None
+        self._cleared_on = None    # stream of the zero-fill, until the first call has been ordered behind it
         if nbytes:
             self.ensure(nbytes)
 
-    def ensure(self, nbytes: int) -> "Workspace":
+    def ensure(self, nbytes: int, stream=None) -> "Workspace":
+        """At least nbytes, allocated and cleared on `stream` (default: the current one)."""
         if nbytes and (self.buf is None or self.buf.numel() < nbytes):
-            self.buf = torch.zeros(int(nbytes), dtype=torch.uint8, device=self.device)
+            s = torch.cuda.current_stream(self.device) if stream is None else stream
+            if self.buf is not None:
+                self.buf.record_stream(s)      # calls on s may still be using it
+            with torch.cuda.stream(s):
+                self.buf = torch.zeros(int(nbytes), dtype=torch.uint8, device=self.device)
+            self._cleared_on = s
         return self
 
-    def args(self):
+    def args(self, stream=None):
+        """(pointer, bytes) for a call on `stream`."""
         if self.buf is None:
             return None, 0
+        if self._cleared_on is not None:
+            self._order(stream)
         return self.buf.data_ptr(), self.buf.numel()
 
+    def _order(self, stream):
+        if torch.cuda.is_current_stream_capturing():     # (a capture waits for the device before it begins)
+            return
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        if s != self._cleared_on:
+            s.wait_stream(self._cleared_on)
+            self.buf.record_stream(s)
+        self._cleared_on = None
 
-def _ws_args(ws: Workspace | None, need: int, device):
+
+def _ws_args(ws: Workspace | None, need: int, device, stream=None):
     if need == 0:
-        return (ws.args() if ws is not None else (None, 0))
+        return (ws.args(stream) if ws is not None else (None, 0))
     if ws is None:
         ws = Workspace(device)
-    ws.ensure(need)
-    return ws.args()
+    ws.ensure(need, stream)
+    return ws.args(stream)
 
 
 # --------------------------------------------------------------------------- verify linear
@@ -268,13 +287,13 @@ def spec_verify_linear(X, W, Y=None, residual=None, ws: Workspace | None = None,
     if residual is not None:
         _need(residual, torch.bfloat16, "residual")
     if norm is not None:
-        wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, N, K), X.device)
+        wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, N, K), X.device, stream)
         _check(_lib.spec_verify_linear_norm(
             _p(X), M, K, _rowmajor(X, "X"), _p(W), N, _rowmajor(W, "W"), _p(Y), _rowmajor(Y, "Y"),
             _p(residual), _rowmajor(residual, "residual") if residual is not None else 0,
             ctypes.byref(norm), wp, wn, _stream(stream)), True)
         return Y
-    wp, wn = _ws_args(ws, spec_linear_workspace_bytes(M, N, K), X.device)
+    wp, wn = _ws_args(ws, spec_linear_workspace_bytes(M, N, K), X.device, stream)
     _check(_lib.spec_verify_linear(
         _p(X), M, K, _rowmajor(X, "X"), _p(W), N, _rowmajor(W, "W"), _p(Y), _rowmajor(Y, "Y"),
         _p(residual), _rowmajor(residual, "residual") if residual is not None else 0,
@@ -337,7 +356,7 @@ def spec_verify_linear_chain(ops, M: int, ws=None, stream=None, device=None) -> 
     """Run the products `ops` (a list of linear_op(...)) over M rows in one weight stream."""
     arr = _op_array(ops)
     need = int(_lib.spec_linear_chain_workspace_bytes(arr, len(ops), int(M)))
-    wp, wn = _ws_args(ws, need, device if device is not None else torch.cuda.current_device())
+    wp, wn = _ws_args(ws, need, device if device is not None else torch.cuda.current_device(), stream)
     _check(_lib.spec_verify_linear_chain(arr, len(ops), int(M), wp, wn, _stream(stream)), True)
 
 
@@ -391,12 +410,12 @@ def spec_verify_linear_rope(X, W, cs, rope_heads: int, Y=None, ws: Workspace | N
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
     _need(Y, torch.bfloat16, "Y")
     if norm is not None:
-        wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, N, K), X.device)
+        wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, N, K), X.device, stream)
         _check(_lib.spec_verify_linear_rope_norm(_p(X), M, K, _rowmajor(X, "X"), _p(W), N, _rowmajor(W, "W"), _p(Y),
                                                  _rowmajor(Y, "Y"), _p(cs), int(rope_heads), ctypes.byref(norm), wp,
                                                  wn, _stream(stream)), True)
         return Y
-    wp, wn = _ws_args(ws, spec_linear_workspace_bytes(M, N, K), X.device)
+    wp, wn = _ws_args(ws, spec_linear_workspace_bytes(M, N, K), X.device, stream)
     _check(_lib.spec_verify_linear_rope(_p(X), M, K, _rowmajor(X, "X"), _p(W), N, _rowmajor(W, "W"), _p(Y),
                                         _rowmajor(Y, "Y"), _p(cs), int(rope_heads), wp, wn, _stream(stream)), True)
     return Y
@@ -433,12 +452,12 @@ def spec_verify_linear_swiglu(X, Wgu, A=None, ws: Workspace | None = None, strea
         A = torch.empty((M, inter), dtype=torch.bfloat16, device=X.device)
     _need(A, torch.bfloat16, "A")
     if norm is not None:
-        wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, inter, K, swiglu=True), X.device)
+        wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, inter, K, swiglu=True), X.device, stream)
         _check(_lib.spec_verify_linear_swiglu_norm(
             _p(X), M, K, _rowmajor(X, "X"), _p(Wgu), _rowmajor(Wgu, "Wgu"), inter,
             _p(A), _rowmajor(A, "A"), ctypes.byref(norm), wp, wn, _stream(stream)), True)
         return A
-    wp, wn = _ws_args(ws, spec_swiglu_linear_workspace_bytes(M, inter, K), X.device)
+    wp, wn = _ws_args(ws, spec_swiglu_linear_workspace_bytes(M, inter, K), X.device, stream)
     _check(_lib.spec_verify_linear_swiglu(
         _p(X), M, K, _rowmajor(X, "X"), _p(Wgu), _rowmajor(Wgu, "Wgu"), inter,
         _p(A), _rowmajor(A, "A"), wp, wn, _stream(stream)), True)
@@ -473,7 +492,7 @@ def spec_verify_attention(Q, Knew, Vnew, cu_rows, ctx_len, Kcache, Vcache, max_r
         O = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=Q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    wp, wn = _ws_args(ws, spec_attention_workspace_bytes(B, max_rows, Hq, Hkv, D, cap), Q.device)
+    wp, wn = _ws_args(ws, spec_attention_workspace_bytes(B, max_rows, Hq, Hkv, D, cap), Q.device, stream)
     _check(_lib.spec_verify_attention(
         _p(Q), _rowmajor(Q, "Q"), _p(Knew), _p(Vnew), ldkv, _p(cu_rows), _p(ctx_len), B,
         int(max_rows), _p(Kcache), _p(Vcache), cap, Hq, Hkv, D, float(scale), _p(O),
@@ -508,7 +527,7 @@ def spec_verify_attention_paged(Q, Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, b
         O = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=Q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    wp, wn = _ws_args(ws, spec_attention_paged_workspace_bytes(B, max_rows, Hq, Hkv, D, max_pages), Q.device)
+    wp, wn = _ws_args(ws, spec_attention_paged_workspace_bytes(B, max_rows, Hq, Hkv, D, max_pages), Q.device, stream)
     _check(_lib.spec_verify_attention_paged(
         _p(Q), _rowmajor(Q, "Q"), _p(Knew), _p(Vnew), ldkv, _p(cu_rows), _p(ctx_len), B, int(max_rows),
         _p(Kpool), _p(Vpool), num_pages, _p(block_table), max_pages, Hq, Hkv, D, float(scale), _p(O),
@@ -619,11 +638,11 @@ def spec_chunk_attention_paged(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, s
     Hq = width // D
     args = (Q.data_ptr(), ldq, cu_rows.data_ptr(), ctx_len.data_ptr(), B, M, Kpool.data_ptr(), Vpool.data_ptr(),
             num_pages, block_table.data_ptr(), max_pages, Hq, Hkv, D, scale, O.data_ptr(), ldo)
-    wp, wn = (None, 0) if ws is None else ws.args()
+    wp, wn = (None, 0) if ws is None else ws.args(stream)
     rc = _lib.spec_chunk_attention_paged(*args, wp, wn, _stream(stream))
     # (asking for the size first would cost a decode step's call another microsecond)
     if rc != SPEC_OK and wn < (need := spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages)):
-        wp, wn = _ws_args(ws, need, Q.device)
+        wp, wn = _ws_args(ws, need, Q.device, stream)
         rc = _lib.spec_chunk_attention_paged(*args, wp, wn, _stream(stream))
     _check(rc, True)
     return O
@@ -646,7 +665,7 @@ def spec_lmhead_softmax(H, Wlm, temperature: float, P=None, ws: Workspace | None
     _need(P, torch.float32, "P")
     if P.shape != (M, V) or P.stride(1) != 1:
         raise ValueError("P must be [M, V] with unit column stride")
-    wp, wn = _ws_args(ws, spec_lmhead_workspace_bytes(M, K, V), H.device)
+    wp, wn = _ws_args(ws, spec_lmhead_workspace_bytes(M, K, V), H.device, stream)
     if P.stride(0) == V:
         _check(_lib.spec_lmhead_softmax(_p(H), M, K, _p(Wlm), V, float(temperature), _p(P), wp, wn,
                                         _stream(stream)), True)
@@ -759,7 +778,7 @@ def spec_lmhead_reject_sample(H, W_lm, temperature: float, Q, draft_tok, U, cu_r
         out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(M, dtype=torch.int32, device=dev),
                torch.empty(B, dtype=torch.int32, device=dev))
     n_acc, out_tok, near = out
-    wp, wn = _ws_args(ws, spec_lmhead_sample_workspace_bytes(M, K, V, temperature), H.device)
+    wp, wn = _ws_args(ws, spec_lmhead_sample_workspace_bytes(M, K, V, temperature), H.device, stream)
     if norm is not None:
         _check(_lib.spec_lmhead_reject_sample_norm(_p(H), M, K, _p(W_lm), V, float(temperature), _p(Q),
                                                    _p(draft_tok), _p(U), _p(cu_rows), B, float(tie_eps), _p(n_acc),
