@@ -224,6 +224,17 @@ class Workspace:
         self._cleared_on = None
 
 
+def _empty(shape, dtype, device, stream):
+    """An output made for a call on `stream`.  On another stream than the current one it comes from that stream's memory (the
+    current one's may still be in use by what was issued before), and stays until the current one is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _ws_args(ws: Workspace | None, need: int, device, stream=None):
     if need == 0:
         return (ws.args(stream) if ws is not None else (None, 0))
@@ -263,7 +274,7 @@ def spec_row_ssq(X, out=None, stream=None):
     _need(X, torch.bfloat16, "X")
     M, N = X.shape
     if out is None:
-        out = torch.empty((M, (N + 127) // 128), dtype=torch.float32, device=X.device)
+        out = _empty((M, (N + 127) // 128), torch.float32, X.device, stream)
     _need(out, torch.float32, "out")
     _check(_lib.spec_row_ssq(_p(X), M, N, _rowmajor(X, "X"), _p(out), _stream(stream)), True)
     return out
@@ -282,7 +293,7 @@ def spec_verify_linear(X, W, Y=None, residual=None, ws: Workspace | None = None,
     if W.shape[1] != K:
         raise ValueError("W must be [N, K]")
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        Y = _empty((M, N), torch.bfloat16, X.device, stream)
     _need(Y, torch.bfloat16, "Y")
     if residual is not None:
         _need(residual, torch.bfloat16, "residual")
@@ -365,7 +376,7 @@ def spec_rope_table(cu_rows, ctx_len, M: int, D: int, theta: float = 1e6, cs=Non
     _need(cu_rows, torch.int32, "cu_rows"); _need(ctx_len, torch.int32, "ctx_len")
     B = cu_rows.numel() - 1
     if cs is None:
-        cs = torch.empty((M, D // 2, 2), dtype=torch.float32, device=cu_rows.device)
+        cs = _empty((M, D // 2, 2), torch.float32, cu_rows.device, stream)
     _need(cs, torch.float32, "cs")
     if not cs.is_contiguous():
         raise ValueError("cs must be contiguous")
@@ -385,7 +396,7 @@ def spec_rope_table_axes(pos, sections, D: int, theta: float = 1e6, interleaved:
     if len(sections) != axes or axes > 8:
         raise ValueError("sections must have an entry per axis of pos (8 at most)")
     if cs is None:
-        cs = torch.empty((M, D // 2, 2), dtype=torch.float32, device=pos.device)
+        cs = _empty((M, D // 2, 2), torch.float32, pos.device, stream)
     else:
         _need(cs, torch.float32, "cs")
         if not cs.is_contiguous() or cs.shape != (M, D // 2, 2):
@@ -407,7 +418,7 @@ def spec_verify_linear_rope(X, W, cs, rope_heads: int, Y=None, ws: Workspace | N
     if not cs.is_contiguous() or cs.shape[0] < M:
         raise ValueError("cs must be a contiguous table with a row per verify row")
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        Y = _empty((M, N), torch.bfloat16, X.device, stream)
     _need(Y, torch.bfloat16, "Y")
     if norm is not None:
         wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, N, K), X.device, stream)
@@ -449,7 +460,7 @@ def spec_verify_linear_swiglu(X, Wgu, A=None, ws: Workspace | None = None, strea
         raise ValueError("Wgu must be [2I, K] with I % 64 == 0")
     inter = N2 // 2
     if A is None:
-        A = torch.empty((M, inter), dtype=torch.bfloat16, device=X.device)
+        A = _empty((M, inter), torch.bfloat16, X.device, stream)
     _need(A, torch.bfloat16, "A")
     if norm is not None:
         wp, wn = _ws_args(ws, spec_linear_norm_workspace_bytes(M, inter, K, swiglu=True), X.device, stream)
@@ -489,7 +500,7 @@ def spec_verify_attention(Q, Knew, Vnew, cu_rows, ctx_len, Kcache, Vcache, max_r
     if _rowmajor(Vnew, "Vnew") != ldkv:
         raise ValueError("Knew and Vnew must share a leading dimension")
     if O is None:
-        O = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=Q.device)
+        O = _empty((M, Hq * D), torch.bfloat16, Q.device, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     wp, wn = _ws_args(ws, spec_attention_workspace_bytes(B, max_rows, Hq, Hkv, D, cap), Q.device, stream)
@@ -524,7 +535,7 @@ def spec_verify_attention_paged(Q, Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, b
     if _rowmajor(Vnew, "Vnew") != ldkv:
         raise ValueError("Knew and Vnew must share a leading dimension")
     if O is None:
-        O = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=Q.device)
+        O = _empty((M, Hq * D), torch.bfloat16, Q.device, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     wp, wn = _ws_args(ws, spec_attention_paged_workspace_bytes(B, max_rows, Hq, Hkv, D, max_pages), Q.device, stream)
@@ -628,7 +639,7 @@ def spec_chunk_attention_paged(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, s
     if width % D:
         raise ValueError("Q must be [M, Hq*D]")
     if O is None:
-        O, ldo = torch.empty(shape, dtype=_BF16, device=Q.device), width
+        O, ldo = _empty(shape, _BF16, Q.device, stream), width
     else:
         oshape, ldo = _rows_bf16(O, "O")
         if oshape != shape:
@@ -661,7 +672,7 @@ def spec_lmhead_softmax(H, Wlm, temperature: float, P=None, ws: Workspace | None
     if not (H.is_contiguous() and Wlm.is_contiguous()):
         raise ValueError("H and Wlm must be contiguous")
     if P is None:
-        P = torch.empty((M, V), dtype=torch.float32, device=H.device)
+        P = _empty((M, V), torch.float32, H.device, stream)
     _need(P, torch.float32, "P")
     if P.shape != (M, V) or P.stride(1) != 1:
         raise ValueError("P must be [M, V] with unit column stride")
@@ -681,7 +692,7 @@ def spec_embed(ids, table, X=None, stream=None):
     M = ids.numel()
     V, d = table.shape
     if X is None:
-        X = torch.empty((M, d), dtype=torch.bfloat16, device=table.device)
+        X = _empty((M, d), torch.bfloat16, table.device, stream)
     _need(X, torch.bfloat16, "X")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
@@ -699,8 +710,8 @@ def spec_reject_sample(P, Q, draft_tok, U, cu_rows, tie_eps: float = 1e-5, out=N
     B = cu_rows.numel() - 1
     if out is None:
         dev = P.device
-        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(M, dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev))
+        out = (_empty(B, torch.int32, dev, stream), _empty(M, torch.int32, dev, stream),
+               _empty(B, torch.int32, dev, stream))
     n_acc, out_tok, near = out
     for t in (P, Q, U, draft_tok, cu_rows):
         if not t.is_contiguous():
@@ -717,8 +728,8 @@ def spec_ngram_propose(tokens, cu_len, k: int, n_min: int, n_max: int, out=None,
         raise ValueError("tokens and cu_len must be contiguous")
     B = cu_len.numel() - 1
     if out is None:
-        out = (torch.empty((B, k), dtype=torch.int32, device=tokens.device),
-               torch.empty(B, dtype=torch.int32, device=tokens.device))
+        out = (_empty((B, k), torch.int32, tokens.device, stream),
+               _empty(B, torch.int32, tokens.device, stream))
     drafts, n = out
     _check(_lib.spec_ngram_propose(_p(tokens), _p(cu_len), B, int(k), int(n_min), int(n_max), _p(drafts), _p(n),
                                    _stream(stream)), True)
@@ -730,7 +741,7 @@ def spec_sample_rows(P, U, out=None, stream=None):
     _need(P, torch.float32, "P"); _need(U, torch.float32, "U")
     M, V = P.shape
     if out is None:
-        out = torch.empty(M, dtype=torch.int32, device=P.device)
+        out = _empty(M, torch.int32, P.device, stream)
     _check(_lib.spec_sample_rows(_p(P), _rowmajor(P, "P"), M, V, _p(U), _p(out), _stream(stream)), True)
     return out
 
@@ -744,8 +755,8 @@ def spec_typical_sample(P, draft_tok, U, cu_rows, epsilon: float, delta: float, 
     B = cu_rows.numel() - 1
     if out is None:
         dev = P.device
-        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(M, dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev))
+        out = (_empty(B, torch.int32, dev, stream), _empty(M, torch.int32, dev, stream),
+               _empty(B, torch.int32, dev, stream))
     n_acc, out_tok, near = out
     for t in (P, U, draft_tok, cu_rows):
         if not t.is_contiguous():
@@ -775,8 +786,8 @@ def spec_lmhead_reject_sample(H, W_lm, temperature: float, Q, draft_tok, U, cu_r
     B = cu_rows.numel() - 1
     if out is None:
         dev = H.device
-        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(M, dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev))
+        out = (_empty(B, torch.int32, dev, stream), _empty(M, torch.int32, dev, stream),
+               _empty(B, torch.int32, dev, stream))
     n_acc, out_tok, near = out
     wp, wn = _ws_args(ws, spec_lmhead_sample_workspace_bytes(M, K, V, temperature), H.device, stream)
     if norm is not None:
@@ -796,7 +807,7 @@ def spec_rmsnorm(X, w, eps: float = 1e-6, Y=None, stream=None):
     _need(X, torch.bfloat16, "X"); _need(w, torch.bfloat16, "w")
     M, N = X.shape
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        Y = _empty((M, N), torch.bfloat16, X.device, stream)
     _check(_lib.spec_rmsnorm(_p(X), M, N, _rowmajor(X, "X"), _p(w), float(eps), _p(Y),
                              _rowmajor(Y, "Y"), _stream(stream)), True)
     return Y
@@ -818,7 +829,7 @@ def spec_silu_mul(GU, A=None, stream=None):
     M, two_i = GU.shape
     inter = two_i // 2
     if A is None:
-        A = torch.empty((M, inter), dtype=torch.bfloat16, device=GU.device)
+        A = _empty((M, inter), torch.bfloat16, GU.device, stream)
     _check(_lib.spec_silu_mul(_p(GU), M, inter, _rowmajor(GU, "GU"), _p(A), _rowmajor(A, "A"),
                               _stream(stream)), True)
     return A

@@ -88,3 +88,44 @@ def test_workspace_grown_while_calls_run(lib):
     for c, O in zip((a, b), outs):
         ref, mag = c.oracle(1.0 / np.sqrt(D))
         assert_attended(f64_of_bf16(O).reshape(ref.shape), ref, mag, "grown workspace")
+
+
+@pytest.mark.parametrize("call", ["attention", "product", "table", "sampler"])
+def test_outputs_made_for_another_stream(lib, call):
+    """The current stream is about to write a block that it has already given back: an output of a call on another stream
+    must not lie in it.  And an output given up while that call still runs goes to nobody."""
+    side = torch.cuda.Stream()
+    if call == "attention":
+        c = Case(85, [2000], [0], 8, 2)
+        cu, ctx, kp, vp, table = c.dev()
+        q, ws = bf16_dev(c.q), lib.Workspace("cuda", lib.spec_chunk_attention_workspace_bytes(1, 2000, 8, 2, D, c.max_pages))
+        run = lambda **k: lib.spec_chunk_attention_paged(q, cu, ctx, kp, vp, table, ws=ws, **k)
+    elif call == "product":
+        x, w = (bf16_dev(synth.normal_bf16_bits(86 + i, (n, 1024), 1.0)) for i, n in enumerate((300, 2048)))
+        ws = lib.Workspace("cuda", max(lib.spec_linear_workspace_bytes(300, 2048, 1024), 1))
+        run = lambda **k: lib.spec_verify_linear(x, w, ws=ws, **k)
+    elif call == "table":
+        pos = torch.arange(3 * 5000, dtype=torch.int32, device="cuda").view(3, 5000)
+        run = lambda **k: lib.spec_rope_table_axes(pos, [16, 24, 24], 128, **k)
+    else:
+        P = torch.rand((4000, 512), device="cuda")
+        P, U = P / P.sum(dim=1, keepdim=True), torch.rand(4000, device="cuda")
+        run = lambda **k: lib.spec_sample_rows(P, U, **k)
+    want = run()
+    torch.cuda.synchronize()
+    nbytes = want.numel() * want.element_size()
+    old = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(BUSY)
+    old.fill_(255)
+    del old
+    got = run(stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    # given up at once: a block of the same size, filled on the current stream, stays as it was filled
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    run(stream=side)
+    fresh = torch.full((nbytes,), 7, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    lib.spec_device_status(side)
+    assert bool((fresh == 7).all())
