@@ -106,7 +106,14 @@ __device__ __forceinline__ void st_past_l1(uint16_t* p, const uint4& v) {
                : "memory");
 }
 
-// One CTA per row.  A thread moves pairs of 16-byte chunks (dims i0 .. and 64 + i0 ..) of heads 4 WARPS apart, so
+// Whether a sequence is outside the M rows or past its table's keys (its length and pages count only if it has rows).
+__device__ __forceinline__ bool out_of_bounds(int c0, int c1, int ctx, const KvAppendArgs& a) {
+  return c0 < 0 || c1 < c0 || c1 > a.M ||
+         (c1 > c0 && (ctx < 0 || (long long)ctx + (c1 - c0) > (long long)a.max_pages * PAGE));
+}
+
+// One CTA per row, and behind them a thread per sequence that checks its bounds (no row has to be in a sequence that
+// breaks them).  A thread of a row moves pairs of 16-byte chunks (dims i0 .. and 64 + i0 ..) of heads 4 WARPS apart, so
 // its eight angles stay in registers; up to UNITS pairs are loaded before the row's place in the cache is known,
 // which takes two dependent loads.  Bound by HBM: 8192 rows of 32 + 2 x 8 heads, 206 MB, take 32.9 us (6.3 TB/s),
 // 24 sequences of 1 to 999 rows, 81 MB, 13.9 us (5.8).
@@ -123,6 +130,11 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArg
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, tid = threadIdx.x, i0 = (tid & 7) * 8;
+  if (r >= a.M) {
+    const long long b = (long long)(r - a.M) * (32 * WARPS) + tid;
+    if (b < a.B && out_of_bounds(a.cu_rows[b], a.cu_rows[b + 1], a.ctx_len[b], a)) set_status(a.status, 0x6F1u);
+    return;
+  }
   const int heads = a.Hq + 2 * a.Hkv;
   float4 t[4];                                          // (cos, sin) of dims i0 ..
   if constexpr (TURN)
@@ -146,10 +158,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArg
       const Place at = place_of(r, a, tid & 31);
       b = at.b;
       if (b < 0 || r >= at.c1) return;                  // padding
-      if (at.c0 < 0 || at.c1 > a.M || at.ctx < 0 || (long long)at.ctx + (at.c1 - at.c0) > (long long)a.max_pages * PAGE) {
-        if (tid == 0) set_status(a.status, 0x6F1u);
-        return;
-      }
+      if (out_of_bounds(at.c0, at.c1, at.ctx, a)) return;
       p = at.ctx + (r - at.c0);
       page = a.block_table[(size_t)b * a.max_pages + p / PAGE];
       if (page < 0 || page >= a.num_pages) {
@@ -203,7 +212,8 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s) {
   const dim3 block(many ? 64 : 128);
   auto* turn = many ? kv_append_kernel<2, 2, true> : kv_append_kernel<4, 4, true>;
   auto* copy = many ? kv_append_kernel<2, 2, false> : kv_append_kernel<4, 4, false>;
-  cudaError_t e = launch_k(a.cs ? turn : copy, dim3(a.M), block, 0, s, a);
+  const unsigned checks = ((unsigned)a.B + block.x - 1) / block.x;
+  cudaError_t e = launch_k(a.cs ? turn : copy, dim3((unsigned)a.M + checks), block, 0, s, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -603,3 +603,37 @@ def test_attention_reach_of_a_non_finite_new_key(lib, Hq, Hkv, block, what):
         clean[block:rows, heads, dim] = False
         assert not np.any(np.isfinite(got[at:rows, heads, dim]))
     assert_attended(got[clean], ref[clean], mag[clean], what)
+
+
+@pytest.mark.parametrize("cu,good", [
+    ([0, 2, 5, 9], 2), ([0, 2, 1 << 30, 1 << 30], 1), ([0, 5, 5, 6], 1), ([-4, 0, 2, 5], 0), ([0, 5, 3, 3], 1),
+    ([0] * 300 + [2, 5, 9], 301)])
+@pytest.mark.parametrize("rotate", [True, False])
+def test_append_flags_every_sequence_out_of_bounds(lib, cu, good, rotate):
+    """Five rows, and sequences that leave them: the status word is set whether or not one of the rows is theirs, the
+    sequences before the first bad one get theirs, and a batch in bounds leaves the word alone."""
+    B, M = len(cu) - 1, 5
+    bits = synth.normal_bf16_bits(73, (M, 4 * D), 1.0)
+    kv, ctx = bf16_dev(bits), dev(np.full(B, 7, np.int32))
+    table = dev(np.arange(B, dtype=np.int32)[:, None].copy())
+    cs = torch.zeros((M, 64, 2), device="cuda")
+    cs[..., 0] = 1.0                                        # (a rotation by 0)
+
+    def append(cu):
+        kp, vp = (torch.zeros((2, B, PAGE, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lib.spec_kv_append_paged(kv[:, :2 * D], kv[:, 2 * D:], dev(np.array(cu, np.int32)), ctx, kp, vp, table,
+                                 cs=cs if rotate else None)
+        rc, _ = lib.spec_device_status_code()
+        lib.spec_device_status()
+        return rc, bits_of(kp)
+
+    rc, kp = append(cu)
+    assert rc == lib.SPEC_EINVAL
+    want = np.zeros_like(kp)
+    for b in range(good):
+        for j in range(cu[b + 1] - cu[b]):
+            want[:, b, 7 + j] = bits[cu[b] + j, :2 * D].reshape(2, D)
+    if cu[0] >= 0 and cu == sorted(cu):
+        assert np.array_equal(kp, want)
+    rc, _ = append([min(max(c, 0), M) for c in sorted(cu)])
+    assert rc == lib.SPEC_OK
