@@ -1190,7 +1190,7 @@ int spec_rope_table_axes(const int32_t* pos, int ldpos, int axes, int M, int D, 
     t -= std::floor(t);
     f.turn[i] = (unsigned long long)std::ldexp(t, 64);
   }
-  cudaError_t e = launch_rope_table_axes(pos, ldpos, M, half, f, reinterpret_cast<float2*>(cs),
+  cudaError_t e = launch_rope_table_axes(pos, ldpos, M, half, f, reinterpret_cast<float2*>(cs), plan_sms(),
                                          static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope_table_axes launch");
   return ok(1);
@@ -1734,7 +1734,7 @@ int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr,
   a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages;
   a.Hq = Q ? Hq : 0; a.Hkv = Hkv;
   a.status = d->status;
-  cudaError_t e = launch_kv_append(a, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_kv_append(a, d->sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
   return ok(1);
 }

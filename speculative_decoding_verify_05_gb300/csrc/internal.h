@@ -193,7 +193,7 @@ struct RopeAxes {
   unsigned char axis[128];        // its position axis
 };
 cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int half, const RopeAxes& f, float2* cs,
-                                   cudaStream_t s);
+                                   int sms, cudaStream_t s);
 struct KvAppendArgs {
   const uint16_t* Q; int ldq;           // nullptr: no queries
   uint16_t* Qrot; int ldqr;
@@ -206,7 +206,7 @@ struct KvAppendArgs {
   int num_pages, max_pages, Hq, Hkv;    // Hq = 0 without queries
   unsigned* status;
 };
-cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
+cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t s);
 struct ChunkAttnArgs {
   const uint16_t* Q; int ldq;
   const int32_t* cu_rows; const int32_t* ctx_len;

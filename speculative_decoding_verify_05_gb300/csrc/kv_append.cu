@@ -197,18 +197,18 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const KvAppendArg
 
 }  // namespace
 
-cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int half, const RopeAxes& f, float2* cs,
+cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int half, const RopeAxes& f, float2* cs, int sms,
                                    cudaStream_t s) {
   // rows per thread: one while that fills the chip, more (up to 8) when there are many
   const int bx = (half + 31) / 32 * 32, by = bx < 256 ? 256 / bx : 1;
-  const int fill = M / (by * 152 * 2), rows = fill < 1 ? 1 : (fill > 8 ? 8 : fill);
+  const int fill = M / (by * sms * 2), rows = fill < 1 ? 1 : (fill > 8 ? 8 : fill);
   cudaError_t e = launch_k(rope_table_axes_kernel, dim3((unsigned)((M + by * rows - 1) / (by * rows))), dim3(bx, by), 0, s,
                            pos, ldpos, M, half, rows, f, cs);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s) {
-  const bool many = a.M > 10 * 152;
+cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t s) {
+  const bool many = a.M > 10 * sms;
   const dim3 block(many ? 64 : 128);
   auto* turn = many ? kv_append_kernel<2, 2, true> : kv_append_kernel<4, 4, true>;
   auto* copy = many ? kv_append_kernel<2, 2, false> : kv_append_kernel<4, 4, false>;
