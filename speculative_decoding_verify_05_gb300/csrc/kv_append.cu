@@ -59,9 +59,9 @@ rope_table_axes_kernel(const int32_t* __restrict__ pos, int ldpos, int M, int ha
   if (i >= half) return;
   const unsigned long long turn = as_memory(f.turn)[i];
   const int32_t* p = pos + (size_t)as_memory(f.axis)[i] * ldpos;
-  const int r0 = (blockIdx.x * blockDim.y + threadIdx.y) * rows, r1 = min(r0 + rows, M);
+  const unsigned r0 = (blockIdx.x * blockDim.y + threadIdx.y) * rows, r1 = min(r0 + rows, (unsigned)M);
 #pragma unroll 4
-  for (int r = r0; r < r1; ++r) cs[(size_t)r * half + i] = cos_sin_turns((unsigned long long)(long long)p[r] * turn);
+  for (unsigned r = r0; r < r1; ++r) cs[(size_t)r * half + i] = cos_sin_turns((unsigned long long)(long long)p[r] * turn);
 }
 
 // The last sequence with cu_rows[b] <= r, 32 candidates at a time by a whole warp; its lengths come with the last
@@ -202,7 +202,7 @@ cudaError_t launch_rope_table_axes(const int32_t* pos, int ldpos, int M, int hal
   // rows per thread: one while that fills the chip, more (up to 8) when there are many
   const int bx = (half + 31) / 32 * 32, by = bx < 256 ? 256 / bx : 1;
   const int fill = M / (by * sms * 2), rows = fill < 1 ? 1 : (fill > 8 ? 8 : fill);
-  cudaError_t e = launch_k(rope_table_axes_kernel, dim3((unsigned)((M + by * rows - 1) / (by * rows))), dim3(bx, by), 0, s,
+  cudaError_t e = launch_k(rope_table_axes_kernel, dim3(((unsigned)M + by * rows - 1) / (by * rows)), dim3(bx, by), 0, s,
                            pos, ldpos, M, half, rows, f, cs);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

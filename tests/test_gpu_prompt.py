@@ -637,3 +637,20 @@ def test_append_flags_every_sequence_out_of_bounds(lib, cu, good, rotate):
         assert np.array_equal(kp, want)
     rc, _ = append([min(max(c, 0), M) for c in sorted(cu)])
     assert rc == lib.SPEC_OK
+
+
+def test_table_of_the_most_rows(lib):
+    """2^31 - 1 rows of a table with one frequency: the last ones (and none behind them) are written."""
+    M = 2 ** 31 - 1
+    pos = torch.zeros((1, M), dtype=torch.int32, device="cuda")
+    pos[0, -100:] = torch.arange(100, dtype=torch.int32, device="cuda")
+    buf = torch.full((M + 9, 1, 2), 5.0, device="cuda")
+    lib.spec_rope_table_axes(pos, [1], 2, cs=buf[:M])
+    lib.spec_device_status()
+    ref = oprompt.rope_table_axes(np.arange(100)[None], [1], 2, 1e6, False)
+    assert abs(buf[M - 100:M].cpu().numpy() - ref).max() <= table_tol(100)
+    assert bool((buf[M:] == 5.0).all()) and bool((buf[:1000, 0, 0] == 1.0).all())
+    sample = buf[:M - 100:12345, 0]
+    assert bool((sample[:, 0] == 1.0).all()) and bool((sample[:, 1] == 0.0).all())
+    del pos, buf, sample
+    torch.cuda.empty_cache()
