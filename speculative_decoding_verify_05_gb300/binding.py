@@ -134,11 +134,16 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+_INT_MAX = (1 << 31) - 1     # (ctypes cuts what is larger off without a word)
+
+
 def _rowmajor(t: torch.Tensor, name: str) -> int:
     """Leading dimension of a 2-D tensor whose rows are contiguous."""
     strides = t.stride()
     if len(strides) != 2 or strides[1] != 1:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    if strides[0] > _INT_MAX:
+        raise ValueError(f"{name}: leading dimension {strides[0]} is above 2^31 - 1")
     return strides[0]
 
 
@@ -579,10 +584,7 @@ def _rows_bf16(t, name):
     """Shape and leading dimension of a 2-D bf16 tensor whose rows are contiguous."""
     if t.dtype is not _BF16 or not t.is_cuda:
         _need(t, _BF16, name)
-    strides = t.stride()
-    if len(strides) != 2 or strides[1] != 1:
-        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    return t.shape, strides[0]
+    return t.shape, _rowmajor(t, name)
 
 
 def spec_kv_append_paged(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table, cs=None, Q=None, Qrot=None,

@@ -654,3 +654,25 @@ def test_table_of_the_most_rows(lib):
     assert bool((sample[:, 0] == 1.0).all()) and bool((sample[:, 1] == 0.0).all())
     del pos, buf, sample
     torch.cuda.empty_cache()
+
+
+def test_binding_refuses_what_does_not_fit_32_bits(lib):
+    """Leading dimensions above 2^31 - 1 are refused, not cut off: cut, the first would be 1024."""
+    c = Case(74, [2], [0], 8, 2)
+    cu, ctx, kp, vp, table = c.dev()
+    far = torch.empty((1 << 32) + 2048, dtype=torch.bfloat16, device="cuda").as_strided((2, 8 * D), ((1 << 32) + 8 * D, 1))
+    near = bf16_dev(c.q)
+    with pytest.raises(ValueError, match="leading dimension"):
+        lib.spec_chunk_attention_paged(far, cu, ctx, kp, vp, table)
+    with pytest.raises(ValueError, match="leading dimension"):
+        lib.spec_chunk_attention_paged(near, cu, ctx, kp, vp, table, O=far)
+    with pytest.raises(ValueError, match="leading dimension"):
+        lib.spec_kv_append_paged(far[:, :2 * D], far[:, 2 * D:4 * D], cu, ctx, kp, vp, table)
+    with pytest.raises(ValueError, match="leading dimension"):
+        lib.spec_verify_linear(far, torch.zeros((128, 8 * D), dtype=torch.bfloat16, device="cuda"))
+    del far
+    wide = torch.empty((1, 1 << 31), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="leading dimension"):
+        lib.spec_rope_table_axes(wide, [1], 2)
+    del wide
+    torch.cuda.empty_cache()
