@@ -98,3 +98,21 @@ def test_workspace_query_is_host_only(S):
     assert S.spec_chunk_attention_workspace_bytes(9, 1000, 32, 8, 128, 64) >= n
     assert S.spec_chunk_attention_workspace_bytes(8, 2000, 32, 8, 128, 64) >= n
     assert S.spec_chunk_attention_workspace_bytes(0, 1000, 32, 8, 128, 64) == 0
+
+
+def test_workspace_follows_the_grid(S):
+    """The attention's workspace is that of its CTAs (two slots of 256 rows each, fp32 outputs, references and sums) behind the
+    counters, whatever the batch; one that was sized for fewer CTAs is refused."""
+    size = lambda: S.spec_chunk_attention_workspace_bytes(2, 5, 8, 2, 128, 2)
+    of = lambda ctas: 64 * 1024 + ctas * 2 * 256 * (128 * 4 + 16)
+    try:
+        for ctas in (1, 37, 600):
+            S.spec_set_option("persistent_grid", ctas)
+            assert size() == of(ctas) == S.spec_chunk_attention_workspace_bytes(900, 100000, 40, 8, 128, 64)
+            assert attn_args(S, ws_bytes=of(ctas) - 1) == S.SPEC_EINVAL
+            assert b"workspace" in S._lib.spec_last_error()
+        S.spec_set_option("persistent_grid", 4096)
+        assert size() == of(1024)                        # (the most CTAs that the counters have room for)
+    finally:
+        S.spec_set_option("persistent_grid", 0)
+    assert size() > 64 * 1024
