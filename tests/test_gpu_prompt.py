@@ -676,3 +676,53 @@ def test_binding_refuses_what_does_not_fit_32_bits(lib):
         lib.spec_rope_table_axes(wide, [1], 2)
     del wide
     torch.cuda.empty_cache()
+
+
+def test_pools_past_32_bits(lib):
+    """Pages whose elements lie past 2^31 of a pool (and past 2^32 bytes): append and attention of a few rows."""
+    pages, Hkv, rows = 70000, 2, 150
+    kp, vp = (torch.zeros((Hkv, pages, PAGE, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = np.array([[69999, 69000], [3, 66001]], np.int32)
+    bits = synth.normal_bf16_bits(75, (2 * rows, (4 + 2 * Hkv) * D), 1.0)
+    x = bf16_dev(bits)
+    q, k, v = x[:, :4 * D], x[:, 4 * D:6 * D], x[:, 6 * D:]
+    cu, ctx = dev(np.array([0, rows, 2 * rows], np.int32)), dev(np.zeros(2, np.int32))
+    lib.spec_kv_append_paged(k, v, cu, ctx, kp, vp, dev(table))
+    O = lib.spec_chunk_attention_paged(q, cu, ctx, kp, vp, dev(table))
+    lib.spec_device_status()
+    dec = obf.decode(bits)
+    pool = np.zeros((2, Hkv, 4, PAGE, D))
+    small = np.array([[0, 1], [2, 3]])
+    kv = [dec[:, a:a + 2 * D].reshape(-1, Hkv, D) for a in (4 * D, 6 * D)]
+    kk, vv = oprompt.kv_append(*kv, [0, rows, 2 * rows], [0, 0], *pool, small)
+    for got, want in ((kp, kk), (vp, vv)):
+        assert np.array_equal(f64_of_bf16(got[:, torch.from_numpy(table.reshape(-1)).long().cuda()]), want)
+    ref, mag = oprompt.chunk_attention(dec[:, :4 * D].reshape(-1, 4, D), [0, rows, 2 * rows], [0, 0], kk, vv, small,
+                                       1.0 / np.sqrt(D))
+    assert_attended(f64_of_bf16(O).reshape(ref.shape), ref, mag, "pages past 32 bits")
+    del kp, vp
+    torch.cuda.empty_cache()
+
+
+def test_two_graphs_on_one_workspace(lib):
+    """Two captured calls of other shapes on one workspace, replayed in turn on one stream."""
+    cases = [Case(76, [3, 40], [9000, 700], 8, 2), Case(77, [300, 1, 0], [0, 5000, 4], 16, 8)]
+    ws = lib.Workspace("cuda")
+    graphs = []
+    for c in cases:
+        args = (bf16_dev(c.q), *c.dev())
+        O = torch.zeros((c.M, c.Hq * D), dtype=torch.bfloat16, device="cuda")
+        lib.spec_chunk_attention_paged(*args, O=O, ws=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lib.spec_chunk_attention_paged(*args, O=O, ws=ws)
+        graphs.append((c, args, O, graph))
+    for _ in range(3):
+        for _, _, O, graph in graphs:
+            O.fill_(4.0)
+            graph.replay()
+        for c, _, O, _ in graphs:
+            ref, mag = c.oracle(1.0 / np.sqrt(D))
+            assert_attended(f64_of_bf16(O).reshape(ref.shape), ref, mag, "replayed in turn")
+    lib.spec_device_status()
