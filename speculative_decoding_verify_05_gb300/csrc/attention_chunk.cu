@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 }
 // The library's bounded wait, short: thirty of them are in this kernel, and what runs once per piece runs from a
 // cold instruction cache.  Each role tells the status word itself when one ran out.
-// (The limit is in cycles, a second or more: the wall clock takes long to read.)
+// (The limit is in cycles, a second or more at the chip's clocks: the wall clock takes long to read.)
 constexpr uint32_t WAIT_CYCLES = 1u << 31;
 __device__ __forceinline__ uint32_t cycles() {
   uint32_t t;

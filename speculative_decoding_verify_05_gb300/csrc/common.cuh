@@ -1,6 +1,7 @@
 // Shared device helpers for the sm_103a kernels: bf16 packing, mbarriers,
 // TMA (cp.async.bulk.tensor), tcgen05 (TMEM alloc / MMA / commit / load),
-// and bounded waits.  Every wait gives up after SPEC_WAIT_NS of wall time,
+// and bounded waits.  Every wait gives up after SPEC_WAIT_NS of wall time
+// (the chunk attention's, which count cycles, after about half of that),
 // records a site code in the library status word and lets the caller bail out.
 #pragma once
 

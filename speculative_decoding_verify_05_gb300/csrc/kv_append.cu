@@ -14,7 +14,8 @@ constexpr int PAGE = 128;
 
 // (cos, sin) of u / 2^64 turns.  The position times the frequency is formed modulo one turn in 64-bit integers
 // (wrap-around is the reduction, exact for any 32-bit position), the nearest quarter turn is split off,
-// and what is left, at most an eighth of a turn, is exact to 2^-33 turns before its one rounding to fp32.  There
+// and what is left, at most an eighth of a turn, is off by less than 2^-32 turns (the low word is dropped) before its
+// one rounding to fp32.  There
 // the Taylor series of sin(pi x) and cos(pi x) on |x| <= 1/4 (terms to (pi x)^9 and (pi x)^10: the next are below
 // 2e-9) take 11 multiply-adds; sincospif, which has the whole line to care for, took 1.7 us
 // more for the 16000-row table.  No fp64 instruction: the chip has few of them.
