@@ -26,10 +26,12 @@
 // Bound.  With many rows, the tensor cores: a key tile's four products of 128^3 take 2048 of their cycles, in which
 // the softmax warps have to form 256 x 128 weights, which is why nothing else is in their way: a
 // maximum once per row (the reference below), two fp32 operations per instruction, a row per thread.  A prompt of 8192 rows
-// (32 + 2 x 8 heads) takes 320 us = 1715 TFLOP/s, 2048 rows at 30000 keys 640 us = 1630.  With few rows, HBM: 61 rows
-// at 131000 keys 99 us = 5.4 TB/s, 16 x 32 rows at 4000 keys 47 us = 5.8 TB/s.  In between and below, what a
+// (32 + 2 x 8 heads) takes 317 us = 1735 TFLOP/s, 2048 rows at 30000 keys 655 us = 1590.  With few rows, HBM: 61 rows
+// at 131000 keys 97 to 101 us = 5.4 TB/s, 16 x 32 rows at 4000 keys 47 us = 5.8 TB/s.  (That is for some tens of calls. In
+// seconds of them the power limit takes the clock from 2.05 to 1.7 GHz and below: 330 to 360 us for the prompt,
+// 106 to 112 us for the 61 rows, from a graph and called one by one alike.)  In between and below, what a
 // call costs whatever its size: 4 to 5 us to the first product (lengths, the CTA's pieces, page table, first
-// tiles) and, where items are shared, about 8 us to join them; one token of 4 sequences (12.9 us) pays the first,
+// tiles) and, where items are shared, about 8 us to join them; one token of 4 sequences (13.0 us) pays the first,
 // a chunk of 512 at 7680 keys (55 us) both.
 //
 // Roles (12 warps): 0-3 and 4-7 softmax and epilogue of slot 0 and 1 (thread = TMEM lane = row); 8 loads K
@@ -188,7 +190,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // 32 bytes to a 32-byte boundary: a row per lane then fills whole sectors (as 16-byte stores the outputs of a prompt of
 // 8192 rows took 24 us more; exchanged between lanes first to fill lines, 8 us more).  Past L1, whose lines the 32 rows
-// of a warp would take one each (8 prompts of 500 rows 30.2 us without the hint, 27.5 with it).
+// of a warp would take one each (8 prompts of 500 rows 30.9 us without the hint, 28.1 with it).
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
   asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
                "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -248,7 +250,7 @@ struct Shares {
 };
 // Equal shares, but of so many keys that an item's pieces are not joined for longer than they take: with `keys` of the
 // longest item and a piece's reading back as long as PIECE_KEYS, n sharers take keys / n and n PIECE_KEYS (9 rows of 5
-// heads at 63118 keys: 63 us with 152 sharers, 28 with 42).  inv_grid = floor((2^64 - 1) / grid).
+// heads at 63118 keys: 63 us with 152 sharers, 27.6 with 42).  inv_grid = floor((2^64 - 1) / grid).
 __device__ __forceinline__ Shares shares_of(const ChunkAttnArgs& a, long long total, int keys) {
   const long long even = (long long)__umul64hi((unsigned long long)total, a.inv_grid) + 1;
   return Shares{total, max(even, (long long)(W_ONE * sqrtf((float)PIECE_KEYS * keys)))};
@@ -473,8 +475,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
       if (bad && blockIdx.x == 0) set_status(a.status, 0x7F1u);
       // Where they come out about even, whole items, the longest first, dealt to the CTAs in rows that run forth and
-      // back: nothing is left to join.  (8 prompts of 100 to 1900 rows 39.7 us, cut 52.2; one of 2048 rows 29.2,
-      // cut 41.2; of 8192 rows 318, cut 335; 16 x 32 rows at 4000 keys 47.0, cut 53.1.)  What the deal leaves uneven
+      // back: nothing is left to join.  (8 prompts of 100 to 1900 rows 40.4 us, cut 53.5; one of 2048 rows 29.2,
+      // cut 42.6; of 8192 rows 317, cut 335; 16 x 32 rows at 4000 keys 46.8, cut 53.9.)  What the deal leaves uneven
       // is about the longest item of the last row times the share of the CTAs that the row leaves out: the rule is
       // that this costs less than joining.  Over 20 batches it took the faster side, or one within 1 us of it.  Items of
       // one tile are never cut.
@@ -1245,7 +1247,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         // is then 1, exactly.  (bf16 weights are off by 1.7e-3 each in rms; a reference that is no maximum leaves that
         // to the largest weight too: rows of 16 keys 2.3e-3 off instead of 1.85e-3, of 128 keys 2.35e-3 instead of
         // 1.9e-3, logits of a few units; and scores far below a reference of 0 take small values out of fp32's range.
-        // Looking costs 1 to 3 % on short prompts: 8 of 500 rows 27.5 -> 28.3 us, of 100 to 1900 rows 40.0 -> 40.9.)
+        // Looking costs 1 to 3 % on short prompts: 8 of 500 rows 27.2 -> 28.1 us, of 100 to 1900 rows 39.5 -> 40.4.)
         // Later tiles keep it, so that they need not wait for a maximum: any reference down to 2^20 below
         // the maximum gives the same quotients (bf16 and fp32 have exponents to spare, with values up to 1e25).
         // The tile's sum tells when it is out of that range; then the maximum is taken, O rescaled, and the weights
