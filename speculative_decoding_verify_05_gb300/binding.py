@@ -186,6 +186,13 @@ def spec_probe_bounded_wait(limit_us: int, arrive: bool = False, stream=None) ->
     _check(_lib.spec_probe_bounded_wait(int(limit_us), 1 if arrive else 0, _stream(stream)), compute=True)
 
 
+def _zeros(nbytes, device, stream):
+    if stream is None:
+        return torch.zeros(int(nbytes), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(int(nbytes), dtype=torch.uint8, device=device)
+
+
 class Workspace:
     """A zero-filled device buffer that grows on demand (plumbing for the kernels' scratch).
 
@@ -206,8 +213,7 @@ class Workspace:
             s = torch.cuda.current_stream(self.device) if stream is None else stream
             if self.buf is not None:
                 self.buf.record_stream(s)      # calls on s may still be using it
-            with torch.cuda.stream(s):
-                self.buf = torch.zeros(int(nbytes), dtype=torch.uint8, device=self.device)
+            self.buf = _zeros(nbytes, self.device, stream)
             self._cleared_on = s
         return self
 
@@ -241,11 +247,11 @@ def _empty(shape, dtype, device, stream):
 
 
 def _ws_args(ws: Workspace | None, need: int, device, stream=None):
-    if need == 0:
-        return (ws.args(stream) if ws is not None else (None, 0))
     if ws is None:
-        ws = Workspace(device)
-    ws.ensure(need, stream)
+        # (given back at once, to the pool of the call's stream: whatever comes to lie there is issued behind the call)
+        return (_zeros(need, device, stream).data_ptr(), need) if need else (None, 0)
+    if need:
+        ws.ensure(need, stream)
     return ws.args(stream)
 
 
