@@ -476,6 +476,67 @@ SPEC_API int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32
                                         size_t workspace_bytes, spec_stream stream);
 
 /* ------------------------------------------------------------------------ */
+/* Norms of queries and keys, and a paged cache in 4 bits                    */
+/* ------------------------------------------------------------------------ */
+/* RMSNorm of each query and key head over its D dims, and the rotation, in one pass (a stack that normalises
+ * q and k between the projection and the rotation):
+ *   y = x / sqrt(mean(x^2) + eps) * w, then rotate-half pairs (i, i + D/2) by cs[r]
+ * fp32, every operation rounded once, the squares summed neighbours first (1, 2, 4 .. apart), one rounding to bf16.
+ *   Q, Qout  row r, query head h at + r*ldq + h*D / + r*ldqo + h*D; Qout may be Q itself (same leading
+ *            dimension); Hq = 0: no queries (Q, Qout, wq ignored)
+ *   K, Kout  the same for Hkv key heads; Hkv = 0: no keys
+ *   wq, wk   [D] bf16
+ *   cs       [M x D/2] pairs (cos, sin) (spec_rope_table / _axes), 16-byte aligned, or NULL: no rotation
+ * Requires D == 128, eps finite and >= 0, leading dimensions multiples of 8, 16-byte aligned pointers.
+ * One kernel, no workspace. */
+SPEC_API int spec_qk_norm_rope(const spec_bf16* Q, int ldq, spec_bf16* Qout, int ldqo, const spec_bf16* K, int ldk,
+                               spec_bf16* Kout, int ldko, const spec_bf16* wq, const spec_bf16* wk, float eps,
+                               const float* cs, int M, int Hq, int Hkv, int D, spec_stream stream);
+
+/* A cache in 4 bits: pools [Hkv][num_pages][SPEC_Q4_PAGE_BYTES], a page 128 keys of one kv head, 4.25 bits
+ * per value instead of bf16's 16 (3.76 times as many tokens in the same memory, and as many fewer bytes for an
+ * attention to read).  Each value is a whole number of -7 .. 7 times the scale of the 32 dims (32 g ..) it lies with:
+ *   t = max |x| / 7 clamped to 2^-20 .. 3840, scale = t to 3 bits behind the leading one (nearest, halves to even),
+ *   n = x / scale to the nearest (halves to even), -7 .. 7
+ * all in fp32 (every operation rounded once).  So values are off by half a scale at most (about a fourteenth of
+ * their group's largest); magnitudes above 26880 and infinities become 26880 (and take their group's scale with
+ * them), NaN becomes 0: what a cache returns is always finite.  A page's bytes: 4 planes of 128 rows of 16 bytes (32
+ * entries each), then 512 scales; byte c of a scale stands for (1 + (c & 7) / 8) 2^((c >> 3) - 20).
+ *   keys    plane q, row k: dims 32 q .. 32 q + 31 of key k;  scale of dims 32 g .. of key k at byte 4 k + g
+ *   values  plane q, row d: keys 32 q .. 32 q + 31 of dim d;  scale of dims 32 g .. of key k at byte 128 g + k
+ * A row's 16 bytes are 4 words (little endian) of 8 entries: n + 8 of entries 0, 2, 4, 6, 1, 3, 5, 7 from the low bits
+ * up.  Memory that nothing was appended to may hold anything. */
+#define SPEC_Q4_PAGE_BYTES 8704
+
+/* Append to a cache in 4 bits: as spec_kv_append_paged, keys and values quantised on the way, and with wk
+ * (and wq, with Q) the keys and queries normed as by spec_qk_norm_rope before the rotation.  Keys are quantised
+ * from fp32, without a rounding to bf16 before it.
+ *   wq, wk   [D] bf16, or both NULL: no norm (then Q needs cs).  eps is ignored without them
+ *   Kpool, Vpool [Hkv][num_pages][SPEC_Q4_PAGE_BYTES] (in/out); no input may overlap them.  Of a page that
+ *            receives rows only those rows change; it must belong to one sequence
+ * The rest, and what is checked on the device, as for spec_kv_append_paged.  M <= 4194304.  One kernel, no
+ * workspace. */
+SPEC_API int spec_kv_append_paged_q4(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr, const spec_bf16* Knew,
+                                     const spec_bf16* Vnew, int ldkv, const spec_bf16* wq, const spec_bf16* wk,
+                                     float eps, const float* cs, const int32_t* cu_rows, const int32_t* ctx_len, int B,
+                                     int M, uint8_t* Kpool, uint8_t* Vpool, int num_pages, const int32_t* block_table,
+                                     int max_pages, int Hq, int Hkv, int D, spec_stream stream);
+
+/* The mirror of the append: row r of sequence b (cu_rows[b] <= r < cu_rows[b + 1]) is the cached key and value at
+ * position ctx_len[b] + r - cu_rows[b], as bf16 (exact: a whole number of 3 bits times a scale of 4).  So the rows
+ * that an append wrote come back from the same cu_rows and ctx_len, and a run of keys from the start with
+ * ctx_len = 0; spec_kv_append_paged (cs NULL) takes the result into a bf16 cache.
+ *   Kout, Vout  row r, kv head g at + r*ldkv + g*D (bf16 out; must not overlap the pools)
+ * Rows outside cu_rows[0] .. cu_rows[B] - 1 are left as they were.  Checked on the device, with the status word
+ * set: a sequence outside the M rows or past 128 * max_pages keys is skipped; rows whose page id is outside
+ * [0, num_pages) are not written.  Requires D == 128, ldkv a multiple of 8, 16-byte aligned pointers.  One
+ * kernel, no workspace. */
+SPEC_API int spec_kv_read_paged_q4(const uint8_t* Kpool, const uint8_t* Vpool, int num_pages,
+                                   const int32_t* block_table, int max_pages, const int32_t* cu_rows,
+                                   const int32_t* ctx_len, int B, int M, spec_bf16* Kout, spec_bf16* Vout, int ldkv,
+                                   int Hkv, int D, spec_stream stream);
+
+/* ------------------------------------------------------------------------ */
 /* LM head + softmax: P = softmax((H W_lm^T) / T); T == 0 -> one-hot argmax  */
 /* ------------------------------------------------------------------------ */
 /* Produces p_1 .. p_{gamma+1} for every verify row from the same pass

@@ -23,6 +23,7 @@ What it computes, and where the pages define it:
   head counts; the layer internals are the builder's reading.
 * ``prompt`` — the prompt side of the paged cache (rotation table of several
   position axes, append, attention of a chunk of new tokens).
+* ``q4`` — the paged cache in 4 bits (quantisation, pages, read) and the norms of queries and keys.
 * ``formulas`` — the closed forms the pages print (expected tokens per
   round, Theorem 3.11's arithmetic increase, the speedup / break-even model,
   the verify-cost division, vLLM's acceptance metrics).
@@ -30,4 +31,4 @@ What it computes, and where the pages define it:
 Parity pins (tests marked ``not gpu``) tie every function here to values the
 pages print, closed forms, invariants or brute force; see ``tests/``.
 """
-from . import bf16, formulas, ops, prompt, sampler, stack  # noqa: F401
+from . import bf16, formulas, ops, prompt, q4, sampler, stack  # noqa: F401

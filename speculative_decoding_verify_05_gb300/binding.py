@@ -48,6 +48,10 @@ _SIGS = {
     "spec_chunk_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "spec_chunk_attention_paged": (_i, [_vp, _i, _vp, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _vp, _i,
                                         _vp, _sz, _vp]),
+    "spec_qk_norm_rope": (_i, [_vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _f, _vp, _i, _i, _i, _i, _vp]),
+    "spec_kv_append_paged_q4": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _f, _vp, _vp, _vp, _i, _i, _vp, _vp, _i,
+                                     _vp, _i, _i, _i, _i, _vp]),
+    "spec_kv_read_paged_q4": (_i, [_vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i, _vp]),
     "spec_swiglu_linear_workspace_bytes": (_sz, [_i, _i, _i]),
     "spec_verify_linear_swiglu": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _i, _vp, _sz, _vp]),
     "spec_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
@@ -558,27 +562,37 @@ def spec_verify_attention_paged(Q, Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, b
 
 
 # --------------------------------------------------------------------------- prompt side of the paged cache
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+
+Q4_PAGE_BYTES = 8704        # of a page of a cache in 4 bits: 128 keys of one kv head
 
 
-def _paged(cu_rows, ctx_len, Kpool, Vpool, block_table):
+def _paged(cu_rows, ctx_len, Kpool, Vpool, block_table, q4=False):
     """Checks the batch and cache arguments of a chunk call; returns (B, Hkv, num_pages, D, max_pages).
 
     (A decode step's call costs more host time than its kernel takes: one expression for what is right as
     a rule, and the checks one by one only to name what is not.)"""
-    if not (Kpool.dtype is _BF16 and Vpool.dtype is _BF16 and cu_rows.dtype is _I32 and ctx_len.dtype is _I32
+    kind = _U8 if q4 else _BF16
+    if not (Kpool.dtype is kind and Vpool.dtype is kind and cu_rows.dtype is _I32 and ctx_len.dtype is _I32
             and block_table.dtype is _I32 and Kpool.is_cuda and Vpool.is_cuda and cu_rows.is_cuda and ctx_len.is_cuda
             and block_table.is_cuda):
         for t, n in ((Kpool, "Kpool"), (Vpool, "Vpool")):
-            _need(t, _BF16, n)
+            _need(t, kind, n)
         for t, n in ((cu_rows, "cu_rows"), (ctx_len, "ctx_len"), (block_table, "block_table")):
             _need(t, _I32, n)
     if not (cu_rows.is_contiguous() and ctx_len.is_contiguous() and block_table.is_contiguous()):
         raise ValueError("cu_rows, ctx_len and block_table must be contiguous")
     pool = Kpool.shape
-    if len(pool) != 4 or pool[2] != 128 or Vpool.shape != pool or not (Kpool.is_contiguous() and Vpool.is_contiguous()):
-        raise ValueError("Kpool/Vpool must be contiguous [Hkv, num_pages, 128, D]")
-    Hkv, num_pages, _, D = pool
+    if q4:
+        if len(pool) != 3 or pool[2] != Q4_PAGE_BYTES or Vpool.shape != pool or not (Kpool.is_contiguous()
+                                                                                     and Vpool.is_contiguous()):
+            raise ValueError(f"Kpool/Vpool must be contiguous [Hkv, num_pages, {Q4_PAGE_BYTES}]")
+        Hkv, num_pages, D = pool[0], pool[1], 128
+    else:
+        if (len(pool) != 4 or pool[2] != 128 or Vpool.shape != pool
+                or not (Kpool.is_contiguous() and Vpool.is_contiguous())):
+            raise ValueError("Kpool/Vpool must be contiguous [Hkv, num_pages, 128, D]")
+        Hkv, num_pages, _, D = pool
     table = block_table.shape
     B = cu_rows.numel() - 1
     if len(table) != 2 or table[0] != B or ctx_len.numel() != B:
@@ -665,6 +679,118 @@ def spec_chunk_attention_paged(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, s
         rc = _lib.spec_chunk_attention_paged(*args, wp, wn, _stream(stream))
     _check(rc, True)
     return O
+
+
+# --------------------------------------------------------------------------- norms of q and k, cache in 4 bits
+def q4_pool(Hkv: int, num_pages: int, device="cuda"):
+    """Memory for the keys (or the values) of a paged cache in 4 bits: uint8 [Hkv, num_pages, Q4_PAGE_BYTES]."""
+    return torch.empty((Hkv, num_pages, Q4_PAGE_BYTES), dtype=_U8, device=device)
+
+
+def _table(cs, M, D):
+    if cs.dtype is not _F32 or not cs.is_cuda:
+        _need(cs, _F32, "cs")
+    shape = cs.shape
+    if len(shape) != 3 or shape[0] < M or shape[1] != D // 2 or shape[2] != 2 or not cs.is_contiguous():
+        raise ValueError("cs must be a contiguous [M, D/2, 2] table with an entry per row")
+
+
+def _norm_weight(w, D, name):
+    if w is not None:
+        _need(w, _BF16, name)
+        if w.shape != (D,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [D] tensor")
+
+
+def _heads(X, Y, M, D, names):
+    """(rows, heads, leading dimensions) of X [M, heads*D] and its output Y (None: X itself)."""
+    shape, ld = _rows_bf16(X, names[0])
+    if Y is None:
+        Y, ldy = X, ld
+    else:
+        yshape, ldy = _rows_bf16(Y, names[1])
+        if yshape != shape:
+            raise ValueError(f"{names[0]} and {names[1]} must have the same shape")
+    if shape[1] % D or (M is not None and shape[0] != M):
+        raise ValueError(f"{names[0]} must be [M, heads*D]")
+    return shape[0], shape[1] // D, ld, ldy, Y
+
+
+def spec_qk_norm_rope(Q, K, wq, wk, eps: float = 1e-6, cs=None, Qout=None, Kout=None, stream=None):
+    """RMSNorm of each head of Q [M, Hq*D] and K [M, Hkv*D] (weights wq, wk [D]) and, with the table cs
+    [M, D/2, 2], their rotation, into Qout and Kout (default: in place); returns (Qout, Kout).  Q or K may be None."""
+    D = 128
+    M = None
+    Hq = Hkv = ldq = ldqo = ldk = ldko = 0
+    if Q is not None:
+        M, Hq, ldq, ldqo, Qout = _heads(Q, Qout, M, D, ("Q", "Qout"))
+    elif Qout is not None or wq is not None:
+        raise ValueError("Qout or wq without Q")
+    if K is not None:
+        M, Hkv, ldk, ldko, Kout = _heads(K, Kout, M, D, ("K", "Kout"))
+    elif Kout is not None or wk is not None:
+        raise ValueError("Kout or wk without K")
+    if M is None:
+        return None, None
+    _norm_weight(wq, D, "wq")
+    _norm_weight(wk, D, "wk")
+    if cs is not None:
+        _table(cs, M, D)
+    _check(_lib.spec_qk_norm_rope(_p(Q), ldq, _p(Qout), ldqo, _p(K), ldk, _p(Kout), ldko, _p(wq), _p(wk), eps, _p(cs), M,
+                                  Hq, Hkv, D, _stream(stream)), True)
+    return Qout, Kout
+
+
+def spec_kv_append_paged_q4(Knew, Vnew, cu_rows, ctx_len, Kpool, Vpool, block_table, cs=None, Q=None, Qrot=None,
+                            wq=None, wk=None, eps: float = 1e-6, stream=None):
+    """spec_kv_append_paged into a cache in 4 bits (Kpool/Vpool uint8 [Hkv, num_pages, Q4_PAGE_BYTES], see q4_pool):
+    keys (normed with wk, if given, and rotated with cs, if given) and values are quantised on the way.  Q, if
+    given, is normed with wq and rotated into Qrot (default: in place).  Returns Qrot."""
+    B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table, q4=True)
+    shape, ldkv = _rows_bf16(Knew, "Knew")
+    vshape, ldv = _rows_bf16(Vnew, "Vnew")
+    if ldv != ldkv:
+        raise ValueError("Knew and Vnew must share a leading dimension")
+    M, width = shape
+    if width != Hkv * D or vshape != shape:
+        raise ValueError("Knew and Vnew must be [M, Hkv*D]")
+    if cs is not None:
+        _table(cs, M, D)
+    _norm_weight(wq, D, "wq")
+    _norm_weight(wk, D, "wk")
+    Hq = ldq = ldqr = 0
+    if Q is not None:
+        _, Hq, ldq, ldqr, Qrot = _heads(Q, Qrot, M, D, ("Q", "Qrot"))
+    elif Qrot is not None:
+        raise ValueError("Qrot without Q")
+    _check(_lib.spec_kv_append_paged_q4(
+        _p(Q), ldq, _p(Qrot), ldqr, Knew.data_ptr(), Vnew.data_ptr(), ldkv, _p(wq), _p(wk), eps, _p(cs),
+        cu_rows.data_ptr(), ctx_len.data_ptr(), B, M, Kpool.data_ptr(), Vpool.data_ptr(), num_pages,
+        block_table.data_ptr(), max_pages, Hq, Hkv, D, _stream(stream)), True)
+    return Qrot
+
+
+def spec_kv_read_paged_q4(cu_rows, ctx_len, Kpool, Vpool, block_table, M: int, Kout=None, Vout=None, stream=None):
+    """The keys and values that a cache in 4 bits holds at positions ctx_len[b] + j of sequence b, j < cu_rows[b + 1] -
+    cu_rows[b], as rows cu_rows[b] + j of Kout and Vout [M, Hkv*D] bf16; returns (Kout, Vout)."""
+    B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table, q4=True)
+    M = int(M)
+    outs = []
+    for t, name in ((Kout, "Kout"), (Vout, "Vout")):
+        if t is None:
+            t, ld = _empty((M, Hkv * D), _BF16, Kpool.device, stream), Hkv * D
+        else:
+            shape, ld = _rows_bf16(t, name)
+            if shape != (M, Hkv * D):
+                raise ValueError(f"{name} must be [M, Hkv*D]")
+        outs.append((t, ld))
+    (Kout, ldkv), (Vout, ldv) = outs
+    if ldv != ldkv:
+        raise ValueError("Kout and Vout must share a leading dimension")
+    _check(_lib.spec_kv_read_paged_q4(
+        Kpool.data_ptr(), Vpool.data_ptr(), num_pages, block_table.data_ptr(), max_pages, cu_rows.data_ptr(),
+        ctx_len.data_ptr(), B, M, Kout.data_ptr(), Vout.data_ptr(), ldkv, Hkv, D, _stream(stream)), True)
+    return Kout, Vout
 
 
 # --------------------------------------------------------------------------- LM head

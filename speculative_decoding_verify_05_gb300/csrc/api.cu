@@ -1686,8 +1686,8 @@ int spec_verify_attention_paged(const spec_bf16* Q, int ldq, const spec_bf16* Kn
 
 // --------------------------------------------------------------------------- prompt side of the paged cache
 // Checks shared by the append and the attention of a chunk.
-static int check_paged_chunk(const int32_t* cu_rows, const int32_t* ctx_len, int B, const spec_bf16* Kpool,
-                             const spec_bf16* Vpool, int num_pages, const int32_t* block_table, int max_pages,
+static int check_paged_chunk(const int32_t* cu_rows, const int32_t* ctx_len, int B, const void* Kpool,
+                             const void* Vpool, int num_pages, const int32_t* block_table, int max_pages,
                              int Hkv, int D) {
   if (!cu_rows || !ctx_len || !block_table || !Kpool || !Vpool) return fail(SPEC_EINVAL, "NULL tensor argument");
   if (D != 128) return fail(SPEC_EUNSUPPORTED, "head_dim %d: only 128 is implemented", D);
@@ -1736,6 +1736,108 @@ int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr,
   a.status = d->status;
   cudaError_t e = launch_kv_append(a, d->sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return ok(1);
+}
+
+// --------------------------------------------------------------------------- paged cache in 4 bits
+static int check_norm(const spec_bf16* wq, const spec_bf16* wk, float eps) {
+  if (!aligned16(wq) || !aligned16(wk)) return fail(SPEC_EINVAL, "norm weights must be 16-byte aligned");
+  if (!std::isfinite(eps) || eps < 0.f) return fail(SPEC_EINVAL, "eps must be finite and >= 0");
+  return SPEC_OK;
+}
+
+int spec_qk_norm_rope(const spec_bf16* Q, int ldq, spec_bf16* Qout, int ldqo, const spec_bf16* K, int ldk,
+                      spec_bf16* Kout, int ldko, const spec_bf16* wq, const spec_bf16* wk, float eps, const float* cs,
+                      int M, int Hq, int Hkv, int D, spec_stream stream) {
+  if (M < 0 || Hq < 0 || Hkv < 0) return fail(SPEC_EINVAL, "bad sizes M=%d Hq=%d Hkv=%d", M, Hq, Hkv);
+  if (D != 128) return fail(SPEC_EUNSUPPORTED, "head_dim %d: only 128 is implemented", D);
+  if (M == 0 || Hq + (long long)Hkv == 0) return ok();
+  if ((Hq && (!Q || !Qout || !wq)) || (Hkv && (!K || !Kout || !wk))) return fail(SPEC_EINVAL, "NULL tensor argument");
+  if (!aligned16(Q) || !aligned16(Qout) || !aligned16(K) || !aligned16(Kout) || !aligned16(cs))
+    return fail(SPEC_EINVAL, "tensors must be 16-byte aligned");
+  if (Hq && (ldq < (long long)Hq * D || ldqo < (long long)Hq * D || ldq % 8 || ldqo % 8))
+    return fail(SPEC_EINVAL, "bad leading dimensions ldq=%d ldqo=%d", ldq, ldqo);
+  if (Hkv && (ldk < (long long)Hkv * D || ldko < (long long)Hkv * D || ldk % 8 || ldko % 8))
+    return fail(SPEC_EINVAL, "bad leading dimensions ldk=%d ldko=%d", ldk, ldko);
+  if (Hq && Q == Qout && ldq != ldqo) return fail(SPEC_EINVAL, "Qout may be Q only with the same leading dimension");
+  if (Hkv && K == Kout && ldk != ldko) return fail(SPEC_EINVAL, "Kout may be K only with the same leading dimension");
+  if (int rc = check_norm(wq, wk, eps)) return rc;
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
+  NormRopeArgs a{};
+  a.Q = Q; a.ldq = ldq; a.Qout = Qout; a.ldqo = ldqo; a.K = K; a.ldk = ldk; a.Kout = Kout; a.ldko = ldko;
+  a.wq = wq; a.wk = wk; a.eps = eps; a.cs = reinterpret_cast<const float2*>(cs);
+  a.M = M; a.Hq = Hq; a.Hkv = Hkv;
+  cudaError_t e = launch_qk_norm_rope(a, d->sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+  return ok(1);
+}
+
+int spec_kv_append_paged_q4(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr, const spec_bf16* Knew,
+                            const spec_bf16* Vnew, int ldkv, const spec_bf16* wq, const spec_bf16* wk, float eps,
+                            const float* cs, const int32_t* cu_rows, const int32_t* ctx_len, int B, int M,
+                            uint8_t* Kpool, uint8_t* Vpool, int num_pages, const int32_t* block_table, int max_pages,
+                            int Hq, int Hkv, int D, spec_stream stream) {
+  if (B < 0 || M < 0) return fail(SPEC_EINVAL, "bad sizes B=%d M=%d", B, M);
+  if (B == 0 || M == 0) return ok();
+  if (int rc = check_paged_chunk(cu_rows, ctx_len, B, Kpool, Vpool, num_pages, block_table, max_pages, Hkv, D))
+    return rc;
+  if (!Knew || !Vnew) return fail(SPEC_EINVAL, "Knew and Vnew must be non-NULL");
+  if (ldkv < (long long)Hkv * D || ldkv % 8) return fail(SPEC_EINVAL, "bad leading dimension ldkv=%d", ldkv);
+  if (!aligned16(Knew) || !aligned16(Vnew) || !aligned16(cs) || !aligned16(Q) || !aligned16(Qrot))
+    return fail(SPEC_EINVAL, "tensors must be 16-byte aligned");
+  if (int rc = check_norm(wq, wk, eps)) return rc;
+  if (Q) {
+    if (!cs && !wk) return fail(SPEC_EINVAL, "queries without a rotation table and norm weights");
+    if (!wq != !wk) return fail(SPEC_EINVAL, "norm weights of queries and keys come together");
+    if (!Qrot) return fail(SPEC_EINVAL, "Qrot must be non-NULL with Q");
+    if (Hq <= 0) return fail(SPEC_EINVAL, "Hq=%d must be >= 1", Hq);
+    if (ldq < (long long)Hq * D || ldqr < (long long)Hq * D || ldq % 8 || ldqr % 8)
+      return fail(SPEC_EINVAL, "bad leading dimensions ldq=%d ldqr=%d", ldq, ldqr);
+    if (Q == Qrot && ldq != ldqr) return fail(SPEC_EINVAL, "Qrot may be Q only with the same leading dimension");
+  } else if (Qrot || wq) {
+    return fail(SPEC_EINVAL, "Qrot or wq without Q");
+  }
+  if (M > 1 << 22) return fail(SPEC_EUNSUPPORTED, "M=%d > %d rows", M, 1 << 22);
+  if (((M >> 3) + 2ll * B) * Hkv > 1ll << 30) return fail(SPEC_EUNSUPPORTED, "B=%d sequences of Hkv=%d heads", B, Hkv);
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
+  KvAppendQ4Args a{};
+  a.Q = Q; a.ldq = ldq; a.Qrot = Qrot; a.ldqr = ldqr;
+  a.Knew = Knew; a.Vnew = Vnew; a.ldkv = ldkv;
+  a.wq = wq; a.wk = wk; a.eps = eps;
+  a.cs = reinterpret_cast<const float2*>(cs);
+  a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M;
+  a.Kpool = Kpool; a.Vpool = Vpool;
+  a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages;
+  a.Hq = Q ? Hq : 0; a.Hkv = Hkv;
+  a.status = d->status;
+  cudaError_t e = launch_kv_append_q4(a, d->sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append_q4 launch");
+  return ok(1);
+}
+
+int spec_kv_read_paged_q4(const uint8_t* Kpool, const uint8_t* Vpool, int num_pages, const int32_t* block_table,
+                          int max_pages, const int32_t* cu_rows, const int32_t* ctx_len, int B, int M, spec_bf16* Kout,
+                          spec_bf16* Vout, int ldkv, int Hkv, int D, spec_stream stream) {
+  if (B < 0 || M < 0) return fail(SPEC_EINVAL, "bad sizes B=%d M=%d", B, M);
+  if (B == 0 || M == 0) return ok();
+  if (int rc = check_paged_chunk(cu_rows, ctx_len, B, Kpool, Vpool, num_pages, block_table, max_pages, Hkv, D))
+    return rc;
+  if (!Kout || !Vout) return fail(SPEC_EINVAL, "Kout and Vout must be non-NULL");
+  if (ldkv < (long long)Hkv * D || ldkv % 8) return fail(SPEC_EINVAL, "bad leading dimension ldkv=%d", ldkv);
+  if (!aligned16(Kout) || !aligned16(Vout)) return fail(SPEC_EINVAL, "tensors must be 16-byte aligned");
+  if (((M >> 5) + 2ll * B) * Hkv > 1ll << 30)
+    return fail(SPEC_EUNSUPPORTED, "M=%d rows of B=%d sequences, Hkv=%d heads", M, B, Hkv);
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
+  KvReadQ4Args a{};
+  a.Kpool = Kpool; a.Vpool = Vpool; a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M;
+  a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages; a.Hkv = Hkv;
+  a.Kout = Kout; a.Vout = Vout; a.ldkv = ldkv;
+  a.status = d->status;
+  cudaError_t e = launch_kv_read_q4(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_read_q4 launch");
   return ok(1);
 }
 

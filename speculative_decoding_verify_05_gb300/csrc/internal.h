@@ -207,6 +207,46 @@ struct KvAppendArgs {
   unsigned* status;
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t s);
+
+// ---- paged cache in 4 bits (pages of 8704 bytes, q4.cuh) and the norms of queries and keys
+struct NormRopeArgs {
+  const uint16_t* Q; int ldq;           // Hq = 0: no queries
+  uint16_t* Qout; int ldqo;
+  const uint16_t* K; int ldk;           // Hkv = 0: no keys
+  uint16_t* Kout; int ldko;
+  const uint16_t* wq; const uint16_t* wk;
+  float eps;
+  const float2* cs;                     // [M][64], nullptr: no rotation
+  int M, Hq, Hkv;
+};
+cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t s);
+struct KvAppendQ4Args {
+  const uint16_t* Q; int ldq;
+  uint16_t* Qrot; int ldqr;
+  const uint16_t* Knew; const uint16_t* Vnew; int ldkv;
+  const uint16_t* wq; const uint16_t* wk;   // both nullptr: no norm
+  float eps;
+  const float2* cs;                     // [M][64], nullptr: no rotation
+  const int32_t* cu_rows; const int32_t* ctx_len;
+  int B, M;
+  uint8_t* Kpool; uint8_t* Vpool;       // [Hkv][num_pages][8704]
+  const int32_t* block_table;
+  int num_pages, max_pages, Hq, Hkv;    // Hq = 0 without queries
+  int blocks;                           // (set by the launcher)
+  unsigned* status;
+};
+cudaError_t launch_kv_append_q4(const KvAppendQ4Args& a, int sms, cudaStream_t s);
+struct KvReadQ4Args {
+  const uint8_t* Kpool; const uint8_t* Vpool;
+  const int32_t* cu_rows; const int32_t* ctx_len;
+  int B, M;
+  const int32_t* block_table;
+  int num_pages, max_pages, Hkv;
+  uint16_t* Kout; uint16_t* Vout; int ldkv;
+  int blocks;                           // (set by the launcher)
+  unsigned* status;
+};
+cudaError_t launch_kv_read_q4(const KvReadQ4Args& a, cudaStream_t s);
 struct ChunkAttnArgs {
   const uint16_t* Q; int ldq;
   const int32_t* cu_rows; const int32_t* ctx_len;

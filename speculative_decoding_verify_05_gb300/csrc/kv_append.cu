@@ -3,8 +3,7 @@
 // rotation applied on the way.
 #include "common.cuh"
 #include "internal.h"
-
-#include <climits>
+#include "paged_rows.cuh"
 
 namespace spec {
 namespace {
@@ -63,54 +62,6 @@ rope_table_axes_kernel(const int32_t* __restrict__ pos, int ldpos, int M, int ha
   const unsigned r0 = (blockIdx.x * blockDim.y + threadIdx.y) * rows, r1 = min(r0 + rows, (unsigned)M);
 #pragma unroll 4
   for (unsigned r = r0; r < r1; ++r) cs[(size_t)r * half + i] = cos_sin_turns((unsigned long long)(long long)p[r] * turn);
-}
-
-// The last sequence with cu_rows[b] <= r, 32 candidates at a time by a whole warp; its lengths come with the last
-// 32, so that they cost no load of their own after it.
-struct Place {
-  int b, c0, c1, ctx;                                   // b -1: r is before the first
-};
-__device__ __forceinline__ Place place_of(int r, const KvAppendArgs& a, int lane) {
-  int lo = 0, n = a.B;
-  while (true) {
-    const int step = (n + 31) >> 5, b = lo + lane * step;
-    const bool in = b < lo + n, last = step == 1;
-    int c0 = INT_MAX, c1 = 0, ctx = 0;
-    if (in) {
-      c0 = a.cu_rows[b];
-      if (last) {
-        c1 = a.cu_rows[b + 1];
-        ctx = a.ctx_len[b];
-      }
-    }
-    const unsigned votes = __ballot_sync(0xffffffffu, in && c0 <= r);
-    if (votes == 0) return Place{-1, 0, 0, 0};          // (only before the first)
-    const int k = 31 - __clz(votes);
-    if (last)
-      return Place{lo + k, __shfl_sync(0xffffffffu, c0, k), __shfl_sync(0xffffffffu, c1, k),
-                   __shfl_sync(0xffffffffu, ctx, k)};
-    n = min(step, n - k * step);
-    lo += k * step;
-  }
-}
-
-// 16 bytes past L1, which has no use for them.
-__device__ __forceinline__ uint4 ld_past_l1(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ void st_past_l1(uint16_t* p, const uint4& v) {
-  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
-// Whether a sequence is outside the M rows or past its table's keys (its length and pages count only if it has rows).
-__device__ __forceinline__ bool out_of_bounds(int c0, int c1, int ctx, const KvAppendArgs& a) {
-  return c0 < 0 || c1 < c0 || c1 > a.M ||
-         (c1 > c0 && (ctx < 0 || (long long)ctx + (c1 - c0) > (long long)a.max_pages * PAGE));
 }
 
 // One CTA per row, and behind them a thread per sequence that checks its bounds (no row has to be in a sequence that

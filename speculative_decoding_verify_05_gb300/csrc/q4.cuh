@@ -1,0 +1,63 @@
+// The paged cache in 4 bits: a value is a whole number n of -7 .. 7 times the scale of its 32 neighbouring dims of one
+// key, an 8-bit float without a sign (5 exponent bits, 3 mantissa bits): byte c stands for
+// (1 + (c & 7) / 8) 2^((c >> 3) - 20).  Why whole numbers and not the 4-bit floats (0 .5 1 1.5 2 3 4 6): with groups
+// this small, scaled by their maximum, the levels of normal values are used evenly, and the floats' wide steps at
+// the top cost twice the squared error (normal values in groups of 32: 9.75 % off in rms, 12.9 % as
+// floats); and two of them leave an integer word by one logical operation.  The scale needs no second one per tensor: it
+// reaches from 2^-20 to 3840, so values of 7e-6 to 26880 keep their precision whatever the tensor's range.
+//
+// A page holds 128 keys of one kv head in 8704 bytes: 4 planes of 128 rows of 16 bytes (32 entries), then 512 scales.
+//   keys    plane q, row k: dims 32 q .. 32 q + 31 of key k;  scale of dims 32 g .. of key k at byte 4 k + g
+//   values  plane q, row d: keys 32 q .. 32 q + 31 of dim d;  scale of dims 32 g .. of key k at byte 128 g + k
+// Values lie transposed: both products of an attention then contract over what is contiguous in a row (dims in Q K^T,
+// keys in P V), so K and V tiles are brought to bf16 by the same code, one row per thread.  Planes, so that 32
+// threads with a row each read 512 consecutive bytes.
+// A row's 16 bytes are 4 words of 8 entries: n + 8 of entries 0, 2, 4, 6, 1, 3, 5, 7 from the low bits up, so that a shift and
+// one logical operation leave two neighbouring entries in the halves of a word.
+#pragma once
+
+#include "common.cuh"
+
+namespace spec {
+
+constexpr int Q4_PAGE = 128;             // keys per page
+constexpr int Q4_PLANE = 128 * 16;
+constexpr int Q4_SCALES = 4 * Q4_PLANE;  // offset of the scales
+constexpr int Q4_BYTES = Q4_SCALES + 512;
+
+// Position (in bits) of entry e of 8 in its word.
+__host__ __device__ constexpr int q4_shift(int e) { return 4 * ((e >> 1) + 4 * (e & 1)); }
+
+// Products and sums with exactly one rounding each (never contracted): what is stored in 4 bits hangs on the last bit of
+// what it is rounded from, so the definition fixes every operation and their order.
+__device__ __forceinline__ float q4_scale(float top, unsigned& code) {
+  // a seventh of the largest magnitude, to 3 bits behind the leading one, halves to even
+  const float t = fminf(fmaxf(__fdiv_rn(top, 7.f), 0x1p-20f), 3840.f);
+  unsigned i = __float_as_uint(t);
+  i = (i + 0x7FFFFu + ((i >> 20) & 1u)) & 0xFFF00000u;
+  code = (i >> 20) - 107u * 8u;
+  return __uint_as_float(i);
+}
+// n + 8 of a value (NaN gives 8, a stored 0).
+__device__ __forceinline__ unsigned q4_entry(float x, float scale) {
+  return (unsigned)(min(max(__float2int_rn(__fdiv_rn(x, scale)), -7), 7) + 8);
+}
+
+// ----------------------------------------------------------------- back to bf16
+__device__ __forceinline__ uint32_t q4_fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// bf16 bits of the scales of two codes (each in the low byte of a half).
+__device__ __forceinline__ uint32_t q4_scale2(uint32_t codes) { return (codes << 4) + ((107u << 7) * 0x10001u); }
+// -136 times two scales, exact: 136 = 17 * 8, and 17 times a 4-bit significand has 8 bits.
+__device__ __forceinline__ uint32_t q4_offset2(uint32_t scale2) { return q4_fma2(scale2, 0xC308C308u, 0x80008000u); }
+// Entries 2 j and 2 j + 1 of a word as bf16: n + 8 in the mantissa of 128 makes 128 + n + 8, and (n + 136) s - 136 s is
+// rounded once; n s has 3 + 4 bits, so nothing is lost.
+template <int J>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t scale2, uint32_t offset2) {
+  return q4_fma2(((w >> (4 * J)) & 0x000F000Fu) | 0x43004300u, scale2, offset2);
+}
+
+}  // namespace spec
