@@ -536,6 +536,24 @@ SPEC_API int spec_kv_read_paged_q4(const uint8_t* Kpool, const uint8_t* Vpool, i
                                    const int32_t* ctx_len, int B, int M, spec_bf16* Kout, spec_bf16* Vout, int ldkv,
                                    int Hkv, int D, spec_stream stream);
 
+/* Attention of a chunk of new rows over a cache in 4 bits: as spec_chunk_attention_paged, over the keys and values that
+ * spec_kv_read_paged_q4 returns (they enter the products as they are, in bf16).
+ *   max_rows  an upper bound on the rows of one sequence, which the host knows (M if it does not): up to 64
+ *             rows per kv head (max_rows * Hq / Hkv) a kernel for few rows runs
+ *   Kpool, Vpool [Hkv][num_pages][SPEC_Q4_PAGE_BYTES]
+ * What lies behind a sequence's last key in its page may hold anything.  Checked on the device, with the status
+ * word set: a sequence outside the M rows, of more than max_rows rows or past 128 * max_pages keys is skipped; a
+ * page id outside [0, num_pages) reads page 0 instead.
+ * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, max_rows >= 1, scale finite and >= 0.
+ * Workspace: spec_chunk_attention_q4_workspace_bytes. */
+SPEC_API size_t spec_chunk_attention_q4_workspace_bytes(int B, int M, int max_rows, int Hq, int Hkv, int D,
+                                                        int max_pages);
+SPEC_API int spec_chunk_attention_paged_q4(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len,
+                                           int B, int M, int max_rows, const uint8_t* Kpool, const uint8_t* Vpool,
+                                           int num_pages, const int32_t* block_table, int max_pages, int Hq, int Hkv,
+                                           int D, float scale, spec_bf16* O, int ldo, void* workspace,
+                                           size_t workspace_bytes, spec_stream stream);
+
 /* ------------------------------------------------------------------------ */
 /* LM head + softmax: P = softmax((H W_lm^T) / T); T == 0 -> one-hot argmax  */
 /* ------------------------------------------------------------------------ */

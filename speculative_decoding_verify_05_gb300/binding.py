@@ -52,6 +52,9 @@ _SIGS = {
     "spec_kv_append_paged_q4": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _f, _vp, _vp, _vp, _i, _i, _vp, _vp, _i,
                                      _vp, _i, _i, _i, _i, _vp]),
     "spec_kv_read_paged_q4": (_i, [_vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i, _vp]),
+    "spec_chunk_attention_q4_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "spec_chunk_attention_paged_q4": (_i, [_vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _vp, _i,
+                                           _vp, _sz, _vp]),
     "spec_swiglu_linear_workspace_bytes": (_sz, [_i, _i, _i]),
     "spec_verify_linear_swiglu": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _i, _vp, _sz, _vp]),
     "spec_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
@@ -791,6 +794,42 @@ def spec_kv_read_paged_q4(cu_rows, ctx_len, Kpool, Vpool, block_table, M: int, K
         Kpool.data_ptr(), Vpool.data_ptr(), num_pages, block_table.data_ptr(), max_pages, cu_rows.data_ptr(),
         ctx_len.data_ptr(), B, M, Kout.data_ptr(), Vout.data_ptr(), ldkv, Hkv, D, _stream(stream)), True)
     return Kout, Vout
+
+
+def spec_chunk_attention_q4_workspace_bytes(B, M, max_rows, Hq, Hkv, D, max_pages) -> int:
+    return _lib.spec_chunk_attention_q4_workspace_bytes(B, M, max_rows, Hq, Hkv, D, max_pages)
+
+
+def spec_chunk_attention_paged_q4(Q, cu_rows, ctx_len, Kpool, Vpool, block_table, scale: float | None = None, O=None,
+                                  max_rows: int | None = None, ws: Workspace | None = None, stream=None):
+    """spec_chunk_attention_paged over a cache in 4 bits (Kpool/Vpool uint8 [Hkv, num_pages, Q4_PAGE_BYTES]).  max_rows:
+    the most rows that a sequence of the batch has (default: not known); few rows have a kernel of their own."""
+    B, Hkv, num_pages, D, max_pages = _paged(cu_rows, ctx_len, Kpool, Vpool, block_table, q4=True)
+    shape, ldq = _rows_bf16(Q, "Q")
+    M, width = shape
+    if width % D:
+        raise ValueError("Q must be [M, Hq*D]")
+    if O is None:
+        O, ldo = _empty(shape, _BF16, Q.device, stream), width
+    else:
+        oshape, ldo = _rows_bf16(O, "O")
+        if oshape != shape:
+            raise ValueError("O must be [M, Hq*D]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if max_rows is None:
+        max_rows = max(M, 1)
+    Hq = width // D
+    args = (Q.data_ptr(), ldq, cu_rows.data_ptr(), ctx_len.data_ptr(), B, M, max_rows, Kpool.data_ptr(), Vpool.data_ptr(),
+            num_pages, block_table.data_ptr(), max_pages, Hq, Hkv, D, scale, O.data_ptr(), ldo)
+    wp, wn = (None, 0) if ws is None else ws.args(stream)
+    rc = _lib.spec_chunk_attention_paged_q4(*args, wp, wn, _stream(stream))
+    # (asked for only when the one given is refused, as in spec_chunk_attention_paged)
+    if rc != SPEC_OK and wn < (need := spec_chunk_attention_q4_workspace_bytes(B, M, max_rows, Hq, Hkv, D, max_pages)):
+        wp, wn = _ws_args(ws, need, Q.device, stream)
+        rc = _lib.spec_chunk_attention_paged_q4(*args, wp, wn, _stream(stream))
+    _check(rc, True)
+    return O
 
 
 # --------------------------------------------------------------------------- LM head

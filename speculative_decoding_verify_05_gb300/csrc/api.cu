@@ -1860,15 +1860,17 @@ size_t spec_chunk_attention_workspace_bytes(int B, int M, int Hq, int Hkv, int D
   return plan_chunk().bytes;
 }
 
-int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len, int B,
-                               int M, const spec_bf16* Kpool, const spec_bf16* Vpool, int num_pages,
-                               const int32_t* block_table, int max_pages, int Hq, int Hkv, int D, float scale,
-                               spec_bf16* O, int ldo, void* workspace, size_t workspace_bytes, spec_stream stream) {
+// The attention of a chunk over pools of bf16 (q4 false) or of 4 bits.
+static int chunk_attention_impl(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len, int B, int M,
+                                int max_rows, const void* Kpool, const void* Vpool, bool q4, int num_pages,
+                                const int32_t* block_table, int max_pages, int Hq, int Hkv, int D, float scale,
+                                spec_bf16* O, int ldo, void* workspace, size_t workspace_bytes, spec_stream stream) {
   if (B < 0 || M < 0) return fail(SPEC_EINVAL, "bad sizes B=%d M=%d", B, M);
   if (B == 0 || M == 0) return ok();
   if (int rc = check_paged_chunk(cu_rows, ctx_len, B, Kpool, Vpool, num_pages, block_table, max_pages, Hkv, D))
     return rc;
   if (!Q || !O) return fail(SPEC_EINVAL, "NULL tensor argument");
+  if (max_rows <= 0) return fail(SPEC_EINVAL, "max_rows=%d must be >= 1", max_rows);
   if (Hq <= 0 || Hq % Hkv) return fail(SPEC_EINVAL, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
   if (Hq / Hkv > 128) return fail(SPEC_EUNSUPPORTED, "Hq/Hkv = %d > 128", Hq / Hkv);
   if (M > 1 << 22) return fail(SPEC_EUNSUPPORTED, "M=%d > %d rows", M, 1 << 22);
@@ -1890,7 +1892,7 @@ int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_ro
     cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tpt};
     if (int rc = encode_bf16(&tq, Q, 3, dims, str, box, "Q")) return rc;
   }
-  {
+  if (!q4) {
     const cuuint64_t kt = attention_tc_key_tile();
     cuuint64_t dims[3] = {(cuuint64_t)D, kt, (cuuint64_t)num_pages * Hkv};
     cuuint64_t str[2] = {(cuuint64_t)D * 2, kt * D * 2};
@@ -1900,7 +1902,7 @@ int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_ro
   }
   char* ws = static_cast<char*>(workspace);
   ChunkAttnArgs a{};
-  a.Q = Q; a.ldq = ldq; a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M;
+  a.Q = Q; a.ldq = ldq; a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M; a.max_rows = max_rows;
   a.Kpool = Kpool; a.Vpool = Vpool; a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages;
   a.Hkv = Hkv; a.G = G; a.tpt = tpt;
   // (a scale of 0 weighs every visible key alike; masked scores have to stay -inf under it)
@@ -1913,9 +1915,31 @@ int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_ro
   a.t_magic = (unsigned)((1ull << 32) / (2 * tpt)) + 1;
   a.inv_grid = ~0ull / p.grid;
   a.status = d->status;
-  cudaError_t e = launch_chunk_attention(tq, tk, tv, a, p.grid, static_cast<cudaStream_t>(stream));
+  cudaError_t e = q4 ? launch_chunk_attention_q4(tq, a, p.grid, static_cast<cudaStream_t>(stream))
+                     : launch_chunk_attention(tq, tk, tv, a, p.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   return ok(1);
+}
+
+int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len, int B,
+                               int M, const spec_bf16* Kpool, const spec_bf16* Vpool, int num_pages,
+                               const int32_t* block_table, int max_pages, int Hq, int Hkv, int D, float scale,
+                               spec_bf16* O, int ldo, void* workspace, size_t workspace_bytes, spec_stream stream) {
+  return chunk_attention_impl(Q, ldq, cu_rows, ctx_len, B, M, INT32_MAX, Kpool, Vpool, false, num_pages, block_table,
+                              max_pages, Hq, Hkv, D, scale, O, ldo, workspace, workspace_bytes, stream);
+}
+
+size_t spec_chunk_attention_q4_workspace_bytes(int B, int M, int max_rows, int Hq, int Hkv, int D, int max_pages) {
+  if (max_rows <= 0) return 0;
+  return spec_chunk_attention_workspace_bytes(B, M, Hq, Hkv, D, max_pages);
+}
+
+int spec_chunk_attention_paged_q4(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len, int B,
+                                  int M, int max_rows, const uint8_t* Kpool, const uint8_t* Vpool, int num_pages,
+                                  const int32_t* block_table, int max_pages, int Hq, int Hkv, int D, float scale,
+                                  spec_bf16* O, int ldo, void* workspace, size_t workspace_bytes, spec_stream stream) {
+  return chunk_attention_impl(Q, ldq, cu_rows, ctx_len, B, M, max_rows, Kpool, Vpool, true, num_pages, block_table,
+                              max_pages, Hq, Hkv, D, scale, O, ldo, workspace, workspace_bytes, stream);
 }
 
 // --------------------------------------------------------------------------- sampler

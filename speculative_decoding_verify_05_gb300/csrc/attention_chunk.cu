@@ -42,6 +42,7 @@
 // none of them waits for the lengths or keeps a walk in registers.
 #include "common.cuh"
 #include "internal.h"
+#include "q4.cuh"
 
 #include <climits>
 
@@ -51,22 +52,28 @@ namespace {
 constexpr int D = 128;
 constexpr int KT = 128;                   // keys per tile (one page)
 constexpr int TM = 128;                   // rows per row tile
-constexpr int ST = 5;                     // ring stages of one K or V tile
 constexpr int HALF = 128 * 128;           // 128 rows x 64 bf16 (128-byte swizzled rows), 16 KB
 constexpr int TILE = 2 * HALF;
-constexpr int THREADS = 384;
-constexpr int REGS_ALL = 168, REGS_SOFTMAX = 208, REGS_OTHER = 80;
-static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * REGS_ALL, "register split");
+constexpr int PR = 4;                     // posted pieces
+constexpr int PST = 3;                    // packed pages in flight (cache in 4 bits)
 constexpr int OFF_Q = 0;                  // two row tiles
 constexpr int OFF_RING = 2 * TILE;
-constexpr int OFF_BAR = OFF_RING + ST * TILE;
-constexpr int PR = 4;                     // posted pieces
-constexpr int N_BARS = 3 * ST + 18 + 2 * PR;
-constexpr int OFF_RINGP = OFF_BAR + (N_BARS + 1) * 8;   // posted pieces
-constexpr int OFF_ML = OFF_BAR + 1024;    // (max, sum) of 128 rows for each slot
-constexpr int SMEM = OFF_ML + 2 * TM * 8;
-static_assert(SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;       // S0 S1 O0 O1
+template <bool Q4>
+struct Shape {
+  static constexpr int ST = Q4 ? 4 : 5;   // ring stages of one K or V tile
+  static constexpr int THREADS = Q4 ? 512 : 384;
+  static constexpr int REGS_ALL = Q4 ? 128 : 168, REGS_SOFTMAX = Q4 ? 192 : 208, REGS_OTHER = Q4 ? 72 : 80, REGS_Q4 = 56;
+  static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER + (Q4 ? 128 * REGS_Q4 : 0) <= THREADS * REGS_ALL, "register split");
+  static constexpr int OFF_PACKED = OFF_RING + ST * TILE;              // pages as they lie in the cache
+  static constexpr int OFF_EXP = OFF_PACKED + (Q4 ? PST * Q4_BYTES : 0);   // scales of a tile of values, as pairs
+  static constexpr int OFF_BAR = OFF_EXP + (Q4 ? 2048 : 0);
+  static constexpr int N_BARS = 3 * ST + 18 + 2 * PR + (Q4 ? 2 * PST : 0);
+  static constexpr int OFF_RINGP = OFF_BAR + (N_BARS + 1) * 8;         // posted pieces
+  static constexpr int OFF_ML = OFF_BAR + 1024;                        // (max, sum) of 128 rows for each slot
+  static constexpr int SMEM = OFF_ML + 2 * TM * 8;
+  static_assert(SMEM <= 227 * 1024 && OFF_BAR % 16 == 0, "shared memory budget");
+};
 
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // Cost of a key for an item of two row tiles and of one, and what an item's start and end cost in keys; the time that
@@ -214,7 +221,7 @@ struct Seq {
 // Sequence b; one that breaks its bounds counts as having no rows (*bad set).
 __device__ __forceinline__ Seq seq_of(const ChunkAttnArgs& a, int b, bool* bad = nullptr) {
   const int c0 = a.cu_rows[b], c1 = a.cu_rows[b + 1], ctx = a.ctx_len[b];
-  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.M &&
+  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.M && c1 - c0 <= a.max_rows &&
                   (c0 == c1 || (ctx >= 0 && (long long)ctx + (c1 - c0) <= (long long)a.max_pages * KT));
   if (bad) *bad = !ok;
   return Seq{c0, ok ? c1 - c0 : 0, ctx};
@@ -335,7 +342,24 @@ struct Piece {
   __device__ __forceinline__ int keys() const { return pos + tok; }
   __device__ __forceinline__ bool tail() const { return t1 == nt && (keys() & 15) != 0; }
 };
-static_assert(OFF_RINGP + (PR + 1) * sizeof(Piece) + sizeof(Shares) <= OFF_ML && OFF_RINGP % 8 == 0, "posted pieces");
+template <class S>
+constexpr bool pieces_fit() {
+  return S::OFF_RINGP + (PR + 1) * sizeof(Piece) + sizeof(Shares) + PST * 4 <= S::OFF_ML && S::OFF_RINGP % 8 == 0;
+}
+static_assert(pieces_fit<Shape<false>>() && pieces_fit<Shape<true>>(), "posted pieces");
+
+// A packed page to shared memory (16-byte boundaries on both sides, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
+               : "memory");
+}
 
 // The walk over a CTA's pieces, by a whole warp.
 struct Walk {
@@ -397,11 +421,14 @@ struct Walk {
   }
 };
 
-__global__ void __launch_bounds__(THREADS, 1)
+template <bool Q4>
+__global__ void __launch_bounds__(Shape<Q4>::THREADS, 1)
 chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const ChunkAttnArgs a) {
+  using SH = Shape<Q4>;
+  constexpr int ST = SH::ST, N_BARS = SH::N_BARS, OFF_RINGP = SH::OFF_RINGP, OFF_ML = SH::OFF_ML;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SH::OFF_BAR);
   uint64_t* full = bars;                   // [ST] tile ready
   uint64_t* empty = full + ST;             // [ST] its products done
   uint64_t* land = empty + ST;             // [ST] load landed of a V tile whose end is to be zeroed
@@ -413,10 +440,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint64_t* pair = o_full + 2;             // [4][2] the warps of both slots with the same rows: sums exchanged, O read
   uint64_t* posted = pair + 8;             // [PR] piece posted
   uint64_t* taken = posted + PR;           // [PR] everyone is done with its entry
+  uint64_t* p_land = taken + PR;           // [PST] packed page landed (4 bits)
+  uint64_t* p_free = p_land + PST;         // [PST] ... and read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RINGP);
   Piece* s_first = ring + PR;              // the CTA's first piece, for the end
   Shares* s_shares = reinterpret_cast<Shares*>(ring + PR + 1);
+  int* p_kind = reinterpret_cast<int*>(s_shares + 1);      // [PST] what is in a packed stage: 0 keys, 1 values, 2 nothing more
   float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -426,9 +456,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   }
   if (tid == 0) {
     tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-    for (int i = 0; i < 3 * ST; ++i) mbar_init(&bars[i], 1);
+    if constexpr (!Q4) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    for (int i = 0; i < 3 * ST; ++i) mbar_init(&bars[i], Q4 && i < ST ? 4 : 1);
+    if constexpr (Q4)
+      for (int i = 0; i < PST; ++i) {
+        mbar_init(&p_land[i], 1);
+        mbar_init(&p_free[i], 4);
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
@@ -455,8 +492,65 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   pdl_trigger();
 
   // the softmax warps hold a row of scores each: the other warpgroup leaves them its registers
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+  if (Q4 && warp >= 12) {
+    // -------------------------------------------------------------- tiles of 4 bits to bf16
+    // A row per thread, 128 entries: a key's dims, or a dim's keys.  Rows 8 apart lie in different 16-byte columns of the
+    // swizzled tile, so the stores of 8 lanes fill all banks.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REGS_Q4));
+    const int row = tid & 127;
+    uint4* exp = reinterpret_cast<uint4*>(smem + SH::OFF_EXP) + (warp & 3) * 32;
+    bool ok = true;
+    for (int idx = 0;; ++idx) {
+      const int ps = idx % PST, st = idx % ST;
+      ok = wait_for(&p_land[ps], (uint32_t)((idx / PST) & 1));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int kind = p_kind[ps];
+      if (kind == 2) break;
+      const uint8_t* page = smem + SH::OFF_PACKED + ps * Q4_BYTES;
+      uint4 w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4*>(page + q * Q4_PLANE + row * 16);
+      // keys: their own four scales; values: those of the 4 keys whose scales this lane spreads for the warp
+      const uint32_t codes = *reinterpret_cast<const uint32_t*>(page + Q4_SCALES + row * 4);
+      if (kind == 1) {
+        const uint32_t s0 = q4_scale2(__byte_perm(codes, 0, 0x4140)), s1 = q4_scale2(__byte_perm(codes, 0, 0x4342));
+        exp[lane] = make_uint4(s0, q4_offset2(s0), s1, q4_offset2(s1));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_free[ps]);
+      if (idx >= ST) ok = wait_for(&empty[st], (uint32_t)((idx / ST - 1) & 1));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint8_t* dst = smem + OFF_RING + st * TILE + row * 128;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+        uint32_t s = 0, o = 0;
+        if (kind == 0) {
+          s = q4_scale2(__byte_perm(codes, 0, 0x4040 | q * 0x0101));
+          o = q4_offset2(s);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 v;
+          if (kind == 0) {
+            v = make_uint4(q4_pair<0>(x[i], s, o), q4_pair<1>(x[i], s, o), q4_pair<2>(x[i], s, o), q4_pair<3>(x[i], s, o));
+          } else {
+            const uint4 a0 = exp[8 * q + 2 * i], a1 = exp[8 * q + 2 * i + 1];
+            v = make_uint4(q4_pair<0>(x[i], a0.x, a0.y), q4_pair<1>(x[i], a0.z, a0.w), q4_pair<2>(x[i], a1.x, a1.y),
+                           q4_pair<3>(x[i], a1.z, a1.w));
+          }
+          *reinterpret_cast<uint4*>(dst + (q >> 1) * HALF + ((((q & 1) * 4 + i) ^ (row & 7)) << 4)) = v;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+    }
+    if (!ok) set_status(a.status, 0x751u);
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REGS_OTHER));
     if (warp == 11) {
       // ------------------------------------------------------------ pieces
       // The sequences, a run of them per lane.
@@ -622,6 +716,23 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           }
         }
         const int page = __shfl_sync(0xffffffffu, pg.id, t - pg.base);
+        if constexpr (Q4) {
+          const int ps = idx % PST;
+          if (idx >= PST) ok = ok && wait_for(&p_free[ps], (uint32_t)((idx / PST - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return;
+          if (lane == 0) {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(is_v ? a.Vpool : a.Kpool) +
+                                 ((size_t)p.h * a.num_pages + page) * Q4_BYTES;
+            uint8_t* dst = smem + SH::OFF_PACKED + ps * Q4_BYTES;
+            p_kind[ps] = is_v;
+            mbar_arrive_expect_tx(&p_land[ps], Q4_BYTES);
+            if (p.once) bulk_load_hint(dst, src, Q4_BYTES, &p_land[ps], pol);
+            else bulk_load(dst, src, Q4_BYTES, &p_land[ps]);
+          }
+          ++idx;
+          return;
+        }
         const int st = idx % ST;
         if (idx >= ST) ok = ok && wait_for(&empty[st], (uint32_t)((idx / ST - 1) & 1));
         ok = __all_sync(0xffffffffu, ok);
@@ -684,7 +795,20 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           pv.base = -1;
         }
       }
-      if (!ok) {                             // gave up: see the copies in flight land before leaving
+      if constexpr (Q4) {
+        if (ok) {                            // nothing more to bring to bf16
+          const int ps = idx % PST;
+          if (idx >= PST) ok = wait_for(&p_free[ps], (uint32_t)((idx / PST - 1) & 1));
+          if (ok && lane == 0) {
+            p_kind[ps] = 2;
+            mbar_arrive(&p_land[ps]);
+          }
+        }
+        if (!ok) {
+          set_status(a.status, 0x711u);
+          for (int j = idx > PST ? idx - PST : 0; j < idx; ++j) wait_for(&p_land[j % PST], (uint32_t)((j / PST) & 1));
+        }
+      } else if (!ok) {                      // gave up: see the copies in flight land before leaving
         set_status(a.status, 0x711u);
         for (int j = idx > ST ? idx - ST : 0; j < idx; ++j) {
           const int st = j % ST;
@@ -702,9 +826,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       // ran out the warp goes on without waiting (to garbage that nobody reads) instead of voting each time.
       const bool leader = elect_one();
       constexpr uint32_t idesc_s = umma_idesc_bf16(TM, KT);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (1u << 16);   // B (V) MN-major
+      // B (V): rows of keys, MN-major; in 4 bits rows of dims, K-major like the keys
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(TM, D) | (Q4 ? 0u : 1u << 16);
       const uint64_t q0 = umma_desc_sw128(smem_u32(smem + OFF_Q)), k0 = umma_desc_sw128(smem_u32(smem + OFF_RING));
-      const uint64_t v0 = desc_mn(smem_u32(smem + OFF_RING), HALF);
+      const uint64_t v0 = Q4 ? k0 : desc_mn(smem_u32(smem + OFF_RING), HALF);
       int st = 0;                            // next ring stage
       uint32_t ph = 0, ph_p = 0, ph_q = 0;   // phases: the ring's; each slot's weights and Q tile, one bit per slot
       bool ok = true;
@@ -753,7 +878,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           umma_bf16_ts(t_o + sl * D, sl * KT, vd, idesc_pv, first ? 0u : 1u);
 #pragma unroll
           for (int kk = 1; kk < 8; ++kk)
-            umma_bf16_ts_if(t_o + sl * D, sl * KT + kk * 8, vd + kk * 128, idesc_pv, kk < steps);
+            umma_bf16_ts_if(t_o + sl * D, sl * KT + kk * 8,
+                            vd + (Q4 ? ((kk >> 2) * HALF + (kk & 3) * 32) >> 4 : kk * 128), idesc_pv, kk < steps);
           if (release) umma_commit(&empty[vst]);
           if (last) umma_commit(&o_full[sl]);
         }
@@ -881,7 +1007,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
         // the piece before: rows of its last V tile from the sequence's last key to the next multiple of 16
         if (had) {
-          if (before->tail()) {
+          if (!Q4 && before->tail()) {       // (what is held in 4 bits is finite, whatever it is)
             // loads before that tile: every K and V before it, its own K, and the first K of the next piece
             // if it came before slot 1's V
             const int st = (2 * (tiles - 1) + 1 + (!before->dual && !(before->tiles() & 1) && more ? 1 : 0)) % ST;
@@ -911,7 +1037,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           if (n_q[sl] > 0) wait_for(&q_full[sl], (n_q[sl] - 1) & 1);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REGS_SOFTMAX));
     // ------------------------------------------------------------ softmax and epilogue of slot sl
     const int sl = warp >> 2, row = tid & 127;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -1326,23 +1452,33 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 
 }  // namespace
 
-cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                   const ChunkAttnArgs& a, int grid, cudaStream_t s) {
+template <bool Q4>
+static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkAttnArgs& a,
+                          int grid, cudaStream_t s) {
+  using SH = Shape<Q4>;
   static bool configured[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
     if (e != cudaSuccess) return e;
     // the split of registers between the warpgroups draws on what the launch has
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, chunk_attention_kernel);
+    e = cudaFuncGetAttributes(&fa, chunk_attention_kernel<Q4>);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs < REGS_ALL) return cudaErrorLaunchOutOfResources;
+    if (fa.numRegs < SH::REGS_ALL) return cudaErrorLaunchOutOfResources;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  cudaError_t e = launch_k(chunk_attention_kernel, dim3(grid), dim3(THREADS), SMEM, s, tq, tk, tv, a);
+  cudaError_t e = launch_k(chunk_attention_kernel<Q4>, dim3(grid), dim3(SH::THREADS), SH::SMEM, s, tq, tk, tv, a);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const ChunkAttnArgs& a, int grid, cudaStream_t s) {
+  return launch<false>(tq, tk, tv, a, grid, s);
+}
+cudaError_t launch_chunk_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& a, int grid, cudaStream_t s) {
+  return launch<true>(tq, tq, tq, a, grid, s);      // (no maps of the pools: pages are copied whole)
 }
 
 }  // namespace spec

@@ -251,7 +251,8 @@ struct ChunkAttnArgs {
   const uint16_t* Q; int ldq;
   const int32_t* cu_rows; const int32_t* ctx_len;
   int B, M;
-  const uint16_t* Kpool; const uint16_t* Vpool;
+  int max_rows;                         // a sequence with more rows is refused
+  const void* Kpool; const void* Vpool;
   const int32_t* block_table;
   int num_pages, max_pages, Hkv, G;
   int tpt;                              // tokens per row tile: 128 / G
@@ -273,6 +274,8 @@ constexpr int CHUNK_MAX_GRID = 1024;
 // Q map: boxes of 64 dims x G heads x tpt rows; K / V maps: boxes of 64 dims x one page.  `grid` CTAs.
 cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                    const ChunkAttnArgs& a, int grid, cudaStream_t s);
+// The same over a cache in 4 bits (q4.cuh).
+cudaError_t launch_chunk_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& a, int grid, cudaStream_t s);
 
 // ---- rejection sampler
 cudaError_t launch_reject_sample(const float* P, const float* Q, const int32_t* draft,

@@ -104,3 +104,38 @@ def test_binding_refuses_before_the_library(S):
         with pytest.raises(TypeError):
             call()
     assert S.q4_pool(3, 5, "cpu").shape == (3, 5, 8704) and S.Q4_PAGE_BYTES == 8704
+
+
+def attn_args(S, **kw):
+    a = dict(Q=FAKE, ldq=1024, cu=FAKE, ctx=FAKE, B=2, M=5, max_rows=3, Kp=FAKE, Vp=FAKE, num_pages=4, table=FAKE, max_pages=2,
+             Hq=8, Hkv=2, D=128, scale=0.1, O=FAKE, ldo=1024, ws=FAKE, ws_bytes=1 << 40)
+    a.update(kw)
+    return S._lib.spec_chunk_attention_paged_q4(*a.values(), None)
+
+
+@pytest.mark.parametrize("most", [3, 1000])
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), "SPEC_EINVAL"), (dict(M=-1), "SPEC_EINVAL"), (dict(D=64), "SPEC_EUNSUPPORTED"),
+    (dict(Q=None), "SPEC_EINVAL"), (dict(O=None), "SPEC_EINVAL"), (dict(Q=ODD), "SPEC_EINVAL"),
+    (dict(O=ODD), "SPEC_EINVAL"), (dict(cu=None), "SPEC_EINVAL"), (dict(ctx=None), "SPEC_EINVAL"),
+    (dict(table=None), "SPEC_EINVAL"), (dict(Kp=ODD), "SPEC_EINVAL"), (dict(Vp=None), "SPEC_EINVAL"),
+    (dict(num_pages=0), "SPEC_EINVAL"), (dict(max_pages=0), "SPEC_EINVAL"), (dict(Hq=7), "SPEC_EINVAL"),
+    (dict(Hq=0), "SPEC_EINVAL"), (dict(Hq=258), "SPEC_EUNSUPPORTED"), (dict(ldq=1016), "SPEC_EINVAL"),
+    (dict(ldo=1028), "SPEC_EINVAL"), (dict(scale=float("nan")), "SPEC_EINVAL"), (dict(scale=float("inf")), "SPEC_EINVAL"),
+    (dict(scale=-0.1), "SPEC_EINVAL"), (dict(ws_bytes=16), "SPEC_EINVAL"), (dict(ws=None, ws_bytes=0), "SPEC_EINVAL"),
+    (dict(ws=ODD), "SPEC_EINVAL"), (dict(M=(1 << 22) + 1), "SPEC_EUNSUPPORTED"),
+])
+def test_attention_refusals(S, kw, code, most):
+    assert attn_args(S, **{"max_rows": most, **kw}) == getattr(S, code)
+    assert S._lib.spec_last_error() and S._lib.spec_launches() == 0
+
+
+def test_attention_workspace(S):
+    assert attn_args(S, max_rows=0) == attn_args(S, max_rows=-1) == S.SPEC_EINVAL
+    for most in (1, 16, 17, 5000):
+        n = S.spec_chunk_attention_q4_workspace_bytes(8, 5000, most, 32, 8, 128, 64)
+        assert n > 64 * 1024
+        assert attn_args(S, max_rows=most, M=5000, Hq=32, Hkv=8, ldq=4096, ldo=4096, ws_bytes=n - 1) == S.SPEC_EINVAL
+        assert b"workspace" in S._lib.spec_last_error()
+    assert S.spec_chunk_attention_q4_workspace_bytes(8, 1000, 0, 32, 8, 128, 64) == 0
+    assert attn_args(S, B=0, Q=None) == 0 and attn_args(S, M=0, Q=None) == 0 and S._lib.spec_launches() == 0
