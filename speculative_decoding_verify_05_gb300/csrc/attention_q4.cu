@@ -1,0 +1,929 @@
+// Attention of a few rows per sequence (decode steps, verify rounds) over the paged cache in 4 bits, on tcgen05 tensor
+// cores: the R = G * rows <= 64 query rows of a kv head attend their sequence's keys, a page (128 keys) at a time.
+//
+// Products.  The cache's side is the MMA's 128 rows (its A operand), the queries its N = 16 .. 64 columns:
+//   S[key, row] = K . Q^T     M = 128 keys, K = 128 dims
+//   O[dim, row] += V^T . P    M = 128 dims, K = 128 keys
+// so a tile of 128 x 128 cached values is never padded, however few the rows.  K and V^T go to TMEM, not to shared
+// memory: a thread unpacks one row (a key's dims; a dim's keys, which is why the cache holds values transposed) to 64
+// registers of bf16 pairs and stores them to its TMEM lane, where the MMA reads its A operand.  Through shared memory the same
+// tiles would be written and read again at 128 bytes a cycle: 64 KB in and 64 KB out a page of keys and values, 1024
+// cycles, where HBM takes 740 to bring the page.  Only Q and P (bf16, N columns) are read from shared memory.
+//
+// TMEM (all 512 columns): two K and two V tiles (64 columns each), S and O of two slots (64 each).  Tile n belongs to slot
+// n mod 2: its own softmax warps, P buffer and O, each slot with references of its own, joined at the end of an item.
+//
+// Work.  An item is a (sequence, kv head).  The tiles of all items in a row are cut into equal shares by cost, one per
+// CTA; every CTA works its own out from the lengths on the device.  Pieces of an item that several CTAs share go to the
+// workspace as unnormalised O, reference and sum; the warps of its CTAs that are done when the last piece arrives join
+// it, a row at a time, in CTA order whoever does it.
+//
+// Roles (20 warps): 0-3, 4-7 softmax and epilogue of slot 0 and 1 (a thread per key, then per dim); 8 loads pages
+// by bulk copies, keys and values to a ring each; 9 issues the MMAs; 10 stages the queries; 11 walks the batch and posts the
+// CTA's pieces; 12-15 bring keys to bf16, 16-19 values.
+#include "attention_util.cuh"
+#include "internal.h"
+#include "q4.cuh"
+
+#include <climits>
+
+namespace spec {
+namespace {
+
+constexpr int D = 128;
+constexpr int KT = 128;                   // keys per tile (one page)
+constexpr int MAXR = 64;                  // rows of an item
+constexpr int PR = 4;                     // posted pieces
+constexpr int SP = 8;                     // pages in flight, of keys and of values
+constexpr int THREADS = 640;
+constexpr int REGS_ALL = 96, REGS_SOFTMAX = 144, REGS_OTHER = 64;
+static_assert(256 * REGS_SOFTMAX + 384 * REGS_OTHER <= THREADS * REGS_ALL, "register split");
+constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   // two of 64 columns each
+
+constexpr int Q_HALF = MAXR * 128;        // rows x 64 dims (128-byte swizzled rows)
+constexpr int OFF_Q = 0;                  // two buffers of two halves
+constexpr int OFF_P = OFF_Q + 2 * 2 * Q_HALF;          // of each slot: [key][row], 128-byte swizzled rows
+constexpr int OFF_KP = OFF_P + 2 * KT * 128;
+constexpr int OFF_VP = OFF_KP + SP * Q4_BYTES;
+constexpr int OFF_EXP = OFF_VP + SP * Q4_BYTES;        // scales of a tile of values, as pairs
+constexpr int OFF_REF = OFF_EXP + 2048;                // [2][64] references, [2][64] what is added to a score for it
+constexpr int OFF_ALPHA = OFF_REF + 4 * MAXR * 4;      // [2][64]
+constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;      // [8][64] maxima, later sums, of the softmax warps
+constexpr int OFF_F = OFF_MAX + 8 * MAXR * 4;          // [64] factors of the two slots' O
+constexpr int OFF_TOK = OFF_F + MAXR * 8;              // [64] token of each row
+constexpr int OFF_BAR = OFF_TOK + MAXR * 4;
+constexpr int N_BARS = 4 * SP + 18 + 2 * PR;
+constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+static_assert(OFF_KP % 128 == 0 && OFF_EXP % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+
+constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
+// What an item's start and end cost, in keys; what reading a piece back takes (see shares_of).
+constexpr int ITEM_KEYS = 320, PIECE_KEYS = 60;
+
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool bar_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r)
+               : "r"((uint32_t)x), "r"(id), "r"(n)
+               : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float x) {      // (NaN is passed over)
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {      // (0 bytes: zeros)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_cols8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ----------------------------------------------------------------- the batch
+struct Seq {
+  int r0, rows, ctx;
+};
+// Sequence b; one that breaks its bounds counts as having no rows (*bad set).
+__device__ __forceinline__ Seq seq_of(const ChunkAttnArgs& a, int b, bool* bad = nullptr) {
+  const int c0 = a.cu_rows[b], c1 = a.cu_rows[b + 1], ctx = a.ctx_len[b];
+  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.M && c1 - c0 <= a.max_rows &&
+                  (c0 == c1 || (ctx >= 0 && (long long)ctx + (c1 - c0) <= (long long)a.max_pages * KT));
+  if (bad) *bad = !ok;
+  return Seq{c0, ok ? c1 - c0 : 0, ctx};
+}
+__device__ __forceinline__ long long item_cost(const Seq& s) { return (long long)s.ctx + s.rows + ITEM_KEYS; }
+// The tile that a cut at cost y of an item (its start 0) falls before: 0 .. nt.
+__device__ __forceinline__ int cut_tile(long long y, int keys, int nt) {
+  y -= ITEM_KEYS;
+  if (y <= 0) return 0;
+  if (y >= keys) return nt;
+  const int t = ((int)y + KT / 2) / KT;
+  return t * KT + KT / 2 >= keys ? nt : t;              // (no piece of a few keys)
+}
+// The cost of the batch and of a CTA's share of it.  Equal shares, but of so many keys that an item's pieces are not
+// joined for longer than they take.
+struct Shares {
+  long long total, each;
+  __device__ __forceinline__ long long start(int c) const { return min(total, c * each); }
+};
+__device__ __forceinline__ Shares shares_of(const ChunkAttnArgs& a, long long total, int keys) {
+  const long long even = (long long)__umul64hi((unsigned long long)total, a.inv_grid) + 1;
+  return Shares{total, max(even, (long long)sqrtf((float)PIECE_KEYS * keys))};
+}
+
+// A CTA's consecutive tiles of one item, as posted.
+struct Piece {
+  int b, h;
+  int t0, t1, nt;      // tiles t0 .. t1 - 1 of the item's nt
+  int row0, rows, ctx;
+  int more;            // 0: no piece, the CTA is done
+  long long start;     // cost of everything before the item
+  __device__ __forceinline__ int tiles() const { return t1 - t0; }
+  __device__ __forceinline__ bool shared() const { return t0 > 0 || t1 < nt; }
+};
+constexpr int OFF_RINGP = (OFF_MISC + 8 + 2 * SP * 4 + 7) & ~7;      // behind the TMEM address and the stages' marks
+constexpr int SMEM = OFF_RINGP + (PR + 1) * (int)sizeof(Piece) + (int)sizeof(Shares);
+static_assert(SMEM <= 227 * 1024, "shared memory budget");
+
+// NC: columns of the MMAs (rows of the queries, a multiple of 16).
+template <int NC>
+__global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const ChunkAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* k_land = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [SP] page of keys landed
+  uint64_t* k_free = k_land + SP;          // [SP] ... and read
+  uint64_t* v_land = k_free + SP;
+  uint64_t* v_free = v_land + SP;
+  uint64_t* ka_full = v_free + SP;         // [2] K tile in TMEM
+  uint64_t* ka_free = ka_full + 2;         // [2] its product done
+  uint64_t* va_full = ka_free + 2;
+  uint64_t* va_free = va_full + 2;
+  uint64_t* s_full = va_free + 2;          // [2] scores of a slot in TMEM (and the slot's P V before them done)
+  uint64_t* p_full = s_full + 2;           // [2] P in shared memory, S read, O rescaled
+  uint64_t* o_full = p_full + 2;           // [2] the slot's last P V of a piece done
+  uint64_t* q_full = o_full + 2;           // [2] queries staged
+  uint64_t* q_free = q_full + 2;           // [2] the last product with them done
+  uint64_t* posted = q_free + 2;           // [PR]
+  uint64_t* taken = posted + PR;           // [PR]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(taken + PR);
+  int* k_more = reinterpret_cast<int*>(tmem_slot + 2);      // [SP] 0: nothing more behind this stage
+  int* v_more = k_more + SP;
+  Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RINGP);
+  Piece* s_first = ring + PR;              // the CTA's first piece, for the end
+  Shares* s_shares = reinterpret_cast<Shares*>(ring + PR + 1);
+  float* s_ref = reinterpret_cast<float*>(smem + OFF_REF);
+  float* s_add = s_ref + 2 * MAXR;
+  float* s_alpha = reinterpret_cast<float*>(smem + OFF_ALPHA);
+  float* s_max = reinterpret_cast<float*>(smem + OFF_MAX);
+  float2* s_f = reinterpret_cast<float2*>(smem + OFF_F);
+  int* s_tok = reinterpret_cast<int*>(smem + OFF_TOK);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((smem_u32(smem) & 1023u) != 0) {     // (the swizzled tiles need it; the same for every thread)
+    if (tid == 0) set_status(a.status, 0xAF3u);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < SP; ++i) {
+      mbar_init(&k_land[i], 1);
+      mbar_init(&k_free[i], 4);
+      mbar_init(&v_land[i], 1);
+      mbar_init(&v_free[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ka_full[i], 4);
+      mbar_init(&ka_free[i], 1);
+      mbar_init(&va_full[i], 4);
+      mbar_init(&va_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
+    }
+    for (int i = 0; i < PR; ++i) {
+      mbar_init(&posted[i], 1);
+      mbar_init(&taken[i], 11);            // loads, MMA, queries, 8 softmax warps
+    }
+    fence_barrier_init();
+  }
+  if (tid < MAXR) s_tok[tid] = tid / a.G;
+  if (warp == 9) tmem_alloc(tmem_slot, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*tmem_slot != 0 && tid == 0) set_status(a.status, 0xAF4u);       // (all 512 columns are this CTA's)
+  // everything above overlaps the kernel before; global memory only below
+  pdl_wait();
+  pdl_trigger();
+
+  // the k-th posted piece, by a whole warp; false after a wait that ran out
+  auto open = [&](int k, bool& ok) {
+    ok = __all_sync(0xffffffffu, ok && wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1)));
+    return ring[k % PR];
+  };
+  auto close = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&taken[k % PR]);
+  };
+
+  if (warp >= 12) {
+    // -------------------------------------------------------------- pages to bf16: keys (12-15), values (16-19)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    const bool is_v = warp >= 16;
+    const int row = tid & 127;
+    const uint32_t t_dst = (is_v ? T_V : T_K) + (uint32_t((warp & 3) * 32) << 16);
+    uint64_t *land = is_v ? v_land : k_land, *free_ = is_v ? v_free : k_free;
+    uint64_t *full = is_v ? va_full : ka_full, *gone = is_v ? va_free : ka_free;
+    const int* more = is_v ? v_more : k_more;
+    uint4* exp = reinterpret_cast<uint4*>(smem + OFF_EXP) + (warp & 3) * 32;
+    bool ok = true;
+    for (int n = 0;; ++n) {
+      const int st = n % SP, buf = n & 1;
+      ok = __all_sync(0xffffffffu, wait_for(&land[st], (uint32_t)((n / SP) & 1)));
+      if (!ok || !more[st]) break;
+      const uint8_t* page = smem + (is_v ? OFF_VP : OFF_KP) + st * Q4_BYTES;
+      uint4 w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4*>(page + q * Q4_PLANE + row * 16);
+      // keys: their own four scales; values: those of the 4 keys whose scales this lane spreads for the warp
+      const uint32_t codes = *reinterpret_cast<const uint32_t*>(page + Q4_SCALES + row * 4);
+      if (is_v) {
+        const uint32_t s0 = q4_scale2(__byte_perm(codes, 0, 0x4140)), s1 = q4_scale2(__byte_perm(codes, 0, 0x4342));
+        exp[lane] = make_uint4(s0, q4_offset2(s0), s1, q4_offset2(s1));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&free_[st]);
+      if (n >= 2) ok = wait_for(&gone[buf], (uint32_t)(((n >> 1) - 1) & 1));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t r[32];
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          const int q = 2 * half + q2;
+          const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+          if (!is_v) {
+            const uint32_t s = q4_scale2(__byte_perm(codes, 0, 0x4040 | q * 0x0101)), o = q4_offset2(s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t* v = r + 16 * q2 + 4 * i;
+              v[0] = q4_pair<0>(x[i], s, o);
+              v[1] = q4_pair<1>(x[i], s, o);
+              v[2] = q4_pair<2>(x[i], s, o);
+              v[3] = q4_pair<3>(x[i], s, o);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 e0 = exp[8 * q + 2 * i], e1 = exp[8 * q + 2 * i + 1];
+              uint32_t* v = r + 16 * q2 + 4 * i;
+              v[0] = q4_pair<0>(x[i], e0.x, e0.y);
+              v[1] = q4_pair<1>(x[i], e0.z, e0.w);
+              v[2] = q4_pair<2>(x[i], e1.x, e1.y);
+              v[3] = q4_pair<3>(x[i], e1.z, e1.w);
+            }
+          }
+        }
+        tmem_st_cols32(t_dst + buf * 64 + half * 32, r);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[buf]);
+    }
+    if (!ok) set_status(a.status, 0x851u);
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    if (warp == 11) {
+      // ------------------------------------------------------------ pieces
+      const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
+      long long own = 0;
+      bool bad = false;
+      int longest = 0;
+#pragma unroll 4
+      for (int b = b0; b < b1; ++b) {
+        bool wrong;
+        const Seq s = seq_of(a, b, &wrong);
+        bad |= wrong;
+        if (s.rows > 0) {
+          own += item_cost(s) * a.Hkv;
+          longest = max(longest, s.ctx + s.rows);
+        }
+      }
+      if (bad && blockIdx.x == 0) set_status(a.status, 0xAF1u);
+      long long before = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      const Shares shares = shares_of(a, __shfl_sync(0xffffffffu, before, 31),
+                                      (int)__reduce_max_sync(0xffffffffu, (unsigned)longest));
+      before -= own;
+      // where a cut falls: before tile t of kv head h of sequence b
+      struct Cut {
+        int b, h, t;
+        Seq s;
+        long long start;
+      };
+      auto cut_at = [&](long long x) {
+        Cut c{a.B, 0, 0, Seq{0, 0, 0}, 0};
+        const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + own);
+        if (owner == 0) return c;              // (the end of everything, or nothing at all)
+        long long at = before;
+        if (x >= before && x < before + own)
+          for (c.b = b0;; ++c.b) {
+            c.s = seq_of(a, c.b);
+            const long long all = c.s.rows > 0 ? item_cost(c.s) * a.Hkv : 0;
+            if (x < at + all) break;
+            at += all;
+          }
+        const int from = __ffs(owner) - 1;
+        c.b = __shfl_sync(0xffffffffu, c.b, from);
+        c.s.r0 = __shfl_sync(0xffffffffu, c.s.r0, from);
+        c.s.rows = __shfl_sync(0xffffffffu, c.s.rows, from);
+        c.s.ctx = __shfl_sync(0xffffffffu, c.s.ctx, from);
+        at = __shfl_sync(0xffffffffu, at, from);
+        const long long item = item_cost(c.s);
+        c.h = (int)((unsigned long long)(x - at) / (unsigned long long)item);
+        c.start = at + c.h * item;
+        const int keys = c.s.ctx + c.s.rows;
+        c.t = cut_tile(x - c.start, keys, (keys + KT - 1) / KT);
+        return c;
+      };
+      Cut c = cut_at(shares.start(blockIdx.x));
+      const Cut e = cut_at(shares.start(blockIdx.x + 1));
+      for (int k = 0;;) {
+        Piece p{};
+        if (c.b < a.B) {
+          const int keys = c.s.ctx + c.s.rows;
+          p = Piece{c.b, c.h, c.t, (keys + KT - 1) / KT, (keys + KT - 1) / KT, c.s.r0, c.s.rows, c.s.ctx, 1, c.start};
+          const bool last = c.b == e.b && c.h == e.h;
+          if (last) p.t1 = e.t;
+          if (c.b > e.b || (c.b == e.b && c.h > e.h)) p.more = 0;
+          else if (p.t1 <= p.t0) p.more = last ? 0 : -1;             // (nothing of this item)
+        }
+        if (p.more >= 0) {
+          const bool ok = k < PR || wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1));
+          if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) set_status(a.status, 0x801u);
+            break;
+          }
+          if (lane == 0) {
+            if (k == 0) {
+              *s_first = p;
+              *s_shares = shares;
+            }
+            ring[k % PR] = p;
+            mbar_arrive(&posted[k % PR]);
+          }
+          __syncwarp();
+          ++k;
+        }
+        if (p.more == 0) break;
+        // the next item
+        c.t = 0;
+        c.start += item_cost(c.s);
+        if (++c.h == a.Hkv) {
+          c.h = 0;
+          // the next sequence with rows, 32 candidates at a time (a padded batch may have hundreds without)
+          int from = c.b + 1;
+          for (c.b = a.B; from < a.B && from <= e.b; from += 32) {
+            const Seq s = from + lane < a.B ? seq_of(a, from + lane) : Seq{0, 0, 0};
+            const unsigned has = __ballot_sync(0xffffffffu, s.rows > 0);
+            if (has == 0) continue;
+            const int i = __ffs(has) - 1;
+            c.b = from + i;
+            c.s.r0 = __shfl_sync(0xffffffffu, s.r0, i);
+            c.s.rows = __shfl_sync(0xffffffffu, s.rows, i);
+            c.s.ctx = __shfl_sync(0xffffffffu, s.ctx, i);
+            break;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      // ------------------------------------------------------------ pages
+      bool ok = true;
+      int n = 0;
+      const uint64_t pol = l2_policy_evict_first();
+      for (int k = 0;; ++k) {
+        const Piece p = open(k, ok);
+        if (!ok || !p.more) break;
+        int ids = 0, base = -1;              // page ids of 32 tiles at a time, one per lane
+        for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
+          if (base < 0 || t >= base + 32) {
+            base = t;
+            ids = t + lane < p.t1 ? a.block_table[(size_t)p.b * a.max_pages + t + lane] : 0;
+            if (ids < 0 || ids >= a.num_pages) {
+              set_status(a.status, 0xAF2u);
+              ids = 0;
+            }
+          }
+          const size_t at = ((size_t)p.h * a.num_pages + __shfl_sync(0xffffffffu, ids, t - base)) * Q4_BYTES;
+          const int st = n % SP;
+          if (n >= SP)
+            ok = wait_for(&k_free[st], (uint32_t)((n / SP - 1) & 1)) && wait_for(&v_free[st], (uint32_t)((n / SP - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            k_more[st] = v_more[st] = 1;
+            mbar_arrive_expect_tx(&k_land[st], Q4_BYTES);
+            bulk_load_hint(smem + OFF_KP + st * Q4_BYTES, static_cast<const uint8_t*>(a.Kpool) + at, Q4_BYTES, &k_land[st], pol);
+            mbar_arrive_expect_tx(&v_land[st], Q4_BYTES);
+            bulk_load_hint(smem + OFF_VP + st * Q4_BYTES, static_cast<const uint8_t*>(a.Vpool) + at, Q4_BYTES, &v_land[st], pol);
+          }
+        }
+        close(k);
+      }
+      if (ok) {                              // nothing more to bring to bf16
+        const int st = n % SP;
+        if (n >= SP)
+          ok = wait_for(&k_free[st], (uint32_t)((n / SP - 1) & 1)) && wait_for(&v_free[st], (uint32_t)((n / SP - 1) & 1));
+        if (ok && lane == 0) {
+          k_more[st] = v_more[st] = 0;
+          mbar_arrive(&k_land[st]);
+          mbar_arrive(&v_land[st]);
+        }
+      }
+      if (!ok) {                             // gave up: see the copies in flight land before leaving
+        set_status(a.status, 0x811u);
+        for (int j = n > SP ? n - SP : 0; j < n; ++j) {
+          wait_for(&k_land[j % SP], (uint32_t)((j / SP) & 1));
+          wait_for(&v_land[j % SP], (uint32_t)((j / SP) & 1));
+        }
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMA issue
+      // Tile n + 2's scores are issued behind tile n's P V (the slot's S is read by then).  The whole warp walks the
+      // tiles and one elected lane issues; after a wait that ran out it goes on without waiting (to garbage that nobody
+      // reads).
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = umma_idesc_bf16(KT, NC), idesc_pv = umma_idesc_bf16(D, NC) | (1u << 16);   // (P: MN-major)
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = wait_for(bar, parity);
+      };
+      struct Cursor {
+        int k, j, tiles, more;               // piece, its tile, tiles
+      };
+      auto enter = [&](Cursor& c) {
+        wait(&posted[c.k % PR], (uint32_t)((c.k / PR) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        const Piece& p = ring[c.k % PR];
+        c.j = 0;
+        c.tiles = p.tiles();
+        c.more = ok && p.more;
+      };
+      auto step = [&](Cursor& c) {
+        if (++c.j == c.tiles) {
+          ++c.k;
+          enter(c);
+        }
+      };
+      auto scores = [&](int n, Cursor& c) {
+        const int buf = n & 1, qb = c.k & 1;
+        if (c.j == 0) wait(&q_full[qb], (uint32_t)((c.k >> 1) & 1));
+        wait(&ka_full[buf], (uint32_t)((n >> 1) & 1));
+        tc_fence_after();
+        if (leader) {
+          const uint64_t qd = umma_desc_sw128(smem_u32(smem + OFF_Q + qb * 2 * Q_HALF));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_ts(T_S + buf * 64, T_K + buf * 64 + kk * 8, qd + (((kk >> 2) * Q_HALF + (kk & 3) * 32) >> 4), idesc_s,
+                         kk > 0 ? 1u : 0u);
+          umma_commit(&s_full[buf]);
+          umma_commit(&ka_free[buf]);
+          if (c.j + 1 == c.tiles) umma_commit(&q_free[qb]);
+        }
+        __syncwarp();
+      };
+      auto weigh = [&](int n, Cursor& c) {
+        const int buf = n & 1;
+        wait(&va_full[buf], (uint32_t)((n >> 1) & 1));
+        wait(&p_full[buf], (uint32_t)((n >> 1) & 1));
+        tc_fence_after();
+        if (leader) {
+          const uint64_t pd = desc_mn(smem_u32(smem + OFF_P + buf * KT * 128), 0);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_ts(T_O + buf * 64, T_V + buf * 64 + kk * 8, pd + kk * 128, idesc_pv, c.j >= 2 || kk > 0 ? 1u : 0u);
+          umma_commit(&va_free[buf]);
+          if (c.j + 2 >= c.tiles) umma_commit(&o_full[buf]);
+        }
+        __syncwarp();
+      };
+      Cursor cs{0, 0, 0, 0}, cp{0, 0, 0, 0};
+      enter(cs);
+      cp = cs;
+      int ns = 0;
+      for (; ns < 2 && cs.more; ++ns) {
+        scores(ns, cs);
+        step(cs);
+      }
+      for (int n = 0; cp.more; ++n) {
+        weigh(n, cp);
+        const int done = cp.k;
+        step(cp);
+        if (cp.k != done) close(done);
+        if (cs.more) {
+          scores(ns, cs);
+          ++ns;
+          step(cs);
+        }
+      }
+      if (!ok) set_status(a.status, 0x821u);
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ queries: row r = token r / G, head r mod G; zeros behind
+      bool ok = true;
+      for (int k = 0;; ++k) {
+        const Piece p = open(k, ok);
+        if (!ok || !p.more) break;
+        const int qb = k & 1;
+        if (k >= 2) ok = wait_for(&q_free[qb], (uint32_t)(((k >> 1) - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int R = p.rows * a.G, ch = lane & 15;
+        const uint32_t dst = smem_u32(smem + OFF_Q + qb * 2 * Q_HALF) + (ch >> 3) * Q_HALF;
+#pragma unroll 4
+        for (int r = lane >> 4; r < NC; r += 2) {
+          const int tok = r < R ? s_tok[r] : 0, g = r < R ? r - tok * a.G : 0;
+          cp_async16(dst + sw128_off(r, (ch & 7) * 8),
+                     a.Q + (size_t)(p.row0 + tok) * a.ldq + (size_t)(p.h * a.G + g) * D + ch * 8, r < R ? 16u : 0u);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qb]);
+        close(k);
+      }
+      if (!ok) set_status(a.status, 0x831u);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    // ------------------------------------------------------------ softmax and epilogue of a slot
+    // (After a wait that ran out a warp stops waiting, but keeps the control flow up to the next piece, so that the
+    // named barriers stay matched.)
+    const int slot = warp >> 2, t = tid & 127;           // key of the tile; dim of the output
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t t_s = T_S + slot * 64 + lanes, t_o = T_O + slot * 64 + lanes;
+    float *ref = s_ref + slot * MAXR, *add = s_add + slot * MAXR, *alpha = s_alpha + slot * MAXR;
+    uint8_t* prow = smem + OFF_P + slot * KT * 128 + t * 128;
+    const float scale = a.scale_log2;
+    const int me = blockIdx.x;
+    bool ok = true;
+    int n = 0;                             // tiles of the pieces before
+    uint32_t n_s = 0, ph_o = 0;            // scores so far; phase of each slot's o_full, a bit each
+    Shares shares{0, 0};
+    const Piece* shared_last = nullptr;    // the CTA's last piece, where its item goes on in the next CTA
+    bool shared_first = false;             // the first piece's item came from the CTA before
+    // the last CTA up to this one whose share does not start inside the item, 32 at a time
+    auto first_of = [&](const Piece& p) {
+      const int keys = p.ctx + p.rows;
+      int c = me;
+      for (unsigned out = 0; out == 0; c -= out ? __ffs(out) - 1 : 32)
+        out = __ballot_sync(0xffffffffu, cut_tile(shares.start(max(c - lane, 0)) - p.start, keys, p.nt) == 0);
+      return c;
+    };
+    for (int k = 0;; ++k) {
+      ok = ok && wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1));
+      // (also: everybody has read what the piece before left in shared memory and TMEM)
+      if (bar_or(1, 256, !ok)) {
+        ok = false;
+        break;
+      }
+      const Piece& p = ring[k % PR];
+      if (k == 0) shares = *s_shares;
+      if (!p.more) break;
+      const int tiles = p.tiles();
+      float2 l[NC / 2];
+#pragma unroll
+      for (int c = 0; c < NC / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      if (t < MAXR) {
+        ref[t] = -INFINITY;
+        add[t] = 0.f;
+      }
+      const int j0 = (n + slot) & 1;
+      for (int j = j0; j < tiles; j += 2) {
+        const int key = (p.t0 + j) * KT + t;
+        const bool masked = (p.t0 + j) * KT + KT - 1 > p.ctx;       // (some row does not see some key)
+        ok = ok && wait_for(&s_full[slot], n_s & 1);
+        ++n_s;
+        __syncwarp();
+        tc_fence_after();
+        float x[NC];
+        auto load = [&]() {
+          tmem_ld_cols<NC>(t_s, x);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (key > p.ctx + s_tok[c]) x[c] = -INFINITY;
+          }
+        };
+        auto relate = [&]() {
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(add + c);
+            const float2 u = fma2(make_float2(x[c], x[c + 1]), make_float2(scale, scale), make_float2(r.x, r.y));
+            const float2 v = fma2(make_float2(x[c + 2], x[c + 3]), make_float2(scale, scale), make_float2(r.z, r.w));
+            x[c] = u.x;
+            x[c + 1] = u.y;
+            x[c + 2] = v.x;
+            x[c + 3] = v.y;
+          }
+        };
+        load();
+        // Weights are relative to the row's reference: the maximum of the slot's first tile in which it sees a key, whose
+        // own weight is then 1, exactly.  Later tiles keep it as long as no weight passes 2^24 (any reference far below
+        // the maximum gives the same quotients: bf16 and fp32 have exponents to spare); then, and where rows see
+        // keys for the first time (masked tiles), the maximum is taken, and O and the sums rescaled.
+        bool look = j == j0 || masked;
+        if (!look) {
+          relate();
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
+          look = bar_or(2 + slot, 128, top > 24.f);
+          if (look) load();
+        }
+        if (look) {
+          float* mine = s_max + warp * MAXR;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float m = warp_max(x[c]);
+            if (lane == (c & 31)) mine[c] = m;
+          }
+          bar_sync(2 + slot, 128);
+          bool moved = false;
+          if (t < NC) {
+            const float* m4 = s_max + slot * 4 * MAXR + t;
+            const float mx = fmaxf(fmaxf(m4[0], m4[MAXR]), fmaxf(m4[2 * MAXR], m4[3 * MAXR])) * scale;
+            const float old = ref[t];
+            const bool move = old == -INFINITY ? mx > -INFINITY : mx > old + 19.f;
+            const float f = move && old != -INFINITY ? ex2(old - mx) : 1.f;
+            if (move) {
+              ref[t] = mx;
+              add[t] = -mx;
+            }
+            alpha[t] = f;
+            moved = f != 1.f;
+          }
+          if (bar_or(2 + slot, 128, moved)) {
+#pragma unroll
+            for (int c = 0; c < NC; c += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(alpha + c);
+              l[c / 2].x *= f.x;
+              l[c / 2].y *= f.y;
+            }
+            // O is whole here: the scores' barrier came after the slot's P V before them
+#pragma unroll 1
+            for (int c = 0; c < NC; c += 16) {
+              uint32_t o[16];
+              tmem_ld_cols16(t_o + c, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[c + i]);
+              tmem_st_cols16(t_o + c, o);
+            }
+            tmem_st_wait();
+          }
+          relate();
+        }
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 e = make_float2(ex2(x[c + 2 * i]), ex2(x[c + 2 * i + 1]));
+            l[c / 2 + i] = add2(l[c / 2 + i], e);
+            w[i] = cvt_bf16x2(e.x, e.y);
+          }
+          *reinterpret_cast<uint4*>(prow + (((c >> 3) ^ (t & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[slot]);
+      }
+      // ---------------------------------------------------------- end of the piece
+      // sums of the warp's 32 keys, column c to lane c mod 32: each step halves the columns that a lane still holds
+      float* sums = s_max + warp * MAXR;
+#pragma unroll
+      for (int c0 = 0; c0 < NC; c0 += 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[2 * i] = l[c0 / 2 + i].x;
+          v[2 * i + 1] = l[c0 / 2 + i].y;
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+          const bool up = (lane & o) != 0;
+#pragma unroll
+          for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+        if (lane < 16) sums[c0 + lane] = v[0];
+      }
+      const bool shared = p.shared();
+      const int c_first = shared ? first_of(p) : me;
+      const size_t at = (size_t)me * 2 + (me == c_first ? 1 : 0);
+      bar_sync(1, 256);
+      if (tid < NC) {
+        const float m0 = s_ref[tid], m1 = s_ref[MAXR + tid], m = fmaxf(m0, m1), base = m == -INFINITY ? 0.f : m;
+        float f0 = ex2(m0 - base), f1 = ex2(m1 - base);
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          l0 += s_max[w * MAXR + tid];
+          l1 += s_max[(4 + w) * MAXR + tid];
+        }
+        const float sum = l0 * f0 + l1 * f1;
+        if (shared) {
+          __stcg(a.part_ml + at * MAXR + tid, make_float2(m, sum));
+        } else {
+          f0 /= sum;
+          f1 /= sum;
+        }
+        s_f[tid] = make_float2(f0, f1);
+      }
+      bar_sync(1, 256);
+      const bool have0 = tiles > (n & 1), have1 = tiles > ((n + 1) & 1);
+      if (have0) ok = ok && wait_for(&o_full[0], ph_o & 1u);
+      if (have1) ok = ok && wait_for(&o_full[1], (ph_o >> 1) & 1u);
+      ph_o ^= (have0 ? 1u : 0u) | (have1 ? 2u : 0u);
+      __syncwarp();
+      tc_fence_after();
+      // a slot's warps take half of the rows, of both slots' O
+      const int R = p.rows * a.G;
+#pragma unroll 1
+      for (int c = slot * (NC / 2); c < (slot + 1) * (NC / 2) && c < R; c += 8) {
+        float o[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.f;
+        if (have0) {
+          tmem_ld_cols8(T_O + lanes + c, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = u[i] * s_f[c + i].x;
+        }
+        if (have1) {
+          tmem_ld_cols8(T_O + 64 + lanes + c, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] += u[i] * s_f[c + i].y;
+        }
+        if (shared) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < R) __stcg(a.part_o + (at * MAXR + c + i) * D + t, o[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (c + i < R) {
+              const int tok = s_tok[c + i], g = c + i - tok * a.G;
+              a.O[(size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + g) * D + t] = f2bf(o[i]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (shared) {
+        if (p.t0 > 0) shared_first = true;
+        else shared_last = &p;             // (its entry of the ring is not posted again)
+        __syncwarp();
+        if (lane == 0) red_release(a.counters + 16 * c_first, (unsigned)tiles);
+      }
+      n += tiles;
+      close(k);
+    }
+    if (!ok) set_status(a.status, 0x841u);
+    // At the CTA's end: the rows of a shared item are joined by the warps of all its CTAs that are still here when
+    // the last piece arrives, a row at a time.  A warp waits for that a while only: the warp that brings the last
+    // piece joins whatever is left, so no CTA needs another one to run beside it.
+    ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      if (!ok || !(i ? shared_first : shared_last != nullptr)) continue;
+      const Piece& p = i ? *s_first : *shared_last;
+      const int c_first = first_of(p), keys = p.ctx + p.rows, R = p.rows * a.G;
+      unsigned *arrived = a.counters + 16 * c_first, *tickets = arrived + 8;
+      // the CTAs that have a piece: those of 32 from `base` on, and the tiles up to the last of them
+      struct Sharers {
+        unsigned has;
+        int t;
+      };
+      auto sharers = [&](int base, int before) {
+        const int to = cut_tile(shares.start(base + lane + 1) - p.start, keys, p.nt);
+        const int prev = __shfl_up_sync(0xffffffffu, to, 1);
+        return Sharers{__ballot_sync(0xffffffffu, to > (lane == 0 ? before : prev)), __shfl_sync(0xffffffffu, to, 31)};
+      };
+      const Sharers all = sharers(c_first, 0);
+      unsigned there = 0;
+      if (lane == 0) {
+        const uint64_t t0 = globaltimer();
+        do {
+          there = ld_acquire(arrived) == 8u * (unsigned)p.nt;
+        } while (!there && globaltimer() - t0 < JOIN_WAIT_NS);
+      }
+      int count = __popc(all.has);
+      Sharers s = all;
+      for (int base = c_first; s.t < p.nt; count += __popc(s.has)) s = sharers(base += 32, s.t);
+      if (__shfl_sync(0xffffffffu, there, 0)) {
+        __syncwarp();
+        for (;;) {
+          unsigned r = 0;
+          if (lane == 0) r = atomicAdd(tickets, 1u) & 0xffffu;
+          r = __shfl_sync(0xffffffffu, r, 0);
+          if (r >= (unsigned)R) break;
+          float top = -INFINITY, sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          Sharers s = all;
+          for (int base = c_first;; base += 32) {
+            while (s.has) {
+              constexpr int BATCH = 8;
+              float4 u[BATCH];
+              float2 ml[BATCH];
+#pragma unroll
+              for (int j = 0; j < BATCH; ++j) {
+                const int c = s.has ? base + __ffs(s.has) - 1 : -1;
+                s.has &= s.has - 1;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                u[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c >= 0) {
+                  const size_t at = ((size_t)c * 2 + (c == c_first ? 1 : 0)) * MAXR + r;
+                  ml[j] = __ldcg(a.part_ml + at);
+                  u[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
+                }
+              }
+              float high = top;
+#pragma unroll
+              for (int j = 0; j < BATCH; ++j) high = fmaxf(high, ml[j].x);
+              const float base_m = high == -INFINITY ? 0.f : high, keep = ex2(top - base_m);
+              sum *= keep;
+              acc.x *= keep;
+              acc.y *= keep;
+              acc.z *= keep;
+              acc.w *= keep;
+              top = high;
+#pragma unroll
+              for (int j = 0; j < BATCH; ++j) {
+                const float w = ex2(ml[j].x - base_m);
+                sum += ml[j].y * w;
+                acc.x += u[j].x * w;
+                acc.y += u[j].y * w;
+                acc.z += u[j].z * w;
+                acc.w += u[j].w * w;
+              }
+            }
+            if (s.t >= p.nt) break;
+            s = sharers(base + 32, s.t);
+          }
+          const float inv = 1.f / sum;
+          const int tok = s_tok[r], g = (int)r - tok * a.G;
+          *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + g) * D + lane * 4) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+      }
+      // done with it; the last warp of the sharers clears their two words for the next launch
+      if (lane == 0 && (int)(atomicAdd(tickets, 0x10000u) >> 16) + 1 == 8 * count) {
+        *tickets = 0u;
+        *arrived = 0u;
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(0, TMEM_COLS);
+  }
+}
+
+template <int NC>
+cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t s) {
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(few_attention_q4_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    // the split of registers between the warpgroups draws on what the launch has
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, few_attention_q4_kernel<NC>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < REGS_ALL) return cudaErrorLaunchOutOfResources;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  cudaError_t e = launch_k(few_attention_q4_kernel<NC>, dim3(grid), dim3(THREADS), SMEM, s, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+int few_attention_q4_rows() { return MAXR; }
+
+cudaError_t launch_few_attention_q4(const ChunkAttnArgs& a, int grid, cudaStream_t s) {
+  switch ((a.G * a.max_rows + 15) / 16) {
+    case 1: return launch<16>(a, grid, s);
+    case 2: return launch<32>(a, grid, s);
+    case 3: return launch<48>(a, grid, s);
+    default: return launch<64>(a, grid, s);
+  }
+}
+
+}  // namespace spec

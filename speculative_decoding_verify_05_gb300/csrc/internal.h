@@ -276,6 +276,10 @@ cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk,
                                    const ChunkAttnArgs& a, int grid, cudaStream_t s);
 // The same over a cache in 4 bits (q4.cuh).
 cudaError_t launch_chunk_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& a, int grid, cudaStream_t s);
+// ... and the same for few rows: G * max_rows <= few_attention_q4_rows().  Of the workspace it uses the counters, and
+// part_o as [grid][2][64][128] and part_ml as [grid][2][64].
+int few_attention_q4_rows();
+cudaError_t launch_few_attention_q4(const ChunkAttnArgs& a, int grid, cudaStream_t s);
 
 // ---- rejection sampler
 cudaError_t launch_reject_sample(const float* P, const float* Q, const int32_t* draft,
