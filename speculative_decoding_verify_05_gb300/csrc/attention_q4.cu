@@ -18,9 +18,10 @@
 // workspace as unnormalised O, reference and sum; the warps of its CTAs that are done when the last piece arrives join
 // it, a row at a time, in CTA order whoever does it.
 //
-// Roles (20 warps): 0-3, 4-7 softmax and epilogue of slot 0 and 1 (a thread per key, then per dim); 8 loads pages
+// Roles (28 warps): 0-3, 4-7 softmax and epilogue of slot 0 and 1 (a thread per key, then per dim); 8 loads pages
 // by bulk copies, keys and values to a ring each; 9 issues the MMAs; 10 stages the queries; 11 walks the batch and posts the
-// CTA's pieces; 12-15 bring keys to bf16, 16-19 values.
+// CTA's pieces; 12-19 bring keys to bf16, 20-27 values, four warps a slot (with four in all for each, one tile after
+// the other, what a tile waits for was in the way: 16 x 1 row at 30000 keys 168 us).
 #include "attention_util.cuh"
 #include "internal.h"
 #include "q4.cuh"
@@ -35,9 +36,9 @@ constexpr int KT = 128;                   // keys per tile (one page)
 constexpr int MAXR = 64;                  // rows of an item
 constexpr int PR = 4;                     // posted pieces
 constexpr int SP = 8;                     // pages in flight, of keys and of values
-constexpr int THREADS = 640;
-constexpr int REGS_ALL = 96, REGS_SOFTMAX = 144, REGS_OTHER = 64;
-static_assert(256 * REGS_SOFTMAX + 384 * REGS_OTHER <= THREADS * REGS_ALL, "register split");
+constexpr int THREADS = 896;
+constexpr int REGS_ALL = 72, REGS_SOFTMAX = 112, REGS_OTHER = 56;
+static_assert(256 * REGS_SOFTMAX + 640 * REGS_OTHER <= THREADS * REGS_ALL, "register split");
 constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   // two of 64 columns each
 
 constexpr int Q_HALF = MAXR * 128;        // rows x 64 dims (128-byte swizzled rows)
@@ -46,7 +47,7 @@ constexpr int OFF_P = OFF_Q + 2 * 2 * Q_HALF;          // of each slot: [key][ro
 constexpr int OFF_KP = OFF_P + 2 * KT * 128;
 constexpr int OFF_VP = OFF_KP + SP * Q4_BYTES;
 constexpr int OFF_EXP = OFF_VP + SP * Q4_BYTES;        // scales of a tile of values, as pairs
-constexpr int OFF_REF = OFF_EXP + 2048;                // [2][64] references, [2][64] what is added to a score for it
+constexpr int OFF_REF = OFF_EXP + 4096;                // [2][64] references, [2][64] what is added to a score for it
 constexpr int OFF_ALPHA = OFF_REF + 4 * MAXR * 4;      // [2][64]
 constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;      // [8][64] maxima, later sums, of the softmax warps
 constexpr int OFF_F = OFF_MAX + 8 * MAXR * 4;          // [64] factors of the two slots' O
@@ -217,18 +218,18 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
   };
 
   if (warp >= 12) {
-    // -------------------------------------------------------------- pages to bf16: keys (12-15), values (16-19)
+    // -------------------------------------------------------------- pages to bf16: keys (12-19), values (20-27)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-    const bool is_v = warp >= 16;
-    const int row = tid & 127;
-    const uint32_t t_dst = (is_v ? T_V : T_K) + (uint32_t((warp & 3) * 32) << 16);
+    const bool is_v = warp >= 20;
+    const int row = tid & 127, buf = ((warp - 12) >> 2) & 1;
+    const uint32_t t_dst = (is_v ? T_V : T_K) + buf * 64 + (uint32_t((warp & 3) * 32) << 16);
     uint64_t *land = is_v ? v_land : k_land, *free_ = is_v ? v_free : k_free;
     uint64_t *full = is_v ? va_full : ka_full, *gone = is_v ? va_free : ka_free;
     const int* more = is_v ? v_more : k_more;
-    uint4* exp = reinterpret_cast<uint4*>(smem + OFF_EXP) + (warp & 3) * 32;
+    uint4* exp = reinterpret_cast<uint4*>(smem + OFF_EXP) + (warp & 7) * 32;
     bool ok = true;
-    for (int n = 0;; ++n) {
-      const int st = n % SP, buf = n & 1;
+    for (int n = buf;; n += 2) {
+      const int st = n % SP;
       ok = __all_sync(0xffffffffu, wait_for(&land[st], (uint32_t)((n / SP) & 1)));
       if (!ok || !more[st]) break;
       const uint8_t* page = smem + (is_v ? OFF_VP : OFF_KP) + st * Q4_BYTES;
@@ -248,35 +249,29 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t r[32];
+      for (int q = 0; q < 4; ++q) {
+        uint32_t r[16];
+        const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+        if (!is_v) {
+          const uint32_t s = q4_scale2(__byte_perm(codes, 0, 0x4040 | q * 0x0101)), o = q4_offset2(s);
 #pragma unroll
-        for (int q2 = 0; q2 < 2; ++q2) {
-          const int q = 2 * half + q2;
-          const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-          if (!is_v) {
-            const uint32_t s = q4_scale2(__byte_perm(codes, 0, 0x4040 | q * 0x0101)), o = q4_offset2(s);
+          for (int i = 0; i < 4; ++i) {
+            r[4 * i] = q4_pair<0>(x[i], s, o);
+            r[4 * i + 1] = q4_pair<1>(x[i], s, o);
+            r[4 * i + 2] = q4_pair<2>(x[i], s, o);
+            r[4 * i + 3] = q4_pair<3>(x[i], s, o);
+          }
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t* v = r + 16 * q2 + 4 * i;
-              v[0] = q4_pair<0>(x[i], s, o);
-              v[1] = q4_pair<1>(x[i], s, o);
-              v[2] = q4_pair<2>(x[i], s, o);
-              v[3] = q4_pair<3>(x[i], s, o);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 e0 = exp[8 * q + 2 * i], e1 = exp[8 * q + 2 * i + 1];
-              uint32_t* v = r + 16 * q2 + 4 * i;
-              v[0] = q4_pair<0>(x[i], e0.x, e0.y);
-              v[1] = q4_pair<1>(x[i], e0.z, e0.w);
-              v[2] = q4_pair<2>(x[i], e1.x, e1.y);
-              v[3] = q4_pair<3>(x[i], e1.z, e1.w);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint4 e0 = exp[8 * q + 2 * i], e1 = exp[8 * q + 2 * i + 1];
+            r[4 * i] = q4_pair<0>(x[i], e0.x, e0.y);
+            r[4 * i + 1] = q4_pair<1>(x[i], e0.z, e0.w);
+            r[4 * i + 2] = q4_pair<2>(x[i], e1.x, e1.y);
+            r[4 * i + 3] = q4_pair<3>(x[i], e1.z, e1.w);
           }
         }
-        tmem_st_cols32(t_dst + buf * 64 + half * 32, r);
+        tmem_st_cols16(t_dst + q * 16, r);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -428,7 +423,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         }
         close(k);
       }
-      if (ok) {                              // nothing more to bring to bf16
+      const int loads = n;
+      for (int i = 0; i < 2 && ok; ++i, ++n) {       // nothing more to bring to bf16, for either slot's warps
         const int st = n % SP;
         if (n >= SP)
           ok = wait_for(&k_free[st], (uint32_t)((n / SP - 1) & 1)) && wait_for(&v_free[st], (uint32_t)((n / SP - 1) & 1));
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       }
       if (!ok) {                             // gave up: see the copies in flight land before leaving
         set_status(a.status, 0x811u);
-        for (int j = n > SP ? n - SP : 0; j < n; ++j) {
+        for (int j = loads > SP ? loads - SP : 0; j < loads; ++j) {
           wait_for(&k_land[j % SP], (uint32_t)((j / SP) & 1));
           wait_for(&v_land[j % SP], (uint32_t)((j / SP) & 1));
         }
@@ -604,93 +600,108 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         ++n_s;
         __syncwarp();
         tc_fence_after();
-        float x[NC];
-        auto load = [&]() {
-          tmem_ld_cols<NC>(t_s, x);
+        // 16 columns' scores
+        auto load = [&](int c0, float (&x)[16]) {
+          tmem_ld16(t_s + c0, x);
           if (masked) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (key > p.ctx + s_tok[c]) x[c] = -INFINITY;
+            for (int c = 0; c < 16; ++c)
+              if (key > p.ctx + s_tok[c0 + c]) x[c] = -INFINITY;
           }
         };
-        auto relate = [&]() {
-#pragma unroll
-          for (int c = 0; c < NC; c += 4) {
-            const float4 r = *reinterpret_cast<const float4*>(add + c);
-            const float2 u = fma2(make_float2(x[c], x[c + 1]), make_float2(scale, scale), make_float2(r.x, r.y));
-            const float2 v = fma2(make_float2(x[c + 2], x[c + 3]), make_float2(scale, scale), make_float2(r.z, r.w));
-            x[c] = u.x;
-            x[c + 1] = u.y;
-            x[c + 2] = v.x;
-            x[c + 3] = v.y;
-          }
+        // ... as weights: 2 columns from c0 + c
+        auto weight = [&](const float (&x)[16], int c0, int c) {
+          const float2 r = *reinterpret_cast<const float2*>(add + c0 + c);
+          float2 e = fma2(make_float2(x[c], x[c + 1]), make_float2(scale, scale), r);
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          return e;
         };
-        load();
         // Weights are relative to the row's reference: the maximum of the slot's first tile in which it sees a key, whose
         // own weight is then 1, exactly.  Later tiles keep it as long as no weight passes 2^24 (any reference far below
         // the maximum gives the same quotients: bf16 and fp32 have exponents to spare); then, and where rows see
-        // keys for the first time (masked tiles), the maximum is taken, and O and the sums rescaled.
-        bool look = j == j0 || masked;
-        if (!look) {
-          relate();
-          float top = -INFINITY;
+        // keys for the first time (masked tiles), the maximum is taken, O and the sums rescaled, and the weights formed again.
+        for (bool look = j == j0 || masked;; look = true) {
+          if (look) {
+            float* mine = s_max + warp * MAXR;
 #pragma unroll
-          for (int c = 0; c < NC; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
-          look = bar_or(2 + slot, 128, top > 24.f);
-          if (look) load();
-        }
-        if (look) {
-          float* mine = s_max + warp * MAXR;
+            for (int c0 = 0; c0 < NC; c0 += 16) {
+              float x[16];
+              load(c0, x);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float m = warp_max(x[c]);
-            if (lane == (c & 31)) mine[c] = m;
-          }
-          bar_sync(2 + slot, 128);
-          bool moved = false;
-          if (t < NC) {
-            const float* m4 = s_max + slot * 4 * MAXR + t;
-            const float mx = fmaxf(fmaxf(m4[0], m4[MAXR]), fmaxf(m4[2 * MAXR], m4[3 * MAXR])) * scale;
-            const float old = ref[t];
-            const bool move = old == -INFINITY ? mx > -INFINITY : mx > old + 19.f;
-            const float f = move && old != -INFINITY ? ex2(old - mx) : 1.f;
-            if (move) {
-              ref[t] = mx;
-              add[t] = -mx;
+              for (int c = 0; c < 16; ++c) {
+                const float m = warp_max(x[c]);
+                if (lane == c) mine[c0 + c] = m;
+              }
             }
-            alpha[t] = f;
-            moved = f != 1.f;
-          }
-          if (bar_or(2 + slot, 128, moved)) {
-#pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(alpha + c);
-              l[c / 2].x *= f.x;
-              l[c / 2].y *= f.y;
+            bar_sync(2 + slot, 128);
+            bool moved = false;
+            if (t < NC) {
+              const float* m4 = s_max + slot * 4 * MAXR + t;
+              const float mx = fmaxf(fmaxf(m4[0], m4[MAXR]), fmaxf(m4[2 * MAXR], m4[3 * MAXR])) * scale;
+              const float old = ref[t];
+              const bool move = old == -INFINITY ? mx > -INFINITY : mx > old + 19.f;
+              const float f = move && old != -INFINITY ? ex2(old - mx) : 1.f;
+              if (move) {
+                ref[t] = mx;
+                add[t] = -mx;
+              }
+              alpha[t] = f;
+              moved = f != 1.f;
             }
-            // O is whole here: the scores' barrier came after the slot's P V before them
+            if (bar_or(2 + slot, 128, moved)) {
+#pragma unroll
+              for (int c = 0; c < NC; c += 2) {
+                const float2 f = *reinterpret_cast<const float2*>(alpha + c);
+                l[c / 2].x *= f.x;
+                l[c / 2].y *= f.y;
+              }
+              // O is whole here: the scores' barrier came after the slot's P V before them
 #pragma unroll 1
-            for (int c = 0; c < NC; c += 16) {
-              uint32_t o[16];
-              tmem_ld_cols16(t_o + c, o);
+              for (int c = 0; c < NC; c += 16) {
+                uint32_t o[16];
+                tmem_ld_cols16(t_o + c, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[c + i]);
-              tmem_st_cols16(t_o + c, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[c + i]);
+                tmem_st_cols16(t_o + c, o);
+              }
+              tmem_st_wait();
             }
-            tmem_st_wait();
           }
-          relate();
-        }
+          uint32_t top = 0;                  // the largest weights of the even and odd columns (NaN is passed over)
 #pragma unroll
-        for (int c = 0; c < NC; c += 8) {
-          uint32_t w[4];
+          for (int c0 = 0; c0 < NC; c0 += 16) {
+            float x[16];
+            load(c0, x);
+            uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 e = make_float2(ex2(x[c + 2 * i]), ex2(x[c + 2 * i + 1]));
-            l[c / 2 + i] = add2(l[c / 2 + i], e);
-            w[i] = cvt_bf16x2(e.x, e.y);
+            for (int i = 0; i < 8; ++i) {
+              const float2 e = weight(x, c0, 2 * i);
+              l[c0 / 2 + i] = add2(l[c0 / 2 + i], e);
+              w[i] = cvt_bf16x2(e.x, e.y);
+              asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4*>(prow + ((((c0 >> 3) + i) ^ (t & 7)) << 4)) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
-          *reinterpret_cast<uint4*>(prow + (((c >> 3) ^ (t & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          // (0x4B80: 2^24; weights are not negative, so their bits are in order)
+          if (look || !bar_or(2 + slot, 128, (top & 0xffffu) > 0x4B80u || (top >> 16) > 0x4B80u)) break;
+          // Taken back: what is lost of the sums is 2^-24 of the weights taken back, of which the new reference leaves
+          // at most 1 in a sum that has a 1; an infinite one leaves nothing of what was there before.
+#pragma unroll
+          for (int c0 = 0; c0 < NC; c0 += 16) {
+            float x[16];
+            load(c0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 e = weight(x, c0, 2 * i);
+              float2& s = l[c0 / 2 + i];
+              s.x = e.x == INFINITY ? 0.f : s.x - e.x;
+              s.y = e.y == INFINITY ? 0.f : s.y - e.y;
+            }
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
