@@ -1908,6 +1908,7 @@ static int chunk_attention_impl(const spec_bf16* Q, int ldq, const int32_t* cu_r
   a.Hkv = Hkv; a.G = G; a.tpt = tpt;
   // (a scale of 0 weighs every visible key alike; masked scores have to stay -inf under it)
   a.scale_log2 = std::max(scale * 1.4426950408889634f, 1e-30f);
+  if (q4) a.scale_log2 *= q4_tile_scale();      // (keys and values enter the products scaled down by as much)
   a.O = O; a.ldo = ldo;
   a.wide = (reinterpret_cast<uintptr_t>(O) & 31u) == 0 && ldo % 16 == 0 ? 1 : 0;
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);

@@ -386,8 +386,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       // keys: their own four scales; values: those of the 4 keys whose scales this lane spreads for the warp
       const uint32_t codes = *reinterpret_cast<const uint32_t*>(page + Q4_SCALES + row * 4);
       if (kind == 1) {
-        const uint32_t s0 = q4_scale2(__byte_perm(codes, 0, 0x4140)), s1 = q4_scale2(__byte_perm(codes, 0, 0x4342));
-        exp[lane] = make_uint4(s0, q4_offset2(s0), s1, q4_offset2(s1));
+        const uint32_t c0 = __byte_perm(codes, 0, 0x4140), c1 = __byte_perm(codes, 0, 0x4342);
+        exp[lane] = make_uint4(q4_even2(c0), q4_less2(c0), q4_odd2(c1), q4_less2(c1));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_free[ps]);
@@ -398,20 +398,24 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-        uint32_t s = 0, o = 0;
+        uint32_t even = 0, odd = 0, less = 0;
         if (kind == 0) {
-          s = q4_scale2(__byte_perm(codes, 0, 0x4040 | q * 0x0101));
-          o = q4_offset2(s);
+          const uint32_t c = __byte_perm(codes, 0, 0x4040 | q * 0x0101);
+          even = q4_even2(c);
+          odd = q4_odd2(c);
+          less = q4_less2(c);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          const uint32_t x8 = x[i] >> 8;
           uint4 v;
           if (kind == 0) {
-            v = make_uint4(q4_pair<0>(x[i], s, o), q4_pair<1>(x[i], s, o), q4_pair<2>(x[i], s, o), q4_pair<3>(x[i], s, o));
+            v = make_uint4(q4_tile_pair<0>(x[i], x8, even, less), q4_tile_pair<1>(x[i], x8, odd, less),
+                           q4_tile_pair<2>(x[i], x8, even, less), q4_tile_pair<3>(x[i], x8, odd, less));
           } else {
-            const uint4 a0 = exp[8 * q + 2 * i], a1 = exp[8 * q + 2 * i + 1];
-            v = make_uint4(q4_pair<0>(x[i], a0.x, a0.y), q4_pair<1>(x[i], a0.z, a0.w), q4_pair<2>(x[i], a1.x, a1.y),
-                           q4_pair<3>(x[i], a1.z, a1.w));
+            const uint4 e0 = exp[8 * q + 2 * i], e1 = exp[8 * q + 2 * i + 1];
+            v = make_uint4(q4_tile_pair<0>(x[i], x8, e0.x, e0.y), q4_tile_pair<1>(x[i], x8, e0.z, e0.w),
+                           q4_tile_pair<2>(x[i], x8, e1.x, e1.y), q4_tile_pair<3>(x[i], x8, e1.z, e1.w));
           }
           *reinterpret_cast<uint4*>(dst + (q >> 1) * HALF + ((((q & 1) * 4 + i) ^ (row & 7)) << 4)) = v;
         }
@@ -1091,7 +1095,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             }
           }
         });
-        store(r, c0, acc, 1.f / sum, dims);
+        store(r, c0, acc, (Q4 ? Q4_TILE_SCALE : 1.f) / sum, dims);
         __syncwarp();
       }
     };
@@ -1125,7 +1129,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       __syncwarp();
       tc_fence_after();
       if (!r.arrived) {
-        const float inv = 1.f / l;
+        const float inv = (Q4 ? Q4_TILE_SCALE : 1.f) / l;
 #pragma unroll 1
         for (int c = r.c_lo; c < r.c_hi; c += 32) {
           float v[32];

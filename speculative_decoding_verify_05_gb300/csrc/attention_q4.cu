@@ -70,10 +70,20 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool x) {
                : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float warp_max(float x) {      // (NaN is passed over)
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
+// Columns folded over a warp's lanes: v[0] of lane i is then column i mod 16 of all 32 lanes.  Each step halves the columns
+// that a lane still holds (16 shuffles; a reduction instruction per column took longer than all of a tile's weights).
+template <class F>
+__device__ __forceinline__ void fold16(float (&v)[16], int lane, F&& f) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {      // (0 bytes: zeros)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -239,8 +249,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       // keys: their own four scales; values: those of the 4 keys whose scales this lane spreads for the warp
       const uint32_t codes = *reinterpret_cast<const uint32_t*>(page + Q4_SCALES + row * 4);
       if (is_v) {
-        const uint32_t s0 = q4_scale2(__byte_perm(codes, 0, 0x4140)), s1 = q4_scale2(__byte_perm(codes, 0, 0x4342));
-        exp[lane] = make_uint4(s0, q4_offset2(s0), s1, q4_offset2(s1));
+        const uint32_t c0 = __byte_perm(codes, 0, 0x4140), c1 = __byte_perm(codes, 0, 0x4342);
+        exp[lane] = make_uint4(q4_even2(c0), q4_less2(c0), q4_odd2(c1), q4_less2(c1));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&free_[st]);
@@ -253,22 +263,25 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         uint32_t r[16];
         const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
         if (!is_v) {
-          const uint32_t s = q4_scale2(__byte_perm(codes, 0, 0x4040 | q * 0x0101)), o = q4_offset2(s);
+          const uint32_t c = __byte_perm(codes, 0, 0x4040 | q * 0x0101);
+          const uint32_t even = q4_even2(c), odd = q4_odd2(c), less = q4_less2(c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            r[4 * i] = q4_pair<0>(x[i], s, o);
-            r[4 * i + 1] = q4_pair<1>(x[i], s, o);
-            r[4 * i + 2] = q4_pair<2>(x[i], s, o);
-            r[4 * i + 3] = q4_pair<3>(x[i], s, o);
+            const uint32_t x8 = x[i] >> 8;
+            r[4 * i] = q4_tile_pair<0>(x[i], x8, even, less);
+            r[4 * i + 1] = q4_tile_pair<1>(x[i], x8, odd, less);
+            r[4 * i + 2] = q4_tile_pair<2>(x[i], x8, even, less);
+            r[4 * i + 3] = q4_tile_pair<3>(x[i], x8, odd, less);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint4 e0 = exp[8 * q + 2 * i], e1 = exp[8 * q + 2 * i + 1];
-            r[4 * i] = q4_pair<0>(x[i], e0.x, e0.y);
-            r[4 * i + 1] = q4_pair<1>(x[i], e0.z, e0.w);
-            r[4 * i + 2] = q4_pair<2>(x[i], e1.x, e1.y);
-            r[4 * i + 3] = q4_pair<3>(x[i], e1.z, e1.w);
+            const uint32_t x8 = x[i] >> 8;
+            r[4 * i] = q4_tile_pair<0>(x[i], x8, e0.x, e0.y);
+            r[4 * i + 1] = q4_tile_pair<1>(x[i], x8, e0.z, e0.w);
+            r[4 * i + 2] = q4_tile_pair<2>(x[i], x8, e1.x, e1.y);
+            r[4 * i + 3] = q4_tile_pair<3>(x[i], x8, e1.z, e1.w);
           }
         }
         tmem_st_cols16(t_dst + q * 16, r);
@@ -600,15 +613,19 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         ++n_s;
         __syncwarp();
         tc_fence_after();
-        // 16 columns' scores
-        auto load = [&](int c0, float (&x)[16]) {
-          tmem_ld16(t_s + c0, x);
-          if (masked) {
+        // hidden scores become -inf in place (once or twice an item: a loop, so that few instructions are fetched for it)
+        if (masked) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < NC; c0 += 16) {
+            uint32_t h[16];
+            tmem_ld_cols16(t_s + c0, h);
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              if (key > p.ctx + s_tok[c0 + c]) x[c] = -INFINITY;
+              if (key > p.ctx + s_tok[c0 + c]) h[c] = 0xff800000u;        // -inf
+            tmem_st_cols16(t_s + c0, h);
           }
-        };
+          tmem_st_wait();
+        }
         // ... as weights: 2 columns from c0 + c
         auto weight = [&](const float (&x)[16], int c0, int c) {
           const float2 r = *reinterpret_cast<const float2*>(add + c0 + c);
@@ -619,20 +636,17 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         };
         // Weights are relative to the row's reference: the maximum of the slot's first tile in which it sees a key, whose
         // own weight is then 1, exactly.  Later tiles keep it as long as no weight passes 2^24 (any reference far below
-        // the maximum gives the same quotients: bf16 and fp32 have exponents to spare); then, and where rows see
-        // keys for the first time (masked tiles), the maximum is taken, O and the sums rescaled, and the weights formed again.
-        for (bool look = j == j0 || masked;; look = true) {
+        // the maximum gives the same quotients: bf16 and fp32 have exponents to spare); then the maximum is taken, O and
+        // the sums rescaled, and the weights formed again.  (A row that sees no key of the slot's first tile sees none
+        // of its later ones.)
+        for (bool look = j == j0;; look = true) {
           if (look) {
-            float* mine = s_max + warp * MAXR;
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < NC; c0 += 16) {
               float x[16];
-              load(c0, x);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float m = warp_max(x[c]);
-                if (lane == c) mine[c0 + c] = m;
-              }
+              tmem_ld16(t_s + c0, x);
+              fold16(x, lane, [](float a, float b) { return fmaxf(a, b); });
+              if (lane < 16) s_max[warp * MAXR + c0 + lane] = x[0];
             }
             bar_sync(2 + slot, 128);
             bool moved = false;
@@ -672,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 16) {
             float x[16];
-            load(c0, x);
+            tmem_ld16(t_s + c0, x);
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 16) {
             float x[16];
-            load(c0, x);
+            tmem_ld16(t_s + c0, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float2 e = weight(x, c0, 2 * i);
@@ -709,7 +723,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         if (lane == 0) mbar_arrive(&p_full[slot]);
       }
       // ---------------------------------------------------------- end of the piece
-      // sums of the warp's 32 keys, column c to lane c mod 32: each step halves the columns that a lane still holds
+      // sums of the warp's 32 keys
       float* sums = s_max + warp * MAXR;
 #pragma unroll
       for (int c0 = 0; c0 < NC; c0 += 16) {
@@ -719,16 +733,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
           v[2 * i] = l[c0 / 2 + i].x;
           v[2 * i + 1] = l[c0 / 2 + i].y;
         }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          const bool up = (lane & o) != 0;
-#pragma unroll
-          for (int i = 0; i < o; ++i) {
-            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
-        }
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+        fold16(v, lane, [](float a, float b) { return a + b; });
         if (lane < 16) sums[c0 + lane] = v[0];
       }
       const bool shared = p.shared();
@@ -748,8 +753,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         if (shared) {
           __stcg(a.part_ml + at * MAXR + tid, make_float2(m, sum));
         } else {
-          f0 /= sum;
-          f1 /= sum;
+          f0 *= Q4_TILE_SCALE / sum;
+          f1 *= Q4_TILE_SCALE / sum;
         }
         s_f[tid] = make_float2(f0, f1);
       }
@@ -883,7 +888,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
             if (s.t >= p.nt) break;
             s = sharers(base + 32, s.t);
           }
-          const float inv = 1.f / sum;
+          const float inv = Q4_TILE_SCALE / sum;
           const int tok = s_tok[r], g = (int)r - tok * a.G;
           *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + g) * D + lane * 4) =
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -927,6 +932,7 @@ cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t s) {
 }  // namespace
 
 int few_attention_q4_rows() { return MAXR; }
+float q4_tile_scale() { return Q4_TILE_SCALE; }
 
 cudaError_t launch_few_attention_q4(const ChunkAttnArgs& a, int grid, cudaStream_t s) {
   switch ((a.G * a.max_rows + 15) / 16) {

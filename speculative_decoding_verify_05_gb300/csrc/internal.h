@@ -279,6 +279,7 @@ cudaError_t launch_chunk_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs
 // ... and the same for few rows: G * max_rows <= few_attention_q4_rows().  Of the workspace it uses the counters, and
 // part_o as [grid][2][64][128] and part_ml as [grid][2][64].
 int few_attention_q4_rows();
+float q4_tile_scale();                  // scale_log2 of both is this times the softmax scale * log2(e)
 cudaError_t launch_few_attention_q4(const ChunkAttnArgs& a, int grid, cudaStream_t s);
 
 // ---- rejection sampler
