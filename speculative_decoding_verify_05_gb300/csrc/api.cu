@@ -1884,10 +1884,10 @@ static int chunk_attention_impl(const spec_bf16* Q, int ldq, const int32_t* cu_r
   if (!aligned16(workspace)) return fail(SPEC_EINVAL, "the workspace must be 16-byte aligned");
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
-  const int G = Hq / Hkv, tpt = 128 / G;
-  const bool few = q4 && (long long)G * max_rows <= few_attention_q4_rows();
+  const int G = Hq / Hkv, few = q4 ? few_attention_q4_columns(G, max_rows) : 0;
+  const int tpt = (few ? few : 128) / G;
   CUtensorMap tq, tk, tv;
-  if (!few) {
+  {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)M};
     cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)ldq * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tpt};
@@ -1917,7 +1917,7 @@ static int chunk_attention_impl(const spec_bf16* Q, int ldq, const int32_t* cu_r
   a.t_magic = (unsigned)((1ull << 32) / (2 * tpt)) + 1;
   a.inv_grid = ~0ull / p.grid;
   a.status = d->status;
-  cudaError_t e = few  ? launch_few_attention_q4(a, p.grid, static_cast<cudaStream_t>(stream))
+  cudaError_t e = few  ? launch_few_attention_q4(tq, a, few, p.grid, static_cast<cudaStream_t>(stream))
                   : q4 ? launch_chunk_attention_q4(tq, a, p.grid, static_cast<cudaStream_t>(stream))
                        : launch_chunk_attention(tq, tk, tv, a, p.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");

@@ -10,18 +10,17 @@
 // tiles would be written and read again at 128 bytes a cycle: 64 KB in and 64 KB out a page of keys and values, 1024
 // cycles, where HBM takes 740 to bring the page.  Only Q and P (bf16, N columns) are read from shared memory.
 //
-// TMEM (all 512 columns): two K and two V tiles (64 columns each), S and O of two slots (64 each).  Tile n belongs to slot
-// n mod 2: its own softmax warps, P buffer and O, each slot with references of its own, joined at the end of an item.
+// Work.  An item is a (sequence, kv head).  The tiles of all items in a row are cut into equal shares by cost, one for each
+// of a CTA's two slots; every slot works its own out from the lengths on the device.  The slots run on their own, each
+// with its warps, K, V, S and O tiles in TMEM (4 x 64 columns, all 512 for both) and page rings, so that one goes on while the
+// other starts or ends an item (with an item's tiles in turn to both, ending an item cost 4 us of the CTA: 64
+// sequences of 2 to 11 rows 126 us).  Pieces of an item that several slots share go to the
+// workspace as unnormalised O, reference and sum; the warps of its slots that are done when the last piece arrives join
+// it, a row at a time, in order of the slots whoever does it.
 //
-// Work.  An item is a (sequence, kv head).  The tiles of all items in a row are cut into equal shares by cost, one per
-// CTA; every CTA works its own out from the lengths on the device.  Pieces of an item that several CTAs share go to the
-// workspace as unnormalised O, reference and sum; the warps of its CTAs that are done when the last piece arrives join
-// it, a row at a time, in CTA order whoever does it.
-//
-// Roles (28 warps): 0-3, 4-7 softmax and epilogue of slot 0 and 1 (a thread per key, then per dim); 8 loads pages
-// by bulk copies, keys and values to a ring each; 9 issues the MMAs; 10 stages the queries; 11 walks the batch and posts the
-// CTA's pieces; 12-19 bring keys to bf16, 20-27 values, four warps a slot (with four in all for each, one tile after
-// the other, what a tile waits for was in the way: 16 x 1 row at 30000 keys 168 us).
+// Roles (28 warps; four to a slot where not said otherwise): 0-7 softmax and epilogue (a thread per key, then per dim); 8 and 9
+// issue a slot's MMAs; 10 and 11 walk the batch for a slot, post its pieces and load its queries and pages; 12-19
+// bring keys to bf16, 20-27 values.
 #include "attention_util.cuh"
 #include "internal.h"
 #include "q4.cuh"
@@ -34,28 +33,11 @@ namespace {
 constexpr int D = 128;
 constexpr int KT = 128;                   // keys per tile (one page)
 constexpr int MAXR = 64;                  // rows of an item
-constexpr int PR = 4;                     // posted pieces
-constexpr int SP = 8;                     // pages in flight, of keys and of values
+constexpr int PR = 4;                     // posted pieces of a slot
 constexpr int THREADS = 896;
 constexpr int REGS_ALL = 72, REGS_SOFTMAX = 112, REGS_OTHER = 56;
 static_assert(256 * REGS_SOFTMAX + 640 * REGS_OTHER <= THREADS * REGS_ALL, "register split");
-constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   // two of 64 columns each
-
-constexpr int Q_HALF = MAXR * 128;        // rows x 64 dims (128-byte swizzled rows)
-constexpr int OFF_Q = 0;                  // two buffers of two halves
-constexpr int OFF_P = OFF_Q + 2 * 2 * Q_HALF;          // of each slot: [key][row], 128-byte swizzled rows
-constexpr int OFF_KP = OFF_P + 2 * KT * 128;
-constexpr int OFF_VP = OFF_KP + SP * Q4_BYTES;
-constexpr int OFF_EXP = OFF_VP + SP * Q4_BYTES;        // scales of a tile of values, as pairs
-constexpr int OFF_REF = OFF_EXP + 4096;                // [2][64] references, [2][64] what is added to a score for it
-constexpr int OFF_ALPHA = OFF_REF + 4 * MAXR * 4;      // [2][64]
-constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;      // [8][64] maxima, later sums, of the softmax warps
-constexpr int OFF_F = OFF_MAX + 8 * MAXR * 4;          // [64] factors of the two slots' O
-constexpr int OFF_TOK = OFF_F + MAXR * 8;              // [64] token of each row
-constexpr int OFF_BAR = OFF_TOK + MAXR * 4;
-constexpr int N_BARS = 4 * SP + 18 + 2 * PR;
-constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
-static_assert(OFF_KP % 128 == 0 && OFF_EXP % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   // 64 columns for each slot
 
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // What an item's start and end cost, in keys; what reading a piece back takes (see shares_of).
@@ -85,21 +67,6 @@ __device__ __forceinline__ void fold16(float (&v)[16], int lane, F&& f) {
   }
   v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {      // (0 bytes: zeros)
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tmem_ld_cols8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // ----------------------------------------------------------------- the batch
 struct Seq {
   int r0, rows, ctx;
@@ -121,62 +88,73 @@ __device__ __forceinline__ int cut_tile(long long y, int keys, int nt) {
   const int t = ((int)y + KT / 2) / KT;
   return t * KT + KT / 2 >= keys ? nt : t;              // (no piece of a few keys)
 }
-// The cost of the batch and of a CTA's share of it.  Equal shares, but of so many keys that an item's pieces are not
+// The cost of the batch and of a slot's share of it.  Equal shares, but of so many keys that an item's pieces are not
 // joined for longer than they take.
 struct Shares {
   long long total, each;
   __device__ __forceinline__ long long start(int c) const { return min(total, c * each); }
 };
 __device__ __forceinline__ Shares shares_of(const ChunkAttnArgs& a, long long total, int keys) {
-  const long long even = (long long)__umul64hi((unsigned long long)total, a.inv_grid) + 1;
+  const long long even = (long long)__umul64hi((unsigned long long)total, a.inv_grid) / 2 + 1;      // (two slots)
   return Shares{total, max(even, (long long)sqrtf((float)PIECE_KEYS * keys))};
 }
 
-// A CTA's consecutive tiles of one item, as posted.
+// A slot's consecutive tiles of one item, as posted.
 struct Piece {
   int b, h;
   int t0, t1, nt;      // tiles t0 .. t1 - 1 of the item's nt
   int row0, rows, ctx;
-  int more;            // 0: no piece, the CTA is done
+  int more;            // 0: no piece, the slot is done
   long long start;     // cost of everything before the item
   __device__ __forceinline__ int tiles() const { return t1 - t0; }
   __device__ __forceinline__ bool shared() const { return t0 > 0 || t1 < nt; }
 };
-constexpr int OFF_RINGP = (OFF_MISC + 8 + 2 * SP * 4 + 7) & ~7;      // behind the TMEM address and the stages' marks
-constexpr int SMEM = OFF_RINGP + (PR + 1) * (int)sizeof(Piece) + (int)sizeof(Shares);
-static_assert(SMEM <= 227 * 1024, "shared memory budget");
 
 // NC: columns of the MMAs (rows of the queries, a multiple of 16).
 template <int NC>
-__global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const ChunkAttnArgs a) {
+struct Layout {
+  static constexpr int SP = NC <= 48 ? 4 : 3;                     // pages in flight of a slot, of keys and of values
+  static constexpr int Q_HALF = NC * 128;                         // rows x 64 dims (128-byte swizzled rows)
+  static constexpr int OFF_P = 0;                                 // of each slot: [key][row], 128-byte swizzled rows
+  static constexpr int OFF_Q = OFF_P + 2 * KT * 128;              // of each slot two buffers of two halves
+  static constexpr int OFF_KP = OFF_Q + 2 * 2 * 2 * Q_HALF;
+  static constexpr int OFF_VP = OFF_KP + 2 * SP * Q4_BYTES;
+  static constexpr int OFF_EXP = OFF_VP + 2 * SP * Q4_BYTES;      // scales of a tile of values, as pairs
+  static constexpr int OFF_REF = OFF_EXP + 4096;                  // [2][64] references
+  static constexpr int OFF_ADD = OFF_REF + 2 * MAXR * 4;          // [2][64] what is added to a score for it
+  static constexpr int OFF_ALPHA = OFF_ADD + 2 * MAXR * 4;        // [2][64] factors (of an end: what O is multiplied by)
+  static constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;        // [8][64] maxima, later sums, of the softmax warps
+  static constexpr int OFF_TOK = OFF_MAX + 8 * MAXR * 4;          // [64] token of each row
+  static constexpr int OFF_PIECE = OFF_TOK + MAXR * 4;            // [2][PR + 1]: posted, and the slot's first for the end
+  static constexpr int OFF_SHARES = OFF_PIECE + 2 * (PR + 1) * (int)sizeof(Piece);
+  static constexpr int OFF_BAR = OFF_SHARES + 2 * (int)sizeof(Shares);
+  static constexpr int N_BARS = 2 * (4 * SP + 5 + 4 + 2 * PR);
+  static constexpr int OFF_MORE = OFF_BAR + N_BARS * 8;           // marks of the page rings' stages, then the TMEM address
+  static constexpr int SMEM = OFF_MORE + 2 * 2 * SP * 4 + 8;
+  static_assert(OFF_KP % 128 == 0 && OFF_EXP % 16 == 0 && OFF_PIECE % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+template <int NC>
+__global__ void __launch_bounds__(THREADS, 1)
+few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttnArgs a) {
+  using L = Layout<NC>;
+  constexpr int SP = L::SP;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* k_land = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [SP] page of keys landed
-  uint64_t* k_free = k_land + SP;          // [SP] ... and read
-  uint64_t* v_land = k_free + SP;
-  uint64_t* v_free = v_land + SP;
-  uint64_t* ka_full = v_free + SP;         // [2] K tile in TMEM
-  uint64_t* ka_free = ka_full + 2;         // [2] its product done
-  uint64_t* va_full = ka_free + 2;
-  uint64_t* va_free = va_full + 2;
-  uint64_t* s_full = va_free + 2;          // [2] scores of a slot in TMEM (and the slot's P V before them done)
-  uint64_t* p_full = s_full + 2;           // [2] P in shared memory, S read, O rescaled
-  uint64_t* o_full = p_full + 2;           // [2] the slot's last P V of a piece done
-  uint64_t* q_full = o_full + 2;           // [2] queries staged
-  uint64_t* q_free = q_full + 2;           // [2] the last product with them done
-  uint64_t* posted = q_free + 2;           // [PR]
-  uint64_t* taken = posted + PR;           // [PR]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(taken + PR);
-  int* k_more = reinterpret_cast<int*>(tmem_slot + 2);      // [SP] 0: nothing more behind this stage
-  int* v_more = k_more + SP;
-  Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RINGP);
-  Piece* s_first = ring + PR;              // the CTA's first piece, for the end
-  Shares* s_shares = reinterpret_cast<Shares*>(ring + PR + 1);
-  float* s_ref = reinterpret_cast<float*>(smem + OFF_REF);
-  float* s_add = s_ref + 2 * MAXR;
-  float* s_alpha = reinterpret_cast<float*>(smem + OFF_ALPHA);
-  float* s_max = reinterpret_cast<float*>(smem + OFF_MAX);
-  float2* s_f = reinterpret_cast<float2*>(smem + OFF_F);
-  int* s_tok = reinterpret_cast<int*>(smem + OFF_TOK);
+  struct Bars {
+    uint64_t k_land[SP], k_free[SP];     // page of keys landed, read
+    uint64_t v_land[SP], v_free[SP];
+    uint64_t ka_full, va_full;           // K, V tile in TMEM
+    uint64_t s_full;                     // scores in TMEM (K read)
+    uint64_t p_full;                     // P in shared memory, S read, O rescaled
+    uint64_t o_done;                     // P V done (V and P read, O whole)
+    uint64_t q_full[2], q_free[2];
+    uint64_t posted[PR], taken[PR];
+  };
+  static_assert(2 * sizeof(Bars) == L::N_BARS * 8, "barriers");
+  Bars* all_bars = reinterpret_cast<Bars*>(smem + L::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MORE + 2 * 2 * SP * 4);
+  int* s_tok = reinterpret_cast<int*>(smem + L::OFF_TOK);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if ((smem_u32(smem) & 1023u) != 0) {     // (the swizzled tiles need it; the same for every thread)
@@ -184,31 +162,33 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < SP; ++i) {
-      mbar_init(&k_land[i], 1);
-      mbar_init(&k_free[i], 4);
-      mbar_init(&v_land[i], 1);
-      mbar_init(&v_free[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ka_full[i], 4);
-      mbar_init(&ka_free[i], 1);
-      mbar_init(&va_full[i], 4);
-      mbar_init(&va_free[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_free[i], 1);
-    }
-    for (int i = 0; i < PR; ++i) {
-      mbar_init(&posted[i], 1);
-      mbar_init(&taken[i], 11);            // loads, MMA, queries, 8 softmax warps
+    tma_prefetch_desc(&tmQ);
+    for (int x = 0; x < 2; ++x) {
+      Bars& b = all_bars[x];
+      for (int i = 0; i < SP; ++i) {
+        mbar_init(&b.k_land[i], 1);
+        mbar_init(&b.k_free[i], 4);
+        mbar_init(&b.v_land[i], 1);
+        mbar_init(&b.v_free[i], 4);
+      }
+      mbar_init(&b.ka_full, 4);
+      mbar_init(&b.va_full, 4);
+      mbar_init(&b.s_full, 1);
+      mbar_init(&b.p_full, 4);
+      mbar_init(&b.o_done, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&b.q_full[i], 1);
+        mbar_init(&b.q_free[i], 1);
+      }
+      for (int i = 0; i < PR; ++i) {
+        mbar_init(&b.posted[i], 1);
+        mbar_init(&b.taken[i], 5);         // MMA, 4 softmax warps
+      }
     }
     fence_barrier_init();
   }
   if (tid < MAXR) s_tok[tid] = tid / a.G;
-  if (warp == 9) tmem_alloc(tmem_slot, TMEM_COLS);
+  if (warp == 8) tmem_alloc(tmem_slot, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -217,32 +197,32 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
   pdl_wait();
   pdl_trigger();
 
-  // the k-th posted piece, by a whole warp; false after a wait that ran out
-  auto open = [&](int k, bool& ok) {
-    ok = __all_sync(0xffffffffu, ok && wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1)));
-    return ring[k % PR];
-  };
-  auto close = [&](int k) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&taken[k % PR]);
-  };
+  // slot of the warp: softmax 0-7, MMA 8 and 9, pages 10 and 11, keys 12-19, values 20-27
+  const int slot = warp < 8 || warp >= 12 ? (warp >> 2) + (warp >= 12 ? 1 : 0) & 1 : warp & 1;
+  Bars& bar = all_bars[slot];
+  Piece* ring = reinterpret_cast<Piece*>(smem + L::OFF_PIECE) + slot * (PR + 1);
+  Piece* s_first = ring + PR;
+  Shares* s_shares = reinterpret_cast<Shares*>(smem + L::OFF_SHARES) + slot;
+  int* k_more = reinterpret_cast<int*>(smem + L::OFF_MORE) + slot * 2 * SP;      // [SP] 0: nothing more from this stage on
+  int* v_more = k_more + SP;
+  const int me = blockIdx.x * 2 + slot;
 
   if (warp >= 12) {
     // -------------------------------------------------------------- pages to bf16: keys (12-19), values (20-27)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     const bool is_v = warp >= 20;
-    const int row = tid & 127, buf = ((warp - 12) >> 2) & 1;
-    const uint32_t t_dst = (is_v ? T_V : T_K) + buf * 64 + (uint32_t((warp & 3) * 32) << 16);
-    uint64_t *land = is_v ? v_land : k_land, *free_ = is_v ? v_free : k_free;
-    uint64_t *full = is_v ? va_full : ka_full, *gone = is_v ? va_free : ka_free;
+    const int row = tid & 127;
+    const uint32_t t_dst = (is_v ? T_V : T_K) + slot * 64 + (uint32_t((warp & 3) * 32) << 16);
+    uint64_t *land = is_v ? bar.v_land : bar.k_land, *free_ = is_v ? bar.v_free : bar.k_free;
+    uint64_t *full = is_v ? &bar.va_full : &bar.ka_full, *gone = is_v ? &bar.o_done : &bar.s_full;
     const int* more = is_v ? v_more : k_more;
-    uint4* exp = reinterpret_cast<uint4*>(smem + OFF_EXP) + (warp & 7) * 32;
+    uint4* exp = reinterpret_cast<uint4*>(smem + L::OFF_EXP) + (warp & 7) * 32;
     bool ok = true;
-    for (int n = buf;; n += 2) {
+    for (int n = 0;; ++n) {
       const int st = n % SP;
       ok = __all_sync(0xffffffffu, wait_for(&land[st], (uint32_t)((n / SP) & 1)));
       if (!ok || !more[st]) break;
-      const uint8_t* page = smem + (is_v ? OFF_VP : OFF_KP) + st * Q4_BYTES;
+      const uint8_t* page = smem + (is_v ? L::OFF_VP : L::OFF_KP) + (slot * SP + st) * Q4_BYTES;
       uint4 w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4*>(page + q * Q4_PLANE + row * 16);
@@ -254,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&free_[st]);
-      if (n >= 2) ok = wait_for(&gone[buf], (uint32_t)(((n >> 1) - 1) & 1));
+      if (n > 0) ok = wait_for(gone, (uint32_t)((n - 1) & 1));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -289,13 +269,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[buf]);
+      if (lane == 0) mbar_arrive(full);
     }
     if (!ok) set_status(a.status, 0x851u);
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-    if (warp == 11) {
-      // ------------------------------------------------------------ pieces
+    if (warp >= 10) {
+      // ------------------------------------------------------------ pieces, queries, pages
       const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
       long long own = 0;
       bool bad = false;
@@ -310,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
           longest = max(longest, s.ctx + s.rows);
         }
       }
-      if (bad && blockIdx.x == 0) set_status(a.status, 0xAF1u);
+      if (bad && me == 0) set_status(a.status, 0xAF1u);
       long long before = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -351,9 +331,21 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         c.t = cut_tile(x - c.start, keys, (keys + KT - 1) / KT);
         return c;
       };
-      Cut c = cut_at(shares.start(blockIdx.x));
-      const Cut e = cut_at(shares.start(blockIdx.x + 1));
-      for (int k = 0;;) {
+      Cut c = cut_at(shares.start(me));
+      const Cut e = cut_at(shares.start(me + 1));
+      const uint64_t pol = l2_policy_evict_first();
+      const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * D * 2);
+      bool ok = true;
+      int n = 0, k = 0;                      // tiles and pieces so far
+      auto stage_free = [&](int n) {
+        const int st = n % SP;
+        if (n >= SP)
+          ok = ok && wait_for(&bar.k_free[st], (uint32_t)((n / SP - 1) & 1)) &&
+               wait_for(&bar.v_free[st], (uint32_t)((n / SP - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        return st;
+      };
+      for (;;) {
         Piece p{};
         if (c.b < a.B) {
           const int keys = c.s.ctx + c.s.rows;
@@ -364,23 +356,53 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
           else if (p.t1 <= p.t0) p.more = last ? 0 : -1;             // (nothing of this item)
         }
         if (p.more >= 0) {
-          const bool ok = k < PR || wait_for(&taken[k % PR], (uint32_t)((k / PR - 1) & 1));
-          if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) set_status(a.status, 0x801u);
-            break;
-          }
+          ok = __all_sync(0xffffffffu, ok && (k < PR || wait_for(&bar.taken[k % PR], (uint32_t)((k / PR - 1) & 1))));
+          if (!ok) break;
           if (lane == 0) {
             if (k == 0) {
               *s_first = p;
               *s_shares = shares;
             }
             ring[k % PR] = p;
-            mbar_arrive(&posted[k % PR]);
+            mbar_arrive(&bar.posted[k % PR]);
           }
           __syncwarp();
+          if (p.more == 0) break;
+          const int qb = k & 1;
+          if (k >= 2) ok = wait_for(&bar.q_free[qb], (uint32_t)(((k >> 1) - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            uint8_t* dst = smem + L::OFF_Q + (slot * 2 + qb) * 2 * L::Q_HALF;
+            mbar_arrive_expect_tx(&bar.q_full[qb], q_bytes);
+            tma_load_3d(dst, &tmQ, &bar.q_full[qb], 0, p.h * a.G, p.row0);
+            tma_load_3d(dst + L::Q_HALF, &tmQ, &bar.q_full[qb], 64, p.h * a.G, p.row0);
+          }
           ++k;
+          int ids = 0, base = -1;            // page ids of 32 tiles at a time, one per lane
+          for (int t = p.t0; t < p.t1; ++t, ++n) {
+            if (base < 0 || t >= base + 32) {
+              base = t;
+              ids = t + lane < p.t1 ? a.block_table[(size_t)p.b * a.max_pages + t + lane] : 0;
+              if (ids < 0 || ids >= a.num_pages) {
+                set_status(a.status, 0xAF2u);
+                ids = 0;
+              }
+            }
+            const size_t at = ((size_t)p.h * a.num_pages + __shfl_sync(0xffffffffu, ids, t - base)) * Q4_BYTES;
+            const int st = stage_free(n);
+            if (!ok) break;
+            if (lane == 0) {
+              uint8_t *kd = smem + L::OFF_KP + (slot * SP + st) * Q4_BYTES, *vd = smem + L::OFF_VP + (slot * SP + st) * Q4_BYTES;
+              k_more[st] = v_more[st] = 1;
+              mbar_arrive_expect_tx(&bar.k_land[st], Q4_BYTES);
+              bulk_load_hint(kd, static_cast<const uint8_t*>(a.Kpool) + at, Q4_BYTES, &bar.k_land[st], pol);
+              mbar_arrive_expect_tx(&bar.v_land[st], Q4_BYTES);
+              bulk_load_hint(vd, static_cast<const uint8_t*>(a.Vpool) + at, Q4_BYTES, &bar.v_land[st], pol);
+            }
+          }
+          if (!ok) break;
         }
-        if (p.more == 0) break;
         // the next item
         c.t = 0;
         c.start += item_cost(c.s);
@@ -401,75 +423,41 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
           }
         }
       }
-      __syncwarp();
-    } else if (warp == 8) {
-      // ------------------------------------------------------------ pages
-      bool ok = true;
-      int n = 0;
-      const uint64_t pol = l2_policy_evict_first();
-      for (int k = 0;; ++k) {
-        const Piece p = open(k, ok);
-        if (!ok || !p.more) break;
-        int ids = 0, base = -1;              // page ids of 32 tiles at a time, one per lane
-        for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-          if (base < 0 || t >= base + 32) {
-            base = t;
-            ids = t + lane < p.t1 ? a.block_table[(size_t)p.b * a.max_pages + t + lane] : 0;
-            if (ids < 0 || ids >= a.num_pages) {
-              set_status(a.status, 0xAF2u);
-              ids = 0;
-            }
-          }
-          const size_t at = ((size_t)p.h * a.num_pages + __shfl_sync(0xffffffffu, ids, t - base)) * Q4_BYTES;
-          const int st = n % SP;
-          if (n >= SP)
-            ok = wait_for(&k_free[st], (uint32_t)((n / SP - 1) & 1)) && wait_for(&v_free[st], (uint32_t)((n / SP - 1) & 1));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            k_more[st] = v_more[st] = 1;
-            mbar_arrive_expect_tx(&k_land[st], Q4_BYTES);
-            bulk_load_hint(smem + OFF_KP + st * Q4_BYTES, static_cast<const uint8_t*>(a.Kpool) + at, Q4_BYTES, &k_land[st], pol);
-            mbar_arrive_expect_tx(&v_land[st], Q4_BYTES);
-            bulk_load_hint(smem + OFF_VP + st * Q4_BYTES, static_cast<const uint8_t*>(a.Vpool) + at, Q4_BYTES, &v_land[st], pol);
-          }
-        }
-        close(k);
-      }
       const int loads = n;
-      for (int i = 0; i < 2 && ok; ++i, ++n) {       // nothing more to bring to bf16, for either slot's warps
-        const int st = n % SP;
-        if (n >= SP)
-          ok = wait_for(&k_free[st], (uint32_t)((n / SP - 1) & 1)) && wait_for(&v_free[st], (uint32_t)((n / SP - 1) & 1));
+      if (ok) {                              // nothing more to bring to bf16
+        const int st = stage_free(n);
         if (ok && lane == 0) {
           k_more[st] = v_more[st] = 0;
-          mbar_arrive(&k_land[st]);
-          mbar_arrive(&v_land[st]);
+          mbar_arrive(&bar.k_land[st]);
+          mbar_arrive(&bar.v_land[st]);
         }
       }
       if (!ok) {                             // gave up: see the copies in flight land before leaving
         set_status(a.status, 0x811u);
         for (int j = loads > SP ? loads - SP : 0; j < loads; ++j) {
-          wait_for(&k_land[j % SP], (uint32_t)((j / SP) & 1));
-          wait_for(&v_land[j % SP], (uint32_t)((j / SP) & 1));
+          wait_for(&bar.k_land[j % SP], (uint32_t)((j / SP) & 1));
+          wait_for(&bar.v_land[j % SP], (uint32_t)((j / SP) & 1));
         }
+        for (int j = k > 2 ? k - 2 : 0; j < k; ++j) wait_for(&bar.q_full[j & 1], (uint32_t)((j >> 1) & 1));
       }
-    } else if (warp == 9) {
+      __syncwarp();
+    } else {
       // ------------------------------------------------------------ MMA issue
-      // Tile n + 2's scores are issued behind tile n's P V (the slot's S is read by then).  The whole warp walks the
-      // tiles and one elected lane issues; after a wait that ran out it goes on without waiting (to garbage that nobody
-      // reads).
+      // A tile's scores are issued as soon as the softmax has read those before them, ahead of the P V of the tile
+      // before, which the softmax waits for only when it stores its weights.  The whole warp walks the tiles and one elected
+      // lane issues; after a wait that ran out it goes on without waiting (to garbage that nobody reads).
       const bool leader = elect_one();
       constexpr uint32_t idesc_s = umma_idesc_bf16(KT, NC), idesc_pv = umma_idesc_bf16(D, NC) | (1u << 16);   // (P: MN-major)
+      const uint32_t t0 = slot * 64;
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = wait_for(bar, parity);
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        if (ok) ok = wait_for(b, parity);
       };
       struct Cursor {
         int k, j, tiles, more;               // piece, its tile, tiles
       };
       auto enter = [&](Cursor& c) {
-        wait(&posted[c.k % PR], (uint32_t)((c.k / PR) & 1));
+        wait(&bar.posted[c.k % PR], (uint32_t)((c.k / PR) & 1));
         ok = __all_sync(0xffffffffu, ok);
         const Piece& p = ring[c.k % PR];
         c.j = 0;
@@ -483,103 +471,73 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         }
       };
       auto scores = [&](int n, Cursor& c) {
-        const int buf = n & 1, qb = c.k & 1;
-        if (c.j == 0) wait(&q_full[qb], (uint32_t)((c.k >> 1) & 1));
-        wait(&ka_full[buf], (uint32_t)((n >> 1) & 1));
+        const int qb = c.k & 1;
+        if (c.j == 0) wait(&bar.q_full[qb], (uint32_t)((c.k >> 1) & 1));
+        wait(&bar.ka_full, (uint32_t)(n & 1));
         tc_fence_after();
         if (leader) {
-          const uint64_t qd = umma_desc_sw128(smem_u32(smem + OFF_Q + qb * 2 * Q_HALF));
+          const uint64_t qd = umma_desc_sw128(smem_u32(smem + L::OFF_Q + (slot * 2 + qb) * 2 * L::Q_HALF));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(T_S + buf * 64, T_K + buf * 64 + kk * 8, qd + (((kk >> 2) * Q_HALF + (kk & 3) * 32) >> 4), idesc_s,
+            umma_bf16_ts(T_S + t0, T_K + t0 + kk * 8, qd + (((kk >> 2) * L::Q_HALF + (kk & 3) * 32) >> 4), idesc_s,
                          kk > 0 ? 1u : 0u);
-          umma_commit(&s_full[buf]);
-          umma_commit(&ka_free[buf]);
-          if (c.j + 1 == c.tiles) umma_commit(&q_free[qb]);
-        }
-        __syncwarp();
-      };
-      auto weigh = [&](int n, Cursor& c) {
-        const int buf = n & 1;
-        wait(&va_full[buf], (uint32_t)((n >> 1) & 1));
-        wait(&p_full[buf], (uint32_t)((n >> 1) & 1));
-        tc_fence_after();
-        if (leader) {
-          const uint64_t pd = desc_mn(smem_u32(smem + OFF_P + buf * KT * 128), 0);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(T_O + buf * 64, T_V + buf * 64 + kk * 8, pd + kk * 128, idesc_pv, c.j >= 2 || kk > 0 ? 1u : 0u);
-          umma_commit(&va_free[buf]);
-          if (c.j + 2 >= c.tiles) umma_commit(&o_full[buf]);
+          umma_commit(&bar.s_full);
+          if (c.j + 1 == c.tiles) umma_commit(&bar.q_free[qb]);
         }
         __syncwarp();
       };
       Cursor cs{0, 0, 0, 0}, cp{0, 0, 0, 0};
       enter(cs);
       cp = cs;
-      int ns = 0;
-      for (; ns < 2 && cs.more; ++ns) {
-        scores(ns, cs);
+      if (cs.more) {
+        scores(0, cs);
         step(cs);
       }
       for (int n = 0; cp.more; ++n) {
-        weigh(n, cp);
-        const int done = cp.k;
-        step(cp);
-        if (cp.k != done) close(done);
+        wait(&bar.p_full, (uint32_t)(n & 1));
         if (cs.more) {
-          scores(ns, cs);
-          ++ns;
+          scores(n + 1, cs);
           step(cs);
         }
+        wait(&bar.va_full, (uint32_t)(n & 1));
+        tc_fence_after();
+        if (leader) {
+          const uint64_t pd = desc_mn(smem_u32(smem + L::OFF_P + slot * KT * 128), 0);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_ts(T_O + t0, T_V + t0 + kk * 8, pd + kk * 128, idesc_pv, cp.j > 0 || kk > 0 ? 1u : 0u);
+          umma_commit(&bar.o_done);
+        }
+        __syncwarp();
+        const int done = cp.k;
+        step(cp);
+        if (cp.k != done && lane == 0) mbar_arrive(&bar.taken[done % PR]);
       }
       if (!ok) set_status(a.status, 0x821u);
       __syncwarp();
-    } else {
-      // ------------------------------------------------------------ queries: row r = token r / G, head r mod G; zeros behind
-      bool ok = true;
-      for (int k = 0;; ++k) {
-        const Piece p = open(k, ok);
-        if (!ok || !p.more) break;
-        const int qb = k & 1;
-        if (k >= 2) ok = wait_for(&q_free[qb], (uint32_t)(((k >> 1) - 1) & 1));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int R = p.rows * a.G, ch = lane & 15;
-        const uint32_t dst = smem_u32(smem + OFF_Q + qb * 2 * Q_HALF) + (ch >> 3) * Q_HALF;
-#pragma unroll 4
-        for (int r = lane >> 4; r < NC; r += 2) {
-          const int tok = r < R ? s_tok[r] : 0, g = r < R ? r - tok * a.G : 0;
-          cp_async16(dst + sw128_off(r, (ch & 7) * 8),
-                     a.Q + (size_t)(p.row0 + tok) * a.ldq + (size_t)(p.h * a.G + g) * D + ch * 8, r < R ? 16u : 0u);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[qb]);
-        close(k);
-      }
-      if (!ok) set_status(a.status, 0x831u);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
-    // ------------------------------------------------------------ softmax and epilogue of a slot
+    // ------------------------------------------------------------ softmax and epilogue
     // (After a wait that ran out a warp stops waiting, but keeps the control flow up to the next piece, so that the
     // named barriers stay matched.)
-    const int slot = warp >> 2, t = tid & 127;           // key of the tile; dim of the output
+    const int t = tid & 127;               // key of the tile; dim of the output
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t t_s = T_S + slot * 64 + lanes, t_o = T_O + slot * 64 + lanes;
-    float *ref = s_ref + slot * MAXR, *add = s_add + slot * MAXR, *alpha = s_alpha + slot * MAXR;
-    uint8_t* prow = smem + OFF_P + slot * KT * 128 + t * 128;
+    float* ref = reinterpret_cast<float*>(smem + L::OFF_REF) + slot * MAXR;
+    float* add = reinterpret_cast<float*>(smem + L::OFF_ADD) + slot * MAXR;
+    float* alpha = reinterpret_cast<float*>(smem + L::OFF_ALPHA) + slot * MAXR;
+    float* s_max = reinterpret_cast<float*>(smem + L::OFF_MAX) + slot * 4 * MAXR;
+    uint8_t* tile_p = smem + L::OFF_P + slot * KT * 128;
+    uint8_t* prow = tile_p + t * 128;
     const float scale = a.scale_log2;
-    const int me = blockIdx.x;
+    const int wq = warp & 3;
     bool ok = true;
-    int n = 0;                             // tiles of the pieces before
-    uint32_t n_s = 0, ph_o = 0;            // scores so far; phase of each slot's o_full, a bit each
+    uint32_t n = 0;                        // tiles so far
     Shares shares{0, 0};
-    const Piece* shared_last = nullptr;    // the CTA's last piece, where its item goes on in the next CTA
-    bool shared_first = false;             // the first piece's item came from the CTA before
-    // the last CTA up to this one whose share does not start inside the item, 32 at a time
+    const Piece* shared_last = nullptr;    // the slot's last piece, where its item goes on in the next slot
+    bool shared_first = false;             // the first piece's item came from the slot before
+    // the last slot up to this one whose share does not start inside the item, 32 at a time
     auto first_of = [&](const Piece& p) {
       const int keys = p.ctx + p.rows;
       int c = me;
@@ -588,9 +546,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       return c;
     };
     for (int k = 0;; ++k) {
-      ok = ok && wait_for(&posted[k % PR], (uint32_t)((k / PR) & 1));
+      ok = ok && wait_for(&bar.posted[k % PR], (uint32_t)((k / PR) & 1));
       // (also: everybody has read what the piece before left in shared memory and TMEM)
-      if (bar_or(1, 256, !ok)) {
+      if (bar_or(1 + slot, 128, !ok)) {
         ok = false;
         break;
       }
@@ -601,16 +559,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       float2 l[NC / 2];
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      // (columns behind the rows hold anything: their weights are 0, or NaN, and nobody looks at them)
+      const int R = p.rows * a.G;
       if (t < MAXR) {
         ref[t] = -INFINITY;
-        add[t] = 0.f;
+        add[t] = t < R ? 0.f : -INFINITY;
       }
-      const int j0 = (n + slot) & 1;
-      for (int j = j0; j < tiles; j += 2) {
+      for (int j = 0; j < tiles; ++j, ++n) {
         const int key = (p.t0 + j) * KT + t;
         const bool masked = (p.t0 + j) * KT + KT - 1 > p.ctx;       // (some row does not see some key)
-        ok = ok && wait_for(&s_full[slot], n_s & 1);
-        ++n_s;
+        ok = ok && wait_for(&bar.s_full, n & 1);
         __syncwarp();
         tc_fence_after();
         // hidden scores become -inf in place (once or twice an item: a loop, so that few instructions are fetched for it)
@@ -634,24 +592,24 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
           e.y = ex2(e.y);
           return e;
         };
-        // Weights are relative to the row's reference: the maximum of the slot's first tile in which it sees a key, whose
+        // Weights are relative to the row's reference: the maximum of the piece's first tile in which it sees a key, whose
         // own weight is then 1, exactly.  Later tiles keep it as long as no weight passes 2^24 (any reference far below
         // the maximum gives the same quotients: bf16 and fp32 have exponents to spare); then the maximum is taken, O and
-        // the sums rescaled, and the weights formed again.  (A row that sees no key of the slot's first tile sees none
+        // the sums rescaled, and the weights formed again.  (A row that sees no key of the piece's first tile sees none
         // of its later ones.)
-        for (bool look = j == j0;; look = true) {
+        for (bool look = j == 0;; look = true) {
           if (look) {
 #pragma unroll 1
             for (int c0 = 0; c0 < NC; c0 += 16) {
               float x[16];
               tmem_ld16(t_s + c0, x);
               fold16(x, lane, [](float a, float b) { return fmaxf(a, b); });
-              if (lane < 16) s_max[warp * MAXR + c0 + lane] = x[0];
+              if (lane < 16) s_max[wq * MAXR + c0 + lane] = x[0];
             }
-            bar_sync(2 + slot, 128);
+            bar_sync(1 + slot, 128);
             bool moved = false;
-            if (t < NC) {
-              const float* m4 = s_max + slot * 4 * MAXR + t;
+            if (t < R) {
+              const float* m4 = s_max + t;
               const float mx = fmaxf(fmaxf(m4[0], m4[MAXR]), fmaxf(m4[2 * MAXR], m4[3 * MAXR])) * scale;
               const float old = ref[t];
               const bool move = old == -INFINITY ? mx > -INFINITY : mx > old + 19.f;
@@ -663,14 +621,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
               alpha[t] = f;
               moved = f != 1.f;
             }
-            if (bar_or(2 + slot, 128, moved)) {
+            if (bar_or(1 + slot, 128, moved)) {
 #pragma unroll
               for (int c = 0; c < NC; c += 2) {
                 const float2 f = *reinterpret_cast<const float2*>(alpha + c);
                 l[c / 2].x *= f.x;
                 l[c / 2].y *= f.y;
               }
-              // O is whole here: the scores' barrier came after the slot's P V before them
+              ok = ok && wait_for(&bar.o_done, (n - 1) & 1);       // O whole (some tile was before: a factor is not 1)
+              __syncwarp();
+              tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < NC; c += 16) {
                 uint32_t o[16];
@@ -682,6 +642,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
               tmem_st_wait();
             }
           }
+          if (j > 0) ok = ok && wait_for(&bar.o_done, (n - 1) & 1);      // P read
           uint32_t top = 0;                  // the largest weights of the even and odd columns (NaN is passed over)
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 16) {
@@ -701,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
                   make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
           // (0x4B80: 2^24; weights are not negative, so their bits are in order)
-          if (look || !bar_or(2 + slot, 128, (top & 0xffffu) > 0x4B80u || (top >> 16) > 0x4B80u)) break;
+          if (look || !bar_or(1 + slot, 128, (top & 0xffffu) > 0x4B80u || (top >> 16) > 0x4B80u)) break;
           // Taken back: what is lost of the sums is 2^-24 of the weights taken back, of which the new reference leaves
           // at most 1 in a sum that has a 1; an infinite one leaves nothing of what was there before.
 #pragma unroll
@@ -720,11 +681,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[slot]);
+        if (lane == 0) mbar_arrive(&bar.p_full);
       }
       // ---------------------------------------------------------- end of the piece
       // sums of the warp's 32 keys
-      float* sums = s_max + warp * MAXR;
+      float* sums = s_max + wq * MAXR;
 #pragma unroll
       for (int c0 = 0; c0 < NC; c0 += 16) {
         float v[16];
@@ -739,61 +700,30 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       const bool shared = p.shared();
       const int c_first = shared ? first_of(p) : me;
       const size_t at = (size_t)me * 2 + (me == c_first ? 1 : 0);
-      bar_sync(1, 256);
-      if (tid < NC) {
-        const float m0 = s_ref[tid], m1 = s_ref[MAXR + tid], m = fmaxf(m0, m1), base = m == -INFINITY ? 0.f : m;
-        float f0 = ex2(m0 - base), f1 = ex2(m1 - base);
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          l0 += s_max[w * MAXR + tid];
-          l1 += s_max[(4 + w) * MAXR + tid];
-        }
-        const float sum = l0 * f0 + l1 * f1;
-        if (shared) {
-          __stcg(a.part_ml + at * MAXR + tid, make_float2(m, sum));
-        } else {
-          f0 *= Q4_TILE_SCALE / sum;
-          f1 *= Q4_TILE_SCALE / sum;
-        }
-        s_f[tid] = make_float2(f0, f1);
+      bar_sync(1 + slot, 128);
+      if (t < R) {
+        const float sum = (s_max[t] + s_max[MAXR + t]) + (s_max[2 * MAXR + t] + s_max[3 * MAXR + t]);
+        if (shared) __stcg(a.part_ml + at * MAXR + t, make_float2(ref[t], sum));
+        else alpha[t] = Q4_TILE_SCALE / sum;
       }
-      bar_sync(1, 256);
-      const bool have0 = tiles > (n & 1), have1 = tiles > ((n + 1) & 1);
-      if (have0) ok = ok && wait_for(&o_full[0], ph_o & 1u);
-      if (have1) ok = ok && wait_for(&o_full[1], (ph_o >> 1) & 1u);
-      ph_o ^= (have0 ? 1u : 0u) | (have1 ? 2u : 0u);
-      __syncwarp();
+      ok = ok && wait_for(&bar.o_done, (n - 1) & 1);
+      bar_sync(1 + slot, 128);
       tc_fence_after();
-      // a slot's warps take half of the rows, of both slots' O
-      const int R = p.rows * a.G;
+      // O^T: a dim per thread.  To the workspace as it is; as outputs by way of P's memory, whose rows then leave in
+      // 16 bytes a thread.
+      uint16_t* rows = reinterpret_cast<uint16_t*>(tile_p);            // [row][dim]
 #pragma unroll 1
-      for (int c = slot * (NC / 2); c < (slot + 1) * (NC / 2) && c < R; c += 8) {
-        float o[8], u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = 0.f;
-        if (have0) {
-          tmem_ld_cols8(T_O + lanes + c, u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = u[i] * s_f[c + i].x;
-        }
-        if (have1) {
-          tmem_ld_cols8(T_O + 64 + lanes + c, u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] += u[i] * s_f[c + i].y;
-        }
+      for (int c0 = 0; c0 < R; c0 += 16) {
+        float o[16];
+        tmem_ld16(t_o + c0, o);
         if (shared) {
+          float* dst = a.part_o + (at * MAXR + c0) * D + t;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < R) __stcg(a.part_o + (at * MAXR + c + i) * D + t, o[i]);
+          for (int i = 0; i < 16; ++i)
+            if (c0 + i < R) __stcg(dst + i * D, o[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (c + i < R) {
-              const int tok = s_tok[c + i], g = c + i - tok * a.G;
-              a.O[(size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + g) * D + t] = f2bf(o[i]);
-            }
-          }
+          for (int i = 0; i < 16; ++i) rows[(c0 + i) * D + t] = f2bf(o[i] * alpha[c0 + i]);
         }
       }
       tc_fence_before();
@@ -801,13 +731,22 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         if (p.t0 > 0) shared_first = true;
         else shared_last = &p;             // (its entry of the ring is not posted again)
         __syncwarp();
-        if (lane == 0) red_release(a.counters + 16 * c_first, (unsigned)tiles);
+        if (lane == 0) red_release(a.counters + 8 * c_first, (unsigned)tiles);
+      } else {
+        bar_sync(1 + slot, 128);
+        uint16_t* out = a.O + (size_t)p.row0 * a.ldo + (size_t)p.h * a.G * D + (t & 15) * 8;
+#pragma unroll 1
+        for (int r = t >> 4; r < R; r += 8) {
+          const int tok = s_tok[r], g = r - tok * a.G;
+          *reinterpret_cast<uint4*>(out + (size_t)tok * a.ldo + g * D) =
+              *reinterpret_cast<const uint4*>(rows + r * D + (t & 15) * 8);
+        }
       }
-      n += tiles;
-      close(k);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.taken[k % PR]);
     }
     if (!ok) set_status(a.status, 0x841u);
-    // At the CTA's end: the rows of a shared item are joined by the warps of all its CTAs that are still here when
+    // At the slot's end: the rows of a shared item are joined by the warps of all its slots that are still here when
     // the last piece arrives, a row at a time.  A warp waits for that a while only: the warp that brings the last
     // piece joins whatever is left, so no CTA needs another one to run beside it.
     ok = __all_sync(0xffffffffu, ok);
@@ -816,8 +755,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       if (!ok || !(i ? shared_first : shared_last != nullptr)) continue;
       const Piece& p = i ? *s_first : *shared_last;
       const int c_first = first_of(p), keys = p.ctx + p.rows, R = p.rows * a.G;
-      unsigned *arrived = a.counters + 16 * c_first, *tickets = arrived + 8;
-      // the CTAs that have a piece: those of 32 from `base` on, and the tiles up to the last of them
+      unsigned *arrived = a.counters + 8 * c_first, *tickets = arrived + 4;
+      // the slots that have a piece: those of 32 from `base` on, and the tiles up to the last of them
       struct Sharers {
         unsigned has;
         int t;
@@ -832,7 +771,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
       if (lane == 0) {
         const uint64_t t0 = globaltimer();
         do {
-          there = ld_acquire(arrived) == 8u * (unsigned)p.nt;
+          there = ld_acquire(arrived) == 4u * (unsigned)p.nt;
         } while (!there && globaltimer() - t0 < JOIN_WAIT_NS);
       }
       int count = __popc(all.has);
@@ -895,7 +834,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
         }
       }
       // done with it; the last warp of the sharers clears their two words for the next launch
-      if (lane == 0 && (int)(atomicAdd(tickets, 0x10000u) >> 16) + 1 == 8 * count) {
+      if (lane == 0 && (int)(atomicAdd(tickets, 0x10000u) >> 16) + 1 == 4 * count) {
         *tickets = 0u;
         *arrived = 0u;
       }
@@ -904,15 +843,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_attention_q4_kernel(const Chun
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(0, TMEM_COLS);
   }
 }
 
 template <int NC>
-cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tq, const ChunkAttnArgs& a, int grid, cudaStream_t s) {
   static bool configured[64] = {};
+  constexpr int SMEM = Layout<NC>::SMEM;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev]) {
@@ -925,21 +865,23 @@ cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t s) {
     if (fa.numRegs < REGS_ALL) return cudaErrorLaunchOutOfResources;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  cudaError_t e = launch_k(few_attention_q4_kernel<NC>, dim3(grid), dim3(THREADS), SMEM, s, a);
+  cudaError_t e = launch_k(few_attention_q4_kernel<NC>, dim3(grid), dim3(THREADS), SMEM, s, tq, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-int few_attention_q4_rows() { return MAXR; }
+int few_attention_q4_columns(int G, int max_rows) {
+  return (long long)G * max_rows <= MAXR ? (G * max_rows + 15) / 16 * 16 : 0;
+}
 float q4_tile_scale() { return Q4_TILE_SCALE; }
 
-cudaError_t launch_few_attention_q4(const ChunkAttnArgs& a, int grid, cudaStream_t s) {
-  switch ((a.G * a.max_rows + 15) / 16) {
-    case 1: return launch<16>(a, grid, s);
-    case 2: return launch<32>(a, grid, s);
-    case 3: return launch<48>(a, grid, s);
-    default: return launch<64>(a, grid, s);
+cudaError_t launch_few_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& a, int columns, int grid, cudaStream_t s) {
+  switch (columns) {
+    case 16: return launch<16>(tq, a, grid, s);
+    case 32: return launch<32>(tq, a, grid, s);
+    case 48: return launch<48>(tq, a, grid, s);
+    default: return launch<64>(tq, a, grid, s);
   }
 }
 
