@@ -41,7 +41,7 @@ constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   
 
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // What an item's start and end cost, in keys; what reading a piece back takes (see shares_of).
-constexpr int ITEM_KEYS = 320, PIECE_KEYS = 60;
+constexpr int ITEM_KEYS = 320, PIECE_KEYS = 10;
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ bool bar_or(int id, int n, bool x) {
@@ -67,6 +67,11 @@ __device__ __forceinline__ void fold16(float (&v)[16], int lane, F&& f) {
   }
   v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 // ----------------------------------------------------------------- the batch
 struct Seq {
   int r0, rows, ctx;
@@ -767,6 +772,9 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
         return Sharers{__ballot_sync(0xffffffffu, to > (lane == 0 ? before : prev)), __shfl_sync(0xffffffffu, to, 31)};
       };
       const Sharers all = sharers(c_first, 0);
+      int count = __popc(all.has);
+      Sharers s = all;
+      for (int base = c_first; s.t < p.nt; count += __popc(s.has)) s = sharers(base += 32, s.t);
       unsigned there = 0;
       if (lane == 0) {
         const uint64_t t0 = globaltimer();
@@ -774,69 +782,98 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
           there = ld_acquire(arrived) == 4u * (unsigned)p.nt;
         } while (!there && globaltimer() - t0 < JOIN_WAIT_NS);
       }
-      int count = __popc(all.has);
-      Sharers s = all;
-      for (int base = c_first; s.t < p.nt; count += __popc(s.has)) s = sharers(base += 32, s.t);
-      if (__shfl_sync(0xffffffffu, there, 0)) {
-        __syncwarp();
+      there = __shfl_sync(0xffffffffu, there, 0);
+      // `units` of rows to be taken, a ticket each.  A warp's last ticket is one that finds nothing left; those that gave up
+      // count in the upper half.  Whoever sees all warps of the sharers in one of the two clears the words for the next launch.
+      auto last_of = [&](unsigned before, int units) {
+        const int fails = max((int)(before & 0xffffu) - units, 0), gave_up = (int)(before >> 16);
+        if (fails + gave_up + 1 == 4 * count) {
+          *tickets = 0u;
+          *arrived = 0u;
+        }
+      };
+      // ROWS rows at a time, PIECES pieces of each: eight loads under way.  The next ticket is asked for beside them.
+      auto join = [&](auto rows_, auto pieces_) {
+        constexpr int ROWS = decltype(rows_)::value, PIECES = decltype(pieces_)::value;
+        const int units = (R + ROWS - 1) / ROWS;
+        unsigned v = 0;
+        if (lane == 0) v = atomicAdd(tickets, 1u);
         for (;;) {
-          unsigned r = 0;
-          if (lane == 0) r = atomicAdd(tickets, 1u) & 0xffffu;
-          r = __shfl_sync(0xffffffffu, r, 0);
-          if (r >= (unsigned)R) break;
-          float top = -INFINITY, sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int unit = (int)(__shfl_sync(0xffffffffu, v, 0) & 0xffffu);
+          if (unit >= units) break;
+          if (lane == 0) v = atomicAdd(tickets, 1u);
+          const int r0 = unit * ROWS;
+          float top[ROWS], sum[ROWS];
+          float4 acc[ROWS];
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i) {
+            top[i] = -INFINITY;
+            sum[i] = 0.f;
+            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
           Sharers s = all;
           for (int base = c_first;; base += 32) {
             while (s.has) {
-              constexpr int BATCH = 8;
-              float4 u[BATCH];
-              float2 ml[BATCH];
+              float4 u[PIECES][ROWS];
+              float2 ml[PIECES][ROWS];
 #pragma unroll
-              for (int j = 0; j < BATCH; ++j) {
+              for (int j = 0; j < PIECES; ++j) {
                 const int c = s.has ? base + __ffs(s.has) - 1 : -1;
                 s.has &= s.has - 1;
-                ml[j] = make_float2(-INFINITY, 0.f);
-                u[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c >= 0) {
-                  const size_t at = ((size_t)c * 2 + (c == c_first ? 1 : 0)) * MAXR + r;
-                  ml[j] = __ldcg(a.part_ml + at);
-                  u[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) {
+                  ml[j][i] = make_float2(-INFINITY, 0.f);
+                  u[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (c >= 0 && r0 + i < R) {
+                    const size_t at = ((size_t)c * 2 + (c == c_first ? 1 : 0)) * MAXR + r0 + i;
+                    ml[j][i] = __ldcg(a.part_ml + at);
+                    u[j][i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
+                  }
                 }
               }
-              float high = top;
 #pragma unroll
-              for (int j = 0; j < BATCH; ++j) high = fmaxf(high, ml[j].x);
-              const float base_m = high == -INFINITY ? 0.f : high, keep = ex2(top - base_m);
-              sum *= keep;
-              acc.x *= keep;
-              acc.y *= keep;
-              acc.z *= keep;
-              acc.w *= keep;
-              top = high;
+              for (int i = 0; i < ROWS; ++i) {
+                float high = top[i];
 #pragma unroll
-              for (int j = 0; j < BATCH; ++j) {
-                const float w = ex2(ml[j].x - base_m);
-                sum += ml[j].y * w;
-                acc.x += u[j].x * w;
-                acc.y += u[j].y * w;
-                acc.z += u[j].z * w;
-                acc.w += u[j].w * w;
+                for (int j = 0; j < PIECES; ++j) high = fmaxf(high, ml[j][i].x);
+                const float base_m = high == -INFINITY ? 0.f : high, keep = ex2(top[i] - base_m);
+                sum[i] *= keep;
+                acc[i].x *= keep;
+                acc[i].y *= keep;
+                acc[i].z *= keep;
+                acc[i].w *= keep;
+                top[i] = high;
+#pragma unroll
+                for (int j = 0; j < PIECES; ++j) {
+                  const float w = ex2(ml[j][i].x - base_m);
+                  sum[i] += ml[j][i].y * w;
+                  acc[i].x += u[j][i].x * w;
+                  acc[i].y += u[j][i].y * w;
+                  acc[i].z += u[j][i].z * w;
+                  acc[i].w += u[j][i].w * w;
+                }
               }
             }
             if (s.t >= p.nt) break;
             s = sharers(base + 32, s.t);
           }
-          const float inv = Q4_TILE_SCALE / sum;
-          const int tok = s_tok[r], g = (int)r - tok * a.G;
-          *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + g) * D + lane * 4) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i) {
+            if (r0 + i >= R) break;
+            const float inv = Q4_TILE_SCALE / sum[i];
+            const int tok = s_tok[r0 + i], g = r0 + i - tok * a.G;
+            *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + g) * D + lane * 4) =
+                make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+          }
         }
-      }
-      // done with it; the last warp of the sharers clears their two words for the next launch
-      if (lane == 0 && (int)(atomicAdd(tickets, 0x10000u) >> 16) + 1 == 4 * count) {
-        *tickets = 0u;
-        *arrived = 0u;
+        if (lane == 0) last_of(v, units);
+      };
+      if (there) {
+        __syncwarp();
+        if (count == 2) join(Int<4>{}, Int<2>{});
+        else join(Int<1>{}, Int<8>{});
+      } else if (lane == 0) {
+        last_of(atomicAdd(tickets, 0x10000u), count == 2 ? (R + 3) / 4 : R);
       }
       __syncwarp();
     }
