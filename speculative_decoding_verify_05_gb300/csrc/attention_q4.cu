@@ -35,8 +35,7 @@ constexpr int KT = 128;                   // keys per tile (one page)
 constexpr int MAXR = 64;                  // rows of an item
 constexpr int PR = 4;                     // posted pieces of a slot
 constexpr int THREADS = 896;
-constexpr int REGS_ALL = 72, REGS_SOFTMAX = 112, REGS_OTHER = 56;
-static_assert(256 * REGS_SOFTMAX + 640 * REGS_OTHER <= THREADS * REGS_ALL, "register split");
+constexpr int REGS_ALL = 72;
 constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   // 64 columns for each slot
 
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
@@ -118,6 +117,9 @@ struct Piece {
 // NC: columns of the MMAs (rows of the queries, a multiple of 16).
 template <int NC>
 struct Layout {
+  // Registers: of few columns the softmax leaves some to the warps that bring pages to bf16, which wait less with them.
+  static constexpr int REGS_SOFTMAX = NC <= 16 ? 96 : 112, REGS_ROLES = 56, REGS_BF16 = NC <= 16 ? 64 : 56;
+  static_assert(256 * REGS_SOFTMAX + 128 * REGS_ROLES + 512 * REGS_BF16 <= THREADS * REGS_ALL, "register split");
   static constexpr int SP = NC <= 48 ? 4 : 3;                     // pages in flight of a slot, of keys and of values
   static constexpr int Q_HALF = NC * 128;                         // rows x 64 dims (128-byte swizzled rows)
   static constexpr int OFF_P = 0;                                 // of each slot: [key][row], 128-byte swizzled rows
@@ -133,7 +135,7 @@ struct Layout {
   static constexpr int OFF_PIECE = OFF_TOK + MAXR * 4;            // [2][PR + 1]: posted, and the slot's first for the end
   static constexpr int OFF_SHARES = OFF_PIECE + 2 * (PR + 1) * (int)sizeof(Piece);
   static constexpr int OFF_BAR = OFF_SHARES + 2 * (int)sizeof(Shares);
-  static constexpr int N_BARS = 2 * (4 * SP + 5 + 4 + 2 * PR);
+  static constexpr int N_BARS = 2 * (4 * SP + 6 + 4 + 2 * PR);
   static constexpr int OFF_MORE = OFF_BAR + N_BARS * 8;           // marks of the page rings' stages, then the TMEM address
   static constexpr int SMEM = OFF_MORE + 2 * 2 * SP * 4 + 8;
   static_assert(OFF_KP % 128 == 0 && OFF_EXP % 16 == 0 && OFF_PIECE % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
@@ -151,7 +153,8 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
     uint64_t v_land[SP], v_free[SP];
     uint64_t ka_full, va_full;           // K, V tile in TMEM
     uint64_t s_full;                     // scores in TMEM (K read)
-    uint64_t p_full;                     // P in shared memory, S read, O rescaled
+    uint64_t s_free;                     // ... read
+    uint64_t p_full;                     // P in shared memory, O rescaled
     uint64_t o_done;                     // P V done (V and P read, O whole)
     uint64_t q_full[2], q_free[2];
     uint64_t posted[PR], taken[PR];
@@ -179,6 +182,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
       mbar_init(&b.ka_full, 4);
       mbar_init(&b.va_full, 4);
       mbar_init(&b.s_full, 1);
+      mbar_init(&b.s_free, 4);
       mbar_init(&b.p_full, 4);
       mbar_init(&b.o_done, 1);
       for (int i = 0; i < 2; ++i) {
@@ -214,7 +218,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
 
   if (warp >= 12) {
     // -------------------------------------------------------------- pages to bf16: keys (12-19), values (20-27)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::REGS_BF16));
     const bool is_v = warp >= 20;
     const int row = tid & 127;
     const uint32_t t_dst = (is_v ? T_V : T_K) + slot * 64 + (uint32_t((warp & 3) * 32) << 16);
@@ -278,7 +282,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
     }
     if (!ok) set_status(a.status, 0x851u);
   } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::REGS_ROLES));
     if (warp >= 10) {
       // ------------------------------------------------------------ pieces, queries, pages
       const int run = (a.B + 31) >> 5, b0 = min(lane * run, a.B), b1 = min(b0 + run, a.B);
@@ -448,8 +452,8 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
       __syncwarp();
     } else {
       // ------------------------------------------------------------ MMA issue
-      // A tile's scores are issued as soon as the softmax has read those before them, ahead of the P V of the tile
-      // before, which the softmax waits for only when it stores its weights.  The whole warp walks the tiles and one elected
+      // A tile's scores are issued as soon as the softmax has those before them in its registers, while it works on them and
+      // ahead of their P V.  The whole warp walks the tiles and one elected
       // lane issues; after a wait that ran out it goes on without waiting (to garbage that nobody reads).
       const bool leader = elect_one();
       constexpr uint32_t idesc_s = umma_idesc_bf16(KT, NC), idesc_pv = umma_idesc_bf16(D, NC) | (1u << 16);   // (P: MN-major)
@@ -499,12 +503,13 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
         step(cs);
       }
       for (int n = 0; cp.more; ++n) {
-        wait(&bar.p_full, (uint32_t)(n & 1));
+        wait(&bar.s_free, (uint32_t)(n & 1));
         if (cs.more) {
           scores(n + 1, cs);
           step(cs);
         }
         wait(&bar.va_full, (uint32_t)(n & 1));
+        wait(&bar.p_full, (uint32_t)(n & 1));
         tc_fence_after();
         if (leader) {
           const uint64_t pd = desc_mn(smem_u32(smem + L::OFF_P + slot * KT * 128), 0);
@@ -522,7 +527,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::REGS_SOFTMAX));
     // ------------------------------------------------------------ softmax and epilogue
     // (After a wait that ran out a warp stops waiting, but keeps the control flow up to the next piece, so that the
     // named barriers stay matched.)
@@ -589,6 +594,27 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
           }
           tmem_st_wait();
         }
+        // Of few columns a thread takes its scores to registers, so that the next tile's can take their place while it works
+        // on these (16 x 1 row at 30000 keys 109 -> 105.6 us); 32 and more do not fit beside their sums.
+        constexpr bool EARLY = NC <= 16;
+        float all[EARLY ? NC : 1];
+        auto s_read = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.s_free);
+        };
+        if constexpr (EARLY) {
+          tmem_ld_cols<NC>(t_s, all);
+          s_read();
+        }
+        auto get = [&](int c0, float (&x)[16]) {
+          if constexpr (EARLY) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = all[c0 + c];
+          } else {
+            tmem_ld16(t_s + c0, x);
+          }
+        };
         // ... as weights: 2 columns from c0 + c
         auto weight = [&](const float (&x)[16], int c0, int c) {
           const float2 r = *reinterpret_cast<const float2*>(add + c0 + c);
@@ -604,10 +630,10 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
         // of its later ones.)
         for (bool look = j == 0;; look = true) {
           if (look) {
-#pragma unroll 1
+#pragma unroll
             for (int c0 = 0; c0 < NC; c0 += 16) {
               float x[16];
-              tmem_ld16(t_s + c0, x);
+              get(c0, x);
               fold16(x, lane, [](float a, float b) { return fmaxf(a, b); });
               if (lane < 16) s_max[wq * MAXR + c0 + lane] = x[0];
             }
@@ -652,7 +678,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 16) {
             float x[16];
-            tmem_ld16(t_s + c0, x);
+            get(c0, x);
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -673,7 +699,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 16) {
             float x[16];
-            tmem_ld16(t_s + c0, x);
+            get(c0, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float2 e = weight(x, c0, 2 * i);
@@ -683,6 +709,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
             }
           }
         }
+        if constexpr (!EARLY) s_read();
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
