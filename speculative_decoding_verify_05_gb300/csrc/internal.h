@@ -232,7 +232,7 @@ struct KvAppendQ4Args {
   uint8_t* Kpool; uint8_t* Vpool;       // [Hkv][num_pages][8704]
   const int32_t* block_table;
   int num_pages, max_pages, Hq, Hkv;    // Hq = 0 without queries
-  int blocks;                           // (set by the launcher)
+  int blocks, value_ctas, check_ctas;   // (set by the launcher)
   unsigned* status;
 };
 cudaError_t launch_kv_append_q4(const KvAppendQ4Args& a, int sms, cudaStream_t s);

@@ -1,6 +1,6 @@
 // The paged cache in 4 bits (q4.cuh): norms of queries and keys with their rotation, the append that quantises a
 // chunk's keys and values, and the read of cached keys and values.
-#include "common.cuh"
+#include "attention_util.cuh"
 #include "internal.h"
 #include "paged_rows.cuh"
 #include "q4.cuh"
@@ -12,68 +12,79 @@ constexpr int D = 128;
 constexpr unsigned ALL = 0xffffffffu;
 
 // ----------------------------------------------------------------- norm and rotation of a head
-// Eight lanes hold a head: dims i0 .. i0 + 7 and 64 + i0 .. (i0 = 8 (lane % 8)), which the rotation turns into one another.
+// Eight lanes hold a head: dims i0 .. i0 + 7 and 64 + i0 .. (i0 = 8 (lane % 8)), which the rotation turns into one another,
+// as pairs, on which the packed fp32 instructions work (each half rounded as by itself, so every operation is rounded
+// once; 8192 rows of 32 + 8 heads 37.1 us without).
 struct Head {
-  float a[8], b[8];
+  float2 v[8];
 };
-__device__ __forceinline__ void unpack8(const uint4& x, float* v) {
-  v[0] = bf16lo(x.x); v[1] = bf16hi(x.x); v[2] = bf16lo(x.y); v[3] = bf16hi(x.y);
-  v[4] = bf16lo(x.z); v[5] = bf16hi(x.z); v[6] = bf16lo(x.w); v[7] = bf16hi(x.w);
-}
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ float squares8(const float* v) {
-  float p[8];
+__device__ __forceinline__ Head head_of(const uint4& x, const uint4& y) {
+  Head h;
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) p[e] = __fmul_rn(v[e], v[e]);
-  return __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3])),
-                   __fadd_rn(__fadd_rn(p[4], p[5]), __fadd_rn(p[6], p[7])));
-}
-// y = x / sqrt(mean(x^2) + eps) * w.  The squares are summed neighbours first (1, 2, 4, .. 64 apart), and every
-// operation is rounded once, so that a row's bytes in the cache do not depend on the chunk it came in or on which kernel
-// normed it.  By all lanes of a warp.
-__device__ __forceinline__ void norm_head(Head& h, const uint16_t* w, int i0, float eps) {
-  float s0 = squares8(h.a), s1 = squares8(h.b);
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    s0 = __fadd_rn(s0, __shfl_xor_sync(ALL, s0, o));
-    s1 = __fadd_rn(s1, __shfl_xor_sync(ALL, s1, o));
+  for (int e = 0; e < 4; ++e) {
+    h.v[2 * e] = make_float2(bf16lo(a[e]), bf16lo(b[e]));
+    h.v[2 * e + 1] = make_float2(bf16hi(a[e]), bf16hi(b[e]));
   }
-  const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(__fadd_rn(s0, s1), 1.f / D), eps)));
-  float wa[8], wb[8];
-  unpack8(__ldg(reinterpret_cast<const uint4*>(w + i0)), wa);
-  unpack8(__ldg(reinterpret_cast<const uint4*>(w + 64 + i0)), wb);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    h.a[e] = __fmul_rn(__fmul_rn(h.a[e], r), wa[e]);
-    h.b[e] = __fmul_rn(__fmul_rn(h.b[e], r), wb[e]);
-  }
+  return h;
 }
-// (a, b) -> (a c - b s, b c + a s); t: (cos, sin) of dims i0 ..
-__device__ __forceinline__ void turn_head(Head& h, const float4* t) {
+__device__ __forceinline__ void store_head(uint16_t* dst, const Head& h) {
+  uint32_t a[4], b[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float c = (e & 1) ? t[e >> 1].z : t[e >> 1].x, s = (e & 1) ? t[e >> 1].w : t[e >> 1].y;
-    const float a = h.a[e], b = h.b[e];
-    h.a[e] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-    h.b[e] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  for (int e = 0; e < 4; ++e) {
+    a[e] = cvt_bf16x2(h.v[2 * e].x, h.v[2 * e + 1].x);
+    b[e] = cvt_bf16x2(h.v[2 * e].y, h.v[2 * e + 1].y);
   }
+  st_past_l1(dst, make_uint4(a[0], a[1], a[2], a[3]));
+  st_past_l1(dst + 64, make_uint4(b[0], b[1], b[2], b[3]));
 }
-__device__ __forceinline__ void turns_of(const float2* cs, int r, int i0, float4* t) {
+// y = x / sqrt(mean(x^2) + eps) * w.  The squares are summed neighbours first (1, 2, 4, .. 64 apart), so that a row's bytes
+// in the cache do not depend on the chunk it came in or on which kernel normed it.  By all lanes of a warp; w: the
+// weights, as head_of has them.
+__device__ __forceinline__ void norm_head(Head& h, const Head& w, float eps) {
+  float2 p[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) t[k] = __ldg(reinterpret_cast<const float4*>(cs + (size_t)r * 64 + i0) + k);
+  for (int e = 0; e < 8; ++e) p[e] = q4_mul2(h.v[e], h.v[e]);
+  float2 s = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1)
+    s = add2(s, make_float2(__shfl_xor_sync(ALL, s.x, o), __shfl_xor_sync(ALL, s.y, o)));
+  const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(__fadd_rn(s.x, s.y), 1.f / D), eps)));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h.v[e] = q4_mul2(q4_mul2(h.v[e], make_float2(r, r)), w.v[e]);
+}
+// (a, b) -> (a c - b s, b c + a s)
+struct Turns {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void turn_head(Head& h, const Turns& t) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    h.v[e] = add2(q4_mul2(h.v[e], make_float2(t.c[e], t.c[e])),
+                  q4_mul2(make_float2(h.v[e].y, h.v[e].x), make_float2(-t.s[e], t.s[e])));
+}
+__device__ __forceinline__ Turns turns_of(const float2* cs, int r, int i0) {
+  Turns t;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(cs + (size_t)r * 64 + i0) + k);
+    t.c[2 * k] = u.x;
+    t.s[2 * k] = u.y;
+    t.c[2 * k + 1] = u.z;
+    t.s[2 * k + 1] = u.w;
+  }
+  return t;
 }
 
-// One CTA per row; eight lanes per head, heads 4 WARPS apart.
-template <int WARPS, int UNITS>
-__global__ void __launch_bounds__(32 * WARPS) qk_norm_rope_kernel(const NormRopeArgs a) {
+// The heads `heads` of one row (row r's at src), four to a warp, UNITS rounds of the CTA's warps under way at once: normed (w
+// not null), rotated (turn), and handed to put(head number, head) by whole warps (heads >= `heads` are void).
+template <int WARPS, int UNITS, class Before, class Put>
+__device__ __forceinline__ void each_head(const uint16_t* src, int heads, const uint16_t* w, float eps, bool turn,
+                                          const Turns& t, Before&& before, Put&& put) {
   constexpr int STEP = 4 * WARPS;
-  pdl_wait();
-  pdl_trigger();
-  const int r = blockIdx.x, lane = threadIdx.x & 31, i0 = (lane & 7) * 8, heads = a.Hq + a.Hkv;
-  float4 t[4];
-  if (a.cs) turns_of(a.cs, r, i0, t);
+  const int lane = threadIdx.x & 31, i0 = (lane & 7) * 8;
+  Head wh;
+  if (w) wh = head_of(__ldg(reinterpret_cast<const uint4*>(w + i0)), __ldg(reinterpret_cast<const uint4*>(w + 64 + i0)));
   for (int h0 = (threadIdx.x >> 5) * 4; h0 < heads; h0 += STEP * UNITS) {
     uint4 x[UNITS], y[UNITS];
 #pragma unroll
@@ -81,27 +92,36 @@ __global__ void __launch_bounds__(32 * WARPS) qk_norm_rope_kernel(const NormRope
       const int hd = h0 + STEP * k + (lane >> 3);
       x[k] = y[k] = make_uint4(0, 0, 0, 0);
       if (hd >= heads) continue;
-      const uint16_t* src = hd < a.Hq ? a.Q + (size_t)r * a.ldq + (size_t)hd * D
-                                      : a.K + (size_t)r * a.ldk + (size_t)(hd - a.Hq) * D;
-      x[k] = ld_past_l1(src + i0);
-      y[k] = ld_past_l1(src + 64 + i0);
+      x[k] = ld_past_l1(src + (size_t)hd * D + i0);
+      y[k] = ld_past_l1(src + (size_t)hd * D + 64 + i0);
     }
+    if (!before()) return;
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
-      const int hd = h0 + STEP * k + (lane >> 3);
       if (h0 + STEP * k >= heads) continue;              // (the whole warp)
-      Head h;
-      unpack8(x[k], h.a);
-      unpack8(y[k], h.b);
-      norm_head(h, hd < a.Hq || a.Hkv == 0 ? a.wq : a.wk, i0, a.eps);    // (lanes past the last head: any weights)
-      if (a.cs) turn_head(h, t);
-      if (hd >= heads) continue;
-      uint16_t* dst = hd < a.Hq ? a.Qout + (size_t)r * a.ldqo + (size_t)hd * D
-                                : a.Kout + (size_t)r * a.ldko + (size_t)(hd - a.Hq) * D;
-      st_past_l1(dst + i0, pack8(h.a));
-      st_past_l1(dst + 64 + i0, pack8(h.b));
+      Head h = head_of(x[k], y[k]);
+      if (w) norm_head(h, wh, eps);
+      if (turn) turn_head(h, t);
+      put(h0 + STEP * k + (lane >> 3), h);
     }
   }
+}
+
+// One CTA per row.
+template <int WARPS, int UNITS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 2 ? 14 : 5) qk_norm_rope_kernel(const NormRopeArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x, i0 = (threadIdx.x & 7) * 8;
+  Turns t;
+  if (a.cs) t = turns_of(a.cs, r, i0);
+  auto nothing = []() { return true; };
+  each_head<WARPS, UNITS>(a.Q + (size_t)r * a.ldq, a.Hq, a.wq, a.eps, a.cs != nullptr, t, nothing, [&](int hd, const Head& h) {
+    if (hd < a.Hq) store_head(a.Qout + (size_t)r * a.ldqo + (size_t)hd * D + i0, h);
+  });
+  each_head<WARPS, 1>(a.K + (size_t)r * a.ldk, a.Hkv, a.wk, a.eps, a.cs != nullptr, t, nothing, [&](int hd, const Head& h) {
+    if (hd < a.Hkv) store_head(a.Kout + (size_t)r * a.ldko + (size_t)hd * D + i0, h);
+  });
 }
 
 // ----------------------------------------------------------------- blocks of keys
@@ -141,75 +161,121 @@ __device__ __forceinline__ void check_sequence(const Args& a, long long b, unsig
 }
 
 // ----------------------------------------------------------------- append
-// Values of a block of 8 keys of one kv head, by a warp: a lane has dims 4 lane .. 4 lane + 3 of all 8 keys, which are 4
-// words of the page.  Entries of other keys in a word stay as they are (a page that receives rows belongs to
-// one sequence, and a sequence's words each to one warp).
+// Values of a block of 2^LB keys (8 or 32) of one kv head, by a warp: a lane has dims 4 lane .. 4 lane + 3 of all of them, which
+// are one word or all four words of four rows of the page.  Entries of other keys in a word stay as they are (a
+// page that receives rows belongs to one sequence, and a sequence's words each to one warp).
+template <int LB>
 __device__ __forceinline__ void append_values(const KvAppendQ4Args& a, int v, int g, int lane) {
-  const Block k = block_of<3>(v, a, lane, 0x8F2u);
+  constexpr int WORDS = 1 << (LB - 3);
+  const Block k = block_of<LB>(v, a, lane, 0x8F2u);
   if (k.b < 0) return;
   uint8_t* page = a.Vpool + ((size_t)g * a.num_pages + k.page) * Q4_BYTES;
   const int slot = k.key0 % Q4_PAGE;
   uint32_t* words = reinterpret_cast<uint32_t*>(page + (slot >> 5) * Q4_PLANE + lane * 64) + ((slot >> 3) & 3);
+  const uint16_t* src = a.Vnew + (size_t)g * D + lane * 4;
+  uint32_t w[WORDS][4];
+  auto load = [&](int i, uint2 (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = make_uint2(0, 0);
+      const int key = 8 * i + j;
+      if (key >= k.lo && key < k.hi) x[j] = __ldg(reinterpret_cast<const uint2*>(src + (size_t)(k.row0 + key) * a.ldkv));
+    }
+  };
   uint2 x[8];
+  load(0, x);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[j] = make_uint2(0, 0);
-    if (j >= k.lo && j < k.hi)
-      x[j] = __ldg(reinterpret_cast<const uint2*>(a.Vnew + (size_t)(k.row0 + j) * a.ldkv + (size_t)g * D + lane * 4));
+  for (int i = 0; i < WORDS; ++i) {
+    uint2 next[8];
+    if (i + 1 < WORDS) load(i + 1, next);
+    const int lo = k.lo - 8 * i, hi = k.hi - 8 * i;
+    uint32_t keep = 0;                     // entries of other keys
+    if (lo > 0 || hi < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < lo || j >= hi) keep |= 15u << q4_shift(j);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[i][e] = (keep ? words[4 * e + i] & keep : 0u) | (0x88888888u & ~keep);
+    unsigned mine = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < lo || j >= hi) continue;
+      const float2 f0 = make_float2(bf16lo(x[j].x), bf16hi(x[j].x)), f1 = make_float2(bf16lo(x[j].y), bf16hi(x[j].y));
+      // (as bits: NaN lies above everything)
+      unsigned bits = max(max(__float_as_uint(f0.x) & 0x7fffffffu, __float_as_uint(f0.y) & 0x7fffffffu),
+                          max(__float_as_uint(f1.x) & 0x7fffffffu, __float_as_uint(f1.y) & 0x7fffffffu));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) bits = max(bits, __shfl_xor_sync(ALL, bits, o));
+      unsigned code;
+      if (__any_sync(ALL, bits >= __float_as_uint(Q4_LARGE))) {
+        const uint2 r = q4_any(make_float4(f0.x, f0.y, f1.x, f1.y), make_float4(0.f, 0.f, 0.f, 0.f), 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[i][e] += (((r.x >> (4 * e)) & 15u) - 8u) << q4_shift(j);
+        code = r.y;
+      } else {
+        const Q4Scale s = q4_scale(__uint_as_float(bits));
+        const float2 sc = make_float2(s.scale, s.scale), rc = make_float2(s.reciprocal, s.reciprocal);
+        const int2 n0 = q4_whole2(f0, sc, rc), n1 = q4_whole2(f1, sc, rc);
+        w[i][0] += (unsigned)n0.x << q4_shift(j);
+        w[i][1] += (unsigned)n0.y << q4_shift(j);
+        w[i][2] += (unsigned)n1.x << q4_shift(j);
+        w[i][3] += (unsigned)n1.y << q4_shift(j);
+        code = s.code;
+      }
+      if ((lane & 7) == j) mine = code;
+    }
+    const int j = lane & 7;
+    if (j >= lo && j < hi) page[Q4_SCALES + (lane >> 3) * 128 + slot + 8 * i + j] = (uint8_t)mine;
+    if (i + 1 < WORDS)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = next[j];
   }
-  uint32_t w[4] = {0, 0, 0, 0}, mask = 0;
-  const bool part = k.hi - k.lo < 8;
-  if (part) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < k.lo || j >= k.hi) mask |= 15u << q4_shift(j);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = words[4 * e] & mask;
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(words + 4 * e) = make_uint4(w[0][e], w[1][e], w[2][e], w[3][e]);
+    else words[4 * e] = w[0][e];
   }
-  unsigned mine = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (j < k.lo || j >= k.hi) continue;
-    const float f[4] = {bf16lo(x[j].x), bf16hi(x[j].x), bf16lo(x[j].y), bf16hi(x[j].y)};
-    float top = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, o));
-    unsigned code;
-    const float s = q4_scale(top, code);
-    if ((lane & 7) == j) mine = code;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] |= q4_entry(f[e], s) << q4_shift(j);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) words[4 * e] = w[e];
-  const int j = lane & 7;
-  if (j >= k.lo && j < k.hi) page[Q4_SCALES + (lane >> 3) * 128 + slot + j] = (uint8_t)mine;
 }
 
 // Keys, of eight lanes with a head: a lane's two runs of 8 dims are a word each, four lanes have a scale together.
 __device__ __forceinline__ void append_key(const KvAppendQ4Args& a, const Head& h, int g, int page, int slot, int lane,
                                            bool used) {
-  float ta = 0.f, tb = 0.f;
+  unsigned ta = 0, tb = 0;               // (as bits: NaN lies above everything)
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    ta = fmaxf(ta, fabsf(h.a[e]));
-    tb = fmaxf(tb, fabsf(h.b[e]));
+    ta = max(ta, __float_as_uint(h.v[e].x) & 0x7fffffffu);
+    tb = max(tb, __float_as_uint(h.v[e].y) & 0x7fffffffu);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    ta = fmaxf(ta, __shfl_xor_sync(ALL, ta, o));
-    tb = fmaxf(tb, __shfl_xor_sync(ALL, tb, o));
+    ta = max(ta, __shfl_xor_sync(ALL, ta, o));
+    tb = max(tb, __shfl_xor_sync(ALL, tb, o));
   }
-  unsigned ca, cb;
-  const float sa = q4_scale(ta, ca), sb = q4_scale(tb, cb);
-  uint32_t wa = 0, wb = 0;
+  uint32_t wa = 0x88888888u, wb = 0x88888888u, mine;
+  if (__any_sync(ALL, max(ta, tb) >= __float_as_uint(Q4_LARGE))) {
+    const float2* v = h.v;
+    const uint2 ra = q4_any(make_float4(v[0].x, v[1].x, v[2].x, v[3].x), make_float4(v[4].x, v[5].x, v[6].x, v[7].x), 4);
+    const uint2 rb = q4_any(make_float4(v[0].y, v[1].y, v[2].y, v[3].y), make_float4(v[4].y, v[5].y, v[6].y, v[7].y), 4);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wa |= q4_entry(h.a[e], sa) << q4_shift(e);
-    wb |= q4_entry(h.b[e], sb) << q4_shift(e);
+    for (int e = 0; e < 8; ++e) {
+      wa += (((ra.x >> (4 * e)) & 15u) - 8u) << q4_shift(e);
+      wb += (((rb.x >> (4 * e)) & 15u) - 8u) << q4_shift(e);
+    }
+    mine = ra.y | (rb.y << 16);
+  } else {
+    const Q4Scale sa = q4_scale(__uint_as_float(ta)), sb = q4_scale(__uint_as_float(tb));
+    const float2 sc = make_float2(sa.scale, sb.scale), rc = make_float2(sa.reciprocal, sb.reciprocal);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int2 n = q4_whole2(h.v[e], sc, rc);
+      wa += (unsigned)n.x << q4_shift(e);
+      wb += (unsigned)n.y << q4_shift(e);
+    }
+    mine = sa.code | (sb.code << 16);
   }
   // scales of dims 0, 32, 64, 96 ..: lanes 0 and 4 of the eight
-  const unsigned mine = ca | (cb << 16), codes = mine | (__shfl_xor_sync(ALL, mine, 4) << 8);
+  const unsigned codes = mine | (__shfl_xor_sync(ALL, mine, 4) << 8);
   if (!used) return;
   uint8_t* p = a.Kpool + ((size_t)g * a.num_pages + page) * Q4_BYTES;
   const int l = lane & 7;
@@ -219,71 +285,51 @@ __device__ __forceinline__ void append_key(const KvAppendQ4Args& a, const Head& 
   if (l == 0) reinterpret_cast<uint32_t*>(p + Q4_SCALES)[slot] = codes;
 }
 
-// CTAs: one per row for its queries and keys, then four blocks of values each, then a thread per sequence that checks its
-// bounds (no row has to be in a sequence that breaks them).
-template <int WARPS, int UNITS>
-__global__ void __launch_bounds__(32 * WARPS) kv_append_q4_kernel(const KvAppendQ4Args a) {
-  constexpr int STEP = 4 * WARPS;
+// CTAs: a thread per sequence that checks its bounds (no row has to be in a sequence that breaks them) and blocks of values, a
+// warp each, then one CTA per row for its keys and queries.  Blocks of 32 keys write whole lines of a page, those of 8
+// leave more warps to a few rows.
+template <int WARPS, int UNITS, int LB>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 2 ? 14 : 5) kv_append_q4_kernel(const KvAppendQ4Args a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = (lane & 7) * 8;
-  const int r = blockIdx.x;
-  if (r >= a.M) {
-    const unsigned u = (unsigned)(r - a.M) * WARPS + warp, units = (unsigned)a.blocks * a.Hkv;
-    const unsigned ctas = (units + WARPS - 1) / WARPS;
-    if ((unsigned)(r - a.M) < ctas) {
-      if (u < units) append_values(a, u / a.Hkv, u % a.Hkv, lane);
-    } else {
-      check_sequence(a, (long long)(r - a.M - ctas) * (32 * WARPS) + threadIdx.x, 0x8F1u);
-    }
+  if (blockIdx.x < (unsigned)a.check_ctas) {
+    check_sequence(a, (long long)blockIdx.x * (32 * WARPS) + threadIdx.x, 0x8F1u);
     return;
   }
-  const int heads = a.Hq + a.Hkv;
-  float4 t[4];
-  if (a.cs) turns_of(a.cs, r, i0, t);
-  int b = -2, page = 0, p = 0;
-  for (int h0 = warp * 4; h0 < heads || b == -2; h0 += STEP * UNITS) {
-    uint4 x[UNITS], y[UNITS];
-#pragma unroll
-    for (int k = 0; k < UNITS; ++k) {
-      const int hd = h0 + STEP * k + (lane >> 3);
-      x[k] = y[k] = make_uint4(0, 0, 0, 0);
-      if (hd >= heads) continue;
-      const uint16_t* src = hd < a.Hq ? a.Q + (size_t)r * a.ldq + (size_t)hd * D
-                                      : a.Knew + (size_t)r * a.ldkv + (size_t)(hd - a.Hq) * D;
-      x[k] = ld_past_l1(src + i0);
-      y[k] = ld_past_l1(src + 64 + i0);
-    }
-    if (b == -2) {                                      // the row's sequence, position and page
-      const Place at = place_of(r, a, lane);
-      b = at.b;
-      if (b < 0 || r >= at.c1) return;                  // padding
-      if (out_of_bounds(at.c0, at.c1, at.ctx, a)) return;
-      p = at.ctx + (r - at.c0);
-      page = a.block_table[(size_t)b * a.max_pages + p / Q4_PAGE];
-      if (page < 0 || page >= a.num_pages) {
-        if (threadIdx.x == 0) set_status(a.status, 0x8F2u);
-        page = -1;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < UNITS; ++k) {
-      const int hd = h0 + STEP * k + (lane >> 3);
-      if (h0 + STEP * k >= heads) continue;             // (the whole warp)
-      Head h;
-      unpack8(x[k], h.a);
-      unpack8(y[k], h.b);
-      if (a.wk) norm_head(h, hd < a.Hq ? a.wq : a.wk, i0, a.eps);      // (wq is there if Hq > 0)
-      if (a.cs) turn_head(h, t);
-      const bool is_q = hd < a.Hq;
-      if (is_q) {
-        uint16_t* dst = a.Qrot + (size_t)r * a.ldqr + (size_t)hd * D;
-        st_past_l1(dst + i0, pack8(h.a));
-        st_past_l1(dst + 64 + i0, pack8(h.b));
-      }
-      if (__any_sync(ALL, !is_q)) append_key(a, h, hd - a.Hq, page, p % Q4_PAGE, lane, !is_q && hd < heads && page >= 0);
-    }
+  if (blockIdx.x < (unsigned)(a.check_ctas + a.value_ctas)) {
+    const unsigned u = (blockIdx.x - a.check_ctas) * WARPS + warp;
+    if (u < (unsigned)a.blocks * a.Hkv) append_values<LB>(a, u / a.Hkv, u % a.Hkv, lane);
+    return;
   }
+  const int r = blockIdx.x - a.check_ctas - a.value_ctas;
+  Turns t;
+  if (a.cs) t = turns_of(a.cs, r, i0);
+  int b = -2, page = 0, p = 0;
+  // the row's sequence, position and page, looked up beside the first loads; false: padding
+  auto place = [&]() {
+    if (b != -2) return b >= 0;
+    const Place at = place_of(r, a, lane);
+    b = at.b;
+    if (b < 0 || r >= at.c1 || out_of_bounds(at.c0, at.c1, at.ctx, a)) {
+      b = -1;
+      return false;
+    }
+    p = at.ctx + (r - at.c0);
+    page = a.block_table[(size_t)b * a.max_pages + p / Q4_PAGE];
+    if (page < 0 || page >= a.num_pages) {
+      if (threadIdx.x == 0) set_status(a.status, 0x8F2u);
+      page = -1;
+    }
+    return true;
+  };
+  each_head<WARPS, 1>(a.Knew + (size_t)r * a.ldkv, a.Hkv, a.wk, a.eps, a.cs != nullptr, t, place, [&](int hd, const Head& h) {
+    append_key(a, h, hd, page, p % Q4_PAGE, lane, hd < a.Hkv && page >= 0);
+  });
+  if (a.Hq > 0 && place())
+    each_head<WARPS, UNITS>(a.Q + (size_t)r * a.ldq, a.Hq, a.wq, a.eps, a.cs != nullptr, t, place, [&](int hd, const Head& h) {
+      if (hd < a.Hq) store_head(a.Qrot + (size_t)r * a.ldqr + (size_t)hd * D + i0, h);
+    });
 }
 
 // ----------------------------------------------------------------- read
@@ -357,12 +403,14 @@ cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t s) 
 
 cudaError_t launch_kv_append_q4(const KvAppendQ4Args& args, int sms, cudaStream_t s) {
   KvAppendQ4Args a = args;
-  const bool many = a.M > 10 * sms;
-  const unsigned warps = many ? 2 : 4;
-  a.blocks = (a.M >> 3) + 2 * a.B;
-  const unsigned values = ((unsigned)a.blocks * a.Hkv + warps - 1) / warps, checks = ((unsigned)a.B + 32 * warps - 1) / (32 * warps);
-  auto* k = many ? kv_append_q4_kernel<2, 2> : kv_append_q4_kernel<4, 3>;
-  cudaError_t e = launch_k(k, dim3((unsigned)a.M + values + checks), dim3(32 * warps), 0, s, a);
+  const bool many = a.M > 10 * sms, wide = a.M >= 64 * a.B;
+  const int warps = many ? 2 : 4;
+  a.blocks = (a.M >> (wide ? 5 : 3)) + 2 * a.B;
+  a.value_ctas = (a.blocks * a.Hkv + warps - 1) / warps;
+  a.check_ctas = (a.B + 32 * warps - 1) / (32 * warps);
+  auto* k = many ? (wide ? kv_append_q4_kernel<2, 2, 5> : kv_append_q4_kernel<2, 2, 3>)
+                 : (wide ? kv_append_q4_kernel<4, 3, 5> : kv_append_q4_kernel<4, 3, 3>);
+  cudaError_t e = launch_k(k, dim3((unsigned)a.M + a.value_ctas + a.check_ctas), dim3(32 * warps), 0, s, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -16,7 +16,7 @@
 // one logical operation leave two neighbouring entries in the halves of a word.
 #pragma once
 
-#include "common.cuh"
+#include "attention_util.cuh"
 
 namespace spec {
 
@@ -28,19 +28,63 @@ constexpr int Q4_BYTES = Q4_SCALES + 512;
 // Position (in bits) of entry e of 8 in its word.
 __host__ __device__ constexpr int q4_shift(int e) { return 4 * ((e >> 1) + 4 * (e & 1)); }
 
-// Products and sums with exactly one rounding each (never contracted): what is stored in 4 bits hangs on the last bit of
-// what it is rounded from, so the definition fixes every operation and their order.
-__device__ __forceinline__ float q4_scale(float top, unsigned& code) {
-  // a seventh of the largest magnitude, to 3 bits behind the leading one, halves to even
-  const float t = fminf(fmaxf(__fdiv_rn(top, 7.f), 0x1p-20f), 3840.f);
-  unsigned i = __float_as_uint(t);
+// ----------------------------------------------------------------- to 4 bits
+// What is stored hangs on the last bit of what it is rounded from, so the definition fixes every operation: a seventh of
+// the group's largest magnitude, rounded to 3 bits behind the leading one, halves to even, is the scale; a value over
+// the scale, rounded, and again to a whole number, halves to even, is the entry; both quotients rounded correctly.
+struct Q4Scale {
+  float scale, reciprocal;
+  unsigned code;
+};
+// Of a finite maximum below Q4_LARGE.  Quotients by Markstein's theorem ("Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): with the correctly rounded reciprocal of the divisor, one step by the exact remainder
+// leaves the correctly rounded quotient.  The scale's reciprocal is one Newton step (y + y (1 - s y)) from the hardware's
+// approximation: 1 - s y is exact (s has 4 bits), and what is rounded is 1 / s off by the square of the approximation's
+// error, far less than 1 / s is from the middle of two numbers (s has 8 significands; 1/9 .. 1/15 repeat in at most 12 bits).
+// (The division operator's general sequence, per value, made the append of 8192 rows wait for instructions: 48 us.)
+constexpr float Q4_LARGE = 26880.f;      // 7 scales of the largest
+__device__ __forceinline__ Q4Scale q4_scale(float top) {
+  constexpr float seventh = 1.f / 7.f;
+  const float q = __fmul_rn(top, seventh), t = __fmaf_rn(__fmaf_rn(-q, 7.f, top), seventh, q);
+  unsigned i = __float_as_uint(fmaxf(t, 0x1p-20f));
   i = (i + 0x7FFFFu + ((i >> 20) & 1u)) & 0xFFF00000u;
-  code = (i >> 20) - 107u * 8u;
-  return __uint_as_float(i);
+  Q4Scale d;
+  d.code = (i >> 20) - 107u * 8u;
+  d.scale = __uint_as_float(i);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d.scale));
+  d.reciprocal = __fmaf_rn(__fmaf_rn(-d.scale, y, 1.f), y, y);
+  return d;
 }
-// n + 8 of a value (NaN gives 8, a stored 0).
-__device__ __forceinline__ unsigned q4_entry(float x, float scale) {
-  return (unsigned)(min(max(__float2int_rn(__fdiv_rn(x, scale)), -7), 7) + 8);
+__device__ __forceinline__ float2 q4_mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// Whole numbers of two values, each with a scale (which leaves |x| below 7.5 scales; NaN gives 0).
+__device__ __forceinline__ int2 q4_whole2(float2 x, float2 scale, float2 reciprocal) {
+  const float2 q = q4_mul2(x, reciprocal), r = fma2(make_float2(-q.x, -q.y), scale, x), y = fma2(r, reciprocal, q);
+  return make_int2(__float2int_rn(y.x), __float2int_rn(y.y));
+}
+// Any values, infinities and NaN among them: the entries of 8 values, 4 bits each in order, and the code of the scale that
+// they share with the lanes up to `span` apart (a power of two).  Out of line: seldom needed.
+static __device__ __noinline__ uint2 q4_any(float4 a, float4 b, int span) {
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));       // (NaN is passed over)
+  for (int o = 1; o < span; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  unsigned i = __float_as_uint(fminf(fmaxf(__fdiv_rn(top, 7.f), 0x1p-20f), 3840.f));
+  i = (i + 0x7FFFFu + ((i >> 20) & 1u)) & 0xFFF00000u;
+  uint2 r = make_uint2(0u, (i >> 20) - 107u * 8u);
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    const float x = e < 4 ? (e < 2 ? (e ? a.y : a.x) : (e & 1 ? a.w : a.z)) : (e < 6 ? (e & 1 ? b.y : b.x) : (e & 1 ? b.w : b.z));
+    r.x |= (unsigned)(min(max(__float2int_rn(__fdiv_rn(x, __uint_as_float(i))), -7), 7) + 8) << (4 * e);
+  }
+  return r;
 }
 
 // ----------------------------------------------------------------- back to bf16
