@@ -25,7 +25,7 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from . import ops, prompt
+from . import ops, prompt, q4
 from .bf16 import decode, round_to_bf16 as r16
 
 
@@ -53,6 +53,8 @@ class LayerWeights:
     w_down: np.ndarray           # [d, I]
     attn_norm: np.ndarray        # [d]
     mlp_norm: np.ndarray         # [d]
+    q_norm: np.ndarray | None = None     # [D] norm of each query and key head before the rotation
+    k_norm: np.ndarray | None = None
 
 
 @dataclass
@@ -62,11 +64,12 @@ class StackWeights:
     w_lm: np.ndarray | None = None   # [V, d]
 
 
-def layer_forward(x, lw: LayerWeights, dims: Dims, cu_rows, ctx_len, Kc, Vc, positions=None):
+def layer_forward(x, lw: LayerWeights, dims: Dims, cu_rows, ctx_len, Kc, Vc, positions=None, stored=None):
     """One decoder layer over the packed verify rows.
 
     x [M, d] (bf16 values, fp64); Kc/Vc [B, Hkv, cap, D] this layer's cache; positions [axes, M]
-    the rows' positions on dims.rope_sections' axes (default: ctx_b + j, one axis).
+    the rows' positions on dims.rope_sections' axes (default: ctx_b + j, one axis).  stored(k, v)
+    [M, Hkv, D]: what a cache makes of the rows' keys (unrounded) and values, which is what is attended.
     Returns (x', Kc', Vc').
     """
     M = x.shape[0]
@@ -78,11 +81,15 @@ def layer_forward(x, lw: LayerWeights, dims: Dims, cu_rows, ctx_len, Kc, Vc, pos
     q = qkv[:, :Hq * D].reshape(M, Hq, D)
     k = qkv[:, Hq * D:(Hq + Hkv) * D].reshape(M, Hkv, D)
     v = r16(qkv[:, (Hq + Hkv) * D:]).reshape(M, Hkv, D)
+    if lw.q_norm is not None:
+        q, k = q4.norm(q, decode(lw.q_norm), dims.eps), q4.norm(k, decode(lw.k_norm), dims.eps)
     if positions is None:
-        q, k = r16(ops.rope(q, pos, dims.theta)), r16(ops.rope(k, pos, dims.theta))
+        q, k = ops.rope(q, pos, dims.theta), ops.rope(k, pos, dims.theta)
     else:
         cs = prompt.rope_table_axes(positions, dims.rope_sections or (D // 2,), D, dims.theta, dims.rope_interleaved)
-        q, k = r16(prompt.rotate(q, cs)[0]), r16(prompt.rotate(k, cs)[0])
+        q, k = prompt.rotate(q, cs)[0], prompt.rotate(k, cs)[0]
+    q = r16(q)
+    k, v = (r16(k), v) if stored is None else stored(k, v)
     o, Kc, Vc = ops.verify_attention(q, k, v, cu_rows, Kc, Vc, ctx_len, 1.0 / np.sqrt(D))
     o = r16(o)
     x = r16(ops.linear(o.reshape(M, Hq * D), decode(lw.w_o), residual=x))
@@ -100,8 +107,9 @@ def head_logits(x, sw: StackWeights, dims: Dims):
 
 
 def verify_pass(x0, sw: StackWeights, dims: Dims, cu_rows, ctx_len, Kcaches, Vcaches,
-                n_layers: int | None = None, positions=None):
-    """Run the stack once over all packed verify rows (positions: see layer_forward).
+                n_layers: int | None = None, positions=None, stored=None):
+    """Run the stack once over all packed verify rows (positions: see layer_forward; stored: one function
+    per layer, see there).
 
     Returns (final hidden x [M, d], logits [M, V] or None if there is no LM
     head, updated caches).
@@ -111,7 +119,8 @@ def verify_pass(x0, sw: StackWeights, dims: Dims, cu_rows, ctx_len, Kcaches, Vca
     Vc = list(Vcaches)
     L = len(sw.layers) if n_layers is None else n_layers
     for li in range(L):
-        x, Kc[li], Vc[li] = layer_forward(x, sw.layers[li], dims, cu_rows, ctx_len, Kc[li], Vc[li], positions)
+        x, Kc[li], Vc[li] = layer_forward(x, sw.layers[li], dims, cu_rows, ctx_len, Kc[li], Vc[li], positions,
+                                             None if stored is None else stored[li])
     logits = head_logits(x, sw, dims) if sw.w_lm is not None else None
     return x, logits, Kc, Vc
 

@@ -18,6 +18,11 @@ in place, when it is built.
 Over a paged cache the engine also runs the prompts that a verify pass starts from, in chunks of any
 length (``prefill``): per layer the QKV projection, spec_kv_append_paged (which rotates q and k on
 the way to the pages), spec_chunk_attention_paged, and the rest as above.
+
+Layers with norms of queries and keys (``q_norm``, ``k_norm``: RMSNorm of each head before the rotation)
+run spec_qk_norm_rope behind the projection.  Over a paged cache in 4 bits (pools of uint8) prompts and verify
+passes alike run spec_kv_append_paged_q4 (norm, rotation and quantisation in one) and
+spec_chunk_attention_paged_q4.
 """
 from __future__ import annotations
 
@@ -62,6 +67,8 @@ class LayerW:
     attn_norm: torch.Tensor  # [d]
     mlp_norm: torch.Tensor   # [d]
     gu_layout: str = "split"  # "split": gate rows then up rows; "interleaved": blocks of 16
+    q_norm: torch.Tensor | None = None   # [D] norm weights of each query and key head, both or neither
+    k_norm: torch.Tensor | None = None
 
 
 @dataclass
@@ -92,8 +99,10 @@ def fold_norm_weights(sw: StackW) -> None:
     sw.norms_folded = True
 
 
-def random_stack(dims: Dims, seed: int, device, std: float = 0.02, with_head: bool = True) -> StackW:
-    """Random-init bf16 weights N(0, std^2) of the stack's shapes (norm weights = 1)."""
+def random_stack(dims: Dims, seed: int, device, std: float = 0.02, with_head: bool = True,
+                 qk_norm: bool = False) -> StackW:
+    """Random-init bf16 weights N(0, std^2) of the stack's shapes (norm weights = 1; qk_norm: norms of queries and
+    keys too)."""
     g = torch.Generator(device=device)
     g.manual_seed(seed)
 
@@ -107,6 +116,8 @@ def random_stack(dims: Dims, seed: int, device, std: float = 0.02, with_head: bo
     for _ in range(dims.layers):
         sw.layers.append(LayerW(w(dims.qkv, dims.d), w(dims.d, dims.Hq * dims.D), w(2 * dims.I, dims.d),
                                 w(dims.d, dims.I), ones, ones))
+        if qk_norm:
+            sw.layers[-1].q_norm = sw.layers[-1].k_norm = torch.ones(dims.D, dtype=torch.bfloat16, device=device)
     sw.final_norm = ones
     if with_head:
         sw.w_lm = w(dims.V, dims.d)
@@ -138,14 +149,24 @@ class VerifyEngine:
                  device=None, fused_swiglu: bool = True, fused_sampler: bool = True, fused_rope: bool = True,
                  fold_norms: bool = True, block_table=None):
         """kcaches, vcaches: per layer [B, Hkv, cap, D], or with block_table [B, max_pages] int32 the pools
-        [Hkv, num_pages, 128, D] of a paged cache (every layer's pages under the same ids)."""
+        [Hkv, num_pages, 128, D] of a paged cache (every layer's pages under the same ids), or a cache in 4 bits
+        (binding.q4_pool)."""
         self.dims = dims
         self.w = weights
         self.block_table = block_table
         # verify_round: LM head and sampler in one call that never materialises p
         self.fused_sampler = fused_sampler
         # RoPE applied by the QKV projection from a per-pass (cos, sin) table (head size 128 only)
-        self.fused_rope = fused_rope and dims.D == 128
+        # (norms of q and k come before the rotation, and a cache in 4 bits rotates on the way into it)
+        norms = {w is not None for lw in weights.layers for w in (lw.q_norm, lw.k_norm)}
+        if len(norms) > 1:
+            raise ValueError("q_norm and k_norm: of every layer or of none")
+        self.qk_norm = True in norms
+        self.q4 = bool(kcaches) and kcaches[0].dtype == torch.uint8
+        if self.q4 and block_table is None:
+            raise ValueError("a cache in 4 bits is paged (block_table)")
+        self.fused_rope = fused_rope and dims.D == 128 and not self.qk_norm and not self.q4
+        self.rope_table = self.fused_rope or self.qk_norm or self.q4      # a verify pass needs the rotation table
         self.fused_swiglu = fused_swiglu and dims.I % 64 == 0
         want = "interleaved" if self.fused_swiglu else "split"
         for lw in weights.layers:
@@ -191,8 +212,12 @@ class VerifyEngine:
                            S.spec_linear_norm_workspace_bytes(M, dims.I, dims.d, swiglu=True))
         if kcaches and block_table is not None:
             B, mp = block_table.shape
-            need = max(need, S.spec_attention_paged_workspace_bytes(B, max_rows, dims.Hq, dims.Hkv, dims.D, mp),
-                       S.spec_chunk_attention_workspace_bytes(B, max_M, dims.Hq, dims.Hkv, dims.D, mp))
+            if self.q4:
+                need = max(need, *(S.spec_chunk_attention_q4_workspace_bytes(B, max_M, r, dims.Hq, dims.Hkv, dims.D, mp)
+                                   for r in (max_rows, max_M)))
+            else:
+                need = max(need, S.spec_attention_paged_workspace_bytes(B, max_rows, dims.Hq, dims.Hkv, dims.D, mp),
+                           S.spec_chunk_attention_workspace_bytes(B, max_M, dims.Hq, dims.Hkv, dims.D, mp))
         elif kcaches:
             need = max(need, S.spec_attention_workspace_bytes(B, max_rows, dims.Hq, dims.Hkv, dims.D, cap))
         if weights.w_lm is not None:
@@ -219,13 +244,23 @@ class VerifyEngine:
         else:
             S.spec_verify_linear(hin, lw.w_qkv, Y=qkv, ws=self.ws, norm=nin)
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
-        if prompt:
+        if self.q4:
+            S.spec_kv_append_paged_q4(k, v, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table,
+                                      cs=self.cs[:M], Q=q, wq=lw.q_norm, wk=lw.k_norm, eps=dm.eps)
+            S.spec_chunk_attention_paged_q4(q, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table, O=o,
+                                            max_rows=max(M, 1) if prompt else max_rows, ws=self.ws)
+        elif prompt:
+            turned = lw.q_norm is not None
+            if turned:
+                S.spec_qk_norm_rope(q, k, lw.q_norm, lw.k_norm, dm.eps, cs=self.cs[:M])
             S.spec_kv_append_paged(k, v, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table,
-                                   cs=self.cs[:M], Q=q)
+                                   cs=None if turned else self.cs[:M], Q=None if turned else q)
             S.spec_chunk_attention_paged(q, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table, O=o,
                                          ws=self.ws)
         else:
-            if not self.fused_rope:
+            if lw.q_norm is not None:
+                S.spec_qk_norm_rope(q, k, lw.q_norm, lw.k_norm, dm.eps, cs=self.cs[:M])
+            elif not self.fused_rope:
                 S.spec_rope(q, k, cu_rows, ctx_len, dm.D, dm.theta)
             if self.block_table is not None:
                 S.spec_verify_attention_paged(q, k, v, cu_rows, ctx_len, self.kc[li], self.vc[li], self.block_table,
@@ -257,12 +292,12 @@ class VerifyEngine:
             self.x[:M].copy_(x0)
         L = len(self.w.layers) if n_layers is None else n_layers
         if positions is not None:
-            if not (self.fused_rope or prompt):
+            if not (self.rope_table or prompt):
                 raise ValueError("positions need the rotation table (fused_rope)")
             sections = self.dims.rope_sections or (self.dims.D // 2,)
             S.spec_rope_table_axes(positions, sections, self.dims.D, self.dims.theta, self.dims.rope_interleaved,
                                    cs=self.cs[:M])
-        elif (self.fused_rope or prompt) and L > 0:
+        elif (self.rope_table or prompt) and L > 0:
             S.spec_rope_table(cu_rows, ctx_len, M, self.dims.D, self.dims.theta, cs=self.cs[:M])
         if self.fold_norms and L > 0:
             S.spec_row_ssq(self.x[:M], out=self.ssq[:M])     # the first layer's input has no producer
