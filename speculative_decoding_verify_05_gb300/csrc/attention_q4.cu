@@ -1,7 +1,7 @@
 // Attention of a few rows per sequence (decode steps, verify rounds) over the paged cache in 4 bits, on tcgen05 tensor
-// cores: the R = G * rows <= 64 query rows of a kv head attend their sequence's keys, a page (128 keys) at a time.
+// cores: the R = G * rows <= 48 query rows of a kv head attend their sequence's keys, a page (128 keys) at a time.
 //
-// Products.  The cache's side is the MMA's 128 rows (its A operand), the queries its N = 16 .. 64 columns:
+// Products.  The cache's side is the MMA's 128 rows (its A operand), the queries its N = 16 .. 48 columns:
 //   S[key, row] = K . Q^T     M = 128 keys, K = 128 dims
 //   O[dim, row] += V^T . P    M = 128 dims, K = 128 keys
 // so a tile of 128 x 128 cached values is never padded, however few the rows.  K and V^T go to TMEM, not to shared
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int D = 128;
 constexpr int KT = 128;                   // keys per tile (one page)
-constexpr int MAXR = 64;                  // rows of an item
+constexpr int MAXR = 48;                  // rows of an item
 constexpr int PR = 4;                     // posted pieces of a slot
 constexpr int THREADS = 896;
 constexpr int REGS_ALL = 72;
@@ -120,18 +120,18 @@ struct Layout {
   // Registers: of few columns the softmax leaves some to the warps that bring pages to bf16, which wait less with them.
   static constexpr int REGS_SOFTMAX = NC <= 16 ? 96 : 112, REGS_ROLES = 56, REGS_BF16 = NC <= 16 ? 64 : 56;
   static_assert(256 * REGS_SOFTMAX + 128 * REGS_ROLES + 512 * REGS_BF16 <= THREADS * REGS_ALL, "register split");
-  static constexpr int SP = NC <= 48 ? 4 : 3;                     // pages in flight of a slot, of keys and of values
+  static constexpr int SP = 4;                                    // pages in flight of a slot, of keys and of values
   static constexpr int Q_HALF = NC * 128;                         // rows x 64 dims (128-byte swizzled rows)
   static constexpr int OFF_P = 0;                                 // of each slot: [key][row], 128-byte swizzled rows
   static constexpr int OFF_Q = OFF_P + 2 * KT * 128;              // of each slot two buffers of two halves
   static constexpr int OFF_KP = OFF_Q + 2 * 2 * 2 * Q_HALF;
   static constexpr int OFF_VP = OFF_KP + 2 * SP * Q4_BYTES;
   static constexpr int OFF_EXP = OFF_VP + 2 * SP * Q4_BYTES;      // scales of a tile of values, as pairs
-  static constexpr int OFF_REF = OFF_EXP + 4096;                  // [2][64] references
-  static constexpr int OFF_ADD = OFF_REF + 2 * MAXR * 4;          // [2][64] what is added to a score for it
-  static constexpr int OFF_ALPHA = OFF_ADD + 2 * MAXR * 4;        // [2][64] factors (of an end: what O is multiplied by)
-  static constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;        // [8][64] maxima, later sums, of the softmax warps
-  static constexpr int OFF_TOK = OFF_MAX + 8 * MAXR * 4;          // [64] token of each row
+  static constexpr int OFF_REF = OFF_EXP + 4096;                  // [2][48] references
+  static constexpr int OFF_ADD = OFF_REF + 2 * MAXR * 4;          // [2][48] what is added to a score for it
+  static constexpr int OFF_ALPHA = OFF_ADD + 2 * MAXR * 4;        // [2][48] factors (of an end: what O is multiplied by)
+  static constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;        // [8][48] maxima, later sums, of the softmax warps
+  static constexpr int OFF_TOK = OFF_MAX + 8 * MAXR * 4;          // [48] token of each row
   static constexpr int OFF_PIECE = OFF_TOK + MAXR * 4;            // [2][PR + 1]: posted, and the slot's first for the end
   static constexpr int OFF_SHARES = OFF_PIECE + 2 * (PR + 1) * (int)sizeof(Piece);
   static constexpr int OFF_BAR = OFF_SHARES + 2 * (int)sizeof(Shares);
@@ -944,8 +944,7 @@ cudaError_t launch_few_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& 
   switch (columns) {
     case 16: return launch<16>(tq, a, grid, s);
     case 32: return launch<32>(tq, a, grid, s);
-    case 48: return launch<48>(tq, a, grid, s);
-    default: return launch<64>(tq, a, grid, s);
+    default: return launch<48>(tq, a, grid, s);
   }
 }
 

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(128) kv_read_q4_kernel(const KvReadQ4Args a) {
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t s) {
-  const bool many = a.M > 10 * sms;
+  const bool many = a.M > 4 * sms;
   auto* k = many ? qk_norm_rope_kernel<2, 2> : qk_norm_rope_kernel<4, 3>;
   cudaError_t e = launch_k(k, dim3((unsigned)a.M), dim3(many ? 64 : 128), 0, s, a);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -403,7 +403,7 @@ cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t s) 
 
 cudaError_t launch_kv_append_q4(const KvAppendQ4Args& args, int sms, cudaStream_t s) {
   KvAppendQ4Args a = args;
-  const bool many = a.M > 10 * sms, wide = a.M >= 64 * a.B;
+  const bool many = a.M > 4 * sms, wide = a.M >= 64ll * a.B && (long long)(a.M >> 5) * a.Hkv >= 10 * sms;
   const int warps = many ? 2 : 4;
   a.blocks = (a.M >> (wide ? 5 : 3)) + 2 * a.B;
   a.value_ctas = (a.blocks * a.Hkv + warps - 1) / warps;

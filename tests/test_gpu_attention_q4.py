@@ -252,6 +252,48 @@ def test_deterministic_on_one_workspace(lib):
 
 
 @both
+def test_a_page_twice_in_one_sequence(lib, few):
+    """A table may name a page more than once: attention only reads."""
+    c = Case(25, [5, 3], [800, 300], 8, 2)
+    c.table[0, 4] = c.table[0, 1]
+    c.table[1, 0] = c.table[1, 1] = c.table[0, 2]
+    check(lib, c, "a page twice", few)
+
+
+def test_two_graphs_in_turn_on_one_workspace(lib):
+    """Both forms captured on one workspace, replayed in turn on one stream, and an eager call between them."""
+    cases = [(Case(26, [7, 1], [3000, 5000], 32, 8), True), (Case(27, [300, 9], [0, 2500], 16, 8), False),
+             (Case(28, [1, 2], [20000, 0], 8, 2), True)]
+    ws = lib.Workspace("cuda", max(lib.spec_chunk_attention_q4_workspace_bytes(c.B, c.M, c.M, c.Hq, c.Hkv, D, c.max_pages)
+                                   for c, _ in cases))
+    held, graphs = [], []
+    for c, few in cases:
+        args = (bf16_dev(c.q), *c.dev())
+        O = torch.zeros((c.M, c.Hq * D), dtype=torch.bfloat16, device="cuda")
+        held.append((args, O))
+
+        def call():
+            lib.spec_chunk_attention_paged_q4(*args, O=O, ws=ws, max_rows=int(c.rows.max()) if few else None)
+        call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    want = [bits_of(O) for _, O in held]
+    for (c, _), (_, O) in zip(cases, held):
+        ref, mag = c.oracle(1.0 / np.sqrt(D))
+        assert_attended(f64_of_bf16(O).reshape(ref.shape), ref, mag, "before capture")
+        O.fill_(3.0)
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+        lib.spec_chunk_attention_paged_q4(*held[0][0], O=held[0][1], ws=ws, max_rows=7)
+    lib.spec_device_status()
+    for w, (_, O) in zip(want, held):
+        assert np.array_equal(bits_of(O), w)
+
+
+@both
 def test_bad_input_is_flagged(lib, few):
     c = Case(19, [5, 7, 3], [130, 40, 0], 8, 2, spare=1)
     ref, mag = c.oracle(1.0 / np.sqrt(D))
