@@ -16,7 +16,17 @@
 // other starts or ends an item (with an item's tiles in turn to both, ending an item cost 4 us of the CTA: 64
 // sequences of 2 to 11 rows 126 us).  Pieces of an item that several slots share go to the
 // workspace as unnormalised O, reference and sum; the warps of its slots that are done when the last piece arrives join
-// it, a row at a time, in order of the slots whoever does it.
+// it, rows or parts of rows at a time, in order of the slots whoever does it.
+//
+// Bound.  Not HBM, though the work is a stream of pages: 16 sequences of one token at 30000 keys (32 / 8 heads) take 106
+// us = 4.8 TB/s where the copy takes 75, 64 sequences of 2 to 11 rows at up to 8192 keys 98 us of 46.  A page of keys and
+// one of values are 32768 entries to unpack, 725 warp instructions for each quarter of the SM with their share of the
+// softmax, and a slot's tiles wait for one another: unpack K, score, weigh, and only then P V, whose end frees V's and
+// P's place.  The SM issues in 72 % of the cycles with 16 columns, in 58 % with 48, where the softmax's share of
+// that chain is three times as long (a tile and slot about 1.3 and 2.4 us).  With few keys to a slot: 4 us to the first
+// product (lengths, page table, first pages), 4 to 5 to join shared items; 4 sequences of one token at 300 to 1000 keys 11.0 us.
+// Tried without gain: two places for P, tiles brought to bf16 in halves, eight softmax warps a slot, shares that count an
+// item's rows beside its keys.
 //
 // Roles (28 warps; four to a slot where not said otherwise): 0-7 softmax and epilogue (a thread per key, then per dim); 8 and 9
 // issue a slot's MMAs; 10 and 11 walk the batch for a slot, post its pieces and load its queries and pages; 12-19
@@ -39,8 +49,11 @@ constexpr int REGS_ALL = 72;
 constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   // 64 columns for each slot
 
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
-// What an item's start and end cost, in keys; what reading a piece back takes (see shares_of).
-constexpr int ITEM_KEYS = 320, PIECE_KEYS = 10;
+// What an item's start and end cost, in keys (64 sequences of 2 to 11 rows: 98.2 us, with 160 104.8, with 640 100.4).
+constexpr int ITEM_KEYS = 320;
+// What a piece costs the join, in keys (see shares_of): one sequence of one kv head, 8 query heads, at 20000 keys 13.3 us, at
+// 1000 9.0; cut into equal shares down to single tiles 17.8 and 13.5, with 10 keys a piece 14.4 and 9.0.
+constexpr int PIECE_KEYS = 3;
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ bool bar_or(int id, int n, bool x) {
@@ -117,10 +130,11 @@ struct Piece {
 // NC: columns of the MMAs (rows of the queries, a multiple of 16).
 template <int NC>
 struct Layout {
-  // Registers: of few columns the softmax leaves some to the warps that bring pages to bf16, which wait less with them.
+  // Registers: of few columns the softmax leaves some to the warps that bring pages to bf16 (16 x 1 row at 30000 keys
+  // 112.9 us with the other split).
   static constexpr int REGS_SOFTMAX = NC <= 16 ? 96 : 112, REGS_ROLES = 56, REGS_BF16 = NC <= 16 ? 64 : 56;
   static_assert(256 * REGS_SOFTMAX + 128 * REGS_ROLES + 512 * REGS_BF16 <= THREADS * REGS_ALL, "register split");
-  static constexpr int SP = 4;                                    // pages in flight of a slot, of keys and of values
+  static constexpr int SP = 4;     // pages in flight of a slot, of keys and of values (64 sequences of 2 to 11 rows: 100.1 us with 3)
   static constexpr int Q_HALF = NC * 128;                         // rows x 64 dims (128-byte swizzled rows)
   static constexpr int OFF_P = 0;                                 // of each slot: [key][row], 128-byte swizzled rows
   static constexpr int OFF_Q = OFF_P + 2 * KT * 128;              // of each slot two buffers of two halves
@@ -624,7 +638,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
           return e;
         };
         // Weights are relative to the row's reference: the maximum of the piece's first tile in which it sees a key, whose
-        // own weight is then 1, exactly.  Later tiles keep it as long as no weight passes 2^24 (any reference far below
+        // own weight is then 1.  Later tiles keep it as long as no weight passes 2^24 (any reference far below
         // the maximum gives the same quotients: bf16 and fp32 have exponents to spare); then the maximum is taken, O and
         // the sums rescaled, and the weights formed again.  (A row that sees no key of the piece's first tile sees none
         // of its later ones.)
@@ -895,12 +909,99 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
         }
         if (lane == 0) last_of(v, units);
       };
+      // A quarter of a row's dims at a time, its pieces dealt to four groups of eight lanes, which are joined at the end: 32
+      // pieces under way.  For many pieces of few rows (each piece brings four warps): one sequence of one kv head, 8 query
+      // heads, at 100000 keys 20.9 us, by whole rows 26.6; of 8 kv heads, 4 rows each, at 8000 keys 12.4 and 13.7.
+      auto join_quarters = [&]() {
+        const int units = 4 * R, sub = lane >> 3;
+        unsigned v = 0;
+        if (lane == 0) v = atomicAdd(tickets, 1u);
+        for (;;) {
+          const int unit = (int)(__shfl_sync(0xffffffffu, v, 0) & 0xffffu);
+          if (unit >= units) break;
+          if (lane == 0) v = atomicAdd(tickets, 1u);
+          const int r = unit >> 2, d = (unit & 3) * 32 + (lane & 7) * 4;
+          float top = -INFINITY, sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto add_piece = [&](float4 u, float2 ml, float base_m) {
+            const float w = ex2(ml.x - base_m);
+            sum += ml.y * w;
+            acc.x += u.x * w;
+            acc.y += u.y * w;
+            acc.z += u.z * w;
+            acc.w += u.w * w;
+          };
+          auto lift = [&](float high) {
+            const float base_m = high == -INFINITY ? 0.f : high, keep = ex2(top - base_m);
+            sum *= keep;
+            acc.x *= keep;
+            acc.y *= keep;
+            acc.z *= keep;
+            acc.w *= keep;
+            top = high;
+            return base_m;
+          };
+          Sharers s = all;
+          for (int base = c_first;; base += 32) {
+            const int rank = __popc(s.has & ((1u << lane) - 1u));
+            unsigned mine = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const unsigned of_k = __ballot_sync(0xffffffffu, (s.has >> lane & 1u) && (rank & 3) == k);
+              if (sub == k) mine = of_k;
+            }
+            float4 u[8];
+            float2 ml[8];
+            float high = top;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              ml[j] = make_float2(-INFINITY, 0.f);
+              u[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (mine) {
+                const int c = base + __ffs(mine) - 1;
+                const size_t at = ((size_t)c * 2 + (c == c_first ? 1 : 0)) * MAXR + r;
+                ml[j] = __ldcg(a.part_ml + at);
+                u[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + d));
+              }
+              mine &= mine - 1;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) high = fmaxf(high, ml[j].x);
+            const float base_m = lift(high);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) add_piece(u[j], ml[j], base_m);
+            if (s.t >= p.nt) break;
+            s = sharers(base + 32, s.t);
+          }
+#pragma unroll
+          for (int o = 8; o < 32; o <<= 1) {
+            float2 ml;
+            float4 u;
+            ml.x = __shfl_xor_sync(0xffffffffu, top, o);
+            ml.y = __shfl_xor_sync(0xffffffffu, sum, o);
+            u.x = __shfl_xor_sync(0xffffffffu, acc.x, o);
+            u.y = __shfl_xor_sync(0xffffffffu, acc.y, o);
+            u.z = __shfl_xor_sync(0xffffffffu, acc.z, o);
+            u.w = __shfl_xor_sync(0xffffffffu, acc.w, o);
+            add_piece(u, ml, lift(fmaxf(top, ml.x)));
+          }
+          if (sub == 0) {
+            const float inv = Q4_TILE_SCALE / sum;
+            const int tok = s_tok[r], g = r - tok * a.G;
+            *reinterpret_cast<uint2*>(a.O + (size_t)(p.row0 + tok) * a.ldo + (size_t)(p.h * a.G + g) * D + d) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          }
+        }
+        if (lane == 0) last_of(v, units);
+      };
+      const bool quarters = count > 8 && count >= R;
       if (there) {
         __syncwarp();
         if (count == 2) join(Int<4>{}, Int<2>{});
+        else if (quarters) join_quarters();
         else join(Int<1>{}, Int<8>{});
       } else if (lane == 0) {
-        last_of(atomicAdd(tickets, 0x10000u), count == 2 ? (R + 3) / 4 : R);
+        last_of(atomicAdd(tickets, 0x10000u), count == 2 ? (R + 3) / 4 : quarters ? 4 * R : R);
       }
       __syncwarp();
     }
@@ -935,6 +1036,10 @@ cudaError_t launch(const CUtensorMap& tq, const ChunkAttnArgs& a, int grid, cuda
 
 }  // namespace
 
+// Up to 48 rows this kernel is the faster one, with few exceptions (in us, this one / attention_chunk.cu's; 32 query and 8 kv
+// heads): 64 sequences of 4000 keys with 16 rows per kv head 76 / 170, with 32 106 / 173, with 48 140 / 173, with 64 195 / 173;
+// 8 of 30000 keys 67 / 153, 93 / 155, 118 / 155, 173 / 154.  The exceptions: batches that give the other's CTAs about an
+// item each, 8 to 19 sequences of 500 to 1000 keys, with 32 rows up to 1.7 us, with 48 up to 5 (16 at 1000 keys 25.2 / 20.5).
 int few_attention_q4_columns(int G, int max_rows) {
   return (long long)G * max_rows <= MAXR ? (G * max_rows + 15) / 16 * 16 : 0;
 }

@@ -251,6 +251,18 @@ def test_deterministic_on_one_workspace(lib):
             assert np.array_equal(bits_of(run(lib, c, few, ws=ws)), want)
 
 
+@pytest.mark.parametrize("grid", [0, 600])
+@pytest.mark.parametrize("Hq,Hkv,rows,ctx", [
+    (4, 1, [1], [30000]), (8, 1, [2], [40000]), (48, 1, [1], [50000]), (16, 1, [3, 1], [20000, 25000]), (12, 2, [3], [9000])])
+def test_items_of_many_pieces(lib, Hq, Hkv, rows, ctx, grid):
+    """Few rows over a context that more than 32 slots share."""
+    lib.spec_set_option("persistent_grid", grid)
+    try:
+        check(lib, Case(29, rows, ctx, Hq, Hkv), (rows, ctx, grid), True)
+    finally:
+        lib.spec_set_option("persistent_grid", 0)
+
+
 @both
 def test_a_page_twice_in_one_sequence(lib, few):
     """A table may name a page more than once: attention only reads."""
