@@ -1,5 +1,12 @@
 // The paged cache in 4 bits (q4.cuh): norms of queries and keys with their rotation, the append that quantises a
 // chunk's keys and values, and the read of cached keys and values.
+//
+// Bound.  Of a few rows, a launch and the chain of loads behind it (norm of 9 rows 3.5 us, append of 8 4.1, read of 77
+// keys 5.6: lengths, page id, page, output).  Of many, with 32 / 8 heads:
+//   norm, 8192 rows    29.5 us = 5.8 TB/s, 86 % of the copy; loads wait for HBM (issue 46 %)
+//   append, 8192 rows  39.7 us = 3.2 TB/s, 47 %; issue 56 %: 15 instructions a value for norm, rotation, maximum,
+//                      quotient and packing, and the rows' chains of shuffles leave the rest idle; keys and values only 16.6 us
+//   read, 32 contexts  63.8 us = 6.0 TB/s, 88 %
 #include "attention_util.cuh"
 #include "internal.h"
 #include "paged_rows.cuh"
@@ -107,7 +114,7 @@ __device__ __forceinline__ void each_head(const uint16_t* src, int heads, const 
   }
 }
 
-// One CTA per row.
+// One CTA per row.  At least 14 CTAs of two warps an SM (72 registers a thread): 8192 rows 29.5 us, 32.9 without the bound.
 template <int WARPS, int UNITS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 2 ? 14 : 5) qk_norm_rope_kernel(const NormRopeArgs a) {
   pdl_wait();
@@ -286,8 +293,7 @@ __device__ __forceinline__ void append_key(const KvAppendQ4Args& a, const Head& 
 }
 
 // CTAs: a thread per sequence that checks its bounds (no row has to be in a sequence that breaks them) and blocks of values, a
-// warp each, then one CTA per row for its keys and queries.  Blocks of 32 keys write whole lines of a page, those of 8
-// leave more warps to a few rows.
+// warp each, then one CTA per row for its keys and queries.  (8192 rows without a bound on the registers: 44 us.)
 template <int WARPS, int UNITS, int LB>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 2 ? 14 : 5) kv_append_q4_kernel(const KvAppendQ4Args a) {
   pdl_wait();
@@ -394,6 +400,9 @@ __global__ void __launch_bounds__(128) kv_read_q4_kernel(const KvReadQ4Args a) {
 
 }  // namespace
 
+// CTAs of two warps where there are more than four rows for each SM, of four below, where they shorten a row's chain
+// (norm with 32 / 8 heads, in us, four warps and two: 8 rows 3.5 / 4.1, 400 4.1 / 4.2, 600 4.8 / 4.8 to 5.5, 900 6.9 / 6.2, 8192
+// 37.6 / 29.3; append 8 rows 4.1 / 4.8, 600 5.5 to 8.9 / 6.2 to 8.2, 900 8.6 / 7.6, 8192 57 / 40.6).
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t s) {
   const bool many = a.M > 4 * sms;
   auto* k = many ? qk_norm_rope_kernel<2, 2> : qk_norm_rope_kernel<4, 3>;
@@ -401,15 +410,19 @@ cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t s) 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Values in blocks of 32 keys write whole 16-byte rows of a page, in blocks of 8 a word of each, and leave four times as many
+// warps.  The wide ones are taken where sequences bring at least two of them and they alone are ten warps an SM (32 / 8 heads,
+// in us, blocks of 8 and of 32: one sequence of 600 rows 5.5 / 10.1, 3000 17.7 / 16.4, 4000 21.2 / 21.2, 6500 33.5 / 31.6, 8192 40.6 /
+// 39.4; its keys and values only 4.2 / 9.6, 8.2 / 11.2, 10.3 / 11.7, 15.0 / 14.3, 18.5 / 16.6).
 cudaError_t launch_kv_append_q4(const KvAppendQ4Args& args, int sms, cudaStream_t s) {
   KvAppendQ4Args a = args;
-  const bool many = a.M > 4 * sms, wide = a.M >= 64ll * a.B && (long long)(a.M >> 5) * a.Hkv >= 10 * sms;
+  const bool many = a.M > 4 * sms, wide = many && a.M >= 64ll * a.B && (long long)(a.M >> 5) * a.Hkv >= 10 * sms;
   const int warps = many ? 2 : 4;
   a.blocks = (a.M >> (wide ? 5 : 3)) + 2 * a.B;
   a.value_ctas = (a.blocks * a.Hkv + warps - 1) / warps;
   a.check_ctas = (a.B + 32 * warps - 1) / (32 * warps);
   auto* k = many ? (wide ? kv_append_q4_kernel<2, 2, 5> : kv_append_q4_kernel<2, 2, 3>)
-                 : (wide ? kv_append_q4_kernel<4, 3, 5> : kv_append_q4_kernel<4, 3, 3>);
+                 : kv_append_q4_kernel<4, 3, 3>;
   cudaError_t e = launch_k(k, dim3((unsigned)a.M + a.value_ctas + a.check_ctas), dim3(32 * warps), 0, s, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -1,9 +1,8 @@
 // The paged cache in 4 bits: a value is a whole number n of -7 .. 7 times the scale of its 32 neighbouring dims of one
 // key, an 8-bit float without a sign (5 exponent bits, 3 mantissa bits): byte c stands for
-// (1 + (c & 7) / 8) 2^((c >> 3) - 20).  Why whole numbers and not the 4-bit floats (0 .5 1 1.5 2 3 4 6): with groups
-// this small, scaled by their maximum, the levels of normal values are used evenly, and the floats' wide steps at
-// the top cost twice the squared error (normal values in groups of 32: 9.75 % off in rms, 12.9 % as
-// floats); and two of them leave an integer word by one logical operation.  The scale needs no second one per tensor: it
+// (1 + (c & 7) / 8) 2^((c >> 3) - 20).  Why whole numbers and not the 4-bit floats (0 .5 1 1.5 2 3 4 6): scaled by
+// the maximum of so small a group their even steps fit normal values at least as well (off by 9.8 % in rms, the floats by
+// 10.2 %), and two of them leave a word by one logical operation.  The scale needs no second one per tensor: it
 // reaches from 2^-20 to 3840, so values of 7e-6 to 26880 keep their precision whatever the tensor's range.
 //
 // A page holds 128 keys of one kv head in 8704 bytes: 4 planes of 128 rows of 16 bytes (32 entries), then 512 scales.
@@ -38,7 +37,8 @@ struct Q4Scale {
 };
 // Of a finite maximum below Q4_LARGE.  Quotients by Markstein's theorem ("Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990): with the correctly rounded reciprocal of the divisor, one step by the exact remainder
-// leaves the correctly rounded quotient.  The scale's reciprocal is one Newton step (y + y (1 - s y)) from the hardware's
+// leaves the correctly rounded quotient (here the divisor has at most 4 bits, so a quotient that is no number of 24 bits lies
+// at least a thirtieth of a unit from the middle of two).  The scale's reciprocal is one Newton step (y + y (1 - s y)) from the hardware's
 // approximation: 1 - s y is exact (s has 4 bits), and what is rounded is 1 / s off by the square of the approximation's
 // error, far less than 1 / s is from the middle of two numbers (s has 8 significands; 1/9 .. 1/15 repeat in at most 12 bits).
 // (The division operator's general sequence, per value, made the append of 8192 rows wait for instructions: 48 us.)
