@@ -4,8 +4,8 @@
 // Bound.  Of a few rows, a launch and the chain of loads behind it (norm of 9 rows 3.5 us, append of 8 4.1, read of 77
 // keys 5.6: lengths, page id, page, output).  Of many, with 32 / 8 heads:
 //   norm, 8192 rows    29.5 us = 5.8 TB/s, 86 % of the copy; loads wait for HBM (issue 46 %)
-//   append, 8192 rows  39.7 us = 3.2 TB/s, 47 %; issue 56 %: 15 instructions a value for norm, rotation, maximum,
-//                      quotient and packing, and the rows' chains of shuffles leave the rest idle; keys and values only 16.6 us
+//   append, 8192 rows  38.6 us = 3.3 TB/s, 49 %; issue 56 %: some 15 instructions a value for norm, rotation, maximum,
+//                      quotient and packing, and chains of shuffles; keys and values only 15.2 us
 //   read, 32 contexts  63.8 us = 6.0 TB/s, 88 %
 #include "attention_util.cuh"
 #include "internal.h"
@@ -168,6 +168,22 @@ __device__ __forceinline__ void check_sequence(const Args& a, long long b, unsig
 }
 
 // ----------------------------------------------------------------- append
+// What eight keys of any values, infinities and NaN among them, add to a lane's four words; returns the code of key lane % 8.
+// Out of line: seldom needed.
+__device__ __noinline__ unsigned any_values(const uint2 (&x)[8], uint32_t (&add)[4]) {
+  unsigned mine = 0;
+  add[0] = add[1] = add[2] = add[3] = 0;
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) {
+    const uint2 r = q4_any(make_float4(bf16lo(x[j].x), bf16hi(x[j].x), bf16lo(x[j].y), bf16hi(x[j].y)),
+                           make_float4(0.f, 0.f, 0.f, 0.f), 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) add[e] += (((r.x >> (4 * e)) & 15u) - 8u) << q4_shift(j);
+    if ((threadIdx.x & 7) == j) mine = r.y;
+  }
+  return mine;
+}
+
 // Values of a block of 2^LB keys (8 or 32) of one kv head, by a warp: a lane has dims 4 lane .. 4 lane + 3 of all of them, which
 // are one word or all four words of four rows of the page.  Entries of other keys in a word stay as they are (a
 // page that receives rows belongs to one sequence, and a sequence's words each to one warp).
@@ -204,33 +220,44 @@ __device__ __forceinline__ void append_values(const KvAppendQ4Args& a, int v, in
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[i][e] = (keep ? words[4 * e + i] & keep : 0u) | (0x88888888u & ~keep);
-    unsigned mine = 0;
+    // (keys of other chunks and sequences are zeros here, which add nothing)
+    unsigned top[8], mine;                 // (as bits: NaN lies above everything)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < lo || j >= hi) continue;
-      const float2 f0 = make_float2(bf16lo(x[j].x), bf16hi(x[j].x)), f1 = make_float2(bf16lo(x[j].y), bf16hi(x[j].y));
-      // (as bits: NaN lies above everything)
-      unsigned bits = max(max(__float_as_uint(f0.x) & 0x7fffffffu, __float_as_uint(f0.y) & 0x7fffffffu),
-                          max(__float_as_uint(f1.x) & 0x7fffffffu, __float_as_uint(f1.y) & 0x7fffffffu));
+    for (int j = 0; j < 8; ++j)
+      top[j] = max(max((x[j].x << 16) & 0x7fffffffu, x[j].x & 0x7fffffffu), max((x[j].y << 16) & 0x7fffffffu, x[j].y & 0x7fffffffu));
+    // folded over the eight lanes of a scale: lane k of them is left with key k's, and works out its scale for all (each lane
+    // for each key: 8192 rows 39.6 us, 24 sequences 11.7 instead of 11.0)
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) bits = max(bits, __shfl_xor_sync(ALL, bits, o));
-      unsigned code;
-      if (__any_sync(ALL, bits >= __float_as_uint(Q4_LARGE))) {
-        const uint2 r = q4_any(make_float4(f0.x, f0.y, f1.x, f1.y), make_float4(0.f, 0.f, 0.f, 0.f), 8);
+    for (int o = 4; o > 0; o >>= 1) {
+      const bool up = (lane & o) != 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[i][e] += (((r.x >> (4 * e)) & 15u) - 8u) << q4_shift(j);
-        code = r.y;
-      } else {
-        const Q4Scale s = q4_scale(__uint_as_float(bits));
-        const float2 sc = make_float2(s.scale, s.scale), rc = make_float2(s.reciprocal, s.reciprocal);
-        const int2 n0 = q4_whole2(f0, sc, rc), n1 = q4_whole2(f1, sc, rc);
+      for (int k = 0; k < o; ++k) {
+        const unsigned send = up ? top[k] : top[k + o], stay = up ? top[k + o] : top[k];
+        top[k] = max(stay, __shfl_xor_sync(ALL, send, o));
+      }
+    }
+    if (__any_sync(ALL, top[0] >= __float_as_uint(Q4_LARGE))) {
+      uint2 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = x[j];
+      uint32_t add[4];
+      mine = any_values(v, add);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[i][e] += add[e];
+    } else {
+      const Q4Scale s = q4_scale(__uint_as_float(top[0] & 0xffff0000u));
+      mine = s.code;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float a_scale = __shfl_sync(ALL, s.scale, (lane & 24) | j), its = __shfl_sync(ALL, s.reciprocal, (lane & 24) | j);
+        const float2 sc = make_float2(a_scale, a_scale), rc = make_float2(its, its);
+        const int2 n0 = q4_whole2(make_float2(bf16lo(x[j].x), bf16hi(x[j].x)), sc, rc);
+        const int2 n1 = q4_whole2(make_float2(bf16lo(x[j].y), bf16hi(x[j].y)), sc, rc);
         w[i][0] += (unsigned)n0.x << q4_shift(j);
         w[i][1] += (unsigned)n0.y << q4_shift(j);
         w[i][2] += (unsigned)n1.x << q4_shift(j);
         w[i][3] += (unsigned)n1.y << q4_shift(j);
-        code = s.code;
       }
-      if ((lane & 7) == j) mine = code;
     }
     const int j = lane & 7;
     if (j >= lo && j < hi) page[Q4_SCALES + (lane >> 3) * 128 + slot + 8 * i + j] = (uint8_t)mine;
@@ -293,7 +320,7 @@ __device__ __forceinline__ void append_key(const KvAppendQ4Args& a, const Head& 
 }
 
 // CTAs: a thread per sequence that checks its bounds (no row has to be in a sequence that breaks them) and blocks of values, a
-// warp each, then one CTA per row for its keys and queries.  (8192 rows without a bound on the registers: 44 us.)
+// warp each, then one CTA per row for its keys and queries.  (8192 rows: without a bound on the registers 44 us, with 12 CTAs an SM 40.7.)
 template <int WARPS, int UNITS, int LB>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 2 ? 14 : 5) kv_append_q4_kernel(const KvAppendQ4Args a) {
   pdl_wait();
@@ -412,8 +439,8 @@ cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t s) 
 
 // Values in blocks of 32 keys write whole 16-byte rows of a page, in blocks of 8 a word of each, and leave four times as many
 // warps.  The wide ones are taken where sequences bring at least two of them and they alone are ten warps an SM (32 / 8 heads,
-// in us, blocks of 8 and of 32: one sequence of 600 rows 5.5 / 10.1, 3000 17.7 / 16.4, 4000 21.2 / 21.2, 6500 33.5 / 31.6, 8192 40.6 /
-// 39.4; its keys and values only 4.2 / 9.6, 8.2 / 11.2, 10.3 / 11.7, 15.0 / 14.3, 18.5 / 16.6).
+// keys and values only, in us, blocks of 8 and of 32: one sequence of 600 rows 3.5 / 9.6, 5000 12.3 / 12.4, 6500 15.0 / 14.3, 8192
+// 16.6 / 15.2; with queries and norms 8192 39.0 / 38.6).
 cudaError_t launch_kv_append_q4(const KvAppendQ4Args& args, int sms, cudaStream_t s) {
   KvAppendQ4Args a = args;
   const bool many = a.M > 4 * sms, wide = many && a.M >= 64ll * a.B && (long long)(a.M >> 5) * a.Hkv >= 10 * sms;
