@@ -93,6 +93,23 @@ def test_append_many_rows(lib):
     assert np.array_equal(vp.cpu().numpy(), c.append(c.v, c.vp, False))
 
 
+def test_append_many_rows_and_heads(lib):
+    """Enough of both for values in blocks of 32 keys: sequences that end inside a block, rows of other chunks beside them,
+    infinities, NaN and values past the scales here and there."""
+    c = Cache(14, [333, 40, 427], [77, 500, 5], 64)
+    rng = np.random.default_rng(15)
+    at = rng.integers(0, c.M, 200), rng.integers(0, 2 * 64 * D, 200)
+    c.qkv[at] = rng.choice(np.array([0x7F80, 0xFF80, 0x7FC0, 0x46D2, 0xC6D3, 0x7F7F, 0x0001], np.uint16), 200)
+    x = obf.decode(c.qkv[:, :2 * 64 * D]).reshape(c.M, 128, D)
+    c.k, c.v = x[:, :64], x[:, 64:]
+    cu, cx, kp, vp, table = c.dev()
+    _, k, v = c.parts()
+    lib.spec_kv_append_paged_q4(k, v, cu, cx, kp, vp, table)
+    lib.spec_device_status()
+    assert np.array_equal(kp.cpu().numpy(), c.append(c.k, c.kp, True))
+    assert np.array_equal(vp.cpu().numpy(), c.append(c.v, c.vp, False))
+
+
 def test_append_every_bf16(lib):
     """Every bf16 bit pattern, infinities and NaN among them, and borders of the scales and of the whole numbers."""
     bits = np.random.default_rng(5).permutation(np.arange(65536).astype(np.uint16))
