@@ -538,7 +538,7 @@ SPEC_API int spec_kv_read_paged_q4(const uint8_t* Kpool, const uint8_t* Vpool, i
 
 /* Attention of a chunk of new rows over a cache in 4 bits: as spec_chunk_attention_paged, over the keys and values that
  * spec_kv_read_paged_q4 returns (they enter the products as they are, in bf16).
- *   max_rows  an upper bound on the rows of one sequence, which the host knows (M if it does not): up to 48
+ *   max_rows  an upper bound on the rows of one sequence, which the host knows (M if it does not): up to 64
  *             rows per kv head (max_rows * Hq / Hkv) a kernel for few rows runs
  *   Kpool, Vpool [Hkv][num_pages][SPEC_Q4_PAGE_BYTES]
  * What lies behind a sequence's last key in its page may hold anything.  Checked on the device, with the status

@@ -44,10 +44,10 @@
 // Over a cache in 4 bits (q4.cuh) the same kernel has four more warps, 12-15: they take pages as they lie in the cache from
 // a ring of 3 and write them as bf16 tiles into the ring of K and V (4 stages beside it), values transposed, so that
 // both products read their tiles alike.  Keys and values come scaled down by 2^19, which the softmax scale and the
-// outputs take back.  Bound: a K and a V tile are written once and read by two products each, and with the packed pages, the scales
-// and Q that is about 2320 cycles of shared memory at 128 bytes where the products take 2048; a prompt of 8192 rows 357 us = 1541
-// TFLOP/s (bf16 pools 306 in the same run).  Fewer rows than a tile waste the products but not the pages: the
-// kernel for few rows, attention_q4.cu, takes over at 48 rows per kv head.
+// outputs take back.  Bound: besides what bounds bf16 pools, how fast four warps, one on each quarter of the SM, bring a tile
+// to bf16, some 250 instructions and their waits; a prompt of 8192 rows 330 us = 1665 TFLOP/s (bf16 pools 306 to 337 in the
+// same runs, with the clock), 64 x 4 rows at 4000 keys 144 us.  Fewer rows than a tile waste the products but not the pages: the
+// kernel for few rows, attention_q4.cu, takes over at 64 rows per kv head.
 #include "attention_util.cuh"
 #include "internal.h"
 #include "q4.cuh"
@@ -71,7 +71,7 @@ template <bool Q4>
 struct Shape {
   static constexpr int ST = Q4 ? 4 : 5;   // ring stages of one K or V tile
   static constexpr int THREADS = Q4 ? 512 : 384;
-  static constexpr int REGS_ALL = Q4 ? 128 : 168, REGS_SOFTMAX = Q4 ? 192 : 208, REGS_OTHER = Q4 ? 72 : 80, REGS_Q4 = 56;
+  static constexpr int REGS_ALL = Q4 ? 128 : 168, REGS_SOFTMAX = Q4 ? 192 : 208, REGS_OTHER = Q4 ? 64 : 80, REGS_Q4 = 64;
   static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER + (Q4 ? 128 * REGS_Q4 : 0) <= THREADS * REGS_ALL, "register split");
   static constexpr int OFF_PACKED = OFF_RING + ST * TILE;              // pages as they lie in the cache
   static constexpr int OFF_EXP = OFF_PACKED + (Q4 ? PST * Q4_BYTES : 0);   // scales of a tile of values, as pairs
@@ -403,29 +403,38 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       uint8_t* dst = smem + OFF_RING + st * TILE + row * 128;
+      auto put = [&](int q, int i, uint4 v) {
+        *reinterpret_cast<uint4*>(dst + (q >> 1) * HALF + ((((q & 1) * 4 + i) ^ (row & 7)) << 4)) = v;
+      };
+      if (kind == 0) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-        uint32_t even = 0, odd = 0, less = 0;
-        if (kind == 0) {
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
           const uint32_t c = __byte_perm(codes, 0, 0x4040 | q * 0x0101);
-          even = q4_even2(c);
-          odd = q4_odd2(c);
-          less = q4_less2(c);
-        }
+          const uint32_t even = q4_even2(c), odd = q4_odd2(c), less = q4_less2(c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x8 = x[i] >> 8;
-          uint4 v;
-          if (kind == 0) {
-            v = make_uint4(q4_tile_pair<0>(x[i], x8, even, less), q4_tile_pair<1>(x[i], x8, odd, less),
-                           q4_tile_pair<2>(x[i], x8, even, less), q4_tile_pair<3>(x[i], x8, odd, less));
-          } else {
-            const uint4 e0 = exp[8 * q + 2 * i], e1 = exp[8 * q + 2 * i + 1];
-            v = make_uint4(q4_tile_pair<0>(x[i], x8, e0.x, e0.y), q4_tile_pair<1>(x[i], x8, e0.z, e0.w),
-                           q4_tile_pair<2>(x[i], x8, e1.x, e1.y), q4_tile_pair<3>(x[i], x8, e1.z, e1.w));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x8 = x[i] >> 8;
+            put(q, i, make_uint4(q4_tile_pair<0>(x[i], x8, even, less), q4_tile_pair<1>(x[i], x8, odd, less),
+                                 q4_tile_pair<2>(x[i], x8, even, less), q4_tile_pair<3>(x[i], x8, odd, less)));
           }
-          *reinterpret_cast<uint4*>(dst + (q >> 1) * HALF + ((((q & 1) * 4 + i) ^ (row & 7)) << 4)) = v;
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+          // (ahead of the stores, which the compiler would keep each of them behind: 8192 rows 357 us, 64 x 4 rows at
+          // 4000 keys 163)
+          uint4 e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e[i] = exp[8 * q + i];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x8 = x[i] >> 8;
+            const uint4 e0 = e[2 * i], e1 = e[2 * i + 1];
+            put(q, i, make_uint4(q4_tile_pair<0>(x[i], x8, e0.x, e0.y), q4_tile_pair<1>(x[i], x8, e0.z, e0.w),
+                                 q4_tile_pair<2>(x[i], x8, e1.x, e1.y), q4_tile_pair<3>(x[i], x8, e1.z, e1.w)));
+          }
         }
       }
       fence_proxy_async_smem();

@@ -1,7 +1,7 @@
 // Attention of a few rows per sequence (decode steps, verify rounds) over the paged cache in 4 bits, on tcgen05 tensor
-// cores: the R = G * rows <= 48 query rows of a kv head attend their sequence's keys, a page (128 keys) at a time.
+// cores: the R = G * rows <= 64 query rows of a kv head attend their sequence's keys, a page (128 keys) at a time.
 //
-// Products.  The cache's side is the MMA's 128 rows (its A operand), the queries its N = 16 .. 48 columns:
+// Products.  The cache's side is the MMA's 128 rows (its A operand), the queries its N = 16 .. 64 columns:
 //   S[key, row] = K . Q^T     M = 128 keys, K = 128 dims
 //   O[dim, row] += V^T . P    M = 128 dims, K = 128 keys
 // so a tile of 128 x 128 cached values is never padded, however few the rows.  K and V^T go to TMEM, not to shared
@@ -23,7 +23,7 @@
 // one of values are 32768 entries to unpack, 725 warp instructions for each quarter of the SM with their share of the
 // softmax, and a slot's tiles wait for one another: unpack K, score, weigh, and only then P V, whose end frees V's and
 // P's place.  The SM issues in 72 % of the cycles with 16 columns, in 58 % with 48, where the softmax's share of
-// that chain is three times as long (a tile and slot about 1.3 and 2.4 us).  With few keys to a slot: 4 us to the first
+// that chain is three times as long (a tile of a slot takes about 1.2 us with 16 columns, 1.6 with 48).  With few keys to a slot: 4 us to the first
 // product (lengths, page table, first pages), 4 to 5 to join shared items; 4 sequences of one token at 300 to 1000 keys 11.0 us.
 // Tried without gain: two places for P, tiles brought to bf16 in halves, eight softmax warps a slot, shares that count an
 // item's rows beside its keys.
@@ -42,7 +42,7 @@ namespace {
 
 constexpr int D = 128;
 constexpr int KT = 128;                   // keys per tile (one page)
-constexpr int MAXR = 48;                  // rows of an item
+constexpr int MAXR = 64;                  // rows of an item
 constexpr int PR = 4;                     // posted pieces of a slot
 constexpr int THREADS = 896;
 constexpr int REGS_ALL = 72;
@@ -51,8 +51,8 @@ constexpr uint32_t TMEM_COLS = 512, T_K = 0, T_V = 128, T_S = 256, T_O = 384;   
 constexpr uint64_t JOIN_WAIT_NS = 20000;  // how long a warp that is done waits for the other pieces of a shared item
 // What an item's start and end cost, in keys (64 sequences of 2 to 11 rows: 98.2 us, with 160 104.8, with 640 100.4).
 constexpr int ITEM_KEYS = 320;
-// What a piece costs the join, in keys (see shares_of): one sequence of one kv head, 8 query heads, at 20000 keys 13.3 us, at
-// 1000 9.0; cut into equal shares down to single tiles 17.8 and 13.5, with 10 keys a piece 14.4 and 9.0.
+// What a piece costs the join, in keys (see shares_of): one sequence of one kv head, 8 query heads, at 20000 keys 13.0 us, at
+// 1000 8.9; cut into equal shares down to single tiles 17.8 and 13.4, with 1 key a piece 14.5 and 9.2.
 constexpr int PIECE_KEYS = 3;
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -134,18 +134,19 @@ struct Layout {
   // 112.9 us with the other split).
   static constexpr int REGS_SOFTMAX = NC <= 16 ? 96 : 112, REGS_ROLES = 56, REGS_BF16 = NC <= 16 ? 64 : 56;
   static_assert(256 * REGS_SOFTMAX + 128 * REGS_ROLES + 512 * REGS_BF16 <= THREADS * REGS_ALL, "register split");
-  static constexpr int SP = 4;     // pages in flight of a slot, of keys and of values (64 sequences of 2 to 11 rows: 100.1 us with 3)
+  // Pages in flight of a slot, of keys and of values (64 sequences of 2 to 11 rows, in 48 columns: 100.1 us with 3)
+  static constexpr int SP = NC <= 48 ? 4 : 3;
   static constexpr int Q_HALF = NC * 128;                         // rows x 64 dims (128-byte swizzled rows)
   static constexpr int OFF_P = 0;                                 // of each slot: [key][row], 128-byte swizzled rows
   static constexpr int OFF_Q = OFF_P + 2 * KT * 128;              // of each slot two buffers of two halves
   static constexpr int OFF_KP = OFF_Q + 2 * 2 * 2 * Q_HALF;
   static constexpr int OFF_VP = OFF_KP + 2 * SP * Q4_BYTES;
   static constexpr int OFF_EXP = OFF_VP + 2 * SP * Q4_BYTES;      // scales of a tile of values, as pairs
-  static constexpr int OFF_REF = OFF_EXP + 4096;                  // [2][48] references
-  static constexpr int OFF_ADD = OFF_REF + 2 * MAXR * 4;          // [2][48] what is added to a score for it
-  static constexpr int OFF_ALPHA = OFF_ADD + 2 * MAXR * 4;        // [2][48] factors (of an end: what O is multiplied by)
-  static constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;        // [8][48] maxima, later sums, of the softmax warps
-  static constexpr int OFF_TOK = OFF_MAX + 8 * MAXR * 4;          // [48] token of each row
+  static constexpr int OFF_REF = OFF_EXP + 4096;                  // [2][64] references
+  static constexpr int OFF_ADD = OFF_REF + 2 * MAXR * 4;          // [2][64] what is added to a score for it
+  static constexpr int OFF_ALPHA = OFF_ADD + 2 * MAXR * 4;        // [2][64] factors (of an end: what O is multiplied by)
+  static constexpr int OFF_MAX = OFF_ALPHA + 2 * MAXR * 4;        // [8][64] maxima, later sums, of the softmax warps
+  static constexpr int OFF_TOK = OFF_MAX + 8 * MAXR * 4;          // [64] token of each row
   static constexpr int OFF_PIECE = OFF_TOK + MAXR * 4;            // [2][PR + 1]: posted, and the slot's first for the end
   static constexpr int OFF_SHARES = OFF_PIECE + 2 * (PR + 1) * (int)sizeof(Piece);
   static constexpr int OFF_BAR = OFF_SHARES + 2 * (int)sizeof(Shares);
@@ -911,7 +912,7 @@ few_attention_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const ChunkAttn
       };
       // A quarter of a row's dims at a time, its pieces dealt to four groups of eight lanes, which are joined at the end: 32
       // pieces under way.  For many pieces of few rows (each piece brings four warps): one sequence of one kv head, 8 query
-      // heads, at 100000 keys 20.9 us, by whole rows 26.6; of 8 kv heads, 4 rows each, at 8000 keys 12.4 and 13.7.
+      // heads, at 100000 keys 19.2 us, by whole rows 24.0; of 8 kv heads, 4 rows each, at 8000 keys 11.7 and 13.6.
       auto join_quarters = [&]() {
         const int units = 4 * R, sub = lane >> 3;
         unsigned v = 0;
@@ -1036,10 +1037,11 @@ cudaError_t launch(const CUtensorMap& tq, const ChunkAttnArgs& a, int grid, cuda
 
 }  // namespace
 
-// Up to 48 rows this kernel is the faster one, with few exceptions (in us, this one / attention_chunk.cu's; 32 query and 8 kv
-// heads): 64 sequences of 4000 keys with 16 rows per kv head 76 / 170, with 32 106 / 173, with 48 140 / 173, with 64 195 / 173;
-// 8 of 30000 keys 67 / 153, 93 / 155, 118 / 155, 173 / 154.  The exceptions: batches that give the other's CTAs about an
-// item each, 8 to 19 sequences of 500 to 1000 keys, with 32 rows up to 1.7 us, with 48 up to 5 (16 at 1000 keys 25.2 / 20.5).
+// Up to 64 rows (TMEM has 64 columns for a slot's scores) this kernel is the faster one, with few exceptions (in us, this one /
+// attention_chunk.cu's; 32 query and 8 kv heads): 64 sequences of 4000 keys with 16 rows per kv head 67 / 144, with 32 80 /
+// 144, with 48 93 / 145, with 64 119 / 145; 8 of 30000 keys 60 / 129, 71 / 130, 82 / 130, 108 / 129.  The exceptions: batches
+// that give the other's CTAs about one short item each, 8 to 16 sequences of 500 to 1000 keys, with 48 rows up to 4 us, with
+// 64 up to 8 (16 at 1000 keys 25.9 / 18.5); the host does not know the lengths.
 int few_attention_q4_columns(int G, int max_rows) {
   return (long long)G * max_rows <= MAXR ? (G * max_rows + 15) / 16 * 16 : 0;
 }
@@ -1049,7 +1051,8 @@ cudaError_t launch_few_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& 
   switch (columns) {
     case 16: return launch<16>(tq, a, grid, s);
     case 32: return launch<32>(tq, a, grid, s);
-    default: return launch<48>(tq, a, grid, s);
+    case 48: return launch<48>(tq, a, grid, s);
+    default: return launch<64>(tq, a, grid, s);
   }
 }
 

@@ -276,9 +276,9 @@ cudaError_t launch_chunk_attention(const CUtensorMap& tq, const CUtensorMap& tk,
                                    const ChunkAttnArgs& a, int grid, cudaStream_t s);
 // The same over a cache in 4 bits (q4.cuh).
 cudaError_t launch_chunk_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& a, int grid, cudaStream_t s);
-// ... and the same for few rows.  few_attention_q4_columns: the columns of its products, 16 .. 48 (0: too many rows); tq has
+// ... and the same for few rows.  few_attention_q4_columns: the columns of its products, 16 .. 64 (0: too many rows); tq has
 // boxes of 64 dims x G heads x columns / G rows, which are a.tpt.  Of the workspace it uses the counters as [2 grid][8],
-// part_o as [2 grid][2][48][128] and part_ml as [2 grid][2][48].
+// part_o as [2 grid][2][64][128] and part_ml as [2 grid][2][64].
 int few_attention_q4_columns(int G, int max_rows);
 float q4_tile_scale();                  // scale_log2 of both is this times the softmax scale * log2(e)
 cudaError_t launch_few_attention_q4(const CUtensorMap& tq, const ChunkAttnArgs& a, int columns, int grid, cudaStream_t s);
