@@ -23,10 +23,10 @@
 // one of values are 32768 entries to unpack, 725 warp instructions for each quarter of the SM with their share of the
 // softmax, and a slot's tiles wait for one another: unpack K, score, weigh, and only then P V, whose end frees V's and
 // P's place.  The SM issues in 72 % of the cycles with 16 columns, in 58 % with 48, where the softmax's share of
-// that chain is three times as long (a tile of a slot takes about 1.2 us with 16 columns, 1.6 with 48).  With few keys to a slot: 4 us to the first
-// product (lengths, page table, first pages), 4 to 5 to join shared items; 4 sequences of one token at 300 to 1000 keys 11.0 us.
-// Tried without gain: two places for P, tiles brought to bf16 in halves, eight softmax warps a slot, shares that count an
-// item's rows beside its keys.
+// that chain is three times as long (a tile of a slot takes about 1.2 us with 16 columns, 1.6 with 48).  With few keys to
+// a slot: 4 us to the first product (lengths, page table, first pages), 4 to 5 to join shared items; 4 sequences of one token
+// at 300 to 1000 keys 11.0 us.  Tried without gain: two places for P, tiles brought to bf16 in halves, eight softmax warps a
+// slot, fewer columns for the sequences of few rows in a batch of more.
 //
 // Roles (28 warps; four to a slot where not said otherwise): 0-7 softmax and epilogue (a thread per key, then per dim); 8 and 9
 // issue a slot's MMAs; 10 and 11 walk the batch for a slot, post its pieces and load its queries and pages; 12-19
