@@ -2,11 +2,11 @@
 // chunk's keys and values, and the read of cached keys and values.
 //
 // Bound.  Of a few rows, a launch and the chain of loads behind it (norm of 9 rows 3.5 us, append of 8 4.1, read of 77
-// keys 5.6: lengths, page id, page, output).  Of many, with 32 / 8 heads:
+// keys 4.2: lengths, page id, page, output).  Of many, with 32 / 8 heads:
 //   norm, 8192 rows    29.5 us = 5.8 TB/s, 86 % of the copy; loads wait for HBM (issue 46 %)
-//   append, 8192 rows  38.6 us = 3.3 TB/s, 49 %; issue 56 %: some 15 instructions a value for norm, rotation, maximum,
-//                      quotient and packing, and chains of shuffles; keys and values only 15.2 us
-//   read, 32 contexts  63.8 us = 6.0 TB/s, 88 %
+//   append, 8192 rows  37.8 us = 3.4 TB/s, 50 %; issue 56 %: some 15 instructions a value for norm, rotation, maximum,
+//                      quotient and packing, and chains of shuffles; keys and values only 14.4 us
+//   read, 32 contexts  63.1 us = 6.1 TB/s, 89 %
 #include "attention_util.cuh"
 #include "internal.h"
 #include "paged_rows.cuh"
@@ -143,7 +143,7 @@ struct Block {
   int row0;                                // packed row of key key0 + 0 (may be before the sequence's first)
 };
 template <int LB, class Args>
-__device__ __forceinline__ Block block_of(int v, const Args& a, int lane, unsigned site) {
+__device__ __forceinline__ Block block_of(int v, const Args& a, int lane) {
   Block k{-1, 0, 0, 0, 0, 0};
   const Place at = place_of(v, a, lane, [](int c0, int b) { return (c0 >> LB) + 2 * b; });
   if (at.b < 0 || at.c1 <= at.c0 || out_of_bounds(at.c0, at.c1, at.ctx, a)) return k;
@@ -155,12 +155,15 @@ __device__ __forceinline__ Block block_of(int v, const Args& a, int lane, unsign
   k.hi = min(end - k.key0, 1 << LB);
   k.row0 = at.c0 + (k.key0 - at.ctx);
   k.page = a.block_table[(size_t)at.b * a.max_pages + k.key0 / Q4_PAGE];
-  if (k.page < 0 || k.page >= a.num_pages) {
-    if (lane == 0) set_status(a.status, site);
-    return k;
-  }
   k.b = at.b;
   return k;
+}
+// (apart, so that loads that need no page are issued before its id is there: append of 8192 rows 38.7 us otherwise)
+template <class Args>
+__device__ __forceinline__ bool page_exists(const Block& k, const Args& a, int lane, unsigned site) {
+  const bool yes = k.page >= 0 && k.page < a.num_pages;
+  if (!yes && lane == 0) set_status(a.status, site);
+  return yes;
 }
 template <class Args>
 __device__ __forceinline__ void check_sequence(const Args& a, long long b, unsigned site) {
@@ -190,11 +193,8 @@ __device__ __noinline__ unsigned any_values(const uint2 (&x)[8], uint32_t (&add)
 template <int LB>
 __device__ __forceinline__ void append_values(const KvAppendQ4Args& a, int v, int g, int lane) {
   constexpr int WORDS = 1 << (LB - 3);
-  const Block k = block_of<LB>(v, a, lane, 0x8F2u);
+  const Block k = block_of<LB>(v, a, lane);
   if (k.b < 0) return;
-  uint8_t* page = a.Vpool + ((size_t)g * a.num_pages + k.page) * Q4_BYTES;
-  const int slot = k.key0 % Q4_PAGE;
-  uint32_t* words = reinterpret_cast<uint32_t*>(page + (slot >> 5) * Q4_PLANE + lane * 64) + ((slot >> 3) & 3);
   const uint16_t* src = a.Vnew + (size_t)g * D + lane * 4;
   uint32_t w[WORDS][4];
   auto load = [&](int i, uint2 (&x)[8]) {
@@ -207,6 +207,10 @@ __device__ __forceinline__ void append_values(const KvAppendQ4Args& a, int v, in
   };
   uint2 x[8];
   load(0, x);
+  if (!page_exists(k, a, lane, 0x8F2u)) return;
+  uint8_t* page = a.Vpool + ((size_t)g * a.num_pages + k.page) * Q4_BYTES;
+  const int slot = k.key0 % Q4_PAGE;
+  uint32_t* words = reinterpret_cast<uint32_t*>(page + (slot >> 5) * Q4_PLANE + lane * 64) + ((slot >> 3) & 3);
 #pragma unroll
   for (int i = 0; i < WORDS; ++i) {
     uint2 next[8];
@@ -380,8 +384,8 @@ __global__ void __launch_bounds__(128) kv_read_q4_kernel(const KvReadQ4Args a) {
   }
   if (u >= units) return;
   const int g = u % a.Hkv;
-  const Block k = block_of<5>(u / a.Hkv, a, lane, 0x9F2u);
-  if (k.b < 0) return;
+  const Block k = block_of<5>(u / a.Hkv, a, lane);
+  if (k.b < 0 || !page_exists(k, a, lane, 0x9F2u)) return;
   const size_t at = ((size_t)g * a.num_pages + k.page) * Q4_BYTES;
   const int slot0 = k.key0 % Q4_PAGE;
   // values first: their loads are the longer wait
@@ -396,20 +400,27 @@ __global__ void __launch_bounds__(128) kv_read_q4_kernel(const KvReadQ4Args a) {
     vc[e] = *reinterpret_cast<const uint4*>(vp + Q4_SCALES + (lane >> 3) * 128 + slot0 + 16 * e);
   const uint8_t* kp = a.Kpool + at;
   const int l = lane & 7;
+  // (all loads ahead of the stores, which they would otherwise stay behind: 77 keys 5.6 us)
+  uint32_t wa[8], wb[8], cs[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int j = 4 * i + (lane >> 3), slot = slot0 + j;
-    if (j < k.lo || j >= k.hi) continue;
+    const int slot = slot0 + 4 * i + (lane >> 3);
     const uint32_t* word = reinterpret_cast<const uint32_t*>(kp + (l >> 2) * Q4_PLANE + slot * 16) + (l & 3);
-    const uint32_t wa = word[0], wb = word[2 * Q4_PLANE / 4];
-    const uint32_t codes = reinterpret_cast<const uint32_t*>(kp + Q4_SCALES)[slot] >> (8 * (l >> 2));
-    const uint32_t sa = q4_scale2((codes & 255u) * 0x10001u), sb = q4_scale2(((codes >> 16) & 255u) * 0x10001u);
+    wa[i] = word[0];
+    wb[i] = word[2 * Q4_PLANE / 4];
+    cs[i] = reinterpret_cast<const uint32_t*>(kp + Q4_SCALES)[slot] >> (8 * (l >> 2));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int j = 4 * i + (lane >> 3);
+    if (j < k.lo || j >= k.hi) continue;
+    const uint32_t sa = q4_scale2((cs[i] & 255u) * 0x10001u), sb = q4_scale2(((cs[i] >> 16) & 255u) * 0x10001u);
     const uint32_t oa = q4_offset2(sa), ob = q4_offset2(sb);
     uint16_t* dst = a.Kout + (size_t)(k.row0 + j) * a.ldkv + (size_t)g * D + l * 8;
-    st_past_l1(dst, make_uint4(q4_pair<0>(wa, sa, oa), q4_pair<1>(wa, sa, oa), q4_pair<2>(wa, sa, oa),
-                               q4_pair<3>(wa, sa, oa)));
-    st_past_l1(dst + 64, make_uint4(q4_pair<0>(wb, sb, ob), q4_pair<1>(wb, sb, ob), q4_pair<2>(wb, sb, ob),
-                                    q4_pair<3>(wb, sb, ob)));
+    st_past_l1(dst, make_uint4(q4_pair<0>(wa[i], sa, oa), q4_pair<1>(wa[i], sa, oa), q4_pair<2>(wa[i], sa, oa),
+                               q4_pair<3>(wa[i], sa, oa)));
+    st_past_l1(dst + 64, make_uint4(q4_pair<0>(wb[i], sb, ob), q4_pair<1>(wb[i], sb, ob), q4_pair<2>(wb[i], sb, ob),
+                                    q4_pair<3>(wb[i], sb, ob)));
   }
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
