@@ -60,15 +60,19 @@ __device__ __forceinline__ void norm_head(Head& h, const Head& w, float eps) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) h.v[e] = q4_mul2(q4_mul2(h.v[e], make_float2(r, r)), w.v[e]);
 }
-// (a, b) -> (a c - b s, b c + a s)
+// (a, b) -> (a c - b s, b c + a s), each product rounded before the sum.  The sums are __fadd_rn, which is never merged with a
+// product; a packed add of packed products was compiled to a multiply-add, in which a c stays unrounded (16 of a million
+// bf16 results were off by a step).
 struct Turns {
   float c[8], s[8];
 };
 __device__ __forceinline__ void turn_head(Head& h, const Turns& t) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    h.v[e] = add2(q4_mul2(h.v[e], make_float2(t.c[e], t.c[e])),
-                  q4_mul2(make_float2(h.v[e].y, h.v[e].x), make_float2(-t.s[e], t.s[e])));
+  for (int e = 0; e < 8; ++e) {
+    const float2 x = q4_mul2(h.v[e], make_float2(t.c[e], t.c[e]));
+    const float2 y = q4_mul2(make_float2(h.v[e].y, h.v[e].x), make_float2(-t.s[e], t.s[e]));
+    h.v[e] = make_float2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+  }
 }
 __device__ __forceinline__ Turns turns_of(const float2* cs, int r, int i0) {
   Turns t;
