@@ -1741,6 +1741,7 @@ int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr,
 
 // --------------------------------------------------------------------------- paged cache in 4 bits
 static int check_norm(const spec_bf16* wq, const spec_bf16* wk, float eps) {
+  if (!wq && !wk) return SPEC_OK;                       // (no norm: eps is ignored)
   if (!aligned16(wq) || !aligned16(wk)) return fail(SPEC_EINVAL, "norm weights must be 16-byte aligned");
   if (!std::isfinite(eps) || eps < 0.f) return fail(SPEC_EINVAL, "eps must be finite and >= 0");
   return SPEC_OK;
