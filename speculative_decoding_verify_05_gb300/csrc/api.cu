@@ -1753,6 +1753,8 @@ int spec_qk_norm_rope(const spec_bf16* Q, int ldq, spec_bf16* Qout, int ldqo, co
   if (M < 0 || Hq < 0 || Hkv < 0) return fail(SPEC_EINVAL, "bad sizes M=%d Hq=%d Hkv=%d", M, Hq, Hkv);
   if (D != 128) return fail(SPEC_EUNSUPPORTED, "head_dim %d: only 128 is implemented", D);
   if (M == 0 || Hq + (long long)Hkv == 0) return ok();
+  if (!Hq) Q = wq = Qout = nullptr;                     // (ignored)
+  if (!Hkv) K = wk = Kout = nullptr;
   if ((Hq && (!Q || !Qout || !wq)) || (Hkv && (!K || !Kout || !wk))) return fail(SPEC_EINVAL, "NULL tensor argument");
   if (!aligned16(Q) || !aligned16(Qout) || !aligned16(K) || !aligned16(Kout) || !aligned16(cs))
     return fail(SPEC_EINVAL, "tensors must be 16-byte aligned");
