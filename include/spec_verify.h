@@ -466,7 +466,8 @@ SPEC_API int spec_kv_append_paged(const spec_bf16* Q, int ldq, spec_bf16* Qrot, 
  * unnormalised sums in range.  Checked on the device, with the status
  * word set: a sequence outside the M rows or past 128 * max_pages keys is skipped; a page id outside
  * [0, num_pages) reads page 0 instead.
- * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, scale finite and >= 0.
+ * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, scale of 0 to 2e38 (scale * log2(e) is the
+ * kernel's factor).
  * Workspace: spec_chunk_attention_workspace_bytes. */
 SPEC_API size_t spec_chunk_attention_workspace_bytes(int B, int M, int Hq, int Hkv, int D, int max_pages);
 SPEC_API int spec_chunk_attention_paged(const spec_bf16* Q, int ldq, const int32_t* cu_rows, const int32_t* ctx_len,
@@ -544,7 +545,8 @@ SPEC_API int spec_kv_read_paged_q4(const uint8_t* Kpool, const uint8_t* Vpool, i
  * What lies behind a sequence's last key in its page may hold anything.  Checked on the device, with the status
  * word set: a sequence outside the M rows, of more than max_rows rows or past 128 * max_pages keys is skipped; a
  * page id outside [0, num_pages) reads page 0 instead.
- * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, max_rows >= 1, scale finite and >= 0.
+ * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 128, M <= 4194304, max_rows >= 1, scale of 0 to 4e32 (scale * log2(e) *
+ * 2^19 is the kernel's factor).
  * Workspace: spec_chunk_attention_q4_workspace_bytes. */
 SPEC_API size_t spec_chunk_attention_q4_workspace_bytes(int B, int M, int max_rows, int Hq, int Hkv, int D,
                                                         int max_pages);

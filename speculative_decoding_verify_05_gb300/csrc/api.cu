@@ -1881,6 +1881,10 @@ static int chunk_attention_impl(const spec_bf16* Q, int ldq, const int32_t* cu_r
     return fail(SPEC_EINVAL, "bad leading dimensions ldq=%d ldo=%d", ldq, ldo);
   if (!aligned16(Q) || !aligned16(O)) return fail(SPEC_EINVAL, "bf16 tensors must be 16-byte aligned");
   if (!std::isfinite(scale) || scale < 0.f) return fail(SPEC_EINVAL, "scale must be finite and >= 0");
+  // (a scale of 0 weighs every visible key alike; masked scores have to stay -inf under it)
+  float scale_log2 = std::max(scale * 1.4426950408889634f, 1e-30f);
+  if (q4) scale_log2 *= q4_tile_scale();        // (keys and values enter the products scaled down by as much)
+  if (!std::isfinite(scale_log2)) return fail(SPEC_EINVAL, "scale=%g is too large for the kernel's factor", scale);
   const ChunkPlan p = plan_chunk();
   if (!workspace || workspace_bytes < p.bytes)
     return fail(SPEC_EINVAL, "workspace too small: need %zu bytes", p.bytes);
@@ -1909,9 +1913,7 @@ static int chunk_attention_impl(const spec_bf16* Q, int ldq, const int32_t* cu_r
   a.Q = Q; a.ldq = ldq; a.cu_rows = cu_rows; a.ctx_len = ctx_len; a.B = B; a.M = M; a.max_rows = max_rows;
   a.Kpool = Kpool; a.Vpool = Vpool; a.block_table = block_table; a.num_pages = num_pages; a.max_pages = max_pages;
   a.Hkv = Hkv; a.G = G; a.tpt = tpt;
-  // (a scale of 0 weighs every visible key alike; masked scores have to stay -inf under it)
-  a.scale_log2 = std::max(scale * 1.4426950408889634f, 1e-30f);
-  if (q4) a.scale_log2 *= q4_tile_scale();      // (keys and values enter the products scaled down by as much)
+  a.scale_log2 = scale_log2;
   a.O = O; a.ldo = ldo;
   a.wide = (reinterpret_cast<uintptr_t>(O) & 31u) == 0 && ldo % 16 == 0 ? 1 : 0;
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
