@@ -515,8 +515,8 @@ SPEC_API int spec_qk_norm_rope(const spec_bf16* Q, int ldq, spec_bf16* Qout, int
  *   wq, wk   [D] bf16, or both NULL: no norm (then Q needs cs).  eps is ignored without them
  *   Kpool, Vpool [Hkv][num_pages][SPEC_Q4_PAGE_BYTES] (in/out); no input may overlap them.  Of a page that
  *            receives rows only those rows change; it must belong to one sequence
- * The rest, and what is checked on the device, as for spec_kv_append_paged.  M <= 4194304.  One kernel, no
- * workspace. */
+ * The rest, and what is checked on the device, as for spec_kv_append_paged.  M <= 4194304 and
+ * (M / 8 + 2 B) Hkv <= 2^30.  One kernel, no workspace. */
 SPEC_API int spec_kv_append_paged_q4(const spec_bf16* Q, int ldq, spec_bf16* Qrot, int ldqr, const spec_bf16* Knew,
                                      const spec_bf16* Vnew, int ldkv, const spec_bf16* wq, const spec_bf16* wk,
                                      float eps, const float* cs, const int32_t* cu_rows, const int32_t* ctx_len, int B,
@@ -530,8 +530,8 @@ SPEC_API int spec_kv_append_paged_q4(const spec_bf16* Q, int ldq, spec_bf16* Qro
  *   Kout, Vout  row r, kv head g at + r*ldkv + g*D (bf16 out; must not overlap the pools)
  * Rows outside cu_rows[0] .. cu_rows[B] - 1 are left as they were.  Checked on the device, with the status word
  * set: a sequence outside the M rows or past 128 * max_pages keys is skipped; rows whose page id is outside
- * [0, num_pages) are not written.  Requires D == 128, ldkv a multiple of 8, 16-byte aligned pointers.  One
- * kernel, no workspace. */
+ * [0, num_pages) are not written.  Requires D == 128, ldkv a multiple of 8, 16-byte aligned pointers,
+ * (M / 32 + 2 B) Hkv <= 2^30.  One kernel, no workspace. */
 SPEC_API int spec_kv_read_paged_q4(const uint8_t* Kpool, const uint8_t* Vpool, int num_pages,
                                    const int32_t* block_table, int max_pages, const int32_t* cu_rows,
                                    const int32_t* ctx_len, int B, int M, spec_bf16* Kout, spec_bf16* Vout, int ldkv,

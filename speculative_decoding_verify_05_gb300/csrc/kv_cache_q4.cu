@@ -2,11 +2,13 @@
 // chunk's keys and values, and the read of cached keys and values.
 //
 // Bound.  Of a few rows, a launch and the chain of loads behind it (norm of 9 rows 3.5 us, append of 8 4.1, read of 77
-// keys 4.2: lengths, page id, page, output).  Of many, with 32 / 8 heads:
-//   norm, 8192 rows    29.5 us = 5.8 TB/s, 86 % of the copy; loads wait for HBM (issue 46 %)
-//   append, 8192 rows  37.8 us = 3.4 TB/s, 50 %; issue 56 %: some 15 instructions a value for norm, rotation, maximum,
-//                      quotient and packing, and chains of shuffles; keys and values only 14.4 us
-//   read, 32 contexts  63.1 us = 6.1 TB/s, 89 %
+// keys 4.2: lengths, page id, page, output).  Of many, with 32 / 8 heads, in bytes of inputs and outputs:
+//   norm, 8192 rows    29.7 us = 5.8 TB/s, 87 % of the copy; loads wait for HBM (issue 50 %)
+//   append, 8192 rows  38.8 us = 4.7 TB/s, 70 %; issue 59 %: some 15 instructions a value for norm, rotation, maximum,
+//                      quotient and packing, and chains of shuffles.  Keys and values alone take 14.7 us, which
+//                      wait for instructions, the queries' share of the norm above 24, which waits for HBM: the grid
+//                      has the one before the other, and the times add up
+//   read, 32 contexts  62.4 us = 6.1 TB/s, 92 %
 #include "attention_util.cuh"
 #include "internal.h"
 #include "paged_rows.cuh"
@@ -118,7 +120,7 @@ __device__ __forceinline__ void each_head(const uint16_t* src, int heads, const 
   }
 }
 
-// One CTA per row.  At least 14 CTAs of two warps an SM (72 registers a thread): 8192 rows 29.5 us, 32.9 without the bound.
+// One CTA per row.  At least 14 CTAs of two warps an SM (72 registers a thread): 8192 rows 29.7 us, 3.4 more without the bound.
 template <int WARPS, int UNITS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 2 ? 14 : 5) qk_norm_rope_kernel(const NormRopeArgs a) {
   pdl_wait();
@@ -162,7 +164,7 @@ __device__ __forceinline__ Block block_of(int v, const Args& a, int lane) {
   k.b = at.b;
   return k;
 }
-// (apart, so that loads that need no page are issued before its id is there: append of 8192 rows 38.7 us otherwise)
+// (apart, so that loads that need no page are issued before its id is there: append of 8192 rows 0.9 us more otherwise)
 template <class Args>
 __device__ __forceinline__ bool page_exists(const Block& k, const Args& a, int lane, unsigned site) {
   const bool yes = k.page >= 0 && k.page < a.num_pages;
@@ -234,7 +236,7 @@ __device__ __forceinline__ void append_values(const KvAppendQ4Args& a, int v, in
     for (int j = 0; j < 8; ++j)
       top[j] = max(max((x[j].x << 16) & 0x7fffffffu, x[j].x & 0x7fffffffu), max((x[j].y << 16) & 0x7fffffffu, x[j].y & 0x7fffffffu));
     // folded over the eight lanes of a scale: lane k of them is left with key k's, and works out its scale for all (each lane
-    // for each key: 8192 rows 39.6 us, 24 sequences 11.7 instead of 11.0)
+    // for each key: 8192 rows 1.0 us more, 24 sequences 0.7)
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) {
       const bool up = (lane & o) != 0;
